@@ -14,6 +14,11 @@ Functions take torch CUDA tensors and work in place (outputs are arguments):
   value_channel_scale(...) per-channel V dequant scale
   mla_sparse_decode(...)   MLA sparse attention over a packed FP8 latent cache
   mla_sparse_decode_kvc(...) the same over rows the KV compress epilog wrote
+and a speculative decode step over the same cache:
+  qkv_norm_rope_append(...) per-head norm, rotation and quantisation of q and k, K/V append
+  tree_decode(...)         attention of a tree of drafted tokens
+  tree_verify(...)         drafted tokens against the target's probabilities
+  cache_keep_path(...)     the accepted branch kept in the cache
 """
 from __future__ import annotations
 
@@ -104,6 +109,21 @@ def lib():
         L.pa_mla_sparse_decode_kvc.argtypes = [P, P, P, i64, i64, i32, P, P, P, P, i32, i32, i32,
                                                i32, i32, i32, i64, i32, f32, i32, P, P]
         L.pa_mla_sparse_decode_kvc.restype = i32
+        L.pa_fp8_qkv_norm_rope_append.argtypes = [
+            P, P, P, i32, i64, i64, i64, P, P, i32, f32, P, i32, i64, i32, P, i32, P, P, P, P, P,
+            i32, P, P, P, i32, i64, i32, i32, i32, i64, i32, i32, P]
+        L.pa_fp8_qkv_norm_rope_append.restype = i32
+        L.pa_fp8_tree_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32,
+                                                        ctypes.POINTER(sz)]
+        L.pa_fp8_tree_decode_workspace_size.restype = i32
+        L.pa_fp8_tree_decode.argtypes = [P, P, P, P, P, P, P, P, P, P, i64, P, i32, i32, i32, i32,
+                                         i32, i32, i64, i32, i32, f32, P, sz, P]
+        L.pa_fp8_tree_decode.restype = i32
+        L.pa_tree_verify.argtypes = [P, P, P, P, P, P, i32, i32, i32, P, P, P, P]
+        L.pa_tree_verify.restype = i32
+        L.pa_fp8_cache_keep_path.argtypes = [P, P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32,
+                                             i64, i32, i32, P]
+        L.pa_fp8_cache_keep_path.restype = i32
         _lib = L
         return L
 
@@ -453,11 +473,364 @@ def value_channel_scale(v, cu_seqlens, v_scale, *, stream=None):
     _check(st, "pa_fp8_value_channel_scale")
 
 
+# --------------------------------------------------------------------------
+# Speculative decode step: a tree of drafted tokens for each sequence
+# --------------------------------------------------------------------------
+
+def _one_device(**tensors):
+    """Every tensor on the current device: the launch goes to that device's
+    stream, and a pointer of another device would fault there."""
+    torch = _torch()
+    cur = torch.cuda.current_device()
+    for n, t in tensors.items():
+        if t is not None and t.device.index != cur:
+            raise ValueError("%s is on %s, the current device is cuda:%d" % (n, t.device, cur))
+
+
+def _shape(t, name, *want):
+    if tuple(t.shape) != tuple(want):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(want)))
+
+
+def _norm_rope_args(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes, q_scale, key_cache,
+                    value_cache, slot_mapping, key_scale_cache, v_scale, token_batch, eps,
+                    interleaved, layout):
+    torch = _torch()
+    floats = (torch.float32, torch.bfloat16)
+    _need(q, "q", floats, contiguous=False)
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, n, (q.dtype,), contiguous=False)
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+            raise ValueError("%s must be [tokens, heads, head_size] with contiguous heads" % n)
+    T, NQ, D = q.shape
+    NKV = k.shape[1]
+    _shape(k, "k", T, NKV, D)
+    _shape(v, "v", T, NKV, D)
+    wdt = torch.float32
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _need(t, n, floats)
+            _shape(t, n, D)
+            wdt = t.dtype
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise TypeError("q_weight and k_weight must have one dtype")
+    rd = max_pos = pos_type = 0
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", torch.float32)
+        max_pos, rd = cos_sin.shape
+        if positions is None:
+            raise ValueError("cos_sin needs positions")
+    if positions is not None:
+        _need(positions, "positions", (torch.int32, torch.int64))
+        _shape(positions, "positions", T)
+        pos_type = INDEX_I64 if positions.dtype == torch.int64 else INDEX_I32
+    _need(q_codes, "q_codes", _fp8_types())
+    _shape(q_codes, "q_codes", T, NQ, D)
+    _need(q_scale, "q_scale", torch.float32)
+    _shape(q_scale, "q_scale", T, NQ)
+    for t, n in ((key_cache, "key_cache"), (value_cache, "value_cache")):
+        _need(t, n, _fp8_types())
+    _need(slot_mapping, "slot_mapping", (torch.int32, torch.int64))
+    _shape(slot_mapping, "slot_mapping", T)
+    _need(key_scale_cache, "key_scale_cache", torch.float32)
+    _need(v_scale, "v_scale", torch.float32)
+    _need(token_batch, "token_batch", torch.int32)
+    _shape(token_batch, "token_batch", T)
+    NB, H, BS = _cache_dims(key_cache, layout)
+    cache = (NB, BS, H) if layout == LAYOUT_BSND else (NB, H, BS)
+    _shape(key_cache, "key_cache", *cache, D)
+    _shape(value_cache, "value_cache", *cache, D)
+    if key_scale_cache.numel() != NB * BS * H or H != NKV:
+        raise ValueError("key_scale_cache and the caches must have one scale a row and k's heads")
+    _shape(v_scale, "v_scale", v_scale.shape[0], NKV, D)
+    _one_device(q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
+                positions=positions, q_codes=q_codes, q_scale=q_scale, key_cache=key_cache,
+                value_cache=value_cache, slot_mapping=slot_mapping,
+                key_scale_cache=key_scale_cache, v_scale=v_scale, token_batch=token_batch)
+    args = (_ptr(q), _ptr(k), _ptr(v), _in_dtype(q), q.stride(0), k.stride(0), v.stride(0),
+            _ptr(q_weight), _ptr(k_weight), DTYPE_BF16 if wdt == torch.bfloat16 else DTYPE_F32,
+            float(eps), _ptr(cos_sin), rd, max_pos, int(bool(interleaved)), _ptr(positions),
+            pos_type, _ptr(q_codes), _ptr(q_scale), _ptr(key_cache), _ptr(value_cache),
+            _ptr(slot_mapping), _slot_type(slot_mapping), _ptr(key_scale_cache), _ptr(v_scale),
+            _ptr(token_batch), v_scale.shape[0], T, NQ, NKV, D, NB, BS, layout)
+    keep = (q, k, v, q_weight, k_weight, cos_sin, positions, q_codes, q_scale, key_cache,
+            value_cache, slot_mapping, key_scale_cache, v_scale, token_batch)
+    return args, keep
+
+
+def qkv_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes, q_scale,
+                         key_cache, value_cache, slot_mapping, key_scale_cache, v_scale,
+                         token_batch, *, eps: float = 1e-5, interleaved: bool = False,
+                         layout: int = LAYOUT_BNBD, stream=None):
+    """Per-head RMSNorm and rotation of q and k, E4M3 quantisation, and the
+    append of k and v, in one pass (in place into q_codes, q_scale and the
+    caches).
+
+    q [T, NQ, D], k and v [T, NKV, D] float32 or bfloat16, tokens any stride
+    apart (views of one projection's output), D 64, 128 or 256; q_weight,
+    k_weight [D] float32 or bfloat16 or None (no norm); cos_sin float32
+    [max_position, rotary_dim], cosines then sines, or None (no rotation);
+    positions int32/int64 [T]; q_codes E4M3 [T, NQ, D], q_scale float32
+    [T, NQ]; the caches, slot_mapping, v_scale and token_batch as in
+    cache_quant_scatter. interleaved: channels (2i, 2i+1) are a pair instead
+    of (i, i + rotary_dim/2)."""
+    args, keep = _norm_rope_args(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes,
+                                 q_scale, key_cache, value_cache, slot_mapping, key_scale_cache,
+                                 v_scale, token_batch, eps, interleaved, layout)
+    _check(lib().pa_fp8_qkv_norm_rope_append(*args, _stream(stream)),
+           "pa_fp8_qkv_norm_rope_append")
+    del keep
+
+
+def prepare_qkv_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes,
+                                 q_scale, key_cache, value_cache, slot_mapping, key_scale_cache,
+                                 v_scale, token_batch, *, eps: float = 1e-5,
+                                 interleaved: bool = False, layout: int = LAYOUT_BNBD,
+                                 stream=None):
+    """qkv_norm_rope_append() prepared once: returns a callable that launches
+    the same call on the same buffers."""
+    args, keep = _norm_rope_args(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes,
+                                 q_scale, key_cache, value_cache, slot_mapping, key_scale_cache,
+                                 v_scale, token_batch, eps, interleaved, layout)
+    return _Prepared(lib().pa_fp8_qkv_norm_rope_append, "pa_fp8_qkv_norm_rope_append", args, keep,
+                     stream)
+
+
+def tree_decode_workspace_size(B: int, S1: int, NQ: int, NKV: int, D: int = 128) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().pa_fp8_tree_decode_workspace_size(B, S1, NQ, NKV, D, ctypes.byref(n)),
+           "pa_fp8_tree_decode_workspace_size")
+    return n.value
+
+
+class TreeWorkspace:
+    """Zero-initialised device scratch for tree_decode (reusable: every call
+    leaves what must be zero at zero). Calls that may run at the same time,
+    replays of two captured graphs among them, need one each."""
+
+    def __init__(self, B, S1, NQ, NKV, D=128, *, device=None):
+        torch = _torch()
+        self.nbytes = tree_decode_workspace_size(B, S1, NQ, NKV, D)
+        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+
+    def error_flags(self) -> int:
+        """Non-zero if a kernel wait gave up (bitmask of the wait sites)."""
+        return int(self.buf[:4].view(_torch().int32).item())
+
+    def clear_error_flags(self) -> None:
+        """Zero the error word (on the current stream)."""
+        self.buf[:4].zero_()
+
+
+def _tree_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_act_seqs,
+               tree_mask, out, S1, tree_len, layout, softmax_scale, workspace, stream):
+    torch = _torch()
+    for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, (torch.uint8, torch.float8_e4m3fn))
+    for t, n in ((q_scale, "q_scale"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need(t, n, torch.float32)
+    _need(block_table, "block_table", torch.int32)
+    _need(kv_act_seqs, "kv_act_seqs", torch.int32)
+    _need(tree_mask, "tree_mask", (torch.bool, torch.uint8), contiguous=False)
+    _need(out, "out", torch.bfloat16)
+    B = kv_act_seqs.shape[0]
+    BS1, NQ, D = q.shape
+    if BS1 != B * S1:
+        raise ValueError("q has %d tokens, expected B * S1 = %d" % (BS1, B * S1))
+    NB, NKV, BS = _cache_dims(k_cache, layout)
+    cache = (NB, BS, NKV) if layout == LAYOUT_BSND else (NB, NKV, BS)
+    _shape(k_cache, "k_cache", *cache, D)
+    _shape(v_cache, "v_cache", *cache, D)
+    if k_scale.numel() != NB * BS * NKV:
+        raise ValueError("k_scale must have one scale a cache row")
+    _shape(q_scale, "q_scale", BS1, NQ)
+    _shape(v_scale, "v_scale", B, NKV, D)
+    _shape(out, "out", BS1, NQ, D)
+    _shape(kv_act_seqs, "kv_act_seqs", B)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_blocks]")
+    if tree_mask.dim() == 2:
+        tree_mask = tree_mask.unsqueeze(0).expand(B, S1, S1) if tuple(tree_mask.shape) == (S1, S1) \
+            else tree_mask
+    _shape(tree_mask, "tree_mask", B, S1, S1)
+    if B > 0 and ((S1 > 1 and tree_mask.stride(2) != 1) or (S1 > 1 and tree_mask.stride(1) != S1)):
+        raise ValueError("tree_mask must have contiguous rows within a sequence")
+    if tree_len is not None:
+        _need(tree_len, "tree_len", torch.int32)
+        _shape(tree_len, "tree_len", B)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    if workspace is None:
+        # zeroed on the stream that uses it, and handed back to it
+        with torch.cuda.stream(stream):
+            workspace = TreeWorkspace(B, S1, NQ, NKV, D, device=q.device)
+    _one_device(q=q, q_scale=q_scale, k_cache=k_cache, k_scale=k_scale, v_cache=v_cache,
+                v_scale=v_scale, block_table=block_table, kv_act_seqs=kv_act_seqs,
+                tree_mask=tree_mask, tree_len=tree_len, out=out, workspace=workspace.buf)
+    args = (_ptr(q), _ptr(q_scale), _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale),
+            _ptr(block_table), _ptr(kv_act_seqs), _ptr(tree_len), _ptr(tree_mask),
+            tree_mask.stride(0), _ptr(out), B, S1, NQ, NKV, D, BS, NB, block_table.shape[1],
+            layout, float(softmax_scale), _ptr(workspace.buf), workspace.nbytes)
+    keep = (q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_act_seqs, tree_len,
+            tree_mask, out, workspace)
+    return args, keep
+
+
+def tree_decode(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_act_seqs,
+                tree_mask, out, *, S1: int, tree_len=None, layout: int = LAYOUT_BSND,
+                softmax_scale=None, workspace: TreeWorkspace | None = None, stream=None):
+    """Attention of a tree of drafted tokens over the paged FP8 cache (in place
+    into ``out``): each of a sequence's tree_len[b] <= S1 drafted tokens, whose
+    K/V are the sequence's last positions, attends to everything before them
+    and to the drafted tokens its row of tree_mask names.
+
+    tree_mask bool or uint8 [B, S1, S1], or [S1, S1] for all sequences;
+    tree_len int32 [B] or None (all S1); the other arguments as in decode().
+    Rows at and behind tree_len[b], and rows that see nothing, get zeros."""
+    args, keep = _tree_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table,
+                            kv_act_seqs, tree_mask, out, S1, tree_len, layout, softmax_scale,
+                            workspace, stream)
+    _check(lib().pa_fp8_tree_decode(*args, _stream(stream)), "pa_fp8_tree_decode")
+    del keep   # (a workspace made here lives until the launch is enqueued)
+    return out
+
+
+def prepare_tree_decode(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_act_seqs,
+                        tree_mask, out, *, S1: int, tree_len=None, layout: int = LAYOUT_BSND,
+                        softmax_scale=None, workspace: TreeWorkspace | None = None, stream=None):
+    """tree_decode() prepared once: returns a callable that launches the same
+    call on the same buffers."""
+    args, keep = _tree_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table,
+                            kv_act_seqs, tree_mask, out, S1, tree_len, layout, softmax_scale,
+                            workspace, stream)
+    return _Prepared(lib().pa_fp8_tree_decode, "pa_fp8_tree_decode", args, keep, stream)
+
+
+def _verify_args(target_probs, draft_probs, draft_tokens, parents, uniforms, accepted, path,
+                 tokens, tree_len):
+    torch = _torch()
+    _need(target_probs, "target_probs", torch.float32)
+    if target_probs.dim() != 3:
+        raise ValueError("target_probs must be [B, S1, V]")
+    B, S1, V = target_probs.shape
+    if draft_probs is not None:
+        _need(draft_probs, "draft_probs", torch.float32)
+        _shape(draft_probs, "draft_probs", B, S1, V)
+    for t, n in ((draft_tokens, "draft_tokens"), (parents, "parents"), (path, "path"),
+                 (tokens, "tokens")):
+        _need(t, n, torch.int32)
+        _shape(t, n, B, S1)
+    _need(uniforms, "uniforms", torch.float32)
+    _shape(uniforms, "uniforms", B, S1)
+    _need(accepted, "accepted", torch.int32)
+    _shape(accepted, "accepted", B)
+    if tree_len is not None:
+        _need(tree_len, "tree_len", torch.int32)
+        _shape(tree_len, "tree_len", B)
+    _one_device(target_probs=target_probs, draft_probs=draft_probs, draft_tokens=draft_tokens,
+                parents=parents, uniforms=uniforms, accepted=accepted, path=path, tokens=tokens,
+                tree_len=tree_len)
+    args = (_ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens), _ptr(parents),
+            _ptr(uniforms), _ptr(tree_len), B, S1, V, _ptr(accepted), _ptr(path), _ptr(tokens))
+    keep = (target_probs, draft_probs, draft_tokens, parents, uniforms, accepted, path, tokens,
+            tree_len)
+    return args, keep
+
+
+def tree_verify(target_probs, draft_probs, draft_tokens, parents, uniforms, accepted, path,
+                tokens, *, tree_len=None, stream=None):
+    """Verification of drafted tokens against the target's probabilities from
+    given random numbers (in place into accepted, path and tokens).
+
+    target_probs float32 [B, S1, V], row s the target's distribution after node
+    s; draft_probs float32 [B, S1, V], row s the distribution node s's children
+    were drawn from, or None (drafts not drawn at random); draft_tokens, parents
+    int32 [B, S1]; uniforms float32 [B, S1] in [0, 1): entry s tests node s,
+    entry 0 draws the last token. accepted int32 [B]: nodes on the accepted
+    branch, node 0 counted; path int32 [B, S1]: those nodes; tokens int32
+    [B, S1]: the new tokens, accepted[b] of them, the last one drawn from what
+    is left of the target's distribution; -1 behind."""
+    args, keep = _verify_args(target_probs, draft_probs, draft_tokens, parents, uniforms,
+                              accepted, path, tokens, tree_len)
+    _check(lib().pa_tree_verify(*args, _stream(stream)), "pa_tree_verify")
+    del keep
+
+
+def prepare_tree_verify(target_probs, draft_probs, draft_tokens, parents, uniforms, accepted,
+                        path, tokens, *, tree_len=None, stream=None):
+    """tree_verify() prepared once: returns a callable that launches the same
+    call on the same buffers."""
+    args, keep = _verify_args(target_probs, draft_probs, draft_tokens, parents, uniforms,
+                              accepted, path, tokens, tree_len)
+    return _Prepared(lib().pa_tree_verify, "pa_tree_verify", args, keep, stream)
+
+
+def _keep_args(key_cache, value_cache, key_scale_cache, block_table, kv_act_seqs, path, accepted,
+               new_act_seqs, tree_len, layout):
+    torch = _torch()
+    for t, n in ((key_cache, "key_cache"), (value_cache, "value_cache")):
+        _need(t, n, _fp8_types())
+    _need(key_scale_cache, "key_scale_cache", torch.float32)
+    for t, n in ((block_table, "block_table"), (kv_act_seqs, "kv_act_seqs"), (path, "path"),
+                 (accepted, "accepted"), (new_act_seqs, "new_act_seqs")):
+        _need(t, n, torch.int32)
+    if path.dim() != 2 or block_table.dim() != 2:
+        raise ValueError("path must be [B, S1] and block_table [B, max_blocks]")
+    B, S1 = path.shape
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must have one row a sequence")
+    for t, n in ((kv_act_seqs, "kv_act_seqs"), (accepted, "accepted"),
+                 (new_act_seqs, "new_act_seqs")):
+        _shape(t, n, B)
+    if tree_len is not None:
+        _need(tree_len, "tree_len", torch.int32)
+        _shape(tree_len, "tree_len", B)
+    NB, H, BS = _cache_dims(key_cache, layout)
+    _shape(value_cache, "value_cache", *key_cache.shape)
+    if key_scale_cache.numel() != NB * BS * H:
+        raise ValueError("key_scale_cache must have one scale a cache row")
+    _one_device(key_cache=key_cache, value_cache=value_cache, key_scale_cache=key_scale_cache,
+                block_table=block_table, kv_act_seqs=kv_act_seqs, path=path, accepted=accepted,
+                new_act_seqs=new_act_seqs, tree_len=tree_len)
+    args = (_ptr(key_cache), _ptr(value_cache), _ptr(key_scale_cache), _ptr(block_table),
+            _ptr(kv_act_seqs), _ptr(tree_len), _ptr(path), _ptr(accepted), _ptr(new_act_seqs), B,
+            S1, H, key_cache.shape[3], BS, NB, block_table.shape[1], layout)
+    keep = (key_cache, value_cache, key_scale_cache, block_table, kv_act_seqs, tree_len, path,
+            accepted, new_act_seqs)
+    return args, keep
+
+
+def cache_keep_path(key_cache, value_cache, key_scale_cache, block_table, kv_act_seqs, path,
+                    accepted, new_act_seqs, *, tree_len=None, layout: int = LAYOUT_BNBD,
+                    stream=None):
+    """The accepted branch kept in the cache, in place: the K/V codes and key
+    scales of the drafted nodes path[b][:accepted[b]] (tree_verify's, strictly
+    increasing) move to the first drafted positions, and new_act_seqs int32 [B]
+    (another tensor than kv_act_seqs) becomes the length that leaves."""
+    args, keep = _keep_args(key_cache, value_cache, key_scale_cache, block_table, kv_act_seqs,
+                            path, accepted, new_act_seqs, tree_len, layout)
+    _check(lib().pa_fp8_cache_keep_path(*args, _stream(stream)), "pa_fp8_cache_keep_path")
+    del keep
+
+
+def prepare_cache_keep_path(key_cache, value_cache, key_scale_cache, block_table, kv_act_seqs,
+                            path, accepted, new_act_seqs, *, tree_len=None,
+                            layout: int = LAYOUT_BNBD, stream=None):
+    """cache_keep_path() prepared once: returns a callable that launches the
+    same call on the same buffers."""
+    args, keep = _keep_args(key_cache, value_cache, key_scale_cache, block_table, kv_act_seqs,
+                            path, accepted, new_act_seqs, tree_len, layout)
+    return _Prepared(lib().pa_fp8_cache_keep_path, "pa_fp8_cache_keep_path", args, keep, stream)
+
+
 __all__ = [
     "LAYOUT_BSND", "LAYOUT_BNBD", "PaError", "build", "lib", "decode", "decode_workspace_size",
     "auto_s2_tile", "prepare_decode", "prepare_cache_quant_scatter",
     "DecodeWorkspace", "cache_scatter", "cache_quant_scatter", "quantize_rows",
-    "value_channel_scale",
+    "value_channel_scale", "qkv_norm_rope_append", "prepare_qkv_norm_rope_append",
+    "tree_decode", "prepare_tree_decode", "tree_decode_workspace_size", "TreeWorkspace",
+    "tree_verify", "prepare_tree_verify", "cache_keep_path", "prepare_cache_keep_path",
 ]
 
 

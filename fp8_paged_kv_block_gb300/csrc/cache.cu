@@ -21,20 +21,6 @@
 namespace pa {
 namespace {
 
-constexpr float kE4M3Max = 448.0f;
-
-__device__ __forceinline__ int64_t cache_row(int layout, int64_t blk, int64_t off, int64_t h,
-                                             int BS, int H)
-{
-    return layout == PA_LAYOUT_BSND ? (blk * BS + off) * H + h : (blk * H + h) * BS + off;
-}
-
-__device__ __forceinline__ int64_t load_slot(const void* slots, int slot_type, int64_t i)
-{
-    return slot_type == PA_INDEX_I64 ? __ldg(static_cast<const long long*>(slots) + i)
-                                     : static_cast<int64_t>(__ldg(static_cast<const int*>(slots) + i));
-}
-
 template <typename T>
 __device__ __forceinline__ void load4(const T* p, float (&x)[4]);
 

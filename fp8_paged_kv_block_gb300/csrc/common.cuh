@@ -32,6 +32,21 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// ---- paged cache addressing --------------------------------------------------
+constexpr float kE4M3Max = 448.0f;
+
+__device__ __forceinline__ int64_t cache_row(int layout, int64_t blk, int64_t off, int64_t h,
+                                             int BS, int H)
+{
+    return layout == PA_LAYOUT_BSND ? (blk * BS + off) * H + h : (blk * H + h) * BS + off;
+}
+
+__device__ __forceinline__ int64_t load_slot(const void* slots, int slot_type, int64_t i)
+{
+    return slot_type == PA_INDEX_I64 ? __ldg(static_cast<const long long*>(slots) + i)
+                                     : static_cast<int64_t>(__ldg(static_cast<const int*>(slots) + i));
+}
+
 // E4M3 encode of two floats, round to nearest even, saturating to +-448:
 // `lo` lands in the low byte, `hi` in the high byte.
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi)

@@ -1,0 +1,326 @@
+// norm_rope.cu -- per-head RMSNorm and rotation of q and k, E4M3 quantisation,
+// and the append of k and v to the paged cache, in one pass.
+//
+// A row is one head of one token: y = x * rsqrt(mean(x^2) + eps) * w, the
+// first rotary_dim channels rotated in pairs by the position's angles, scale =
+// max|y| / 448, codes E4M3(y * (448 / max|y|)). One read of each input value
+// and one write of each code: bound by those bytes on long prompts, by the
+// launch and one chain of dependent loads on a few tokens.
+//
+// A row's head_size values lie 8 to a lane, so that a BF16 row is one 16-byte
+// load per lane: 16 lanes per row of 128, two rows to a warp, and the sums and
+// maxima take four shuffles for both. A warp works on kRowSets of those at
+// once: that many more loads in flight.
+#include "common.cuh"
+
+#include <cmath>
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kRowSets = 2;
+
+struct NormRopeParams {
+    const void *q, *k, *v;
+    int64_t qs, ks, vs;               // elements from one token to the next
+    const void *qw, *kw;
+    int w_bf16;
+    float eps;
+    const float* cos_sin;
+    int rd;
+    int64_t max_pos;
+    const void* pos;
+    int pos_type;
+    uint8_t* q_codes;
+    float* q_scale;
+    uint8_t *kc, *vc;
+    const void* slots;
+    int slot_type;
+    float* k_scale;
+    const float* v_scale;
+    const int* token_batch;
+    int num_batches;
+    int64_t T;
+    int NQ, NKV;
+    int64_t num_blocks;
+    int BS, layout;
+};
+
+__device__ __forceinline__ void unpack_bf16(uint4 v, float (&x)[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ void load8(const float* p, float (&x)[8])
+{
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8])
+{
+    unpack_bf16(__ldg(reinterpret_cast<const uint4*>(p)), x);
+}
+
+// Eight codes of y * (448 / amax). Where the quotient leaves the float range
+// (amax below 2^-118) both sides are first taken times 2^100.
+__device__ __forceinline__ uint2 encode8(const float (&y)[8], float amax)
+{
+    if (amax == 0.0f) return make_uint2(0u, 0u);
+    const float up = amax < 0x1p-118f ? 0x1p100f : 1.0f;
+    const float inv = __fdiv_rn(kE4M3Max, amax * up);
+    uint2 r;
+    r.x = e4m3x4(y[0] * up * inv, y[1] * up * inv, y[2] * up * inv, y[3] * up * inv);
+    r.y = e4m3x4(y[4] * up * inv, y[5] * up * inv, y[6] * up * inv, y[7] * up * inv);
+    return r;
+}
+
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kThreads) qkv_norm_rope_append_kernel(const NormRopeParams p)
+{
+    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    const int lane = threadIdx.x & 31, sub = lane % LPR, d0 = 8 * sub;
+    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+    const int H = p.NQ + 2 * p.NKV;
+    const int64_t rows = p.T * H;
+    const int64_t r0 = warp * (kRowSets * RPW) + lane / LPR;
+
+    float x[kRowSets][8];
+    int64_t tok[kRowSets];
+    int head[kRowSets];
+#pragma unroll
+    for (int i = 0; i < kRowSets; ++i) {
+        const int64_t r = r0 + i * RPW;
+        tok[i] = r < rows ? r / H : -1;
+        head[i] = static_cast<int>(r - tok[i] * H);
+        if (tok[i] >= 0) {
+            const T* src = head[i] < p.NQ ? static_cast<const T*>(p.q) + tok[i] * p.qs + head[i] * D
+                           : head[i] < p.NQ + p.NKV
+                               ? static_cast<const T*>(p.k) + tok[i] * p.ks + (head[i] - p.NQ) * D
+                               : static_cast<const T*>(p.v) + tok[i] * p.vs + (head[i] - p.NQ - p.NKV) * D;
+            load8(src + d0, x[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRowSets; ++i) {
+        // every lane takes part in the shuffles, whatever its row is
+        const bool live = tok[i] >= 0, is_q = head[i] < p.NQ, is_v = head[i] >= p.NQ + p.NKV;
+        float ss = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss += x[i][e] * x[i][e];
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        // squares that leave the float range (or, with no eps to speak of, vanish
+        // below it) are taken of x * 2^-64 (2^64)
+        float sc = 1.0f;
+        const bool big = !(ss <= 1e38f), small = ss < 1e-30f && p.eps < 1e-20f;
+        if (__any_sync(0xffffffffu, big || small)) {
+            sc = big ? 0x1p-64f : (small ? 0x1p64f : 1.0f);
+            ss = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss += (x[i][e] * sc) * (x[i][e] * sc);
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        }
+        float y[8];
+        const void* w = is_q ? p.qw : p.kw;
+        const bool norm = live && !is_v && w != nullptr;
+        if (norm) {
+            const float ms = ss * (1.0f / D) + p.eps * sc * sc;
+            const float inv = ms == 0.0f ? 0.0f : __fdiv_rn(1.0f, __fsqrt_rn(ms));
+            float wt[8];
+            if (p.w_bf16) load8(static_cast<const __nv_bfloat16*>(w) + d0, wt);
+            else load8(static_cast<const float*>(w) + d0, wt);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = x[i][e] * sc * inv * wt[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = x[i][e];
+        }
+        if (p.rd > 0) {
+            const int half = p.rd >> 1;
+            const bool rot = live && !is_v && d0 < p.rd;
+            const float* cs = nullptr;
+            if (rot) {
+                int64_t pos = load_slot(p.pos, p.pos_type, tok[i]);
+                pos = pos < 0 ? 0 : (pos >= p.max_pos ? p.max_pos - 1 : pos);
+                cs = p.cos_sin + pos * p.rd;
+            }
+            if constexpr (INTER) {
+                if (rot) {
+                    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + (d0 >> 1)));
+                    const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half + (d0 >> 1)));
+                    const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float a = y[2 * e], b = y[2 * e + 1];
+                        y[2 * e] = a * cc[e] - b * sn[e];
+                        y[2 * e + 1] = b * cc[e] + a * sn[e];
+                    }
+                }
+            } else {
+                // channel i's partner sits rd / 16 lanes up or down
+                const int step = half >> 3;
+                const bool low = d0 < half;
+                const int from = lane + (rot ? (low ? step : -step) : 0);
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, y[e], from);
+                if (rot) {
+                    const int j = low ? d0 : d0 - half;
+                    float c[8], s[8];
+                    load8(cs + j, c);
+                    load8(cs + half + j, s);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = y[e] * c[e] + (low ? -o[e] : o[e]) * s[e];
+                }
+            }
+        }
+        float amax = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (!live) continue;
+        if (is_q) {
+            const int64_t row = tok[i] * p.NQ + head[i];
+            *reinterpret_cast<uint2*>(p.q_codes + row * D + d0) = encode8(y, amax);
+            if (sub == 0) p.q_scale[row] = __fdiv_rn(amax, kE4M3Max);
+            continue;
+        }
+        const int64_t s = load_slot(p.slots, p.slot_type, tok[i]);
+        if (s < 0 || s >= p.num_blocks * p.BS) continue;
+        const int h = head[i] - p.NQ - (is_v ? p.NKV : 0);
+        const int64_t row = cache_row(p.layout, s / p.BS, s % p.BS, h, p.BS, p.NKV);
+        if (!is_v) {
+            *reinterpret_cast<uint2*>(p.kc + row * D + d0) = encode8(y, amax);
+            if (sub == 0) p.k_scale[row] = __fdiv_rn(amax, kE4M3Max);
+        } else {
+            int tb = __ldg(p.token_batch + tok[i]);
+            tb = tb < 0 ? 0 : (tb >= p.num_batches ? p.num_batches - 1 : tb);
+            float sc[8], z[8];
+            load8(p.v_scale + (static_cast<int64_t>(tb) * p.NKV + h) * D + d0, sc);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = sc[e] == 0.0f ? 0.0f : __fdiv_rn(y[e], sc[e]);
+            uint2 c;
+            c.x = e4m3x4(z[0], z[1], z[2], z[3]);
+            c.y = e4m3x4(z[4], z[5], z[6], z[7]);
+            *reinterpret_cast<uint2*>(p.vc + row * D + d0) = c;
+        }
+    }
+}
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+template <typename T, int D>
+void launch(const NormRopeParams& p, bool inter, cudaStream_t st)
+{
+    constexpr int per_block = kThreads / 32 * kRowSets * (32 / (D / 8));
+    const int64_t rows = p.T * (p.NQ + 2 * p.NKV);
+    const unsigned grid = static_cast<unsigned>((rows + per_block - 1) / per_block);
+    if (inter) qkv_norm_rope_append_kernel<T, D, true><<<grid, kThreads, 0, st>>>(p);
+    else qkv_norm_rope_append_kernel<T, D, false><<<grid, kThreads, 0, st>>>(p);
+}
+
+template <typename T>
+void launch_d(const NormRopeParams& p, int D, bool inter, cudaStream_t st)
+{
+    if (D == 64) launch<T, 64>(p, inter, st);
+    else if (D == 128) launch<T, 128>(p, inter, st);
+    else launch<T, 256>(p, inter, st);
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" pa_status pa_fp8_qkv_norm_rope_append(
+    const void* q, const void* k, const void* v, int in_dtype, int64_t q_stride, int64_t k_stride,
+    int64_t v_stride, const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+    const float* cos_sin, int rotary_dim, int64_t max_position, int interleaved,
+    const void* positions, int pos_type, void* q_codes, float* q_scale, void* key_cache,
+    void* value_cache, const void* slot_mapping, int slot_type, float* key_scale_cache,
+    const float* v_scale, const int32_t* token_batch, int num_batches, int64_t num_tokens, int NQ,
+    int NKV, int head_size, int64_t num_blocks, int block_size, int layout, void* stream)
+{
+    const char* name = "pa_fp8_qkv_norm_rope_append";
+    PA_REQUIRE(q && k && v && q_codes && q_scale && key_cache && value_cache && slot_mapping &&
+                   key_scale_cache && v_scale && token_batch,
+               PA_ERR_NULLPTR, "%s: NULL tensor pointer", name);
+    PA_REQUIRE(num_tokens >= 0 && NQ > 0 && NKV > 0 && head_size > 0 && num_blocks > 0 &&
+                   block_size > 0 && num_batches > 0,
+               PA_ERR_INVALID, "%s: empty or negative size", name);
+    PA_REQUIRE(head_size == 64 || head_size == 128 || head_size == 256, PA_ERR_UNSUPPORTED,
+               "%s: head_size %d (64, 128 and 256 are built)", name, head_size);
+    PA_REQUIRE(rotary_dim >= 0 && rotary_dim <= head_size, PA_ERR_INVALID,
+               "%s: rotary_dim %d outside [0, head_size]", name, rotary_dim);
+    PA_REQUIRE(rotary_dim % (interleaved ? 8 : 16) == 0, PA_ERR_UNSUPPORTED,
+               "%s: rotary_dim %d (a multiple of 16, or of 8 if interleaved)", name, rotary_dim);
+    PA_REQUIRE(rotary_dim == 0 || (cos_sin && positions), PA_ERR_NULLPTR,
+               "%s: NULL cos_sin or positions", name);
+    PA_REQUIRE(rotary_dim == 0 || max_position > 0, PA_ERR_INVALID, "%s: empty cos_sin", name);
+    PA_REQUIRE(in_dtype == PA_DTYPE_F32 || in_dtype == PA_DTYPE_BF16, PA_ERR_INVALID,
+               "%s: unknown input dtype %d", name, in_dtype);
+    PA_REQUIRE(weight_dtype == PA_DTYPE_F32 || weight_dtype == PA_DTYPE_BF16, PA_ERR_INVALID,
+               "%s: unknown weight dtype %d", name, weight_dtype);
+    PA_REQUIRE((slot_type == PA_INDEX_I32 || slot_type == PA_INDEX_I64) &&
+                   (pos_type == PA_INDEX_I32 || pos_type == PA_INDEX_I64),
+               PA_ERR_INVALID, "%s: unknown slot or position type", name);
+    PA_REQUIRE(layout == PA_LAYOUT_BSND || layout == PA_LAYOUT_BNBD, PA_ERR_INVALID,
+               "%s: unknown layout %d", name, layout);
+    PA_REQUIRE(std::isfinite(eps) && eps >= 0.0f, PA_ERR_INVALID, "%s: eps is negative or not finite", name);
+    const int64_t per16 = in_dtype == PA_DTYPE_F32 ? 4 : 8;
+    PA_REQUIRE(aligned(q, 16) && aligned(k, 16) && aligned(v, 16) && q_stride % per16 == 0 &&
+                   k_stride % per16 == 0 && v_stride % per16 == 0,
+               PA_ERR_INVALID, "%s: q, k and v tokens must start on 16-byte boundaries", name);
+    PA_REQUIRE(aligned(q_weight, 16) && aligned(k_weight, 16) && aligned(cos_sin, 16) &&
+                   aligned(v_scale, 16) && aligned(q_codes, 8) && aligned(key_cache, 8) &&
+                   aligned(value_cache, 8) && aligned(q_scale, 4) && aligned(key_scale_cache, 4),
+               PA_ERR_INVALID, "%s: misaligned pointer", name);
+    PA_REQUIRE(num_tokens * (static_cast<int64_t>(NQ) + 2 * NKV) <= (static_cast<int64_t>(1) << 32),
+               PA_ERR_UNSUPPORTED, "%s: more than 2^32 head rows", name);
+    if (num_tokens == 0) return PA_OK;
+    NormRopeParams p;
+    p.q = q; p.k = k; p.v = v;
+    p.qs = q_stride; p.ks = k_stride; p.vs = v_stride;
+    p.qw = q_weight; p.kw = k_weight;
+    p.w_bf16 = weight_dtype == PA_DTYPE_BF16;
+    p.eps = eps;
+    p.cos_sin = cos_sin;
+    p.rd = rotary_dim;
+    p.max_pos = max_position;
+    p.pos = positions;
+    p.pos_type = pos_type;
+    p.q_codes = static_cast<uint8_t*>(q_codes);
+    p.q_scale = q_scale;
+    p.kc = static_cast<uint8_t*>(key_cache);
+    p.vc = static_cast<uint8_t*>(value_cache);
+    p.slots = slot_mapping;
+    p.slot_type = slot_type;
+    p.k_scale = key_scale_cache;
+    p.v_scale = v_scale;
+    p.token_batch = token_batch;
+    p.num_batches = num_batches;
+    p.T = num_tokens;
+    p.NQ = NQ;
+    p.NKV = NKV;
+    p.num_blocks = num_blocks;
+    p.BS = block_size;
+    p.layout = layout;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (in_dtype == PA_DTYPE_F32) launch_d<float>(p, head_size, interleaved != 0, st);
+    else launch_d<__nv_bfloat16>(p, head_size, interleaved != 0, st);
+    return check_launch(name);
+}

@@ -486,6 +486,162 @@ PA_API pa_status pa_mla_sparse_decode_kvc(const void* q_nope, const void* q_rope
                                           int max_blocks_per_seq, float softmax_scale,
                                           int s2_tile, int* status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A speculative decode step over the paged FP8 cache. A sequence's drafted
+ * tokens form a tree of at most S1 nodes: node 0 is the last token that is
+ * already accepted (its K/V is not in the cache yet), every other node s has
+ * a parent of a lower index. Of sequence b, n = tree_len[b] nodes are in use
+ * (tree_len NULL: all S1; values are clamped to [0, S1]); node j's K/V sits
+ * at position ctx + j, ctx = kv_act_seqs[b] - n, kv_act_seqs counting the
+ * nodes in. The pages have no counterpart to the four calls; they use the
+ * pages' cache layouts, scales and codes. One step is
+ *   pa_fp8_qkv_norm_rope_append  the nodes' q to FP8, k and v into the cache;
+ *   pa_fp8_tree_decode           each node attends to the context and to the
+ *                                nodes its mask row names;
+ *   pa_tree_verify               which branch the target's probabilities
+ *                                accept, and the token after it;
+ *   pa_fp8_cache_keep_path       the accepted branch's K/V moved to positions
+ *                                ctx, ctx + 1, ...
+ * ------------------------------------------------------------------------ */
+
+/* ------------------------------------------------------------------------
+ * pa_fp8_qkv_norm_rope_append -- per-head norm and rotation of q and k,
+ * quantisation of q, and the append of k and v, in one pass. For token t,
+ * head h, x = q[t][h] or k[t][h] (head_size values, FP32 arithmetic):
+ *   y = x / sqrt(mean(x^2) + eps) * weight         (weight NULL: y = x)
+ *   pairs (a, b) of the first rotary_dim channels: (a c - b s, b c + a s)
+ *     with c = cos_sin[pos][i], s = cos_sin[pos][rotary_dim / 2 + i], pair i
+ *     being channels (i, i + rotary_dim / 2), or (2 i, 2 i + 1) if
+ *     `interleaved`; pos = positions[t] clamped to [0, max_position)
+ *   scale = max|y| / 448, codes E4M3(y * (448 / max|y|)), round to nearest
+ *     even, saturating (max 0: scale 0, codes 0)
+ * q's codes and scales go to q_codes [T, NQ, head_size] and q_scale [T, NQ];
+ * k's to the cache row of slot_mapping[t] and key_scale_cache; v is encoded
+ * as pa_fp8_cache_quant_scatter does, E4M3(v / v_scale[token_batch[t]]). A
+ * slot outside [0, num_blocks * block_size) writes neither k nor v (q is
+ * still written). With duplicate slots which write wins is undefined.
+ * q, k, v      FP32 or BF16 (in_dtype) [T, NQ or NKV, head_size], heads
+ *              contiguous, tokens *_stride elements apart (views of one
+ *              projection's output qualify); 16-byte aligned, strides a
+ *              multiple of 16 bytes.
+ * q_weight, k_weight  [head_size] of weight_dtype, or NULL; 16-byte aligned.
+ * cos_sin      float [max_position, rotary_dim], 16-byte aligned; not read
+ *              (may be NULL, as positions) with rotary_dim 0.
+ * positions    int32 or int64 [T] (pos_type).
+ * head_size    64, 128 or 256 (else PA_ERR_UNSUPPORTED). rotary_dim at most
+ *              head_size, a multiple of 16, or of 8 if interleaved (else
+ *              PA_ERR_UNSUPPORTED).
+ * q_codes, caches 8-byte aligned, v_scale 16-byte aligned. Slots, layout,
+ * token_batch and v_scale as in pa_fp8_cache_quant_scatter. num_tokens 0
+ * enqueues nothing.
+ * ------------------------------------------------------------------------ */
+PA_API pa_status pa_fp8_qkv_norm_rope_append(
+    const void* q, const void* k, const void* v, int in_dtype, int64_t q_stride, int64_t k_stride,
+    int64_t v_stride, const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+    const float* cos_sin, int rotary_dim, int64_t max_position, int interleaved,
+    const void* positions, int pos_type, void* q_codes, float* q_scale, void* key_cache,
+    void* value_cache, const void* slot_mapping, int slot_type, float* key_scale_cache,
+    const float* v_scale, const int32_t* token_batch, int num_batches, int64_t num_tokens, int NQ,
+    int NKV, int head_size, int64_t num_blocks, int block_size, int layout, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_fp8_tree_decode -- attention of a tree of drafted tokens over the paged
+ * FP8 cache. For row (b, s < n, h), kv head h / (NQ / NKV), over the keys
+ * j < ctx and the nodes ctx + j, j < n, with tree_mask[b][s][j] != 0:
+ *   S_j = (Q_fp8 . K_fp8,j) * q_scale * k_scale_j * softmax_scale
+ *   out = BF16((sum_j exp(S_j - M) V_fp8,j) * v_scale / sum_j exp(S_j - M))
+ * with M the maximum of the row's S_j. P = exp(S - M) is not quantised to
+ * FP8 as pa_fp8_decode's is: it enters the second contraction as FP16 (see
+ * tree.cu), the sums are FP32. A row that sees no key, the rows s >= n of a
+ * sequence and sequences with kv_act_seqs <= 0 get zeros.
+ * tree_mask    bytes [B, S1, S1], sequences mask_stride bytes apart (0: one
+ *              mask for all). Ancestors and the node itself, as a rule; any
+ *              mask is accepted, entries j >= n are not read.
+ * Other arguments as in pa_fp8_decode: kv_act_seqs is clamped to
+ * max_blocks_per_seq * block_size, n to kv_act_seqs; block ids outside
+ * [0, num_blocks) read block 0. Cache bytes at positions >= kv_act_seqs[b]
+ * do not matter; E4M3 NaN codes below it are out of contract.
+ * D, block_size  128 and 128 (else PA_ERR_UNSUPPORTED). S1 at most 128, NQ /
+ * NKV at most 128, B at most 1024 (else PA_ERR_UNSUPPORTED).
+ * workspace    at least pa_fp8_tree_decode_workspace_size() bytes, 256-byte
+ *              aligned, its first 256 bytes zero before the first call (every
+ *              call leaves them so). Calls that share a workspace must not
+ *              overlap in time: two captured graphs that may run at once need
+ *              one each. Its first word is an error word as pa_fp8_decode's:
+ *              a wait that gave up (about 2 s) sets a bit, the output is then
+ *              undefined.
+ * Alignment: q, k_cache, v_cache, v_scale and out 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+PA_API pa_status pa_fp8_tree_decode_workspace_size(int B, int S1, int NQ, int NKV, int D,
+                                                   size_t* bytes);
+
+PA_API pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, const void* k_cache,
+                                    const float* k_scale, const void* v_cache,
+                                    const float* v_scale, const int32_t* block_table,
+                                    const int32_t* kv_act_seqs, const int32_t* tree_len,
+                                    const uint8_t* tree_mask, int64_t mask_stride, void* out,
+                                    int B, int S1, int NQ, int NKV, int D, int block_size,
+                                    int64_t num_blocks, int max_blocks_per_seq, int layout,
+                                    float softmax_scale, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_tree_verify -- drafted tokens against the target's probabilities, from
+ * given random numbers (so that the same numbers give the same tokens). The
+ * walk starts at node cur = 0 with R = target_probs[b][0], z = 1 and takes
+ * the nodes s = 1 .. n-1 with parents[b][s] == cur in index order; node s
+ * holds token x = draft_tokens[b][s]:
+ *   accepted if u[b][s] * z * Q(x) < R(x) (products in FP64, left to right),
+ *     Q = draft_probs[b][cur], the distribution cur's children were drawn
+ *     from (independently); then cur = s, R = target_probs[b][s], z = 1;
+ *   else R = max(R - z Q, 0) (FP32: product rounded, then difference) and z =
+ *     FP32(sum of R).
+ * Without draft_probs (NULL: the drafts were not drawn at random) node s is
+ * accepted if u[b][s] * z < R(x), else z = z - R(x) (FP64) and R(x) = 0.
+ * At the end a token is drawn from R: the first i with sum_{k <= i} W_k >
+ * floor(u[b][0] * sum W), W_k = floor(min(R_k, 1) * 2^45) as integers, so
+ * that no order of summation changes it (sums of R use W too). If all W are
+ * 0, target_probs[b][cur] takes R's place, and if its W are 0 the token is
+ * -1. Tokens so drawn follow the target's distribution.
+ * target_probs, draft_probs  float [B, S1, V]; values outside [0, 1] are
+ *              clamped where they enter a sum, NaN counts as 0.
+ * draft_tokens int32 [B, S1] (node 0's is not read); a token outside [0, V)
+ *              is never accepted and changes nothing.
+ * parents      int32 [B, S1]; a node whose parent is not a lower index is
+ *              never reached.
+ * uniforms     float [B, S1] in [0, 1).
+ * accepted     int32 [B]: nodes on the accepted branch, node 0 counted (0 for
+ *              a sequence with n = 0).
+ * path         int32 [B, S1]: the branch's nodes, path[b][0] = 0; -1 behind.
+ * tokens       int32 [B, S1]: the accepted nodes' tokens, then the drawn one
+ *              (accepted[b] in all); -1 behind.
+ * S1 at most 1024, V at most 262144 (else PA_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------ */
+PA_API pa_status pa_tree_verify(const float* target_probs, const float* draft_probs,
+                                const int32_t* draft_tokens, const int32_t* parents,
+                                const float* uniforms, const int32_t* tree_len, int B, int S1,
+                                int V, int32_t* accepted, int32_t* path, int32_t* tokens,
+                                void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_fp8_cache_keep_path -- the accepted branch's K and V codes and key
+ * scales moved from positions ctx + path[b][i] to ctx + i, i < accepted[b],
+ * in place, and new_act_seqs[b] = ctx + accepted[b] (accepted is clamped to
+ * [0, n]). path rows must increase strictly, as pa_tree_verify's do; what
+ * other positions hold stays. A move is skipped where path[b][i] is outside
+ * [0, n) or one of its two positions has a block id outside [0, num_blocks)
+ * or lies past the block table.
+ * head_size    a multiple of 16; caches 16-byte aligned. S1 at most 1024.
+ * new_act_seqs int32 [B], not kv_act_seqs itself.
+ * ------------------------------------------------------------------------ */
+PA_API pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache,
+                                        float* key_scale_cache, const int32_t* block_table,
+                                        const int32_t* kv_act_seqs, const int32_t* tree_len,
+                                        const int32_t* path, const int32_t* accepted,
+                                        int32_t* new_act_seqs, int B, int S1, int NKV,
+                                        int head_size, int block_size, int64_t num_blocks,
+                                        int max_blocks_per_seq, int layout, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
