@@ -1,7 +1,10 @@
-// status.cu -- status codes, per-thread error text, device queries.
+// status.cu -- status codes, per-thread error text, device queries, tensor maps
+// of the paged caches.
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
+
+#include <cudaTypedefs.h>
 
 #include "common.cuh"
 
@@ -57,6 +60,40 @@ int device_sm_count()
         cache[dev] = n;
     }
     return cache[dev];
+}
+
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
+// 2-D byte view of a paged cache: rows of `inner` bytes, box 128 x 128.
+pa_status make_cache_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows)
+{
+    auto enc = tensor_map_encoder();
+    PA_REQUIRE(enc != nullptr, PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    cuuint64_t dims[2] = {inner, rows};
+    cuuint64_t strides[1] = {inner};
+    cuuint32_t box[2] = {128, 128};
+    cuuint32_t estr[2] = {1, 1};
+    // L2 promotion to 128 bytes, the row size: with PA_BSND a row is one head's
+    // 128 bytes of a token, and a larger promotion would also fetch the next
+    // head's bytes, which another CTA reads at another time
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
+                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    PA_REQUIRE(r == CUDA_SUCCESS, PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return PA_OK;
 }
 
 }  // namespace pa

@@ -1,9 +1,44 @@
 // tree.cu -- attention of a tree of drafted tokens over the paged FP8 cache.
+//
+// The query rows that share a kv head are the S1 drafted tokens x the group of
+// query heads: R = n G rows of sequence b, each attending to the context and
+// to the drafted tokens its mask row names. Rows are taken in items of at most
+// 256 (two tensor tiles of 128 rows), so that a K/V block read serves 256 rows.
+//
+//   S = Q_fp8 K_fp8^T                 tcgen05 kind::f8f6f4, 128 x 128 x 128
+//   x = S k_scale q_scale scale log2e, -inf where the row does not see the key
+//   P = 2^(x - m + 7), L += sum P     one thread per row, FP32
+//   O += FP16(P) V                    tcgen05 kind::f16, P from tensor memory
+//   out = BF16(O v_scale / L)
+//
+// P enters the second contraction as FP16 (half a step: 2^-11) and V as the
+// FP16 values of its E4M3 codes, which are exact: P in E4M3 as in
+// pa_fp8_decode would be off by up to 2^-4 where few keys count. The reference
+// m is the running maximum, but raised only when a tile's maximum lies more
+// than 2^8 above it, which spares O's rescaling in tensor memory on most tiles;
+// P then stays below 2^15, inside FP16, and a key 2^31 below the maximum still
+// counts.
+//
+// A CTA has two streams of (S, P, O) in tensor memory, 256 columns each, and a
+// softmax warpgroup for each. An item of more than 128 rows runs its two row
+// tiles as the streams, every K/V block read once for both; a smaller item
+// runs even and odd blocks as the streams and joins them at the end. While one
+// stream's softmax runs, the other's contractions do.
+//   warps 0-3, 4-7   softmax of stream 0, 1 (thread = row = tensor memory lane)
+//   warp 8           K and V blocks by TMA, key scales by cp.async
+//   warp 9           issues the MMAs of whichever stream is ready
+//   warps 10, 11     V codes to FP16 in shared memory, zeros behind the end
+//
+// The blocks of all items, in (sequence, kv head, item, block) order, a block
+// of a two-tile item counting twice, are dealt to the CTAs in equal runs; items
+// that a run's end cuts leave FP32 partial sums, which a second kernel joins.
 #include "common.cuh"
 
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include <cmath>
+#include <cstddef>
 
 namespace pa {
 namespace {
@@ -13,92 +48,809 @@ constexpr int kBS = 128;
 constexpr int kMaxNodes = 128;
 constexpr int kMaxGroup = 128;
 constexpr int kMaxB = 1024;
-constexpr size_t kWsHeader = 256;
+constexpr int kMaxCtas = 192;
+constexpr int kItemRows = 256;
+constexpr int kTile = kBS * kD;              // bytes of a block of codes
+constexpr int kKStages = 4, kVStages = 3, kHStages = 2;
+constexpr int kProdWarp = 8, kMmaWarp = 9, kConvWarp = 10, kConvWarps = 2;
+constexpr int kThreads = (kConvWarp + kConvWarps) * 32;
+constexpr uint32_t kTmemCols = 512, kOCol = 256;
+constexpr float kRaise = 8.0f;               // log2 units: see the top of the file
+constexpr float kShift = 7.0f;
+
+// Workspace: error word, then at kCumOff the weights before each sequence
+// (int64 [B + 1]), then per CTA two partial items: O [rows][128], m, l [rows].
+constexpr size_t kCumOff = 256;
+constexpr size_t kPartOff = kCumOff + (kMaxB + 1 + 31) / 32 * 32 * sizeof(int64_t);
 
 struct TreeParams {
     const uint8_t* q;
     const float* q_scale;
-    const uint8_t* kc;
     const float* k_scale;
-    const uint8_t* vc;
     const float* v_scale;
     const int *bt, *act, *len;
     const uint8_t* mask;
     int64_t mask_stride;
     __nv_bfloat16* out;
-    int S1, NQ, NKV;
+    int* err;
+    int64_t* cum;
+    float* part;
+    int part_rows;                           // rows of a partial item
+    int B, S1, NQ, NKV, G;
     int64_t num_blocks;
-    int max_blocks, layout;
+    int max_blocks, layout, ctas;
     float scale_log2;
 };
 
-__device__ __forceinline__ float e4m3_to_float(uint8_t c)
+struct TreeSmem {
+    alignas(1024) uint8_t k[kKStages][kTile];
+    alignas(1024) uint8_t v[kVStages][kTile];
+    alignas(1024) uint8_t vh[kHStages][2][kTile];   // FP16, channels 0-63 and 64-127
+    alignas(1024) uint8_t q[2][kTile];
+    alignas(16) float ks[kKStages][kBS];
+    float ml[2][2][128];                     // m and l of the two streams
+    int64_t cum[kMaxB + 1];
+    int64_t warp_sum[kThreads / 32];
+    int act[kMaxB];
+    uint8_t n[kMaxB];
+    uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+    uint64_t h_full[kHStages], h_empty[kHStages];
+    uint64_t s_full[2], p_full[2], o_done[2], q_full, drain;
+    uint32_t tmem;
+    int abort;
+};
+static_assert(sizeof(TreeSmem) + 1024 <= 232448, "tree decode shared memory over budget");
+
+// ---- the schedule -----------------------------------------------------------------
+struct Seg {
+    int b, h, row0, rows;                    // the item
+    int t0, t1, tiles;                       // its blocks that this run has
+    bool first, dual;                        // first of the CTA's run; two row tiles
+};
+
+struct Run {
+    int64_t pos, hi;
+    int b;
+    bool fresh;
+};
+
+__device__ __forceinline__ int tiles_of(int act) { return (act + kBS - 1) / kBS; }
+// weight of one kv head's block: 2 for every item of 129..256 rows, 1 for a smaller one
+__device__ __forceinline__ int head_weight(int rows) { return (rows + 127) / 128; }
+
+__device__ __forceinline__ int64_t run_begin(int64_t total, int c, int ctas) { return total * c / ctas; }
+// the CTA whose run holds position pos
+__device__ __forceinline__ int cta_of(int64_t total, int64_t pos, int ctas)
 {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-    return __half2float(*reinterpret_cast<const __half*>(&h));
+    return static_cast<int>(((pos + 1) * ctas - 1) / total);
 }
 
-// One CTA per query row (b, s, h): tiles of 128 keys, thread = key for the
-// scores, thread = channel for the output; running maximum and sum.
-__global__ void __launch_bounds__(kD) tree_decode_kernel(const TreeParams p)
+// the item at `pos` inside sequence b, whose first position is `base0`
+__device__ __forceinline__ void locate(int64_t pos, int64_t base0, int rows_b, int tiles, Seg& s, int64_t& base)
 {
-    __shared__ float qf[kD], pr[kD], red[4];
-    __shared__ int64_t rows[kD];
-    const int tid = threadIdx.x, warp = tid >> 5;
-    const int64_t row = blockIdx.x;
-    const int h = static_cast<int>(row % p.NQ);
-    const int64_t t = row / p.NQ;
-    const int b = static_cast<int>(t / p.S1), s = static_cast<int>(t - static_cast<int64_t>(b) * p.S1);
-    const int h2 = h / (p.NQ / p.NKV);
-    const int act = max(min(static_cast<int64_t>(__ldg(p.act + b)), static_cast<int64_t>(p.max_blocks) * kBS), static_cast<int64_t>(0));
-    int n = p.len ? __ldg(p.len + b) : p.S1;
-    n = min(max(n, 0), min(p.S1, act));
-    const int ctx = act - n;
-    qf[tid] = e4m3_to_float(p.q[row * kD + tid]) * p.q_scale[row] * p.scale_log2;
-    __syncthreads();
-    float M = -INFINITY, L = 0.0f, o = 0.0f;
-    if (s < n) {
-        for (int j0 = 0; j0 < act; j0 += kD) {
-            const int j = j0 + tid;
-            bool see = j < act;
-            if (see && j >= ctx) see = p.mask[b * p.mask_stride + static_cast<int64_t>(s) * p.S1 + (j - ctx)] != 0;
-            float x = -INFINITY;
-            int64_t r = 0;
-            if (j < act) {
-                int blk = __ldg(p.bt + static_cast<int64_t>(b) * p.max_blocks + j / kBS);
-                if (blk < 0 || blk >= p.num_blocks) blk = 0;
-                r = cache_row(p.layout, blk, j % kBS, h2, kBS, p.NKV);
+    const int hw = head_weight(rows_b);
+    const int64_t per_head = static_cast<int64_t>(hw) * tiles;
+    const int64_t rem = pos - base0;
+    s.h = static_cast<int>(rem / per_head);
+    const int64_t in_head = rem - s.h * per_head;
+    const int item = min(static_cast<int>(in_head / (2 * static_cast<int64_t>(tiles))), (hw - 1) / 2);
+    s.row0 = item * kItemRows;
+    s.rows = min(rows_b - s.row0, kItemRows);
+    s.dual = s.rows > 128;
+    s.tiles = tiles;
+    base = base0 + s.h * per_head + static_cast<int64_t>(item) * 2 * tiles;
+}
+
+__device__ __forceinline__ bool next_seg(const int64_t* cum, const int* act, const uint8_t* n, int G, Run& r, Seg& s)
+{
+    while (r.pos < r.hi) {
+        while (cum[r.b + 1] <= r.pos) ++r.b;
+        s.b = r.b;
+        int64_t base;
+        locate(r.pos, cum[r.b], n[r.b] * G, tiles_of(act[r.b]), s, base);
+        const int w = s.dual ? 2 : 1;
+        const int64_t end = base + static_cast<int64_t>(w) * s.tiles;
+        s.t0 = static_cast<int>((r.pos - base + w - 1) / w);
+        s.t1 = r.hi >= end ? s.tiles : static_cast<int>((r.hi - base + w - 1) / w);
+        s.first = r.fresh;
+        r.fresh = false;
+        r.pos = end < r.hi ? end : r.hi;
+        if (s.t0 < s.t1) return true;
+    }
+    return false;
+}
+
+// ---- small device helpers ------------------------------------------------------------
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn)
+{
+    return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// D(tmem) (+)= A(tmem, FP16 pairs) * B(smem, FP16): K = 16 per MMA.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t codes_to_half2(uint32_t two)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, w, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+
+// Index of the first row of item `s`, row r of it, in q and out.
+__device__ __forceinline__ int64_t q_row(const TreeParams& p, const Seg& s, int r)
+{
+    const int rr = s.row0 + r, node = rr / p.G;
+    return (static_cast<int64_t>(s.b) * p.S1 + node) * p.NQ + s.h * p.G + (rr - node * p.G);
+}
+
+__device__ __forceinline__ float* part_of(const TreeParams& p, int cta, bool first)
+{
+    return p.part + (static_cast<int64_t>(cta) * 2 + (first ? 0 : 1)) * p.part_rows * (kD + 2);
+}
+
+// ---- the warps' parts ------------------------------------------------------------------
+__device__ void producer(TreeSmem& sm, const TreeParams& p, const CUtensorMap* tk, const CUtensorMap* tv, Run run,
+                         int lane)
+{
+    const uint64_t pol = l2_evict_first_policy();
+    Seg s;
+    int kc = 0, vc = 0;                      // blocks requested so far
+    bool stop = false;
+    while (!stop && next_seg(sm.cum, sm.act, sm.n, p.G, run, s)) {
+        const int* row = p.bt + static_cast<int64_t>(s.b) * p.max_blocks;
+        int ids = 0;
+        for (int t = s.t0; t < s.t1; ++t) {
+            const int at = (t - s.t0) & 31;
+            if (at == 0) {
+                ids = t + lane < s.t1 ? __ldg(row + t + lane) : 0;
+                if (ids < 0 || ids >= p.num_blocks) ids = 0;
             }
-            if (see) {
-                float d = 0.0f;
-                for (int c = 0; c < kD; ++c) d += qf[c] * e4m3_to_float(p.kc[r * kD + c]);
-                x = d * p.k_scale[r];
+            const int64_t blk = __shfl_sync(0xffffffffu, ids, at);
+            const int x = p.layout == PA_LAYOUT_BSND ? s.h * kD : 0;
+            const int y = static_cast<int>(p.layout == PA_LAYOUT_BSND ? blk * kBS : (blk * p.NKV + s.h) * kBS);
+            const int kslot = kc % kKStages, vslot = vc % kVStages;
+            if (!mbar_wait(&sm.k_empty[kslot], ((kc / kKStages) & 1) ^ 1, p.err, 1, &sm.abort)) stop = true;
+            if (__any_sync(0xffffffffu, stop)) {
+                stop = true;
+                break;
             }
-            float m = warp_max_f32(x);
-            if ((tid & 31) == 0) red[warp] = m;
-            __syncthreads();
-            m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-            const float Mn = fmaxf(M, m), ref = Mn == -INFINITY ? 0.0f : Mn;
-            const float f = ex2(M - ref);
-            pr[tid] = ex2(x - ref);
-            rows[tid] = r;
-            __syncthreads();
-            M = Mn;
-            L *= f;
-            o *= f;
-            const int lim = min(kD, act - j0);
-            for (int k = 0; k < lim; ++k) {
-                L += pr[k];
-                o += pr[k] * e4m3_to_float(p.vc[rows[k] * kD + tid]);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sm.k_full[kslot], kTile);
+                tma_load_2d(sm.k[kslot], tk, x, y, &sm.k_full[kslot], pol);
             }
-            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = lane + 32 * i;
+                cp_async4(&sm.ks[kslot][j], p.k_scale + cache_row(p.layout, blk, j, s.h, kBS, p.NKV), 4);
+            }
+            cp_async_arrive_noinc(&sm.k_full[kslot]);
+            ++kc;
+            if (!mbar_wait(&sm.v_empty[vslot], ((vc / kVStages) & 1) ^ 1, p.err, 2, &sm.abort)) stop = true;
+            if (__any_sync(0xffffffffu, stop)) {
+                stop = true;
+                break;
+            }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&sm.v_full[vslot], kTile);
+                tma_load_2d(sm.v[vslot], tv, x, y, &sm.v_full[vslot], pol);
+            }
+            ++vc;
+            __syncwarp();
         }
     }
-    const float vs = p.v_scale[(static_cast<int64_t>(b) * p.NKV + h2) * kD + tid];
-    p.out[row * kD + tid] = __float2bfloat16_rn(L > 0.0f ? o * vs / L : 0.0f);
+    // every copy has landed before this CTA's shared memory is given up
+    for (int i = max(0, kc - kKStages); i < kc; ++i)
+        mbar_wait_drain(&sm.k_full[i % kKStages], (i / kKStages) & 1, p.err, 256);
+    for (int i = max(0, vc - kVStages); i < vc; ++i)
+        mbar_wait_drain(&sm.v_full[i % kVStages], (i / kVStages) & 1, p.err, 256);
+}
+
+// V codes [key][channel] (128-byte swizzled rows) to FP16 in two chunks of 64
+// channels, swizzled the same way; keys at and behind `act` become zeros, so
+// that no stale code (a NaN among them) meets their P = 0.
+__device__ void converter(TreeSmem& sm, const TreeParams& p, Run run, int w, int lane)
+{
+    Seg s;
+    int c = 0;
+    const int u = lane & 7, r = lane >> 3;
+    while (next_seg(sm.cum, sm.act, sm.n, p.G, run, s)) {
+        const int act = sm.act[s.b];
+        for (int t = s.t0; t < s.t1; ++t, ++c) {
+            const int vslot = c % kVStages, hslot = c % kHStages;
+            mbar_wait(&sm.v_full[vslot], (c / kVStages) & 1, p.err, 4, &sm.abort);
+            mbar_wait(&sm.h_empty[hslot], ((c / kHStages) & 1) ^ 1, p.err, 8, &sm.abort);
+            const uint8_t* src = sm.v[vslot];
+            uint8_t* dst = sm.vh[hslot][u >> 2];
+            const int u0 = 2 * (u & 3), swap = u >> 2;   // the two halves' order keeps the stores apart
+            const int limit = act - t * kBS;
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const int key = w * 64 + i * 4 + r;
+                uint4 x = *reinterpret_cast<const uint4*>(src + sw128(key, u));
+                if (key >= limit) x = make_uint4(0, 0, 0, 0);
+                uint4 lo, hi;
+                lo.x = codes_to_half2(x.x & 0xFFFFu);
+                lo.y = codes_to_half2(x.x >> 16);
+                lo.z = codes_to_half2(x.y & 0xFFFFu);
+                lo.w = codes_to_half2(x.y >> 16);
+                hi.x = codes_to_half2(x.z & 0xFFFFu);
+                hi.y = codes_to_half2(x.z >> 16);
+                hi.z = codes_to_half2(x.w & 0xFFFFu);
+                hi.w = codes_to_half2(x.w >> 16);
+                *reinterpret_cast<uint4*>(dst + sw128(key, u0 + swap)) = swap ? hi : lo;
+                *reinterpret_cast<uint4*>(dst + sw128(key, u0 + 1 - swap)) = swap ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm.h_full[hslot]);
+                mbar_arrive(&sm.v_empty[vslot]);
+            }
+        }
+    }
+}
+
+// One thread issues both streams' MMAs, whichever is ready: S of a stream's
+// next block once its previous P V is complete (P lies over S), P V once the
+// softmax has written P and the block's V is converted.
+__device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem)
+{
+    constexpr uint32_t kIdescS = idesc_e4m3(128, 128, 0, 0);
+    constexpr uint32_t kIdescO = idesc_f16(128, 128, 0, 1);   // P K-major in tensor memory, V MN-major
+    Seg s;
+    int base = 0, seg = 0;
+    int done[2] = {0, 0};                    // blocks of each stream in earlier segments
+    bool stop = false;
+    while (!stop && next_seg(sm.cum, sm.act, sm.n, p.G, run, s)) {
+        const int cnt = s.t1 - s.t0;
+        const int nt[2] = {s.dual ? cnt : (cnt + 1) / 2, s.dual ? cnt : cnt / 2};
+        int a[2] = {0, 0}, v[2] = {0, 0};    // S and P V issued
+        if (!mbar_wait(&sm.q_full, seg & 1, p.err, 16, &sm.abort)) break;
+        uint32_t polls = 0;
+        uint64_t since = 0;
+        while (v[0] < nt[0] || v[1] < nt[1]) {
+            bool moved = false;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const uint32_t S = tmem + 128 * w, O = tmem + kOCol + 128 * w;
+                const int g = done[w] + a[w];         // the stream's blocks so far
+                if (a[w] == v[w] && a[w] < nt[w]) {
+                    const int i = base + (s.dual ? a[w] : 2 * a[w] + w);
+                    const int slot = i % kKStages;
+                    if ((g == 0 || mbar_test(&sm.o_done[w], (g - 1) & 1)) &&
+                        mbar_test(&sm.k_full[slot], (i / kKStages) & 1)) {
+                        tc_fence_after();
+                        const uint64_t qd = smem_desc(smem_u32(sm.q[s.dual ? w : 0]), 16, 1024, kSmem128BSwizzle);
+                        const uint64_t kd = smem_desc(smem_u32(sm.k[slot]), 16, 1024, kSmem128BSwizzle);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) umma_e4m3(S, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
+                        umma_commit(&sm.s_full[w]);
+                        ++a[w];
+                        moved = true;
+                    }
+                } else if (a[w] > v[w]) {
+                    const int i = base + (s.dual ? v[w] : 2 * v[w] + w);
+                    const int slot = i % kHStages;
+                    if (mbar_test(&sm.p_full[w], (g - 1) & 1) && mbar_test(&sm.h_full[slot], (i / kHStages) & 1)) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < kBS / 16; ++kk)
+                            umma_f16_ta(O, S + 8 * kk,
+                                        smem_desc(smem_u32(sm.vh[slot][0]) + kk * 2048, kTile, 1024, kSmem128BSwizzle),
+                                        kIdescO, (v[w] > 0 || kk > 0) ? 1u : 0u);
+                        umma_commit(&sm.o_done[w]);
+                        ++v[w];
+                        // the block's V is free after the last stream that uses it
+                        if (!s.dual || v[w ^ 1] >= v[w]) umma_commit(&sm.h_empty[slot]);
+                        moved = true;
+                    }
+                }
+            }
+            if (moved) {
+                polls = 0;
+                continue;
+            }
+            if ((++polls & 255u) == 0) {
+                if (*(volatile int*)&sm.abort) stop = true;
+                const uint64_t now = globaltimer_ns();
+                if (polls == 256u) since = now;
+                else if (now - since > kWaitLimitNs) {
+                    sm.abort = 1;
+                    atomicOr(p.err, 32);
+                    stop = true;
+                }
+                if (stop) break;
+            }
+        }
+        done[0] += nt[0];
+        done[1] += nt[1];
+        base += cnt;
+        ++seg;
+    }
+    umma_commit(&sm.drain);
+    mbar_wait_drain(&sm.drain, 0, p.err, 512);
+}
+
+__device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w, int warp, int lane)
+{
+    const int q4 = warp & 3, row = 32 * q4 + lane, tid = row;
+    const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
+    const uint32_t S = tmem + lanes + 128 * w;
+    Seg s;
+    int base = 0, g = 0;
+    while (next_seg(sm.cum, sm.act, sm.n, p.G, run, s)) {
+        const int act = sm.act[s.b], n = sm.n[s.b], ctx = act - n, cnt = s.t1 - s.t0;
+        const int nt = s.dual ? cnt : (cnt + 1 - w) / 2;
+        // ---- Q rows into the operand layout: this warpgroup's row tile, or its half of the one ----
+        {
+            const int tile = s.dual ? w : 0, r_lo = s.dual ? 0 : 64 * w, r_n = s.dual ? 128 : 64;
+            for (int i = tid; i < r_n * 8; i += 128) {
+                const int r = r_lo + (i >> 3), u = i & 7, rr = 128 * tile + r;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (rr < s.rows) {
+                    const int64_t at = q_row(p, s, rr);
+                    x = __ldg(reinterpret_cast<const uint4*>(p.q + at * kD) + u);
+                    // a negative scale: the codes' signs, so that the maximum stays a maximum
+                    if (__ldg(p.q_scale + at) * p.scale_log2 < 0.0f) {
+                        x.x ^= 0x80808080u;
+                        x.y ^= 0x80808080u;
+                        x.z ^= 0x80808080u;
+                        x.w ^= 0x80808080u;
+                    }
+                }
+                *reinterpret_cast<uint4*>(sm.q[tile] + sw128(r, u)) = x;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_full);
+        }
+        const int my = (s.dual ? 128 * w : 0) + row;          // row of the item
+        const bool warp_live = (s.dual ? 128 * w : 0) + 32 * q4 < s.rows;
+        const bool live = my < s.rows;
+        float rs = live ? fabsf(__ldg(p.q_scale + q_row(p, s, my)) * p.scale_log2) : 1.0f;
+        if (rs < 1.17549435e-38f) rs = 1.17549435e-38f;       // (-inf times it stays -inf)
+        // ---- the row's mask, one bit per drafted token ----
+        uint64_t m_lo = 0, m_hi = 0;
+        if (warp_live && s.t1 * kBS > ctx) {
+            const int first = (s.row0 + my - lane) / p.G;
+            const int last = min(s.row0 + my - lane + 31, s.row0 + s.rows - 1) / p.G;
+            const int mine = (s.row0 + my) / p.G;
+            for (int node = first; node <= last; ++node) {
+                const uint8_t* mr = p.mask + s.b * p.mask_stride + static_cast<int64_t>(node) * p.S1;
+                uint32_t bits[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    bits[j] = __ballot_sync(0xffffffffu, 32 * j + lane < n && __ldg(mr + min(32 * j + lane, p.S1 - 1)));
+                if (node == mine) {
+                    m_lo = (static_cast<uint64_t>(bits[1]) << 32) | bits[0];
+                    m_hi = (static_cast<uint64_t>(bits[3]) << 32) | bits[2];
+                }
+            }
+        }
+        float m = -INFINITY, l = 0.0f;
+        for (int j = 0; j < nt; ++j, ++g) {
+            const int t = s.t0 + (s.dual ? j : 2 * j + w), i = base + (s.dual ? j : 2 * j + w);
+            const int slot = i % kKStages;
+            mbar_wait(&sm.s_full[w], g & 1, p.err, 64, &sm.abort);
+            if (warp_live) {
+                tc_fence_after();
+                // k_full is complete too (S came out of it), but the scales were
+                // written by other threads' copies: its wait orders them
+                mbar_wait(&sm.k_full[slot], (i / kKStages) & 1, p.err, 64, &sm.abort);
+                float v[kBS];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, v + 32 * c);
+                tmem_wait_ld();
+                const float4* ks = reinterpret_cast<const float4*>(sm.ks[slot]);
+#pragma unroll
+                for (int c = 0; c < kBS / 4; ++c) {
+                    const float4 k4 = ks[c];
+                    const float2 a = mul2(make_float2(v[4 * c], v[4 * c + 1]), make_float2(k4.x, k4.y));
+                    const float2 b = mul2(make_float2(v[4 * c + 2], v[4 * c + 3]), make_float2(k4.z, k4.w));
+                    v[4 * c] = a.x;
+                    v[4 * c + 1] = a.y;
+                    v[4 * c + 2] = b.x;
+                    v[4 * c + 3] = b.y;
+                }
+                const int off = ctx - t * kBS;                 // the first drafted token's key in this block
+                if (off < kBS) {
+                    // which keys the row sees: the context's, then its mask's bits
+                    uint64_t lo, hi;
+                    if (off >= 64) {
+                        lo = ~0ull;
+                        hi = (off == 64 ? 0ull : ~0ull >> (128 - off)) | (m_lo << (off - 64));
+                    } else if (off > 0) {
+                        lo = (~0ull >> (64 - off)) | (m_lo << off);
+                        hi = (m_hi << off) | (m_lo >> (64 - off));
+                    } else if (off == 0) {
+                        lo = m_lo;
+                        hi = m_hi;
+                    } else if (off > -64) {
+                        lo = (m_lo >> -off) | (m_hi << (64 + off));
+                        hi = m_hi >> -off;
+                    } else {
+                        lo = off > -128 ? m_hi >> (-off - 64) : 0ull;
+                        hi = 0ull;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) {
+                        if (!((lo >> k) & 1)) v[k] = -INFINITY;
+                        if (!((hi >> k) & 1)) v[64 + k] = -INFINITY;
+                    }
+                }
+                float mx = v[0];
+#pragma unroll
+                for (int k = 1; k < kBS; ++k) mx = fmaxf(mx, v[k]);
+                mx *= rs;
+                const bool raise = mx > m + kRaise || (m == -INFINITY && mx > -INFINITY);
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float f = raise ? ex2(m - mx) : 1.0f;
+                    if (raise) m = mx;
+                    l *= f;
+                    if (j > 0) {
+                        // S of this block was issued after the last P V had completed
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            float o[32];
+                            const uint32_t at = tmem + lanes + kOCol + 128 * w + 32 * c;
+                            tmem_ld32(at, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] *= f;
+                            tmem_st32(at, o);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.0f : m - kShift;
+                const float2 rs2 = make_float2(rs, rs), nref = make_float2(-ref, -ref);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t h[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float2 x = fma2(make_float2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), rs2, nref);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        sum[k & 1] = add2(sum[k & 1], x);
+                        h[k] = half2_bits(x.x, x.y);
+                    }
+                    tmem_st16(S + 16 * c, h);
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm.p_full[w]);
+                mbar_arrive_n(&sm.k_empty[slot], s.dual ? 1 : 2);
+            }
+        }
+        if (nt > 0) mbar_wait(&sm.o_done[w], (g - 1) & 1, p.err, 128, &sm.abort);
+        tc_fence_before();
+        // ---- the item's (or its part's) output ----
+        const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+        float* const part = part_of(p, blockIdx.x, s.first);
+        if (!s.dual) {
+            sm.ml[w][0][row] = m;
+            sm.ml[w][1][row] = l;
+        }
+        named_bar_sync(1, 256);
+        tc_fence_after();
+        float f0 = 1.0f, f1 = 0.0f;                            // factors of this stream's O, or of O 0 and 1
+        int d0 = 0, dn = kD;
+        uint32_t o_at = tmem + lanes + kOCol + 128 * w;
+        const bool two = !s.dual && cnt > 1;
+        if (!s.dual) {
+            const float m0 = sm.ml[0][0][row], m1 = cnt > 1 ? sm.ml[1][0][row] : -INFINITY;
+            const float l0 = sm.ml[0][1][row], l1 = cnt > 1 ? sm.ml[1][1][row] : 0.0f;
+            m = fmaxf(m0, m1);
+            f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - m);
+            f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - m);
+            l = l0 * f0 + l1 * f1;
+            d0 = 64 * w;
+            dn = 64;
+            o_at = tmem + lanes + kOCol + d0;
+        }
+        if (warp_live) {
+            const int64_t at = live ? q_row(p, s, my) : 0;
+            const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+            const float4* vs = reinterpret_cast<const float4*>(p.v_scale +
+                                                               (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD + d0);
+#pragma unroll 1
+            for (int c = 0; c < dn / 32; ++c) {
+                float o[32], o2[32];
+                tmem_ld32(o_at + 32 * c, o);
+                if (two) tmem_ld32(o_at + 128 + 32 * c, o2);
+                tmem_wait_ld();
+                if (!s.dual) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] *= f0;
+                    if (two) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] += o2[k] * f1;
+                    }
+                }
+                if (!live) continue;
+                if (whole) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + at * kD + d0 + 32 * c);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 a = __ldg(vs + 8 * c + 2 * k), b = __ldg(vs + 8 * c + 2 * k + 1);
+                        const float* x = o + 8 * k;
+                        const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * inv * a.x, x[1] * inv * a.y);
+                        const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * inv * a.z, x[3] * inv * a.w);
+                        const __nv_bfloat162 y2 = __floats2bfloat162_rn(x[4] * inv * b.x, x[5] * inv * b.y);
+                        const __nv_bfloat162 y3 = __floats2bfloat162_rn(x[6] * inv * b.z, x[7] * inv * b.w);
+                        dst[k] = make_uint4(*reinterpret_cast<const uint32_t*>(&y0),
+                                            *reinterpret_cast<const uint32_t*>(&y1),
+                                            *reinterpret_cast<const uint32_t*>(&y2),
+                                            *reinterpret_cast<const uint32_t*>(&y3));
+                    }
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(part + static_cast<int64_t>(my) * kD + d0 + 32 * c);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+            }
+            if (!whole && live && d0 == 0) {
+                float* ml = part + static_cast<int64_t>(p.part_rows) * kD;
+                ml[my] = m;
+                ml[p.part_rows + my] = l;
+            }
+        }
+        tc_fence_before();
+        // (O, ml and Q of this segment are not touched before both warpgroups are here)
+        named_bar_sync(1, 256);
+        base += cnt;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const TreeParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
+    TreeSmem& sm = *reinterpret_cast<TreeSmem*>(smem_raw + ((1024u - (raw & 1023u)) & 1023u));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < kKStages; ++i) {
+            mbar_init(&sm.k_full[i], 33);
+            mbar_init(&sm.k_empty[i], 8);
+        }
+        for (int i = 0; i < kVStages; ++i) {
+            mbar_init(&sm.v_full[i], 1);
+            mbar_init(&sm.v_empty[i], kConvWarps);
+        }
+        for (int i = 0; i < kHStages; ++i) {
+            mbar_init(&sm.h_full[i], kConvWarps);
+            mbar_init(&sm.h_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.o_done[i], 1);
+        }
+        mbar_init(&sm.q_full, 8);
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) tmem_alloc(&sm.tmem, kTmemCols);
+
+    // ---- weights before each sequence: thread i takes sequences i, i + 1, ... of its share ----
+    {
+        const int per = (p.B + kThreads - 1) / kThreads;
+        int64_t mine = 0;
+        for (int b = tid * per; b < min(p.B, tid * per + per); ++b) {
+            const int64_t cap = static_cast<int64_t>(p.max_blocks) * kBS;
+            const int act = static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.act + b), 0)), cap));
+            int n = p.len ? __ldg(p.len + b) : p.S1;
+            n = min(max(n, 0), min(p.S1, act));
+            sm.act[b] = act;
+            sm.n[b] = static_cast<uint8_t>(n);
+            sm.cum[b] = mine;
+            mine += static_cast<int64_t>(p.NKV) * head_weight(n * p.G) * tiles_of(act);
+        }
+        int64_t x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) sm.warp_sum[warp] = x;
+        __syncthreads();
+        int64_t before = x - mine;
+        for (int i = 0; i < warp; ++i) before += sm.warp_sum[i];
+        for (int b = tid * per; b < min(p.B, tid * per + per); ++b) sm.cum[b] += before;
+        if (tid == kThreads - 1) sm.cum[p.B] = before + mine;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    const int64_t total = sm.cum[p.B];
+    Run run;
+    run.pos = run_begin(total, blockIdx.x, p.ctas);
+    run.hi = run_begin(total, blockIdx.x + 1, p.ctas);
+    run.fresh = true;
+    run.b = 0;
+    if (run.pos < run.hi) {
+        int lo = 0, hi = p.B - 1;            // the last sequence that starts at or before pos
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (sm.cum[mid] <= run.pos) lo = mid;
+            else hi = mid - 1;
+        }
+        run.b = lo;
+    }
+
+    if (warp < kProdWarp) {
+        softmax(sm, p, run, tmem, warp >> 2, warp, lane);
+    } else if (warp == kProdWarp) {
+        if (blockIdx.x == 0)
+            for (int b = lane; b <= p.B; b += 32) p.cum[b] = sm.cum[b];
+        producer(sm, p, &tk, &tv, run, lane);
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) mma_issuer(sm, p, run, tmem);
+        __syncwarp();
+    } else {
+        // rows that see nothing because their sequence has no such node
+        for (int64_t tok = blockIdx.x; tok < static_cast<int64_t>(p.B) * p.S1; tok += gridDim.x) {
+            const int b = static_cast<int>(tok / p.S1);
+            if (tok - static_cast<int64_t>(b) * p.S1 < sm.n[b]) continue;
+            uint4* dst = reinterpret_cast<uint4*>(p.out + tok * p.NQ * kD);
+            for (int i = tid - kConvWarp * 32; i < p.NQ * (kD / 8); i += kConvWarps * 32) dst[i] = make_uint4(0, 0, 0, 0);
+        }
+        converter(sm, p, run, warp - kConvWarp, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+    grid_launch_dependents();
+}
+
+// Joins the parts of the items that a run's end cut: CTA (c, y) takes the item
+// at the begin of run c, if run c - 1 is the item's first, and its rows 8 y ..
+// 8 y + 7, one warp each.
+constexpr int kJoinWarps = 8;
+
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeParams p)
+{
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const int c = blockIdx.x + 1;
+    const int64_t total = p.cum[p.B];
+    const int64_t pos = run_begin(total, c, p.ctas);
+    if (total == 0 || pos >= total) return;
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.cum[mid] <= pos) lo = mid;
+        else hi = mid - 1;
+    }
+    const int64_t cap = static_cast<int64_t>(p.max_blocks) * kBS;
+    const int act = static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.act + lo), 0)), cap));
+    int n = p.len ? __ldg(p.len + lo) : p.S1;
+    n = min(max(n, 0), min(p.S1, act));
+    Seg s;
+    s.b = lo;
+    int64_t base;
+    locate(pos, p.cum[lo], n * p.G, tiles_of(act), s, base);
+    const int w = s.dual ? 2 : 1;
+    const int64_t end = base + static_cast<int64_t>(w) * s.tiles;
+    const int c0 = cta_of(total, base, p.ctas), c1 = cta_of(total, end - 1, p.ctas);
+    if (c != c0 + 1 || pos == base) return;
+    const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+    if (row >= s.rows) return;
+
+    // blocks [t0, t1) of the item in run i, and where its part lies
+    auto part = [&](int i, bool& some) -> const float* {
+        const int64_t b0 = run_begin(total, i, p.ctas), b1 = run_begin(total, i + 1, p.ctas);
+        const int64_t t0 = b0 > base ? (b0 - base + w - 1) / w : 0;
+        const int64_t t1 = b1 >= end ? s.tiles : (b1 - base + w - 1) / w;
+        some = t0 < t1;
+        return (t0 == 0 && t1 == s.tiles) ? nullptr : part_of(p, i, b0 >= base);
+    };
+    float M = -INFINITY;
+    for (int i = c0; i <= c1; ++i) {
+        bool some;
+        const float* q = part(i, some);
+        if (!q) return;                      // one run had all of it
+        if (some) M = fmaxf(M, q[static_cast<int64_t>(p.part_rows) * kD + row]);
+    }
+    float L = 0.0f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = c0; i <= c1; ++i) {
+        bool some;
+        const float* q = part(i, some);
+        if (!some) continue;
+        const float* ml = q + static_cast<int64_t>(p.part_rows) * kD;
+        const float mi = ml[row];
+        const float f = mi == -INFINITY ? 0.0f : ex2(mi - M);
+        const float4 x = reinterpret_cast<const float4*>(q + static_cast<int64_t>(row) * kD)[lane];
+        L += ml[p.part_rows + row] * f;
+        o.x += x.x * f;
+        o.y += x.y * f;
+        o.z += x.z * f;
+        o.w += x.w * f;
+    }
+    const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p.v_scale + (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD) + lane);
+    const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * inv * v.x, o.y * inv * v.y);
+    const __nv_bfloat162 y1 = __floats2bfloat162_rn(o.z * inv * v.z, o.w * inv * v.w);
+    reinterpret_cast<uint2*>(p.out + q_row(p, s, row) * kD)[lane] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// rows of the largest item, a multiple of 64 so that parts start on 256 bytes
+int part_rows(int S1, int G)
+{
+    const int64_t r = static_cast<int64_t>(S1) * G;
+    return r >= kItemRows ? kItemRows : static_cast<int>((r + 63) / 64 * 64);
+}
 
 pa_status check_shape(const char* name, int B, int S1, int NQ, int NKV, int D)
 {
@@ -123,7 +875,7 @@ extern "C" pa_status pa_fp8_tree_decode_workspace_size(int B, int S1, int NQ, in
     PA_REQUIRE(bytes, PA_ERR_NULLPTR, "pa_fp8_tree_decode_workspace_size: bytes is NULL");
     const pa_status st = check_shape("pa_fp8_tree_decode", B, S1, NQ, NKV, D);
     if (st != PA_OK) return st;
-    *bytes = kWsHeader;
+    *bytes = kPartOff + static_cast<size_t>(kMaxCtas) * 2 * part_rows(S1, NQ / NKV) * (kD + 2) * sizeof(float);
     return PA_OK;
 }
 
@@ -160,12 +912,21 @@ extern "C" pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, con
                workspace ? workspace_bytes : static_cast<size_t>(0), need);
     PA_REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, PA_ERR_INVALID,
                "%s: workspace must be 256-byte aligned", name);
+    const int sms = device_sm_count();
+    PA_REQUIRE(sms > 0, PA_ERR_CUDA, "%s: cannot query the device", name);
+    CUtensorMap tk, tv;
+    const uint64_t inner = layout == PA_LAYOUT_BSND ? static_cast<uint64_t>(NKV) * kD : kD;
+    const uint64_t rows = static_cast<uint64_t>(num_blocks) * kBS * (layout == PA_LAYOUT_BNBD ? NKV : 1);
+    pa_status st = make_cache_map(&tk, k_cache, inner, rows);
+    if (st != PA_OK) return st;
+    st = make_cache_map(&tv, v_cache, inner, rows);
+    if (st != PA_OK) return st;
+
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     TreeParams p;
     p.q = static_cast<const uint8_t*>(q);
     p.q_scale = q_scale;
-    p.kc = static_cast<const uint8_t*>(k_cache);
     p.k_scale = k_scale;
-    p.vc = static_cast<const uint8_t*>(v_cache);
     p.v_scale = v_scale;
     p.bt = block_table;
     p.act = kv_act_seqs;
@@ -173,13 +934,40 @@ extern "C" pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, con
     p.mask = tree_mask;
     p.mask_stride = mask_stride;
     p.out = static_cast<__nv_bfloat16*>(out);
+    p.err = reinterpret_cast<int*>(ws);
+    p.cum = reinterpret_cast<int64_t*>(ws + kCumOff);
+    p.part = reinterpret_cast<float*>(ws + kPartOff);
+    p.part_rows = part_rows(S1, NQ / NKV);
+    p.B = B;
     p.S1 = S1;
     p.NQ = NQ;
     p.NKV = NKV;
+    p.G = NQ / NKV;
     p.num_blocks = num_blocks;
     p.max_blocks = max_blocks_per_seq;
     p.layout = layout;
+    p.ctas = sms < kMaxCtas ? sms : kMaxCtas;
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
-    tree_decode_kernel<<<static_cast<unsigned>(B) * S1 * NQ, kD, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return check_launch(name);
+
+    const size_t smem = sizeof(TreeSmem) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(tree_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+    PA_REQUIRE(e == cudaSuccess, PA_ERR_CUDA, "%s: smem attribute: %s", name, cudaGetErrorString(e));
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    tree_decode_kernel<<<static_cast<unsigned>(p.ctas), kThreads, smem, cs>>>(tk, tv, p);
+    st = check_launch(name);
+    if (st != PA_OK || p.ctas == 1) return st;
+    const int64_t most = static_cast<int64_t>(S1) * p.G < kItemRows ? static_cast<int64_t>(S1) * p.G : kItemRows;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(static_cast<unsigned>(p.ctas - 1), static_cast<unsigned>((most + kJoinWarps - 1) / kJoinWarps));
+    lc.blockDim = dim3(kJoinWarps * 32);
+    lc.stream = cs;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    e = cudaLaunchKernelEx(&lc, tree_join_kernel, p);
+    PA_REQUIRE(e == cudaSuccess, PA_ERR_CUDA, "%s: launch: %s", name, cudaGetErrorString(e));
+    return PA_OK;
 }
