@@ -26,8 +26,8 @@
 // stream's softmax runs, the other's contractions do.
 //   warps 0-3, 4-7   softmax of stream 0, 1 (thread = row = tensor memory lane)
 //   warp 8           K and V blocks by TMA, key scales by cp.async
-//   warp 9           issues the MMAs of whichever stream is ready
-//   warps 10, 11     V codes to FP16 in shared memory, zeros behind the end
+//   warps 9, 10      one thread each issues stream 0's, stream 1's MMAs
+//   warps 12-15      V codes to FP16 in shared memory, zeros behind the end
 //
 // The blocks of all items, in (sequence, kv head, item, block) order, a block
 // of a two-tile item counting twice, are dealt to the CTAs in equal runs; items
@@ -52,7 +52,11 @@ constexpr int kMaxCtas = 192;
 constexpr int kItemRows = 256;
 constexpr int kTile = kBS * kD;              // bytes of a block of codes
 constexpr int kKStages = 4, kVStages = 3, kHStages = 2;
-constexpr int kProdWarp = 8, kMmaWarp = 9, kConvWarp = 10, kConvWarps = 2;
+constexpr int kProdWarp = 8, kMmaWarp = 9, kConvWarp = 12, kConvWarps = 4;
+// Registers: 512 threads start with 128 each; the softmax warpgroups, which
+// hold a row's 128 scores, go up to 184 and the other two down to 72 (256 x
+// 184 + 256 x 72 = 512 x 128).
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 constexpr int kThreads = (kConvWarp + kConvWarps) * 32;
 constexpr uint32_t kTmemCols = 512, kOCol = 256;
 constexpr float kRaise = 8.0f;               // log2 units: see the top of the file
@@ -95,7 +99,7 @@ struct TreeSmem {
     uint8_t n[kMaxB];
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t h_full[kHStages], h_empty[kHStages];
-    uint64_t s_full[2], p_full[2], o_done[2], q_full, drain;
+    uint64_t s_full[2], p_full[2], o_done[2], q_full, drain[2];
     uint32_t tmem;
     int abort;
 };
@@ -229,7 +233,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return r;
 }
 
-// Index of the first row of item `s`, row r of it, in q and out.
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Row r of item `s` in q and out.
 __device__ __forceinline__ int64_t q_row(const TreeParams& p, const Seg& s, int r)
 {
     const int rr = s.row0 + r, node = rr / p.G;
@@ -317,8 +328,8 @@ __device__ void converter(TreeSmem& sm, const TreeParams& p, Run run, int w, int
             const int u0 = 2 * (u & 3), swap = u >> 2;   // the two halves' order keeps the stores apart
             const int limit = act - t * kBS;
 #pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-                const int key = w * 64 + i * 4 + r;
+            for (int i = 0; i < kBS / kConvWarps / 4; ++i) {
+                const int key = w * (kBS / kConvWarps) + i * 4 + r;
                 uint4 x = *reinterpret_cast<const uint4*>(src + sw128(key, u));
                 if (key >= limit) x = make_uint4(0, 0, 0, 0);
                 uint4 lo, hi;
@@ -343,85 +354,50 @@ __device__ void converter(TreeSmem& sm, const TreeParams& p, Run run, int w, int
     }
 }
 
-// One thread issues both streams' MMAs, whichever is ready: S of a stream's
-// next block once its previous P V is complete (P lies over S), P V once the
-// softmax has written P and the block's V is converted.
-__device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem)
+// One thread per stream issues its MMAs: S of the next block once the previous
+// P V is complete (P lies over S), P V once the softmax has written P and the
+// block's V is converted.
+__device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w)
 {
     constexpr uint32_t kIdescS = idesc_e4m3(128, 128, 0, 0);
     constexpr uint32_t kIdescO = idesc_f16(128, 128, 0, 1);   // P K-major in tensor memory, V MN-major
+    const uint32_t S = tmem + 128 * w, O = tmem + kOCol + 128 * w;
     Seg s;
-    int base = 0, seg = 0;
-    int done[2] = {0, 0};                    // blocks of each stream in earlier segments
-    bool stop = false;
-    while (!stop && next_seg(sm.cum, sm.act, sm.n, p.G, run, s)) {
+    int base = 0, seg = 0, g = 0;            // blocks of all streams, segments, own blocks so far
+    bool ok = true;
+    while (ok && next_seg(sm.cum, sm.act, sm.n, p.G, run, s)) {
         const int cnt = s.t1 - s.t0;
-        const int nt[2] = {s.dual ? cnt : (cnt + 1) / 2, s.dual ? cnt : cnt / 2};
-        int a[2] = {0, 0}, v[2] = {0, 0};    // S and P V issued
-        if (!mbar_wait(&sm.q_full, seg & 1, p.err, 16, &sm.abort)) break;
-        uint32_t polls = 0;
-        uint64_t since = 0;
-        while (v[0] < nt[0] || v[1] < nt[1]) {
-            bool moved = false;
+        const int nt = s.dual ? cnt : (cnt + 1 - w) / 2;
+        ok = mbar_wait(&sm.q_full, seg & 1, p.err, 16, &sm.abort);
+        const uint64_t qd = smem_desc(smem_u32(sm.q[s.dual ? w : 0]), 16, 1024, kSmem128BSwizzle);
+        for (int j = 0; j < nt && ok; ++j, ++g) {
+            const int i = base + (s.dual ? j : 2 * j + w);
+            const int ks = i % kKStages, hs = i % kHStages;
+            ok = mbar_wait(&sm.k_full[ks], (i / kKStages) & 1, p.err, 16, &sm.abort) &&
+                 (g == 0 || mbar_wait(&sm.o_done[w], (g - 1) & 1, p.err, 32, &sm.abort));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd = smem_desc(smem_u32(sm.k[ks]), 16, 1024, kSmem128BSwizzle);
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const uint32_t S = tmem + 128 * w, O = tmem + kOCol + 128 * w;
-                const int g = done[w] + a[w];         // the stream's blocks so far
-                if (a[w] == v[w] && a[w] < nt[w]) {
-                    const int i = base + (s.dual ? a[w] : 2 * a[w] + w);
-                    const int slot = i % kKStages;
-                    if ((g == 0 || mbar_test(&sm.o_done[w], (g - 1) & 1)) &&
-                        mbar_test(&sm.k_full[slot], (i / kKStages) & 1)) {
-                        tc_fence_after();
-                        const uint64_t qd = smem_desc(smem_u32(sm.q[s.dual ? w : 0]), 16, 1024, kSmem128BSwizzle);
-                        const uint64_t kd = smem_desc(smem_u32(sm.k[slot]), 16, 1024, kSmem128BSwizzle);
+            for (int kk = 0; kk < 4; ++kk) umma_e4m3(S, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
+            umma_commit(&sm.s_full[w]);
+            const uint64_t vd = smem_desc(smem_u32(sm.vh[hs][0]), kTile, 1024, kSmem128BSwizzle);
+            ok = mbar_wait(&sm.h_full[hs], (i / kHStages) & 1, p.err, 32, &sm.abort) &&
+                 mbar_wait(&sm.p_full[w], g & 1, p.err, 32, &sm.abort);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) umma_e4m3(S, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
-                        umma_commit(&sm.s_full[w]);
-                        ++a[w];
-                        moved = true;
-                    }
-                } else if (a[w] > v[w]) {
-                    const int i = base + (s.dual ? v[w] : 2 * v[w] + w);
-                    const int slot = i % kHStages;
-                    if (mbar_test(&sm.p_full[w], (g - 1) & 1) && mbar_test(&sm.h_full[slot], (i / kHStages) & 1)) {
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < kBS / 16; ++kk)
-                            umma_f16_ta(O, S + 8 * kk,
-                                        smem_desc(smem_u32(sm.vh[slot][0]) + kk * 2048, kTile, 1024, kSmem128BSwizzle),
-                                        kIdescO, (v[w] > 0 || kk > 0) ? 1u : 0u);
-                        umma_commit(&sm.o_done[w]);
-                        ++v[w];
-                        // the block's V is free after the last stream that uses it
-                        if (!s.dual || v[w ^ 1] >= v[w]) umma_commit(&sm.h_empty[slot]);
-                        moved = true;
-                    }
-                }
-            }
-            if (moved) {
-                polls = 0;
-                continue;
-            }
-            if ((++polls & 255u) == 0) {
-                if (*(volatile int*)&sm.abort) stop = true;
-                const uint64_t now = globaltimer_ns();
-                if (polls == 256u) since = now;
-                else if (now - since > kWaitLimitNs) {
-                    sm.abort = 1;
-                    atomicOr(p.err, 32);
-                    stop = true;
-                }
-                if (stop) break;
-            }
+            for (int kk = 0; kk < kBS / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of V
+                umma_f16_ta(O, S + 8 * kk, vd + 128 * kk, kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&sm.o_done[w]);
+            umma_commit(&sm.h_empty[hs]);
+            if (!s.dual) umma_commit(&sm.h_empty[hs]);   // (two arrivals a block)
         }
-        done[0] += nt[0];
-        done[1] += nt[1];
         base += cnt;
         ++seg;
     }
-    umma_commit(&sm.drain);
-    mbar_wait_drain(&sm.drain, 0, p.err, 512);
+    umma_commit(&sm.drain[w]);
+    mbar_wait_drain(&sm.drain[w], 0, p.err, 512);
 }
 
 __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w, int warp, int lane)
@@ -437,21 +413,28 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
         // ---- Q rows into the operand layout: this warpgroup's row tile, or its half of the one ----
         {
             const int tile = s.dual ? w : 0, r_lo = s.dual ? 0 : 64 * w, r_n = s.dual ? 128 : 64;
-            for (int i = tid; i < r_n * 8; i += 128) {
-                const int r = r_lo + (i >> 3), u = i & 7, rr = 128 * tile + r;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (rr < s.rows) {
+            // 16 bytes a thread, all loads in flight before the first is stored
+            const int u = tid & 7;
+            uint4 x[8];
+            float sc[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int rr = 128 * tile + r_lo + 16 * i + (tid >> 3);
+                x[i] = make_uint4(0, 0, 0, 0);
+                sc[i] = 0.0f;
+                if (16 * i < r_n && rr < s.rows) {
                     const int64_t at = q_row(p, s, rr);
-                    x = __ldg(reinterpret_cast<const uint4*>(p.q + at * kD) + u);
-                    // a negative scale: the codes' signs, so that the maximum stays a maximum
-                    if (__ldg(p.q_scale + at) * p.scale_log2 < 0.0f) {
-                        x.x ^= 0x80808080u;
-                        x.y ^= 0x80808080u;
-                        x.z ^= 0x80808080u;
-                        x.w ^= 0x80808080u;
-                    }
+                    x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + at * kD) + u);
+                    sc[i] = __ldg(p.q_scale + at);
                 }
-                *reinterpret_cast<uint4*>(sm.q[tile] + sw128(r, u)) = x;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (16 * i >= r_n) break;
+                // a negative scale: the codes' signs, so that the maximum stays a maximum
+                const uint32_t flip = sc[i] * p.scale_log2 < 0.0f ? 0x80808080u : 0u;
+                *reinterpret_cast<uint4*>(sm.q[tile] + sw128(r_lo + 16 * i + (tid >> 3), u)) =
+                    make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -531,10 +514,14 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                         if (!((hi >> k) & 1)) v[64 + k] = -INFINITY;
                     }
                 }
-                float mx = v[0];
+                float m4[4];
 #pragma unroll
-                for (int k = 1; k < kBS; ++k) mx = fmaxf(mx, v[k]);
-                mx *= rs;
+                for (int c = 0; c < 4; ++c) {
+                    m4[c] = fmaxf(v[32 * c], v[32 * c + 1]);
+#pragma unroll
+                    for (int k = 2; k < 32; k += 2) m4[c] = max3(m4[c], v[32 * c + k], v[32 * c + k + 1]);
+                }
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rs;
                 const bool raise = mx > m + kRaise || (m == -INFINITY && mx > -INFINITY);
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? ex2(m - mx) : 1.0f;
@@ -607,27 +594,32 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
             o_at = tmem + lanes + kOCol + d0;
         }
         if (warp_live) {
-            const int64_t at = live ? q_row(p, s, my) : 0;
+            // Rows leave in 128-byte pieces of each, staged in this warp's 32 rows
+            // of its warpgroup's Q tile (every S of the segment is computed): a
+            // store covers four rows' pieces instead of 16 bytes of 32 rows.
             const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+            const int at = live ? static_cast<int>(q_row(p, s, my)) : -1;
+            uint8_t* const stage = sm.q[w];
             const float4* vs = reinterpret_cast<const float4*>(p.v_scale +
                                                                (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD + d0);
+            const int nc = dn / 32;
 #pragma unroll 1
-            for (int c = 0; c < dn / 32; ++c) {
-                float o[32], o2[32];
+            for (int c = 0; c < nc; ++c) {
+                float o[32];
                 tmem_ld32(o_at + 32 * c, o);
-                if (two) tmem_ld32(o_at + 128 + 32 * c, o2);
                 tmem_wait_ld();
                 if (!s.dual) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] *= f0;
                     if (two) {
+                        float o2[32];
+                        tmem_ld32(o_at + 128 + 32 * c, o2);
+                        tmem_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] += o2[k] * f1;
                     }
                 }
-                if (!live) continue;
                 if (whole) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.out + at * kD + d0 + 32 * c);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float4 a = __ldg(vs + 8 * c + 2 * k), b = __ldg(vs + 8 * c + 2 * k + 1);
@@ -636,17 +628,30 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                         const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * inv * a.z, x[3] * inv * a.w);
                         const __nv_bfloat162 y2 = __floats2bfloat162_rn(x[4] * inv * b.x, x[5] * inv * b.y);
                         const __nv_bfloat162 y3 = __floats2bfloat162_rn(x[6] * inv * b.z, x[7] * inv * b.w);
-                        dst[k] = make_uint4(*reinterpret_cast<const uint32_t*>(&y0),
-                                            *reinterpret_cast<const uint32_t*>(&y1),
-                                            *reinterpret_cast<const uint32_t*>(&y2),
-                                            *reinterpret_cast<const uint32_t*>(&y3));
+                        *reinterpret_cast<uint4*>(stage + sw128(row, 4 * (c & 1) + k)) =
+                            make_uint4(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1),
+                                       *reinterpret_cast<const uint32_t*>(&y2), *reinterpret_cast<const uint32_t*>(&y3));
                     }
+                    if ((c & 1) == 0) continue;
                 } else {
-                    float4* dst = reinterpret_cast<float4*>(part + static_cast<int64_t>(my) * kD + d0 + 32 * c);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        *reinterpret_cast<float4*>(stage + sw128(row, k)) =
+                            make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3), u = lane & 7;
+                    const int to = __shfl_sync(0xffffffffu, at, r);
+                    const uint4 x = *reinterpret_cast<const uint4*>(stage + sw128(32 * q4 + r, u));
+                    if (to < 0) continue;
+                    if (whole)
+                        reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(to) * kD + d0 + 64 * (c >> 1))[u] = x;
+                    else
+                        reinterpret_cast<uint4*>(part + static_cast<int64_t>(my - lane + r) * kD + d0 + 32 * c)[u] = x;
+                }
+                __syncwarp();
             }
             if (!whole && live && d0 == 0) {
                 float* ml = part + static_cast<int64_t>(p.part_rows) * kD;
@@ -680,15 +685,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kHStages; ++i) {
             mbar_init(&sm.h_full[i], kConvWarps);
-            mbar_init(&sm.h_empty[i], 1);
+            mbar_init(&sm.h_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.o_done[i], 1);
+            mbar_init(&sm.drain[i], 1);
         }
         mbar_init(&sm.q_full, 8);
-        mbar_init(&sm.drain, 1);
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -742,15 +747,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     if (warp < kProdWarp) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         softmax(sm, p, run, tmem, warp >> 2, warp, lane);
-    } else if (warp == kProdWarp) {
+    } else if (warp < kConvWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp != kProdWarp) {
+            if (warp - kMmaWarp < 2 && lane == 0) mma_issuer(sm, p, run, tmem, warp - kMmaWarp);
+            __syncwarp();
+        } else {
         if (blockIdx.x == 0)
             for (int b = lane; b <= p.B; b += 32) p.cum[b] = sm.cum[b];
         producer(sm, p, &tk, &tv, run, lane);
-    } else if (warp == kMmaWarp) {
-        if (lane == 0) mma_issuer(sm, p, run, tmem);
-        __syncwarp();
+        }
     } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // rows that see nothing because their sequence has no such node
         for (int64_t tok = blockIdx.x; tok < static_cast<int64_t>(p.B) * p.S1; tok += gridDim.x) {
             const int b = static_cast<int>(tok / p.S1);
@@ -803,38 +813,58 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
     const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
     if (row >= s.rows) return;
 
-    // blocks [t0, t1) of the item in run i, and where its part lies
-    auto part = [&](int i, bool& some) -> const float* {
-        const int64_t b0 = run_begin(total, i, p.ctas), b1 = run_begin(total, i + 1, p.ctas);
-        const int64_t t0 = b0 > base ? (b0 - base + w - 1) / w : 0;
-        const int64_t t1 = b1 >= end ? s.tiles : (b1 - base + w - 1) / w;
-        some = t0 < t1;
-        return (t0 == 0 && t1 == s.tiles) ? nullptr : part_of(p, i, b0 >= base);
-    };
-    float M = -INFINITY;
-    for (int i = c0; i <= c1; ++i) {
-        bool some;
-        const float* q = part(i, some);
-        if (!q) return;                      // one run had all of it
-        if (some) M = fmaxf(M, q[static_cast<int64_t>(p.part_rows) * kD + row]);
+    // lane i looks at runs c0 + i, c0 + i + 32, ...: their blocks [t0, t1) of the
+    // item, where their part lies, its m and l
+    constexpr int kPer = kMaxCtas / 32;
+    float mi[kPer], li[kPer], M = -INFINITY;
+    int slot[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int i = c0 + 32 * k + lane;
+        mi[k] = -INFINITY;
+        li[k] = 0.0f;
+        slot[k] = -1;
+        bool all = false;
+        if (i <= c1) {
+            const int64_t b0 = run_begin(total, i, p.ctas), b1 = run_begin(total, i + 1, p.ctas);
+            const int64_t t0 = b0 > base ? (b0 - base + w - 1) / w : 0;
+            const int64_t t1 = b1 >= end ? s.tiles : (b1 - base + w - 1) / w;
+            all = t0 == 0 && t1 == s.tiles;
+            if (t0 < t1 && !all) {
+                slot[k] = 2 * i + (b0 >= base ? 0 : 1);
+                const float* ml = p.part + static_cast<int64_t>(slot[k]) * p.part_rows * (kD + 2) +
+                                  static_cast<int64_t>(p.part_rows) * kD;
+                mi[k] = ml[row];
+                li[k] = ml[p.part_rows + row];
+            }
+        }
+        if (__any_sync(0xffffffffu, all)) return;   // one run had all of it
+        M = fmaxf(M, mi[k]);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float L = 0.0f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = c0; i <= c1; ++i) {
-        bool some;
-        const float* q = part(i, some);
-        if (!some) continue;
-        const float* ml = q + static_cast<int64_t>(p.part_rows) * kD;
-        const float mi = ml[row];
-        const float f = mi == -INFINITY ? 0.0f : ex2(mi - M);
-        const float4 x = reinterpret_cast<const float4*>(q + static_cast<int64_t>(row) * kD)[lane];
-        L += ml[p.part_rows + row] * f;
-        o.x += x.x * f;
-        o.y += x.y * f;
-        o.z += x.z * f;
-        o.w += x.w * f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const float f = mi[k] == -INFINITY ? 0.0f : ex2(mi[k] - M);
+        L += li[k] * f;
+        const int last = min(c1 - c0 - 32 * k, 31);
+#pragma unroll 8
+        for (int i = 0; i <= last; ++i) {
+            const int sl = __shfl_sync(0xffffffffu, slot[k], i);
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            if (sl < 0) continue;
+            const float4 x = reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(sl) * p.part_rows * (kD + 2) +
+                                                             static_cast<int64_t>(row) * kD)[lane];
+            o.x += x.x * fi;
+            o.y += x.y * fi;
+            o.z += x.z * fi;
+            o.w += x.w * fi;
+        }
     }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) L += __shfl_xor_sync(0xffffffffu, L, i);
     const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
     const float4 v = __ldg(reinterpret_cast<const float4*>(p.v_scale + (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD) + lane);
     const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * inv * v.x, o.y * inv * v.y);
@@ -907,6 +937,8 @@ extern "C" pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, con
     PA_REQUIRE(mask_stride >= 0, PA_ERR_INVALID, "%s: negative mask_stride", name);
     PA_REQUIRE(aligned16(q) && aligned16(k_cache) && aligned16(v_cache) && aligned16(v_scale) && aligned16(out),
                PA_ERR_INVALID, "%s: q, the caches, v_scale and out must be 16-byte aligned", name);
+    PA_REQUIRE(static_cast<int64_t>(B) * S1 * NQ <= 0x7FFFFFFF, PA_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 query rows",
+               name);
     if (B == 0) return PA_OK;
     PA_REQUIRE(workspace && workspace_bytes >= need, PA_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", name,
                workspace ? workspace_bytes : static_cast<size_t>(0), need);
