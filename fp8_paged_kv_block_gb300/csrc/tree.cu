@@ -19,18 +19,20 @@
 // P then stays below 2^15, inside FP16, and a key 2^31 below the maximum still
 // counts.
 //
-// A CTA has two streams of (S, P, O) in tensor memory, 256 columns each, and a
-// softmax warpgroup for each. An item of more than 128 rows runs its two row
-// tiles as the streams, every K/V block read once for both; a smaller item
-// runs even and odd blocks as the streams and joins them at the end. While one
-// stream's softmax runs, the other's contractions do.
+// A CTA has two streams with a softmax warpgroup each. An item of more than 128
+// rows runs its two row tiles as the streams, every K/V block read once for
+// both; a smaller item runs even and odd blocks as the streams and joins them at
+// the end. A stream walks half blocks of 64 keys through two S buffers in tensor
+// memory (64 columns each, P over S; O takes 128 columns), so that S of the next
+// half block is computed, and O gets the last one's P V, while the softmax works.
 //   warps 0-3, 4-7   softmax of stream 0, 1 (thread = row = tensor memory lane)
 //   warp 8           K and V blocks by TMA, key scales by cp.async
 //   warps 9, 10      one thread each issues stream 0's, stream 1's MMAs
+//   warp 11          tells the joining kernel about the item at the run's begin
 //   warps 12-15      V codes to FP16 in shared memory, zeros behind the end
 //
-// The blocks of all items, in (sequence, kv head, item, block) order, a block
-// of a two-tile item counting twice, are dealt to the CTAs in equal runs; items
+// The items in (sequence, kv head, item) order are dealt to the CTAs in runs of
+// equal weight: a row tile's block counts 1, an item kItemCost besides. Items
 // that a run's end cuts leave FP32 partial sums, which a second kernel joins.
 #include "common.cuh"
 
@@ -52,7 +54,7 @@ constexpr int kMaxCtas = 192;
 constexpr int kItemRows = 256;
 constexpr int kTile = kBS * kD;              // bytes of a block of codes
 constexpr int kKStages = 4, kVStages = 3, kHStages = 2;
-constexpr int kProdWarp = 8, kMmaWarp = 9, kConvWarp = 12, kConvWarps = 4;
+constexpr int kProdWarp = 8, kMmaWarp = 9, kCutWarp = 11, kConvWarp = 12, kConvWarps = 4;
 // Registers: 512 threads start with 128 each; the softmax warpgroups, which
 // hold a row's 128 scores, go up to 184 and the other two down to 72 (256 x
 // 184 + 256 x 72 = 512 x 128).
@@ -62,10 +64,21 @@ constexpr uint32_t kTmemCols = 512, kOCol = 256;
 constexpr float kRaise = 8.0f;               // log2 units: see the top of the file
 constexpr float kShift = 7.0f;
 
-// Workspace: error word, then at kCumOff the weights before each sequence
-// (int64 [B + 1]), then per CTA two partial items: O [rows][128], m, l [rows].
-constexpr size_t kCumOff = 256;
-constexpr size_t kPartOff = kCumOff + (kMaxB + 1 + 31) / 32 * 32 * sizeof(int64_t);
+constexpr int kHalf = kBS / 2;
+constexpr int kItemCost = 4;
+
+// What the joining kernel has to know of the item at the begin of a run.
+struct Cut {
+    int b, h, row0, rows;                    // rows 0: nothing to join
+    int c0, c1;                              // the runs that have its first and its last block
+    int slot0, pad;                          // where run c0's part lies
+};
+
+// Workspace: error word, a Cut per CTA, then per CTA two partial items: O
+// [rows][128], m and l [rows]. Slot 2 c is of run c's first item, slot 2 c + 1
+// of its last. m = -inf: the part does not count.
+constexpr size_t kCutOff = 256;
+constexpr size_t kPartOff = kCutOff + kMaxCtas * sizeof(Cut);
 
 struct TreeParams {
     const uint8_t* q;
@@ -77,12 +90,13 @@ struct TreeParams {
     int64_t mask_stride;
     __nv_bfloat16* out;
     int* err;
-    int64_t* cum;
+    Cut* cuts;
     float* part;
     int part_rows;                           // rows of a partial item
     int B, S1, NQ, NKV, G;
     int64_t num_blocks;
     int max_blocks, layout, ctas;
+    int keep_l2;                             // K/V blocks serve several items
     float scale_log2;
 };
 
@@ -93,13 +107,14 @@ struct TreeSmem {
     alignas(1024) uint8_t q[2][kTile];
     alignas(16) float ks[kKStages][kBS];
     float ml[2][2][128];                     // m and l of the two streams
+    alignas(16) float vs[kD];
     int64_t cum[kMaxB + 1];
     int64_t warp_sum[kThreads / 32];
     int act[kMaxB];
     uint8_t n[kMaxB];
     uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t h_full[kHStages], h_empty[kHStages];
-    uint64_t s_full[2], p_full[2], o_done[2], q_full, drain[2];
+    uint64_t s_full[2][2], p_full[2][2], o_done[2][2], q_full, q_seen, drain[2];
     uint32_t tmem;
     int abort;
 };
@@ -118,49 +133,74 @@ struct Run {
     bool fresh;
 };
 
-__device__ __forceinline__ int tiles_of(int act) { return (act + kBS - 1) / kBS; }
-// weight of one kv head's block: 2 for every item of 129..256 rows, 1 for a smaller one
-__device__ __forceinline__ int head_weight(int rows) { return (rows + 127) / 128; }
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
 
-__device__ __forceinline__ int64_t run_begin(int64_t total, int c, int ctas) { return total * c / ctas; }
+__device__ __forceinline__ int tiles_of(int act) { return (act + kBS - 1) / kBS; }
+
+// weight of one kv head of a sequence with `rows` query rows a kv head
+__device__ __forceinline__ int64_t head_weight(int rows, int tiles)
+{
+    if (rows == 0 || tiles == 0) return 0;
+    return static_cast<int64_t>((rows + 127) / 128) * tiles + (rows + kItemRows - 1) / kItemRows * kItemCost;
+}
+
+__device__ __forceinline__ int64_t run_begin(int64_t total, int c, int ctas) { return div64(total * c, ctas); }
 // the CTA whose run holds position pos
 __device__ __forceinline__ int cta_of(int64_t total, int64_t pos, int ctas)
 {
-    return static_cast<int>(((pos + 1) * ctas - 1) / total);
+    return static_cast<int>(div64((pos + 1) * ctas - 1, total));
 }
 
-// the item at `pos` inside sequence b, whose first position is `base0`
-__device__ __forceinline__ void locate(int64_t pos, int64_t base0, int rows_b, int tiles, Seg& s, int64_t& base)
+// the item at `pos` of sequence s.b, whose first position is base0; its first
+// position and the one behind it
+__device__ __forceinline__ void locate(int64_t pos, int64_t base0, int rows_b, int tiles, Seg& s, int64_t& base,
+                                       int64_t& end)
 {
-    const int hw = head_weight(rows_b);
-    const int64_t per_head = static_cast<int64_t>(hw) * tiles;
+    const int64_t per_head = head_weight(rows_b, tiles);
     const int64_t rem = pos - base0;
-    s.h = static_cast<int>(rem / per_head);
-    const int64_t in_head = rem - s.h * per_head;
-    const int item = min(static_cast<int>(in_head / (2 * static_cast<int64_t>(tiles))), (hw - 1) / 2);
+    s.h = static_cast<int>(div64(rem, per_head));
+    const int64_t in_head = rem - s.h * per_head, full = 2 * static_cast<int64_t>(tiles) + kItemCost;
+    const int item = min(static_cast<int>(div64(in_head, full)), (rows_b - 1) / kItemRows);
     s.row0 = item * kItemRows;
     s.rows = min(rows_b - s.row0, kItemRows);
     s.dual = s.rows > 128;
     s.tiles = tiles;
-    base = base0 + s.h * per_head + static_cast<int64_t>(item) * 2 * tiles;
+    base = base0 + s.h * per_head + item * full;
+    end = base + (s.dual ? 2 : 1) * static_cast<int64_t>(tiles) + kItemCost;
+}
+
+// blocks of item `s` before position `off` behind its first one
+__device__ __forceinline__ int blocks_before(const Seg& s, int64_t off)
+{
+    const int64_t o = off - kItemCost;
+    const int64_t t = o <= 0 ? 0 : (s.dual ? (o + 1) >> 1 : o);
+    return t < s.tiles ? static_cast<int>(t) : s.tiles;
+}
+
+// The run's next item, its blocks [t0, t1) perhaps none.
+__device__ __forceinline__ bool next_item(const int64_t* cum, const int* act, const uint8_t* n, int G, Run& r, Seg& s)
+{
+    if (r.pos >= r.hi) return false;
+    while (cum[r.b + 1] <= r.pos) ++r.b;
+    s.b = r.b;
+    int64_t base, end;
+    locate(r.pos, cum[r.b], n[r.b] * G, tiles_of(act[r.b]), s, base, end);
+    s.t0 = blocks_before(s, r.pos - base);
+    s.t1 = r.hi >= end ? s.tiles : blocks_before(s, r.hi - base);
+    s.first = r.fresh;
+    r.fresh = false;
+    r.pos = end < r.hi ? end : r.hi;
+    return true;
 }
 
 __device__ __forceinline__ bool next_seg(const int64_t* cum, const int* act, const uint8_t* n, int G, Run& r, Seg& s)
 {
-    while (r.pos < r.hi) {
-        while (cum[r.b + 1] <= r.pos) ++r.b;
-        s.b = r.b;
-        int64_t base;
-        locate(r.pos, cum[r.b], n[r.b] * G, tiles_of(act[r.b]), s, base);
-        const int w = s.dual ? 2 : 1;
-        const int64_t end = base + static_cast<int64_t>(w) * s.tiles;
-        s.t0 = static_cast<int>((r.pos - base + w - 1) / w);
-        s.t1 = r.hi >= end ? s.tiles : static_cast<int>((r.hi - base + w - 1) / w);
-        s.first = r.fresh;
-        r.fresh = false;
-        r.pos = end < r.hi ? end : r.hi;
+    while (next_item(cum, act, n, G, r, s))
         if (s.t0 < s.t1) return true;
-    }
     return false;
 }
 
@@ -240,6 +280,13 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
+__device__ __forceinline__ uint64_t l2_keep_policy()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_unchanged.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 // Row r of item `s` in q and out.
 __device__ __forceinline__ int64_t q_row(const TreeParams& p, const Seg& s, int r)
 {
@@ -256,7 +303,7 @@ __device__ __forceinline__ float* part_of(const TreeParams& p, int cta, bool fir
 __device__ void producer(TreeSmem& sm, const TreeParams& p, const CUtensorMap* tk, const CUtensorMap* tv, Run run,
                          int lane)
 {
-    const uint64_t pol = l2_evict_first_policy();
+    const uint64_t pol = p.keep_l2 ? l2_keep_policy() : l2_evict_first_policy();
     Seg s;
     int kc = 0, vc = 0;                      // blocks requested so far
     bool stop = false;
@@ -354,45 +401,58 @@ __device__ void converter(TreeSmem& sm, const TreeParams& p, Run run, int w, int
     }
 }
 
-// One thread per stream issues its MMAs: S of the next block once the previous
-// P V is complete (P lies over S), P V once the softmax has written P and the
-// block's V is converted.
+// One thread per stream issues its MMAs: P V of a half block once the softmax
+// has written P, then S of the half block after the next, into the same buffer
+// (P lies over S), once that P V is complete.
 __device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w)
 {
-    constexpr uint32_t kIdescS = idesc_e4m3(128, 128, 0, 0);
-    constexpr uint32_t kIdescO = idesc_f16(128, 128, 0, 1);   // P K-major in tensor memory, V MN-major
+    constexpr uint32_t kIdescS = idesc_e4m3(128, kHalf, 0, 0);
+    constexpr uint32_t kIdescO = idesc_f16(128, kD, 0, 1);   // P K-major in tensor memory, V MN-major
     const uint32_t S = tmem + 128 * w, O = tmem + kOCol + 128 * w;
     Seg s;
-    int base = 0, seg = 0, g = 0;            // blocks of all streams, segments, own blocks so far
+    int base = 0, seg = 0, g = 0;            // blocks of all streams, segments, own half blocks so far
     bool ok = true;
     while (ok && next_seg(sm.cum, sm.act, sm.n, p.G, run, s)) {
         const int cnt = s.t1 - s.t0;
-        const int nt = s.dual ? cnt : (cnt + 1 - w) / 2;
-        ok = mbar_wait(&sm.q_full, seg & 1, p.err, 16, &sm.abort);
+        const int nh = 2 * (s.dual ? cnt : (cnt + 1 - w) / 2);
+        auto block = [&](int h) { return base + (s.dual ? h >> 1 : (h & ~1) + w); };
         const uint64_t qd = smem_desc(smem_u32(sm.q[s.dual ? w : 0]), 16, 1024, kSmem128BSwizzle);
-        for (int j = 0; j < nt && ok; ++j, ++g) {
-            const int i = base + (s.dual ? j : 2 * j + w);
-            const int ks = i % kKStages, hs = i % kHStages;
-            ok = mbar_wait(&sm.k_full[ks], (i / kKStages) & 1, p.err, 16, &sm.abort) &&
-                 (g == 0 || mbar_wait(&sm.o_done[w], (g - 1) & 1, p.err, 32, &sm.abort));
+        auto issue_s = [&](int h) {
+            const int i = block(h), slot = i % kKStages;
+            if ((h & 1) == 0 && !mbar_wait(&sm.k_full[slot], (i / kKStages) & 1, p.err, 16, &sm.abort)) return false;
+            tc_fence_after();
+            const uint64_t kd = smem_desc(smem_u32(sm.k[slot]) + (h & 1) * (kHalf * kD), 16, 1024, kSmem128BSwizzle);
+            const int buf = (g + h) & 1;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) umma_e4m3(S + kHalf * buf, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
+            umma_commit(&sm.s_full[w][buf]);
+            return true;
+        };
+        ok = mbar_wait(&sm.q_full, seg & 1, p.err, 16, &sm.abort);
+        mbar_arrive(&sm.q_seen);
+        for (int h = 0; h < 2 && h < nh && ok; ++h) ok = issue_s(h);
+        for (int h = 0; h < nh && ok; ++h) {
+            const int i = block(h), slot = i % kHStages, buf = (g + h) & 1;
+            ok = ((h & 1) != 0 || mbar_wait(&sm.h_full[slot], (i / kHStages) & 1, p.err, 32, &sm.abort)) &&
+                 mbar_wait(&sm.p_full[w][buf], ((g + h) >> 1) & 1, p.err, 32, &sm.abort);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t kd = smem_desc(smem_u32(sm.k[ks]), 16, 1024, kSmem128BSwizzle);
+            const uint64_t vd =
+                smem_desc(smem_u32(sm.vh[slot][0]) + (h & 1) * (kHalf * 128), kTile, 1024, kSmem128BSwizzle);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_e4m3(S, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
-            umma_commit(&sm.s_full[w]);
-            const uint64_t vd = smem_desc(smem_u32(sm.vh[hs][0]), kTile, 1024, kSmem128BSwizzle);
-            ok = mbar_wait(&sm.h_full[hs], (i / kHStages) & 1, p.err, 32, &sm.abort) &&
-                 mbar_wait(&sm.p_full[w], g & 1, p.err, 32, &sm.abort);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < kBS / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of V
-                umma_f16_ta(O, S + 8 * kk, vd + 128 * kk, kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&sm.o_done[w]);
-            umma_commit(&sm.h_empty[hs]);
-            if (!s.dual) umma_commit(&sm.h_empty[hs]);   // (two arrivals a block)
+            for (int kk = 0; kk < kHalf / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of V
+                umma_f16_ta(O, S + kHalf * buf + 8 * kk, vd + 128 * kk, kIdescO, (h > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&sm.o_done[w][buf]);
+            if (h & 1) {
+                umma_commit(&sm.h_empty[slot]);
+                if (!s.dual) umma_commit(&sm.h_empty[slot]);   // (two arrivals a block)
+            }
+            if (h + 2 < nh) {
+                ok = mbar_wait(&sm.o_done[w][buf], ((g + h) >> 1) & 1, p.err, 32, &sm.abort);
+                if (ok) ok = issue_s(h + 2);
+            }
         }
+        g += nh;
         base += cnt;
         ++seg;
     }
@@ -400,42 +460,57 @@ __device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t 
     mbar_wait_drain(&sm.drain[w], 0, p.err, 512);
 }
 
+// One thread's share of a segment's Q rows (16 bytes of eight rows), loaded
+// ahead of the segment, and one channel's value scale.
+struct QLoad {
+    uint4 x[8];
+    float sc[8], vs;
+};
+
+__device__ __forceinline__ void q_load(const TreeParams& p, const Seg& s, int w, int tid, QLoad& q)
+{
+    // this warpgroup's row tile, or its half of the only one
+    const int r_lo = s.dual ? 128 * w : 64 * w, r_n = s.dual ? 128 : 64;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int rr = r_lo + 16 * i + (tid >> 3);
+        q.x[i] = make_uint4(0, 0, 0, 0);
+        q.sc[i] = 0.0f;
+        if (16 * i < r_n && rr < s.rows) {
+            const int64_t at = q_row(p, s, rr);
+            q.x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + at * kD) + (tid & 7));
+            q.sc[i] = __ldg(p.q_scale + at);
+        }
+    }
+    q.vs = __ldg(p.v_scale + (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD + tid);
+}
+
 __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w, int warp, int lane)
 {
     const int q4 = warp & 3, row = 32 * q4 + lane, tid = row;
     const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
-    const uint32_t S = tmem + lanes + 128 * w;
-    Seg s;
-    int base = 0, g = 0;
-    while (next_seg(sm.cum, sm.act, sm.n, p.G, run, s)) {
+    const uint32_t O = tmem + lanes + kOCol + 128 * w;
+    Seg s, ns;
+    int base = 0, g = 0, seg = 0;            // blocks of all streams, own half blocks, segments
+    bool more = next_seg(sm.cum, sm.act, sm.n, p.G, run, ns);
+    QLoad ql;
+    if (more) q_load(p, ns, w, tid, ql);
+    while (more) {
+        s = ns;
         const int act = sm.act[s.b], n = sm.n[s.b], ctx = act - n, cnt = s.t1 - s.t0;
         const int nt = s.dual ? cnt : (cnt + 1 - w) / 2;
-        // ---- Q rows into the operand layout: this warpgroup's row tile, or its half of the one ----
+        // ---- Q rows into the operand layout ----
         {
             const int tile = s.dual ? w : 0, r_lo = s.dual ? 0 : 64 * w, r_n = s.dual ? 128 : 64;
-            // 16 bytes a thread, all loads in flight before the first is stored
-            const int u = tid & 7;
-            uint4 x[8];
-            float sc[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int rr = 128 * tile + r_lo + 16 * i + (tid >> 3);
-                x[i] = make_uint4(0, 0, 0, 0);
-                sc[i] = 0.0f;
-                if (16 * i < r_n && rr < s.rows) {
-                    const int64_t at = q_row(p, s, rr);
-                    x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + at * kD) + u);
-                    sc[i] = __ldg(p.q_scale + at);
-                }
-            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (16 * i >= r_n) break;
                 // a negative scale: the codes' signs, so that the maximum stays a maximum
-                const uint32_t flip = sc[i] * p.scale_log2 < 0.0f ? 0x80808080u : 0u;
-                *reinterpret_cast<uint4*>(sm.q[tile] + sw128(r_lo + 16 * i + (tid >> 3), u)) =
-                    make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
+                const uint32_t flip = ql.sc[i] * p.scale_log2 < 0.0f ? 0x80808080u : 0u;
+                *reinterpret_cast<uint4*>(sm.q[tile] + sw128(r_lo + 16 * i + (tid >> 3), tid & 7)) =
+                    make_uint4(ql.x[i].x ^ flip, ql.x[i].y ^ flip, ql.x[i].z ^ flip, ql.x[i].w ^ flip);
             }
+            if (w == 0) sm.vs[tid] = ql.vs;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.q_full);
@@ -464,22 +539,23 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
             }
         }
         float m = -INFINITY, l = 0.0f;
-        for (int j = 0; j < nt; ++j, ++g) {
-            const int t = s.t0 + (s.dual ? j : 2 * j + w), i = base + (s.dual ? j : 2 * j + w);
-            const int slot = i % kKStages;
-            mbar_wait(&sm.s_full[w], g & 1, p.err, 64, &sm.abort);
+        for (int h = 0; h < 2 * nt; ++h, ++g) {
+            const int j = s.dual ? h >> 1 : (h & ~1) + w;      // block of the segment
+            const int slot = (base + j) % kKStages;
+            const uint32_t S = tmem + lanes + 128 * w + kHalf * (g & 1);
+            mbar_wait(&sm.s_full[w][g & 1], (g >> 1) & 1, p.err, 64, &sm.abort);
             if (warp_live) {
                 tc_fence_after();
                 // k_full is complete too (S came out of it), but the scales were
                 // written by other threads' copies: its wait orders them
-                mbar_wait(&sm.k_full[slot], (i / kKStages) & 1, p.err, 64, &sm.abort);
-                float v[kBS];
+                mbar_wait(&sm.k_full[slot], ((base + j) / kKStages) & 1, p.err, 64, &sm.abort);
+                float v[kHalf];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, v + 32 * c);
+                for (int c = 0; c < 2; ++c) tmem_ld32(S + 32 * c, v + 32 * c);
                 tmem_wait_ld();
-                const float4* ks = reinterpret_cast<const float4*>(sm.ks[slot]);
+                const float4* ks = reinterpret_cast<const float4*>(sm.ks[slot] + (h & 1) * kHalf);
 #pragma unroll
-                for (int c = 0; c < kBS / 4; ++c) {
+                for (int c = 0; c < kHalf / 4; ++c) {
                     const float4 k4 = ks[c];
                     const float2 a = mul2(make_float2(v[4 * c], v[4 * c + 1]), make_float2(k4.x, k4.y));
                     const float2 b = mul2(make_float2(v[4 * c + 2], v[4 * c + 3]), make_float2(k4.z, k4.w));
@@ -488,56 +564,43 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                     v[4 * c + 2] = b.x;
                     v[4 * c + 3] = b.y;
                 }
-                const int off = ctx - t * kBS;                 // the first drafted token's key in this block
-                if (off < kBS) {
+                const int off = ctx - (s.t0 + j) * kBS - (h & 1) * kHalf;   // the first drafted token's key here
+                if (off < kHalf) {
                     // which keys the row sees: the context's, then its mask's bits
-                    uint64_t lo, hi;
-                    if (off >= 64) {
-                        lo = ~0ull;
-                        hi = (off == 64 ? 0ull : ~0ull >> (128 - off)) | (m_lo << (off - 64));
-                    } else if (off > 0) {
-                        lo = (~0ull >> (64 - off)) | (m_lo << off);
-                        hi = (m_hi << off) | (m_lo >> (64 - off));
-                    } else if (off == 0) {
-                        lo = m_lo;
-                        hi = m_hi;
-                    } else if (off > -64) {
-                        lo = (m_lo >> -off) | (m_hi << (64 + off));
-                        hi = m_hi >> -off;
-                    } else {
-                        lo = off > -128 ? m_hi >> (-off - 64) : 0ull;
-                        hi = 0ull;
-                    }
+                    uint64_t see;
+                    if (off > 0) see = (~0ull >> (64 - off)) | (m_lo << off);
+                    else if (off == 0) see = m_lo;
+                    else if (off > -64) see = (m_lo >> -off) | (m_hi << (64 + off));
+                    else see = off > -128 ? m_hi >> (-off - 64) : 0ull;
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) {
-                        if (!((lo >> k) & 1)) v[k] = -INFINITY;
-                        if (!((hi >> k) & 1)) v[64 + k] = -INFINITY;
-                    }
+                    for (int k = 0; k < kHalf; ++k)
+                        if (!((see >> k) & 1)) v[k] = -INFINITY;
                 }
                 float m4[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    m4[c] = fmaxf(v[32 * c], v[32 * c + 1]);
+                    m4[c] = fmaxf(v[16 * c], v[16 * c + 1]);
 #pragma unroll
-                    for (int k = 2; k < 32; k += 2) m4[c] = max3(m4[c], v[32 * c + k], v[32 * c + k + 1]);
+                    for (int k = 2; k < 16; k += 2) m4[c] = max3(m4[c], v[16 * c + k], v[16 * c + k + 1]);
                 }
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rs;
+                const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * rs;
                 const bool raise = mx > m + kRaise || (m == -INFINITY && mx > -INFINITY);
                 if (__any_sync(0xffffffffu, raise)) {
                     const float f = raise ? ex2(m - mx) : 1.0f;
                     if (raise) m = mx;
                     l *= f;
-                    if (j > 0) {
-                        // S of this block was issued after the last P V had completed
+                    if (h > 0) {
+                        // O is complete up to the last half block before it is scaled
+                        mbar_wait(&sm.o_done[w][(g - 1) & 1], ((g - 1) >> 1) & 1, p.err, 128, &sm.abort);
+                        tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             float o[32];
-                            const uint32_t at = tmem + lanes + kOCol + 128 * w + 32 * c;
-                            tmem_ld32(at, o);
+                            tmem_ld32(O + 32 * c, o);
                             tmem_wait_ld();
 #pragma unroll
                             for (int k = 0; k < 32; ++k) o[k] *= f;
-                            tmem_st32(at, o);
+                            tmem_st32(O + 32 * c, o);
                         }
                     }
                 }
@@ -545,17 +608,17 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                 const float2 rs2 = make_float2(rs, rs), nref = make_float2(-ref, -ref);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t h[16];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t hp[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
                         float2 x = fma2(make_float2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), rs2, nref);
                         x.x = ex2(x.x);
                         x.y = ex2(x.y);
                         sum[k & 1] = add2(sum[k & 1], x);
-                        h[k] = half2_bits(x.x, x.y);
+                        hp[k] = half2_bits(x.x, x.y);
                     }
-                    tmem_st16(S + 16 * c, h);
+                    tmem_st16(S + 16 * c, hp);
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tmem_wait_st();
@@ -563,11 +626,21 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
             }
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sm.p_full[w]);
-                mbar_arrive_n(&sm.k_empty[slot], s.dual ? 1 : 2);
+                mbar_arrive(&sm.p_full[w][g & 1]);
+                if (h & 1) mbar_arrive_n(&sm.k_empty[slot], s.dual ? 1 : 2);
             }
         }
-        if (nt > 0) mbar_wait(&sm.o_done[w], (g - 1) & 1, p.err, 128, &sm.abort);
+        more = next_seg(sm.cum, sm.act, sm.n, p.G, run, ns);
+        if (more) q_load(p, ns, w, tid, ql);
+        // both issuing threads have seen this segment's Q (a stream without blocks
+        // waits for nothing else, and must not fall two phases behind)
+        mbar_wait(&sm.q_seen, seg++ & 1, p.err, 128, &sm.abort);
+        if (nt > 0) {
+            // (the last two half blocks: one barrier each, as a wait by parity is for
+            // a barrier's latest phase alone)
+            mbar_wait(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
+            mbar_wait(&sm.o_done[w][(g - 1) & 1], ((g - 1) >> 1) & 1, p.err, 128, &sm.abort);
+        }
         tc_fence_before();
         // ---- the item's (or its part's) output ----
         const bool whole = s.t0 == 0 && s.t1 == s.tiles;
@@ -600,8 +673,7 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
             const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
             const int at = live ? static_cast<int>(q_row(p, s, my)) : -1;
             uint8_t* const stage = sm.q[w];
-            const float4* vs = reinterpret_cast<const float4*>(p.v_scale +
-                                                               (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD + d0);
+            const float4* vs = reinterpret_cast<const float4*>(sm.vs + d0);
             const int nc = dn / 32;
 #pragma unroll 1
             for (int c = 0; c < nc; ++c) {
@@ -622,7 +694,7 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                 if (whole) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float4 a = __ldg(vs + 8 * c + 2 * k), b = __ldg(vs + 8 * c + 2 * k + 1);
+                        const float4 a = vs[8 * c + 2 * k], b = vs[8 * c + 2 * k + 1];
                         const float* x = o + 8 * k;
                         const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * inv * a.x, x[1] * inv * a.y);
                         const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * inv * a.z, x[3] * inv * a.w);
@@ -666,6 +738,54 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
     }
 }
 
+// What the joining kernel has to know of the item at the begin of this CTA's run.
+__device__ void describe_cut(TreeSmem& sm, const TreeParams& p, Run run, int64_t total, int lane)
+{
+    const int c = blockIdx.x;
+    const int64_t lo = run.pos;
+    Cut cut = {};
+    Seg s;
+    // (an empty run has positions of the item behind it, but no part)
+    if (lo < total && c > 0) {
+        if (run.pos == run.hi) {
+            int a = 0, z = p.B - 1;
+            while (a < z) {
+                const int mid = (a + z + 1) >> 1;
+                if (sm.cum[mid] <= lo) a = mid;
+                else z = mid - 1;
+            }
+            run.b = a;
+        }
+        while (sm.cum[run.b + 1] <= lo) ++run.b;
+        s.b = run.b;
+        int64_t base, end;
+        locate(lo, sm.cum[s.b], sm.n[s.b] * p.G, tiles_of(sm.act[s.b]), s, base, end);
+        if (lo > base) {
+            const int t0 = blocks_before(s, lo - base);
+            const int t1 = run.hi >= end ? s.tiles : blocks_before(s, run.hi - base);
+            if (t0 >= t1) {                  // no block of it here: a part that does not count
+                float* ml = part_of(p, c, true) + static_cast<int64_t>(p.part_rows) * kD;
+                for (int r = lane; r < s.rows; r += 32) {
+                    ml[r] = -INFINITY;
+                    ml[p.part_rows + r] = 0.0f;
+                }
+            }
+            // the runs that hold the first and the last block's positions
+            const int c0 = cta_of(total, base + kItemCost, p.ctas), c1 = cta_of(total, end - (s.dual ? 2 : 1), p.ctas);
+            if (c == c0 + 1 && c0 < c1) {
+                cut.b = s.b;
+                cut.h = s.h;
+                cut.row0 = s.row0;
+                cut.rows = s.rows;
+                cut.c0 = c0;
+                cut.c1 = c1;
+                cut.slot0 = 2 * c0 + (run_begin(total, c0, p.ctas) >= base ? 0 : 1);
+            }
+        }
+    }
+    if (lane == 0) p.cuts[c] = cut;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     tree_decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const TreeParams p)
 {
@@ -688,16 +808,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.h_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 4);
-            mbar_init(&sm.o_done[i], 1);
+            mbar_init(&sm.s_full[i][0], 1);
+            mbar_init(&sm.s_full[i][1], 1);
+            mbar_init(&sm.p_full[i][0], 4);
+            mbar_init(&sm.p_full[i][1], 4);
+            mbar_init(&sm.o_done[i][0], 1);
+            mbar_init(&sm.o_done[i][1], 1);
             mbar_init(&sm.drain[i], 1);
         }
         mbar_init(&sm.q_full, 8);
+        mbar_init(&sm.q_seen, 2);
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) tmem_alloc(&sm.tmem, kTmemCols);
+    grid_launch_dependents();   // (the joining kernel waits for this one's end)
 
     // ---- weights before each sequence: thread i takes sequences i, i + 1, ... of its share ----
     {
@@ -711,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sm.act[b] = act;
             sm.n[b] = static_cast<uint8_t>(n);
             sm.cum[b] = mine;
-            mine += static_cast<int64_t>(p.NKV) * head_weight(n * p.G) * tiles_of(act);
+            mine += static_cast<int64_t>(p.NKV) * head_weight(n * p.G, tiles_of(act));
         }
         int64_t x = mine;
 #pragma unroll
@@ -751,14 +876,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         softmax(sm, p, run, tmem, warp >> 2, warp, lane);
     } else if (warp < kConvWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp != kProdWarp) {
-            if (warp - kMmaWarp < 2 && lane == 0) mma_issuer(sm, p, run, tmem, warp - kMmaWarp);
-            __syncwarp();
-        } else {
-        if (blockIdx.x == 0)
-            for (int b = lane; b <= p.B; b += 32) p.cum[b] = sm.cum[b];
-        producer(sm, p, &tk, &tv, run, lane);
-        }
+        if (warp == kProdWarp) producer(sm, p, &tk, &tv, run, lane);
+        else if (warp == kCutWarp) describe_cut(sm, p, run, total, lane);
+        else if (lane == 0) mma_issuer(sm, p, run, tmem, warp - kMmaWarp);
+        __syncwarp();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // rows that see nothing because their sequence has no such node
@@ -776,73 +897,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
-    grid_launch_dependents();
 }
 
 // Joins the parts of the items that a run's end cut: CTA (c, y) takes the item
-// at the begin of run c, if run c - 1 is the item's first, and its rows 8 y ..
-// 8 y + 7, one warp each.
+// whose first block run c has and whose last one a later run, its rows 8 y .. 8 y + 7, one warp each.
 constexpr int kJoinWarps = 8;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeParams p)
 {
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
-    const int c = blockIdx.x + 1;
-    const int64_t total = p.cum[p.B];
-    const int64_t pos = run_begin(total, c, p.ctas);
-    if (total == 0 || pos >= total) return;
-    int lo = 0, hi = p.B - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.cum[mid] <= pos) lo = mid;
-        else hi = mid - 1;
-    }
-    const int64_t cap = static_cast<int64_t>(p.max_blocks) * kBS;
-    const int act = static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.act + lo), 0)), cap));
-    int n = p.len ? __ldg(p.len + lo) : p.S1;
-    n = min(max(n, 0), min(p.S1, act));
+    const int4 a = *reinterpret_cast<const int4*>(p.cuts + blockIdx.x + 1);
+    const int4 z = *(reinterpret_cast<const int4*>(p.cuts + blockIdx.x + 1) + 1);
     Seg s;
-    s.b = lo;
-    int64_t base;
-    locate(pos, p.cum[lo], n * p.G, tiles_of(act), s, base);
-    const int w = s.dual ? 2 : 1;
-    const int64_t end = base + static_cast<int64_t>(w) * s.tiles;
-    const int c0 = cta_of(total, base, p.ctas), c1 = cta_of(total, end - 1, p.ctas);
-    if (c != c0 + 1 || pos == base) return;
+    s.b = a.x;
+    s.h = a.y;
+    s.row0 = a.z;
+    s.rows = a.w;
     const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
     if (row >= s.rows) return;
-
-    // lane i looks at runs c0 + i, c0 + i + 32, ...: their blocks [t0, t1) of the
-    // item, where their part lies, its m and l
+    const int c0 = z.x, c1 = z.y, slot0 = z.z;
+    const float4 v =
+        __ldg(reinterpret_cast<const float4*>(p.v_scale + (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD) + lane);
+    // lane i has m and l of runs c0 + i, c0 + i + 32, ...
     constexpr int kPer = kMaxCtas / 32;
     float mi[kPer], li[kPer], M = -INFINITY;
-    int slot[kPer];
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int i = c0 + 32 * k + lane;
+        const int slot = i == c0 ? slot0 : 2 * i;
         mi[k] = -INFINITY;
         li[k] = 0.0f;
-        slot[k] = -1;
-        bool all = false;
         if (i <= c1) {
-            const int64_t b0 = run_begin(total, i, p.ctas), b1 = run_begin(total, i + 1, p.ctas);
-            const int64_t t0 = b0 > base ? (b0 - base + w - 1) / w : 0;
-            const int64_t t1 = b1 >= end ? s.tiles : (b1 - base + w - 1) / w;
-            all = t0 == 0 && t1 == s.tiles;
-            if (t0 < t1 && !all) {
-                slot[k] = 2 * i + (b0 >= base ? 0 : 1);
-                const float* ml = p.part + static_cast<int64_t>(slot[k]) * p.part_rows * (kD + 2) +
-                                  static_cast<int64_t>(p.part_rows) * kD;
-                mi[k] = ml[row];
-                li[k] = ml[p.part_rows + row];
-            }
+            const float* ml = p.part + static_cast<int64_t>(slot) * p.part_rows * (kD + 2) +
+                              static_cast<int64_t>(p.part_rows) * kD;
+            mi[k] = ml[row];
+            li[k] = ml[p.part_rows + row];
         }
-        if (__any_sync(0xffffffffu, all)) return;   // one run had all of it
         M = fmaxf(M, mi[k]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    M = warp_max_f32(M);
     float L = 0.0f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -852,10 +946,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
         const int last = min(c1 - c0 - 32 * k, 31);
 #pragma unroll 8
         for (int i = 0; i <= last; ++i) {
-            const int sl = __shfl_sync(0xffffffffu, slot[k], i);
             const float fi = __shfl_sync(0xffffffffu, f, i);
-            if (sl < 0) continue;
-            const float4 x = reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(sl) * p.part_rows * (kD + 2) +
+            if (fi == 0.0f) continue;        // (its O may be anything)
+            const int c = c0 + 32 * k + i, slot = c == c0 ? slot0 : 2 * c;
+            const float4 x = reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(slot) * p.part_rows * (kD + 2) +
                                                              static_cast<int64_t>(row) * kD)[lane];
             o.x += x.x * fi;
             o.y += x.y * fi;
@@ -866,7 +960,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) L += __shfl_xor_sync(0xffffffffu, L, i);
     const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
-    const float4 v = __ldg(reinterpret_cast<const float4*>(p.v_scale + (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD) + lane);
     const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * inv * v.x, o.y * inv * v.y);
     const __nv_bfloat162 y1 = __floats2bfloat162_rn(o.z * inv * v.z, o.w * inv * v.w);
     reinterpret_cast<uint2*>(p.out + q_row(p, s, row) * kD)[lane] =
@@ -967,7 +1060,7 @@ extern "C" pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, con
     p.mask_stride = mask_stride;
     p.out = static_cast<__nv_bfloat16*>(out);
     p.err = reinterpret_cast<int*>(ws);
-    p.cum = reinterpret_cast<int64_t*>(ws + kCumOff);
+    p.cuts = reinterpret_cast<Cut*>(ws + kCutOff);
     p.part = reinterpret_cast<float*>(ws + kPartOff);
     p.part_rows = part_rows(S1, NQ / NKV);
     p.B = B;
@@ -979,6 +1072,7 @@ extern "C" pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, con
     p.max_blocks = max_blocks_per_seq;
     p.layout = layout;
     p.ctas = sms < kMaxCtas ? sms : kMaxCtas;
+    p.keep_l2 = static_cast<int64_t>(S1) * p.G > kItemRows;
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
 
     const size_t smem = sizeof(TreeSmem) + 1024;
