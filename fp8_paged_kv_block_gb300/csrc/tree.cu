@@ -53,7 +53,16 @@ constexpr int kMaxB = 1024;
 constexpr int kMaxCtas = 192;
 constexpr int kItemRows = 256;
 constexpr int kTile = kBS * kD;              // bytes of a block of codes
-constexpr int kKStages = 4, kVStages = 3, kHStages = 2;
+// K blocks, V blocks as codes and as FP16, key scales. The scales' ring needs no
+// barrier that says a slot is free: block i + 6 is requested once the K blocks
+// up to i + 3 are free, i.e. S of their second halves complete, which is issued
+// after the stream's previous block's P V (block i + 1's at least) and so after
+// the softmax of the blocks up to i. K's and the scales' arrival share a barrier
+// of that ring: six is even, so that a stream that takes every other block finds
+// its own earlier block in the barrier's last phase, never one that it has not
+// waited for (copies may land out of order, and a parity wait is good for the
+// phase after a completed one only).
+constexpr int kKStages = 3, kVStages = 2, kHStages = 3, kSStages = 6;
 constexpr int kProdWarp = 8, kMmaWarp = 9, kCutWarp = 11, kConvWarp = 12, kConvWarps = 4;
 // Registers: 512 threads start with 128 each; the softmax warpgroups, which
 // hold a row's 128 scores, go up to 184 and the other two down to 72 (256 x
@@ -105,14 +114,12 @@ struct TreeSmem {
     alignas(1024) uint8_t v[kVStages][kTile];
     alignas(1024) uint8_t vh[kHStages][2][kTile];   // FP16, channels 0-63 and 64-127
     alignas(1024) uint8_t q[2][kTile];
-    alignas(16) float ks[kKStages][kBS];
-    float ml[2][2][128];                     // m and l of the two streams
+    alignas(16) float ks[kSStages][kBS];
+    alignas(8) float ml[2][2][128];                     // m and l of the two streams
     alignas(16) float vs[kD];
     int64_t cum[kMaxB + 1];
-    int64_t warp_sum[kThreads / 32];
-    int act[kMaxB];
-    uint8_t n[kMaxB];
-    uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+    uint32_t len[kMaxB];                     // length << 8 | drafted tokens
+    uint64_t k_full[kSStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t h_full[kHStages], h_empty[kHStages];
     uint64_t s_full[2][2], p_full[2][2], o_done[2][2], q_full, q_seen, drain[2];
     uint32_t tmem;
@@ -182,13 +189,13 @@ __device__ __forceinline__ int blocks_before(const Seg& s, int64_t off)
 }
 
 // The run's next item, its blocks [t0, t1) perhaps none.
-__device__ __forceinline__ bool next_item(const int64_t* cum, const int* act, const uint8_t* n, int G, Run& r, Seg& s)
+__device__ __forceinline__ bool next_item(const int64_t* cum, const uint32_t* len, int G, Run& r, Seg& s)
 {
     if (r.pos >= r.hi) return false;
     while (cum[r.b + 1] <= r.pos) ++r.b;
     s.b = r.b;
     int64_t base, end;
-    locate(r.pos, cum[r.b], n[r.b] * G, tiles_of(act[r.b]), s, base, end);
+    locate(r.pos, cum[r.b], (len[r.b] & 0xFF) * G, tiles_of(len[r.b] >> 8), s, base, end);
     s.t0 = blocks_before(s, r.pos - base);
     s.t1 = r.hi >= end ? s.tiles : blocks_before(s, r.hi - base);
     s.first = r.fresh;
@@ -197,9 +204,9 @@ __device__ __forceinline__ bool next_item(const int64_t* cum, const int* act, co
     return true;
 }
 
-__device__ __forceinline__ bool next_seg(const int64_t* cum, const int* act, const uint8_t* n, int G, Run& r, Seg& s)
+__device__ __forceinline__ bool next_seg(const int64_t* cum, const uint32_t* len, int G, Run& r, Seg& s)
 {
-    while (next_item(cum, act, n, G, r, s))
+    while (next_item(cum, len, G, r, s))
         if (s.t0 < s.t1) return true;
     return false;
 }
@@ -307,7 +314,7 @@ __device__ void producer(TreeSmem& sm, const TreeParams& p, const CUtensorMap* t
     Seg s;
     int kc = 0, vc = 0;                      // blocks requested so far
     bool stop = false;
-    while (!stop && next_seg(sm.cum, sm.act, sm.n, p.G, run, s)) {
+    while (!stop && next_seg(sm.cum, sm.len, p.G, run, s)) {
         const int* row = p.bt + static_cast<int64_t>(s.b) * p.max_blocks;
         int ids = 0;
         for (int t = s.t0; t < s.t1; ++t) {
@@ -319,22 +326,22 @@ __device__ void producer(TreeSmem& sm, const TreeParams& p, const CUtensorMap* t
             const int64_t blk = __shfl_sync(0xffffffffu, ids, at);
             const int x = p.layout == PA_LAYOUT_BSND ? s.h * kD : 0;
             const int y = static_cast<int>(p.layout == PA_LAYOUT_BSND ? blk * kBS : (blk * p.NKV + s.h) * kBS);
-            const int kslot = kc % kKStages, vslot = vc % kVStages;
+            const int kslot = kc % kKStages, vslot = vc % kVStages, sslot = kc % kSStages;
             if (!mbar_wait(&sm.k_empty[kslot], ((kc / kKStages) & 1) ^ 1, p.err, 1, &sm.abort)) stop = true;
             if (__any_sync(0xffffffffu, stop)) {
                 stop = true;
                 break;
             }
             if (lane == 0) {
-                mbar_arrive_expect_tx(&sm.k_full[kslot], kTile);
-                tma_load_2d(sm.k[kslot], tk, x, y, &sm.k_full[kslot], pol);
+                mbar_arrive_expect_tx(&sm.k_full[sslot], kTile);
+                tma_load_2d(sm.k[kslot], tk, x, y, &sm.k_full[sslot], pol);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int j = lane + 32 * i;
-                cp_async4(&sm.ks[kslot][j], p.k_scale + cache_row(p.layout, blk, j, s.h, kBS, p.NKV), 4);
+                cp_async4(&sm.ks[sslot][j], p.k_scale + cache_row(p.layout, blk, j, s.h, kBS, p.NKV), 4);
             }
-            cp_async_arrive_noinc(&sm.k_full[kslot]);
+            cp_async_arrive_noinc(&sm.k_full[sslot]);
             ++kc;
             if (!mbar_wait(&sm.v_empty[vslot], ((vc / kVStages) & 1) ^ 1, p.err, 2, &sm.abort)) stop = true;
             if (__any_sync(0xffffffffu, stop)) {
@@ -350,8 +357,8 @@ __device__ void producer(TreeSmem& sm, const TreeParams& p, const CUtensorMap* t
         }
     }
     // every copy has landed before this CTA's shared memory is given up
-    for (int i = max(0, kc - kKStages); i < kc; ++i)
-        mbar_wait_drain(&sm.k_full[i % kKStages], (i / kKStages) & 1, p.err, 256);
+    for (int i = max(0, kc - kSStages); i < kc; ++i)
+        mbar_wait_drain(&sm.k_full[i % kSStages], (i / kSStages) & 1, p.err, 256);
     for (int i = max(0, vc - kVStages); i < vc; ++i)
         mbar_wait_drain(&sm.v_full[i % kVStages], (i / kVStages) & 1, p.err, 256);
 }
@@ -364,8 +371,8 @@ __device__ void converter(TreeSmem& sm, const TreeParams& p, Run run, int w, int
     Seg s;
     int c = 0;
     const int u = lane & 7, r = lane >> 3;
-    while (next_seg(sm.cum, sm.act, sm.n, p.G, run, s)) {
-        const int act = sm.act[s.b];
+    while (next_seg(sm.cum, sm.len, p.G, run, s)) {
+        const int act = static_cast<int>(sm.len[s.b] >> 8);
         for (int t = s.t0; t < s.t1; ++t, ++c) {
             const int vslot = c % kVStages, hslot = c % kHStages;
             mbar_wait(&sm.v_full[vslot], (c / kVStages) & 1, p.err, 4, &sm.abort);
@@ -412,20 +419,24 @@ __device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t 
     Seg s;
     int base = 0, seg = 0, g = 0;            // blocks of all streams, segments, own half blocks so far
     bool ok = true;
-    while (ok && next_seg(sm.cum, sm.act, sm.n, p.G, run, s)) {
+    while (ok && next_seg(sm.cum, sm.len, p.G, run, s)) {
         const int cnt = s.t1 - s.t0;
         const int nh = 2 * (s.dual ? cnt : (cnt + 1 - w) / 2);
         auto block = [&](int h) { return base + (s.dual ? h >> 1 : (h & ~1) + w); };
         const uint64_t qd = smem_desc(smem_u32(sm.q[s.dual ? w : 0]), 16, 1024, kSmem128BSwizzle);
         auto issue_s = [&](int h) {
             const int i = block(h), slot = i % kKStages;
-            if ((h & 1) == 0 && !mbar_wait(&sm.k_full[slot], (i / kKStages) & 1, p.err, 16, &sm.abort)) return false;
+            if ((h & 1) == 0 && !mbar_wait(&sm.k_full[i % kSStages], (i / kSStages) & 1, p.err, 16, &sm.abort)) return false;
             tc_fence_after();
             const uint64_t kd = smem_desc(smem_u32(sm.k[slot]) + (h & 1) * (kHalf * kD), 16, 1024, kSmem128BSwizzle);
             const int buf = (g + h) & 1;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) umma_e4m3(S + kHalf * buf, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
             umma_commit(&sm.s_full[w][buf]);
+            if (h & 1) {
+                umma_commit(&sm.k_empty[slot]);
+                if (!s.dual) umma_commit(&sm.k_empty[slot]);   // (two arrivals a block)
+            }
             return true;
         };
         ok = mbar_wait(&sm.q_full, seg & 1, p.err, 16, &sm.abort);
@@ -445,7 +456,7 @@ __device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t 
             umma_commit(&sm.o_done[w][buf]);
             if (h & 1) {
                 umma_commit(&sm.h_empty[slot]);
-                if (!s.dual) umma_commit(&sm.h_empty[slot]);   // (two arrivals a block)
+                if (!s.dual) umma_commit(&sm.h_empty[slot]);
             }
             if (h + 2 < nh) {
                 ok = mbar_wait(&sm.o_done[w][buf], ((g + h) >> 1) & 1, p.err, 32, &sm.abort);
@@ -492,12 +503,12 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
     const uint32_t O = tmem + lanes + kOCol + 128 * w;
     Seg s, ns;
     int base = 0, g = 0, seg = 0;            // blocks of all streams, own half blocks, segments
-    bool more = next_seg(sm.cum, sm.act, sm.n, p.G, run, ns);
+    bool more = next_seg(sm.cum, sm.len, p.G, run, ns);
     QLoad ql;
     if (more) q_load(p, ns, w, tid, ql);
     while (more) {
         s = ns;
-        const int act = sm.act[s.b], n = sm.n[s.b], ctx = act - n, cnt = s.t1 - s.t0;
+        const int act = static_cast<int>(sm.len[s.b] >> 8), n = static_cast<int>(sm.len[s.b] & 0xFF), ctx = act - n, cnt = s.t1 - s.t0;
         const int nt = s.dual ? cnt : (cnt + 1 - w) / 2;
         // ---- Q rows into the operand layout ----
         {
@@ -541,14 +552,12 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
         float m = -INFINITY, l = 0.0f;
         for (int h = 0; h < 2 * nt; ++h, ++g) {
             const int j = s.dual ? h >> 1 : (h & ~1) + w;      // block of the segment
-            const int slot = (base + j) % kKStages;
+            const int slot = (base + j) % kSStages;
             const uint32_t S = tmem + lanes + 128 * w + kHalf * (g & 1);
             mbar_wait(&sm.s_full[w][g & 1], (g >> 1) & 1, p.err, 64, &sm.abort);
             if (warp_live) {
                 tc_fence_after();
-                // k_full is complete too (S came out of it), but the scales were
-                // written by other threads' copies: its wait orders them
-                mbar_wait(&sm.k_full[slot], ((base + j) / kKStages) & 1, p.err, 64, &sm.abort);
+                mbar_wait(&sm.k_full[slot], ((base + j) / kSStages) & 1, p.err, 64, &sm.abort);
                 float v[kHalf];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) tmem_ld32(S + 32 * c, v + 32 * c);
@@ -625,12 +634,9 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                 tc_fence_before();
             }
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sm.p_full[w][g & 1]);
-                if (h & 1) mbar_arrive_n(&sm.k_empty[slot], s.dual ? 1 : 2);
-            }
+            if (lane == 0) mbar_arrive(&sm.p_full[w][g & 1]);
         }
-        more = next_seg(sm.cum, sm.act, sm.n, p.G, run, ns);
+        more = next_seg(sm.cum, sm.len, p.G, run, ns);
         if (more) q_load(p, ns, w, tid, ql);
         // both issuing threads have seen this segment's Q (a stream without blocks
         // waits for nothing else, and must not fall two phases behind)
@@ -759,7 +765,7 @@ __device__ void describe_cut(TreeSmem& sm, const TreeParams& p, Run run, int64_t
         while (sm.cum[run.b + 1] <= lo) ++run.b;
         s.b = run.b;
         int64_t base, end;
-        locate(lo, sm.cum[s.b], sm.n[s.b] * p.G, tiles_of(sm.act[s.b]), s, base, end);
+        locate(lo, sm.cum[s.b], (sm.len[s.b] & 0xFF) * p.G, tiles_of(sm.len[s.b] >> 8), s, base, end);
         if (lo > base) {
             const int t0 = blocks_before(s, lo - base);
             const int t1 = run.hi >= end ? s.tiles : blocks_before(s, run.hi - base);
@@ -795,10 +801,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int i = 0; i < kKStages; ++i) {
-            mbar_init(&sm.k_full[i], 33);
-            mbar_init(&sm.k_empty[i], 8);
-        }
+        for (int i = 0; i < kSStages; ++i) mbar_init(&sm.k_full[i], 33);
+        for (int i = 0; i < kKStages; ++i) mbar_init(&sm.k_empty[i], 2);
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(&sm.v_full[i], 1);
             mbar_init(&sm.v_empty[i], kConvWarps);
@@ -833,8 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int act = static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.act + b), 0)), cap));
             int n = p.len ? __ldg(p.len + b) : p.S1;
             n = min(max(n, 0), min(p.S1, act));
-            sm.act[b] = act;
-            sm.n[b] = static_cast<uint8_t>(n);
+            sm.len[b] = static_cast<uint32_t>(act) << 8 | static_cast<uint32_t>(n);
             sm.cum[b] = mine;
             mine += static_cast<int64_t>(p.NKV) * head_weight(n * p.G, tiles_of(act));
         }
@@ -844,10 +847,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        if (lane == 31) sm.warp_sum[warp] = x;
+        int64_t* const warp_sum = reinterpret_cast<int64_t*>(sm.ml);
+        if (lane == 31) warp_sum[warp] = x;
         __syncthreads();
         int64_t before = x - mine;
-        for (int i = 0; i < warp; ++i) before += sm.warp_sum[i];
+        for (int i = 0; i < warp; ++i) before += warp_sum[i];
         for (int b = tid * per; b < min(p.B, tid * per + per); ++b) sm.cum[b] += before;
         if (tid == kThreads - 1) sm.cum[p.B] = before + mine;
     }
@@ -885,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // rows that see nothing because their sequence has no such node
         for (int64_t tok = blockIdx.x; tok < static_cast<int64_t>(p.B) * p.S1; tok += gridDim.x) {
             const int b = static_cast<int>(tok / p.S1);
-            if (tok - static_cast<int64_t>(b) * p.S1 < sm.n[b]) continue;
+            if (tok - static_cast<int64_t>(b) * p.S1 < (sm.len[b] & 0xFF)) continue;
             uint4* dst = reinterpret_cast<uint4*>(p.out + tok * p.NQ * kD);
             for (int i = tid - kConvWarp * 32; i < p.NQ * (kD / 8); i += kConvWarps * 32) dst[i] = make_uint4(0, 0, 0, 0);
         }
@@ -1023,8 +1027,8 @@ extern "C" pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, con
     PA_REQUIRE(block_size == kBS, PA_ERR_UNSUPPORTED, "%s: block_size %d (only 128 is built)", name, block_size);
     PA_REQUIRE(layout == PA_LAYOUT_BSND || layout == PA_LAYOUT_BNBD, PA_ERR_INVALID, "%s: unknown layout %d", name,
                layout);
-    PA_REQUIRE(static_cast<int64_t>(max_blocks_per_seq) * kBS <= 0x7FFFFFFF, PA_ERR_UNSUPPORTED,
-               "%s: block table wider than 2^31 - 1 positions", name);
+    PA_REQUIRE(max_blocks_per_seq < (1 << 24) / kBS, PA_ERR_UNSUPPORTED,
+               "%s: block table of %d blocks, 2^24 positions or more", name, max_blocks_per_seq);
     PA_REQUIRE(num_blocks * kBS * NKV <= 0x7FFFFFFF, PA_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 cache rows", name);
     PA_REQUIRE(std::isfinite(softmax_scale), PA_ERR_INVALID, "%s: softmax_scale not finite", name);
     PA_REQUIRE(mask_stride >= 0, PA_ERR_INVALID, "%s: negative mask_stride", name);
