@@ -22,12 +22,12 @@
 // A CTA has two streams with a softmax warpgroup each. An item of more than 128
 // rows runs its two row tiles as the streams, every K/V block read once for
 // both; a smaller item runs even and odd blocks as the streams and joins them at
-// the end. A stream walks half blocks of 64 keys through two S buffers in tensor
-// memory (64 columns each, P over S; O takes 128 columns), so that S of the next
-// half block is computed, and O gets the last one's P V, while the softmax works.
+// the end. A stream walks half blocks of 64 keys: the softmax takes S out of
+// tensor memory at once, so that S of the next half block is computed, and O gets
+// the last one's P V, while it works.
 //   warps 0-3, 4-7   softmax of stream 0, 1 (thread = row = tensor memory lane)
 //   warp 8           K and V blocks by TMA, key scales by cp.async
-//   warps 9, 10      one thread each issues stream 0's, stream 1's MMAs
+//   warps 9, 10      issue stream 0's, stream 1's MMAs
 //   warp 11          tells the joining kernel about the item at the run's begin
 //   warps 12-15      V codes to FP16 in shared memory, zeros behind the end
 //
@@ -56,8 +56,8 @@ constexpr int kTile = kBS * kD;              // bytes of a block of codes
 // K blocks, V blocks as codes and as FP16, key scales. The scales' ring needs no
 // barrier that says a slot is free: block i + 6 is requested once the K blocks
 // up to i + 3 are free, i.e. S of their second halves complete, which is issued
-// after the stream's previous block's P V (block i + 1's at least) and so after
-// the softmax of the blocks up to i. K's and the scales' arrival share a barrier
+// after the softmax took the first halves' S, and so after it was done with the
+// stream's previous blocks (i + 1 and i, or i + 2). K's and the scales' arrival share a barrier
 // of that ring: six is even, so that a stream that takes every other block finds
 // its own earlier block in the barrier's last phase, never one that it has not
 // waited for (copies may land out of order, and a parity wait is good for the
@@ -69,7 +69,8 @@ constexpr int kProdWarp = 8, kMmaWarp = 9, kCutWarp = 11, kConvWarp = 12, kConvW
 // 184 + 256 x 72 = 512 x 128).
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 constexpr int kThreads = (kConvWarp + kConvWarps) * 32;
-constexpr uint32_t kTmemCols = 512, kOCol = 256;
+// Tensor memory columns: per stream S (64) and two P (32 each) in 128 w .., O at 256 + 128 w.
+constexpr uint32_t kTmemCols = 512, kOCol = 256, kPCol = 64;
 constexpr float kRaise = 8.0f;               // log2 units: see the top of the file
 constexpr float kShift = 7.0f;
 
@@ -121,7 +122,7 @@ struct TreeSmem {
     uint32_t len[kMaxB];                     // length << 8 | drafted tokens
     uint64_t k_full[kSStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t h_full[kHStages], h_empty[kHStages];
-    uint64_t s_full[2][2], p_full[2][2], o_done[2][2], q_full, q_seen, drain[2];
+    uint64_t s_full[2], s_free[2], p_full[2][2], o_done[2][2], q_full, q_seen, drain[2];
     uint32_t tmem;
     int abort;
 };
@@ -294,6 +295,16 @@ __device__ __forceinline__ uint64_t l2_keep_policy()
     return p;
 }
 
+// True in one thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t is;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(is));
+    return is != 0;
+}
+
 // Row r of item `s` in q and out.
 __device__ __forceinline__ int64_t q_row(const TreeParams& p, const Seg& s, int r)
 {
@@ -368,35 +379,41 @@ __device__ void producer(TreeSmem& sm, const TreeParams& p, const CUtensorMap* t
 // that no stale code (a NaN among them) meets their P = 0.
 __device__ void converter(TreeSmem& sm, const TreeParams& p, Run run, int w, int lane)
 {
+    // Lane l takes 16-byte unit u = l % 8 of eight rows whose numbers differ in
+    // the 8-row group only, so that every address is a constant away from the
+    // first. Units 4-7 go with the neighbouring row: a unit becomes two of one
+    // chunk, and units u and u + 4 of a row would meet in the banks.
     Seg s;
     int c = 0;
-    const int u = lane & 7, r = lane >> 3;
+    const int u = lane & 7;
+    const int key0 = 64 * (w >> 1) + 4 * (w & 1) + ((lane >> 3) ^ (u >> 2));
+    const uint32_t from = sw128(key0, u), to = sw128(key0, 2 * (u & 3)) + (u >> 2) * kTile,
+                   to1 = sw128(key0, 2 * (u & 3) + 1) + (u >> 2) * kTile;
     while (next_seg(sm.cum, sm.len, p.G, run, s)) {
         const int act = static_cast<int>(sm.len[s.b] >> 8);
         for (int t = s.t0; t < s.t1; ++t, ++c) {
             const int vslot = c % kVStages, hslot = c % kHStages;
             mbar_wait(&sm.v_full[vslot], (c / kVStages) & 1, p.err, 4, &sm.abort);
-            mbar_wait(&sm.h_empty[hslot], ((c / kHStages) & 1) ^ 1, p.err, 8, &sm.abort);
-            const uint8_t* src = sm.v[vslot];
-            uint8_t* dst = sm.vh[hslot][u >> 2];
-            const int u0 = 2 * (u & 3), swap = u >> 2;   // the two halves' order keeps the stores apart
+            const uint8_t* src = sm.v[vslot] + from;
+            uint4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint4*>(src + 1024 * i);
             const int limit = act - t * kBS;
-#pragma unroll 4
-            for (int i = 0; i < kBS / kConvWarps / 4; ++i) {
-                const int key = w * (kBS / kConvWarps) + i * 4 + r;
-                uint4 x = *reinterpret_cast<const uint4*>(src + sw128(key, u));
-                if (key >= limit) x = make_uint4(0, 0, 0, 0);
-                uint4 lo, hi;
-                lo.x = codes_to_half2(x.x & 0xFFFFu);
-                lo.y = codes_to_half2(x.x >> 16);
-                lo.z = codes_to_half2(x.y & 0xFFFFu);
-                lo.w = codes_to_half2(x.y >> 16);
-                hi.x = codes_to_half2(x.z & 0xFFFFu);
-                hi.y = codes_to_half2(x.z >> 16);
-                hi.z = codes_to_half2(x.w & 0xFFFFu);
-                hi.w = codes_to_half2(x.w >> 16);
-                *reinterpret_cast<uint4*>(dst + sw128(key, u0 + swap)) = swap ? hi : lo;
-                *reinterpret_cast<uint4*>(dst + sw128(key, u0 + 1 - swap)) = swap ? lo : hi;
+            if (limit < kBS) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (key0 + 8 * i >= limit) x[i] = make_uint4(0, 0, 0, 0);
+            }
+            mbar_wait(&sm.h_empty[hslot], ((c / kHStages) & 1) ^ 1, p.err, 8, &sm.abort);
+            uint8_t* dst = sm.vh[hslot][0];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                *reinterpret_cast<uint4*>(dst + to + 1024 * i) =
+                    make_uint4(codes_to_half2(x[i].x & 0xFFFFu), codes_to_half2(x[i].x >> 16),
+                               codes_to_half2(x[i].y & 0xFFFFu), codes_to_half2(x[i].y >> 16));
+                *reinterpret_cast<uint4*>(dst + to1 + 1024 * i) =
+                    make_uint4(codes_to_half2(x[i].z & 0xFFFFu), codes_to_half2(x[i].z >> 16),
+                               codes_to_half2(x[i].w & 0xFFFFu), codes_to_half2(x[i].w >> 16));
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -408,14 +425,17 @@ __device__ void converter(TreeSmem& sm, const TreeParams& p, Run run, int w, int
     }
 }
 
-// One thread per stream issues its MMAs: P V of a half block once the softmax
-// has written P, then S of the half block after the next, into the same buffer
-// (P lies over S), once that P V is complete.
+// One warp per stream issues its MMAs (the whole warp waits, one elected thread
+// issues): S of the next half block as soon as the softmax has taken the last S
+// out of tensor memory, P V once it has written P.
 __device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w)
 {
     constexpr uint32_t kIdescS = idesc_e4m3(128, kHalf, 0, 0);
     constexpr uint32_t kIdescO = idesc_f16(128, kD, 0, 1);   // P K-major in tensor memory, V MN-major
-    const uint32_t S = tmem + 128 * w, O = tmem + kOCol + 128 * w;
+    const uint32_t S = tmem + 128 * w, P = S + kPCol, O = tmem + kOCol + 128 * w;
+    auto wait = [&](uint64_t* bar, int phase, int code) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.err, code, &sm.abort)) != 0;
+    };
     Seg s;
     int base = 0, seg = 0, g = 0;            // blocks of all streams, segments, own half blocks so far
     bool ok = true;
@@ -426,49 +446,54 @@ __device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t 
         const uint64_t qd = smem_desc(smem_u32(sm.q[s.dual ? w : 0]), 16, 1024, kSmem128BSwizzle);
         auto issue_s = [&](int h) {
             const int i = block(h), slot = i % kKStages;
-            if ((h & 1) == 0 && !mbar_wait(&sm.k_full[i % kSStages], (i / kSStages) & 1, p.err, 16, &sm.abort)) return false;
+            if ((h & 1) == 0 && !wait(&sm.k_full[i % kSStages], i / kSStages, 16)) return false;
             tc_fence_after();
             const uint64_t kd = smem_desc(smem_u32(sm.k[slot]) + (h & 1) * (kHalf * kD), 16, 1024, kSmem128BSwizzle);
-            const int buf = (g + h) & 1;
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma_e4m3(S + kHalf * buf, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
-            umma_commit(&sm.s_full[w][buf]);
-            if (h & 1) {
-                umma_commit(&sm.k_empty[slot]);
-                if (!s.dual) umma_commit(&sm.k_empty[slot]);   // (two arrivals a block)
+                for (int kk = 0; kk < 4; ++kk) umma_e4m3(S, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
+                umma_commit(&sm.s_full[w]);
+                if (h & 1) {
+                    umma_commit(&sm.k_empty[slot]);
+                    if (!s.dual) umma_commit(&sm.k_empty[slot]);   // (two arrivals a block)
+                }
             }
+            __syncwarp();
             return true;
         };
-        ok = mbar_wait(&sm.q_full, seg & 1, p.err, 16, &sm.abort);
-        mbar_arrive(&sm.q_seen);
-        for (int h = 0; h < 2 && h < nh && ok; ++h) ok = issue_s(h);
+        ok = wait(&sm.q_full, seg, 16);
+        if (elect_one()) mbar_arrive(&sm.q_seen);
+        __syncwarp();
+        if (ok && nh > 0) ok = issue_s(0);
         for (int h = 0; h < nh && ok; ++h) {
             const int i = block(h), slot = i % kHStages, buf = (g + h) & 1;
-            ok = ((h & 1) != 0 || mbar_wait(&sm.h_full[slot], (i / kHStages) & 1, p.err, 32, &sm.abort)) &&
-                 mbar_wait(&sm.p_full[w][buf], ((g + h) >> 1) & 1, p.err, 32, &sm.abort);
+            if (h + 1 < nh) ok = wait(&sm.s_free[w], g + h, 32) && issue_s(h + 1);
+            ok = ok && ((h & 1) != 0 || wait(&sm.h_full[slot], i / kHStages, 32)) && wait(&sm.p_full[w][buf], (g + h) >> 1, 32);
             if (!ok) break;
             tc_fence_after();
             const uint64_t vd =
                 smem_desc(smem_u32(sm.vh[slot][0]) + (h & 1) * (kHalf * 128), kTile, 1024, kSmem128BSwizzle);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kHalf / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of V
-                umma_f16_ta(O, S + kHalf * buf + 8 * kk, vd + 128 * kk, kIdescO, (h > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&sm.o_done[w][buf]);
-            if (h & 1) {
-                umma_commit(&sm.h_empty[slot]);
-                if (!s.dual) umma_commit(&sm.h_empty[slot]);
+                for (int kk = 0; kk < kHalf / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of V
+                    umma_f16_ta(O, P + 32 * buf + 8 * kk, vd + 128 * kk, kIdescO, (h > 0 || kk > 0) ? 1u : 0u);
+                umma_commit(&sm.o_done[w][buf]);
+                if (h & 1) {
+                    umma_commit(&sm.h_empty[slot]);
+                    if (!s.dual) umma_commit(&sm.h_empty[slot]);
+                }
             }
-            if (h + 2 < nh) {
-                ok = mbar_wait(&sm.o_done[w][buf], ((g + h) >> 1) & 1, p.err, 32, &sm.abort);
-                if (ok) ok = issue_s(h + 2);
-            }
+            __syncwarp();
         }
         g += nh;
         base += cnt;
         ++seg;
     }
-    umma_commit(&sm.drain[w]);
-    mbar_wait_drain(&sm.drain[w], 0, p.err, 512);
+    if (elect_one()) {
+        umma_commit(&sm.drain[w]);
+        mbar_wait_drain(&sm.drain[w], 0, p.err, 512);
+    }
+    __syncwarp();
 }
 
 // One thread's share of a segment's Q rows (16 bytes of eight rows), loaded
@@ -500,7 +525,7 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
 {
     const int q4 = warp & 3, row = 32 * q4 + lane, tid = row;
     const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
-    const uint32_t O = tmem + lanes + kOCol + 128 * w;
+    const uint32_t S = tmem + lanes + 128 * w, O = tmem + lanes + kOCol + 128 * w;
     Seg s, ns;
     int base = 0, g = 0, seg = 0;            // blocks of all streams, own half blocks, segments
     bool more = next_seg(sm.cum, sm.len, p.G, run, ns);
@@ -550,89 +575,101 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
             }
         }
         float m = -INFINITY, l = 0.0f;
-        for (int h = 0; h < 2 * nt; ++h, ++g) {
+        // a warp without rows keeps the others company at the barriers
+        for (int h = 0; h < 2 * nt && !warp_live; ++h, ++g) {
+            mbar_wait(&sm.s_full[w], g & 1, p.err, 64, &sm.abort);
+            if (lane == 0) mbar_arrive(&sm.s_free[w]);
+            if (h > 1) mbar_wait(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
+            if (lane == 0) mbar_arrive(&sm.p_full[w][g & 1]);
+        }
+#pragma unroll 1
+        for (int h = 0; h < 2 * nt && warp_live; ++h, ++g) {
             const int j = s.dual ? h >> 1 : (h & ~1) + w;      // block of the segment
             const int slot = (base + j) % kSStages;
-            const uint32_t S = tmem + lanes + 128 * w + kHalf * (g & 1);
-            mbar_wait(&sm.s_full[w][g & 1], (g >> 1) & 1, p.err, 64, &sm.abort);
-            if (warp_live) {
-                tc_fence_after();
-                mbar_wait(&sm.k_full[slot], ((base + j) / kSStages) & 1, p.err, 64, &sm.abort);
-                float v[kHalf];
+            mbar_wait(&sm.s_full[w], g & 1, p.err, 64, &sm.abort);
+            float v[kHalf];
+            tc_fence_after();
+            mbar_wait(&sm.k_full[slot], ((base + j) / kSStages) & 1, p.err, 64, &sm.abort);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) tmem_ld32(S + 32 * c, v + 32 * c);
-                tmem_wait_ld();
-                const float4* ks = reinterpret_cast<const float4*>(sm.ks[slot] + (h & 1) * kHalf);
+            for (int c = 0; c < 2; ++c) tmem_ld32(S + 32 * c, v + 32 * c);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.s_free[w]);
+            float mx = -INFINITY;
+            const float4* ks = reinterpret_cast<const float4*>(sm.ks[slot] + (h & 1) * kHalf);
 #pragma unroll
-                for (int c = 0; c < kHalf / 4; ++c) {
-                    const float4 k4 = ks[c];
-                    const float2 a = mul2(make_float2(v[4 * c], v[4 * c + 1]), make_float2(k4.x, k4.y));
-                    const float2 b = mul2(make_float2(v[4 * c + 2], v[4 * c + 3]), make_float2(k4.z, k4.w));
-                    v[4 * c] = a.x;
-                    v[4 * c + 1] = a.y;
-                    v[4 * c + 2] = b.x;
-                    v[4 * c + 3] = b.y;
-                }
-                const int off = ctx - (s.t0 + j) * kBS - (h & 1) * kHalf;   // the first drafted token's key here
-                if (off < kHalf) {
-                    // which keys the row sees: the context's, then its mask's bits
-                    uint64_t see;
-                    if (off > 0) see = (~0ull >> (64 - off)) | (m_lo << off);
-                    else if (off == 0) see = m_lo;
-                    else if (off > -64) see = (m_lo >> -off) | (m_hi << (64 + off));
-                    else see = off > -128 ? m_hi >> (-off - 64) : 0ull;
-#pragma unroll
-                    for (int k = 0; k < kHalf; ++k)
-                        if (!((see >> k) & 1)) v[k] = -INFINITY;
-                }
-                float m4[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    m4[c] = fmaxf(v[16 * c], v[16 * c + 1]);
-#pragma unroll
-                    for (int k = 2; k < 16; k += 2) m4[c] = max3(m4[c], v[16 * c + k], v[16 * c + k + 1]);
-                }
-                const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * rs;
-                const bool raise = mx > m + kRaise || (m == -INFINITY && mx > -INFINITY);
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float f = raise ? ex2(m - mx) : 1.0f;
-                    if (raise) m = mx;
-                    l *= f;
-                    if (h > 0) {
-                        // O is complete up to the last half block before it is scaled
-                        mbar_wait(&sm.o_done[w][(g - 1) & 1], ((g - 1) >> 1) & 1, p.err, 128, &sm.abort);
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            float o[32];
-                            tmem_ld32(O + 32 * c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] *= f;
-                            tmem_st32(O + 32 * c, o);
-                        }
-                    }
-                }
-                const float ref = m == -INFINITY ? 0.0f : m - kShift;
-                const float2 rs2 = make_float2(rs, rs), nref = make_float2(-ref, -ref);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t hp[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float2 x = fma2(make_float2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), rs2, nref);
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        sum[k & 1] = add2(sum[k & 1], x);
-                        hp[k] = half2_bits(x.x, x.y);
-                    }
-                    tmem_st16(S + 16 * c, hp);
-                }
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                tmem_wait_st();
-                tc_fence_before();
+            for (int c = 0; c < kHalf / 4; ++c) {
+                const float4 k4 = ks[c];
+                const float2 a = mul2(make_float2(v[4 * c], v[4 * c + 1]), make_float2(k4.x, k4.y));
+                const float2 b = mul2(make_float2(v[4 * c + 2], v[4 * c + 3]), make_float2(k4.z, k4.w));
+                v[4 * c] = a.x;
+                v[4 * c + 1] = a.y;
+                v[4 * c + 2] = b.x;
+                v[4 * c + 3] = b.y;
             }
+            const int off = ctx - (s.t0 + j) * kBS - (h & 1) * kHalf;   // the first drafted token's key here
+            if (off < kHalf) {
+                // which keys the row sees: the context's, then its mask's bits
+                uint64_t see;
+                if (off > 0) see = (~0ull >> (64 - off)) | (m_lo << off);
+                else if (off == 0) see = m_lo;
+                else if (off > -64) see = (m_lo >> -off) | (m_hi << (64 + off));
+                else see = off > -128 ? m_hi >> (-off - 64) : 0ull;
+#pragma unroll
+                for (int k = 0; k < kHalf; ++k)
+                    if (!((see >> k) & 1)) v[k] = -INFINITY;
+            }
+            float m4[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                m4[c] = fmaxf(v[16 * c], v[16 * c + 1]);
+#pragma unroll
+                for (int k = 2; k < 16; k += 2) m4[c] = max3(m4[c], v[16 * c + k], v[16 * c + k + 1]);
+            }
+            mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * rs;
+            // this P buffer's last P V is complete
+            if (h > 1) mbar_wait(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
+            tc_fence_after();
+            const bool raise = mx > m + kRaise || (m == -INFINITY && mx > -INFINITY);
+            if (__any_sync(0xffffffffu, raise)) {
+                const float f = raise ? ex2(m - mx) : 1.0f;
+                if (raise) m = mx;
+                l *= f;
+                if (h > 0) {
+                    // O is complete before it is scaled
+                    mbar_wait(&sm.o_done[w][(g - 1) & 1], ((g - 1) >> 1) & 1, p.err, 128, &sm.abort);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float o[32];
+                        tmem_ld32(O + 32 * c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] *= f;
+                        tmem_st32(O + 32 * c, o);
+                    }
+                }
+            }
+            const float ref = m == -INFINITY ? 0.0f : m - kShift;
+            const float2 rs2 = make_float2(rs, rs), nref = make_float2(-ref, -ref);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t hp[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float2 x = fma2(make_float2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), rs2, nref);
+                    x.x = ex2(x.x);
+                    x.y = ex2(x.y);
+                    sum[k & 1] = add2(sum[k & 1], x);
+                    hp[k] = half2_bits(x.x, x.y);
+                }
+                tmem_st16(S + kPCol + 32 * (g & 1) + 16 * c, hp);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tmem_wait_st();
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_full[w][g & 1]);
         }
@@ -642,8 +679,8 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
         // waits for nothing else, and must not fall two phases behind)
         mbar_wait(&sm.q_seen, seg++ & 1, p.err, 128, &sm.abort);
         if (nt > 0) {
-            // (the last two half blocks: one barrier each, as a wait by parity is for
-            // a barrier's latest phase alone)
+            // (the last two half blocks' barriers: a wait by parity is for a barrier's
+            // latest phase alone)
             mbar_wait(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
             mbar_wait(&sm.o_done[w][(g - 1) & 1], ((g - 1) >> 1) & 1, p.err, 128, &sm.abort);
         }
@@ -812,12 +849,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.h_empty[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.s_full[i][0], 1);
-            mbar_init(&sm.s_full[i][1], 1);
-            mbar_init(&sm.p_full[i][0], 4);
-            mbar_init(&sm.p_full[i][1], 4);
-            mbar_init(&sm.o_done[i][0], 1);
-            mbar_init(&sm.o_done[i][1], 1);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_free[i], 4);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&sm.p_full[i][j], 4);
+                mbar_init(&sm.o_done[i][j], 1);
+            }
             mbar_init(&sm.drain[i], 1);
         }
         mbar_init(&sm.q_full, 8);
@@ -882,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kProdWarp) producer(sm, p, &tk, &tv, run, lane);
         else if (warp == kCutWarp) describe_cut(sm, p, run, total, lane);
-        else if (lane == 0) mma_issuer(sm, p, run, tmem, warp - kMmaWarp);
+        else mma_issuer(sm, p, run, tmem, warp - kMmaWarp);
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
