@@ -104,6 +104,7 @@ struct TreeParams {
     float* part;
     int part_rows;                           // rows of a partial item
     int B, S1, NQ, NKV, G;
+    uint32_t g_mul;                          // 2^22 / G + 1: n / G = n g_mul >> 22 for n < 2^14
     int64_t num_blocks;
     int max_blocks, layout, ctas;
     int keep_l2;                             // K/V blocks serve several items
@@ -118,7 +119,7 @@ struct TreeSmem {
     alignas(16) float ks[kSStages][kBS];
     alignas(8) float ml[2][2][128];                     // m and l of the two streams
     alignas(16) float vs[kD];
-    int64_t cum[kMaxB + 1];
+    uint32_t cum[kMaxB + 1];
     uint32_t len[kMaxB];                     // length << 8 | drafted tokens
     uint64_t k_full[kSStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t h_full[kHStages], h_empty[kHStages];
@@ -136,80 +137,91 @@ struct Seg {
 };
 
 struct Run {
-    int64_t pos, hi;
+    uint32_t pos, hi;
     int b;
     bool fresh;
 };
 
-__device__ __forceinline__ int64_t div64(int64_t a, int64_t b)
-{
-    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-    return a / b;
-}
-
-__device__ __forceinline__ int tiles_of(int act) { return (act + kBS - 1) / kBS; }
+__device__ __forceinline__ int tiles_of(uint32_t act) { return static_cast<int>((act + kBS - 1) / kBS); }
 
 // weight of one kv head of a sequence with `rows` query rows a kv head
-__device__ __forceinline__ int64_t head_weight(int rows, int tiles)
+__device__ __forceinline__ uint32_t head_weight(uint32_t rows, uint32_t tiles)
 {
     if (rows == 0 || tiles == 0) return 0;
-    return static_cast<int64_t>((rows + 127) / 128) * tiles + (rows + kItemRows - 1) / kItemRows * kItemCost;
+    return (rows + 127) / 128 * tiles + (rows + kItemRows - 1) / kItemRows * kItemCost;
 }
 
-__device__ __forceinline__ int64_t run_begin(int64_t total, int c, int ctas) { return div64(total * c, ctas); }
-// the CTA whose run holds position pos
-__device__ __forceinline__ int cta_of(int64_t total, int64_t pos, int ctas)
+// Run c of `ctas` over `total`: the first total % ctas runs are one longer.
+__device__ __forceinline__ uint32_t run_begin(uint32_t total, uint32_t c, uint32_t ctas)
 {
-    return static_cast<int>(div64((pos + 1) * ctas - 1, total));
+    return c * (total / ctas) + min(c, total % ctas);
+}
+// the CTA whose run holds position pos
+__device__ __forceinline__ int cta_of(uint32_t total, uint32_t pos, uint32_t ctas)
+{
+    const uint32_t q = total / ctas, r = total % ctas, longer = r * (q + 1);
+    return static_cast<int>(pos < longer ? pos / (q + 1) : r + (pos - longer) / q);
 }
 
 // the item at `pos` of sequence s.b, whose first position is base0; its first
 // position and the one behind it
-__device__ __forceinline__ void locate(int64_t pos, int64_t base0, int rows_b, int tiles, Seg& s, int64_t& base,
-                                       int64_t& end)
+__device__ __forceinline__ void locate(uint32_t pos, uint32_t base0, int rows_b, int tiles, Seg& s, uint32_t& base,
+                                       uint32_t& end)
 {
-    const int64_t per_head = head_weight(rows_b, tiles);
-    const int64_t rem = pos - base0;
-    s.h = static_cast<int>(div64(rem, per_head));
-    const int64_t in_head = rem - s.h * per_head, full = 2 * static_cast<int64_t>(tiles) + kItemCost;
-    const int item = min(static_cast<int>(div64(in_head, full)), (rows_b - 1) / kItemRows);
+    const uint32_t per_head = head_weight(rows_b, tiles);
+    const uint32_t rem = pos - base0;
+    s.h = static_cast<int>(rem / per_head);
+    const uint32_t in_head = rem - s.h * per_head, full = 2 * tiles + kItemCost;
+    const int item = min(static_cast<int>(in_head / full), (rows_b - 1) / kItemRows);
     s.row0 = item * kItemRows;
     s.rows = min(rows_b - s.row0, kItemRows);
     s.dual = s.rows > 128;
     s.tiles = tiles;
     base = base0 + s.h * per_head + item * full;
-    end = base + (s.dual ? 2 : 1) * static_cast<int64_t>(tiles) + kItemCost;
+    end = base + (s.dual ? 2 : 1) * tiles + kItemCost;
 }
 
 // blocks of item `s` before position `off` behind its first one
-__device__ __forceinline__ int blocks_before(const Seg& s, int64_t off)
+__device__ __forceinline__ int blocks_before(const Seg& s, uint32_t off)
 {
-    const int64_t o = off - kItemCost;
-    const int64_t t = o <= 0 ? 0 : (s.dual ? (o + 1) >> 1 : o);
-    return t < s.tiles ? static_cast<int>(t) : s.tiles;
+    const uint32_t o = off > kItemCost ? off - kItemCost : 0u;
+    return min(static_cast<int>(s.dual ? (o + 1) >> 1 : o), s.tiles);
 }
 
-// The run's next item, its blocks [t0, t1) perhaps none.
-__device__ __forceinline__ bool next_item(const int64_t* cum, const uint32_t* len, int G, Run& r, Seg& s)
+// The run's next item with blocks [t0, t1) in it.
+__device__ __forceinline__ bool next_seg(const uint32_t* cum, const uint32_t* len, int G, Run& r, Seg& s)
 {
-    if (r.pos >= r.hi) return false;
-    while (cum[r.b + 1] <= r.pos) ++r.b;
-    s.b = r.b;
-    int64_t base, end;
-    locate(r.pos, cum[r.b], (len[r.b] & 0xFF) * G, tiles_of(len[r.b] >> 8), s, base, end);
-    s.t0 = blocks_before(s, r.pos - base);
-    s.t1 = r.hi >= end ? s.tiles : blocks_before(s, r.hi - base);
-    s.first = r.fresh;
-    r.fresh = false;
-    r.pos = end < r.hi ? end : r.hi;
-    return true;
-}
-
-__device__ __forceinline__ bool next_seg(const int64_t* cum, const uint32_t* len, int G, Run& r, Seg& s)
-{
-    while (next_item(cum, len, G, r, s))
+    while (r.pos < r.hi) {
+        while (cum[r.b + 1] <= r.pos) ++r.b;
+        s.b = r.b;
+        uint32_t base, end;
+        locate(r.pos, cum[r.b], static_cast<int>(len[r.b] & 0xFF) * G, tiles_of(len[r.b] >> 8), s, base, end);
+        s.t0 = blocks_before(s, r.pos - base);
+        s.t1 = r.hi >= end ? s.tiles : blocks_before(s, r.hi - base);
+        s.first = r.fresh;
+        r.fresh = false;
+        r.pos = min(end, r.hi);
         if (s.t0 < s.t1) return true;
+    }
     return false;
+}
+
+// ---- waits -----------------------------------------------------------------------
+// mbar_wait with a shorter body: the kernel's parts run at once out of one
+// instruction cache.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint32_t t0 = static_cast<uint32_t>(globaltimer_ns());
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort) return false;
+        if (static_cast<uint32_t>(globaltimer_ns()) - t0 > static_cast<uint32_t>(kWaitLimitNs)) {
+            *abort = 1;
+            atomicOr(err, code);
+            return false;
+        }
+    }
+    return true;
 }
 
 // ---- small device helpers ------------------------------------------------------------
@@ -305,11 +317,18 @@ __device__ __forceinline__ bool elect_one()
     return is != 0;
 }
 
-// Row r of item `s` in q and out.
-__device__ __forceinline__ int64_t q_row(const TreeParams& p, const Seg& s, int r)
+// The drafted token of a query row of a kv head (exact: the row is below 2^14,
+// the factor's error times it below 1 / 128).
+__device__ __forceinline__ int node_of(const TreeParams& p, int row)
 {
-    const int rr = s.row0 + r, node = rr / p.G;
-    return (static_cast<int64_t>(s.b) * p.S1 + node) * p.NQ + s.h * p.G + (rr - node * p.G);
+    return static_cast<int>((static_cast<uint64_t>(row) * p.g_mul) >> 22);
+}
+
+// Row r of item `s` in q and out.
+__device__ __forceinline__ int q_row(const TreeParams& p, const Seg& s, int r)
+{
+    const int rr = s.row0 + r, node = node_of(p, rr);
+    return (s.b * p.S1 + node) * p.NQ + s.h * p.G + (rr - node * p.G);
 }
 
 __device__ __forceinline__ float* part_of(const TreeParams& p, int cta, bool first)
@@ -338,7 +357,7 @@ __device__ void producer(TreeSmem& sm, const TreeParams& p, const CUtensorMap* t
             const int x = p.layout == PA_LAYOUT_BSND ? s.h * kD : 0;
             const int y = static_cast<int>(p.layout == PA_LAYOUT_BSND ? blk * kBS : (blk * p.NKV + s.h) * kBS);
             const int kslot = kc % kKStages, vslot = vc % kVStages, sslot = kc % kSStages;
-            if (!mbar_wait(&sm.k_empty[kslot], ((kc / kKStages) & 1) ^ 1, p.err, 1, &sm.abort)) stop = true;
+            if (!wait_for(&sm.k_empty[kslot], ((kc / kKStages) & 1) ^ 1, p.err, 1, &sm.abort)) stop = true;
             if (__any_sync(0xffffffffu, stop)) {
                 stop = true;
                 break;
@@ -354,7 +373,7 @@ __device__ void producer(TreeSmem& sm, const TreeParams& p, const CUtensorMap* t
             }
             cp_async_arrive_noinc(&sm.k_full[sslot]);
             ++kc;
-            if (!mbar_wait(&sm.v_empty[vslot], ((vc / kVStages) & 1) ^ 1, p.err, 2, &sm.abort)) stop = true;
+            if (!wait_for(&sm.v_empty[vslot], ((vc / kVStages) & 1) ^ 1, p.err, 2, &sm.abort)) stop = true;
             if (__any_sync(0xffffffffu, stop)) {
                 stop = true;
                 break;
@@ -393,7 +412,7 @@ __device__ void converter(TreeSmem& sm, const TreeParams& p, Run run, int w, int
         const int act = static_cast<int>(sm.len[s.b] >> 8);
         for (int t = s.t0; t < s.t1; ++t, ++c) {
             const int vslot = c % kVStages, hslot = c % kHStages;
-            mbar_wait(&sm.v_full[vslot], (c / kVStages) & 1, p.err, 4, &sm.abort);
+            wait_for(&sm.v_full[vslot], (c / kVStages) & 1, p.err, 4, &sm.abort);
             const uint8_t* src = sm.v[vslot] + from;
             uint4 x[8];
 #pragma unroll
@@ -404,7 +423,7 @@ __device__ void converter(TreeSmem& sm, const TreeParams& p, Run run, int w, int
                 for (int i = 0; i < 8; ++i)
                     if (key0 + 8 * i >= limit) x[i] = make_uint4(0, 0, 0, 0);
             }
-            mbar_wait(&sm.h_empty[hslot], ((c / kHStages) & 1) ^ 1, p.err, 8, &sm.abort);
+            wait_for(&sm.h_empty[hslot], ((c / kHStages) & 1) ^ 1, p.err, 8, &sm.abort);
             uint8_t* dst = sm.vh[hslot][0];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -434,7 +453,7 @@ __device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t 
     constexpr uint32_t kIdescO = idesc_f16(128, kD, 0, 1);   // P K-major in tensor memory, V MN-major
     const uint32_t S = tmem + 128 * w, P = S + kPCol, O = tmem + kOCol + 128 * w;
     auto wait = [&](uint64_t* bar, int phase, int code) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.err, code, &sm.abort)) != 0;
+        return __all_sync(0xffffffffu, wait_for(bar, phase & 1, p.err, code, &sm.abort)) != 0;
     };
     Seg s;
     int base = 0, seg = 0, g = 0;            // blocks of all streams, segments, own half blocks so far
@@ -464,10 +483,11 @@ __device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t 
         ok = wait(&sm.q_full, seg, 16);
         if (elect_one()) mbar_arrive(&sm.q_seen);
         __syncwarp();
-        if (ok && nh > 0) ok = issue_s(0);
-        for (int h = 0; h < nh && ok; ++h) {
+#pragma unroll 1
+        for (int h = -1; h < nh && ok; ++h) {
+            if (h + 1 < nh) ok = (h < 0 || wait(&sm.s_free[w], g + h, 32)) && issue_s(h + 1);
+            if (h < 0 || !ok) continue;
             const int i = block(h), slot = i % kHStages, buf = (g + h) & 1;
-            if (h + 1 < nh) ok = wait(&sm.s_free[w], g + h, 32) && issue_s(h + 1);
             ok = ok && ((h & 1) != 0 || wait(&sm.h_full[slot], i / kHStages, 32)) && wait(&sm.p_full[w][buf], (g + h) >> 1, 32);
             if (!ok) break;
             tc_fence_after();
@@ -518,7 +538,7 @@ __device__ __forceinline__ void q_load(const TreeParams& p, const Seg& s, int w,
             q.sc[i] = __ldg(p.q_scale + at);
         }
     }
-    q.vs = __ldg(p.v_scale + (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD + tid);
+    q.vs = __ldg(p.v_scale + static_cast<int64_t>(s.b * p.NKV + s.h) * kD + tid);
 }
 
 __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w, int warp, int lane)
@@ -528,13 +548,125 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
     const uint32_t S = tmem + lanes + 128 * w, O = tmem + lanes + kOCol + 128 * w;
     Seg s, ns;
     int base = 0, g = 0, seg = 0;            // blocks of all streams, own half blocks, segments
-    bool more = next_seg(sm.cum, sm.len, p.G, run, ns);
-    QLoad ql;
-    if (more) q_load(p, ns, w, tid, ql);
-    while (more) {
+    int nt = 0, cnt = 0, my = 0;
+    bool have = false, warp_live = false, live = false;
+    float m = -INFINITY, l = 0.0f;
+    for (;;) {
+        // ---- the next segment, its Q on the way while the last one's output leaves ----
+        const bool more = next_seg(sm.cum, sm.len, p.G, run, ns);
+        QLoad ql;
+        if (more) q_load(p, ns, w, tid, ql);
+        if (have) {
+            // both issuing threads have seen this segment's Q (a stream without blocks
+            // waits for nothing else, and must not fall two phases behind)
+            wait_for(&sm.q_seen, seg++ & 1, p.err, 128, &sm.abort);
+            if (nt > 0) {
+                // (the last two half blocks' barriers: a wait by parity is for a barrier's
+                // latest phase alone)
+                wait_for(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
+                wait_for(&sm.o_done[w][(g - 1) & 1], ((g - 1) >> 1) & 1, p.err, 128, &sm.abort);
+            }
+            tc_fence_before();
+            // ---- the item's (or its part's) output ----
+            const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+            float* const part = part_of(p, blockIdx.x, s.first);
+            if (!s.dual) {
+                sm.ml[w][0][row] = m;
+                sm.ml[w][1][row] = l;
+            }
+            named_bar_sync(1, 256);
+            tc_fence_after();
+            float f0 = 1.0f, f1 = 0.0f;                            // factors of this stream's O, or of O 0 and 1
+            int d0 = 0, dn = kD;
+            uint32_t o_at = tmem + lanes + kOCol + 128 * w;
+            const bool two = !s.dual && cnt > 1;
+            if (!s.dual) {
+                const float m0 = sm.ml[0][0][row], m1 = cnt > 1 ? sm.ml[1][0][row] : -INFINITY;
+                const float l0 = sm.ml[0][1][row], l1 = cnt > 1 ? sm.ml[1][1][row] : 0.0f;
+                m = fmaxf(m0, m1);
+                f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - m);
+                f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - m);
+                l = l0 * f0 + l1 * f1;
+                d0 = 64 * w;
+                dn = 64;
+                o_at = tmem + lanes + kOCol + d0;
+            }
+            if (warp_live) {
+                // Rows leave in 128-byte pieces of each, staged in this warp's 32 rows
+                // of its warpgroup's Q tile (every S of the segment is computed): a
+                // store covers four rows' pieces instead of 16 bytes of 32 rows.
+                const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+                const int at = live ? q_row(p, s, my) : -1;
+                uint8_t* const stage = sm.q[w];
+                const float4* vs = reinterpret_cast<const float4*>(sm.vs + d0);
+                const int nc = dn / 32;
+#pragma unroll 1
+                for (int c = 0; c < nc; ++c) {
+                    float o[32];
+                    tmem_ld32(o_at + 32 * c, o);
+                    tmem_wait_ld();
+                    if (!s.dual) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] *= f0;
+                        if (two) {
+                            float o2[32];
+                            tmem_ld32(o_at + 128 + 32 * c, o2);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] += o2[k] * f1;
+                        }
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 a = vs[8 * c + 2 * k], b = vs[8 * c + 2 * k + 1];
+                            const float* x = o + 8 * k;
+                            const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * inv * a.x, x[1] * inv * a.y);
+                            const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * inv * a.z, x[3] * inv * a.w);
+                            const __nv_bfloat162 y2 = __floats2bfloat162_rn(x[4] * inv * b.x, x[5] * inv * b.y);
+                            const __nv_bfloat162 y3 = __floats2bfloat162_rn(x[6] * inv * b.z, x[7] * inv * b.w);
+                            *reinterpret_cast<uint4*>(stage + sw128(row, 4 * (c & 1) + k)) =
+                                make_uint4(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1),
+                                           *reinterpret_cast<const uint32_t*>(&y2), *reinterpret_cast<const uint32_t*>(&y3));
+                        }
+                        if ((c & 1) == 0) continue;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<float4*>(stage + sw128(row, k)) =
+                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                    __syncwarp();
+#pragma unroll 2
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + (lane >> 3), u = lane & 7;
+                        const int to = __shfl_sync(0xffffffffu, at, r);
+                        const uint4 x = *reinterpret_cast<const uint4*>(stage + sw128(32 * q4 + r, u));
+                        if (to < 0) continue;
+                        if (whole)
+                            reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(to) * kD + d0 + 64 * (c >> 1))[u] = x;
+                        else
+                            reinterpret_cast<uint4*>(part + static_cast<int64_t>(my - lane + r) * kD + d0 + 32 * c)[u] = x;
+                    }
+                    __syncwarp();
+                }
+                if (!whole && live && d0 == 0) {
+                    float* ml = part + static_cast<int64_t>(p.part_rows) * kD;
+                    ml[my] = m;
+                    ml[p.part_rows + my] = l;
+                }
+            }
+            tc_fence_before();
+            // (O, ml and Q of this segment are not touched before both warpgroups are here)
+            named_bar_sync(1, 256);
+            base += cnt;
+        }
+        if (!more) break;
+        have = true;
         s = ns;
-        const int act = static_cast<int>(sm.len[s.b] >> 8), n = static_cast<int>(sm.len[s.b] & 0xFF), ctx = act - n, cnt = s.t1 - s.t0;
-        const int nt = s.dual ? cnt : (cnt + 1 - w) / 2;
+        const int act = static_cast<int>(sm.len[s.b] >> 8), n = static_cast<int>(sm.len[s.b] & 0xFF), ctx = act - n;
+        cnt = s.t1 - s.t0;
+        nt = s.dual ? cnt : (cnt + 1 - w) / 2;
         // ---- Q rows into the operand layout ----
         {
             const int tile = s.dual ? w : 0, r_lo = s.dual ? 0 : 64 * w, r_n = s.dual ? 128 : 64;
@@ -551,45 +683,44 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.q_full);
         }
-        const int my = (s.dual ? 128 * w : 0) + row;          // row of the item
-        const bool warp_live = (s.dual ? 128 * w : 0) + 32 * q4 < s.rows;
-        const bool live = my < s.rows;
+        my = (s.dual ? 128 * w : 0) + row;                    // row of the item
+        warp_live = my - lane < s.rows;
+        live = my < s.rows;
         float rs = live ? fabsf(__ldg(p.q_scale + q_row(p, s, my)) * p.scale_log2) : 1.0f;
         if (rs < 1.17549435e-38f) rs = 1.17549435e-38f;       // (-inf times it stays -inf)
         // ---- the row's mask, one bit per drafted token ----
         uint64_t m_lo = 0, m_hi = 0;
         if (warp_live && s.t1 * kBS > ctx) {
-            const int first = (s.row0 + my - lane) / p.G;
-            const int last = min(s.row0 + my - lane + 31, s.row0 + s.rows - 1) / p.G;
-            const int mine = (s.row0 + my) / p.G;
+            const int first = node_of(p, s.row0 + my - lane);
+            const int last = node_of(p, s.row0 + min(my - lane + 31, s.rows - 1));
+            const int mine = node_of(p, s.row0 + my);
+#pragma unroll 1
             for (int node = first; node <= last; ++node) {
                 const uint8_t* mr = p.mask + s.b * p.mask_stride + static_cast<int64_t>(node) * p.S1;
-                uint32_t bits[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    bits[j] = __ballot_sync(0xffffffffu, 32 * j + lane < n && __ldg(mr + min(32 * j + lane, p.S1 - 1)));
-                if (node == mine) {
-                    m_lo = (static_cast<uint64_t>(bits[1]) << 32) | bits[0];
-                    m_hi = (static_cast<uint64_t>(bits[3]) << 32) | bits[2];
+#pragma unroll 1
+                for (int j = 0; j < n; j += 32) {
+                    const uint32_t bits = __ballot_sync(0xffffffffu, j + lane < n && __ldg(mr + min(j + lane, p.S1 - 1)));
+                    if (node == mine) (j < 64 ? m_lo : m_hi) |= static_cast<uint64_t>(bits) << (j & 32);
                 }
             }
         }
-        float m = -INFINITY, l = 0.0f;
+        m = -INFINITY;
+        l = 0.0f;
         // a warp without rows keeps the others company at the barriers
         for (int h = 0; h < 2 * nt && !warp_live; ++h, ++g) {
-            mbar_wait(&sm.s_full[w], g & 1, p.err, 64, &sm.abort);
+            wait_for(&sm.s_full[w], g & 1, p.err, 64, &sm.abort);
             if (lane == 0) mbar_arrive(&sm.s_free[w]);
-            if (h > 1) mbar_wait(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
+            if (h > 1) wait_for(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
             if (lane == 0) mbar_arrive(&sm.p_full[w][g & 1]);
         }
 #pragma unroll 1
         for (int h = 0; h < 2 * nt && warp_live; ++h, ++g) {
             const int j = s.dual ? h >> 1 : (h & ~1) + w;      // block of the segment
             const int slot = (base + j) % kSStages;
-            mbar_wait(&sm.s_full[w], g & 1, p.err, 64, &sm.abort);
+            wait_for(&sm.s_full[w], g & 1, p.err, 64, &sm.abort);
             float v[kHalf];
             tc_fence_after();
-            mbar_wait(&sm.k_full[slot], ((base + j) / kSStages) & 1, p.err, 64, &sm.abort);
+            wait_for(&sm.k_full[slot], ((base + j) / kSStages) & 1, p.err, 64, &sm.abort);
 #pragma unroll
             for (int c = 0; c < 2; ++c) tmem_ld32(S + 32 * c, v + 32 * c);
             tmem_wait_ld();
@@ -629,7 +760,7 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
             }
             mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * rs;
             // this P buffer's last P V is complete
-            if (h > 1) mbar_wait(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
+            if (h > 1) wait_for(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
             tc_fence_after();
             const bool raise = mx > m + kRaise || (m == -INFINITY && mx > -INFINITY);
             if (__any_sync(0xffffffffu, raise)) {
@@ -638,7 +769,7 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                 l *= f;
                 if (h > 0) {
                     // O is complete before it is scaled
-                    mbar_wait(&sm.o_done[w][(g - 1) & 1], ((g - 1) >> 1) & 1, p.err, 128, &sm.abort);
+                    wait_for(&sm.o_done[w][(g - 1) & 1], ((g - 1) >> 1) & 1, p.err, 128, &sm.abort);
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
@@ -673,119 +804,14 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_full[w][g & 1]);
         }
-        more = next_seg(sm.cum, sm.len, p.G, run, ns);
-        if (more) q_load(p, ns, w, tid, ql);
-        // both issuing threads have seen this segment's Q (a stream without blocks
-        // waits for nothing else, and must not fall two phases behind)
-        mbar_wait(&sm.q_seen, seg++ & 1, p.err, 128, &sm.abort);
-        if (nt > 0) {
-            // (the last two half blocks' barriers: a wait by parity is for a barrier's
-            // latest phase alone)
-            mbar_wait(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
-            mbar_wait(&sm.o_done[w][(g - 1) & 1], ((g - 1) >> 1) & 1, p.err, 128, &sm.abort);
-        }
-        tc_fence_before();
-        // ---- the item's (or its part's) output ----
-        const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-        float* const part = part_of(p, blockIdx.x, s.first);
-        if (!s.dual) {
-            sm.ml[w][0][row] = m;
-            sm.ml[w][1][row] = l;
-        }
-        named_bar_sync(1, 256);
-        tc_fence_after();
-        float f0 = 1.0f, f1 = 0.0f;                            // factors of this stream's O, or of O 0 and 1
-        int d0 = 0, dn = kD;
-        uint32_t o_at = tmem + lanes + kOCol + 128 * w;
-        const bool two = !s.dual && cnt > 1;
-        if (!s.dual) {
-            const float m0 = sm.ml[0][0][row], m1 = cnt > 1 ? sm.ml[1][0][row] : -INFINITY;
-            const float l0 = sm.ml[0][1][row], l1 = cnt > 1 ? sm.ml[1][1][row] : 0.0f;
-            m = fmaxf(m0, m1);
-            f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - m);
-            f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - m);
-            l = l0 * f0 + l1 * f1;
-            d0 = 64 * w;
-            dn = 64;
-            o_at = tmem + lanes + kOCol + d0;
-        }
-        if (warp_live) {
-            // Rows leave in 128-byte pieces of each, staged in this warp's 32 rows
-            // of its warpgroup's Q tile (every S of the segment is computed): a
-            // store covers four rows' pieces instead of 16 bytes of 32 rows.
-            const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-            const int at = live ? static_cast<int>(q_row(p, s, my)) : -1;
-            uint8_t* const stage = sm.q[w];
-            const float4* vs = reinterpret_cast<const float4*>(sm.vs + d0);
-            const int nc = dn / 32;
-#pragma unroll 1
-            for (int c = 0; c < nc; ++c) {
-                float o[32];
-                tmem_ld32(o_at + 32 * c, o);
-                tmem_wait_ld();
-                if (!s.dual) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] *= f0;
-                    if (two) {
-                        float o2[32];
-                        tmem_ld32(o_at + 128 + 32 * c, o2);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] += o2[k] * f1;
-                    }
-                }
-                if (whole) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 a = vs[8 * c + 2 * k], b = vs[8 * c + 2 * k + 1];
-                        const float* x = o + 8 * k;
-                        const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * inv * a.x, x[1] * inv * a.y);
-                        const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * inv * a.z, x[3] * inv * a.w);
-                        const __nv_bfloat162 y2 = __floats2bfloat162_rn(x[4] * inv * b.x, x[5] * inv * b.y);
-                        const __nv_bfloat162 y3 = __floats2bfloat162_rn(x[6] * inv * b.z, x[7] * inv * b.w);
-                        *reinterpret_cast<uint4*>(stage + sw128(row, 4 * (c & 1) + k)) =
-                            make_uint4(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1),
-                                       *reinterpret_cast<const uint32_t*>(&y2), *reinterpret_cast<const uint32_t*>(&y3));
-                    }
-                    if ((c & 1) == 0) continue;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<float4*>(stage + sw128(row, k)) =
-                            make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 4 * i + (lane >> 3), u = lane & 7;
-                    const int to = __shfl_sync(0xffffffffu, at, r);
-                    const uint4 x = *reinterpret_cast<const uint4*>(stage + sw128(32 * q4 + r, u));
-                    if (to < 0) continue;
-                    if (whole)
-                        reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(to) * kD + d0 + 64 * (c >> 1))[u] = x;
-                    else
-                        reinterpret_cast<uint4*>(part + static_cast<int64_t>(my - lane + r) * kD + d0 + 32 * c)[u] = x;
-                }
-                __syncwarp();
-            }
-            if (!whole && live && d0 == 0) {
-                float* ml = part + static_cast<int64_t>(p.part_rows) * kD;
-                ml[my] = m;
-                ml[p.part_rows + my] = l;
-            }
-        }
-        tc_fence_before();
-        // (O, ml and Q of this segment are not touched before both warpgroups are here)
-        named_bar_sync(1, 256);
-        base += cnt;
     }
 }
 
 // What the joining kernel has to know of the item at the begin of this CTA's run.
-__device__ void describe_cut(TreeSmem& sm, const TreeParams& p, Run run, int64_t total, int lane)
+__device__ void describe_cut(TreeSmem& sm, const TreeParams& p, Run run, uint32_t total, int lane)
 {
     const int c = blockIdx.x;
-    const int64_t lo = run.pos;
+    const uint32_t lo = run.pos;
     Cut cut = {};
     Seg s;
     // (an empty run has positions of the item behind it, but no part)
@@ -801,7 +827,7 @@ __device__ void describe_cut(TreeSmem& sm, const TreeParams& p, Run run, int64_t
         }
         while (sm.cum[run.b + 1] <= lo) ++run.b;
         s.b = run.b;
-        int64_t base, end;
+        uint32_t base, end;
         locate(lo, sm.cum[s.b], (sm.len[s.b] & 0xFF) * p.G, tiles_of(sm.len[s.b] >> 8), s, base, end);
         if (lo > base) {
             const int t0 = blocks_before(s, lo - base);
@@ -868,26 +894,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- weights before each sequence: thread i takes sequences i, i + 1, ... of its share ----
     {
         const int per = (p.B + kThreads - 1) / kThreads;
-        int64_t mine = 0;
+        uint32_t mine = 0;
         for (int b = tid * per; b < min(p.B, tid * per + per); ++b) {
-            const int64_t cap = static_cast<int64_t>(p.max_blocks) * kBS;
-            const int act = static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.act + b), 0)), cap));
+            const int act = min(max(__ldg(p.act + b), 0), p.max_blocks * kBS);
             int n = p.len ? __ldg(p.len + b) : p.S1;
             n = min(max(n, 0), min(p.S1, act));
             sm.len[b] = static_cast<uint32_t>(act) << 8 | static_cast<uint32_t>(n);
             sm.cum[b] = mine;
-            mine += static_cast<int64_t>(p.NKV) * head_weight(n * p.G, tiles_of(act));
+            mine += p.NKV * head_weight(n * p.G, tiles_of(act));
         }
-        int64_t x = mine;
+        uint32_t x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        int64_t* const warp_sum = reinterpret_cast<int64_t*>(sm.ml);
+        uint32_t* const warp_sum = reinterpret_cast<uint32_t*>(sm.ml);
         if (lane == 31) warp_sum[warp] = x;
         __syncthreads();
-        int64_t before = x - mine;
+        uint32_t before = x - mine;
         for (int i = 0; i < warp; ++i) before += warp_sum[i];
         for (int b = tid * per; b < min(p.B, tid * per + per); ++b) sm.cum[b] += before;
         if (tid == kThreads - 1) sm.cum[p.B] = before + mine;
@@ -896,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    const int64_t total = sm.cum[p.B];
+    const uint32_t total = sm.cum[p.B];
     Run run;
     run.pos = run_begin(total, blockIdx.x, p.ctas);
     run.hi = run_begin(total, blockIdx.x + 1, p.ctas);
@@ -1003,7 +1028,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
     const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
     const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * inv * v.x, o.y * inv * v.y);
     const __nv_bfloat162 y1 = __floats2bfloat162_rn(o.z * inv * v.z, o.w * inv * v.w);
-    reinterpret_cast<uint2*>(p.out + q_row(p, s, row) * kD)[lane] =
+    reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(q_row(p, s, row)) * kD)[lane] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
 }
 
@@ -1109,6 +1134,7 @@ extern "C" pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, con
     p.NQ = NQ;
     p.NKV = NKV;
     p.G = NQ / NKV;
+    p.g_mul = (1u << 22) / p.G + 1;
     p.num_blocks = num_blocks;
     p.max_blocks = max_blocks_per_seq;
     p.layout = layout;
