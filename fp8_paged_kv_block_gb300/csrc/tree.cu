@@ -966,8 +966,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the items that a run's end cut: CTA (c, y) takes the item
-// whose first block run c has and whose last one a later run, its rows 8 y .. 8 y + 7, one warp each.
-constexpr int kJoinWarps = 8;
+// whose first block run c has and whose last one a later run, a warp two rows of it
+// and four parts at once (so that their loads overlap).
+constexpr int kJoinWarps = 8, kJoinRows = 2;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeParams p)
 {
@@ -980,56 +981,60 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
     s.h = a.y;
     s.row0 = a.z;
     s.rows = a.w;
-    const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-    if (row >= s.rows) return;
+    const int row0 = (blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kJoinRows;
+    if (row0 >= s.rows) return;
     const int c0 = z.x, c1 = z.y, slot0 = z.z;
+    const int64_t slot_floats = static_cast<int64_t>(p.part_rows) * (kD + 2);
+    // O's part of run c (its rows begin there), m and l behind the rows; rows
+    // past the item's last are read from it and not written
+    auto part = [&](int c) { return p.part + (c == c0 ? slot0 : 2 * c) * slot_floats; };
+    int row[kJoinRows];
+    float M[kJoinRows], L[kJoinRows];
+    float4 o[kJoinRows];
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) {
+        row[r] = min(row0 + r, s.rows - 1);
+        M[r] = -INFINITY;
+        L[r] = 0.0f;
+        o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 1
+    for (int c = c0 + lane; c <= c1; c += 32) {
+        const float* ml = part(c) + static_cast<int64_t>(p.part_rows) * kD;
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) M[r] = fmaxf(M[r], ml[row[r]]);
+    }
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) M[r] = warp_max_f32(M[r]);
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+        const float* q = part(c);
+        const float* ml = q + static_cast<int64_t>(p.part_rows) * kD;
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) {
+            const float m = ml[row[r]];
+            const float4 x = reinterpret_cast<const float4*>(q + row[r] * kD)[lane];
+            const float l = ml[p.part_rows + row[r]];
+            const bool none = m == -INFINITY;    // the part does not count: its O may be anything
+            const float f = none ? 0.0f : ex2(m - M[r]);
+            L[r] += l * f;
+            o[r].x += none ? 0.0f : x.x * f;
+            o[r].y += none ? 0.0f : x.y * f;
+            o[r].z += none ? 0.0f : x.z * f;
+            o[r].w += none ? 0.0f : x.w * f;
+        }
+    }
     const float4 v =
-        __ldg(reinterpret_cast<const float4*>(p.v_scale + (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD) + lane);
-    // lane i has m and l of runs c0 + i, c0 + i + 32, ...
-    constexpr int kPer = kMaxCtas / 32;
-    float mi[kPer], li[kPer], M = -INFINITY;
+        __ldg(reinterpret_cast<const float4*>(p.v_scale + static_cast<int64_t>(s.b * p.NKV + s.h) * kD) + lane);
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const int i = c0 + 32 * k + lane;
-        const int slot = i == c0 ? slot0 : 2 * i;
-        mi[k] = -INFINITY;
-        li[k] = 0.0f;
-        if (i <= c1) {
-            const float* ml = p.part + static_cast<int64_t>(slot) * p.part_rows * (kD + 2) +
-                              static_cast<int64_t>(p.part_rows) * kD;
-            mi[k] = ml[row];
-            li[k] = ml[p.part_rows + row];
-        }
-        M = fmaxf(M, mi[k]);
+    for (int r = 0; r < kJoinRows; ++r) {
+        if (row0 + r >= s.rows) break;
+        const float inv = L[r] == 0.0f ? 0.0f : __fdiv_rn(1.0f, L[r]);
+        const __nv_bfloat162 y0 = __floats2bfloat162_rn(o[r].x * inv * v.x, o[r].y * inv * v.y);
+        const __nv_bfloat162 y1 = __floats2bfloat162_rn(o[r].z * inv * v.z, o[r].w * inv * v.w);
+        reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(q_row(p, s, row[r])) * kD)[lane] =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
     }
-    M = warp_max_f32(M);
-    float L = 0.0f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const float f = mi[k] == -INFINITY ? 0.0f : ex2(mi[k] - M);
-        L += li[k] * f;
-        const int last = min(c1 - c0 - 32 * k, 31);
-#pragma unroll 8
-        for (int i = 0; i <= last; ++i) {
-            const float fi = __shfl_sync(0xffffffffu, f, i);
-            if (fi == 0.0f) continue;        // (its O may be anything)
-            const int c = c0 + 32 * k + i, slot = c == c0 ? slot0 : 2 * c;
-            const float4 x = reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(slot) * p.part_rows * (kD + 2) +
-                                                             static_cast<int64_t>(row) * kD)[lane];
-            o.x += x.x * fi;
-            o.y += x.y * fi;
-            o.z += x.z * fi;
-            o.w += x.w * fi;
-        }
-    }
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) L += __shfl_xor_sync(0xffffffffu, L, i);
-    const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
-    const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * inv * v.x, o.y * inv * v.y);
-    const __nv_bfloat162 y1 = __floats2bfloat162_rn(o.z * inv * v.z, o.w * inv * v.w);
-    reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(q_row(p, s, row)) * kD)[lane] =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1152,7 +1157,7 @@ extern "C" pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, con
     if (st != PA_OK || p.ctas == 1) return st;
     const int64_t most = static_cast<int64_t>(S1) * p.G < kItemRows ? static_cast<int64_t>(S1) * p.G : kItemRows;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(static_cast<unsigned>(p.ctas - 1), static_cast<unsigned>((most + kJoinWarps - 1) / kJoinWarps));
+    lc.gridDim = dim3(static_cast<unsigned>(p.ctas - 1), static_cast<unsigned>((most + kJoinWarps * kJoinRows - 1) / (kJoinWarps * kJoinRows)));
     lc.blockDim = dim3(kJoinWarps * 32);
     lc.stream = cs;
     cudaLaunchAttribute at[1];
