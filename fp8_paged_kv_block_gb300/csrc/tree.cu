@@ -3,9 +3,9 @@
 // The query rows that share a kv head are the S1 drafted tokens x the group of
 // query heads: R = n G rows of sequence b, each attending to the context and
 // to the drafted tokens its mask row names. Rows are taken in items of at most
-// 256 (two tensor tiles of 128 rows), so that a K/V block read serves 256 rows.
+// 128, one tensor tile.
 //
-//   S = Q_fp8 K_fp8^T                 tcgen05 kind::f8f6f4, 128 x 128 x 128
+//   S = Q_fp8 K_fp8^T                 tcgen05 kind::f8f6f4, 128 rows x 64 keys
 //   x = S k_scale q_scale scale log2e, -inf where the row does not see the key
 //   P = 2^(x - m + 7), L += sum P     one thread per row, FP32
 //   O += FP16(P) V                    tcgen05 kind::f16, P from tensor memory
@@ -14,26 +14,29 @@
 // P enters the second contraction as FP16 (half a step: 2^-11) and V as the
 // FP16 values of its E4M3 codes, which are exact: P in E4M3 as in
 // pa_fp8_decode would be off by up to 2^-4 where few keys count. The reference
-// m is the running maximum, but raised only when a tile's maximum lies more
-// than 2^8 above it, which spares O's rescaling in tensor memory on most tiles;
+// m is the running maximum, but raised only when a half block's maximum lies
+// more than 2^8 above it, which spares O's rescaling in tensor memory on most;
 // P then stays below 2^15, inside FP16, and a key 2^31 below the maximum still
 // counts.
 //
-// A CTA has two streams with a softmax warpgroup each. An item of more than 128
-// rows runs its two row tiles as the streams, every K/V block read once for
-// both; a smaller item runs even and odd blocks as the streams and joins them at
-// the end. A stream walks half blocks of 64 keys: the softmax takes S out of
-// tensor memory at once, so that S of the next half block is computed, and O gets
-// the last one's P V, while it works.
-//   warps 0-3, 4-7   softmax of stream 0, 1 (thread = row = tensor memory lane)
+// What bounds it is the chain from one tensor instruction to the next: a batch
+// of MMAs and its commit take about 1000 clocks from the wake-up of the issuing
+// warp to that of the waiting one, a half block's softmax as long again. So
+// many half blocks are in flight: tensor memory holds O (128 columns), four S
+// (64 each) and four P (32 each); S is issued up to four half blocks ahead, and
+// two softmax warpgroups take even and odd halves. They share m, row by row: a
+// warp decides on m for its half after the other warpgroup's warp has decided on
+// the half before, and only the exponentials wait for that.
+//   warps 0-3, 4-7   softmax of even, odd half blocks (thread = row = tensor lane)
 //   warp 8           K and V blocks by TMA, key scales by cp.async
-//   warps 9, 10      issue stream 0's, stream 1's MMAs
-//   warp 11          tells the joining kernel about the item at the run's begin
+//   warp 9, warp 10  issue S, issue P V
+//   warp 11          Q rows and scales of the next segment; tells the joining
+//                    kernel about the item at the run's begin
 //   warps 12-15      V codes to FP16 in shared memory, zeros behind the end
 //
-// The items in (sequence, kv head, item) order are dealt to the CTAs in runs of
-// equal weight: a row tile's block counts 1, an item kItemCost besides. Items
-// that a run's end cuts leave FP32 partial sums, which a second kernel joins.
+// The items in (sequence, kv head, row tile) order are dealt to the CTAs in runs
+// of equal weight: a block counts 1, an item kItemCost besides. Items that a
+// run's end cuts leave FP32 partial sums, which a second kernel joins.
 #include "common.cuh"
 
 #include <cuda_fp16.h>
@@ -51,26 +54,21 @@ constexpr int kMaxNodes = 128;
 constexpr int kMaxGroup = 128;
 constexpr int kMaxB = 1024;
 constexpr int kMaxCtas = 192;
-constexpr int kItemRows = 256;
+constexpr int kItemRows = 128;
 constexpr int kTile = kBS * kD;              // bytes of a block of codes
 // K blocks, V blocks as codes and as FP16, key scales. The scales' ring needs no
-// barrier that says a slot is free: block i + 6 is requested once the K blocks
-// up to i + 3 are free, i.e. S of their second halves complete, which is issued
-// after the softmax took the first halves' S, and so after it was done with the
-// stream's previous blocks (i + 1 and i, or i + 2). K's and the scales' arrival share a barrier
-// of that ring: six is even, so that a stream that takes every other block finds
-// its own earlier block in the barrier's last phase, never one that it has not
-// waited for (copies may land out of order, and a parity wait is good for the
-// phase after a completed one only).
-constexpr int kKStages = 3, kVStages = 2, kHStages = 3, kSStages = 6;
-constexpr int kProdWarp = 8, kMmaWarp = 9, kCutWarp = 11, kConvWarp = 12, kConvWarps = 4;
+// barrier that says a slot is free: block i + 6 is requested once K block i + 3
+// is free, i.e. S of its halves, 2 i + 6 and 2 i + 7, is complete; those were
+// issued after halves 2 i + 2 and 2 i + 3 had left their S buffers, and so after
+// both warpgroups were done with block i.
+constexpr int kKStages = 3, kVStages = 3, kHStages = 2, kSStages = 6;
+constexpr int kProdWarp = 8, kMmaWarp = 9, kQWarp = 11, kConvWarp = 12, kConvWarps = 4;
 // Registers: 512 threads start with 128 each; the softmax warpgroups, which
 // hold a row's 128 scores, go up to 184 and the other two down to 72 (256 x
 // 184 + 256 x 72 = 512 x 128).
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
 constexpr int kThreads = (kConvWarp + kConvWarps) * 32;
-// Tensor memory columns: per stream S (64) and two P (32 each) in 128 w .., O at 256 + 128 w.
-constexpr uint32_t kTmemCols = 512, kOCol = 256, kPCol = 64;
+constexpr uint32_t kTmemCols = 512, kSCol = 128, kPCol = 384;   // O, four S, four P
 constexpr float kRaise = 8.0f;               // log2 units: see the top of the file
 constexpr float kShift = 7.0f;
 
@@ -115,25 +113,28 @@ struct TreeSmem {
     alignas(1024) uint8_t k[kKStages][kTile];
     alignas(1024) uint8_t v[kVStages][kTile];
     alignas(1024) uint8_t vh[kHStages][2][kTile];   // FP16, channels 0-63 and 64-127
-    alignas(1024) uint8_t q[2][kTile];
+    alignas(1024) uint8_t q[2][kTile];              // by segment parity, as qs and vs
+    alignas(16) uint8_t stage[kProdWarp][32 * 64];
     alignas(16) float ks[kSStages][kBS];
-    alignas(8) float ml[2][2][128];                     // m and l of the two streams
-    alignas(16) float vs[kD];
-    uint32_t cum[kMaxB + 1];
+    alignas(16) float qs[2][kItemRows];
+    alignas(16) float vs[2][kD];
+    float m[kItemRows], m0[kItemRows], l[2][kItemRows];
+    uint32_t cum[kMaxB + 1];                 // weights before each sequence
     uint32_t len[kMaxB];                     // length << 8 | drafted tokens
     uint64_t k_full[kSStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t h_full[kHStages], h_empty[kHStages];
-    uint64_t s_full[2], s_free[2], p_full[2][2], o_done[2][2], q_full, q_seen, drain[2];
+    uint64_t s_full[4], s_free[4], p_full[4], o_done[4], q_full[2], q_empty[2], drain[2];
     uint32_t tmem;
     int abort;
 };
-static_assert(sizeof(TreeSmem) + 1024 <= 232448, "tree decode shared memory over budget");
+constexpr size_t kSmemBytes = offsetof(TreeSmem, abort) + sizeof(int) + 1024;   // (aligned by hand)
+static_assert(kSmemBytes <= 232448, "tree decode shared memory over budget");
 
 // ---- the schedule -----------------------------------------------------------------
 struct Seg {
     int b, h, row0, rows;                    // the item
     int t0, t1, tiles;                       // its blocks that this run has
-    bool first, dual;                        // first of the CTA's run; two row tiles
+    bool first;                              // first of the CTA's run
 };
 
 struct Run {
@@ -148,7 +149,7 @@ __device__ __forceinline__ int tiles_of(uint32_t act) { return static_cast<int>(
 __device__ __forceinline__ uint32_t head_weight(uint32_t rows, uint32_t tiles)
 {
     if (rows == 0 || tiles == 0) return 0;
-    return (rows + 127) / 128 * tiles + (rows + kItemRows - 1) / kItemRows * kItemCost;
+    return (rows + kItemRows - 1) / kItemRows * (tiles + kItemCost);
 }
 
 // Run c of `ctas` over `total`: the first total % ctas runs are one longer.
@@ -171,21 +172,19 @@ __device__ __forceinline__ void locate(uint32_t pos, uint32_t base0, int rows_b,
     const uint32_t per_head = head_weight(rows_b, tiles);
     const uint32_t rem = pos - base0;
     s.h = static_cast<int>(rem / per_head);
-    const uint32_t in_head = rem - s.h * per_head, full = 2 * tiles + kItemCost;
-    const int item = min(static_cast<int>(in_head / full), (rows_b - 1) / kItemRows);
+    const uint32_t full = tiles + kItemCost;
+    const int item = static_cast<int>((rem - s.h * per_head) / full);
     s.row0 = item * kItemRows;
     s.rows = min(rows_b - s.row0, kItemRows);
-    s.dual = s.rows > 128;
     s.tiles = tiles;
     base = base0 + s.h * per_head + item * full;
-    end = base + (s.dual ? 2 : 1) * tiles + kItemCost;
+    end = base + full;
 }
 
 // blocks of item `s` before position `off` behind its first one
 __device__ __forceinline__ int blocks_before(const Seg& s, uint32_t off)
 {
-    const uint32_t o = off > kItemCost ? off - kItemCost : 0u;
-    return min(static_cast<int>(s.dual ? (o + 1) >> 1 : o), s.tiles);
+    return min(static_cast<int>(off > kItemCost ? off - kItemCost : 0u), s.tiles);
 }
 
 // The run's next item with blocks [t0, t1) in it.
@@ -291,6 +290,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
         : "=f"(r.x), "=f"(r.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
+}
+
+__device__ __forceinline__ void named_bar_arrive(int id, int nthreads)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c)
@@ -444,69 +448,56 @@ __device__ void converter(TreeSmem& sm, const TreeParams& p, Run run, int w, int
     }
 }
 
-// One warp per stream issues its MMAs (the whole warp waits, one elected thread
-// issues): S of the next half block as soon as the softmax has taken the last S
-// out of tensor memory, P V once it has written P.
+// The MMAs' two warps: the whole warp waits, one elected thread issues. Warp 0
+// issues S, as far ahead as there are K blocks and free S buffers, warp 1 P V.
 __device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w)
 {
     constexpr uint32_t kIdescS = idesc_e4m3(128, kHalf, 0, 0);
     constexpr uint32_t kIdescO = idesc_f16(128, kD, 0, 1);   // P K-major in tensor memory, V MN-major
-    const uint32_t S = tmem + 128 * w, P = S + kPCol, O = tmem + kOCol + 128 * w;
     auto wait = [&](uint64_t* bar, int phase, int code) {
         return __all_sync(0xffffffffu, wait_for(bar, phase & 1, p.err, code, &sm.abort)) != 0;
     };
     Seg s;
-    int base = 0, seg = 0, g = 0;            // blocks of all streams, segments, own half blocks so far
+    int i = 0, seg = 0;                      // blocks, segments so far
     bool ok = true;
     while (ok && next_seg(sm.cum, sm.len, p.G, run, s)) {
-        const int cnt = s.t1 - s.t0;
-        const int nh = 2 * (s.dual ? cnt : (cnt + 1 - w) / 2);
-        auto block = [&](int h) { return base + (s.dual ? h >> 1 : (h & ~1) + w); };
-        const uint64_t qd = smem_desc(smem_u32(sm.q[s.dual ? w : 0]), 16, 1024, kSmem128BSwizzle);
-        auto issue_s = [&](int h) {
-            const int i = block(h), slot = i % kKStages;
-            if ((h & 1) == 0 && !wait(&sm.k_full[i % kSStages], i / kSStages, 16)) return false;
-            tc_fence_after();
-            const uint64_t kd = smem_desc(smem_u32(sm.k[slot]) + (h & 1) * (kHalf * kD), 16, 1024, kSmem128BSwizzle);
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) umma_e4m3(S, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
-                umma_commit(&sm.s_full[w]);
-                if (h & 1) {
-                    umma_commit(&sm.k_empty[slot]);
-                    if (!s.dual) umma_commit(&sm.k_empty[slot]);   // (two arrivals a block)
-                }
-            }
-            __syncwarp();
-            return true;
-        };
-        ok = wait(&sm.q_full, seg, 16);
-        if (elect_one()) mbar_arrive(&sm.q_seen);
-        __syncwarp();
+        const int nh = 2 * (s.t1 - s.t0);
+        if (w == 0) ok = wait(&sm.q_full[seg & 1], seg >> 1, 16);
+        const uint64_t qd = smem_desc(smem_u32(sm.q[seg & 1]), 16, 1024, kSmem128BSwizzle);
 #pragma unroll 1
-        for (int h = -1; h < nh && ok; ++h) {
-            if (h + 1 < nh) ok = (h < 0 || wait(&sm.s_free[w], g + h, 32)) && issue_s(h + 1);
-            if (h < 0 || !ok) continue;
-            const int i = block(h), slot = i % kHStages, buf = (g + h) & 1;
-            ok = ok && ((h & 1) != 0 || wait(&sm.h_full[slot], i / kHStages, 32)) && wait(&sm.p_full[w][buf], (g + h) >> 1, 32);
+        for (int h = 0; h < nh && ok; ++h) {
+            const int odd = h & 1, g = 2 * i + odd, buf = g & 3, kslot = i % kKStages, hslot = i % kHStages;
+            if (w == 0)
+                ok = (odd || wait(&sm.k_full[i % kSStages], i / kSStages, 16)) &&
+                     (g < 4 || wait(&sm.s_free[buf], (g - 4) >> 2, 32));
+            else
+                ok = (odd || wait(&sm.h_full[hslot], i / kHStages, 32)) && wait(&sm.p_full[buf], g >> 2, 32);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t vd =
-                smem_desc(smem_u32(sm.vh[slot][0]) + (h & 1) * (kHalf * 128), kTile, 1024, kSmem128BSwizzle);
             if (elect_one()) {
+                if (w == 0) {
+                    const uint64_t kd =
+                        smem_desc(smem_u32(sm.k[kslot]) + odd * (kHalf * kD), 16, 1024, kSmem128BSwizzle);
 #pragma unroll
-                for (int kk = 0; kk < kHalf / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of V
-                    umma_f16_ta(O, P + 32 * buf + 8 * kk, vd + 128 * kk, kIdescO, (h > 0 || kk > 0) ? 1u : 0u);
-                umma_commit(&sm.o_done[w][buf]);
-                if (h & 1) {
-                    umma_commit(&sm.h_empty[slot]);
-                    if (!s.dual) umma_commit(&sm.h_empty[slot]);
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_e4m3(tmem + kSCol + kHalf * buf, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
+                    umma_commit(&sm.s_full[buf]);
+                    if (odd) umma_commit(&sm.k_empty[kslot]);
+                    if (h + 1 == nh) umma_commit(&sm.q_empty[seg & 1]);
+                } else {
+                    const uint64_t vd =
+                        smem_desc(smem_u32(sm.vh[hslot][0]) + odd * (kHalf * 128), kTile, 1024, kSmem128BSwizzle);
+#pragma unroll
+                    for (int kk = 0; kk < kHalf / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of V
+                        umma_f16_ta(tmem, tmem + kPCol + 32 * buf + 8 * kk, vd + 128 * kk, kIdescO,
+                                    (h > 0 || kk > 0) ? 1u : 0u);
+                    umma_commit(&sm.o_done[buf]);
+                    if (odd) umma_commit(&sm.h_empty[hslot]);
                 }
             }
             __syncwarp();
+            i += odd;
         }
-        g += nh;
-        base += cnt;
         ++seg;
     }
     if (elect_one()) {
@@ -516,219 +507,98 @@ __device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t 
     __syncwarp();
 }
 
-// One thread's share of a segment's Q rows (16 bytes of eight rows), loaded
-// ahead of the segment, and one channel's value scale.
-struct QLoad {
-    uint4 x[8];
-    float sc[8], vs;
-};
-
-__device__ __forceinline__ void q_load(const TreeParams& p, const Seg& s, int w, int tid, QLoad& q)
+// Q rows (128-byte swizzled), q_scale and v_scale of each segment, ahead of the
+// softmax by one.
+__device__ void q_loader(TreeSmem& sm, const TreeParams& p, Run run, int lane)
 {
-    // this warpgroup's row tile, or its half of the only one
-    const int r_lo = s.dual ? 128 * w : 64 * w, r_n = s.dual ? 128 : 64;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int rr = r_lo + 16 * i + (tid >> 3);
-        q.x[i] = make_uint4(0, 0, 0, 0);
-        q.sc[i] = 0.0f;
-        if (16 * i < r_n && rr < s.rows) {
-            const int64_t at = q_row(p, s, rr);
-            q.x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + at * kD) + (tid & 7));
-            q.sc[i] = __ldg(p.q_scale + at);
+    Seg s;
+    for (int seg = 0; next_seg(sm.cum, sm.len, p.G, run, s); ++seg) {
+        const int buf = seg & 1;
+        if (!__all_sync(0xffffffffu, wait_for(&sm.q_empty[buf], ((seg >> 1) & 1) ^ 1, p.err, 1024, &sm.abort))) break;
+#pragma unroll 4
+        for (int i = 0; i < 32; ++i) {
+            const int r = 4 * i + (lane >> 3), u = lane & 7;
+            const bool in = r < s.rows;
+            const int64_t at = q_row(p, s, in ? r : 0);
+            cp_async16(sm.q[buf] + sw128(r, u), p.q + at * kD + 16 * u, in ? 16 : 0);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 32 * i + lane;
+            cp_async4(&sm.qs[buf][r], p.q_scale + q_row(p, s, r < s.rows ? r : 0), 4);
+        }
+        cp_async16(&sm.vs[buf][4 * lane], p.v_scale + static_cast<int64_t>(s.b * p.NKV + s.h) * kD + 4 * lane, 16);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_full[buf]);
     }
-    q.vs = __ldg(p.v_scale + static_cast<int64_t>(s.b * p.NKV + s.h) * kD + tid);
 }
 
-__device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w, int warp, int lane)
+// Position of 16-byte unit u of row r in a warp's 32 x 64-byte staging area.
+__device__ __forceinline__ uint32_t stage_at(int r, int u)
 {
-    const int q4 = warp & 3, row = 32 * q4 + lane, tid = row;
-    const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
-    const uint32_t S = tmem + lanes + 128 * w, O = tmem + lanes + kOCol + 128 * w;
-    Seg s, ns;
-    int base = 0, g = 0, seg = 0;            // blocks of all streams, own half blocks, segments
-    int nt = 0, cnt = 0, my = 0;
-    bool have = false, warp_live = false, live = false;
-    float m = -INFINITY, l = 0.0f;
-    for (;;) {
-        // ---- the next segment, its Q on the way while the last one's output leaves ----
-        const bool more = next_seg(sm.cum, sm.len, p.G, run, ns);
-        QLoad ql;
-        if (more) q_load(p, ns, w, tid, ql);
-        if (have) {
-            // both issuing threads have seen this segment's Q (a stream without blocks
-            // waits for nothing else, and must not fall two phases behind)
-            wait_for(&sm.q_seen, seg++ & 1, p.err, 128, &sm.abort);
-            if (nt > 0) {
-                // (the last two half blocks' barriers: a wait by parity is for a barrier's
-                // latest phase alone)
-                wait_for(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
-                wait_for(&sm.o_done[w][(g - 1) & 1], ((g - 1) >> 1) & 1, p.err, 128, &sm.abort);
-            }
-            tc_fence_before();
-            // ---- the item's (or its part's) output ----
-            const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-            float* const part = part_of(p, blockIdx.x, s.first);
-            if (!s.dual) {
-                sm.ml[w][0][row] = m;
-                sm.ml[w][1][row] = l;
-            }
-            named_bar_sync(1, 256);
-            tc_fence_after();
-            float f0 = 1.0f, f1 = 0.0f;                            // factors of this stream's O, or of O 0 and 1
-            int d0 = 0, dn = kD;
-            uint32_t o_at = tmem + lanes + kOCol + 128 * w;
-            const bool two = !s.dual && cnt > 1;
-            if (!s.dual) {
-                const float m0 = sm.ml[0][0][row], m1 = cnt > 1 ? sm.ml[1][0][row] : -INFINITY;
-                const float l0 = sm.ml[0][1][row], l1 = cnt > 1 ? sm.ml[1][1][row] : 0.0f;
-                m = fmaxf(m0, m1);
-                f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - m);
-                f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - m);
-                l = l0 * f0 + l1 * f1;
-                d0 = 64 * w;
-                dn = 64;
-                o_at = tmem + lanes + kOCol + d0;
-            }
-            if (warp_live) {
-                // Rows leave in 128-byte pieces of each, staged in this warp's 32 rows
-                // of its warpgroup's Q tile (every S of the segment is computed): a
-                // store covers four rows' pieces instead of 16 bytes of 32 rows.
-                const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-                const int at = live ? q_row(p, s, my) : -1;
-                uint8_t* const stage = sm.q[w];
-                const float4* vs = reinterpret_cast<const float4*>(sm.vs + d0);
-                const int nc = dn / 32;
-#pragma unroll 1
-                for (int c = 0; c < nc; ++c) {
-                    float o[32];
-                    tmem_ld32(o_at + 32 * c, o);
-                    tmem_wait_ld();
-                    if (!s.dual) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= f0;
-                        if (two) {
-                            float o2[32];
-                            tmem_ld32(o_at + 128 + 32 * c, o2);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] += o2[k] * f1;
-                        }
-                    }
-                    if (whole) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float4 a = vs[8 * c + 2 * k], b = vs[8 * c + 2 * k + 1];
-                            const float* x = o + 8 * k;
-                            const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * inv * a.x, x[1] * inv * a.y);
-                            const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * inv * a.z, x[3] * inv * a.w);
-                            const __nv_bfloat162 y2 = __floats2bfloat162_rn(x[4] * inv * b.x, x[5] * inv * b.y);
-                            const __nv_bfloat162 y3 = __floats2bfloat162_rn(x[6] * inv * b.z, x[7] * inv * b.w);
-                            *reinterpret_cast<uint4*>(stage + sw128(row, 4 * (c & 1) + k)) =
-                                make_uint4(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1),
-                                           *reinterpret_cast<const uint32_t*>(&y2), *reinterpret_cast<const uint32_t*>(&y3));
-                        }
-                        if ((c & 1) == 0) continue;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            *reinterpret_cast<float4*>(stage + sw128(row, k)) =
-                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                    }
-                    __syncwarp();
-#pragma unroll 2
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = 4 * i + (lane >> 3), u = lane & 7;
-                        const int to = __shfl_sync(0xffffffffu, at, r);
-                        const uint4 x = *reinterpret_cast<const uint4*>(stage + sw128(32 * q4 + r, u));
-                        if (to < 0) continue;
-                        if (whole)
-                            reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(to) * kD + d0 + 64 * (c >> 1))[u] = x;
-                        else
-                            reinterpret_cast<uint4*>(part + static_cast<int64_t>(my - lane + r) * kD + d0 + 32 * c)[u] = x;
-                    }
-                    __syncwarp();
-                }
-                if (!whole && live && d0 == 0) {
-                    float* ml = part + static_cast<int64_t>(p.part_rows) * kD;
-                    ml[my] = m;
-                    ml[p.part_rows + my] = l;
-                }
-            }
-            tc_fence_before();
-            // (O, ml and Q of this segment are not touched before both warpgroups are here)
-            named_bar_sync(1, 256);
-            base += cnt;
-        }
-        if (!more) break;
-        have = true;
-        s = ns;
+    return static_cast<uint32_t>(r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+}
+
+// Half blocks of parity w: the thread of row `row`.
+__device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w, int q4, int lane)
+{
+    const int row = 32 * q4 + lane;
+    // named barriers: a warp decides on m for its half, the other warpgroup's warp
+    // of the same rows waits for that
+    const int mine = 2 + 2 * q4 + w, theirs = 2 + 2 * q4 + (w ^ 1);
+    const uint32_t O = tmem + (static_cast<uint32_t>(32 * q4) << 16);
+    uint8_t* const stage = sm.stage[4 * w + q4];
+    Seg s;
+    int i = 0;                               // blocks so far
+    for (int seg = 0; next_seg(sm.cum, sm.len, p.G, run, s); ++seg) {
         const int act = static_cast<int>(sm.len[s.b] >> 8), n = static_cast<int>(sm.len[s.b] & 0xFF), ctx = act - n;
-        cnt = s.t1 - s.t0;
-        nt = s.dual ? cnt : (cnt + 1 - w) / 2;
-        // ---- Q rows into the operand layout ----
-        {
-            const int tile = s.dual ? w : 0, r_lo = s.dual ? 0 : 64 * w, r_n = s.dual ? 128 : 64;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (16 * i >= r_n) break;
-                // a negative scale: the codes' signs, so that the maximum stays a maximum
-                const uint32_t flip = ql.sc[i] * p.scale_log2 < 0.0f ? 0x80808080u : 0u;
-                *reinterpret_cast<uint4*>(sm.q[tile] + sw128(r_lo + 16 * i + (tid >> 3), tid & 7)) =
-                    make_uint4(ql.x[i].x ^ flip, ql.x[i].y ^ flip, ql.x[i].z ^ flip, ql.x[i].w ^ flip);
-            }
-            if (w == 0) sm.vs[tid] = ql.vs;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.q_full);
-        }
-        my = (s.dual ? 128 * w : 0) + row;                    // row of the item
-        warp_live = my - lane < s.rows;
-        live = my < s.rows;
-        float rs = live ? fabsf(__ldg(p.q_scale + q_row(p, s, my)) * p.scale_log2) : 1.0f;
-        if (rs < 1.17549435e-38f) rs = 1.17549435e-38f;       // (-inf times it stays -inf)
+        const bool warp_live = 32 * q4 < s.rows, live = row < s.rows;
         // ---- the row's mask, one bit per drafted token ----
         uint64_t m_lo = 0, m_hi = 0;
         if (warp_live && s.t1 * kBS > ctx) {
-            const int first = node_of(p, s.row0 + my - lane);
-            const int last = node_of(p, s.row0 + min(my - lane + 31, s.rows - 1));
-            const int mine = node_of(p, s.row0 + my);
+            const int first = node_of(p, s.row0 + 32 * q4), own = node_of(p, s.row0 + row);
+            const int last = node_of(p, s.row0 + min(32 * q4 + 31, s.rows - 1));
 #pragma unroll 1
             for (int node = first; node <= last; ++node) {
                 const uint8_t* mr = p.mask + s.b * p.mask_stride + static_cast<int64_t>(node) * p.S1;
 #pragma unroll 1
                 for (int j = 0; j < n; j += 32) {
                     const uint32_t bits = __ballot_sync(0xffffffffu, j + lane < n && __ldg(mr + min(j + lane, p.S1 - 1)));
-                    if (node == mine) (j < 64 ? m_lo : m_hi) |= static_cast<uint64_t>(bits) << (j & 32);
+                    if (node == own) (j < 64 ? m_lo : m_hi) |= static_cast<uint64_t>(bits) << (j & 32);
                 }
             }
         }
-        m = -INFINITY;
-        l = 0.0f;
-        // a warp without rows keeps the others company at the barriers
-        for (int h = 0; h < 2 * nt && !warp_live; ++h, ++g) {
-            wait_for(&sm.s_full[w], g & 1, p.err, 64, &sm.abort);
-            if (lane == 0) mbar_arrive(&sm.s_free[w]);
-            if (h > 1) wait_for(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
-            if (lane == 0) mbar_arrive(&sm.p_full[w][g & 1]);
+        wait_for(&sm.q_full[seg & 1], (seg >> 1) & 1, p.err, 64, &sm.abort);
+        float rs = live ? sm.qs[seg & 1][row] * p.scale_log2 : 1.0f;
+        // the maximum of S k_scale has to stay one under a negative scale: S changes sign
+        const bool flip = rs < 0.0f, any_flip = __any_sync(0xffffffffu, flip);
+        rs = fmaxf(fabsf(rs), 1.17549435e-38f);               // (-inf times it stays -inf)
+        float m = -INFINITY, l = 0.0f;
+        const int i_end = i + (s.t1 - s.t0);
+        // A warp without rows keeps the others company at the barriers.
+        for (int j = i; j < i_end && !warp_live; ++j) {
+            const int g = 2 * j + w, buf = g & 3;
+            wait_for(&sm.s_full[buf], (g >> 2) & 1, p.err, 64, &sm.abort);
+            if (lane == 0) mbar_arrive(&sm.s_free[buf]);
+            if (g >= 4) wait_for(&sm.o_done[buf], ((g - 4) >> 2) & 1, p.err, 128, &sm.abort);
+            if (lane == 0) mbar_arrive(&sm.p_full[buf]);
         }
 #pragma unroll 1
-        for (int h = 0; h < 2 * nt && warp_live; ++h, ++g) {
-            const int j = s.dual ? h >> 1 : (h & ~1) + w;      // block of the segment
-            const int slot = (base + j) % kSStages;
-            wait_for(&sm.s_full[w], g & 1, p.err, 64, &sm.abort);
-            float v[kHalf];
+        for (int j = i; j < i_end && warp_live; ++j) {
+            const int g = 2 * j + w, buf = g & 3, slot = j % kSStages;
+            wait_for(&sm.s_full[buf], (g >> 2) & 1, p.err, 64, &sm.abort);
             tc_fence_after();
-            wait_for(&sm.k_full[slot], ((base + j) / kSStages) & 1, p.err, 64, &sm.abort);
+            wait_for(&sm.k_full[slot], (j / kSStages) & 1, p.err, 64, &sm.abort);
+            float v[kHalf];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tmem_ld32(S + 32 * c, v + 32 * c);
+            for (int c = 0; c < 2; ++c) tmem_ld32(O + kSCol + kHalf * buf + 32 * c, v + 32 * c);
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.s_free[w]);
-            float mx = -INFINITY;
-            const float4* ks = reinterpret_cast<const float4*>(sm.ks[slot] + (h & 1) * kHalf);
+            if (lane == 0) mbar_arrive(&sm.s_free[buf]);
+            const float4* ks = reinterpret_cast<const float4*>(sm.ks[slot] + w * kHalf);
 #pragma unroll
             for (int c = 0; c < kHalf / 4; ++c) {
                 const float4 k4 = ks[c];
@@ -739,7 +609,11 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                 v[4 * c + 2] = b.x;
                 v[4 * c + 3] = b.y;
             }
-            const int off = ctx - (s.t0 + j) * kBS - (h & 1) * kHalf;   // the first drafted token's key here
+            if (any_flip) {
+#pragma unroll
+                for (int k = 0; k < kHalf; ++k) v[k] = flip ? -v[k] : v[k];
+            }
+            const int off = ctx - (s.t0 + j - i) * kBS - w * kHalf;   // the first drafted token's key here
             if (off < kHalf) {
                 // which keys the row sees: the context's, then its mask's bits
                 uint64_t see;
@@ -758,19 +632,26 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
 #pragma unroll
                 for (int k = 2; k < 16; k += 2) m4[c] = max3(m4[c], v[16 * c + k], v[16 * c + k + 1]);
             }
-            mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * rs;
+            const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * rs;
             // this P buffer's last P V is complete
-            if (h > 1) wait_for(&sm.o_done[w][g & 1], ((g - 2) >> 1) & 1, p.err, 128, &sm.abort);
-            tc_fence_after();
-            const bool raise = mx > m + kRaise || (m == -INFINITY && mx > -INFINITY);
+            if (g >= 4) wait_for(&sm.o_done[buf], ((g - 4) >> 2) & 1, p.err, 128, &sm.abort);
+            // ---- m, after the half before ----
+            const bool later = w != 0 || j > i;                // a half of the segment lies before this one
+            float mn = -INFINITY;
+            if (later) {
+                named_bar_sync(theirs, 64);
+                mn = sm.m[row];
+            }
+            const bool raise = mx > mn + kRaise || (mn == -INFINITY && mx > -INFINITY);
             if (__any_sync(0xffffffffu, raise)) {
-                const float f = raise ? ex2(m - mx) : 1.0f;
-                if (raise) m = mx;
-                l *= f;
-                if (h > 0) {
-                    // O is complete before it is scaled
-                    wait_for(&sm.o_done[w][(g - 1) & 1], ((g - 1) >> 1) & 1, p.err, 128, &sm.abort);
+                const float old = mn;
+                if (raise) mn = mx;
+                if (later) {
+                    // O is complete before it is scaled (and its barrier's phase is the
+                    // one waited for: the other warp waited for that before its decision)
+                    wait_for(&sm.o_done[(g - 1) & 3], ((g - 1) >> 2) & 1, p.err, 128, &sm.abort);
                     tc_fence_after();
+                    const float f = raise ? ex2(old - mn) : 1.0f;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         float o[32];
@@ -780,8 +661,16 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                         for (int k = 0; k < 32; ++k) o[k] *= f;
                         tmem_st32(O + 32 * c, o);
                     }
+                    tmem_wait_st();
                 }
             }
+            sm.m[row] = mn;
+            if (w == 0 || j + 1 < i_end) named_bar_arrive(mine, 64);
+            if (mn != m) {
+                l *= ex2(m - mn);                              // (0 while m is -inf)
+                m = mn;
+            }
+            tc_fence_after();
             const float ref = m == -INFINITY ? 0.0f : m - kShift;
             const float2 rs2 = make_float2(rs, rs), nref = make_float2(-ref, -ref);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -796,14 +685,84 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                     sum[k & 1] = add2(sum[k & 1], x);
                     hp[k] = half2_bits(x.x, x.y);
                 }
-                tmem_st16(S + kPCol + 32 * (g & 1) + 16 * c, hp);
+                tmem_st16(O + kPCol + 32 * buf + 16 * c, hp);
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_full[w][g & 1]);
+            if (lane == 0) mbar_arrive(&sm.p_full[buf]);
         }
+        i = i_end;
+        // ---- the item's (or its part's) output: this warpgroup's 64 channels ----
+        sm.l[w][row] = l;
+        if (w == 0) sm.m0[row] = m;          // (sm.m: the last decision, an odd half's)
+        named_bar_sync(1, 256);
+        // the last P V, and with it all (one accumulator: they complete in order);
+        // behind the barrier, as the other warpgroup waited for this barrier's last phase
+        wait_for(&sm.o_done[(2 * i - 1) & 3], ((2 * i - 1) >> 2) & 1, p.err, 128, &sm.abort);
+        tc_fence_after();
+        if (warp_live) {
+            const float mf = sm.m[row], m0 = sm.m0[row];
+            const float lt = sm.l[0][row] * (m0 == mf ? 1.0f : ex2(m0 - mf)) + sm.l[1][row];
+            const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+            const float inv = lt == 0.0f ? 0.0f : __fdiv_rn(1.0f, lt);
+            const int at = live ? q_row(p, s, row) : -1;
+            float* const part = part_of(p, blockIdx.x, s.first);
+            // Rows leave in 64-byte pieces (32 BF16 channels, 16 FP32) through this
+            // warp's staging area: a store covers eight rows' pieces instead of 16
+            // bytes of 32 rows.
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                const int d = 64 * w + 16 * c;
+                float o[16];
+                tmem_ld16(O + d, o);
+                tmem_wait_ld();
+                if (whole) {
+                    const float4* vs = reinterpret_cast<const float4*>(sm.vs[seg & 1] + d);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float4 a = vs[2 * k], b = vs[2 * k + 1];
+                        const float* x = o + 8 * k;
+                        const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * inv * a.x, x[1] * inv * a.y);
+                        const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * inv * a.z, x[3] * inv * a.w);
+                        const __nv_bfloat162 y2 = __floats2bfloat162_rn(x[4] * inv * b.x, x[5] * inv * b.y);
+                        const __nv_bfloat162 y3 = __floats2bfloat162_rn(x[6] * inv * b.z, x[7] * inv * b.w);
+                        *reinterpret_cast<uint4*>(stage + stage_at(lane, 2 * (c & 1) + k)) =
+                            make_uint4(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1),
+                                       *reinterpret_cast<const uint32_t*>(&y2), *reinterpret_cast<const uint32_t*>(&y3));
+                    }
+                    if ((c & 1) == 0) continue;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<float4*>(stage + stage_at(lane, k)) =
+                            make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 8 * k + (lane >> 2);
+                    const int to = __shfl_sync(0xffffffffu, at, r);
+                    const uint4 x = *reinterpret_cast<const uint4*>(stage + stage_at(r, lane & 3));
+                    if (to < 0) continue;
+                    uint4* dst = whole ? reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(to) * kD + d - 16)
+                                       : reinterpret_cast<uint4*>(part + (32 * q4 + r) * kD + d);
+                    dst[lane & 3] = x;
+                }
+                __syncwarp();
+            }
+            if (!whole && live && w == 0) {
+                float* ml = part + static_cast<int64_t>(p.part_rows) * kD;
+                ml[row] = mf;
+                ml[p.part_rows + row] = lt;
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_empty[seg & 1]);
+        // (O, m and l of this segment are not touched before both warpgroups are here)
+        named_bar_sync(1, 256);
     }
 }
 
@@ -840,7 +799,7 @@ __device__ void describe_cut(TreeSmem& sm, const TreeParams& p, Run run, uint32_
                 }
             }
             // the runs that hold the first and the last block's positions
-            const int c0 = cta_of(total, base + kItemCost, p.ctas), c1 = cta_of(total, end - (s.dual ? 2 : 1), p.ctas);
+            const int c0 = cta_of(total, base + kItemCost, p.ctas), c1 = cta_of(total, end - 1, p.ctas);
             if (c == c0 + 1 && c0 < c1) {
                 cut.b = s.b;
                 cut.h = s.h;
@@ -865,26 +824,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < kSStages; ++i) mbar_init(&sm.k_full[i], 33);
-        for (int i = 0; i < kKStages; ++i) mbar_init(&sm.k_empty[i], 2);
+        for (int i = 0; i < kKStages; ++i) mbar_init(&sm.k_empty[i], 1);
         for (int i = 0; i < kVStages; ++i) {
             mbar_init(&sm.v_full[i], 1);
             mbar_init(&sm.v_empty[i], kConvWarps);
         }
         for (int i = 0; i < kHStages; ++i) {
             mbar_init(&sm.h_full[i], kConvWarps);
-            mbar_init(&sm.h_empty[i], 2);
+            mbar_init(&sm.h_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_free[i], 4);
-            for (int j = 0; j < 2; ++j) {
-                mbar_init(&sm.p_full[i][j], 4);
-                mbar_init(&sm.o_done[i][j], 1);
-            }
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.o_done[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], 1 + kProdWarp);
             mbar_init(&sm.drain[i], 1);
         }
-        mbar_init(&sm.q_full, 8);
-        mbar_init(&sm.q_seen, 2);
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -909,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        uint32_t* const warp_sum = reinterpret_cast<uint32_t*>(sm.ml);
+        uint32_t* const warp_sum = reinterpret_cast<uint32_t*>(sm.l);
         if (lane == 31) warp_sum[warp] = x;
         __syncthreads();
         uint32_t before = x - mine;
@@ -939,12 +898,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kProdWarp) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        softmax(sm, p, run, tmem, warp >> 2, warp, lane);
+        softmax(sm, p, run, tmem, warp >> 2, warp & 3, lane);
     } else if (warp < kConvWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == kProdWarp) producer(sm, p, &tk, &tv, run, lane);
-        else if (warp == kCutWarp) describe_cut(sm, p, run, total, lane);
-        else mma_issuer(sm, p, run, tmem, warp - kMmaWarp);
+        if (warp == kProdWarp) {
+            producer(sm, p, &tk, &tv, run, lane);
+        } else if (warp == kQWarp) {
+            q_loader(sm, p, run, lane);
+            describe_cut(sm, p, run, total, lane);
+        } else {
+            mma_issuer(sm, p, run, tmem, warp - kMmaWarp);
+        }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -1101,6 +1065,10 @@ extern "C" pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, con
     PA_REQUIRE(mask_stride >= 0, PA_ERR_INVALID, "%s: negative mask_stride", name);
     PA_REQUIRE(aligned16(q) && aligned16(k_cache) && aligned16(v_cache) && aligned16(v_scale) && aligned16(out),
                PA_ERR_INVALID, "%s: q, the caches, v_scale and out must be 16-byte aligned", name);
+    // the schedule counts blocks in 32 bits
+    const int64_t per_block = (static_cast<int64_t>(S1) * (NQ / NKV) + kItemRows - 1) / kItemRows * (1 + kItemCost);
+    PA_REQUIRE(per_block * NKV * B <= 0xFFFFFFFFll / max_blocks_per_seq, PA_ERR_UNSUPPORTED,
+               "%s: B * heads * max_blocks_per_seq too large for the 32-bit schedule", name);
     PA_REQUIRE(static_cast<int64_t>(B) * S1 * NQ <= 0x7FFFFFFF, PA_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 query rows",
                name);
     if (B == 0) return PA_OK;
@@ -1147,12 +1115,11 @@ extern "C" pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, con
     p.keep_l2 = static_cast<int64_t>(S1) * p.G > kItemRows;
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
 
-    const size_t smem = sizeof(TreeSmem) + 1024;
     cudaError_t e = cudaFuncSetAttribute(tree_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         static_cast<int>(kSmemBytes));
     PA_REQUIRE(e == cudaSuccess, PA_ERR_CUDA, "%s: smem attribute: %s", name, cudaGetErrorString(e));
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    tree_decode_kernel<<<static_cast<unsigned>(p.ctas), kThreads, smem, cs>>>(tk, tv, p);
+    tree_decode_kernel<<<static_cast<unsigned>(p.ctas), kThreads, kSmemBytes, cs>>>(tk, tv, p);
     st = check_launch(name);
     if (st != PA_OK || p.ctas == 1) return st;
     const int64_t most = static_cast<int64_t>(S1) * p.G < kItemRows ? static_cast<int64_t>(S1) * p.G : kItemRows;
