@@ -23,6 +23,7 @@ and a speculative decode step over the same cache:
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -306,11 +307,18 @@ class _Prepared:
     the stream passed to the call."""
 
     def __init__(self, fn, where, args, keep, stream):
-        self._fn, self._where, self._args, self._keep = fn, where, args, keep
+        # a function object of its own that takes ready ctypes values as they are:
+        # converting a long argument list anew took longer than a short kernel
+        raw = lib()[where]
+        raw.restype = fn.restype
+        ready = tuple(t(a) if isinstance(a, (int, float)) else a
+                      for t, a in zip(fn.argtypes, args))
+        self._call = functools.partial(raw, *ready)
+        self._where, self._keep = where, keep
         self._stream = _stream(stream)
 
     def __call__(self, stream=None):
-        st = self._fn(*self._args, self._stream if stream is None else _stream(stream))
+        st = self._call(self._stream if stream is None else _stream(stream))
         if st != PA_OK:
             _check(st, self._where)
 

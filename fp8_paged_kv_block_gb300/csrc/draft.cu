@@ -12,41 +12,57 @@ namespace cg = cooperative_groups;
 constexpr int kMaxNodes = 1024;
 
 // ---- verification ------------------------------------------------------------------
-// One cluster of kVC CTAs per sequence; every thread follows the same walk
-// over the nodes. A node's first test needs three values (p, q and u at its
-// token), gathered for all nodes at once ahead of the walk. A rejection of a
-// drawn draft needs all of R = max(R - z Q, 0) and its sum, and the draw at
-// the end needs R: CTA r keeps channels [r, r + 1) * slice of R in shared
-// memory, warp w of it the w-th segment of the slice, in index order, so that
-// the draw needs the 128 segments' sums and then one segment's 32-wide steps.
+// One cluster of CTAs per sequence; every thread follows the same walk over the
+// nodes. A node's tests need p, q and u at its token alone (R after k rejections
+// is replayed from p, q and the z of each), gathered for all nodes at once ahead
+// of the walk. A rejection of a drawn draft needs the sum of R over the
+// vocabulary, and the draw at the end R's prefix sums: warp w of the cluster takes
+// the w-th segment of the vocabulary, replays R there and sums it; the draw then
+// needs the segments' sums and one segment's 128-wide steps.
 // The weights are 2^-45 integers: their sums are exact, so the drawn index
 // depends neither on the number of CTAs nor on the order of summation.
-// Bound by the rows of p and q read (one or two of V floats per sequence) on
-// large batches, by the chain launch, gather, row, two cluster barriers on
-// small ones.
-constexpr int kVC = 8;
+// Bound by the rows of p and q read (one or two of V floats per sequence, again
+// from L2 for each further rejection) on large batches, by the chain launch,
+// gather, row, cluster barrier on small ones.
+// A sequence gets 8 CTAs while the batch's CTAs all fit on the GPU (kResident),
+// half as many for twice the batch.
 constexpr int kVThreads = 512;
 constexpr int kVWarps = kVThreads / 32;
-constexpr int kSegs = kVC * kVWarps;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxSegs = kMaxCluster * kVWarps;
 constexpr int kMaxV = 1 << 18;
+constexpr int kResident = 608;               // 4 CTAs on each of 152 SMs
 
 struct VerifyParams {
     const float *p, *q;
     const int *tok, *par;
     const float* u;
     const int* len;
-    int S1, V, slice, seg;
+    int S1, V, seg;
     int *accepted, *path, *tokens;
 };
 
-// floor(min(r, 1) * 2^45) for r > 0, 0 for the rest and for NaN.
+// floor(min(r, 1) * 2^45), 0 for NaN and below 0, as its top 23 and low 23 bits:
+// r 2^22 and the rest of it 2^23 are exact, and adding 2^23 toward zero leaves
+// their integer parts in the mantissa. hi and lo collect the floats' bits; kBias
+// taken off once for each (modulo 2^32, where the sums of 2^9 terms lie) leaves
+// the sums.
+constexpr uint32_t kBias = 0x4B000000u;      // the bits of 2^23
+
+__device__ __forceinline__ void add_weight(float r, uint32_t& hi, uint32_t& lo)
+{
+    const float x = fminf(fmaxf(r, 0.0f), 1.0f) * 0x1p22f;
+    const float t = __fadd_rz(x, 0x1p23f);
+    const float rest = x - (t - 0x1p23f);
+    hi += __float_as_uint(t);
+    lo += __float_as_uint(__fmaf_rz(rest, 0x1p23f, 0x1p23f));
+}
+
 __device__ __forceinline__ unsigned long long weight(float r)
 {
-    if (!(r > 0.0f)) return 0;
-    const uint32_t u = __float_as_uint(fminf(r, 1.0f));
-    const int sh = static_cast<int>(u >> 23) - 105;      // exponent - 127 - 23 + 45
-    const unsigned long long m = (u & 0x7FFFFFu) | 0x800000u;
-    return sh >= 0 ? m << sh : (sh > -24 ? m >> -sh : 0ull);
+    uint32_t hi = 0, lo = 0;
+    add_weight(r, hi, lo);
+    return (static_cast<unsigned long long>(hi - kBias) << 23) + (lo - kBias);
 }
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v)
@@ -57,22 +73,26 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v)
 }
 
 struct VerifySmem {
-    double p0[kMaxNodes], q0[kMaxNodes];
-    float u[kMaxNodes];
-    int par[kMaxNodes], tok[kMaxNodes];
-    unsigned long long wsum[kVWarps];
-    unsigned long long all[kSegs];
+    unsigned long long wsum[2][kVWarps];     // this CTA's segments, by pass parity
+    unsigned long long all[kMaxSegs];        // the cluster's
+    // then, S1 long each: p and q at a node's token, u, parent, token, the z's
 };
 
-__global__ void __cluster_dims__(kVC, 1, 1) __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyParams a)
+template <bool VEC>
+__global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyParams a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     VerifySmem& sm = *reinterpret_cast<VerifySmem*>(raw);
-    float* R = reinterpret_cast<float*>(raw + sizeof(VerifySmem));
+    float* const p0 = reinterpret_cast<float*>(raw + sizeof(VerifySmem));
+    float* const q0 = p0 + a.S1;
+    float* const un = q0 + a.S1;
+    float* const zs = un + a.S1;
+    int* const par = reinterpret_cast<int*>(zs + a.S1);
+    int* const tok = par + a.S1;
     cg::cluster_group cl = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = static_cast<int>(cl.block_rank());
-    const int64_t b = blockIdx.x / kVC;
+    const int rank = static_cast<int>(cl.block_rank()), ctas = static_cast<int>(cl.num_blocks());
+    const int64_t b = blockIdx.x / ctas;
     int* path = a.path + b * a.S1;
     int* tokens = a.tokens + b * a.S1;
     int n = a.len ? __ldg(a.len + b) : a.S1;
@@ -87,108 +107,130 @@ __global__ void __cluster_dims__(kVC, 1, 1) __launch_bounds__(kVThreads) tree_ve
     const float* pb = a.p + b * a.S1 * a.V;
     const float* qb = a.q ? a.q + b * a.S1 * a.V : nullptr;
     for (int s = tid; s < n; s += kVThreads) {
-        const int par = __ldg(a.par + b * a.S1 + s), x = __ldg(a.tok + b * a.S1 + s);
-        const bool ok = s > 0 && par >= 0 && par < s && x >= 0 && x < a.V;
-        sm.par[s] = ok ? par : -1;
-        sm.tok[s] = x;
-        sm.u[s] = __ldg(a.u + b * a.S1 + s);
-        const int64_t at = static_cast<int64_t>(ok ? par : 0) * a.V + (ok ? x : 0);
-        sm.p0[s] = ok ? static_cast<double>(__ldg(pb + at)) : 0.0;
-        sm.q0[s] = ok ? (qb ? static_cast<double>(__ldg(qb + at)) : 1.0) : 0.0;
+        const int pr = __ldg(a.par + b * a.S1 + s), x = __ldg(a.tok + b * a.S1 + s);
+        const bool ok = s > 0 && pr >= 0 && pr < s && x >= 0 && x < a.V;
+        par[s] = ok ? pr : -1;
+        tok[s] = x;
+        un[s] = __ldg(a.u + b * a.S1 + s);
+        const int64_t at = static_cast<int64_t>(ok ? pr : 0) * a.V + (ok ? x : 0);
+        p0[s] = ok ? __ldg(pb + at) : 0.0f;
+        q0[s] = ok ? (qb ? __ldg(qb + at) : 1.0f) : 0.0f;
     }
     __syncthreads();
 
-    // this warp's channels of R: [lo, hi) of the vocabulary, R[lo - base ..]
-    const int base = rank * a.slice;
-    const int lo = min(base + warp * a.seg, min(base + a.slice, a.V));
-    const int hi = min(lo + a.seg, min(base + a.slice, a.V));
-    // R of node `cur` from p, or one rejection further, and the segments' sums
-    auto sums = [&](unsigned long long mine) {
-        mine = warp_sum(mine);
-        if (lane == 0) sm.wsum[warp] = mine;
-        cl.sync();
-        if (tid < kSegs) sm.all[tid] = cl.map_shared_rank(sm.wsum, tid / kVWarps)[tid % kVWarps];
-        __syncthreads();
-        unsigned long long z = 0;
-        for (int i = lane; i < kSegs; i += 32) z += sm.all[i];
-        return warp_sum(z);
+    // this warp's segment [lo, hi) of the vocabulary
+    const int segs = ctas * kVWarps, mine = rank * kVWarps + warp;
+    const int lo = min(mine * a.seg, a.V), hi = min(lo + a.seg, a.V);
+    const float* prow = pb;
+    const float* qrow = qb;
+    int cur = 0, acc = 1, rej = 0;           // current node, nodes accepted, drafts of cur rejected so far
+    // R after `rej` rejections of drawn drafts, from p and q
+    auto rest = [&](float r, float q) {
+        for (int k = 0; k < rej; ++k) r = fmaxf(__fsub_rn(r, __fmul_rn(zs[k], q)), 0.0f);
+        return r;
     };
-    auto load = [&](int cur) {
+    // R's weights summed over all of the vocabulary, and each segment's into sm.all
+    int pass = 0;
+    auto sums = [&](bool replay) {
         unsigned long long w = 0;
-        const float* src = pb + static_cast<int64_t>(cur) * a.V;
-#pragma unroll 8
-        for (int i = lo + lane; i < hi; i += 32) {
-            const float r = __ldg(src + i);
-            R[i - base] = r;
-            w += weight(r);
+        if (VEC) {
+#pragma unroll 2
+            for (int i = lo + 4 * lane; i < hi; i += 128) {
+                float4 r = __ldg(reinterpret_cast<const float4*>(prow + i));
+                if (replay) {
+                    const float4 q = __ldg(reinterpret_cast<const float4*>(qrow + i));
+                    for (int k = 0; k < rej; ++k) {
+                        const float z = zs[k];
+                        r.x = fmaxf(__fsub_rn(r.x, __fmul_rn(z, q.x)), 0.0f);
+                        r.y = fmaxf(__fsub_rn(r.y, __fmul_rn(z, q.y)), 0.0f);
+                        r.z = fmaxf(__fsub_rn(r.z, __fmul_rn(z, q.z)), 0.0f);
+                        r.w = fmaxf(__fsub_rn(r.w, __fmul_rn(z, q.w)), 0.0f);
+                    }
+                }
+                uint32_t h = 0, l = 0;
+                add_weight(r.x, h, l);
+                add_weight(r.y, h, l);
+                add_weight(r.z, h, l);
+                add_weight(r.w, h, l);
+                w += (static_cast<unsigned long long>(h - 4 * kBias) << 23) + (l - 4 * kBias);
+            }
+        } else {
+#pragma unroll 4
+            for (int i = lo + lane; i < hi; i += 32) {
+                float r = __ldg(prow + i);
+                if (replay) r = rest(r, __ldg(qrow + i));
+                w += weight(r);
+            }
         }
-        return w;
+        if (!replay && !qb && rej > 0) {
+            // tokens of cur's children, all of them rejected, are out
+            for (int t = cur + 1; t < n; ++t) {
+                if (par[t] != cur || tok[t] < lo || tok[t] >= hi) continue;
+                bool again = false;
+                for (int e = cur + 1; e < t; ++e) again = again || (par[e] == cur && tok[e] == tok[t]);
+                if (!again && lane == 0) w -= weight(p0[t]);
+            }
+        }
+        w = warp_sum(w);
+        // (two sets: a CTA may be a pass ahead of one that still reads)
+        if (lane == 0) sm.wsum[pass & 1][warp] = w;
+        cl.sync();
+        if (tid < segs) sm.all[tid] = cl.map_shared_rank(sm.wsum[pass & 1], tid / kVWarps)[tid % kVWarps];
+        __syncthreads();
+        ++pass;
+        unsigned long long z = 0;
+        for (int i = lane; i < segs; i += 32) z += sm.all[i];
+        z = warp_sum(z);
+        __syncthreads();                     // sm.all is read before the next pass writes it
+        return z;
     };
 
-    int cur = 0, acc = 1;
-    bool held = false, summed = false;   // R holds cur's rest; sm.all its sums
     double z = 1.0;
     unsigned long long Z = 0;
+    bool summed = false;                     // Z and sm.wsum are of R as it is
     for (int s = 1; s < n; ++s) {
-        if (sm.par[s] != cur) continue;
-        const int x = sm.tok[s];
-        double rx = sm.p0[s];
+        if (par[s] != cur) continue;
+        const int x = tok[s];
+        double rx;
         if (qb) {
-            if (held) rx = static_cast<double>(*cl.map_shared_rank(R + x % a.slice, x / a.slice));
+            rx = static_cast<double>(rest(p0[s], q0[s]));
         } else {
+            rx = static_cast<double>(p0[s]);
             for (int t = cur + 1; t < s; ++t)
-                if (sm.par[t] == cur && sm.tok[t] == x) rx = 0.0;   // rejected before: R(x) is 0
+                if (par[t] == cur && tok[t] == x) rx = 0.0;   // rejected before: R(x) is 0
         }
-        if (static_cast<double>(sm.u[s]) * z * sm.q0[s] < rx) {
+        if (static_cast<double>(un[s]) * z * static_cast<double>(q0[s]) < rx) {
             if (rank == 0 && tid == 0) {
                 path[acc] = s;
                 tokens[acc - 1] = x;
             }
             ++acc;
             cur = s;
-            held = summed = false;
+            rej = 0;
+            summed = false;
             z = 1.0;
+            prow = pb + static_cast<int64_t>(cur) * a.V;
+            if (qb) qrow = qb + static_cast<int64_t>(cur) * a.V;
         } else if (qb) {
-            const float zf = static_cast<float>(z);
-            const float* src = pb + static_cast<int64_t>(cur) * a.V;
-            const float* qr = qb + static_cast<int64_t>(cur) * a.V;
-            cl.sync();                    // every thread has read R(x)
-            unsigned long long w = 0;
-#pragma unroll 8
-            for (int i = lo + lane; i < hi; i += 32) {
-                const float r0 = held ? R[i - base] : __ldg(src + i);
-                const float r = fmaxf(__fsub_rn(r0, __fmul_rn(zf, __ldg(qr + i))), 0.0f);
-                R[i - base] = r;
-                w += weight(r);
-            }
-            Z = sums(w);
-            held = summed = true;
+            __syncthreads();                 // (a thread may still be at an earlier test's z's)
+            if (tid == 0) zs[rej] = static_cast<float>(z);
+            __syncthreads();
+            ++rej;
+            Z = sums(true);
+            summed = true;
             z = static_cast<double>(static_cast<float>(static_cast<double>(Z) * 0x1p-45));
         } else {
+            ++rej;
             z -= rx;
         }
     }
     // ---- the draw ----
-    if (!summed) {
-        cl.sync();                        // sm.wsum and R of an earlier node are not read any more
-        unsigned long long w = load(cur);
-        if (!qb) {
-            // tokens of cur's children, all of them rejected, are out
-            __syncwarp();
-            for (int t = cur + 1; t < n; ++t)
-                if (sm.par[t] == cur && sm.tok[t] >= lo && sm.tok[t] < hi) {
-                    if (lane == (sm.tok[t] - lo) % 32) {
-                        w -= weight(R[sm.tok[t] - base]);
-                        R[sm.tok[t] - base] = 0.0f;
-                    }
-                    __syncwarp();
-                }
-        }
-        Z = sums(w);
-    }
+    bool all_of_p = false;                   // R is empty: p takes its place
+    if (!summed) Z = sums(false);
     if (Z == 0) {
-        cl.sync();
-        Z = sums(load(cur));
+        all_of_p = true;
+        rej = 0;
+        Z = sums(false);
     }
     if (rank == 0) {
         if (tid == 0) {
@@ -199,40 +241,62 @@ __global__ void __cluster_dims__(kVC, 1, 1) __launch_bounds__(kVThreads) tree_ve
         for (int i = acc + tid; i < a.S1; i += kVThreads) path[i] = tokens[i] = -1;
     }
     if (Z != 0) {
-        const float u0 = sm.u[0];
+        const float u0 = un[0];
         unsigned long long t = u0 > 0.0f ? static_cast<unsigned long long>(static_cast<double>(u0) * static_cast<double>(Z)) : 0ull;
         if (t >= Z) t = Z - 1;
         unsigned long long before = 0;
-        const int mine = rank * kVWarps + warp;
         for (int i = lane; i < mine; i += 32) before += sm.all[i];
         before = warp_sum(before);
         if (t >= before && t - before < sm.all[mine]) {
-            for (int i0 = lo; i0 < hi; i0 += 32) {
-                const int i = i0 + lane;
-                unsigned long long c = i < hi ? weight(R[i - base]) : 0ull;
+            auto weight_at = [&](int i) -> unsigned long long {
+                float r = __ldg(prow + i);
+                if (qb) {
+                    if (rej > 0) r = rest(r, __ldg(qrow + i));
+                } else if (!all_of_p) {
+                    for (int e = cur + 1; e < n; ++e)
+                        if (par[e] == cur && tok[e] == i) r = 0.0f;
+                }
+                return weight(r);
+            };
+            auto scan = [&](unsigned long long c) {
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const unsigned long long up = __shfl_up_sync(0xffffffffu, c, o);
                     if (lane >= o) c += up;
                 }
-                const unsigned hit = __ballot_sync(0xffffffffu, before + c > t);
+                return c;
+            };
+            // the 32nd of the segment that holds it (one lane sums each), then the
+            // value, 32 at a time
+            const int sub = a.seg / 32, l0 = min(lo + lane * sub, hi), l1 = min(l0 + sub, hi);
+            unsigned long long c = 0;
+#pragma unroll 8
+            for (int i = l0; i < l1; ++i) c += weight_at(i);
+            const unsigned long long upto = scan(c);
+            const int at = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, before + upto > t))) - 1;
+            before += __shfl_sync(0xffffffffu, upto - c, at);
+            const int end = __shfl_sync(0xffffffffu, l1, at);
+            for (int i0 = __shfl_sync(0xffffffffu, l0, at); i0 < end; i0 += 32) {
+                const unsigned long long v = scan(i0 + lane < end ? weight_at(i0 + lane) : 0ull);
+                const unsigned hit = __ballot_sync(0xffffffffu, before + v > t);
                 if (hit) {
                     if (lane == 0) tokens[acc - 1] = i0 + __ffs(static_cast<int>(hit)) - 1;
                     break;
                 }
-                before += __shfl_sync(0xffffffffu, c, 31);
+                before += __shfl_sync(0xffffffffu, v, 31);
             }
         }
     }
-    cl.sync();                            // no CTA leaves while another reads its shared memory
+    cl.sync();                               // no CTA leaves while another reads its sums
 }
 
 // ---- the accepted branch in the cache ------------------------------------------------
-// One CTA per (sequence, group of heads); a thread owns one 16-byte chunk of
-// one head's K or V (or one key scale) and moves it for the branch's nodes in
-// order. path[i] >= i, so a node's chunk is read before the move that
-// overwrites it comes, and only this thread touches it: no barrier between
-// loads and stores. Latency-bound: a chain of four dependent loads.
+// One CTA per (sequence, heads_per_cta heads). A round takes rows in order as far
+// as the CTA's registers go (kKBatch 16-byte chunks a thread): all are read, then,
+// behind a barrier, written. path[i] >= i, so a round's writes, to lower rows
+// than any later round's sources, spoil nothing that is still to be read.
+// Latency-bound: a chain of four dependent loads (accepted, path, block table,
+// row), which more rows do not lengthen.
 constexpr int kKThreads = 256;
 constexpr int kKBatch = 8;
 
@@ -248,7 +312,7 @@ struct KeepParams {
 
 __global__ void __launch_bounds__(kKThreads) cache_keep_path_kernel(const KeepParams p)
 {
-    __shared__ int64_t src[kMaxNodes], dst[kMaxNodes];   // token slots, src -1: no move
+    __shared__ int64_t src[kMaxNodes], dst[kMaxNodes];   // rows of head 0; src -1: no move
     const int b = blockIdx.x, tid = threadIdx.x;
     const int act = max(__ldg(p.act + b), 0);
     int n = p.len ? __ldg(p.len + b) : p.S1;
@@ -258,44 +322,63 @@ __global__ void __launch_bounds__(kKThreads) cache_keep_path_kernel(const KeepPa
     m = m < 0 ? 0 : (m > n ? n : m);
     const int ctx = act - n;
     if (blockIdx.y == 0 && tid == 0) p.new_act[b] = ctx + m;
-    auto slot = [&](int pos) -> int64_t {
+    auto row0 = [&](int pos) -> int64_t {
         const int bi = pos / p.BS;
         if (pos < 0 || bi >= p.max_blocks) return -1;
         const int id = __ldg(p.bt + static_cast<int64_t>(b) * p.max_blocks + bi);
-        return id >= 0 && id < p.num_blocks ? static_cast<int64_t>(id) * p.BS + pos % p.BS : -1;
+        return id >= 0 && id < p.num_blocks ? cache_row(p.layout, id, pos - bi * p.BS, 0, p.BS, p.H) : -1;
     };
     for (int i = tid; i < m; i += kKThreads) {
         const int s = __ldg(p.path + static_cast<int64_t>(b) * p.S1 + i);
         int64_t from = -1, to = -1;
         if (s != i && s >= 0 && s < n) {
-            from = slot(ctx + s);
-            to = slot(ctx + i);
+            from = row0(ctx + s);
+            to = row0(ctx + i);
         }
         src[i] = to >= 0 ? from : -1;
         dst[i] = to;
     }
     __syncthreads();
-    const int h0 = blockIdx.y * p.heads_per_cta;
-    const int heads = min(p.heads_per_cta, p.H - h0);
-    const int per = 2 * p.chunks;
-    for (int c = tid; c < heads * (per + 1); c += kKThreads) {
-        const int h = h0 + c / (per + 1), k = c % (per + 1);
-        auto row = [&](int64_t slot_) { return cache_row(p.layout, slot_ / p.BS, slot_ % p.BS, h, p.BS, p.H); };
-        if (k == per) {
-            for (int i = 0; i < m; ++i)
-                if (src[i] >= 0) p.ks[row(dst[i])] = p.ks[row(src[i])];
-            continue;
-        }
-        uint4* base = reinterpret_cast<uint4*>(k < p.chunks ? p.kc : p.vc) + (k < p.chunks ? k : k - p.chunks);
-        for (int i0 = 0; i0 < m; i0 += kKBatch) {
-            uint4 v[kKBatch];
+    const int64_t head_step = p.layout == PA_LAYOUT_BSND ? 1 : p.BS;
+    const int h0 = blockIdx.y * p.heads_per_cta, heads = min(p.heads_per_cta, p.H - h0);
+    const int per_row = heads * 2 * p.chunks;            // chunks of K, then of V, head by head
+    const int rows = max(1, min(kKThreads * kKBatch / per_row, kKThreads / heads));   // a round's
+    for (int i0 = 0; i0 < m; i0 += rows) {
+        const int tasks = min(rows, m - i0) * per_row;
+        uint4 v[kKBatch];
+        uint4* to[kKBatch];
+        float sv = 0.0f;
+        float* sto = nullptr;
 #pragma unroll
-            for (int j = 0; j < kKBatch; ++j)
-                if (i0 + j < m && src[i0 + j] >= 0) v[j] = base[row(src[i0 + j]) * p.chunks];
-#pragma unroll
-            for (int j = 0; j < kKBatch; ++j)
-                if (i0 + j < m && src[i0 + j] >= 0) base[row(dst[i0 + j]) * p.chunks] = v[j];
+        for (int j = 0; j < kKBatch; ++j) {
+            const int t = tid + j * kKThreads;
+            to[j] = nullptr;
+            if (t < tasks) {
+                const int i = t / per_row, r = t - i * per_row;
+                const int c = r / p.chunks, k = r - c * p.chunks;
+                const int64_t from = src[i0 + i];
+                if (from >= 0) {
+                    const int64_t head = (h0 + (c >> 1)) * head_step;
+                    uint4* base = reinterpret_cast<uint4*>((c & 1) ? p.vc : p.kc) + k;
+                    v[j] = base[(from + head) * p.chunks];
+                    to[j] = base + (dst[i0 + i] + head) * p.chunks;
+                }
+            }
         }
+        if (tid < min(rows, m - i0) * heads) {
+            const int i = tid / heads;
+            if (src[i0 + i] >= 0) {
+                const int64_t head = (h0 + tid - i * heads) * head_step;
+                sv = p.ks[src[i0 + i] + head];
+                sto = p.ks + dst[i0 + i] + head;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kKBatch; ++j)
+            if (to[j]) *to[j] = v[j];
+        if (sto) *sto = sv;
+        __syncthreads();
     }
 }
 
@@ -330,18 +413,33 @@ extern "C" pa_status pa_tree_verify(const float* target_probs, const float* draf
     a.len = tree_len;
     a.S1 = S1;
     a.V = V;
-    a.seg = (V + kSegs * 32 - 1) / (kSegs * 32) * 32;
-    a.slice = a.seg * kVWarps;
     a.accepted = accepted;
     a.path = path;
     a.tokens = tokens;
-    const size_t smem = sizeof(VerifySmem) + static_cast<size_t>(a.slice) * sizeof(float);
-    // (per device: set on every call, a host-side table write)
-    cudaError_t e = cudaFuncSetAttribute(tree_verify_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    PA_REQUIRE(e == cudaSuccess, PA_ERR_CUDA, "pa_tree_verify: smem attribute: %s", cudaGetErrorString(e));
-    tree_verify_kernel<<<static_cast<unsigned>(B) * kVC, kVThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
-    return check_launch("pa_tree_verify");
+    int cluster = kMaxCluster;
+    while (cluster > 1 && static_cast<int64_t>(B) * cluster > kResident) cluster >>= 1;
+    // segments of whole 128-value steps
+    const int segs = cluster * kVWarps;
+    a.seg = (V + segs * 128 - 1) / (segs * 128) * 128;
+    const size_t smem = sizeof(VerifySmem) + static_cast<size_t>(S1) * 6 * sizeof(float);
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(static_cast<unsigned>(B) * cluster);
+    lc.blockDim = dim3(kVThreads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    // rows that all start on 16 bytes are read 16 bytes at a time
+    const bool vec = V % 4 == 0 && aligned(target_probs, 16) && aligned(draft_probs, 16);
+    const cudaError_t e = vec ? cudaLaunchKernelEx(&lc, tree_verify_kernel<true>, a)
+                              : cudaLaunchKernelEx(&lc, tree_verify_kernel<false>, a);
+    PA_REQUIRE(e == cudaSuccess, PA_ERR_CUDA, "pa_tree_verify: launch: %s", cudaGetErrorString(e));
+    return PA_OK;
 }
 
 extern "C" pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache, float* key_scale_cache,
@@ -361,8 +459,9 @@ extern "C" pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache, 
     PA_REQUIRE(layout == PA_LAYOUT_BSND || layout == PA_LAYOUT_BNBD, PA_ERR_INVALID,
                "%s: unknown layout %d", name, layout);
     PA_REQUIRE(S1 <= kMaxNodes, PA_ERR_UNSUPPORTED, "%s: S1 %d > %d", name, S1, kMaxNodes);
-    PA_REQUIRE(head_size % 16 == 0, PA_ERR_UNSUPPORTED, "%s: head_size %d is not a multiple of 16", name,
-               head_size);
+    PA_REQUIRE(head_size % 16 == 0 && head_size <= 8192, PA_ERR_UNSUPPORTED,
+               "%s: head_size %d (a multiple of 16 up to 8192)", name, head_size);
+    static_assert(2 * 2 * 8192 / 16 <= kKThreads * kKBatch, "a row of two heads fits a round");
     PA_REQUIRE(new_act_seqs != kv_act_seqs, PA_ERR_INVALID,
                "%s: new_act_seqs must be another buffer than kv_act_seqs", name);
     PA_REQUIRE(aligned(key_cache, 16) && aligned(value_cache, 16) && aligned(key_scale_cache, 4), PA_ERR_INVALID,
@@ -385,8 +484,7 @@ extern "C" pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache, 
     p.num_blocks = num_blocks;
     p.max_blocks = max_blocks_per_seq;
     p.layout = layout;
-    const int per = 2 * p.chunks + 1;
-    p.heads_per_cta = kKThreads / per > 0 ? kKThreads / per : 1;
+    p.heads_per_cta = NKV < 2 ? 1 : 2;
     const int64_t gy = (NKV + p.heads_per_cta - 1) / p.heads_per_cta;
     PA_REQUIRE(gy <= 65535, PA_ERR_UNSUPPORTED, "%s: too many heads (%d)", name, NKV);
     cache_keep_path_kernel<<<dim3(static_cast<unsigned>(B), static_cast<unsigned>(gy)), kKThreads, 0,

@@ -9,8 +9,11 @@
 //
 // A row's head_size values lie 8 to a lane, so that a BF16 row is one 16-byte
 // load per lane: 16 lanes per row of 128, two rows to a warp, and the sums and
-// maxima take four shuffles for both. A warp works on kRowSets of those at
-// once: that many more loads in flight.
+// maxima take four shuffles for both. A warp takes kSets of those, heads of one
+// token and of one kind (q, k or v), with all loads in flight at once: angles and
+// weights stay in registers over them. (A job of rows numbered straight through,
+// with a 64-bit division and its own angles for every row, took 188 us on the
+// 8192-token case.)
 #include "common.cuh"
 
 #include <cmath>
@@ -19,7 +22,7 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRowSets = 2;
+constexpr int kSets = 4;
 
 struct NormRopeParams {
     const void *q, *k, *v;
@@ -43,6 +46,7 @@ struct NormRopeParams {
     int num_batches;
     int64_t T;
     int NQ, NKV;
+    uint32_t q_jobs, kv_jobs;                // warps a token's q heads, its k (and v) heads take
     int64_t num_blocks;
     int BS, layout;
 };
@@ -70,121 +74,185 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8])
     unpack_bf16(__ldg(reinterpret_cast<const uint4*>(p)), x);
 }
 
-// Eight codes of y * (448 / amax). Where the quotient leaves the float range
-// (amax below 2^-118) both sides are first taken times 2^100.
+// Eight values as they lie in memory, unpacked where they are used.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p)
+    {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&x)[8]) const
+    {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void get(float (&x)[8]) const { unpack_bf16(a, x); }
+};
+
+// Eight codes of y * (448 / amax). Where the quotient may leave the float range
+// both sides are first taken times a power of two.
 __device__ __forceinline__ uint2 encode8(const float (&y)[8], float amax)
 {
-    if (amax == 0.0f) return make_uint2(0u, 0u);
-    const float up = amax < 0x1p-118f ? 0x1p100f : 1.0f;
-    const float inv = __fdiv_rn(kE4M3Max, amax * up);
+    const float up = amax < 0x1p-100f ? 0x1p100f : (amax > 0x1p100f ? 0x1p-100f : 1.0f);
+    const float inv = __fdividef(kE4M3Max, amax * up);
     uint2 r;
-    r.x = e4m3x4(y[0] * up * inv, y[1] * up * inv, y[2] * up * inv, y[3] * up * inv);
-    r.y = e4m3x4(y[4] * up * inv, y[5] * up * inv, y[6] * up * inv, y[7] * up * inv);
+    if (amax == 0.0f) {
+        r = make_uint2(0u, 0u);
+    } else if (up == 1.0f) {
+        r.x = e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+        r.y = e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
+    } else {
+        r.x = e4m3x4(y[0] * up * inv, y[1] * up * inv, y[2] * up * inv, y[3] * up * inv);
+        r.y = e4m3x4(y[4] * up * inv, y[5] * up * inv, y[6] * up * inv, y[7] * up * inv);
+    }
     return r;
 }
 
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) qkv_norm_rope_append_kernel(const NormRopeParams p)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 6) qkv_norm_rope_append_kernel(const NormRopeParams p)
 {
-    constexpr int LPR = D / 8, RPW = 32 / LPR;
+    constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = kSets * RPW;
     const int lane = threadIdx.x & 31, sub = lane % LPR, d0 = 8 * sub;
-    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    const int H = p.NQ + 2 * p.NKV;
-    const int64_t rows = p.T * H;
-    const int64_t r0 = warp * (kRowSets * RPW) + lane / LPR;
+    const uint32_t job = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t per_token = p.q_jobs + 2 * p.kv_jobs;
+    const uint32_t tok = job / per_token;
+    if (tok >= p.T) return;
+    uint32_t part = job - tok * per_token;
+    const bool is_q = part < p.q_jobs, is_v = part >= p.q_jobs + p.kv_jobs;
+    if (!is_q) part -= is_v ? p.q_jobs + p.kv_jobs : p.q_jobs;
+    const int heads = is_q ? p.NQ : p.NKV;
+    const int h0 = static_cast<int>(part) * ROWS + lane / LPR;
+    const T* src = is_q ? static_cast<const T*>(p.q) + tok * p.qs
+                   : is_v ? static_cast<const T*>(p.v) + tok * p.vs
+                          : static_cast<const T*>(p.k) + tok * p.ks;
 
-    float x[kRowSets][8];
-    int64_t tok[kRowSets];
-    int head[kRowSets];
+    // (the angles wait for the position: it goes first)
+    int64_t pos = p.rd > 0 && !is_v ? load_slot(p.pos, p.pos_type, tok) : 0;
+    Raw8<T> raw[kSets];
 #pragma unroll
-    for (int i = 0; i < kRowSets; ++i) {
-        const int64_t r = r0 + i * RPW;
-        tok[i] = r < rows ? r / H : -1;
-        head[i] = static_cast<int>(r - tok[i] * H);
-        if (tok[i] >= 0) {
-            const T* src = head[i] < p.NQ ? static_cast<const T*>(p.q) + tok[i] * p.qs + head[i] * D
-                           : head[i] < p.NQ + p.NKV
-                               ? static_cast<const T*>(p.k) + tok[i] * p.ks + (head[i] - p.NQ) * D
-                               : static_cast<const T*>(p.v) + tok[i] * p.vs + (head[i] - p.NQ - p.NKV) * D;
-            load8(src + d0, x[i]);
+    for (int i = 0; i < kSets; ++i) {
+        const int h = h0 + i * RPW;
+        if (h < heads) raw[i].load(src + h * D + d0);
+        else raw[i].zero();
+    }
+    // where k and v go
+    int64_t row = -1, row_step = 0;          // cache row of head 0, from head to head
+    if (!is_q) {
+        const int64_t s = load_slot(p.slots, p.slot_type, tok);
+        if (s < 0 || s >= p.num_blocks * p.BS) return;
+        const int64_t blk = s / p.BS, off = s - blk * p.BS;
+        row = cache_row(p.layout, blk, off, 0, p.BS, p.NKV);
+        row_step = p.layout == PA_LAYOUT_BSND ? 1 : p.BS;
+    }
+    if (is_v) {
+        int tb = __ldg(p.token_batch + tok);
+        tb = tb < 0 ? 0 : (tb >= p.num_batches ? p.num_batches - 1 : tb);
+        const float* vs = p.v_scale + static_cast<int64_t>(tb) * p.NKV * D + d0;
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+            const int h = h0 + i * RPW;
+            if (h >= heads) break;
+            float x[8], sc[8], z[8];
+            raw[i].get(x);
+            load8(vs + h * D, sc);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = sc[e] == 0.0f ? 0.0f : __fdiv_rn(x[e], sc[e]);
+            uint2 c;
+            c.x = e4m3x4(z[0], z[1], z[2], z[3]);
+            c.y = e4m3x4(z[4], z[5], z[6], z[7]);
+            *reinterpret_cast<uint2*>(p.vc + (row + h * row_step) * D + d0) = c;
+        }
+        return;
+    }
+    // ---- this lane's weights and angles ----
+    const void* w = is_q ? p.qw : p.kw;
+    float wt[8];
+    if (w == nullptr) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wt[e] = 1.0f;
+    } else if (p.w_bf16) {
+        load8(static_cast<const __nv_bfloat16*>(w) + d0, wt);
+    } else {
+        load8(static_cast<const float*>(w) + d0, wt);
+    }
+    const int half = p.rd >> 1;
+    const bool rot = d0 < p.rd, low = d0 < half;
+    // channel i's partner sits rd / 16 lanes up or down (INTER: in the same lane)
+    const int from = lane + (!INTER && rot ? (low ? half >> 3 : -(half >> 3)) : 0);
+    float cs[8], sn[8];
+    if (rot) {
+        pos = pos < 0 ? 0 : (pos >= p.max_pos ? p.max_pos - 1 : pos);
+        const float* a = p.cos_sin + pos * p.rd;
+        if constexpr (INTER) {
+            const float4 c4 = __ldg(reinterpret_cast<const float4*>(a + (d0 >> 1)));
+            const float4 s4 = __ldg(reinterpret_cast<const float4*>(a + half + (d0 >> 1)));
+            cs[0] = c4.x; cs[1] = c4.y; cs[2] = c4.z; cs[3] = c4.w;
+            sn[0] = s4.x; sn[1] = s4.y; sn[2] = s4.z; sn[3] = s4.w;
         } else {
+            load8(a + (low ? d0 : d0 - half), cs);
+            load8(a + half + (low ? d0 : d0 - half), sn);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
+            for (int e = 0; e < 8; ++e) sn[e] = low ? -sn[e] : sn[e];
         }
     }
 #pragma unroll
-    for (int i = 0; i < kRowSets; ++i) {
+    for (int i = 0; i < kSets; ++i) {
         // every lane takes part in the shuffles, whatever its row is
-        const bool live = tok[i] >= 0, is_q = head[i] < p.NQ, is_v = head[i] >= p.NQ + p.NKV;
-        float ss = 0.0f;
+        const int h = h0 + i * RPW;
+        float x[8], y[8];
+        raw[i].get(x);
+        if (w != nullptr) {
+            float ss = 0.0f, sc = 1.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += x[i][e] * x[i][e];
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        // squares that leave the float range (or, with no eps to speak of, vanish
-        // below it) are taken of x * 2^-64 (2^64)
-        float sc = 1.0f;
-        const bool big = !(ss <= 1e38f), small = ss < 1e-30f && p.eps < 1e-20f;
-        if (__any_sync(0xffffffffu, big || small)) {
-            sc = big ? 0x1p-64f : (small ? 0x1p64f : 1.0f);
-            ss = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss += (x[i][e] * sc) * (x[i][e] * sc);
+            for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        }
-        float y[8];
-        const void* w = is_q ? p.qw : p.kw;
-        const bool norm = live && !is_v && w != nullptr;
-        if (norm) {
-            const float ms = ss * (1.0f / D) + p.eps * sc * sc;
-            const float inv = ms == 0.0f ? 0.0f : __fdiv_rn(1.0f, __fsqrt_rn(ms));
-            float wt[8];
-            if (p.w_bf16) load8(static_cast<const __nv_bfloat16*>(w) + d0, wt);
-            else load8(static_cast<const float*>(w) + d0, wt);
+            // squares that leave the float range (or, with no eps to speak of, vanish
+            // below it) are taken of x * 2^-64 (2^64)
+            const bool big = !(ss <= 1e38f), small = ss < 1e-30f && p.eps < 1e-20f;
+            if (__any_sync(0xffffffffu, big || small)) {
+                sc = big ? 0x1p-64f : (small ? 0x1p64f : 1.0f);
+                ss = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[i][e] * sc * inv * wt[e];
+                for (int e = 0; e < 8; ++e) ss += (x[e] * sc) * (x[e] * sc);
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            }
+            const float ms = ss * (1.0f / D) + p.eps * sc * sc;
+            const float inv = ms == 0.0f ? 0.0f : rsqrtf(ms) * sc;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = x[e] * inv * wt[e];
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[i][e];
+            for (int e = 0; e < 8; ++e) y[e] = x[e];
         }
-        if (p.rd > 0) {
-            const int half = p.rd >> 1;
-            const bool rot = live && !is_v && d0 < p.rd;
-            const float* cs = nullptr;
+        if constexpr (INTER) {
             if (rot) {
-                int64_t pos = load_slot(p.pos, p.pos_type, tok[i]);
-                pos = pos < 0 ? 0 : (pos >= p.max_pos ? p.max_pos - 1 : pos);
-                cs = p.cos_sin + pos * p.rd;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = y[2 * e], b = y[2 * e + 1];
+                    y[2 * e] = a * cs[e] - b * sn[e];
+                    y[2 * e + 1] = b * cs[e] + a * sn[e];
+                }
             }
-            if constexpr (INTER) {
-                if (rot) {
-                    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + (d0 >> 1)));
-                    const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half + (d0 >> 1)));
-                    const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+        } else if (p.rd > 0) {
+            float o[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float a = y[2 * e], b = y[2 * e + 1];
-                        y[2 * e] = a * cc[e] - b * sn[e];
-                        y[2 * e + 1] = b * cc[e] + a * sn[e];
-                    }
-                }
-            } else {
-                // channel i's partner sits rd / 16 lanes up or down
-                const int step = half >> 3;
-                const bool low = d0 < half;
-                const int from = lane + (rot ? (low ? step : -step) : 0);
-                float o[8];
+            for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, y[e], from);
+            if (rot) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, y[e], from);
-                if (rot) {
-                    const int j = low ? d0 : d0 - half;
-                    float c[8], s[8];
-                    load8(cs + j, c);
-                    load8(cs + half + j, s);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = y[e] * c[e] + (low ? -o[e] : o[e]) * s[e];
-                }
+                for (int e = 0; e < 8; ++e) y[e] = y[e] * cs[e] + o[e] * sn[e];
             }
         }
         float amax = 0.0f;
@@ -192,31 +260,17 @@ __global__ void __launch_bounds__(kThreads) qkv_norm_rope_append_kernel(const No
         for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (!live) continue;
+        if (h >= heads) continue;
+        const uint2 code = encode8(y, amax);
+        const float scale = __fdiv_rn(amax, kE4M3Max);
         if (is_q) {
-            const int64_t row = tok[i] * p.NQ + head[i];
-            *reinterpret_cast<uint2*>(p.q_codes + row * D + d0) = encode8(y, amax);
-            if (sub == 0) p.q_scale[row] = __fdiv_rn(amax, kE4M3Max);
-            continue;
-        }
-        const int64_t s = load_slot(p.slots, p.slot_type, tok[i]);
-        if (s < 0 || s >= p.num_blocks * p.BS) continue;
-        const int h = head[i] - p.NQ - (is_v ? p.NKV : 0);
-        const int64_t row = cache_row(p.layout, s / p.BS, s % p.BS, h, p.BS, p.NKV);
-        if (!is_v) {
-            *reinterpret_cast<uint2*>(p.kc + row * D + d0) = encode8(y, amax);
-            if (sub == 0) p.k_scale[row] = __fdiv_rn(amax, kE4M3Max);
+            const int64_t r = static_cast<int64_t>(tok) * p.NQ + h;
+            *reinterpret_cast<uint2*>(p.q_codes + r * D + d0) = code;
+            if (sub == 0) p.q_scale[r] = scale;
         } else {
-            int tb = __ldg(p.token_batch + tok[i]);
-            tb = tb < 0 ? 0 : (tb >= p.num_batches ? p.num_batches - 1 : tb);
-            float sc[8], z[8];
-            load8(p.v_scale + (static_cast<int64_t>(tb) * p.NKV + h) * D + d0, sc);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = sc[e] == 0.0f ? 0.0f : __fdiv_rn(y[e], sc[e]);
-            uint2 c;
-            c.x = e4m3x4(z[0], z[1], z[2], z[3]);
-            c.y = e4m3x4(z[4], z[5], z[6], z[7]);
-            *reinterpret_cast<uint2*>(p.vc + row * D + d0) = c;
+            const int64_t r = row + h * row_step;
+            *reinterpret_cast<uint2*>(p.kc + r * D + d0) = code;
+            if (sub == 0) p.k_scale[r] = scale;
         }
     }
 }
@@ -224,11 +278,13 @@ __global__ void __launch_bounds__(kThreads) qkv_norm_rope_append_kernel(const No
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 template <typename T, int D>
-void launch(const NormRopeParams& p, bool inter, cudaStream_t st)
+void launch(NormRopeParams p, bool inter, cudaStream_t st)
 {
-    constexpr int per_block = kThreads / 32 * kRowSets * (32 / (D / 8));
-    const int64_t rows = p.T * (p.NQ + 2 * p.NKV);
-    const unsigned grid = static_cast<unsigned>((rows + per_block - 1) / per_block);
+    constexpr uint32_t rows = kSets * (32 / (D / 8));        // rows a warp takes
+    p.q_jobs = (p.NQ + rows - 1) / rows;
+    p.kv_jobs = (p.NKV + rows - 1) / rows;
+    constexpr int warps = kThreads / 32;
+    const unsigned grid = static_cast<unsigned>((p.T * (p.q_jobs + 2 * p.kv_jobs) + warps - 1) / warps);
     if (inter) qkv_norm_rope_append_kernel<T, D, true><<<grid, kThreads, 0, st>>>(p);
     else qkv_norm_rope_append_kernel<T, D, false><<<grid, kThreads, 0, st>>>(p);
 }
@@ -289,7 +345,7 @@ extern "C" pa_status pa_fp8_qkv_norm_rope_append(
                    aligned(v_scale, 16) && aligned(q_codes, 8) && aligned(key_cache, 8) &&
                    aligned(value_cache, 8) && aligned(q_scale, 4) && aligned(key_scale_cache, 4),
                PA_ERR_INVALID, "%s: misaligned pointer", name);
-    PA_REQUIRE(num_tokens * (static_cast<int64_t>(NQ) + 2 * NKV) <= (static_cast<int64_t>(1) << 32),
+    PA_REQUIRE(num_tokens <= 0x7FFFFFFF && num_tokens * (static_cast<int64_t>(NQ) + 2 * NKV) < (static_cast<int64_t>(1) << 32),
                PA_ERR_UNSUPPORTED, "%s: more than 2^32 head rows", name);
     if (num_tokens == 0) return PA_OK;
     NormRopeParams p;

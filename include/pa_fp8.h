@@ -633,7 +633,8 @@ PA_API pa_status pa_tree_verify(const float* target_probs, const float* draft_pr
  * other positions hold stays. A move is skipped where path[b][i] is outside
  * [0, n) or one of its two positions has a block id outside [0, num_blocks)
  * or lies past the block table.
- * head_size    a multiple of 16; caches 16-byte aligned. S1 at most 1024.
+ * head_size    a multiple of 16 up to 8192; caches 16-byte aligned. S1 at most
+ *              1024.
  * new_act_seqs int32 [B], not kv_act_seqs itself.
  * ------------------------------------------------------------------------ */
 PA_API pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache,

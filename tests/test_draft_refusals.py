@@ -104,7 +104,7 @@ def test_keep_path_refusals(L):
     for bad in (dict(B=-1), dict(S1=0), dict(NKV=0), dict(D=0), dict(BS=0), dict(NB=0), dict(MB=0), dict(layout=9),
                 dict(new=fake), dict(kc=P(fake.value + 8))):
         assert call(**bad) == 2, bad
-    for bad in (dict(D=24), dict(S1=1025)):
+    for bad in (dict(D=24), dict(D=8208), dict(S1=1025)):
         assert call(**bad) == 5, bad
 
 
