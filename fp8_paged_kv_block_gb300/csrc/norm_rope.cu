@@ -86,10 +86,10 @@ struct Raw8<float> {
         b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float (&x)[8]) const
+    __device__ __forceinline__ void get(float2 (&x)[4]) const
     {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        x[0] = make_float2(a.x, a.y); x[1] = make_float2(a.z, a.w);
+        x[2] = make_float2(b.x, b.y); x[3] = make_float2(b.z, b.w);
     }
 };
 template <>
@@ -97,26 +97,29 @@ struct Raw8<__nv_bfloat16> {
     uint4 a;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void get(float (&x)[8]) const { unpack_bf16(a, x); }
+    __device__ __forceinline__ void get(float2 (&x)[4]) const
+    {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
 };
 
 // Eight codes of y * (448 / amax). Where the quotient may leave the float range
 // both sides are first taken times a power of two.
-__device__ __forceinline__ uint2 encode8(const float (&y)[8], float amax)
+__device__ __forceinline__ uint2 encode8(float2 (&y)[4], float amax)
 {
-    const float up = amax < 0x1p-100f ? 0x1p100f : (amax > 0x1p100f ? 0x1p-100f : 1.0f);
-    const float inv = __fdividef(kE4M3Max, amax * up);
-    uint2 r;
-    if (amax == 0.0f) {
-        r = make_uint2(0u, 0u);
-    } else if (up == 1.0f) {
-        r.x = e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-        r.y = e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
-    } else {
-        r.x = e4m3x4(y[0] * up * inv, y[1] * up * inv, y[2] * up * inv, y[3] * up * inv);
-        r.y = e4m3x4(y[4] * up * inv, y[5] * up * inv, y[6] * up * inv, y[7] * up * inv);
+    if (!(amax >= 0x1p-100f && amax <= 0x1p100f)) {
+        if (amax == 0.0f) return make_uint2(0u, 0u);
+        const float up = amax < 1.0f ? 0x1p100f : 0x1p-100f;
+        amax *= up;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(y[e], make_float2(up, up));
     }
-    return r;
+    const float inv = __fdividef(kE4M3Max, amax);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(y[e], make_float2(inv, inv));
+    return make_uint2(e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y), e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y));
 }
 
 template <typename T, int D, bool INTER>
@@ -163,11 +166,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 6) qkv_norm_rop
         for (int i = 0; i < kSets; ++i) {
             const int h = h0 + i * RPW;
             if (h >= heads) break;
-            float x[8], sc[8], z[8];
+            float2 x[4];
+            float sc[8], z[8];
             raw[i].get(x);
             load8(vs + h * D, sc);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = sc[e] == 0.0f ? 0.0f : __fdiv_rn(x[e], sc[e]);
+            for (int e = 0; e < 8; ++e)
+                z[e] = sc[e] == 0.0f ? 0.0f : __fdiv_rn((e & 1) ? x[e >> 1].y : x[e >> 1].x, sc[e]);
             uint2 c;
             c.x = e4m3x4(z[0], z[1], z[2], z[3]);
             c.y = e4m3x4(z[4], z[5], z[6], z[7]);
@@ -177,45 +182,61 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 6) qkv_norm_rop
     }
     // ---- this lane's weights and angles ----
     const void* w = is_q ? p.qw : p.kw;
-    float wt[8];
-    if (w == nullptr) {
+    float2 wt[4];
+    {
+        float t[8];
+        if (w == nullptr) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wt[e] = 1.0f;
-    } else if (p.w_bf16) {
-        load8(static_cast<const __nv_bfloat16*>(w) + d0, wt);
-    } else {
-        load8(static_cast<const float*>(w) + d0, wt);
+            for (int e = 0; e < 8; ++e) t[e] = 1.0f;
+        } else if (p.w_bf16) {
+            load8(static_cast<const __nv_bfloat16*>(w) + d0, t);
+        } else {
+            load8(static_cast<const float*>(w) + d0, t);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wt[e] = make_float2(t[2 * e], t[2 * e + 1]);
     }
     const int half = p.rd >> 1;
     const bool rot = d0 < p.rd, low = d0 < half;
     // channel i's partner sits rd / 16 lanes up or down (INTER: in the same lane)
     const int from = lane + (!INTER && rot ? (low ? half >> 3 : -(half >> 3)) : 0);
-    float cs[8], sn[8];
+    float2 cs[4], sn[4];                     // per channel (INTER: a pair's in both)
     if (rot) {
         pos = pos < 0 ? 0 : (pos >= p.max_pos ? p.max_pos - 1 : pos);
         const float* a = p.cos_sin + pos * p.rd;
         if constexpr (INTER) {
             const float4 c4 = __ldg(reinterpret_cast<const float4*>(a + (d0 >> 1)));
             const float4 s4 = __ldg(reinterpret_cast<const float4*>(a + half + (d0 >> 1)));
-            cs[0] = c4.x; cs[1] = c4.y; cs[2] = c4.z; cs[3] = c4.w;
-            sn[0] = s4.x; sn[1] = s4.y; sn[2] = s4.z; sn[3] = s4.w;
+            cs[0] = make_float2(c4.x, c4.x); cs[1] = make_float2(c4.y, c4.y);
+            cs[2] = make_float2(c4.z, c4.z); cs[3] = make_float2(c4.w, c4.w);
+            sn[0] = make_float2(-s4.x, s4.x); sn[1] = make_float2(-s4.y, s4.y);
+            sn[2] = make_float2(-s4.z, s4.z); sn[3] = make_float2(-s4.w, s4.w);
         } else {
-            load8(a + (low ? d0 : d0 - half), cs);
-            load8(a + half + (low ? d0 : d0 - half), sn);
+            float t[8];
+            load8(a + (low ? d0 : d0 - half), t);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sn[e] = low ? -sn[e] : sn[e];
+            for (int e = 0; e < 4; ++e) cs[e] = make_float2(t[2 * e], t[2 * e + 1]);
+            load8(a + half + (low ? d0 : d0 - half), t);
+            const float sign = low ? -1.0f : 1.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sn[e] = make_float2(sign * t[2 * e], sign * t[2 * e + 1]);
         }
     }
+    // this lane's 8 codes of head h0, and from one set to the next
+    uint8_t* dst = is_q ? p.q_codes + (static_cast<int64_t>(tok) * p.NQ + h0) * D + d0
+                        : p.kc + (row + h0 * row_step) * D + d0;
+    const int64_t dst_step = (is_q ? RPW : RPW * row_step) * D;
+    float mine = 0.0f;                       // max|y| of the row whose scale this lane writes
 #pragma unroll
-    for (int i = 0; i < kSets; ++i) {
+    for (int i = 0; i < kSets; ++i, dst += dst_step) {
         // every lane takes part in the shuffles, whatever its row is
-        const int h = h0 + i * RPW;
-        float x[8], y[8];
-        raw[i].get(x);
+        float2 y[4];
+        raw[i].get(y);
         if (w != nullptr) {
-            float ss = 0.0f, sc = 1.0f;
+            float2 s2 = __fmul2_rn(y[0], y[0]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+            for (int e = 1; e < 4; ++e) s2 = __ffma2_rn(y[e], y[e], s2);
+            float ss = s2.x + s2.y, sc = 1.0f;
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             // squares that leave the float range (or, with no eps to speak of, vanish
@@ -225,54 +246,47 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 6) qkv_norm_rop
                 sc = big ? 0x1p-64f : (small ? 0x1p64f : 1.0f);
                 ss = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss += (x[e] * sc) * (x[e] * sc);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 t = __fmul2_rn(y[e], make_float2(sc, sc));
+                    ss += t.x * t.x + t.y * t.y;
+                }
 #pragma unroll
                 for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             }
             const float ms = ss * (1.0f / D) + p.eps * sc * sc;
             const float inv = ms == 0.0f ? 0.0f : rsqrtf(ms) * sc;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e] * inv * wt[e];
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e];
+            for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(__fmul2_rn(y[e], make_float2(inv, inv)), wt[e]);
         }
-        if constexpr (INTER) {
-            if (rot) {
+        if (INTER || p.rd > 0) {
+            float2 o[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float a = y[2 * e], b = y[2 * e + 1];
-                    y[2 * e] = a * cs[e] - b * sn[e];
-                    y[2 * e + 1] = b * cs[e] + a * sn[e];
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (INTER) {
+                    o[e] = make_float2(y[e].y, y[e].x);
+                } else {
+                    o[e].x = __shfl_sync(0xffffffffu, y[e].x, from);
+                    o[e].y = __shfl_sync(0xffffffffu, y[e].y, from);
                 }
             }
-        } else if (p.rd > 0) {
-            float o[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, y[e], from);
             if (rot) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = y[e] * cs[e] + o[e] * sn[e];
+                for (int e = 0; e < 4; ++e) y[e] = __ffma2_rn(o[e], sn[e], __fmul2_rn(y[e], cs[e]));
             }
         }
         float amax = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
+        for (int e = 0; e < 4; ++e) amax = fmaxf(fmaxf(amax, fabsf(y[e].x)), fabsf(y[e].y));
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (h >= heads) continue;
-        const uint2 code = encode8(y, amax);
-        const float scale = __fdiv_rn(amax, kE4M3Max);
-        if (is_q) {
-            const int64_t r = static_cast<int64_t>(tok) * p.NQ + h;
-            *reinterpret_cast<uint2*>(p.q_codes + r * D + d0) = code;
-            if (sub == 0) p.q_scale[r] = scale;
-        } else {
-            const int64_t r = row + h * row_step;
-            *reinterpret_cast<uint2*>(p.kc + r * D + d0) = code;
-            if (sub == 0) p.k_scale[r] = scale;
-        }
+        mine = sub == i ? amax : mine;
+        if (h0 + i * RPW < heads) *reinterpret_cast<uint2*>(dst) = encode8(y, amax);
     }
+    // the scales of all rows at once: lane i of a row's lanes has set i's
+    const int h = h0 + sub * RPW;
+    if (sub < kSets && h < heads)
+        (is_q ? p.q_scale + static_cast<int64_t>(tok) * p.NQ + h : p.k_scale + row + h * row_step)[0] =
+            __fdiv_rn(mine, kE4M3Max);
 }
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
