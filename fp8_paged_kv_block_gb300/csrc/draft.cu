@@ -73,13 +73,12 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v)
 }
 
 struct VerifySmem {
-    unsigned long long wsum[2][kVWarps];     // this CTA's segments, by pass parity
-    unsigned long long all[kMaxSegs];        // the cluster's
-    // then, S1 long each: p and q at a node's token, u, parent, token, the z's
+    unsigned long long all[2][kMaxSegs];     // the cluster's segments' sums, by pass parity
+    // then, S1 long each: p and q at a node's token, u, the z's (two sets), parent, token
 };
 
 template <bool VEC>
-__global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyParams a)
+__global__ void __launch_bounds__(kVThreads, 3) tree_verify_kernel(const VerifyParams a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     VerifySmem& sm = *reinterpret_cast<VerifySmem*>(raw);
@@ -87,7 +86,7 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyPara
     float* const q0 = p0 + a.S1;
     float* const un = q0 + a.S1;
     float* const zs = un + a.S1;
-    int* const par = reinterpret_cast<int*>(zs + a.S1);
+    int* const par = reinterpret_cast<int*>(zs + 2 * a.S1);
     int* const tok = par + a.S1;
     cg::cluster_group cl = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -104,6 +103,8 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyPara
         }
         return;
     }
+    // (no CTA writes into another's shared memory before that one has started)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const float* pb = a.p + b * a.S1 * a.V;
     const float* qb = a.q ? a.q + b * a.S1 * a.V : nullptr;
     for (int s = tid; s < n; s += kVThreads) {
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyPara
         q0[s] = ok ? (qb ? __ldg(qb + at) : 1.0f) : 0.0f;
     }
     __syncthreads();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 
     // this warp's segment [lo, hi) of the vocabulary
     const int segs = ctas * kVWarps, mine = rank * kVWarps + warp;
@@ -124,9 +126,14 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyPara
     const float* prow = pb;
     const float* qrow = qb;
     int cur = 0, acc = 1, rej = 0;           // current node, nodes accepted, drafts of cur rejected so far
+    // The z's of cur's rejections. Every thread writes them, all the same, so that no
+    // barrier is needed before they are read; a node's first takes the set that the
+    // last node with rejections did not, as a slower warp may still be there (it has
+    // passed that node's own cluster barrier, so no more than one set behind).
+    float* zc = zs + a.S1;
     // R after `rej` rejections of drawn drafts, from p and q
     auto rest = [&](float r, float q) {
-        for (int k = 0; k < rej; ++k) r = fmaxf(__fsub_rn(r, __fmul_rn(zs[k], q)), 0.0f);
+        for (int k = 0; k < rej; ++k) r = fmaxf(__fsub_rn(r, __fmul_rn(zc[k], q)), 0.0f);
         return r;
     };
     // R's weights summed over all of the vocabulary, and each segment's into sm.all
@@ -140,7 +147,7 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyPara
                 if (replay) {
                     const float4 q = __ldg(reinterpret_cast<const float4*>(qrow + i));
                     for (int k = 0; k < rej; ++k) {
-                        const float z = zs[k];
+                        const float z = zc[k];
                         r.x = fmaxf(__fsub_rn(r.x, __fmul_rn(z, q.x)), 0.0f);
                         r.y = fmaxf(__fsub_rn(r.y, __fmul_rn(z, q.y)), 0.0f);
                         r.z = fmaxf(__fsub_rn(r.z, __fmul_rn(z, q.z)), 0.0f);
@@ -163,26 +170,20 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyPara
             }
         }
         if (!replay && !qb && rej > 0) {
-            // tokens of cur's children, all of them rejected, are out
-            for (int t = cur + 1; t < n; ++t) {
-                if (par[t] != cur || tok[t] < lo || tok[t] >= hi) continue;
-                bool again = false;
-                for (int e = cur + 1; e < t; ++e) again = again || (par[e] == cur && tok[e] == tok[t]);
-                if (!again && lane == 0) w -= weight(p0[t]);
-            }
+            // tokens of cur's children, all of them rejected, are out (a repeated one
+            // has p0 0)
+            for (int t = cur + 1; t < n; ++t)
+                if (lane == 0 && par[t] == cur && tok[t] >= lo && tok[t] < hi) w -= weight(p0[t]);
         }
         w = warp_sum(w);
-        // (two sets: a CTA may be a pass ahead of one that still reads)
-        if (lane == 0) sm.wsum[pass & 1][warp] = w;
+        // to every CTA of the cluster. (Two sets: a CTA may be a pass ahead of one that
+        // still reads, and not more.)
+        if (lane < ctas) *cl.map_shared_rank(&sm.all[pass & 1][mine], lane) = w;
         cl.sync();
-        if (tid < segs) sm.all[tid] = cl.map_shared_rank(sm.wsum[pass & 1], tid / kVWarps)[tid % kVWarps];
-        __syncthreads();
-        ++pass;
         unsigned long long z = 0;
-        for (int i = lane; i < segs; i += 32) z += sm.all[i];
-        z = warp_sum(z);
-        __syncthreads();                     // sm.all is read before the next pass writes it
-        return z;
+        for (int i = lane; i < segs; i += 32) z += sm.all[pass & 1][i];
+        ++pass;
+        return warp_sum(z);
     };
 
     double z = 1.0;
@@ -195,9 +196,11 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyPara
         if (qb) {
             rx = static_cast<double>(rest(p0[s], q0[s]));
         } else {
-            rx = static_cast<double>(p0[s]);
+            // rejected before: R(x) is 0 (every thread notes it, all the same)
             for (int t = cur + 1; t < s; ++t)
-                if (par[t] == cur && tok[t] == x) rx = 0.0;   // rejected before: R(x) is 0
+                if (par[t] == cur && tok[t] == x) p0[s] = 0.0f;
+            __syncwarp();
+            rx = static_cast<double>(p0[s]);
         }
         if (static_cast<double>(un[s]) * z * static_cast<double>(q0[s]) < rx) {
             if (rank == 0 && tid == 0) {
@@ -212,9 +215,9 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyPara
             prow = pb + static_cast<int64_t>(cur) * a.V;
             if (qb) qrow = qb + static_cast<int64_t>(cur) * a.V;
         } else if (qb) {
-            __syncthreads();                 // (a thread may still be at an earlier test's z's)
-            if (tid == 0) zs[rej] = static_cast<float>(z);
-            __syncthreads();
+            if (rej == 0) zc = zc == zs ? zs + a.S1 : zs;
+            zc[rej] = static_cast<float>(z);
+            __syncwarp();
             ++rej;
             Z = sums(true);
             summed = true;
@@ -241,22 +244,24 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyPara
         for (int i = acc + tid; i < a.S1; i += kVThreads) path[i] = tokens[i] = -1;
     }
     if (Z != 0) {
+        const unsigned long long* all = sm.all[(pass - 1) & 1];
         const float u0 = un[0];
         unsigned long long t = u0 > 0.0f ? static_cast<unsigned long long>(static_cast<double>(u0) * static_cast<double>(Z)) : 0ull;
         if (t >= Z) t = Z - 1;
         unsigned long long before = 0;
-        for (int i = lane; i < mine; i += 32) before += sm.all[i];
+        for (int i = lane; i < mine; i += 32) before += all[i];
         before = warp_sum(before);
-        if (t >= before && t - before < sm.all[mine]) {
+        if (t >= before && t - before < all[mine]) {
             auto weight_at = [&](int i) -> unsigned long long {
-                float r = __ldg(prow + i);
-                if (qb) {
-                    if (rej > 0) r = rest(r, __ldg(qrow + i));
-                } else if (!all_of_p) {
-                    for (int e = cur + 1; e < n; ++e)
-                        if (par[e] == cur && tok[e] == i) r = 0.0f;
-                }
-                return weight(r);
+                const float r = __ldg(prow + i);
+                return weight(qb && rej > 0 ? rest(r, __ldg(qrow + i)) : r);
+            };
+            // the weights of cur's rejected tokens in [from, to) (given drafts only)
+            auto out = [&](int from, int to) {
+                unsigned long long w = 0;
+                for (int e = cur + 1; e < n && !qb && !all_of_p; ++e)
+                    if (par[e] == cur && tok[e] >= from && tok[e] < to) w += weight(p0[e]);
+                return w;
             };
             auto scan = [&](unsigned long long c) {
 #pragma unroll
@@ -272,12 +277,14 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyPara
             unsigned long long c = 0;
 #pragma unroll 8
             for (int i = l0; i < l1; ++i) c += weight_at(i);
+            c -= out(l0, l1);
             const unsigned long long upto = scan(c);
             const int at = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, before + upto > t))) - 1;
             before += __shfl_sync(0xffffffffu, upto - c, at);
             const int end = __shfl_sync(0xffffffffu, l1, at);
             for (int i0 = __shfl_sync(0xffffffffu, l0, at); i0 < end; i0 += 32) {
-                const unsigned long long v = scan(i0 + lane < end ? weight_at(i0 + lane) : 0ull);
+                const int i = i0 + lane;
+                const unsigned long long v = scan(i < end ? weight_at(i) - out(i, i + 1) : 0ull);
                 const unsigned hit = __ballot_sync(0xffffffffu, before + v > t);
                 if (hit) {
                     if (lane == 0) tokens[acc - 1] = i0 + __ffs(static_cast<int>(hit)) - 1;
@@ -287,7 +294,6 @@ __global__ void __launch_bounds__(kVThreads) tree_verify_kernel(const VerifyPara
             }
         }
     }
-    cl.sync();                               // no CTA leaves while another reads its sums
 }
 
 // ---- the accepted branch in the cache ------------------------------------------------
@@ -421,7 +427,7 @@ extern "C" pa_status pa_tree_verify(const float* target_probs, const float* draf
     // segments of whole 128-value steps
     const int segs = cluster * kVWarps;
     a.seg = (V + segs * 128 - 1) / (segs * 128) * 128;
-    const size_t smem = sizeof(VerifySmem) + static_cast<size_t>(S1) * 6 * sizeof(float);
+    const size_t smem = sizeof(VerifySmem) + static_cast<size_t>(S1) * 7 * sizeof(float);
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(static_cast<unsigned>(B) * cluster);
     lc.blockDim = dim3(kVThreads);
