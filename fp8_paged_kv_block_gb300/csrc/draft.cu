@@ -24,8 +24,11 @@ constexpr int kMaxNodes = 1024;
 // Bound by the rows of p and q read (one or two of V floats per sequence, again
 // from L2 for each further rejection) on large batches, by the chain launch,
 // gather, row, cluster barrier on small ones.
-// A sequence gets 8 CTAs while the batch's CTAs all fit on the GPU (kResident),
-// half as many for twice the batch.
+// A sequence gets 8 CTAs while the batch's CTAs number at most kResident, half as
+// many for twice the batch: more CTAs shorten the pass over a row, and cost
+// launches and cluster barriers once they no longer all run at once. kResident
+// 304, 608, 1216: 53, 44, 44 us on 64 sequences of 16 nodes x 131072, 97, 65, 68
+// on 128 of them; 61, 46, 49 us on 256 of 5 x 50000, 44, 36, 42 on 128.
 constexpr int kVThreads = 512;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kMaxCluster = 8;
@@ -400,7 +403,8 @@ extern "C" pa_status pa_tree_verify(const float* target_probs, const float* draf
                                     const float* uniforms, const int32_t* tree_len, int B, int S1, int V,
                                     int32_t* accepted, int32_t* path, int32_t* tokens, void* stream)
 {
-    PA_REQUIRE(target_probs && draft_tokens && parents && uniforms && accepted && path && tokens,
+    // (tensors of no sequences may have no address)
+    PA_REQUIRE(B == 0 || (target_probs && draft_tokens && parents && uniforms && accepted && path && tokens),
                PA_ERR_NULLPTR, "pa_tree_verify: NULL tensor pointer");
     PA_REQUIRE(B >= 0 && S1 > 0 && V > 0, PA_ERR_INVALID, "pa_tree_verify: empty or negative size");
     PA_REQUIRE(S1 <= kMaxNodes, PA_ERR_UNSUPPORTED, "pa_tree_verify: S1 %d > %d", S1, kMaxNodes);
@@ -456,8 +460,8 @@ extern "C" pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache, 
                                             int max_blocks_per_seq, int layout, void* stream)
 {
     const char* name = "pa_fp8_cache_keep_path";
-    PA_REQUIRE(key_cache && value_cache && key_scale_cache && block_table && kv_act_seqs && path &&
-                   accepted && new_act_seqs,
+    PA_REQUIRE(key_cache && value_cache && key_scale_cache &&
+                   (B == 0 || (block_table && kv_act_seqs && path && accepted && new_act_seqs)),
                PA_ERR_NULLPTR, "%s: NULL tensor pointer", name);
     PA_REQUIRE(B >= 0 && S1 > 0 && NKV > 0 && head_size > 0 && block_size > 0 && num_blocks > 0 &&
                    max_blocks_per_seq > 0,
@@ -468,7 +472,7 @@ extern "C" pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache, 
     PA_REQUIRE(head_size % 16 == 0 && head_size <= 8192, PA_ERR_UNSUPPORTED,
                "%s: head_size %d (a multiple of 16 up to 8192)", name, head_size);
     static_assert(2 * 2 * 8192 / 16 <= kKThreads * kKBatch, "a row of two heads fits a round");
-    PA_REQUIRE(new_act_seqs != kv_act_seqs, PA_ERR_INVALID,
+    PA_REQUIRE(B == 0 || new_act_seqs != kv_act_seqs, PA_ERR_INVALID,
                "%s: new_act_seqs must be another buffer than kv_act_seqs", name);
     PA_REQUIRE(aligned(key_cache, 16) && aligned(value_cache, 16) && aligned(key_scale_cache, 4), PA_ERR_INVALID,
                "%s: misaligned pointer", name);

@@ -326,8 +326,9 @@ extern "C" pa_status pa_fp8_qkv_norm_rope_append(
     int NKV, int head_size, int64_t num_blocks, int block_size, int layout, void* stream)
 {
     const char* name = "pa_fp8_qkv_norm_rope_append";
-    PA_REQUIRE(q && k && v && q_codes && q_scale && key_cache && value_cache && slot_mapping &&
-                   key_scale_cache && v_scale && token_batch,
+    // (tensors of no tokens may have no address)
+    PA_REQUIRE(key_cache && value_cache && key_scale_cache && v_scale &&
+                   (num_tokens == 0 || (q && k && v && q_codes && q_scale && slot_mapping && token_batch)),
                PA_ERR_NULLPTR, "%s: NULL tensor pointer", name);
     PA_REQUIRE(num_tokens >= 0 && NQ > 0 && NKV > 0 && head_size > 0 && num_blocks > 0 &&
                    block_size > 0 && num_batches > 0,
@@ -338,7 +339,7 @@ extern "C" pa_status pa_fp8_qkv_norm_rope_append(
                "%s: rotary_dim %d outside [0, head_size]", name, rotary_dim);
     PA_REQUIRE(rotary_dim % (interleaved ? 8 : 16) == 0, PA_ERR_UNSUPPORTED,
                "%s: rotary_dim %d (a multiple of 16, or of 8 if interleaved)", name, rotary_dim);
-    PA_REQUIRE(rotary_dim == 0 || (cos_sin && positions), PA_ERR_NULLPTR,
+    PA_REQUIRE(rotary_dim == 0 || (cos_sin && (positions || num_tokens == 0)), PA_ERR_NULLPTR,
                "%s: NULL cos_sin or positions", name);
     PA_REQUIRE(rotary_dim == 0 || max_position > 0, PA_ERR_INVALID, "%s: empty cos_sin", name);
     PA_REQUIRE(in_dtype == PA_DTYPE_F32 || in_dtype == PA_DTYPE_BF16, PA_ERR_INVALID,

@@ -5,7 +5,7 @@
 // to the drafted tokens its mask row names. Rows are taken in items of at most
 // 128, one tensor tile.
 //
-//   S = Q_fp8 K_fp8^T                 tcgen05 kind::f8f6f4, 128 rows x 64 keys
+//   S = Q_fp8 K_fp8^T                 tcgen05 kind::f8f6f4, 128 rows x 128 keys
 //   x = S k_scale q_scale scale log2e, -inf where the row does not see the key
 //   P = 2^(x - m + 7), L += sum P     one thread per row, FP32
 //   O += FP16(P) V                    tcgen05 kind::f16, P from tensor memory
@@ -14,22 +14,25 @@
 // P enters the second contraction as FP16 (half a step: 2^-11) and V as the
 // FP16 values of its E4M3 codes, which are exact: P in E4M3 as in
 // pa_fp8_decode would be off by up to 2^-4 where few keys count. The reference
-// m is the running maximum, but raised only when a half block's maximum lies
+// m is the running maximum, but raised only when a block's maximum lies
 // more than 2^8 above it, which spares O's rescaling in tensor memory on most;
 // P then stays below 2^15, inside FP16, and a key 2^31 below the maximum still
 // counts.
 //
-// What bounds it is the chain from one tensor instruction to the next: a batch
-// of MMAs and its commit take about 1000 clocks from the wake-up of the issuing
-// warp to that of the waiting one, a half block's softmax as long again. So
-// many half blocks are in flight: tensor memory holds O (128 columns), four S
-// (64 each) and four P (32 each); S is issued up to four half blocks ahead, and
-// two softmax warpgroups take even and odd halves. They share m, row by row: a
-// warp decides on m for its half after the other warpgroup's warp has decided on
-// the half before, and only the exponentials wait for that.
-//   warps 0-3, 4-7   softmax of even, odd half blocks (thread = row = tensor lane)
+// What bounds it short of HBM is the chain from one tensor instruction to the
+// next: a batch of MMAs and its commit take about 1000 clocks from the wake-up of
+// the issuing warp to that of the waiting one, and each hand-over between warps
+// another 50 to 100. So steps are large (a block of 128 keys, whose scores a
+// thread holds in registers) and overlap: two softmax warpgroups take blocks in
+// turn, each with an S and a P buffer of its own (tensor memory: O 128 columns, S
+// 2 x 128, P 2 x 64), and S of a warpgroup's next block is computed while it works
+// on the last. They share m, row by row: a warp decides on m for its block after
+// the other warpgroup's warp has decided on the block before, and only the
+// exponentials wait for that.
+//   warps 0-7        softmax, warpgroup k of blocks k, k + 2, .. (thread = row =
+//                    tensor memory lane)
 //   warp 8           K and V blocks by TMA, key scales by cp.async
-//   warp 9, warp 10  issue S, issue P V
+//   warps 9, 10      issue S, issue P V
 //   warp 11          Q rows and scales of the next segment; tells the joining
 //                    kernel about the item at the run's begin
 //   warps 12-15      V codes to FP16 in shared memory, zeros behind the end
@@ -57,23 +60,29 @@ constexpr int kMaxCtas = 192;
 constexpr int kItemRows = 128;
 constexpr int kTile = kBS * kD;              // bytes of a block of codes
 // K blocks, V blocks as codes and as FP16, key scales. The scales' ring needs no
-// barrier that says a slot is free: block i + 6 is requested once K block i + 3
-// is free, i.e. S of its halves, 2 i + 6 and 2 i + 7, is complete; those were
-// issued after halves 2 i + 2 and 2 i + 3 had left their S buffers, and so after
-// both warpgroups were done with block i.
-constexpr int kKStages = 3, kVStages = 3, kHStages = 2, kSStages = 6;
-constexpr int kProdWarp = 8, kMmaWarp = 9, kQWarp = 11, kConvWarp = 12, kConvWarps = 4;
-// Registers: 512 threads start with 128 each; the softmax warpgroups, which
-// hold a row's 128 scores, go up to 184 and the other two down to 72 (256 x
-// 184 + 256 x 72 = 512 x 128).
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+// barrier that says a slot is free: block i + 8 is requested once K block i + 4
+// is free, i.e. its S complete; that was issued after block i + 2's had left its
+// S buffer, and so after its warpgroup was done with block i.
+constexpr int kKStages = 4, kVStages = 3, kHStages = 2, kSStages = 8;
+// Softmax warpgroups, which take blocks in turn, each with an S and a P buffer of
+// its own.
+constexpr int kTurns = 2;
+constexpr int kProdWarp = 4 * kTurns, kMmaWarp = kProdWarp + 1, kQWarp = kProdWarp + 3;
+constexpr int kConvWarp = kProdWarp + 4, kConvWarps = 4;
 constexpr int kThreads = (kConvWarp + kConvWarps) * 32;
-constexpr uint32_t kTmemCols = 512, kSCol = 128, kPCol = 384;   // O, four S, four P
+// Registers: 512 threads start with 128 each; the softmax warpgroups, which hold
+// 128 scores a thread, go up to 184 and the other two down to 72 (256 x 184 + 256
+// x 72 = 512 x 128).
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+constexpr uint32_t kTmemCols = 512, kSCol = 128, kPCol = kSCol + kTurns * kBS;   // O, then S, then P
 constexpr float kRaise = 8.0f;               // log2 units: see the top of the file
 constexpr float kShift = 7.0f;
 
-constexpr int kHalf = kBS / 2;
-constexpr int kItemCost = 4;
+// What an item costs besides its blocks, in blocks: the first S, the last P V and
+// its output, which nothing of the next item overlaps. 4, 6, 8: 143, 135, 130 us on
+// 16 sequences of up to 4096 keys (as 1 to 4096 fall out) x 64 drafted tokens x 96
+// heads over 8, 32.2, 32.8, 32.9 us with 8 drafted tokens.
+constexpr int kItemCost = 8;
 
 // What the joining kernel has to know of the item at the begin of a run.
 struct Cut {
@@ -114,16 +123,15 @@ struct TreeSmem {
     alignas(1024) uint8_t v[kVStages][kTile];
     alignas(1024) uint8_t vh[kHStages][2][kTile];   // FP16, channels 0-63 and 64-127
     alignas(1024) uint8_t q[2][kTile];              // by segment parity, as qs and vs
-    alignas(16) uint8_t stage[kProdWarp][32 * 64];
     alignas(16) float ks[kSStages][kBS];
     alignas(16) float qs[2][kItemRows];
     alignas(16) float vs[2][kD];
-    float m[kItemRows], m0[kItemRows], l[2][kItemRows];
+    float m[kItemRows], ml[2][kTurns][kItemRows];
     uint32_t cum[kMaxB + 1];                 // weights before each sequence
     uint32_t len[kMaxB];                     // length << 8 | drafted tokens
     uint64_t k_full[kSStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t h_full[kHStages], h_empty[kHStages];
-    uint64_t s_full[4], s_free[4], p_full[4], o_done[4], q_full[2], q_empty[2], drain[2];
+    uint64_t s_full[kTurns], s_free[kTurns], p_full[kTurns], o_done[kTurns], q_full[2], q_empty[2], drain[2];
     uint32_t tmem;
     int abort;
 };
@@ -263,35 +271,6 @@ __device__ __forceinline__ uint32_t codes_to_half2(uint32_t two)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Two FP32 operations in one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, w, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
-        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-
 __device__ __forceinline__ void named_bar_arrive(int id, int nthreads)
 {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
@@ -418,25 +397,28 @@ __device__ void converter(TreeSmem& sm, const TreeParams& p, Run run, int w, int
             const int vslot = c % kVStages, hslot = c % kHStages;
             wait_for(&sm.v_full[vslot], (c / kVStages) & 1, p.err, 4, &sm.abort);
             const uint8_t* src = sm.v[vslot] + from;
-            uint4 x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const uint4*>(src + 1024 * i);
             const int limit = act - t * kBS;
-            if (limit < kBS) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (key0 + 8 * i >= limit) x[i] = make_uint4(0, 0, 0, 0);
-            }
             wait_for(&sm.h_empty[hslot], ((c / kHStages) & 1) ^ 1, p.err, 8, &sm.abort);
             uint8_t* dst = sm.vh[hslot][0];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                *reinterpret_cast<uint4*>(dst + to + 1024 * i) =
-                    make_uint4(codes_to_half2(x[i].x & 0xFFFFu), codes_to_half2(x[i].x >> 16),
-                               codes_to_half2(x[i].y & 0xFFFFu), codes_to_half2(x[i].y >> 16));
-                *reinterpret_cast<uint4*>(dst + to1 + 1024 * i) =
-                    make_uint4(codes_to_half2(x[i].z & 0xFFFFu), codes_to_half2(x[i].z >> 16),
-                               codes_to_half2(x[i].w & 0xFFFFu), codes_to_half2(x[i].w >> 16));
+            for (int i0 = 0; i0 < 8; i0 += 4) {
+                uint4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(src + 1024 * (i0 + i));
+                if (limit < kBS) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (key0 + 8 * (i0 + i) >= limit) x[i] = make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    *reinterpret_cast<uint4*>(dst + to + 1024 * (i0 + i)) =
+                        make_uint4(codes_to_half2(x[i].x & 0xFFFFu), codes_to_half2(x[i].x >> 16),
+                                   codes_to_half2(x[i].y & 0xFFFFu), codes_to_half2(x[i].y >> 16));
+                    *reinterpret_cast<uint4*>(dst + to1 + 1024 * (i0 + i)) =
+                        make_uint4(codes_to_half2(x[i].z & 0xFFFFu), codes_to_half2(x[i].z >> 16),
+                                   codes_to_half2(x[i].w & 0xFFFFu), codes_to_half2(x[i].w >> 16));
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -452,7 +434,7 @@ __device__ void converter(TreeSmem& sm, const TreeParams& p, Run run, int w, int
 // issues S, as far ahead as there are K blocks and free S buffers, warp 1 P V.
 __device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w)
 {
-    constexpr uint32_t kIdescS = idesc_e4m3(128, kHalf, 0, 0);
+    constexpr uint32_t kIdescS = idesc_e4m3(128, kBS, 0, 0);
     constexpr uint32_t kIdescO = idesc_f16(128, kD, 0, 1);   // P K-major in tensor memory, V MN-major
     auto wait = [&](uint64_t* bar, int phase, int code) {
         return __all_sync(0xffffffffu, wait_for(bar, phase & 1, p.err, code, &sm.abort)) != 0;
@@ -461,42 +443,38 @@ __device__ void mma_issuer(TreeSmem& sm, const TreeParams& p, Run run, uint32_t 
     int i = 0, seg = 0;                      // blocks, segments so far
     bool ok = true;
     while (ok && next_seg(sm.cum, sm.len, p.G, run, s)) {
-        const int nh = 2 * (s.t1 - s.t0);
         if (w == 0) ok = wait(&sm.q_full[seg & 1], seg >> 1, 16);
         const uint64_t qd = smem_desc(smem_u32(sm.q[seg & 1]), 16, 1024, kSmem128BSwizzle);
 #pragma unroll 1
-        for (int h = 0; h < nh && ok; ++h) {
-            const int odd = h & 1, g = 2 * i + odd, buf = g & 3, kslot = i % kKStages, hslot = i % kHStages;
+        for (int t = s.t0; t < s.t1 && ok; ++t, ++i) {
+            const int buf = i % kTurns, turn = i / kTurns, kslot = i % kKStages, hslot = i % kHStages;
             if (w == 0)
-                ok = (odd || wait(&sm.k_full[i % kSStages], i / kSStages, 16)) &&
-                     (g < 4 || wait(&sm.s_free[buf], (g - 4) >> 2, 32));
+                ok = wait(&sm.k_full[i % kSStages], i / kSStages, 16) &&
+                     (turn == 0 || wait(&sm.s_free[buf], turn - 1, 32));
             else
-                ok = (odd || wait(&sm.h_full[hslot], i / kHStages, 32)) && wait(&sm.p_full[buf], g >> 2, 32);
+                ok = wait(&sm.h_full[hslot], i / kHStages, 32) && wait(&sm.p_full[buf], turn, 32);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
                 if (w == 0) {
-                    const uint64_t kd =
-                        smem_desc(smem_u32(sm.k[kslot]) + odd * (kHalf * kD), 16, 1024, kSmem128BSwizzle);
+                    const uint64_t kd = smem_desc(smem_u32(sm.k[kslot]), 16, 1024, kSmem128BSwizzle);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_e4m3(tmem + kSCol + kHalf * buf, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
+                        umma_e4m3(tmem + kSCol + kBS * buf, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
                     umma_commit(&sm.s_full[buf]);
-                    if (odd) umma_commit(&sm.k_empty[kslot]);
-                    if (h + 1 == nh) umma_commit(&sm.q_empty[seg & 1]);
+                    umma_commit(&sm.k_empty[kslot]);
+                    if (t + 1 == s.t1) umma_commit(&sm.q_empty[seg & 1]);
                 } else {
-                    const uint64_t vd =
-                        smem_desc(smem_u32(sm.vh[hslot][0]) + odd * (kHalf * 128), kTile, 1024, kSmem128BSwizzle);
+                    const uint64_t vd = smem_desc(smem_u32(sm.vh[hslot][0]), kTile, 1024, kSmem128BSwizzle);
 #pragma unroll
-                    for (int kk = 0; kk < kHalf / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of V
-                        umma_f16_ta(tmem, tmem + kPCol + 32 * buf + 8 * kk, vd + 128 * kk, kIdescO,
-                                    (h > 0 || kk > 0) ? 1u : 0u);
+                    for (int kk = 0; kk < kBS / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of V
+                        umma_f16_ta(tmem, tmem + kPCol + kBS / 2 * buf + 8 * kk, vd + 128 * kk, kIdescO,
+                                    (t > s.t0 || kk > 0) ? 1u : 0u);
                     umma_commit(&sm.o_done[buf]);
-                    if (odd) umma_commit(&sm.h_empty[hslot]);
+                    umma_commit(&sm.h_empty[hslot]);
                 }
             }
             __syncwarp();
-            i += odd;
         }
         ++seg;
     }
@@ -541,17 +519,17 @@ __device__ __forceinline__ uint32_t stage_at(int r, int u)
     return static_cast<uint32_t>(r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
 }
 
-// Half blocks of parity w: the thread of row `row`.
+// Warpgroup w: blocks w, w + kTurns, ..; the thread of row `row`.
 __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w, int q4, int lane)
 {
     const int row = 32 * q4 + lane;
-    // named barriers: a warp decides on m for its half, the other warpgroup's warp
-    // of the same rows waits for that
-    const int mine = 2 + 2 * q4 + w, theirs = 2 + 2 * q4 + (w ^ 1);
+    // named barriers: a warp decides on m for its block, the next warpgroup's warp of
+    // the same rows waits for that
+    const int mine = 2 + kTurns * q4 + w, theirs = 2 + kTurns * q4 + (w + kTurns - 1) % kTurns;
     const uint32_t O = tmem + (static_cast<uint32_t>(32 * q4) << 16);
-    uint8_t* const stage = sm.stage[4 * w + q4];
+    const uint32_t S = O + kSCol + kBS * w, P = O + kPCol + kBS / 2 * w;
     Seg s;
-    int i = 0;                               // blocks so far
+    int g0 = 0, turn = 0, next = w;          // blocks in all so far, own ones, the next own one
     for (int seg = 0; next_seg(sm.cum, sm.len, p.G, run, s); ++seg) {
         const int act = static_cast<int>(sm.len[s.b] >> 8), n = static_cast<int>(sm.len[s.b] & 0xFF), ctx = act - n;
         const bool warp_live = 32 * q4 < s.rows, live = row < s.rows;
@@ -576,34 +554,33 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
         const bool flip = rs < 0.0f, any_flip = __any_sync(0xffffffffu, flip);
         rs = fmaxf(fabsf(rs), 1.17549435e-38f);               // (-inf times it stays -inf)
         float m = -INFINITY, l = 0.0f;
-        const int i_end = i + (s.t1 - s.t0);
+        const int g_end = g0 + (s.t1 - s.t0);
         // A warp without rows keeps the others company at the barriers.
-        for (int j = i; j < i_end && !warp_live; ++j) {
-            const int g = 2 * j + w, buf = g & 3;
-            wait_for(&sm.s_full[buf], (g >> 2) & 1, p.err, 64, &sm.abort);
-            if (lane == 0) mbar_arrive(&sm.s_free[buf]);
-            if (g >= 4) wait_for(&sm.o_done[buf], ((g - 4) >> 2) & 1, p.err, 128, &sm.abort);
-            if (lane == 0) mbar_arrive(&sm.p_full[buf]);
+        for (; next < g_end && !warp_live; next += kTurns, ++turn) {
+            wait_for(&sm.s_full[w], turn & 1, p.err, 64, &sm.abort);
+            if (lane == 0) mbar_arrive(&sm.s_free[w]);
+            if (turn > 0) wait_for(&sm.o_done[w], (turn - 1) & 1, p.err, 128, &sm.abort);
+            if (lane == 0) mbar_arrive(&sm.p_full[w]);
         }
 #pragma unroll 1
-        for (int j = i; j < i_end && warp_live; ++j) {
-            const int g = 2 * j + w, buf = g & 3, slot = j % kSStages;
-            wait_for(&sm.s_full[buf], (g >> 2) & 1, p.err, 64, &sm.abort);
+        for (; next < g_end && warp_live; next += kTurns, ++turn) {
+            const int slot = next % kSStages;
+            wait_for(&sm.s_full[w], turn & 1, p.err, 64, &sm.abort);
             tc_fence_after();
-            wait_for(&sm.k_full[slot], (j / kSStages) & 1, p.err, 64, &sm.abort);
-            float v[kHalf];
+            wait_for(&sm.k_full[slot], (next / kSStages) & 1, p.err, 64, &sm.abort);
+            float v[kBS];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) tmem_ld32(O + kSCol + kHalf * buf + 32 * c, v + 32 * c);
+            for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, v + 32 * c);
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.s_free[buf]);
-            const float4* ks = reinterpret_cast<const float4*>(sm.ks[slot] + w * kHalf);
+            if (lane == 0) mbar_arrive(&sm.s_free[w]);
+            const float4* ks = reinterpret_cast<const float4*>(sm.ks[slot]);
 #pragma unroll
-            for (int c = 0; c < kHalf / 4; ++c) {
+            for (int c = 0; c < kBS / 4; ++c) {
                 const float4 k4 = ks[c];
-                const float2 a = mul2(make_float2(v[4 * c], v[4 * c + 1]), make_float2(k4.x, k4.y));
-                const float2 b = mul2(make_float2(v[4 * c + 2], v[4 * c + 3]), make_float2(k4.z, k4.w));
+                const float2 a = __fmul2_rn(make_float2(v[4 * c], v[4 * c + 1]), make_float2(k4.x, k4.y));
+                const float2 b = __fmul2_rn(make_float2(v[4 * c + 2], v[4 * c + 3]), make_float2(k4.z, k4.w));
                 v[4 * c] = a.x;
                 v[4 * c + 1] = a.y;
                 v[4 * c + 2] = b.x;
@@ -611,32 +588,46 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
             }
             if (any_flip) {
 #pragma unroll
-                for (int k = 0; k < kHalf; ++k) v[k] = flip ? -v[k] : v[k];
+                for (int k = 0; k < kBS; ++k) v[k] = flip ? -v[k] : v[k];
             }
-            const int off = ctx - (s.t0 + j - i) * kBS - w * kHalf;   // the first drafted token's key here
-            if (off < kHalf) {
+            const int off = ctx - (s.t0 + next - g0) * kBS;     // the first drafted token's key here
+            if (off < kBS) {
                 // which keys the row sees: the context's, then its mask's bits
-                uint64_t see;
-                if (off > 0) see = (~0ull >> (64 - off)) | (m_lo << off);
-                else if (off == 0) see = m_lo;
-                else if (off > -64) see = (m_lo >> -off) | (m_hi << (64 + off));
-                else see = off > -128 ? m_hi >> (-off - 64) : 0ull;
+                uint64_t lo, hi;
+                if (off >= 64) {
+                    lo = ~0ull;
+                    hi = (off == 64 ? 0ull : ~0ull >> (128 - off)) | (m_lo << (off - 64));
+                } else if (off > 0) {
+                    lo = (~0ull >> (64 - off)) | (m_lo << off);
+                    hi = (m_hi << off) | (m_lo >> (64 - off));
+                } else if (off == 0) {
+                    lo = m_lo;
+                    hi = m_hi;
+                } else if (off > -64) {
+                    lo = (m_lo >> -off) | (m_hi << (64 + off));
+                    hi = m_hi >> -off;
+                } else {
+                    lo = off > -128 ? m_hi >> (-off - 64) : 0ull;
+                    hi = 0ull;
+                }
 #pragma unroll
-                for (int k = 0; k < kHalf; ++k)
-                    if (!((see >> k) & 1)) v[k] = -INFINITY;
+                for (int k = 0; k < 64; ++k) {
+                    if (!((lo >> k) & 1)) v[k] = -INFINITY;
+                    if (!((hi >> k) & 1)) v[64 + k] = -INFINITY;
+                }
             }
             float m4[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                m4[c] = fmaxf(v[16 * c], v[16 * c + 1]);
+                m4[c] = fmaxf(v[32 * c], v[32 * c + 1]);
 #pragma unroll
-                for (int k = 2; k < 16; k += 2) m4[c] = max3(m4[c], v[16 * c + k], v[16 * c + k + 1]);
+                for (int k = 2; k < 32; k += 2) m4[c] = max3(m4[c], v[32 * c + k], v[32 * c + k + 1]);
             }
             const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * rs;
             // this P buffer's last P V is complete
-            if (g >= 4) wait_for(&sm.o_done[buf], ((g - 4) >> 2) & 1, p.err, 128, &sm.abort);
-            // ---- m, after the half before ----
-            const bool later = w != 0 || j > i;                // a half of the segment lies before this one
+            if (turn > 0) wait_for(&sm.o_done[w], (turn - 1) & 1, p.err, 128, &sm.abort);
+            // ---- m, after the block before ----
+            const bool later = next > g0;                      // a block of the segment lies before this one
             float mn = -INFINITY;
             if (later) {
                 named_bar_sync(theirs, 64);
@@ -649,7 +640,7 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                 if (later) {
                     // O is complete before it is scaled (and its barrier's phase is the
                     // one waited for: the other warp waited for that before its decision)
-                    wait_for(&sm.o_done[(g - 1) & 3], ((g - 1) >> 2) & 1, p.err, 128, &sm.abort);
+                    wait_for(&sm.o_done[(next - 1) % kTurns], ((next - 1) / kTurns) & 1, p.err, 128, &sm.abort);
                     tc_fence_after();
                     const float f = raise ? ex2(old - mn) : 1.0f;
 #pragma unroll 1
@@ -665,7 +656,7 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                 }
             }
             sm.m[row] = mn;
-            if (w == 0 || j + 1 < i_end) named_bar_arrive(mine, 64);
+            if (next + 1 < g_end) named_bar_arrive(mine, 64);
             if (mn != m) {
                 l *= ex2(m - mn);                              // (0 while m is -inf)
                 m = mn;
@@ -675,82 +666,92 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
             const float2 rs2 = make_float2(rs, rs), nref = make_float2(-ref, -ref);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 4; ++c) {
                 uint32_t hp[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    float2 x = fma2(make_float2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), rs2, nref);
+                    float2 x = __ffma2_rn(make_float2(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]), rs2, nref);
                     x.x = ex2(x.x);
                     x.y = ex2(x.y);
-                    sum[k & 1] = add2(sum[k & 1], x);
+                    sum[k & 1] = __fadd2_rn(sum[k & 1], x);
                     hp[k] = half2_bits(x.x, x.y);
                 }
-                tmem_st16(O + kPCol + 32 * buf + 16 * c, hp);
+                tmem_st16(P + 16 * c, hp);
             }
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.p_full[buf]);
+            if (lane == 0) mbar_arrive(&sm.p_full[w]);
         }
-        i = i_end;
-        // ---- the item's (or its part's) output: this warpgroup's 64 channels ----
-        sm.l[w][row] = l;
-        if (w == 0) sm.m0[row] = m;          // (sm.m: the last decision, an odd half's)
-        named_bar_sync(1, 256);
+        g0 = g_end;
+        // ---- the item's (or its part's) output, 32 channels at a time in turn ----
+        sm.ml[0][w][row] = m;
+        sm.ml[1][w][row] = l;
+        named_bar_sync(1, 4 * kTurns * 32);
         // the last P V, and with it all (one accumulator: they complete in order);
-        // behind the barrier, as the other warpgroup waited for this barrier's last phase
-        wait_for(&sm.o_done[(2 * i - 1) & 3], ((2 * i - 1) >> 2) & 1, p.err, 128, &sm.abort);
+        // behind the barrier, as its warpgroup waited for this barrier's last phase
+        wait_for(&sm.o_done[(g_end - 1) % kTurns], ((g_end - 1) / kTurns) & 1, p.err, 128, &sm.abort);
         tc_fence_after();
         if (warp_live) {
-            const float mf = sm.m[row], m0 = sm.m0[row];
-            const float lt = sm.l[0][row] * (m0 == mf ? 1.0f : ex2(m0 - mf)) + sm.l[1][row];
+            const float mf = sm.m[row];      // the last decision's
+            float lt = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kTurns; ++k) {
+                const float mk = sm.ml[0][k][row];
+                lt += sm.ml[1][k][row] * (mk == mf ? 1.0f : ex2(mk - mf));
+            }
             const bool whole = s.t0 == 0 && s.t1 == s.tiles;
             const float inv = lt == 0.0f ? 0.0f : __fdiv_rn(1.0f, lt);
             const int at = live ? q_row(p, s, row) : -1;
             float* const part = part_of(p, blockIdx.x, s.first);
-            // Rows leave in 64-byte pieces (32 BF16 channels, 16 FP32) through this
-            // warp's staging area: a store covers eight rows' pieces instead of 16
-            // bytes of 32 rows.
+            // Rows leave in 64-byte pieces (32 BF16 channels, 16 FP32) staged in this
+            // warp's 2 KB of the Q tile (every S of the segment is computed): a store
+            // covers eight rows' pieces instead of 16 bytes of 32 rows.
+            uint8_t* const stage = sm.q[seg & 1] + (4 * w + q4) * 2048;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                const int d = 64 * w + 16 * c;
-                float o[16];
-                tmem_ld16(O + d, o);
+            for (int c = w; c < kD / 32; c += kTurns) {
+                float o[32];
+                tmem_ld32(O + 32 * c, o);
                 tmem_wait_ld();
-                if (whole) {
-                    const float4* vs = reinterpret_cast<const float4*>(sm.vs[seg & 1] + d);
+                // BF16: one piece; FP32: two
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float4 a = vs[2 * k], b = vs[2 * k + 1];
-                        const float* x = o + 8 * k;
-                        const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * inv * a.x, x[1] * inv * a.y);
-                        const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * inv * a.z, x[3] * inv * a.w);
-                        const __nv_bfloat162 y2 = __floats2bfloat162_rn(x[4] * inv * b.x, x[5] * inv * b.y);
-                        const __nv_bfloat162 y3 = __floats2bfloat162_rn(x[6] * inv * b.z, x[7] * inv * b.w);
-                        *reinterpret_cast<uint4*>(stage + stage_at(lane, 2 * (c & 1) + k)) =
-                            make_uint4(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1),
-                                       *reinterpret_cast<const uint32_t*>(&y2), *reinterpret_cast<const uint32_t*>(&y3));
+                for (int b = 0; b < 2; ++b) {
+                    if (whole) {
+                        const float4* vs = reinterpret_cast<const float4*>(sm.vs[seg & 1] + 32 * c + 16 * b);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float4 a = vs[2 * k], e = vs[2 * k + 1];
+                            const float* x = o + 16 * b + 8 * k;
+                            const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * inv * a.x, x[1] * inv * a.y);
+                            const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * inv * a.z, x[3] * inv * a.w);
+                            const __nv_bfloat162 y2 = __floats2bfloat162_rn(x[4] * inv * e.x, x[5] * inv * e.y);
+                            const __nv_bfloat162 y3 = __floats2bfloat162_rn(x[6] * inv * e.z, x[7] * inv * e.w);
+                            *reinterpret_cast<uint4*>(stage + stage_at(lane, 2 * b + k)) = make_uint4(
+                                *reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1),
+                                *reinterpret_cast<const uint32_t*>(&y2), *reinterpret_cast<const uint32_t*>(&y3));
+                        }
+                        if (b == 0) continue;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<float4*>(stage + stage_at(lane, k)) =
+                                make_float4(o[16 * b + 4 * k], o[16 * b + 4 * k + 1], o[16 * b + 4 * k + 2],
+                                            o[16 * b + 4 * k + 3]);
                     }
-                    if ((c & 1) == 0) continue;
-                } else {
+                    __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        *reinterpret_cast<float4*>(stage + stage_at(lane, k)) =
-                            make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = 8 * k + (lane >> 2);
+                        const int to = __shfl_sync(0xffffffffu, at, r);
+                        const uint4 x = *reinterpret_cast<const uint4*>(stage + stage_at(r, lane & 3));
+                        if (to < 0) continue;
+                        uint4* dst = whole ? reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(to) * kD + 32 * c)
+                                           : reinterpret_cast<uint4*>(part + (32 * q4 + r) * kD + 32 * c + 16 * b);
+                        dst[lane & 3] = x;
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = 8 * k + (lane >> 2);
-                    const int to = __shfl_sync(0xffffffffu, at, r);
-                    const uint4 x = *reinterpret_cast<const uint4*>(stage + stage_at(r, lane & 3));
-                    if (to < 0) continue;
-                    uint4* dst = whole ? reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(to) * kD + d - 16)
-                                       : reinterpret_cast<uint4*>(part + (32 * q4 + r) * kD + d);
-                    dst[lane & 3] = x;
-                }
-                __syncwarp();
             }
             if (!whole && live && w == 0) {
                 float* ml = part + static_cast<int64_t>(p.part_rows) * kD;
@@ -761,8 +762,8 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_empty[seg & 1]);
-        // (O, m and l of this segment are not touched before both warpgroups are here)
-        named_bar_sync(1, 256);
+        // (O, m and l of this segment are not touched before all are here)
+        named_bar_sync(1, 4 * kTurns * 32);
     }
 }
 
@@ -833,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.h_full[i], kConvWarps);
             mbar_init(&sm.h_empty[i], 1);
         }
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kTurns; ++i) {
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_free[i], 4);
             mbar_init(&sm.p_full[i], 4);
@@ -841,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 1);
-            mbar_init(&sm.q_empty[i], 1 + kProdWarp);
+            mbar_init(&sm.q_empty[i], 1 + 4 * kTurns);
             mbar_init(&sm.drain[i], 1);
         }
         sm.abort = 0;
@@ -868,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        uint32_t* const warp_sum = reinterpret_cast<uint32_t*>(sm.l);
+        uint32_t* const warp_sum = reinterpret_cast<uint32_t*>(sm.ml);
         if (lane == 31) warp_sum[warp] = x;
         __syncthreads();
         uint32_t before = x - mine;
@@ -1047,8 +1048,9 @@ extern "C" pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, con
                                         void* stream)
 {
     const char* name = "pa_fp8_tree_decode";
-    PA_REQUIRE(q && q_scale && k_cache && k_scale && v_cache && v_scale && block_table && kv_act_seqs && tree_mask &&
-                   out,
+    // (tensors of no sequences may have no address)
+    PA_REQUIRE(k_cache && k_scale && v_cache &&
+                   (B == 0 || (q && q_scale && v_scale && block_table && kv_act_seqs && tree_mask && out)),
                PA_ERR_NULLPTR, "%s: NULL tensor pointer", name);
     size_t need = 0;
     const pa_status ps = pa_fp8_tree_decode_workspace_size(B, S1, NQ, NKV, D, &need);

@@ -502,6 +502,8 @@ PA_API pa_status pa_mla_sparse_decode_kvc(const void* q_nope, const void* q_rope
  *                                accept, and the token after it;
  *   pa_fp8_cache_keep_path       the accepted branch's K/V moved to positions
  *                                ctx, ctx + 1, ...
+ * A call of no tokens or sequences is checked and enqueues nothing; the
+ * tensors that then have no elements may be NULL.
  * ------------------------------------------------------------------------ */
 
 /* ------------------------------------------------------------------------
@@ -532,8 +534,7 @@ PA_API pa_status pa_mla_sparse_decode_kvc(const void* q_nope, const void* q_rope
  *              head_size, a multiple of 16, or of 8 if interleaved (else
  *              PA_ERR_UNSUPPORTED).
  * q_codes, caches 8-byte aligned, v_scale 16-byte aligned. Slots, layout,
- * token_batch and v_scale as in pa_fp8_cache_quant_scatter. num_tokens 0
- * enqueues nothing.
+ * token_batch and v_scale as in pa_fp8_cache_quant_scatter.
  * ------------------------------------------------------------------------ */
 PA_API pa_status pa_fp8_qkv_norm_rope_append(
     const void* q, const void* k, const void* v, int in_dtype, int64_t q_stride, int64_t k_stride,
@@ -563,7 +564,7 @@ PA_API pa_status pa_fp8_qkv_norm_rope_append(
  * do not matter; E4M3 NaN codes below it are out of contract.
  * D, block_size  128 and 128 (else PA_ERR_UNSUPPORTED). S1 at most 128, NQ /
  * NKV at most 128, B at most 1024, max_blocks_per_seq * 128 below 2^24, and
- * 5 * ceil(S1 * NQ / NKV / 128) * NKV * B * max_blocks_per_seq below 2^32 (else
+ * 9 * ceil(S1 * NQ / NKV / 128) * NKV * B * max_blocks_per_seq below 2^32 (else
  * PA_ERR_UNSUPPORTED).
  * workspace    at least pa_fp8_tree_decode_workspace_size() bytes, 256-byte
  *              aligned, its first 256 bytes zero before the first call (every

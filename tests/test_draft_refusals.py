@@ -38,6 +38,8 @@ def test_append_refusals(L):
         assert call(**{n: None}) == 1, n
     assert call(T=0) == 0                                  # nothing to do
     assert call(T=0, cs=None, pos=None, rd=0, qw=None, kw=None) == 0
+    assert call(T=0, **{n: None for n in "q k v qc qsc slots tb pos".split()}) == 0
+    assert call(T=0, kc=None) == 1 and call(T=0, cs=None) == 1 and call(T=0, layout=2) == 2
     for bad in (dict(T=-1), dict(NQ=0), dict(NKV=0), dict(D=0), dict(NB=0), dict(BS=0), dict(nb=0), dict(dt=2),
                 dict(wdt=-1), dict(sdt=2), dict(pdt=2), dict(layout=2), dict(eps=-1.0), dict(eps=NAN), dict(eps=INF),
                 dict(maxpos=0), dict(rd=-16), dict(rd=144), dict(qs=2044), dict(dt=0, vs=2046),
@@ -66,7 +68,8 @@ def test_tree_decode_refusals(L):
     call = caller(L.pa_fp8_tree_decode, names, d)
     for k in "q qs kc ks vc vs bt act mask out".split():
         assert call(**{k: None}) == 1, k
-    assert call(B=0) == 0
+    assert call(B=0) == 0 and call(B=0, **{k: None for k in "q qs vs bt act len mask out ws".split()}) == 0
+    assert call(B=0, kc=None) == 1 and call(B=0, layout=3) == 2
     for bad in (dict(B=-1), dict(NB=0), dict(MB=0), dict(layout=3), dict(scale=NAN), dict(scale=INF), dict(ms=-1),
                 dict(NQ=97), dict(q=P(fake.value + 8)), dict(out=P(fake.value + 2)),
                 dict(ws=P(((fake.value + 255) & ~255) + 16))):
@@ -85,7 +88,7 @@ def test_verify_refusals(L):
     call = caller(L.pa_tree_verify, names, d)
     for k in "p tok par u acc path new".split():
         assert call(**{k: None}) == 1, k
-    assert call(B=0) == 0 and call(B=0, q=None, len=None) == 0
+    assert call(B=0) == 0 and call(B=0, **{k: None for k in "p q tok par u len acc path new".split()}) == 0
     for bad in (dict(B=-1), dict(S1=0), dict(V=0), dict(p=P(fake.value + 2)), dict(new=P(fake.value + 1))):
         assert call(**bad) == 2, bad
     for bad in (dict(S1=1025), dict(V=262145), dict(B=(1 << 24) + 1)):
@@ -100,7 +103,8 @@ def test_keep_path_refusals(L):
     call = caller(L.pa_fp8_cache_keep_path, names, d)
     for k in "kc vc ks bt act path acc new".split():
         assert call(**{k: None}) == 1, k
-    assert call(B=0) == 0 and call(B=0, len=None) == 0
+    assert call(B=0) == 0 and call(B=0, **{k: None for k in "bt act len path acc new".split()}) == 0
+    assert call(B=0, kc=None) == 1
     for bad in (dict(B=-1), dict(S1=0), dict(NKV=0), dict(D=0), dict(BS=0), dict(NB=0), dict(MB=0), dict(layout=9),
                 dict(new=fake), dict(kc=P(fake.value + 8))):
         assert call(**bad) == 2, bad

@@ -625,3 +625,213 @@ def test_speculative_step(layout, graph):
         case = dict(B=B, S1=S1, NQ=NQ, NKV=NKV, layout=layout, n=n, act=act, bt=bt, kc=snap[0], vc=snap[1],
                     ks=snap[2], q=qc, qs=qs, vs=vs, mask=mask)
         check_tree({k_: x.cpu() if isinstance(x, torch.Tensor) else x for k_, x in case.items()}, out)
+
+
+# ---- sizes and calls at the borders ------------------------------------------------
+
+def test_tree_decode_signs_of_scales():
+    """Scales of either sign and a zero one: the maximum is then over S k_scale
+    with its sign turned."""
+    c = H.tree_case(21, [400, 130], 5, 16, 2, 0)
+    c["qs"][::2] *= -1
+    c["qs"][1, 3] = 0
+    ks = H.by_position(c["ks"], 0)
+    ks[:, ::3] *= -1
+    check_tree(c, run_tree(c))
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_tree_decode_wide_items_cut_by_runs(layout):
+    """Row tiles of 128, 128 and 64 rows (32 in the ragged sequence's last), cut
+    by the runs' ends, next to sequences of nothing."""
+    c = H.tree_case(22, [6000, 0, 2500, 900], 40, 16, 2, layout, n=[40, 0, 20, 33])
+    check_tree(c, run_tree(c))
+
+
+def test_tree_decode_most_sequences():
+    rng = np.random.default_rng(23)
+    c = H.tree_case(23, [int(x) for x in rng.integers(0, 140, 1024)], 3, 4, 1, 1,
+                    n=[int(x) for x in rng.integers(0, 4, 1024)])
+    check_tree(c, run_tree(c))
+
+
+def test_tree_decode_one_workspace_for_calls_of_several_shapes():
+    pa = _pa()
+    ws = pa.TreeWorkspace(8, 64, 96, 8)
+    for i, (ctx, S1, NQ, NKV) in enumerate([([9000, 300], 8, 96, 8), ([5], 1, 1, 1), ([2000] * 3, 64, 48, 4),
+                                            ([0, 1], 4, 4, 4), ([9000, 300], 8, 96, 8)]):
+        c = H.tree_case(30 + i, ctx, S1, NQ, NKV, i % 2)
+        check_tree(c, run_tree(c, ws=ws))
+
+
+def test_tree_decode_two_graphs_at_once():
+    """Two captured calls with a workspace each, replayed on two streams."""
+    pa = _pa()
+    runs = []
+    for i in range(2):
+        c = H.tree_case(40 + i, [5000 + 900 * i, 70], 6, 24, 2, i)
+        g = _cuda(c)
+        out = torch.zeros((12, 24, H.D), dtype=torch.bfloat16, device="cuda")
+        ws, s = pa.TreeWorkspace(2, 6, 24, 2), torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            call = pa.prepare_tree_decode(g["q"], g["qs"], g["kc"], g["ks"], g["vc"], g["vs"], g["bt"], g["act"],
+                                          g["mask"], out, S1=6, tree_len=g["n"], layout=i, workspace=ws)
+            call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            call()
+        out.fill_(float("nan"))
+        runs.append((c, g, out, ws, s, graph))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for *_, s, graph in runs:
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for c, _, out, ws, *_ in runs:
+        assert ws.error_flags() == 0
+        check_tree(c, out)
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_cache_past_32_bit_offsets(layout):
+    """The step's cache calls on blocks at the end of caches of 5.2 GB."""
+    pa = _pa()
+    NB, S1, NQ, NKV = 40000, 4, 16, 8
+    c = H.tree_case(50 + layout, [200, 126], S1, NQ, NKV, layout)
+    small, at = c["kc"].shape[0], NB - c["kc"].shape[0]
+    dev = dict(device="cuda")
+    sh = H.cache_shape(layout, NB, NKV)
+    kc, vc = (torch.zeros(sh + (128,), dtype=torch.uint8, **dev) for _ in range(2))
+    ks = torch.zeros(sh, **dev)
+    for big, k in ((kc, "kc"), (vc, "vc"), (ks, "ks")):
+        big[at:] = c[k].cuda()
+    bt = torch.where(c["bt"] >= 0, c["bt"] + at, -1)
+    g = _cuda(c)
+    out = torch.zeros((2 * S1, NQ, 128), dtype=torch.bfloat16, **dev)
+    pa.tree_decode(g["q"], g["qs"], kc, ks, vc, g["vs"], bt.cuda(), g["act"], g["mask"], out, S1=S1,
+                   tree_len=g["n"], layout=layout)
+    torch.cuda.synchronize()
+    check_tree(c, out)
+    path = torch.tensor([[0, 2, 3, -1], [0, 3, -1, -1]], dtype=torch.int32)
+    acc = torch.tensor([3, 2], dtype=torch.int32)
+    new = torch.zeros(2, dtype=torch.int32, **dev)
+    pa.cache_keep_path(kc, vc, ks, bt.cuda(), g["act"], path.cuda(), acc.cuda(), new, tree_len=g["n"], layout=layout)
+    want = keep_reference(dict(c, path=path, acc=acc, BS=128))
+    for big, w in zip((kc, vc, ks), want):
+        assert torch.equal(H.by_position(big[at:], layout).cpu(), w)
+    assert torch.equal(new.cpu(), want[3])
+    # append to the last block's rows
+    T = 5
+    a = append_case(51, T, NQ, NKV, 128, 64, torch.bfloat16, layout)
+    slots = torch.arange(NB * 128 - T, NB * 128, dtype=torch.int64)
+    a.update(slots=torch.arange(small * 128 - T, small * 128, dtype=torch.int64), NB=small, BS=128)
+    kc[at:], vc[at:], ks[at:] = 0xA5, 0x5A, -7.0
+    qc, qs = torch.zeros((T, NQ, 128), dtype=torch.uint8, **dev), torch.zeros((T, NQ), **dev)
+    pa.qkv_norm_rope_append(a["q"].cuda(), a["k"].cuda(), a["v"].cuda(), a["qw"].cuda(), a["kw"].cuda(),
+                            a["cs"].cuda(), a["pos"].cuda(), qc, qs, kc, vc, slots.cuda(), ks, a["vs"].cuda(),
+                            a["tb"].cuda(), eps=1e-5, interleaved=False, layout=layout)
+    torch.cuda.synchronize()
+    check_append(a, (qc.cpu(), qs.cpu(), kc[at:].cpu(), vc[at:].cpu(), ks[at:].cpu()))
+    assert not kc[:at].any() and not vc[:at].any() and not ks[:at].any()
+
+
+def test_append_of_no_tokens_and_of_many():
+    a = append_case(60, 0, 3, 1, 64, 32, torch.bfloat16, 0)
+    assert (run_append(a)[2] == 0xA5).all()
+    a = append_case(61, 3001, 10, 2, 128, 64, torch.bfloat16, 1)
+    check_append(a, run_append(a))
+
+
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("B,V", [(76, 260), (77, 260), (153, 515), (305, 512), (700, 131)])
+def test_verify_batches_on_fewer_processors_each(B, V, draft):
+    check_verify(verify_case(B, B, 5, V, draft))
+
+
+def test_verify_tokens_do_not_depend_on_the_batch():
+    """A sequence's draw is the same alone and among others."""
+    c = verify_case(70, 320, 6, 2000, True)
+    acc, path, tokens = check_verify(c)
+    for b in (0, 150, 319):
+        one = {k: v[b:b + 1] for k, v in c.items()}
+        for x, y in zip(run_verify(one), (acc, path, tokens)):
+            assert np.array_equal(x[0], y[b])
+
+
+def test_verify_rows_past_32_bit_offsets():
+    """2.5e9 probabilities: the last sequences lie past 2^31 elements."""
+    pa = _pa()
+    B, S1, V = 600, 16, 262144
+    dev = dict(device="cuda")
+    p = torch.zeros((B, S1, V), **dev)
+    hot = [(b * 1009 + 7) % V for b in range(B)]
+    p[torch.arange(B, **dev), 3, torch.tensor(hot, **dev)] = 1.0
+    p[:, 0, 11] = 1.0
+    tok = torch.full((B, S1), 12, dtype=torch.int32, **dev)
+    tok[:, 3] = 11
+    par = torch.zeros((B, S1), dtype=torch.int32, **dev)
+    u = torch.full((B, S1), 0.5, **dev)
+    acc, path, toks = (torch.zeros(s, dtype=torch.int32, **dev) for s in ((B,), (B, S1), (B, S1)))
+    pa.tree_verify(p, None, tok, par, u, acc, path, toks)
+    torch.cuda.synchronize()
+    assert (acc == 2).all() and (path[:, :3].cpu() == torch.tensor([0, 3, -1])).all()
+    assert (toks[:, 0] == 11).all() and toks[:, 1].cpu().tolist() == hot and (toks[:, 2:] == -1).all()
+
+
+@pytest.mark.parametrize("what", ["verify", "keep", "append"])
+def test_step_calls_on_another_stream_and_replayed(what):
+    pa = _pa()
+    side = torch.cuda.Stream()
+    if what == "verify":
+        c = verify_case(80, 6, 7, 900, True)
+        t = {k: torch.from_numpy(v).cuda() for k, v in c.items()}
+        got = [torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((6,), (6, 7), (6, 7))]
+        call = pa.prepare_tree_verify(t["p"], t["q"], t["tok"], t["par"], t["u"], *got, tree_len=t["n"], stream=side)
+        want = [torch.from_numpy(x) for x in H.verify_reference(c["p"], c["q"], c["tok"], c["par"], c["u"], c["n"])]
+    elif what == "keep":
+        c = keep_case(81, [100, 7, 300], 9, 2, 0)
+        t = _cuda(c)
+        got = [t["kc"], t["vc"], t["ks"], torch.zeros(3, dtype=torch.int32, device="cuda")]
+        call = pa.prepare_cache_keep_path(t["kc"], t["vc"], t["ks"], t["bt"], t["act"], t["path"], t["acc"], got[3],
+                                          tree_len=t["n"], layout=0, stream=side)
+        want = keep_reference(c)
+    else:
+        c = append_case(82, 19, 4, 2, 128, 64, torch.float32, 0)
+        want = run_append(c)
+        t = _cuda(c)
+        got = [torch.zeros_like(want[0]).cuda(), torch.zeros_like(want[1]).cuda(), torch.full_like(want[2], 0xA5).cuda(),
+               torch.full_like(want[3], 0x5A).cuda(), torch.full_like(want[4], -7.0).cuda()]
+        call = pa.prepare_qkv_norm_rope_append(t["q"], t["k"], t["v"], t["qw"], t["kw"], t["cs"], t["pos"], got[0],
+                                               got[1], got[2], got[3], t["slots"], got[4], t["vs"], t["tb"], eps=1e-5,
+                                               interleaved=False, layout=0, stream=side)
+    clean = [x.clone() for x in got]
+    torch.cuda.synchronize()
+    call()
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x.cpu(), y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for _ in range(2):
+        for x, y in zip(got, clean):
+            x.copy_(y)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x.cpu(), y)
+
+
+def test_calls_of_no_sequences():
+    pa = _pa()
+    c = _cuda(H.tree_case(90, [10], 2, 4, 2, 0))
+    no = lambda *s, dt=torch.int32: torch.zeros((0,) + s, dtype=dt, device="cuda")  # noqa: E731
+    pa.tree_decode(no(4, 128, dt=torch.uint8), no(4, dt=torch.float32), c["kc"], c["ks"], c["vc"],
+                   no(2, 128, dt=torch.float32), no(3), no(), no(2, 2, dt=torch.bool),
+                   no(4, 128, dt=torch.bfloat16), S1=2, tree_len=no(), layout=0)
+    pa.tree_verify(no(2, 9, dt=torch.float32), None, no(2), no(2), no(2, dt=torch.float32), no(), no(2), no(2))
+    pa.cache_keep_path(c["kc"], c["vc"], c["ks"], no(3), no(), no(2), no(), no(), layout=0)
+    torch.cuda.synchronize()
