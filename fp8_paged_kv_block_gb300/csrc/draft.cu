@@ -4,6 +4,8 @@
 
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 namespace pa {
 namespace {
 
@@ -17,24 +19,34 @@ constexpr int kMaxNodes = 1024;
 // is replayed from p, q and the z of each), gathered for all nodes at once ahead
 // of the walk. A rejection of a drawn draft needs the sum of R over the
 // vocabulary, and the draw at the end R's prefix sums: warp w of the cluster takes
-// the w-th segment of the vocabulary, replays R there and sums it; the draw then
-// needs the segments' sums and one segment's 128-wide steps.
+// the w-th segment of the vocabulary, replays R there and sums it; for the draw
+// the CTA with the segment that holds the value splits it between its warps.
 // The weights are 2^-45 integers: their sums are exact, so the drawn index
 // depends neither on the number of CTAs nor on the order of summation.
-// Bound by the rows of p and q read (one or two of V floats per sequence, again
-// from L2 for each further rejection) on large batches, by the chain launch,
-// gather, row, cluster barrier on small ones.
+//
+// Bound by the chain launch, gather (two loads), then per rejection a pass over
+// the row and an exchange between the CTAs: about 1.5 us of start, 3 us a pass.
+// 64 sequences of 16 nodes x 131072 values take 27 us (of 61 MB read once, 10 us
+// at the copy rate; the sequence with the most has four passes), 256 of 5 x 50000
+// 29 us, one of 8 x 32003 without probabilities 8 us. What made the chain short:
+// - code: a launch runs most of it once, and cold code comes from L2. With passes
+//   and draw inlined and unrolled (61 KB a kernel instead of 27) the 64 took 39 us.
+// - four 16-byte loads of p and of q in flight a lane: with two 39 us, and 512
+//   threads a CTA, which wait longer for one another, 32.
+// - FP64 tests only where FP32 cannot tell, see below.
+// Sums pushed under mbarriers instead of a cluster barrier gained 1 us of 27 and
+// were not kept.
+//
 // A sequence gets 8 CTAs while the batch's CTAs number at most kResident, half as
-// many for twice the batch: more CTAs shorten the pass over a row, and cost
-// launches and cluster barriers once they no longer all run at once. kResident
-// 304, 608, 1216: 53, 44, 44 us on 64 sequences of 16 nodes x 131072, 97, 65, 68
-// on 128 of them; 61, 46, 49 us on 256 of 5 x 50000, 44, 36, 42 on 128.
-constexpr int kVThreads = 512;
+// many for twice the batch: more CTAs shorten a pass, and cost launches and
+// exchanges. kResident 608 or 1216 (two rounds of the GPU): 45 or 41 us on 128
+// sequences of 16 x 131072, 60 or 53 on 500 of 5 x 50000, 29 or 30 on 256.
+constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSegs = kMaxCluster * kVWarps;
 constexpr int kMaxV = 1 << 18;
-constexpr int kResident = 608;               // 4 CTAs on each of 152 SMs
+constexpr int kResident = 1216;
 
 struct VerifyParams {
     const float *p, *q;
@@ -54,9 +66,9 @@ constexpr uint32_t kBias = 0x4B000000u;      // the bits of 2^23
 
 __device__ __forceinline__ void add_weight(float r, uint32_t& hi, uint32_t& lo)
 {
-    const float x = fminf(fmaxf(r, 0.0f), 1.0f) * 0x1p22f;
-    const float t = __fadd_rz(x, 0x1p23f);
-    const float rest = x - (t - 0x1p23f);
+    const float x = fminf(fmaxf(r, 0.0f), 1.0f);
+    const float t = __fmaf_rz(x, 0x1p22f, 0x1p23f);
+    const float rest = __fmaf_rn(x, 0x1p22f, 0x1p23f - t);
     hi += __float_as_uint(t);
     lo += __float_as_uint(__fmaf_rz(rest, 0x1p23f, 0x1p23f));
 }
@@ -75,13 +87,71 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v)
     return v;
 }
 
+// R after `rej` rejections of drawn drafts at four places, from p and q there
+__device__ __forceinline__ void replay(float4& r, const float4& q, float z)
+{
+    r.x = fmaxf(__fsub_rn(r.x, __fmul_rn(z, q.x)), 0.0f);
+    r.y = fmaxf(__fsub_rn(r.y, __fmul_rn(z, q.y)), 0.0f);
+    r.z = fmaxf(__fsub_rn(r.z, __fmul_rn(z, q.z)), 0.0f);
+    r.w = fmaxf(__fsub_rn(r.w, __fmul_rn(z, q.w)), 0.0f);
+}
+
+// Four values of a row in [lo, hi), zeros behind: STRIDE 1: i .. i + 3 (VEC: hi a
+// multiple of 4), else i, i + STRIDE, ..
+template <bool VEC, int STRIDE>
+__device__ __forceinline__ float4 load4(const float* row, int i, int hi)
+{
+    if (VEC) return i < hi ? __ldg(reinterpret_cast<const float4*>(row + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return make_float4(i < hi ? __ldg(row + i) : 0.0f, i + STRIDE < hi ? __ldg(row + i + STRIDE) : 0.0f,
+                       i + 2 * STRIDE < hi ? __ldg(row + i + 2 * STRIDE) : 0.0f,
+                       i + 3 * STRIDE < hi ? __ldg(row + i + 3 * STRIDE) : 0.0f);
+}
+
+// R's weights over [lo, hi), summed by a warp. One copy of it for all callers: a
+// launch runs most of its code once, and what it fetches costs more than the call.
+template <bool VEC>
+__device__ __noinline__ unsigned long long weights_of(const float* prow, const float* qrow, const float* zs, int rej,
+                                                      int lo, int hi)
+{
+    const int lane = threadIdx.x & 31;
+    constexpr int kBatch = 4;                // 128-value steps whose loads are in flight at once
+    unsigned long long w = 0;
+#pragma unroll 1
+    for (int i = lo; i < hi; i += 128 * kBatch) {
+        float4 r[kBatch], q[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int at = i + 128 * j + (VEC ? 4 * lane : lane);
+            r[j] = load4<VEC, 32>(prow, at, hi);
+            if (rej > 0) q[j] = load4<VEC, 32>(qrow, at, hi);
+        }
+#pragma unroll 1
+        for (int k = 0; k < rej; ++k) {
+            const float z = zs[k];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) replay(r[j], q[j], z);
+        }
+        uint32_t h = 0, l = 0;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            add_weight(r[j].x, h, l);
+            add_weight(r[j].y, h, l);
+            add_weight(r[j].z, h, l);
+            add_weight(r[j].w, h, l);
+        }
+        w += (static_cast<unsigned long long>(h - 4 * kBatch * kBias) << 23) + (l - 4 * kBatch * kBias);
+    }
+    return warp_sum(w);
+}
+
 struct VerifySmem {
     unsigned long long all[2][kMaxSegs];     // the cluster's segments' sums, by pass parity
+    unsigned long long part[kVWarps];
     // then, S1 long each: p and q at a node's token, u, the z's (two sets), parent, token
 };
 
 template <bool VEC>
-__global__ void __launch_bounds__(kVThreads, 3) tree_verify_kernel(const VerifyParams a)
+__global__ void __launch_bounds__(kVThreads, 4) tree_verify_kernel(const VerifyParams a)
 {
     extern __shared__ __align__(16) unsigned char raw[];
     VerifySmem& sm = *reinterpret_cast<VerifySmem*>(raw);
@@ -101,6 +171,7 @@ __global__ void __launch_bounds__(kVThreads, 3) tree_verify_kernel(const VerifyP
     n = n < 0 ? 0 : (n > a.S1 ? a.S1 : n);
     if (n == 0) {                                         // the whole cluster
         if (rank == 0) {
+#pragma unroll 1
             for (int i = tid; i < a.S1; i += kVThreads) path[i] = tokens[i] = -1;
             if (tid == 0) a.accepted[b] = 0;
         }
@@ -110,6 +181,7 @@ __global__ void __launch_bounds__(kVThreads, 3) tree_verify_kernel(const VerifyP
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const float* pb = a.p + b * a.S1 * a.V;
     const float* qb = a.q ? a.q + b * a.S1 * a.V : nullptr;
+#pragma unroll 1
     for (int s = tid; s < n; s += kVThreads) {
         const int pr = __ldg(a.par + b * a.S1 + s), x = __ldg(a.tok + b * a.S1 + s);
         const bool ok = s > 0 && pr >= 0 && pr < s && x >= 0 && x < a.V;
@@ -128,186 +200,204 @@ __global__ void __launch_bounds__(kVThreads, 3) tree_verify_kernel(const VerifyP
     const int lo = min(mine * a.seg, a.V), hi = min(lo + a.seg, a.V);
     const float* prow = pb;
     const float* qrow = qb;
-    int cur = 0, acc = 1, rej = 0;           // current node, nodes accepted, drafts of cur rejected so far
+    // current node, nodes accepted, drafts of cur rejected so far, where they end
+    int cur = 0, acc = 1, rej = 0, last = 0;
     // The z's of cur's rejections. Every thread writes them, all the same, so that no
     // barrier is needed before they are read; a node's first takes the set that the
     // last node with rejections did not, as a slower warp may still be there (it has
     // passed that node's own cluster barrier, so no more than one set behind).
     float* zc = zs + a.S1;
-    // R after `rej` rejections of drawn drafts, from p and q
-    auto rest = [&](float r, float q) {
-        for (int k = 0; k < rej; ++k) r = fmaxf(__fsub_rn(r, __fmul_rn(zc[k], q)), 0.0f);
-        return r;
+    // R's weights in [from, to), summed by this warp: with drawn drafts p less z q for
+    // each rejection, else p less the rejected drafts (a repeated one has p0 0)
+    bool all_of_p = false;                   // R is empty: p takes its place
+    auto part = [&](int from, int to) {
+        unsigned long long w = weights_of<VEC>(prow, qrow, zc, qb ? rej : 0, from, to);
+        if (!qb && !all_of_p)
+#pragma unroll 1
+            for (int t = cur + 1; t < last; ++t)
+                if (par[t] == cur && tok[t] >= from && tok[t] < to) w -= weight(p0[t]);
+        return w;
     };
     // R's weights summed over all of the vocabulary, and each segment's into sm.all
     int pass = 0;
-    auto sums = [&](bool replay) {
-        unsigned long long w = 0;
-        if (VEC) {
-#pragma unroll 2
-            for (int i = lo + 4 * lane; i < hi; i += 128) {
-                float4 r = __ldg(reinterpret_cast<const float4*>(prow + i));
-                if (replay) {
-                    const float4 q = __ldg(reinterpret_cast<const float4*>(qrow + i));
-                    for (int k = 0; k < rej; ++k) {
-                        const float z = zc[k];
-                        r.x = fmaxf(__fsub_rn(r.x, __fmul_rn(z, q.x)), 0.0f);
-                        r.y = fmaxf(__fsub_rn(r.y, __fmul_rn(z, q.y)), 0.0f);
-                        r.z = fmaxf(__fsub_rn(r.z, __fmul_rn(z, q.z)), 0.0f);
-                        r.w = fmaxf(__fsub_rn(r.w, __fmul_rn(z, q.w)), 0.0f);
-                    }
-                }
-                uint32_t h = 0, l = 0;
-                add_weight(r.x, h, l);
-                add_weight(r.y, h, l);
-                add_weight(r.z, h, l);
-                add_weight(r.w, h, l);
-                w += (static_cast<unsigned long long>(h - 4 * kBias) << 23) + (l - 4 * kBias);
-            }
-        } else {
-#pragma unroll 4
-            for (int i = lo + lane; i < hi; i += 32) {
-                float r = __ldg(prow + i);
-                if (replay) r = rest(r, __ldg(qrow + i));
-                w += weight(r);
-            }
-        }
-        if (!replay && !qb && rej > 0) {
-            // tokens of cur's children, all of them rejected, are out (a repeated one
-            // has p0 0)
-            for (int t = cur + 1; t < n; ++t)
-                if (lane == 0 && par[t] == cur && tok[t] >= lo && tok[t] < hi) w -= weight(p0[t]);
-        }
-        w = warp_sum(w);
+    auto sums = [&] {
+        const unsigned long long w = part(lo, hi);
         // to every CTA of the cluster. (Two sets: a CTA may be a pass ahead of one that
         // still reads, and not more.)
         if (lane < ctas) *cl.map_shared_rank(&sm.all[pass & 1][mine], lane) = w;
         cl.sync();
         unsigned long long z = 0;
+#pragma unroll 1
         for (int i = lane; i < segs; i += 32) z += sm.all[pass & 1][i];
         ++pass;
         return warp_sum(z);
     };
 
-    double z = 1.0;
+    // z as FP32: exact with drawn drafts, within z_err of the FP64 value without
+    float z = 1.0f, z_err = 0.0f;
     unsigned long long Z = 0;
-    bool summed = false;                     // Z and sm.wsum are of R as it is
-    for (int s = 1; s < n; ++s) {
-        if (par[s] != cur) continue;
-        const int x = tok[s];
-        double rx;
-        if (qb) {
-            rx = static_cast<double>(rest(p0[s], q0[s]));
-        } else {
-            // rejected before: R(x) is 0 (every thread notes it, all the same)
-            for (int t = cur + 1; t < s; ++t)
-                if (par[t] == cur && tok[t] == x) p0[s] = 0.0f;
-            __syncwarp();
-            rx = static_cast<double>(p0[s]);
-        }
-        if (static_cast<double>(un[s]) * z * static_cast<double>(q0[s]) < rx) {
-            if (rank == 0 && tid == 0) {
-                path[acc] = s;
-                tokens[acc - 1] = x;
+    bool summed = false;                     // Z and sm.all are of R as it is
+    int s = 1;
+#pragma unroll 1
+    for (;;) {
+        // ---- to the next rejection of a drawn draft, or the end ----
+        bool rejected = false;
+#pragma unroll 1
+        for (; s < n && !rejected; ++s) {
+            if (par[s] != cur) continue;
+            const int x = tok[s];
+            float rx = p0[s];
+            if (qb) {
+#pragma unroll 1
+                for (int k = 0; k < rej; ++k) rx = fmaxf(__fsub_rn(rx, __fmul_rn(zc[k], q0[s])), 0.0f);
+            } else {
+                // rejected before: R(x) is 0 (every thread notes it, all the same)
+#pragma unroll 1
+                for (int t = cur + 1; t < s; ++t)
+                    if (par[t] == cur && tok[t] == x) p0[s] = 0.0f;
+                __syncwarp();
+                rx = p0[s];
             }
-            ++acc;
-            cur = s;
-            rej = 0;
-            summed = false;
-            z = 1.0;
-            prow = pb + static_cast<int64_t>(cur) * a.V;
-            if (qb) qrow = qb + static_cast<int64_t>(cur) * a.V;
-        } else if (qb) {
-            if (rej == 0) zc = zc == zs ? zs + a.S1 : zs;
-            zc[rej] = static_cast<float>(z);
-            __syncwarp();
-            ++rej;
-            Z = sums(true);
-            summed = true;
-            z = static_cast<double>(static_cast<float>(static_cast<double>(Z) * 0x1p-45));
-        } else {
-            ++rej;
-            z -= rx;
+            // u z Q < R, in FP64 only where FP32 cannot tell: FP64 runs at two lanes a clock
+            // and SM, and all of the cluster's warps do this (5 us of 45 on 64 sequences).
+            // Three roundings of 2^-24 each are below 2^-20 of the product; what underflows
+            // is below 2^-130 as long as Q <= 2^20.
+            const float u = un[s], prod = u * z * q0[s], err = fabsf(prod) * 0x1p-20f + z_err * fabsf(u) + 0x1p-120f;
+            bool take = prod + err < rx;
+            if ((!take && !(prod - err > rx)) || !(fabsf(u) <= 1.0f && fabsf(q0[s]) <= 0x1p20f)) {
+                double zd = z;
+                if (!qb) {
+                    zd = 1.0;
+#pragma unroll 1
+                    for (int t = cur + 1; t < s; ++t)
+                        if (par[t] == cur) zd -= static_cast<double>(p0[t]);
+                }
+                take = static_cast<double>(u) * zd * static_cast<double>(q0[s]) < static_cast<double>(rx);
+            }
+            if (take) {
+                if (rank == 0 && tid == 0) {
+                    path[acc] = s;
+                    tokens[acc - 1] = x;
+                }
+                ++acc;
+                cur = s;
+                rej = 0;
+                last = 0;
+                summed = false;
+                z = 1.0f;
+                z_err = 0.0f;
+                prow = pb + static_cast<int64_t>(cur) * a.V;
+                if (qb) qrow = qb + static_cast<int64_t>(cur) * a.V;
+            } else if (qb) {
+                if (rej == 0) zc = zc == zs ? zs + a.S1 : zs;
+                zc[rej] = z;
+                __syncwarp();
+                ++rej;
+                rejected = true;
+            } else {
+                last = s + 1;
+                z -= rx;
+                z_err += fabsf(z) * 0x1p-23f;
+            }
         }
-    }
-    // ---- the draw ----
-    bool all_of_p = false;                   // R is empty: p takes its place
-    if (!summed) Z = sums(false);
-    if (Z == 0) {
+        if (rejected || !summed) Z = sums();
+        summed = true;
+        z = __ull2float_rn(Z) * 0x1p-45f;
+        if (rejected) continue;
+        if (Z != 0 || all_of_p) break;
         all_of_p = true;
         rej = 0;
-        Z = sums(false);
+        summed = false;
     }
+    // ---- the draw ----
     if (rank == 0) {
         if (tid == 0) {
             a.accepted[b] = acc;
             path[0] = 0;
             if (Z == 0) tokens[acc - 1] = -1;
         }
+#pragma unroll 1
         for (int i = acc + tid; i < a.S1; i += kVThreads) path[i] = tokens[i] = -1;
     }
-    if (Z != 0) {
-        const unsigned long long* all = sm.all[(pass - 1) & 1];
-        const float u0 = un[0];
-        unsigned long long t = u0 > 0.0f ? static_cast<unsigned long long>(static_cast<double>(u0) * static_cast<double>(Z)) : 0ull;
-        if (t >= Z) t = Z - 1;
-        unsigned long long before = 0;
-        for (int i = lane; i < mine; i += 32) before += all[i];
-        before = warp_sum(before);
-        if (t >= before && t - before < all[mine]) {
-            auto weight_at = [&](int i) -> unsigned long long {
-                const float r = __ldg(prow + i);
-                return weight(qb && rej > 0 ? rest(r, __ldg(qrow + i)) : r);
-            };
-            // the weights of cur's rejected tokens in [from, to) (given drafts only)
-            auto out = [&](int from, int to) {
-                unsigned long long w = 0;
-                for (int e = cur + 1; e < n && !qb && !all_of_p; ++e)
-                    if (par[e] == cur && tok[e] >= from && tok[e] < to) w += weight(p0[e]);
-                return w;
-            };
-            auto scan = [&](unsigned long long c) {
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const unsigned long long up = __shfl_up_sync(0xffffffffu, c, o);
-                    if (lane >= o) c += up;
-                }
-                return c;
-            };
-            // the 32nd of the segment that holds it (one lane sums each), then the
-            // value, 32 at a time
-            const int sub = a.seg / 32, l0 = min(lo + lane * sub, hi), l1 = min(l0 + sub, hi);
-            unsigned long long c = 0;
-#pragma unroll 8
-            for (int i = l0; i < l1; ++i) c += weight_at(i);
-            c -= out(l0, l1);
-            const unsigned long long upto = scan(c);
-            const int at = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, before + upto > t))) - 1;
-            before += __shfl_sync(0xffffffffu, upto - c, at);
-            const int end = __shfl_sync(0xffffffffu, l1, at);
-            for (int i0 = __shfl_sync(0xffffffffu, l0, at); i0 < end; i0 += 32) {
-                const int i = i0 + lane;
-                const unsigned long long v = scan(i < end ? weight_at(i) - out(i, i + 1) : 0ull);
-                const unsigned hit = __ballot_sync(0xffffffffu, before + v > t);
-                if (hit) {
-                    if (lane == 0) tokens[acc - 1] = i0 + __ffs(static_cast<int>(hit)) - 1;
-                    break;
-                }
-                before += __shfl_sync(0xffffffffu, v, 31);
+    if (Z == 0) return;
+    // The value lies where t = floor(u0 Z) does. Each CTA looks for it in its own
+    // segments; the one that has it splits that segment between its warps.
+    const unsigned long long* all = sm.all[(pass - 1) & 1];
+    unsigned long long before = 0, here = 0;
+#pragma unroll 1
+    for (int i = lane; i < (rank + 1) * kVWarps; i += 32) (i < rank * kVWarps ? before : here) += all[i];
+    before = warp_sum(before);
+    here = warp_sum(here);
+    // (FP64 again only where FP32 finds t in or near these segments)
+    const float u0 = fminf(fmaxf(un[0], 0.0f), 1.0f);      // (NaN: 0)
+    const float tf = u0 * __ull2float_rn(Z), near = tf * 0x1p-20f + 4.0f;
+    if (__ull2float_rn(before) - near > tf || __ull2float_rn(before + here) + near < tf) return;
+    unsigned long long t = static_cast<unsigned long long>(static_cast<double>(u0) * static_cast<double>(Z));
+    if (t >= Z) t = Z - 1;
+    if (t < before || t - before >= here) return;          // (the whole CTA, as above)
+    int at = rank * kVWarps;
+#pragma unroll 1
+    while (t - before >= all[at]) before += all[at++];
+    const int s0 = min(at * a.seg, a.V), s1 = min(s0 + a.seg, a.V);
+    const int sub = (a.seg / 128 + kVWarps - 1) / kVWarps * 128;
+    const int from = min(s0 + warp * sub, s1), to = min(from + sub, s1);
+    const unsigned long long own = part(from, to);
+    if (lane == 0) sm.part[warp] = own;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < warp; ++i) before += sm.part[i];
+    if (t < before || t - before >= own) return;           // this warp has it
+    const int k0 = qb ? rej : 0;
+#pragma unroll 1
+    for (int i0 = from; i0 < to; i0 += 128) {
+        const int i = i0 + 4 * lane;
+        float4 r = load4<VEC, 1>(prow, i, to);
+        if (k0 > 0) {
+            const float4 q = load4<VEC, 1>(qrow, i, to);
+#pragma unroll 1
+            for (int k = 0; k < k0; ++k) replay(r, q, zc[k]);
+        }
+        if (!qb && !all_of_p) {
+#pragma unroll 1
+            for (int e = cur + 1; e < last; ++e) {
+                const int d = par[e] == cur ? tok[e] - i : -1;
+                r.x = d == 0 ? 0.0f : r.x;
+                r.y = d == 1 ? 0.0f : r.y;
+                r.z = d == 2 ? 0.0f : r.z;
+                r.w = d == 3 ? 0.0f : r.w;
             }
         }
+        const unsigned long long w0 = weight(r.x), w1 = w0 + weight(r.y), w2 = w1 + weight(r.z), w3 = w2 + weight(r.w);
+        unsigned long long v = w3;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long up = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += up;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + v > t);
+        if (hit) {
+            if (lane == __ffs(static_cast<int>(hit)) - 1) {
+                const unsigned long long b = before + v - w3;
+                tokens[acc - 1] = i + (b + w0 > t ? 0 : b + w1 > t ? 1 : b + w2 > t ? 2 : 3);
+            }
+            return;
+        }
+        before += __shfl_sync(0xffffffffu, v, 31);
     }
 }
 
 // ---- the accepted branch in the cache ------------------------------------------------
-// One CTA per (sequence, heads_per_cta heads). A round takes rows in order as far
+// One CTA per (sequence, heads_per_cta heads): four heads of 128 channels. A round takes rows in order as far
 // as the CTA's registers go (kKBatch 16-byte chunks a thread): all are read, then,
 // behind a barrier, written. path[i] >= i, so a round's writes, to lower rows
 // than any later round's sources, spoil nothing that is still to be read.
-// Latency-bound: a chain of four dependent loads (accepted, path, block table,
-// row), which more rows do not lengthen.
+// Latency-bound: a chain of three dependent loads (lengths and path, block table,
+// row), which more rows do not lengthen: 4.5 us on 16 sequences of 16 nodes x 8
+// heads, 8.8 us on 256 of 64 (10.7 with two heads a CTA, 8 chunks a thread and the
+// divisions in the unrolled loop: 24 KB of code instead of 12, and 1024 CTAs of
+// which 608 fit; 11.3 with eight heads a CTA, 12 with 8 chunks).
 constexpr int kKThreads = 256;
-constexpr int kKBatch = 8;
+constexpr int kKHeads = 4, kKBatch = 4, kKResident = 6;   // (6 CTAs an SM: 40 registers)
 
 struct KeepParams {
     uint8_t *kc, *vc;
@@ -317,17 +407,19 @@ struct KeepParams {
     int S1, H, chunks, BS;
     int64_t num_blocks;
     int max_blocks, layout, heads_per_cta;
+    uint32_t chunk_mul;                      // 2^20 / chunks + 1: r / chunks = r chunk_mul >> 20 while r chunks < 2^20
 };
 
-__global__ void __launch_bounds__(kKThreads) cache_keep_path_kernel(const KeepParams p)
+__global__ void __launch_bounds__(kKThreads, kKResident) cache_keep_path_kernel(const KeepParams p)
 {
     __shared__ int64_t src[kMaxNodes], dst[kMaxNodes];   // rows of head 0; src -1: no move
     const int b = blockIdx.x, tid = threadIdx.x;
+    const int* path = p.path + static_cast<int64_t>(b) * p.S1;
+    int s = tid < p.S1 ? __ldg(path + tid) : -1;         // (with the loads below, not behind them)
     const int act = max(__ldg(p.act + b), 0);
     int n = p.len ? __ldg(p.len + b) : p.S1;
-    n = n < 0 ? 0 : (n > p.S1 ? p.S1 : n);
-    n = min(n, act);
     int m = __ldg(p.accepted + b);
+    n = min(n < 0 ? 0 : (n > p.S1 ? p.S1 : n), act);
     m = m < 0 ? 0 : (m > n ? n : m);
     const int ctx = act - n;
     if (blockIdx.y == 0 && tid == 0) p.new_act[b] = ctx + m;
@@ -337,8 +429,9 @@ __global__ void __launch_bounds__(kKThreads) cache_keep_path_kernel(const KeepPa
         const int id = __ldg(p.bt + static_cast<int64_t>(b) * p.max_blocks + bi);
         return id >= 0 && id < p.num_blocks ? cache_row(p.layout, id, pos - bi * p.BS, 0, p.BS, p.H) : -1;
     };
+#pragma unroll 1
     for (int i = tid; i < m; i += kKThreads) {
-        const int s = __ldg(p.path + static_cast<int64_t>(b) * p.S1 + i);
+        if (i != tid) s = __ldg(path + i);
         int64_t from = -1, to = -1;
         if (s != i && s >= 0 && s < n) {
             from = row0(ctx + s);
@@ -352,34 +445,40 @@ __global__ void __launch_bounds__(kKThreads) cache_keep_path_kernel(const KeepPa
     const int h0 = blockIdx.y * p.heads_per_cta, heads = min(p.heads_per_cta, p.H - h0);
     const int per_row = heads * 2 * p.chunks;            // chunks of K, then of V, head by head
     const int rows = max(1, min(kKThreads * kKBatch / per_row, kKThreads / heads));   // a round's
+    // this thread's first chunk of a round (row i, chunk r of it), and its next ones' distance
+    const int i_first = tid / per_row, r_first = tid - i_first * per_row;
+    const int i_step = kKThreads / per_row, r_step = kKThreads - i_step * per_row;
+#pragma unroll 1
     for (int i0 = 0; i0 < m; i0 += rows) {
-        const int tasks = min(rows, m - i0) * per_row;
+        const int end = min(rows, m - i0);
         uint4 v[kKBatch];
         uint4* to[kKBatch];
         float sv = 0.0f;
         float* sto = nullptr;
+        int i = i_first, r = r_first;
 #pragma unroll
         for (int j = 0; j < kKBatch; ++j) {
-            const int t = tid + j * kKThreads;
             to[j] = nullptr;
-            if (t < tasks) {
-                const int i = t / per_row, r = t - i * per_row;
-                const int c = r / p.chunks, k = r - c * p.chunks;
-                const int64_t from = src[i0 + i];
-                if (from >= 0) {
-                    const int64_t head = (h0 + (c >> 1)) * head_step;
-                    uint4* base = reinterpret_cast<uint4*>((c & 1) ? p.vc : p.kc) + k;
-                    v[j] = base[(from + head) * p.chunks];
-                    to[j] = base + (dst[i0 + i] + head) * p.chunks;
-                }
+            if (i < end && src[i0 + i] >= 0) {
+                const int c = static_cast<int>(r * p.chunk_mul >> 20), k = r - c * p.chunks;
+                const int64_t head = (h0 + (c >> 1)) * head_step;
+                uint4* base = reinterpret_cast<uint4*>((c & 1) ? p.vc : p.kc) + k;
+                v[j] = base[(src[i0 + i] + head) * p.chunks];
+                to[j] = base + (dst[i0 + i] + head) * p.chunks;
+            }
+            i += i_step;
+            r += r_step;
+            if (r >= per_row) {
+                r -= per_row;
+                ++i;
             }
         }
-        if (tid < min(rows, m - i0) * heads) {
-            const int i = tid / heads;
-            if (src[i0 + i] >= 0) {
-                const int64_t head = (h0 + tid - i * heads) * head_step;
-                sv = p.ks[src[i0 + i] + head];
-                sto = p.ks + dst[i0 + i] + head;
+        if (tid < end * heads) {
+            const int si = tid / heads;
+            if (src[i0 + si] >= 0) {
+                const int64_t head = (h0 + tid - si * heads) * head_step;
+                sv = p.ks[src[i0 + si] + head];
+                sto = p.ks + dst[i0 + si] + head;
             }
         }
         __syncthreads();
@@ -387,7 +486,7 @@ __global__ void __launch_bounds__(kKThreads) cache_keep_path_kernel(const KeepPa
         for (int j = 0; j < kKBatch; ++j)
             if (to[j]) *to[j] = v[j];
         if (sto) *sto = sv;
-        __syncthreads();
+        if (i0 + rows < m) __syncthreads();
     }
 }
 
@@ -471,7 +570,7 @@ extern "C" pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache, 
     PA_REQUIRE(S1 <= kMaxNodes, PA_ERR_UNSUPPORTED, "%s: S1 %d > %d", name, S1, kMaxNodes);
     PA_REQUIRE(head_size % 16 == 0 && head_size <= 8192, PA_ERR_UNSUPPORTED,
                "%s: head_size %d (a multiple of 16 up to 8192)", name, head_size);
-    static_assert(2 * 2 * 8192 / 16 <= kKThreads * kKBatch, "a row of two heads fits a round");
+    static_assert(2 * 8192 / 16 <= kKThreads * kKBatch, "a head's row fits a round");
     PA_REQUIRE(B == 0 || new_act_seqs != kv_act_seqs, PA_ERR_INVALID,
                "%s: new_act_seqs must be another buffer than kv_act_seqs", name);
     PA_REQUIRE(aligned(key_cache, 16) && aligned(value_cache, 16) && aligned(key_scale_cache, 4), PA_ERR_INVALID,
@@ -494,7 +593,9 @@ extern "C" pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache, 
     p.num_blocks = num_blocks;
     p.max_blocks = max_blocks_per_seq;
     p.layout = layout;
-    p.heads_per_cta = NKV < 2 ? 1 : 2;
+    // a row of a CTA's heads fits a round
+    p.heads_per_cta = std::min(NKV, std::max(1, std::min(kKHeads, kKThreads * kKBatch / (2 * p.chunks))));
+    p.chunk_mul = (1u << 20) / p.chunks + 1;
     const int64_t gy = (NKV + p.heads_per_cta - 1) / p.heads_per_cta;
     PA_REQUIRE(gy <= 65535, PA_ERR_UNSUPPORTED, "%s: too many heads (%d)", name, NKV);
     cache_keep_path_kernel<<<dim3(static_cast<unsigned>(B), static_cast<unsigned>(gy)), kKThreads, 0,

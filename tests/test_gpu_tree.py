@@ -835,3 +835,29 @@ def test_calls_of_no_sequences():
     pa.tree_verify(no(2, 9, dt=torch.float32), None, no(2), no(2), no(2, dt=torch.float32), no(), no(2), no(2))
     pa.cache_keep_path(c["kc"], c["vc"], c["ks"], no(3), no(), no(2), no(), no(), layout=0)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_ties_and_their_neighbours(draft):
+    """u z Q equal to R (not below it: rejected), and one step to either side,
+    for the first draft and the same for the second after it."""
+    B, S1, V = 9, 3, 8
+    p = np.full((B, S1, V), 1 / 16, np.float32)
+    q = np.full((B, S1, V), 1 / 16, np.float32)
+    p[:, 0, 1], p[:, 0, 2], p[:, 0, 3] = 0.25, 0.3125 if draft else 0.375, 0.5
+    q[:, 0, 1], q[:, 0, 2] = 0.5, 0.25
+    step = np.float32(2.0 ** -24)
+    u = np.full((B, S1), 0.3, np.float32)
+    first = 0.5 if draft else 0.25                      # u Q = R, u = R
+    u[0, 1], u[1, 1], u[2, 1] = first - step / 2, first, first + step
+    u[3:, 1] = 0.9
+    c = dict(p=p, q=q if draft else None, tok=np.tile(np.array([0, 1, 2], np.int32), (B, 1)),
+             par=np.tile(np.array([-1, 0, 0], np.int32), (B, 1)), u=u, n=np.full(B, S1, np.int32))
+    # after the first is rejected: R = 0.0625 and 0.4375 elsewhere, z = 0.5, Q = 0.25;
+    # without draft_probs R = 0.375, z = 0.75
+    edge = np.float32(0.5)
+    for i, x in enumerate((edge - step, edge, edge + step, np.nextafter(edge, np.float32(0)),
+                           np.nextafter(edge, np.float32(1)), 0.0)):
+        u[3 + i, 2] = x
+    got = check_verify(c)[1][:, 1].tolist()
+    assert got[0] == 1 and 1 not in got[1:] and [x == 2 for x in got[3:]] == [True, False, False, True, False, True]
