@@ -7,15 +7,26 @@
 // and one write of each code: bound by those bytes on long prompts, by the
 // launch and one chain of dependent loads on a few tokens.
 //
-// A row's head_size values lie 8 to a lane, so that a BF16 row is one 16-byte
-// load per lane: 16 lanes per row of 128, two rows to a warp, and the sums and
-// maxima take four shuffles for both. A warp takes kSets of those, heads of one
-// token and of one kind (q, k or v), with all loads in flight at once: angles and
-// weights stay in registers over them. (A job of rows numbered straight through,
-// with a 64-bit division and its own angles for every row, took 188 us on the
-// 8192-token case.)
+// A row's head_size values lie 8 to a lane in two chunks of 4 channels: the two
+// of a rotary lane hold the two sides of its four pairs, so that the rotation
+// needs no other lane. A job is kSets sets of rows (two rows of 128 a set), heads
+// of one token and of one kind (q, k or v). The sets' sums and maxima are reduced
+// together, half of the sets to either lane at each of the first two steps, after
+// which a lane has one set's and does that set's scalar work; 1 / rms is left out
+// of the codes, which it cancels from, and goes into the scale alone.
+//
+// A warp takes a run of jobs, so that angles and weights last for a token's, and
+// has the next job's rows on their way to shared memory while it works on one.
+// 8192 tokens of 96 + 2 x 8 heads of 128: BF16 81 us (331 MB, 4.1 TB/s; the
+// instructions issue at 67% of the clocks, 550 a job of 8 rows), FP32 94 us (566 MB,
+// 6.0 TB/s). With a job a warp and its rows in registers BF16 took 107 us, FP32
+// 115; rotating through shuffles and reducing each set by itself (820
+// instructions) 113 and 137. Three or four jobs in flight change nothing (83, 84);
+// six CTAs an SM, at 80 registers with spills, 93. Few tokens: 16 take 6 us, 777 of
+// 48 + 2 x 8 heads 11.5 us.
 #include "common.cuh"
 
+#include <algorithm>
 #include <cmath>
 
 namespace pa {
@@ -23,6 +34,9 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kSets = 4;
+constexpr int kBlocks = 5;                   // CTAs an SM: 96 registers
+constexpr int kStages = 2;                   // jobs of a warp in shared memory
+constexpr int kJob = kSets * 256;            // values of a job's rows
 
 struct NormRopeParams {
     const void *q, *k, *v;
@@ -46,269 +60,336 @@ struct NormRopeParams {
     int num_batches;
     int64_t T;
     int NQ, NKV;
-    uint32_t q_jobs, kv_jobs;                // warps a token's q heads, its k (and v) heads take
+    uint32_t q_jobs, kv_jobs;                // jobs a token's q heads, its k (and v) heads make
+    uint32_t jobs, warps;
     int64_t num_blocks;
     int BS, layout;
 };
 
-__device__ __forceinline__ void unpack_bf16(uint4 v, float (&x)[8])
+// Four values as they lie in memory, unpacked where they are used.
+__device__ __forceinline__ float4 load_raw(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ uint2 load_raw(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
+__device__ __forceinline__ float4 load_smem(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ uint2 load_smem(const __nv_bfloat16* p) { return *reinterpret_cast<const uint2*>(p); }
+__device__ __forceinline__ void unpack(const float4& r, float2& a, float2& b)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    a = make_float2(r.x, r.y);
+    b = make_float2(r.z, r.w);
+}
+__device__ __forceinline__ void unpack(const uint2& r, float2& a, float2& b)
+{
+    a = make_float2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u));
+    b = make_float2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 times(float2 a, float f) { return __fmul2_rn(a, make_float2(f, f)); }
+
+// One copy of the four divisions for all callers: only a few warps come here.
+__device__ __noinline__ uint32_t value_codes(float2 a, float2 b, float4 s)
+{
+    return e4m3x4(s.x == 0.0f ? 0.0f : __fdiv_rn(a.x, s.x), s.y == 0.0f ? 0.0f : __fdiv_rn(a.y, s.y),
+                  s.z == 0.0f ? 0.0f : __fdiv_rn(b.x, s.z), s.w == 0.0f ? 0.0f : __fdiv_rn(b.y, s.w));
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8])
+// kSets values of a lane reduced over the `lpr` lanes of its row, set 2 (lane & 1)
+// + (lane >> 1 & 1) to this lane.
+template <bool MAX>
+__device__ __forceinline__ float reduce_sets(const float (&a)[kSets], int lane, int lpr)
 {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8])
-{
-    unpack_bf16(__ldg(reinterpret_cast<const uint4*>(p)), x);
-}
-
-// Eight values as they lie in memory, unpacked where they are used.
-template <typename T>
-struct Raw8;
-template <>
-struct Raw8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p)
-    {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float2 (&x)[4]) const
-    {
-        x[0] = make_float2(a.x, a.y); x[1] = make_float2(a.z, a.w);
-        x[2] = make_float2(b.x, b.y); x[3] = make_float2(b.z, b.w);
-    }
-};
-template <>
-struct Raw8<__nv_bfloat16> {
-    uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
-    __device__ __forceinline__ void get(float2 (&x)[4]) const
-    {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    static_assert(kSets == 4, "two steps halve the sets to one");
+    auto op = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
+    const bool b0 = lane & 1, b1 = lane & 2;
+    const float k0 = op(b0 ? a[2] : a[0], __shfl_xor_sync(0xffffffffu, b0 ? a[0] : a[2], 1));
+    const float k1 = op(b0 ? a[3] : a[1], __shfl_xor_sync(0xffffffffu, b0 ? a[1] : a[3], 1));
+    float v = op(b1 ? k1 : k0, __shfl_xor_sync(0xffffffffu, b1 ? k0 : k1, 2));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-    }
-};
-
-// Eight codes of y * (448 / amax). Where the quotient may leave the float range
-// both sides are first taken times a power of two.
-__device__ __forceinline__ uint2 encode8(float2 (&y)[4], float amax)
-{
-    if (!(amax >= 0x1p-100f && amax <= 0x1p100f)) {
-        if (amax == 0.0f) return make_uint2(0u, 0u);
-        const float up = amax < 1.0f ? 0x1p100f : 0x1p-100f;
-        amax *= up;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(y[e], make_float2(up, up));
-    }
-    const float inv = __fdividef(kE4M3Max, amax);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(y[e], make_float2(inv, inv));
-    return make_uint2(e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y), e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y));
+    for (int o = 4; o < lpr; o <<= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
 }
 
 template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 6) qkv_norm_rope_append_kernel(const NormRopeParams p)
+__global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel(const NormRopeParams p)
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = kSets * RPW;
-    const int lane = threadIdx.x & 31, sub = lane % LPR, d0 = 8 * sub;
-    const uint32_t job = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    __shared__ __align__(16) T ring[kThreads / 32][kStages][kJob];
+    const int lane = threadIdx.x & 31, sub = lane % LPR;
+    const uint32_t wid = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    T(*const mine)[kJob] = ring[threadIdx.x >> 5];
+    // this warp's jobs: the first jobs % warps warps have one more
+    const uint32_t per = p.jobs / p.warps, longer = p.jobs % p.warps;
+    const uint32_t begin = wid * per + min(wid, longer), end = begin + per + (wid < longer ? 1 : 0);
+    if (begin == end) return;
     const uint32_t per_token = p.q_jobs + 2 * p.kv_jobs;
-    const uint32_t tok = job / per_token;
-    if (tok >= p.T) return;
-    uint32_t part = job - tok * per_token;
-    const bool is_q = part < p.q_jobs, is_v = part >= p.q_jobs + p.kv_jobs;
-    if (!is_q) part -= is_v ? p.q_jobs + p.kv_jobs : p.q_jobs;
-    const int heads = is_q ? p.NQ : p.NKV;
-    const int h0 = static_cast<int>(part) * ROWS + lane / LPR;
-    const T* src = is_q ? static_cast<const T*>(p.q) + tok * p.qs
-                   : is_v ? static_cast<const T*>(p.v) + tok * p.vs
-                          : static_cast<const T*>(p.k) + tok * p.ks;
 
-    // (the angles wait for the position: it goes first)
-    int64_t pos = p.rd > 0 && !is_v ? load_slot(p.pos, p.pos_type, tok) : 0;
-    Raw8<T> raw[kSets];
+    // ---- rows on their way to shared memory, kStages - 1 jobs ahead ----
+    uint32_t ahead = begin, a_tok = begin / per_token, a_part = begin - a_tok * per_token;
+    int a_slot = 0;
+    auto fetch = [&] {
+        if (ahead < end) {
+            const bool q = a_part < p.q_jobs, v = a_part >= p.q_jobs + p.kv_jobs;
+            const uint32_t part = q ? a_part : a_part - p.q_jobs - (v ? p.kv_jobs : 0);
+            const T* src = (q ? static_cast<const T*>(p.q) + a_tok * p.qs
+                            : v ? static_cast<const T*>(p.v) + a_tok * p.vs
+                                : static_cast<const T*>(p.k) + a_tok * p.ks) + part * (ROWS * D);
+            const int left = ((q ? p.NQ : p.NKV) - static_cast<int>(part) * ROWS) * D;   // values; zeros behind
 #pragma unroll
-    for (int i = 0; i < kSets; ++i) {
-        const int h = h0 + i * RPW;
-        if (h < heads) raw[i].load(src + h * D + d0);
-        else raw[i].zero();
-    }
-    // where k and v go
-    int64_t row = -1, row_step = 0;          // cache row of head 0, from head to head
-    if (!is_q) {
-        const int64_t s = load_slot(p.slots, p.slot_type, tok);
-        if (s < 0 || s >= p.num_blocks * p.BS) return;
-        const int64_t blk = s / p.BS, off = s - blk * p.BS;
-        row = cache_row(p.layout, blk, off, 0, p.BS, p.NKV);
-        row_step = p.layout == PA_LAYOUT_BSND ? 1 : p.BS;
-    }
-    if (is_v) {
-        int tb = __ldg(p.token_batch + tok);
-        tb = tb < 0 ? 0 : (tb >= p.num_batches ? p.num_batches - 1 : tb);
-        const float* vs = p.v_scale + static_cast<int64_t>(tb) * p.NKV * D + d0;
+            for (int i = 0; i < kJob * static_cast<int>(sizeof(T)) / 512; ++i) {
+                const int at = (32 * i + lane) * (16 / static_cast<int>(sizeof(T)));
+                cp_async16(mine[a_slot] + at, src + (at < left ? at : 0), at < left ? 16 : 0);
+            }
+            if (++a_part == per_token) {
+                a_part = 0;
+                ++a_tok;
+            }
+            ++ahead;
+            a_slot = a_slot + 1 == kStages ? 0 : a_slot + 1;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    uint32_t tok = a_tok, part_all = a_part;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch();
+
+    int slot_now = 0;
+    bool fresh = true;                       // another token or kind than before
+    int64_t row = -1, row_step = 0;          // k, v: cache row of head 0, from head to head
+    int c0 = 0, c1 = 0;                      // this lane's chunks of 4 channels
+    bool rot0 = false, rot1 = false;
+    float2 wt[4], cs[2] = {}, sn[2] = {};    // its weights, the angles of its four pairs
+#pragma unroll 1
+    for (uint32_t job = begin; job < end; ++job) {
+        const bool is_q = part_all < p.q_jobs, is_v = part_all >= p.q_jobs + p.kv_jobs;
+        const uint32_t part = is_q ? part_all : part_all - p.q_jobs - (is_v ? p.kv_jobs : 0);
+        const uint32_t t_now = tok;
+        const T* const x = mine[slot_now];
+        const int heads = is_q ? p.NQ : p.NKV;
+        const int h0 = static_cast<int>(part) * ROWS + lane / LPR;
+        const void* w = is_q ? p.qw : p.kw;
+        if (fresh || part == 0) {
+            const int rd = is_v ? 0 : p.rd, half = rd >> 1;
+            int64_t pos = rd > 0 ? load_slot(p.pos, p.pos_type, t_now) : 0;
+            const int64_t s = is_q ? 0 : load_slot(p.slots, p.slot_type, t_now);
+            if (INTER) {
+                c0 = 4 * sub;
+                c1 = c0 + D / 2;
+            } else {
+                const bool in = 8 * sub < rd;
+                c0 = in ? 4 * sub : rd + 4 * (sub - (rd >> 3));
+                c1 = c0 + (in ? half : (D - rd) >> 1);
+            }
+            rot0 = c0 < rd;
+            rot1 = INTER ? c1 < rd : rot0;
+            if (!is_v) {
+                if (w == nullptr) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) wt[e] = make_float2(1.0f, 1.0f);
+                } else if (p.w_bf16) {
+                    unpack(load_raw(static_cast<const __nv_bfloat16*>(w) + c0), wt[0], wt[1]);
+                    unpack(load_raw(static_cast<const __nv_bfloat16*>(w) + c1), wt[2], wt[3]);
+                } else {
+                    unpack(load_raw(static_cast<const float*>(w) + c0), wt[0], wt[1]);
+                    unpack(load_raw(static_cast<const float*>(w) + c1), wt[2], wt[3]);
+                }
+            }
+            pos = pos < 0 ? 0 : (pos >= p.max_pos ? p.max_pos - 1 : pos);
+            const float* a = p.cos_sin + pos * rd;
+            if (INTER) {
+                if (rot0) {
+                    cs[0] = __ldg(reinterpret_cast<const float2*>(a + (c0 >> 1)));
+                    sn[0] = __ldg(reinterpret_cast<const float2*>(a + half + (c0 >> 1)));
+                }
+                if (rot1) {
+                    cs[1] = __ldg(reinterpret_cast<const float2*>(a + (c1 >> 1)));
+                    sn[1] = __ldg(reinterpret_cast<const float2*>(a + half + (c1 >> 1)));
+                }
+            } else if (rot0) {
+                unpack(load_raw(a + c0), cs[0], cs[1]);
+                unpack(load_raw(a + half + c0), sn[0], sn[1]);
+            }
+            row = -1;
+            row_step = p.layout == PA_LAYOUT_BSND ? 1 : p.BS;
+            if (!is_q && s >= 0 && s < p.num_blocks * p.BS) {
+                const int64_t blk = s >> 31 ? s / p.BS : static_cast<uint32_t>(s) / static_cast<uint32_t>(p.BS);
+                row = cache_row(p.layout, blk, s - blk * p.BS, 0, p.BS, p.NKV);
+            }
+            fresh = false;
+        }
+        // the next job
+        if (++part_all == per_token) {
+            part_all = 0;
+            ++tok;
+            fresh = true;
+        }
+        slot_now = slot_now + 1 == kStages ? 0 : slot_now + 1;
+        // (this warp is done with the slot that is filled now)
+        __syncwarp();
+        fetch();
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncwarp();
+        if (!is_q && row < 0) continue;          // no slot
+        const T* const lane_x = x + (lane / LPR) * D;
+        if (is_v) {
+            int tb = __ldg(p.token_batch + t_now);
+            tb = tb < 0 ? 0 : (tb >= p.num_batches ? p.num_batches - 1 : tb);
+            const float* vs = p.v_scale + static_cast<int64_t>(tb) * p.NKV * D;
+            float4 sc[kSets][2];
+#pragma unroll
+            for (int i = 0; i < kSets; ++i) {
+                const int h = min(h0 + i * RPW, heads - 1);
+                sc[i][0] = load_raw(vs + h * D + c0);
+                sc[i][1] = load_raw(vs + h * D + c1);
+            }
+#pragma unroll
+            for (int i = 0; i < kSets; ++i) {
+                const int h = h0 + i * RPW;
+                if (h >= heads) break;
+                uint8_t* out = p.vc + (row + h * row_step) * D;
+                float2 a, b;
+                unpack(load_smem(lane_x + i * RPW * D + c0), a, b);
+                *reinterpret_cast<uint32_t*>(out + c0) = value_codes(a, b, sc[i][0]);
+                unpack(load_smem(lane_x + i * RPW * D + c1), a, b);
+                *reinterpret_cast<uint32_t*>(out + c1) = value_codes(a, b, sc[i][1]);
+            }
+            continue;
+        }
+        auto rotate = [&](float2 (&y)[4]) {
+            if (INTER) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (e < 2 ? rot0 : rot1) {
+                        const float c = (e & 1) ? cs[e >> 1].y : cs[e >> 1].x;
+                        const float n = (e & 1) ? sn[e >> 1].y : sn[e >> 1].x;
+                        y[e] = make_float2(y[e].x * c - y[e].y * n, y[e].y * c + y[e].x * n);
+                    }
+                }
+            } else if (rot0) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 a = y[e], b = y[e + 2];
+                    y[e] = __ffma2_rn(b, make_float2(-sn[e].x, -sn[e].y), __fmul2_rn(a, cs[e]));
+                    y[e + 2] = __ffma2_rn(a, sn[e], __fmul2_rn(b, cs[e]));
+                }
+            }
+        };
+        auto max_of = [](const float2 (&y)[4]) {
+            float m = fmaxf(fabsf(y[0].x), fabsf(y[0].y));
+#pragma unroll
+            for (int e = 1; e < 4; ++e) m = fmaxf(fmaxf(m, fabsf(y[e].x)), fabsf(y[e].y));
+            return m;
+        };
+        const int64_t q0 = static_cast<int64_t>(t_now) * p.NQ + h0;
+        uint8_t* dst = is_q ? p.q_codes + q0 * D : p.kc + (row + h0 * row_step) * D;
+        const int64_t dst_step = (is_q ? RPW : RPW * row_step) * D;
+        float* const scale = is_q ? p.q_scale + q0 : p.k_scale + row + h0 * row_step;
+        const int64_t scale_step = is_q ? RPW : RPW * row_step;
+        // ---- z = x w, rotated; the sets' sums of x^2 and maxima of |z| ----
+        float2 z[kSets][4];
+        float ss[kSets], amax[kSets];
 #pragma unroll
         for (int i = 0; i < kSets; ++i) {
-            const int h = h0 + i * RPW;
-            if (h >= heads) break;
-            float2 x[4];
-            float sc[8], z[8];
-            raw[i].get(x);
-            load8(vs + h * D, sc);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                z[e] = sc[e] == 0.0f ? 0.0f : __fdiv_rn((e & 1) ? x[e >> 1].y : x[e >> 1].x, sc[e]);
-            uint2 c;
-            c.x = e4m3x4(z[0], z[1], z[2], z[3]);
-            c.y = e4m3x4(z[4], z[5], z[6], z[7]);
-            *reinterpret_cast<uint2*>(p.vc + (row + h * row_step) * D + d0) = c;
-        }
-        return;
-    }
-    // ---- this lane's weights and angles ----
-    const void* w = is_q ? p.qw : p.kw;
-    float2 wt[4];
-    {
-        float t[8];
-        if (w == nullptr) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] = 1.0f;
-        } else if (p.w_bf16) {
-            load8(static_cast<const __nv_bfloat16*>(w) + d0, t);
-        } else {
-            load8(static_cast<const float*>(w) + d0, t);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) wt[e] = make_float2(t[2 * e], t[2 * e + 1]);
-    }
-    const int half = p.rd >> 1;
-    const bool rot = d0 < p.rd, low = d0 < half;
-    // channel i's partner sits rd / 16 lanes up or down (INTER: in the same lane)
-    const int from = lane + (!INTER && rot ? (low ? half >> 3 : -(half >> 3)) : 0);
-    float2 cs[4], sn[4];                     // per channel (INTER: a pair's in both)
-    if (rot) {
-        pos = pos < 0 ? 0 : (pos >= p.max_pos ? p.max_pos - 1 : pos);
-        const float* a = p.cos_sin + pos * p.rd;
-        if constexpr (INTER) {
-            const float4 c4 = __ldg(reinterpret_cast<const float4*>(a + (d0 >> 1)));
-            const float4 s4 = __ldg(reinterpret_cast<const float4*>(a + half + (d0 >> 1)));
-            cs[0] = make_float2(c4.x, c4.x); cs[1] = make_float2(c4.y, c4.y);
-            cs[2] = make_float2(c4.z, c4.z); cs[3] = make_float2(c4.w, c4.w);
-            sn[0] = make_float2(-s4.x, s4.x); sn[1] = make_float2(-s4.y, s4.y);
-            sn[2] = make_float2(-s4.z, s4.z); sn[3] = make_float2(-s4.w, s4.w);
-        } else {
-            float t[8];
-            load8(a + (low ? d0 : d0 - half), t);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) cs[e] = make_float2(t[2 * e], t[2 * e + 1]);
-            load8(a + half + (low ? d0 : d0 - half), t);
-            const float sign = low ? -1.0f : 1.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sn[e] = make_float2(sign * t[2 * e], sign * t[2 * e + 1]);
-        }
-    }
-    // this lane's 8 codes of head h0, and from one set to the next
-    uint8_t* dst = is_q ? p.q_codes + (static_cast<int64_t>(tok) * p.NQ + h0) * D + d0
-                        : p.kc + (row + h0 * row_step) * D + d0;
-    const int64_t dst_step = (is_q ? RPW : RPW * row_step) * D;
-    float mine = 0.0f;                       // max|y| of the row whose scale this lane writes
-#pragma unroll
-    for (int i = 0; i < kSets; ++i, dst += dst_step) {
-        // every lane takes part in the shuffles, whatever its row is
-        float2 y[4];
-        raw[i].get(y);
-        if (w != nullptr) {
+            float2 (&y)[4] = z[i];
+            unpack(load_smem(lane_x + i * RPW * D + c0), y[0], y[1]);
+            unpack(load_smem(lane_x + i * RPW * D + c1), y[2], y[3]);
             float2 s2 = __fmul2_rn(y[0], y[0]);
 #pragma unroll
             for (int e = 1; e < 4; ++e) s2 = __ffma2_rn(y[e], y[e], s2);
-            float ss = s2.x + s2.y, sc = 1.0f;
+            ss[i] = s2.x + s2.y;
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            // squares that leave the float range (or, with no eps to speak of, vanish
-            // below it) are taken of x * 2^-64 (2^64)
-            const bool big = !(ss <= 1e38f), small = ss < 1e-30f && p.eps < 1e-20f;
-            if (__any_sync(0xffffffffu, big || small)) {
-                sc = big ? 0x1p-64f : (small ? 0x1p64f : 1.0f);
-                ss = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 t = __fmul2_rn(y[e], make_float2(sc, sc));
-                    ss += t.x * t.x + t.y * t.y;
-                }
-#pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            }
-            const float ms = ss * (1.0f / D) + p.eps * sc * sc;
-            const float inv = ms == 0.0f ? 0.0f : rsqrtf(ms) * sc;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(__fmul2_rn(y[e], make_float2(inv, inv)), wt[e]);
+            for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(y[e], wt[e]);
+            rotate(y);
+            amax[i] = max_of(y);
         }
-        if (INTER || p.rd > 0) {
-            float2 o[4];
+        const int own = 2 * (lane & 1) + (lane >> 1 & 1);        // the set this lane reduces
+        const float ss_own = reduce_sets<false>(ss, lane, LPR), amax_own = reduce_sets<true>(amax, lane, LPR);
+        // Squares, products or quotients out of the comfortable range, a row of zeros among
+        // them: row by row in the order that keeps all in it.
+        const bool fine = (w == nullptr || (ss_own <= 1e38f && ss_own >= 1e-30f)) && amax_own >= 0x1p-100f &&
+                          amax_own <= 0x1p100f;
+        if (__any_sync(0xffffffffu, !fine && h0 + own * RPW < heads)) {
+#pragma unroll 1
+            for (int i = 0; i < kSets; ++i, dst += dst_step) {
+                const bool in = h0 + i * RPW < heads;
+                float2 y[4];
+                unpack(load_smem(lane_x + i * RPW * D + c0), y[0], y[1]);
+                unpack(load_smem(lane_x + i * RPW * D + c1), y[2], y[3]);
+                float rms = 1.0f;
+                if (w != nullptr) {
+                    // times 2^64 or 2^-80 where squares would leave the range, then normalised
+                    float t = max_of(y);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (INTER) {
-                    o[e] = make_float2(y[e].y, y[e].x);
-                } else {
-                    o[e].x = __shfl_sync(0xffffffffu, y[e].x, from);
-                    o[e].y = __shfl_sync(0xffffffffu, y[e].y, from);
+                    for (int o = LPR / 2; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                    const float f = t > 0x1p56f ? 0x1p-80f : (t < 0x1p-60f ? 0x1p64f : 1.0f);
+                    t = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        y[e] = times(y[e], f);
+                        t += y[e].x * y[e].x + y[e].y * y[e].y;
+                    }
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+                    // (under an eps of 1e-20 and more, squares below 2^-120 do not count; the
+                    // power of two then goes into the scale)
+                    const bool eps_alone = f > 1.0f && p.eps >= 1e-20f;
+                    const float ms = eps_alone ? p.eps : t * (1.0f / D) + p.eps * f * f;
+                    const float inv = ms == 0.0f ? 0.0f : rsqrtf(ms);
+                    rms = eps_alone ? 0x1p-64f : 1.0f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = __fmul2_rn(times(y[e], inv), wt[e]);
                 }
-            }
-            if (rot) {
+                rotate(y);
+                float m = max_of(y);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = __ffma2_rn(o[e], sn[e], __fmul2_rn(y[e], cs[e]));
+                for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const float up = m < 0x1p-100f ? 0x1p100f : (m > 0x1p100f ? 0x1p-100f : 1.0f);
+                const float f = m == 0.0f ? 0.0f : __fdividef(kE4M3Max, m * up);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = times(times(y[e], up), f);
+                if (!in) continue;
+                *reinterpret_cast<uint32_t*>(dst + c0) = m == 0.0f ? 0u : e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y);
+                *reinterpret_cast<uint32_t*>(dst + c1) = m == 0.0f ? 0u : e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y);
+                if (sub == 0) scale[i * scale_step] = __fdiv_rn(m, kE4M3Max) * rms;
+            }
+            continue;
+        }
+        // ---- codes z (448 / max|z|), and the scales ----
+        const float f_own = __fdividef(kE4M3Max, amax_own);
+#pragma unroll
+        for (int i = 0; i < kSets; ++i, dst += dst_step) {
+            const float f = __shfl_sync(0xffffffffu, f_own, (lane - sub) + (i >> 1) + 2 * (i & 1));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[i][e] = times(z[i][e], f);
+            if (h0 + i * RPW < heads) {
+                *reinterpret_cast<uint32_t*>(dst + c0) = e4m3x4(z[i][0].x, z[i][0].y, z[i][1].x, z[i][1].y);
+                *reinterpret_cast<uint32_t*>(dst + c1) = e4m3x4(z[i][2].x, z[i][2].y, z[i][3].x, z[i][3].y);
             }
         }
-        float amax = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) amax = fmaxf(fmaxf(amax, fabsf(y[e].x)), fabsf(y[e].y));
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        mine = sub == i ? amax : mine;
-        if (h0 + i * RPW < heads) *reinterpret_cast<uint2*>(dst) = encode8(y, amax);
+        const float s = __fdiv_rn(amax_own, kE4M3Max);
+        if (sub < kSets && h0 + own * RPW < heads)
+            scale[own * scale_step] = w == nullptr ? s : s * rsqrtf(ss_own * (1.0f / D) + p.eps);
     }
-    // the scales of all rows at once: lane i of a row's lanes has set i's
-    const int h = h0 + sub * RPW;
-    if (sub < kSets && h < heads)
-        (is_q ? p.q_scale + static_cast<int64_t>(tok) * p.NQ + h : p.k_scale + row + h * row_step)[0] =
-            __fdiv_rn(mine, kE4M3Max);
 }
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 template <typename T, int D>
-void launch(NormRopeParams p, bool inter, cudaStream_t st)
+void launch(NormRopeParams p, bool inter, int sms, cudaStream_t st)
 {
     constexpr uint32_t rows = kSets * (32 / (D / 8));        // rows a warp takes
     p.q_jobs = (p.NQ + rows - 1) / rows;
     p.kv_jobs = (p.NKV + rows - 1) / rows;
-    constexpr int warps = kThreads / 32;
-    const unsigned grid = static_cast<unsigned>((p.T * (p.q_jobs + 2 * p.kv_jobs) + warps - 1) / warps);
-    if (inter) qkv_norm_rope_append_kernel<T, D, true><<<grid, kThreads, 0, st>>>(p);
-    else qkv_norm_rope_append_kernel<T, D, false><<<grid, kThreads, 0, st>>>(p);
+    p.jobs = static_cast<uint32_t>(p.T) * (p.q_jobs + 2 * p.kv_jobs);
+    constexpr uint32_t warps = kThreads / 32;
+    const uint32_t ctas = std::min((p.jobs + warps - 1) / warps, static_cast<uint32_t>(sms * kBlocks));
+    p.warps = ctas * warps;
+    if (inter) qkv_norm_rope_append_kernel<T, D, true><<<ctas, kThreads, 0, st>>>(p);
+    else qkv_norm_rope_append_kernel<T, D, false><<<ctas, kThreads, 0, st>>>(p);
 }
 
 template <typename T>
-void launch_d(const NormRopeParams& p, int D, bool inter, cudaStream_t st)
+void launch_d(const NormRopeParams& p, int D, bool inter, int sms, cudaStream_t st)
 {
-    if (D == 64) launch<T, 64>(p, inter, st);
-    else if (D == 128) launch<T, 128>(p, inter, st);
-    else launch<T, 256>(p, inter, st);
+    if (D == 64) launch<T, 64>(p, inter, sms, st);
+    else if (D == 128) launch<T, 128>(p, inter, sms, st);
+    else launch<T, 256>(p, inter, sms, st);
 }
 
 }  // namespace
@@ -391,7 +472,9 @@ extern "C" pa_status pa_fp8_qkv_norm_rope_append(
     p.BS = block_size;
     p.layout = layout;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (in_dtype == PA_DTYPE_F32) launch_d<float>(p, head_size, interleaved != 0, st);
-    else launch_d<__nv_bfloat16>(p, head_size, interleaved != 0, st);
+    const int sms = device_sm_count();
+    PA_REQUIRE(sms > 0, PA_ERR_CUDA, "%s: cannot query the device", name);
+    if (in_dtype == PA_DTYPE_F32) launch_d<float>(p, head_size, interleaved != 0, sms, st);
+    else launch_d<__nv_bfloat16>(p, head_size, interleaved != 0, sms, st);
     return check_launch(name);
 }

@@ -247,7 +247,10 @@ def check_codes(y, code, scale, check_scale=True):
     """E4M3 codes against y: half a step (2^-4 of the value, 2^-10 where the
     code is subnormal) plus the FP32 arithmetic before them, 64 roundings of
     2^-24 of the row's maximum (448 codes). The scale is a float: below 2^-126
-    its step is 2^-149 whatever its value, so half of that is added."""
+    its step is 2^-149 whatever its value, so half of that is added. The same
+    holds of y, which is FP32 by definition: where it lies below 2^-126 each of
+    the 64 roundings is half of 2^-149, or 2^-150 / scale in codes, and not 2^-24
+    of it."""
     amax = y.abs().amax(-1)
     s = amax / 448
     if check_scale:
@@ -255,6 +258,7 @@ def check_codes(y, code, scale, check_scale=True):
     want = y / torch.where(s == 0, 1.0, s)[..., None]
     got = H.value(code)
     tol = 2.0 ** -4 * want.abs() + 2.0 ** -10 + 448 * 2.0 ** -18
+    tol = tol + torch.where((amax > 0) & (amax < 2.0 ** -126), 64 * 2.0 ** -150 / torch.where(s == 0, 1.0, s), 0.0)[..., None]
     assert ((got - want).abs() <= tol).all(), float(((got - want).abs() - tol).max())
 
 
@@ -861,3 +865,17 @@ def test_verify_ties_and_their_neighbours(draft):
         u[3 + i, 2] = x
     got = check_verify(c)[1][:, 1].tolist()
     assert got[0] == 1 and 1 not in got[1:] and [x == 2 for x in got[3:]] == [True, False, False, True, False, True]
+
+
+@pytest.mark.parametrize("D,rd,inter", [(64, 32, False), (128, 128, True), (256, 64, False)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_append_rows_at_the_ends_of_the_range(D, rd, inter, norm):
+    """Rows whose squares leave the float range on either side, rows of zeros and
+    weights of 2^-100 beside ordinary rows of the same call."""
+    c = append_case(95 + D, 24, 9, 3, D, rd, torch.float32, 1, wdt=torch.float32)
+    for t, f in ((1, 2.0 ** 60), (2, 2.0 ** 100), (3, 2.0 ** 122), (4, 2.0 ** -60), (5, 2.0 ** -100), (6, 0.0),
+                 (8, 2.0 ** -20), (9, 2.0 ** 20)):
+        c["qkv"][t] *= f
+    c["kw"] *= 2.0 ** -100
+    eps = 1e-5 if D == 128 else 1e-30
+    check_append(c, run_append(c, eps=eps, inter=inter, norm=norm), eps=eps, inter=inter, norm=norm)
