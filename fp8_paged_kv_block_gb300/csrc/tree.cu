@@ -28,7 +28,13 @@
 // 2 x 128, P 2 x 64), and S of a warpgroup's next block is computed while it works
 // on the last. They share m, row by row: a warp decides on m for its block after
 // the other warpgroup's warp has decided on the block before, and only the
-// exponentials wait for that.
+// exponentials wait for that. A block then takes about 1800 clocks; HBM would
+// take 1400.
+//
+// Measured: 4 sequences of up to 131072 keys x 5 x 96 heads over 8: 129 us (648 MB,
+// 5.0 TB/s; steps of 64 keys with twice the buffers 147, three warpgroups 151); 16
+// of up to 4096 x 64: 128 us (111 GFLOP, 0.87 PFLOP/s, of items of 16 blocks on
+// average); the same x 8: 32 us; 2 of up to 300 keys x 8 x 4 heads: 10 us.
 //   warps 0-7        softmax, warpgroup k of blocks k, k + 2, .. (thread = row =
 //                    tensor memory lane)
 //   warp 8           K and V blocks by TMA, key scales by cp.async
@@ -78,11 +84,11 @@ constexpr uint32_t kTmemCols = 512, kSCol = 128, kPCol = kSCol + kTurns * kBS;  
 constexpr float kRaise = 8.0f;               // log2 units: see the top of the file
 constexpr float kShift = 7.0f;
 
-// What an item costs besides its blocks, in blocks: the first S, the last P V and
-// its output, which nothing of the next item overlaps. 4, 6, 8: 143, 135, 130 us on
-// 16 sequences of up to 4096 keys (as 1 to 4096 fall out) x 64 drafted tokens x 96
-// heads over 8, 32.2, 32.8, 32.9 us with 8 drafted tokens.
-constexpr int kItemCost = 8;
+// What an item costs besides its blocks, in blocks: the last block's softmax and
+// P V, its output and the first softmax of the next item, about 10000 clocks.
+// 5, 6, 7: 133, 128, 127 us on 16 sequences of up to 4096 keys (as 1 to 4096 fall
+// out) x 64 drafted tokens x 96 heads over 8, 31.4, 31.7, 32.8 with 8 drafted tokens.
+constexpr int kItemCost = 6;
 
 // What the joining kernel has to know of the item at the begin of a run.
 struct Cut {
@@ -513,12 +519,6 @@ __device__ void q_loader(TreeSmem& sm, const TreeParams& p, Run run, int lane)
     }
 }
 
-// Position of 16-byte unit u of row r in a warp's 32 x 64-byte staging area.
-__device__ __forceinline__ uint32_t stage_at(int r, int u)
-{
-    return static_cast<uint32_t>(r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
-}
-
 // Warpgroup w: blocks w, w + kTurns, ..; the thread of row `row`.
 __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tmem, int w, int q4, int lane)
 {
@@ -528,26 +528,49 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
     const int mine = 2 + kTurns * q4 + w, theirs = 2 + kTurns * q4 + (w + kTurns - 1) % kTurns;
     const uint32_t O = tmem + (static_cast<uint32_t>(32 * q4) << 16);
     const uint32_t S = O + kSCol + kBS * w, P = O + kPCol + kBS / 2 * w;
+    // The next segment, and the row's mask in it, one bit per drafted token: a ballot
+    // per node of the warp's rows and 32 drafted tokens, eight of them loaded at once.
     Seg s;
-    int g0 = 0, turn = 0, next = w;          // blocks in all so far, own ones, the next own one
-    for (int seg = 0; next_seg(sm.cum, sm.len, p.G, run, s); ++seg) {
-        const int act = static_cast<int>(sm.len[s.b] >> 8), n = static_cast<int>(sm.len[s.b] & 0xFF), ctx = act - n;
-        const bool warp_live = 32 * q4 < s.rows, live = row < s.rows;
-        // ---- the row's mask, one bit per drafted token ----
-        uint64_t m_lo = 0, m_hi = 0;
-        if (warp_live && s.t1 * kBS > ctx) {
-            const int first = node_of(p, s.row0 + 32 * q4), own = node_of(p, s.row0 + row);
-            const int last = node_of(p, s.row0 + min(32 * q4 + 31, s.rows - 1));
+    uint64_t m_lo = 0, m_hi = 0;
+    auto advance = [&] {
+        if (!next_seg(sm.cum, sm.len, p.G, run, s)) return false;
+        const int act = static_cast<int>(sm.len[s.b] >> 8), n = static_cast<int>(sm.len[s.b] & 0xFF);
+        m_lo = m_hi = 0;
+        if (32 * q4 >= s.rows || s.t1 * kBS <= act - n) return true;
+        const int first = node_of(p, s.row0 + 32 * q4), own = node_of(p, s.row0 + row);
+        const int last = node_of(p, s.row0 + min(32 * q4 + 31, s.rows - 1));
+        const uint8_t* mr = p.mask + s.b * p.mask_stride + static_cast<int64_t>(first) * p.S1;
+        int node = first, j = 0;
 #pragma unroll 1
-            for (int node = first; node <= last; ++node) {
-                const uint8_t* mr = p.mask + s.b * p.mask_stride + static_cast<int64_t>(node) * p.S1;
-#pragma unroll 1
-                for (int j = 0; j < n; j += 32) {
-                    const uint32_t bits = __ballot_sync(0xffffffffu, j + lane < n && __ldg(mr + min(j + lane, p.S1 - 1)));
-                    if (node == own) (j < 64 ? m_lo : m_hi) |= static_cast<uint64_t>(bits) << (j & 32);
+        while (node <= last) {
+            int nodes[8], js[8];
+            bool see[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                nodes[i] = node;
+                js[i] = j;
+                see[i] = node <= last && j + lane < n && __ldg(mr + j + lane);
+                j += 32;
+                if (j >= n) {
+                    j = 0;
+                    ++node;
+                    mr += p.S1;
                 }
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t bits = __ballot_sync(0xffffffffu, see[i]);
+                if (nodes[i] == own) (js[i] < 64 ? m_lo : m_hi) |= static_cast<uint64_t>(bits) << (js[i] & 32);
+            }
         }
+        return true;
+    };
+    int g0 = 0, turn = 0, next = w;          // blocks in all so far, own ones, the next own one
+    bool more = advance();
+#pragma unroll 1
+    for (int seg = 0; more; ++seg) {
+        const int ctx = static_cast<int>(sm.len[s.b] >> 8) - static_cast<int>(sm.len[s.b] & 0xFF);
+        const bool warp_live = 32 * q4 < s.rows, live = row < s.rows;
         wait_for(&sm.q_full[seg & 1], (seg >> 1) & 1, p.err, 64, &sm.abort);
         float rs = live ? sm.qs[seg & 1][row] * p.scale_log2 : 1.0f;
         // the maximum of S k_scale has to stay one under a negative scale: S changes sign
@@ -689,6 +712,9 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
         sm.ml[0][w][row] = m;
         sm.ml[1][w][row] = l;
         named_bar_sync(1, 4 * kTurns * 32);
+        // (the next segment's, while the last P V goes on)
+        const Seg done = s;
+        more = advance();
         // the last P V, and with it all (one accumulator: they complete in order);
         // behind the barrier, as its warpgroup waited for this barrier's last phase
         wait_for(&sm.o_done[(g_end - 1) % kTurns], ((g_end - 1) / kTurns) & 1, p.err, 128, &sm.abort);
@@ -701,56 +727,35 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                 const float mk = sm.ml[0][k][row];
                 lt += sm.ml[1][k][row] * (mk == mf ? 1.0f : ex2(mk - mf));
             }
-            const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+            const bool whole = done.t0 == 0 && done.t1 == done.tiles;
             const float inv = lt == 0.0f ? 0.0f : __fdiv_rn(1.0f, lt);
-            const int at = live ? q_row(p, s, row) : -1;
-            float* const part = part_of(p, blockIdx.x, s.first);
-            // Rows leave in 64-byte pieces (32 BF16 channels, 16 FP32) staged in this
-            // warp's 2 KB of the Q tile (every S of the segment is computed): a store
-            // covers eight rows' pieces instead of 16 bytes of 32 rows.
-            uint8_t* const stage = sm.q[seg & 1] + (4 * w + q4) * 2048;
+            const int at = live ? q_row(p, done, row) : -1;
+            float* const part = part_of(p, blockIdx.x, done.first);
 #pragma unroll 1
             for (int c = w; c < kD / 32; c += kTurns) {
                 float o[32];
                 tmem_ld32(O + 32 * c, o);
                 tmem_wait_ld();
-                // BF16: one piece; FP32: two
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    if (whole) {
-                        const float4* vs = reinterpret_cast<const float4*>(sm.vs[seg & 1] + 32 * c + 16 * b);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float4 a = vs[2 * k], e = vs[2 * k + 1];
-                            const float* x = o + 16 * b + 8 * k;
-                            const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * inv * a.x, x[1] * inv * a.y);
-                            const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * inv * a.z, x[3] * inv * a.w);
-                            const __nv_bfloat162 y2 = __floats2bfloat162_rn(x[4] * inv * e.x, x[5] * inv * e.y);
-                            const __nv_bfloat162 y3 = __floats2bfloat162_rn(x[6] * inv * e.z, x[7] * inv * e.w);
-                            *reinterpret_cast<uint4*>(stage + stage_at(lane, 2 * b + k)) = make_uint4(
-                                *reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1),
-                                *reinterpret_cast<const uint32_t*>(&y2), *reinterpret_cast<const uint32_t*>(&y3));
-                        }
-                        if (b == 0) continue;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<float4*>(stage + stage_at(lane, k)) =
-                                make_float4(o[16 * b + 4 * k], o[16 * b + 4 * k + 1], o[16 * b + 4 * k + 2],
-                                            o[16 * b + 4 * k + 3]);
-                    }
-                    __syncwarp();
+                if (!live) continue;
+                if (whole) {
+                    const float4* vs = reinterpret_cast<const float4*>(sm.vs[seg & 1] + 32 * c);
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(at) * kD + 32 * c);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int r = 8 * k + (lane >> 2);
-                        const int to = __shfl_sync(0xffffffffu, at, r);
-                        const uint4 x = *reinterpret_cast<const uint4*>(stage + stage_at(r, lane & 3));
-                        if (to < 0) continue;
-                        uint4* dst = whole ? reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(to) * kD + 32 * c)
-                                           : reinterpret_cast<uint4*>(part + (32 * q4 + r) * kD + 32 * c + 16 * b);
-                        dst[lane & 3] = x;
+                        const float4 a = vs[2 * k], e = vs[2 * k + 1];
+                        const float* x = o + 8 * k;
+                        const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * inv * a.x, x[1] * inv * a.y);
+                        const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * inv * a.z, x[3] * inv * a.w);
+                        const __nv_bfloat162 y2 = __floats2bfloat162_rn(x[4] * inv * e.x, x[5] * inv * e.y);
+                        const __nv_bfloat162 y3 = __floats2bfloat162_rn(x[6] * inv * e.z, x[7] * inv * e.w);
+                        dst[k] = make_uint4(
+                            *reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1),
+                            *reinterpret_cast<const uint32_t*>(&y2), *reinterpret_cast<const uint32_t*>(&y3));
                     }
-                    __syncwarp();
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(part + row * kD + 32 * c);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 }
             }
             if (!whole && live && w == 0) {

@@ -564,7 +564,7 @@ PA_API pa_status pa_fp8_qkv_norm_rope_append(
  * do not matter; E4M3 NaN codes below it are out of contract.
  * D, block_size  128 and 128 (else PA_ERR_UNSUPPORTED). S1 at most 128, NQ /
  * NKV at most 128, B at most 1024, max_blocks_per_seq * 128 below 2^24, and
- * 9 * ceil(S1 * NQ / NKV / 128) * NKV * B * max_blocks_per_seq below 2^32 (else
+ * 7 * ceil(S1 * NQ / NKV / 128) * NKV * B * max_blocks_per_seq below 2^32 (else
  * PA_ERR_UNSUPPORTED).
  * workspace    at least pa_fp8_tree_decode_workspace_size() bytes, 256-byte
  *              aligned, its first 256 bytes zero before the first call (every
