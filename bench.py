@@ -63,8 +63,8 @@ OVERLAP_APPEND = True
 # DRAM traffic of one decode launch on this workload, from an ncu capture
 # (dram__bytes_read.sum + dram__bytes_write.sum), valid only for the kernel
 # sources it was taken with.
-DECODE_TRAFFIC = {"sources_sha1": "913e24342602e851b8cd2947e066b3eae93f7761",
-                  "bytes_per_launch": 57871104 + 116736}
+DECODE_TRAFFIC = {"sources_sha1": "9d4e79883dcc02b9e243733e33b6620daa0d42df",
+                  "bytes_per_launch": 57871616 + 126720}
 
 
 def parse_args(argv=None):
@@ -1099,8 +1099,8 @@ MLA_VARIANTS = 2          # top-k selections rotated between steps (each ~172 MB
 # valid only for the kernel source it was taken with.
 # Captured on the 16-sequence case and scaled by the selected rows (x4): each
 # row is read from DRAM once, so the traffic grows in proportion.
-MLA_TRAFFIC = {"sources_sha1": "0d68231f9ece537b28bc832b8f9d4feb72772394", "format": "page",
-               "bytes_per_launch": 4 * (54289152 + 336640)}
+MLA_TRAFFIC = {"sources_sha1": "873bd441168e0c595677623988589fac528de244", "format": "page",
+               "bytes_per_launch": 4 * (54289920 + 344832)}
 
 
 def mla_sources_sha1() -> str:
