@@ -31,10 +31,10 @@
 // exponentials wait for that. A block then takes about 1800 clocks; HBM would
 // take 1400.
 //
-// Measured: 4 sequences of up to 131072 keys x 5 x 96 heads over 8: 129 us (648 MB,
-// 5.0 TB/s; steps of 64 keys with twice the buffers 147, three warpgroups 151); 16
-// of up to 4096 x 64: 128 us (111 GFLOP, 0.87 PFLOP/s, of items of 16 blocks on
-// average); the same x 8: 32 us; 2 of up to 300 keys x 8 x 4 heads: 10 us.
+// Measured: 4 sequences of up to 131072 keys x 5 x 96 heads over 8: 128 us (648 MB,
+// 5.1 TB/s; steps of 64 keys with twice the buffers 147, three warpgroups 151); 16
+// of up to 4096 x 64: 129 us (111 GFLOP, 0.86 PFLOP/s, of items of 16 blocks on
+// average); the same x 8: 31 us; 2 of up to 300 keys x 8 x 4 heads: 10 us.
 //   warps 0-7        softmax, warpgroup k of blocks k, k + 2, .. (thread = row =
 //                    tensor memory lane)
 //   warp 8           K and V blocks by TMA, key scales by cp.async
@@ -937,8 +937,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of the items that a run's end cut: CTA (c, y) takes the item
 // whose first block run c has and whose last one a later run, a warp two rows of it
-// and four parts at once (so that their loads overlap).
-constexpr int kJoinWarps = 8, kJoinRows = 2;
+// and four parts at once, all their loads in flight together. Launched early, it
+// still adds 4 to 5 us to a call: the decode's CTAs leave no room beside them, so
+// it starts when they end, and its loads are a chain of two (the cut, then parts).
+// (Factors from all maxima first, a third link, took 1.5 us more on 131072 keys;
+// joining in the decode's own last CTAs lost more in the decode than this costs.)
+constexpr int kJoinWarps = 4, kJoinRows = 2, kJoinParts = 4;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreeParams p)
 {
@@ -958,6 +962,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
     // O's part of run c (its rows begin there), m and l behind the rows; rows
     // past the item's last are read from it and not written
     auto part = [&](int c) { return p.part + (c == c0 ? slot0 : 2 * c) * slot_floats; };
+    const float4 v =
+        __ldg(reinterpret_cast<const float4*>(p.v_scale + static_cast<int64_t>(s.b * p.NKV + s.h) * kD) + lane);
     int row[kJoinRows];
     float M[kJoinRows], L[kJoinRows];
     float4 o[kJoinRows];
@@ -968,34 +974,37 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
         L[r] = 0.0f;
         o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    // in order, with a running maximum, so that no load waits for another
 #pragma unroll 1
-    for (int c = c0 + lane; c <= c1; c += 32) {
-        const float* ml = part(c) + static_cast<int64_t>(p.part_rows) * kD;
+    for (int c = c0; c <= c1; c += kJoinParts) {
+        float m[kJoinParts][kJoinRows], l[kJoinParts][kJoinRows];
+        float4 x[kJoinParts][kJoinRows];
 #pragma unroll
-        for (int r = 0; r < kJoinRows; ++r) M[r] = fmaxf(M[r], ml[row[r]]);
-    }
+        for (int i = 0; i < kJoinParts; ++i) {
+            const float* q = part(min(c + i, c1));
+            const float* ml = q + static_cast<int64_t>(p.part_rows) * kD;
 #pragma unroll
-    for (int r = 0; r < kJoinRows; ++r) M[r] = warp_max_f32(M[r]);
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-        const float* q = part(c);
-        const float* ml = q + static_cast<int64_t>(p.part_rows) * kD;
+            for (int r = 0; r < kJoinRows; ++r) {
+                m[i][r] = c + i <= c1 ? ml[row[r]] : -INFINITY;
+                l[i][r] = ml[p.part_rows + row[r]];
+                x[i][r] = reinterpret_cast<const float4*>(q + row[r] * kD)[lane];
+            }
+        }
 #pragma unroll
-        for (int r = 0; r < kJoinRows; ++r) {
-            const float m = ml[row[r]];
-            const float4 x = reinterpret_cast<const float4*>(q + row[r] * kD)[lane];
-            const float l = ml[p.part_rows + row[r]];
-            const bool none = m == -INFINITY;    // the part does not count: its O may be anything
-            const float f = none ? 0.0f : ex2(m - M[r]);
-            L[r] += l * f;
-            o[r].x += none ? 0.0f : x.x * f;
-            o[r].y += none ? 0.0f : x.y * f;
-            o[r].z += none ? 0.0f : x.z * f;
-            o[r].w += none ? 0.0f : x.w * f;
+        for (int i = 0; i < kJoinParts; ++i) {
+#pragma unroll
+            for (int r = 0; r < kJoinRows; ++r) {
+                if (m[i][r] == -INFINITY) continue;      // the part does not count: its O may be anything
+                const float mn = fmaxf(M[r], m[i][r]), f = ex2(M[r] - mn), g = ex2(m[i][r] - mn);
+                M[r] = mn;
+                L[r] = L[r] * f + l[i][r] * g;
+                o[r].x = o[r].x * f + x[i][r].x * g;
+                o[r].y = o[r].y * f + x[i][r].y * g;
+                o[r].z = o[r].z * f + x[i][r].z * g;
+                o[r].w = o[r].w * f + x[i][r].w * g;
+            }
         }
     }
-    const float4 v =
-        __ldg(reinterpret_cast<const float4*>(p.v_scale + static_cast<int64_t>(s.b * p.NKV + s.h) * kD) + lane);
 #pragma unroll
     for (int r = 0; r < kJoinRows; ++r) {
         if (row0 + r >= s.rows) break;
