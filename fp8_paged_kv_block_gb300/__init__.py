@@ -509,7 +509,7 @@ def _norm_rope_args(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes, q_
     for t, n in ((k, "k"), (v, "v")):
         _need(t, n, (q.dtype,), contiguous=False)
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+        if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
             raise ValueError("%s must be [tokens, heads, head_size] with contiguous heads" % n)
     T, NQ, D = q.shape
     NKV = k.shape[1]
@@ -556,7 +556,8 @@ def _norm_rope_args(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes, q_
                 positions=positions, q_codes=q_codes, q_scale=q_scale, key_cache=key_cache,
                 value_cache=value_cache, slot_mapping=slot_mapping,
                 key_scale_cache=key_scale_cache, v_scale=v_scale, token_batch=token_batch)
-    args = (_ptr(q), _ptr(k), _ptr(v), _in_dtype(q), q.stride(0), k.stride(0), v.stride(0),
+    step = [t.stride(0) if T > 1 else 0 for t in (q, k, v)]     # (of one token: any)
+    args = (_ptr(q), _ptr(k), _ptr(v), _in_dtype(q), *step,
             _ptr(q_weight), _ptr(k_weight), DTYPE_BF16 if wdt == torch.bfloat16 else DTYPE_F32,
             float(eps), _ptr(cos_sin), rd, max_pos, int(bool(interleaved)), _ptr(positions),
             pos_type, _ptr(q_codes), _ptr(q_scale), _ptr(key_cache), _ptr(value_cache),

@@ -378,7 +378,7 @@ void launch(NormRopeParams p, bool inter, int sms, cudaStream_t st)
     p.kv_jobs = (p.NKV + rows - 1) / rows;
     p.jobs = static_cast<uint32_t>(p.T) * (p.q_jobs + 2 * p.kv_jobs);
     constexpr uint32_t warps = kThreads / 32;
-    const uint32_t ctas = std::min((p.jobs + warps - 1) / warps, static_cast<uint32_t>(sms * kBlocks));
+    const uint32_t ctas = std::min((p.jobs - 1) / warps + 1, static_cast<uint32_t>(sms * kBlocks));
     p.warps = ctas * warps;
     if (inter) qkv_norm_rope_append_kernel<T, D, true><<<ctas, kThreads, 0, st>>>(p);
     else qkv_norm_rope_append_kernel<T, D, false><<<ctas, kThreads, 0, st>>>(p);

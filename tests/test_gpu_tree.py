@@ -879,3 +879,36 @@ def test_append_rows_at_the_ends_of_the_range(D, rd, inter, norm):
     c["kw"] *= 2.0 ** -100
     eps = 1e-5 if D == 128 else 1e-30
     check_append(c, run_append(c, eps=eps, inter=inter, norm=norm), eps=eps, inter=inter, norm=norm)
+
+
+def test_append_strides_that_do_not_count():
+    """One token and one head: their strides may be anything."""
+    pa = _pa()
+    a = append_case(97, 1, 1, 1, 128, 64, torch.bfloat16, 0)
+    want = run_append(a)
+    got = [torch.zeros_like(want[0]).cuda(), torch.zeros_like(want[1]).cuda(), torch.full_like(want[2], 0xA5).cuda(),
+           torch.full_like(want[3], 0x5A).cuda(), torch.full_like(want[4], -7.0).cuda()]
+    odd = lambda t: t.contiguous().cuda().as_strided((1, 1, 128), (7, 3, 1))  # noqa: E731
+    pa.qkv_norm_rope_append(odd(a["q"]), odd(a["k"]), odd(a["v"]), a["qw"].cuda(), a["kw"].cuda(), a["cs"].cuda(),
+                            a["pos"].cuda(), got[0], got[1], got[2], got[3], a["slots"].cuda(), got[4], a["vs"].cuda(),
+                            a["tb"].cuda(), eps=1e-5, interleaved=False, layout=0)
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x.cpu(), y)
+
+
+def test_verify_random_numbers_at_the_ends():
+    """u[0] at 0 and at the last float below 1 draws the first and the last token
+    of any mass, wherever they lie."""
+    V = 5003
+    p = np.zeros((6, 2, V), np.float32)
+    u = np.zeros((6, 2), np.float32)
+    u[3:, 0] = np.float32(1) - np.float32(2.0 ** -24)
+    spots = [(0, V - 1), (17, 18), (2500, 4999)]
+    for b in range(6):
+        lo, hi = spots[b % 3]
+        p[b, :, lo], p[b, :, hi] = 0.25, 0.75
+    c = dict(p=p, q=None, tok=np.full((6, 2), 100, np.int32), par=np.tile(np.array([-1, 0], np.int32), (6, 1)), u=u,
+             n=np.full(6, 2, np.int32))
+    got = check_verify(c)
+    assert got[2][:, 0].tolist() == [s[0] for s in spots] + [s[1] for s in spots]
