@@ -23,7 +23,7 @@
 // 115; rotating through shuffles and reducing each set by itself (820
 // instructions) 113 and 137. Three or four jobs in flight change nothing (83, 84);
 // six CTAs an SM, at 80 registers with spills, 93. Few tokens: 16 take 6 us, 777 of
-// 48 + 2 x 8 heads 11.5 us.
+// 48 + 2 x 8 heads 11 us.
 #include "common.cuh"
 
 #include <algorithm>
@@ -61,7 +61,7 @@ struct NormRopeParams {
     int64_t T;
     int NQ, NKV;
     uint32_t q_jobs, kv_jobs;                // jobs a token's q heads, its k (and v) heads make
-    uint32_t jobs, warps;
+    uint32_t per, longer;                    // jobs a warp, warps with one more
     int64_t num_blocks;
     int BS, layout;
 };
@@ -81,6 +81,12 @@ __device__ __forceinline__ void unpack(const uint2& r, float2& a, float2& b)
     a = make_float2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u));
     b = make_float2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u));
 }
+__device__ __forceinline__ void prefetch_l1(const void* p, int type, uint32_t i)
+{
+    const char* at = static_cast<const char*>(p) + static_cast<int64_t>(i) * (type == PA_INDEX_I64 ? 8 : 4);
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
+}
+
 __device__ __forceinline__ float2 times(float2 a, float f) { return __fmul2_rn(a, make_float2(f, f)); }
 
 // One copy of the four divisions for all callers: only a few warps come here.
@@ -114,15 +120,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel
     const int lane = threadIdx.x & 31, sub = lane % LPR;
     const uint32_t wid = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     T(*const mine)[kJob] = ring[threadIdx.x >> 5];
-    // this warp's jobs: the first jobs % warps warps have one more
-    const uint32_t per = p.jobs / p.warps, longer = p.jobs % p.warps;
-    const uint32_t begin = wid * per + min(wid, longer), end = begin + per + (wid < longer ? 1 : 0);
+    // this warp's jobs
+    const uint32_t begin = wid * p.per + min(wid, p.longer), end = begin + p.per + (wid < p.longer ? 1 : 0);
     if (begin == end) return;
     const uint32_t per_token = p.q_jobs + 2 * p.kv_jobs;
 
     // ---- rows on their way to shared memory, kStages - 1 jobs ahead ----
     uint32_t ahead = begin, a_tok = begin / per_token, a_part = begin - a_tok * per_token;
     int a_slot = 0;
+    // the first token's position and slot on their way to L1 (the angles and rows wait
+    // for them, and the rows' addresses take a while)
+    if (p.rd > 0) prefetch_l1(p.pos, p.pos_type, a_tok);
+    prefetch_l1(p.slots, p.slot_type, a_tok);
     auto fetch = [&] {
         if (ahead < end) {
             const bool q = a_part < p.q_jobs, v = a_part >= p.q_jobs + p.kv_jobs;
@@ -376,10 +385,11 @@ void launch(NormRopeParams p, bool inter, int sms, cudaStream_t st)
     constexpr uint32_t rows = kSets * (32 / (D / 8));        // rows a warp takes
     p.q_jobs = (p.NQ + rows - 1) / rows;
     p.kv_jobs = (p.NKV + rows - 1) / rows;
-    p.jobs = static_cast<uint32_t>(p.T) * (p.q_jobs + 2 * p.kv_jobs);
+    const uint32_t jobs = static_cast<uint32_t>(p.T) * (p.q_jobs + 2 * p.kv_jobs);
     constexpr uint32_t warps = kThreads / 32;
-    const uint32_t ctas = std::min((p.jobs - 1) / warps + 1, static_cast<uint32_t>(sms * kBlocks));
-    p.warps = ctas * warps;
+    const uint32_t ctas = std::min((jobs - 1) / warps + 1, static_cast<uint32_t>(sms * kBlocks));
+    p.per = jobs / (ctas * warps);
+    p.longer = jobs % (ctas * warps);
     if (inter) qkv_norm_rope_append_kernel<T, D, true><<<ctas, kThreads, 0, st>>>(p);
     else qkv_norm_rope_append_kernel<T, D, false><<<ctas, kThreads, 0, st>>>(p);
 }
