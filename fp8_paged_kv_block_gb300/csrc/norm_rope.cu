@@ -310,13 +310,32 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel
         const int own = 2 * (lane & 1) + (lane >> 1 & 1);        // the set this lane reduces
         const float ss_own = reduce_sets<false>(ss, lane, LPR), amax_own = reduce_sets<true>(amax, lane, LPR);
         // Squares, products or quotients out of the comfortable range, a row of zeros among
-        // them: row by row in the order that keeps all in it.
+        // them: done again below.
         const bool fine = (w == nullptr || (ss_own <= 1e38f && ss_own >= 1e-30f)) && amax_own >= 0x1p-100f &&
                           amax_own <= 0x1p100f;
+        const int own_lane = lane - sub;                        // + (i >> 1) + 2 (i & 1): the lane with set i's
+        // ---- codes z (448 / max|z|), and the scales ----
+        const float f_own = __fdividef(kE4M3Max, amax_own);
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+            const float f = __shfl_sync(0xffffffffu, f_own, own_lane + (i >> 1) + 2 * (i & 1));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[i][e] = times(z[i][e], f);
+            if (h0 + i * RPW < heads) {
+                uint8_t* const at = dst + i * dst_step;
+                *reinterpret_cast<uint32_t*>(at + c0) = e4m3x4(z[i][0].x, z[i][0].y, z[i][1].x, z[i][1].y);
+                *reinterpret_cast<uint32_t*>(at + c1) = e4m3x4(z[i][2].x, z[i][2].y, z[i][3].x, z[i][3].y);
+            }
+        }
+        const float s = __fdiv_rn(amax_own, kE4M3Max);
+        if (sub < kSets && h0 + own * RPW < heads && fine)
+            scale[own * scale_step] = w == nullptr ? s : s * rsqrtf(ss_own * (1.0f / D) + p.eps);
+        // The other rows, one by one in the order that keeps all in range. (Only they: a
+        // row's result does not depend on those beside it.)
         if (__any_sync(0xffffffffu, !fine && h0 + own * RPW < heads)) {
 #pragma unroll 1
             for (int i = 0; i < kSets; ++i, dst += dst_step) {
-                const bool in = h0 + i * RPW < heads;
+                const bool in = !__shfl_sync(0xffffffffu, fine, own_lane + (i >> 1) + 2 * (i & 1)) && h0 + i * RPW < heads;
                 float2 y[4];
                 unpack(load_smem(lane_x + i * RPW * D + c0), y[0], y[1]);
                 unpack(load_smem(lane_x + i * RPW * D + c1), y[2], y[3]);
@@ -357,23 +376,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel
                 *reinterpret_cast<uint32_t*>(dst + c1) = m == 0.0f ? 0u : e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y);
                 if (sub == 0) scale[i * scale_step] = __fdiv_rn(m, kE4M3Max) * rms;
             }
-            continue;
         }
-        // ---- codes z (448 / max|z|), and the scales ----
-        const float f_own = __fdividef(kE4M3Max, amax_own);
-#pragma unroll
-        for (int i = 0; i < kSets; ++i, dst += dst_step) {
-            const float f = __shfl_sync(0xffffffffu, f_own, (lane - sub) + (i >> 1) + 2 * (i & 1));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[i][e] = times(z[i][e], f);
-            if (h0 + i * RPW < heads) {
-                *reinterpret_cast<uint32_t*>(dst + c0) = e4m3x4(z[i][0].x, z[i][0].y, z[i][1].x, z[i][1].y);
-                *reinterpret_cast<uint32_t*>(dst + c1) = e4m3x4(z[i][2].x, z[i][2].y, z[i][3].x, z[i][3].y);
-            }
-        }
-        const float s = __fdiv_rn(amax_own, kE4M3Max);
-        if (sub < kSets && h0 + own * RPW < heads)
-            scale[own * scale_step] = w == nullptr ? s : s * rsqrtf(ss_own * (1.0f / D) + p.eps);
     }
 }
 

@@ -912,3 +912,29 @@ def test_verify_random_numbers_at_the_ends():
              n=np.full(6, 2, np.int32))
     got = check_verify(c)
     assert got[2][:, 0].tolist() == [s[0] for s in spots] + [s[1] for s in spots]
+
+
+@pytest.mark.parametrize("D,inter,dtype", [(64, False, torch.float32), (128, False, torch.bfloat16),
+                                           (128, True, torch.float32), (256, False, torch.bfloat16)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_append_rows_do_not_depend_on_those_beside_them(D, inter, dtype, norm):
+    """Rows of zeros, of 2^-110 and of 2^110 among others: the others come out
+    as without them, bit for bit."""
+    NQ, NKV, T = 9, 3, 8
+    c = append_case(100 + D, T, NQ, NKV, D, 32, dtype, 0, wdt=torch.float32)
+    c["slots"] = torch.arange(T, dtype=torch.int32)
+    clean = run_append(c, inter=inter, norm=norm)
+    heads = c["qkv"].view(T, NQ + 2 * NKV, D)
+    same = torch.ones((T, NQ + 2 * NKV), dtype=torch.bool)
+    for t, h, f in ((0, 0, 0.0), (1, 4, 2.0 ** -110), (2, NQ - 1, 2.0 ** 110), (3, 2, 0.0), (3, 5, 2.0 ** 110),
+                    (4, NQ, 0.0), (5, NQ + 1, 2.0 ** -110), (6, NQ + 2, 2.0 ** 110)):
+        heads[t, h] *= f
+        same[t, h] = False
+    got = run_append(c, inter=inter, norm=norm)
+    check_append(c, got, inter=inter, norm=norm)
+    q, k = same[:, :NQ], same[:, NQ:NQ + NKV]
+    assert torch.equal(got[0][q], clean[0][q]) and torch.equal(got[1][q], clean[1][q])
+    for i in (2, 4):
+        a, b = (x.reshape((-1,) + x.shape[2:])[:T] for x in (got[i], clean[i]))
+        assert torch.equal(a[k], b[k])
+    assert torch.equal(got[3], clean[3])
