@@ -87,6 +87,15 @@ __device__ __forceinline__ void prefetch_l1(const void* p, int type, uint32_t i)
     asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
 }
 
+// The larger one, NaN if either is: a NaN or what infinities make of one must not
+// get lost in a row's maximum, as it would in fmaxf.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 __device__ __forceinline__ float2 times(float2 a, float f) { return __fmul2_rn(a, make_float2(f, f)); }
 
 // One copy of the four divisions for all callers: only a few warps come here.
@@ -102,7 +111,7 @@ template <bool MAX>
 __device__ __forceinline__ float reduce_sets(const float (&a)[kSets], int lane, int lpr)
 {
     static_assert(kSets == 4, "two steps halve the sets to one");
-    auto op = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
+    auto op = [](float x, float y) { return MAX ? max_nan(x, y) : x + y; };
     const bool b0 = lane & 1, b1 = lane & 2;
     const float k0 = op(b0 ? a[2] : a[0], __shfl_xor_sync(0xffffffffu, b0 ? a[0] : a[2], 1));
     const float k1 = op(b0 ? a[3] : a[1], __shfl_xor_sync(0xffffffffu, b0 ? a[1] : a[3], 1));
@@ -280,9 +289,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel
             }
         };
         auto max_of = [](const float2 (&y)[4]) {
-            float m = fmaxf(fabsf(y[0].x), fabsf(y[0].y));
+            float m = max_nan(fabsf(y[0].x), fabsf(y[0].y));
 #pragma unroll
-            for (int e = 1; e < 4; ++e) m = fmaxf(fmaxf(m, fabsf(y[e].x)), fabsf(y[e].y));
+            for (int e = 1; e < 4; ++e) m = max_nan(max_nan(m, fabsf(y[e].x)), fabsf(y[e].y));
             return m;
         };
         const int64_t q0 = static_cast<int64_t>(t_now) * p.NQ + h0;
@@ -309,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel
         }
         const int own = 2 * (lane & 1) + (lane >> 1 & 1);        // the set this lane reduces
         const float ss_own = reduce_sets<false>(ss, lane, LPR), amax_own = reduce_sets<true>(amax, lane, LPR);
-        // Squares, products or quotients out of the comfortable range, a row of zeros among
-        // them: done again below.
+        // Squares, products or quotients out of the comfortable range, a row of zeros or one
+        // with a NaN among them: done again below.
         const bool fine = (w == nullptr || (ss_own <= 1e38f && ss_own >= 1e-30f)) && amax_own >= 0x1p-100f &&
                           amax_own <= 0x1p100f;
         const int own_lane = lane - sub;                        // + (i >> 1) + 2 (i & 1): the lane with set i's
@@ -331,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel
         if (sub < kSets && h0 + own * RPW < heads && fine)
             scale[own * scale_step] = w == nullptr ? s : s * rsqrtf(ss_own * (1.0f / D) + p.eps);
         // The other rows, one by one in the order that keeps all in range. (Only they: a
-        // row's result does not depend on those beside it.)
+        // row's result does not depend on those beside it.) A row with a NaN, its own or an
+        // infinity's, has the maximum NaN and so NaN codes and scale.
         if (__any_sync(0xffffffffu, !fine && h0 + own * RPW < heads)) {
 #pragma unroll 1
             for (int i = 0; i < kSets; ++i, dst += dst_step) {
@@ -344,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel
                     // times 2^64 or 2^-80 where squares would leave the range, then normalised
                     float t = max_of(y);
 #pragma unroll
-                    for (int o = LPR / 2; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                    for (int o = LPR / 2; o > 0; o >>= 1) t = max_nan(t, __shfl_xor_sync(0xffffffffu, t, o));
                     const float f = t > 0x1p56f ? 0x1p-80f : (t < 0x1p-60f ? 0x1p64f : 1.0f);
                     t = 0.0f;
 #pragma unroll
@@ -366,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel
                 rotate(y);
                 float m = max_of(y);
 #pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                for (int o = LPR / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                 const float up = m < 0x1p-100f ? 0x1p100f : (m > 0x1p100f ? 0x1p-100f : 1.0f);
                 const float f = m == 0.0f ? 0.0f : __fdividef(kE4M3Max, m * up);
 #pragma unroll

@@ -521,7 +521,10 @@ PA_API pa_status pa_mla_sparse_decode_kvc(const void* q_nope, const void* q_rope
  * k's to the cache row of slot_mapping[t] and key_scale_cache; v is encoded
  * as pa_fp8_cache_quant_scatter does, E4M3(v / v_scale[token_batch[t]]). A
  * slot outside [0, num_blocks * block_size) writes neither k nor v (q is
- * still written). With duplicate slots which write wins is undefined.
+ * still written). With duplicate slots which write wins is undefined. A row
+ * of q or k whose y has a NaN (an infinity under a norm makes one) gets NaN
+ * codes and a NaN scale, one whose max|y| is infinite that scale, NaN codes
+ * where y is infinite and zeros elsewhere.
  * q, k, v      FP32 or BF16 (in_dtype) [T, NQ or NKV, head_size], heads
  *              contiguous, tokens *_stride elements apart (views of one
  *              projection's output qualify); 16-byte aligned, strides a

@@ -938,3 +938,64 @@ def test_append_rows_do_not_depend_on_those_beside_them(D, inter, dtype, norm):
         a, b = (x.reshape((-1,) + x.shape[2:])[:T] for x in (got[i], clean[i]))
         assert torch.equal(a[k], b[k])
     assert torch.equal(got[3], clean[3])
+
+
+@pytest.mark.parametrize("D,rd,inter,dtype", [(64, 32, False, torch.float32), (128, 64, False, torch.bfloat16),
+                                              (128, 128, True, torch.float32), (256, 0, False, torch.bfloat16)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_append_rows_with_infinities_and_nans(D, rd, inter, dtype, norm):
+    """A row whose y has a NaN is all NaN, scale too; one whose largest value is
+    infinite has that scale, NaN where y is infinite and zeros elsewhere; the
+    rows beside them are what they are without them."""
+    NQ, NKV, T = 9, 3, 8
+    c = append_case(110 + D, T, NQ, NKV, D, rd, dtype, 0, wdt=torch.float32)
+    c["slots"] = torch.arange(T, dtype=torch.int32)
+    clean = run_append(c, inter=inter, norm=norm)
+    inf, nan = float("inf"), float("nan")
+    heads = c["qkv"].view(T, NQ + 2 * NKV, D)
+    heads[0, 0, 3] = inf
+    heads[1, 4, D - 1] = -inf
+    heads[2, NQ - 1, ::7] = inf
+    heads[3, 2, 5] = nan
+    heads[4, 1] = 0                                     # nothing beside it
+    heads[4, 1, D - 2] = nan
+    heads[5, 5] = 0
+    heads[5, 5, 0] = -inf
+    heads[6, 3, 1], heads[6, 3, 2] = inf, nan
+    heads[1, NQ, 0] = inf                               # keys
+    heads[2, NQ + 1, D // 2] = nan
+    heads[6, NQ + 2, D - 1] = -inf
+    got = run_append(c, inter=inter, norm=norm)
+    qc, qs, kc, vc, ks = got
+    kc, ks = (x.reshape((-1,) + x.shape[2:])[:T] for x in (kc, ks))
+    kc0, ks0 = (clean[i].reshape((-1,) + clean[i].shape[2:])[:T] for i in (2, 4))
+    assert torch.equal(vc, clean[3])
+    for x, w, code, scale, code0, scale0 in ((c["q"], c["qw"], qc, qs, clean[0], clean[1]),
+                                             (c["k"], c["kw"], kc, ks, kc0, ks0)):
+        y = H.norm_rope_reference(x, w if norm else None, c["cs"], c["pos"], inter, 1e-5)
+        amax = y.abs().amax(-1)                         # (NaN if there is one)
+        bad = ~torch.isfinite(amax)
+        assert bad.any() and torch.isnan(amax).any() and (norm or torch.isinf(amax).any())
+        nan_row, inf_row = torch.isnan(amax), torch.isinf(amax)
+        assert torch.equal(code[~bad], code0[~bad]) and torch.equal(scale[~bad], scale0[~bad])
+        assert torch.isnan(H.value(code[nan_row])).all() and torch.isnan(scale[nan_row]).all()
+        assert (scale[inf_row] == inf).all()
+        v = H.value(code[inf_row])
+        assert torch.equal(torch.isnan(v), torch.isinf(y[inf_row])) and (v[~torch.isnan(v)] == 0).all()
+
+
+def test_append_takes_nan_angles_and_infinite_weights_for_what_they_are():
+    c = append_case(120, 6, 4, 2, 128, 64, torch.float32, 0, wdt=torch.float32)
+    c["slots"] = torch.arange(6, dtype=torch.int32)
+    c["pos"] = torch.arange(6, dtype=torch.int32)
+    clean = run_append(c)
+    c["cs"][2, 7] = float("nan")
+    got = run_append(c)
+    rows = torch.arange(6) != 2
+    assert torch.equal(got[0][rows], clean[0][rows]) and torch.equal(got[1][rows], clean[1][rows])
+    assert torch.isnan(H.value(got[0][2])).all() and torch.isnan(got[1][2]).all()
+    c["cs"][2, 7] = 1.0
+    c["qw"][70] = float("inf")                          # a channel that is not rotated
+    code, scale = H.value(run_append(c)[0]), run_append(c)[1]
+    assert (scale == float("inf")).all() and torch.isnan(code[..., 70]).all()
+    assert (code[..., torch.arange(128) != 70] == 0).all()
