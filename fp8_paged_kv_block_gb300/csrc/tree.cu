@@ -986,7 +986,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
 #pragma unroll
             for (int r = 0; r < kJoinRows; ++r) {
                 m[i][r] = c + i <= c1 ? ml[row[r]] : -INFINITY;
-                l[i][r] = ml[p.part_rows + row[r]];
+                l[i][r] = c + i <= c1 ? ml[p.part_rows + row[r]] : 0.0f;
                 x[i][r] = reinterpret_cast<const float4*>(q + row[r] * kD)[lane];
             }
         }
@@ -994,7 +994,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const TreePa
         for (int i = 0; i < kJoinParts; ++i) {
 #pragma unroll
             for (int r = 0; r < kJoinRows; ++r) {
-                if (m[i][r] == -INFINITY) continue;      // the part does not count: its O may be anything
+                // nothing seen in this part. (Where all scores are NaN the maximum is -inf
+                // as well, and the sum NaN: that has to reach the output.)
+                if (l[i][r] == 0.0f) continue;
                 const float mn = fmaxf(M[r], m[i][r]), f = ex2(M[r] - mn), g = ex2(m[i][r] - mn);
                 M[r] = mn;
                 L[r] = L[r] * f + l[i][r] * g;

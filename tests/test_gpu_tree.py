@@ -999,3 +999,24 @@ def test_append_takes_nan_angles_and_infinite_weights_for_what_they_are():
     code, scale = H.value(run_append(c)[0]), run_append(c)[1]
     assert (scale == float("inf")).all() and torch.isnan(code[..., 70]).all()
     assert (code[..., torch.arange(128) != 70] == 0).all()
+
+
+def test_tree_decode_nans_reach_the_output_of_cut_items():
+    """NaN query codes, and NaN key scales over many blocks on end, in items that
+    runs' ends cut: rows that meet one are NaN, whatever part it lies in."""
+    c = H.tree_case(25, [20000, 300], 5, 24, 2, 0)
+    clean = run_tree(c).cpu()
+    bad = torch.zeros((10, 24), dtype=torch.bool)
+    for t, h in ((0, 0), (2, 13), (4, 23), (5, 0), (7, 12), (9, 5)):
+        bad[t, h] = True
+    keep = c["q"].clone()
+    c["q"][bad] = 0x7F
+    out = run_tree(c).cpu()
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], clean[~bad])
+    c["q"] = keep
+    ks = H.by_position(c["ks"], 0)
+    ks[c["bt"][0, 40:70].long(), :, 1] = float("nan")        # kv head 1 of the first sequence
+    out = run_tree(c).cpu()
+    bad[:] = False
+    bad[:5, 12:] = True
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], clean[~bad])
