@@ -575,7 +575,8 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
         float rs = live ? sm.qs[seg & 1][row] * p.scale_log2 : 1.0f;
         // the maximum of S k_scale has to stay one under a negative scale: S changes sign
         const bool flip = rs < 0.0f, any_flip = __any_sync(0xffffffffu, flip);
-        rs = fmaxf(fabsf(rs), 1.17549435e-38f);               // (-inf times it stays -inf)
+        rs = fabsf(rs);
+        if (rs < 1.17549435e-38f) rs = 1.17549435e-38f;       // (-inf times it stays -inf; a NaN stays, too)
         float m = -INFINITY, l = 0.0f;
         const int g_end = g0 + (s.t1 - s.t0);
         // A warp without rows keeps the others company at the barriers.

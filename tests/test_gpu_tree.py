@@ -1020,3 +1020,15 @@ def test_tree_decode_nans_reach_the_output_of_cut_items():
     bad[:] = False
     bad[:5, 12:] = True
     assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], clean[~bad])
+
+
+def test_tree_decode_nan_query_scales_give_nan_rows():
+    """A row's scale is NaN: so is its output, and no other row's."""
+    c = H.tree_case(24, [300, 20000] + [100] * 200, 5, 24, 2, 0)      # items cut by runs' ends and whole ones
+    clean = run_tree(c).clone()
+    bad = torch.zeros((1010, 24), dtype=torch.bool)
+    for t, h in ((0, 0), (2, 13), (4, 23), (5, 0), (7, 12), (9, 5), (100, 3), (500, 20), (807, 7)):
+        bad[t, h] = True
+    c["qs"][bad] = float("nan")
+    out = run_tree(c).cpu()
+    assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], clean.cpu()[~bad])
