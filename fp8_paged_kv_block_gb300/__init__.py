@@ -784,6 +784,9 @@ def _keep_args(key_cache, value_cache, key_scale_cache, block_table, kv_act_seqs
     for t, n in ((block_table, "block_table"), (kv_act_seqs, "kv_act_seqs"), (path, "path"),
                  (accepted, "accepted"), (new_act_seqs, "new_act_seqs")):
         _need(t, n, torch.int32)
+    if layout is None:
+        raise TypeError("cache_keep_path needs layout=: no other argument has the caches' heads "
+                        "or block size to hold against their shape")
     if path.dim() != 2 or block_table.dim() != 2:
         raise ValueError("path must be [B, S1] and block_table [B, max_blocks]")
     B, S1 = path.shape
@@ -811,12 +814,14 @@ def _keep_args(key_cache, value_cache, key_scale_cache, block_table, kv_act_seqs
 
 
 def cache_keep_path(key_cache, value_cache, key_scale_cache, block_table, kv_act_seqs, path,
-                    accepted, new_act_seqs, *, tree_len=None, layout: int = LAYOUT_BNBD,
+                    accepted, new_act_seqs, *, tree_len=None, layout: int | None = None,
                     stream=None):
     """The accepted branch kept in the cache, in place: the K/V codes and key
     scales of the drafted nodes path[b][:accepted[b]] (tree_verify's, strictly
     increasing) move to the first drafted positions, and new_act_seqs int32 [B]
-    (another tensor than kv_act_seqs) becomes the length that leaves."""
+    (another tensor than kv_act_seqs) becomes the length that leaves. layout has
+    to be given, the one that tree_decode reads the caches in: no default, as the
+    cache's shape alone does not tell heads from positions."""
     args, keep = _keep_args(key_cache, value_cache, key_scale_cache, block_table, kv_act_seqs,
                             path, accepted, new_act_seqs, tree_len, layout)
     _check(lib().pa_fp8_cache_keep_path(*args, _stream(stream)), "pa_fp8_cache_keep_path")
@@ -825,7 +830,7 @@ def cache_keep_path(key_cache, value_cache, key_scale_cache, block_table, kv_act
 
 def prepare_cache_keep_path(key_cache, value_cache, key_scale_cache, block_table, kv_act_seqs,
                             path, accepted, new_act_seqs, *, tree_len=None,
-                            layout: int = LAYOUT_BNBD, stream=None):
+                            layout: int | None = None, stream=None):
     """cache_keep_path() prepared once: returns a callable that launches the
     same call on the same buffers."""
     args, keep = _keep_args(key_cache, value_cache, key_scale_cache, block_table, kv_act_seqs,

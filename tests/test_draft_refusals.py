@@ -128,3 +128,37 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         pa.tree_decode(None, *[z(1)] * 9, S1=1)
     with pytest.raises(ValueError, match="CUDA"):
         pa.qkv_norm_rope_append(*[z(1, 1, 128)] * 3, None, None, None, None, *[z(1)] * 8)
+
+
+class _Stream:
+    """What the binding takes from a torch stream, without a GPU."""
+    cuda_stream = 0
+
+
+def _on_host(monkeypatch):
+    """The binding with host tensors let through and nothing launched: what it
+    refuses beyond the tensors' place can then be tested without a GPU."""
+    import fp8_paged_kv_block_gb300 as pa
+    monkeypatch.setattr(pa, "_need", lambda t, name, dtype=None, contiguous=True: _need_dtype(t, name, dtype))
+    monkeypatch.setattr(pa, "_one_device", lambda **kw: None)
+    return pa
+
+
+def _need_dtype(t, name, dtype):
+    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError("%s has dtype %s" % (name, t.dtype))
+
+
+def test_keep_path_wants_a_layout(L, monkeypatch):
+    """A cache [NB, 128, 8, 128] reads as 8 heads or as 128: no default decides."""
+    torch = pytest.importorskip("torch")
+    pa = _on_host(monkeypatch)
+    i32 = dict(dtype=torch.int32)
+    cache = [torch.zeros((3, 128, 8, 128), dtype=torch.uint8) for _ in range(2)] + [torch.zeros((3, 128, 8))]
+    args = cache + [torch.zeros((2, 2), **i32), torch.zeros(2, **i32), torch.zeros((2, 4), **i32),
+                    torch.zeros(2, **i32), torch.zeros(2, **i32)]
+    for call in (pa.cache_keep_path, pa.prepare_cache_keep_path):
+        with pytest.raises(TypeError, match="layout"):
+            call(*args, stream=_Stream())
+    for layout in (pa.LAYOUT_BSND, pa.LAYOUT_BNBD):
+        pa.prepare_cache_keep_path(*args, layout=layout, stream=_Stream())
