@@ -513,6 +513,15 @@ extern "C" pa_status pa_tree_verify(const float* target_probs, const float* draf
     for (const void* q : ptrs)
         PA_REQUIRE(aligned(q, 4), PA_ERR_INVALID, "pa_tree_verify: misaligned pointer");
     if (B == 0) return PA_OK;
+    // a sequence's CTAs read the inputs while one of them already writes
+    const uint64_t rows = static_cast<uint64_t>(B) * S1, probs = rows * V * sizeof(float);
+    const struct { const void* at; uint64_t bytes; } bufs[] = {
+        {accepted, 4ull * B}, {path, 4 * rows}, {tokens, 4 * rows}, {target_probs, probs}, {draft_probs, probs},
+        {draft_tokens, 4 * rows}, {parents, 4 * rows}, {uniforms, 4 * rows}, {tree_len, 4ull * B}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 9; ++j)
+            PA_REQUIRE(!overlap(bufs[i].at, bufs[i].bytes, bufs[j].at, bufs[j].bytes), PA_ERR_INVALID,
+                       "pa_tree_verify: accepted, path and tokens must overlap no other buffer");
     VerifyParams a;
     a.p = target_probs;
     a.q = draft_probs;
@@ -571,11 +580,15 @@ extern "C" pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache, 
     PA_REQUIRE(head_size % 16 == 0 && head_size <= 8192, PA_ERR_UNSUPPORTED,
                "%s: head_size %d (a multiple of 16 up to 8192)", name, head_size);
     static_assert(2 * 8192 / 16 <= kKThreads * kKBatch, "a head's row fits a round");
-    PA_REQUIRE(B == 0 || new_act_seqs != kv_act_seqs, PA_ERR_INVALID,
-               "%s: new_act_seqs must be another buffer than kv_act_seqs", name);
     PA_REQUIRE(aligned(key_cache, 16) && aligned(value_cache, 16) && aligned(key_scale_cache, 4), PA_ERR_INVALID,
                "%s: misaligned pointer", name);
     if (B == 0) return PA_OK;
+    // a sequence's CTAs read the inputs while one of them already writes
+    const uint64_t ints = 4ull * B;
+    PA_REQUIRE(!overlap(new_act_seqs, ints, kv_act_seqs, ints) && !overlap(new_act_seqs, ints, tree_len, ints) &&
+                   !overlap(new_act_seqs, ints, accepted, ints) && !overlap(new_act_seqs, ints, path, ints * S1) &&
+                   !overlap(new_act_seqs, ints, block_table, ints * max_blocks_per_seq),
+               PA_ERR_INVALID, "%s: new_act_seqs must overlap no input (kv_act_seqs among them)", name);
     KeepParams p;
     p.kc = static_cast<uint8_t*>(key_cache);
     p.vc = static_cast<uint8_t*>(value_cache);

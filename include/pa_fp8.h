@@ -621,7 +621,8 @@ PA_API pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, const v
  * path         int32 [B, S1]: the branch's nodes, path[b][0] = 0; -1 behind.
  * tokens       int32 [B, S1]: the accepted nodes' tokens, then the drawn one
  *              (accepted[b] in all); -1 behind.
- * S1 at most 1024, V at most 262144 (else PA_ERR_UNSUPPORTED).
+ * The three outputs overlap neither an input nor one another. S1 at most
+ * 1024, V at most 262144 (else PA_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 PA_API pa_status pa_tree_verify(const float* target_probs, const float* draft_probs,
                                 const int32_t* draft_tokens, const int32_t* parents,
@@ -639,7 +640,7 @@ PA_API pa_status pa_tree_verify(const float* target_probs, const float* draft_pr
  * or lies past the block table.
  * head_size    a multiple of 16 up to 8192; caches 16-byte aligned. S1 at most
  *              1024.
- * new_act_seqs int32 [B], not kv_act_seqs itself.
+ * new_act_seqs int32 [B], overlapping none of the int32 inputs.
  * ------------------------------------------------------------------------ */
 PA_API pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache,
                                         float* key_scale_cache, const int32_t* block_table,

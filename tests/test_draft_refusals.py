@@ -162,3 +162,28 @@ def test_keep_path_wants_a_layout(L, monkeypatch):
             call(*args, stream=_Stream())
     for layout in (pa.LAYOUT_BSND, pa.LAYOUT_BNBD):
         pa.prepare_cache_keep_path(*args, layout=layout, stream=_Stream())
+
+
+def test_outputs_that_overlap_inputs_are_refused(L):
+    """The kernels read their inputs while outputs are already written."""
+    pool = _buf().value
+    at = lambda i: P(pool + 4096 * i)  # noqa: E731
+    names = "p q tok par u len B S1 V acc path new stream".split()
+    d = {k: at(i) for i, k in enumerate("p q tok par u len acc path new".split())}
+    d.update(S1=4, V=100, B=2, stream=None)               # 8 rows: 3200 bytes of probabilities
+    verify = caller(L.pa_tree_verify, names, d)
+    for out, size in (("acc", 8), ("path", 32), ("new", 32)):
+        for i, other in enumerate("p q tok par u len acc path new".split()):
+            if other == out:
+                continue
+            for off in (0, 4, -size + 4):
+                assert verify(**{out: P(d[other].value + off)}) == 2, (out, other, off)
+                assert b"overlap" in L.pa_last_error()
+    names = "kc vc ks bt act len path acc new B S1 NKV D BS NB MB layout stream".split()
+    d = {k: at(i) for i, k in enumerate("kc vc ks bt act len path acc new".split())}
+    d.update(B=2, S1=4, NKV=8, D=128, BS=128, NB=16, MB=4, layout=0, stream=None)
+    keep = caller(L.pa_fp8_cache_keep_path, names, d)
+    for other in "bt act len path acc".split():
+        for off in (0, 4, -4):
+            assert keep(new=P(d[other].value + off)) == 2, (other, off)
+            assert b"overlap" in L.pa_last_error()
