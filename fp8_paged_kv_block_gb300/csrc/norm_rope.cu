@@ -466,6 +466,8 @@ extern "C" pa_status pa_fp8_qkv_norm_rope_append(
                PA_ERR_INVALID, "%s: misaligned pointer", name);
     PA_REQUIRE(num_tokens <= 0x7FFFFFFF && num_tokens * (static_cast<int64_t>(NQ) + 2 * NKV) < (static_cast<int64_t>(1) << 32),
                PA_ERR_UNSUPPORTED, "%s: more than 2^32 head rows", name);
+    PA_REQUIRE(NQ <= 0x7FFFFFFF / head_size && NKV <= 0x7FFFFFFF / head_size, PA_ERR_UNSUPPORTED,
+               "%s: a token of 2^31 values or more", name);
     if (num_tokens == 0) return PA_OK;
     NormRopeParams p;
     p.q = q; p.k = k; p.v = v;

@@ -536,6 +536,8 @@ PA_API pa_status pa_mla_sparse_decode_kvc(const void* q_nope, const void* q_rope
  * head_size    64, 128 or 256 (else PA_ERR_UNSUPPORTED). rotary_dim at most
  *              head_size, a multiple of 16, or of 8 if interleaved (else
  *              PA_ERR_UNSUPPORTED).
+ * Limits: NQ * head_size and NKV * head_size below 2^31, num_tokens * (NQ +
+ *              2 NKV) below 2^32 (else PA_ERR_UNSUPPORTED).
  * q_codes, caches 8-byte aligned, v_scale 16-byte aligned. Slots, layout,
  * token_batch and v_scale as in pa_fp8_cache_quant_scatter.
  * ------------------------------------------------------------------------ */

@@ -187,3 +187,17 @@ def test_outputs_that_overlap_inputs_are_refused(L):
         for off in (0, 4, -4):
             assert keep(new=P(d[other].value + off)) == 2, (other, off)
             assert b"overlap" in L.pa_last_error()
+
+
+def test_append_of_tokens_past_32_bits_is_refused(L):
+    """Offsets within a token are 32 bits."""
+    fake = _buf()
+    names = ("q k v dt qs ks vs qw kw wdt eps cs rd maxpos inter pos pdt qc qsc kc vc slots sdt ksc vsc tb nb T NQ "
+             "NKV D NB BS layout stream").split()
+    d = {n: fake for n in "q k v qw kw cs pos qc qsc kc vc slots ksc vsc tb".split()}
+    d.update(dt=1, qs=2048, ks=2048, vs=2048, wdt=1, eps=1e-5, rd=64, maxpos=100, inter=0, pdt=0, sdt=0, nb=2, T=1,
+             NQ=8, NKV=2, D=128, NB=4, BS=128, layout=0, stream=None)
+    call = caller(L.pa_fp8_qkv_norm_rope_append, names, d)
+    for bad in (dict(NQ=1 << 24), dict(NKV=1 << 24), dict(NQ=1 << 23, D=256), dict(NKV=1 << 25, D=64)):
+        assert call(**bad) == 5 and b"2^31" in L.pa_last_error(), bad
+    assert call(T=0, NQ=(1 << 24) - 1) == 0
