@@ -580,8 +580,10 @@ extern "C" pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache, 
     PA_REQUIRE(head_size % 16 == 0 && head_size <= 8192, PA_ERR_UNSUPPORTED,
                "%s: head_size %d (a multiple of 16 up to 8192)", name, head_size);
     static_assert(2 * 8192 / 16 <= kKThreads * kKBatch, "a head's row fits a round");
-    PA_REQUIRE(aligned(key_cache, 16) && aligned(value_cache, 16) && aligned(key_scale_cache, 4), PA_ERR_INVALID,
-               "%s: misaligned pointer", name);
+    PA_REQUIRE(aligned(key_cache, 16) && aligned(value_cache, 16) && aligned(key_scale_cache, 4) &&
+                   aligned(block_table, 4) && aligned(kv_act_seqs, 4) && aligned(tree_len, 4) && aligned(path, 4) &&
+                   aligned(accepted, 4) && aligned(new_act_seqs, 4),
+               PA_ERR_INVALID, "%s: misaligned pointer", name);
     if (B == 0) return PA_OK;
     // a sequence's CTAs read the inputs while one of them already writes
     const uint64_t ints = 4ull * B;

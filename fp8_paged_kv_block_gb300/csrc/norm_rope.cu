@@ -462,7 +462,9 @@ extern "C" pa_status pa_fp8_qkv_norm_rope_append(
                PA_ERR_INVALID, "%s: q, k and v tokens must start on 16-byte boundaries", name);
     PA_REQUIRE(aligned(q_weight, 16) && aligned(k_weight, 16) && aligned(cos_sin, 16) &&
                    aligned(v_scale, 16) && aligned(q_codes, 8) && aligned(key_cache, 8) &&
-                   aligned(value_cache, 8) && aligned(q_scale, 4) && aligned(key_scale_cache, 4),
+                   aligned(value_cache, 8) && aligned(q_scale, 4) && aligned(key_scale_cache, 4) &&
+                   aligned(token_batch, 4) && aligned(positions, pos_type == PA_INDEX_I64 ? 8 : 4) &&
+                   aligned(slot_mapping, slot_type == PA_INDEX_I64 ? 8 : 4),
                PA_ERR_INVALID, "%s: misaligned pointer", name);
     PA_REQUIRE(num_tokens <= 0x7FFFFFFF && num_tokens * (static_cast<int64_t>(NQ) + 2 * NKV) < (static_cast<int64_t>(1) << 32),
                PA_ERR_UNSUPPORTED, "%s: more than 2^32 head rows", name);

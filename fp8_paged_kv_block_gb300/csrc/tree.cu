@@ -1084,6 +1084,11 @@ extern "C" pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, con
     PA_REQUIRE(mask_stride >= 0, PA_ERR_INVALID, "%s: negative mask_stride", name);
     PA_REQUIRE(aligned16(q) && aligned16(k_cache) && aligned16(v_cache) && aligned16(v_scale) && aligned16(out),
                PA_ERR_INVALID, "%s: q, the caches, v_scale and out must be 16-byte aligned", name);
+    for (const void* x : {static_cast<const void*>(q_scale), static_cast<const void*>(k_scale),
+                          static_cast<const void*>(block_table), static_cast<const void*>(kv_act_seqs),
+                          static_cast<const void*>(tree_len)})
+        PA_REQUIRE((reinterpret_cast<uintptr_t>(x) & 3u) == 0, PA_ERR_INVALID,
+                   "%s: q_scale, k_scale, block_table, kv_act_seqs and tree_len must be 4-byte aligned", name);
     // the schedule counts blocks in 32 bits
     const int64_t per_block = (static_cast<int64_t>(S1) * (NQ / NKV) + kItemRows - 1) / kItemRows * (1 + kItemCost);
     PA_REQUIRE(per_block * NKV * B <= 0xFFFFFFFFll / max_blocks_per_seq, PA_ERR_UNSUPPORTED,

@@ -504,6 +504,8 @@ PA_API pa_status pa_mla_sparse_decode_kvc(const void* q_nope, const void* q_rope
  *                                ctx, ctx + 1, ...
  * A call of no tokens or sequences is checked and enqueues nothing; the
  * tensors that then have no elements may be NULL.
+ * Every tensor is aligned to its elements; what needs more says so
+ * (PA_ERR_INVALID otherwise).
  * ------------------------------------------------------------------------ */
 
 /* ------------------------------------------------------------------------

@@ -201,3 +201,33 @@ def test_append_of_tokens_past_32_bits_is_refused(L):
     for bad in (dict(NQ=1 << 24), dict(NKV=1 << 24), dict(NQ=1 << 23, D=256), dict(NKV=1 << 25, D=64)):
         assert call(**bad) == 5 and b"2^31" in L.pa_last_error(), bad
     assert call(T=0, NQ=(1 << 24) - 1) == 0
+
+
+def test_elements_off_their_alignment_are_refused(L):
+    """A misaligned address is a fault on the GPU."""
+    fake, other = _buf(), _buf()
+    names = ("q k v dt qs ks vs qw kw wdt eps cs rd maxpos inter pos pdt qc qsc kc vc slots sdt ksc vsc tb nb T NQ "
+             "NKV D NB BS layout stream").split()
+    d = {n: fake for n in "q k v qw kw cs pos qc qsc kc vc slots ksc vsc tb".split()}
+    d.update(dt=1, qs=2048, ks=2048, vs=2048, wdt=1, eps=1e-5, rd=64, maxpos=100, inter=0, pdt=0, sdt=0, nb=2, T=0,
+             NQ=8, NKV=2, D=128, NB=4, BS=128, layout=0, stream=None)
+    call = caller(L.pa_fp8_qkv_norm_rope_append, names, d)
+    for n in "pos slots tb qsc ksc".split():
+        assert call(**{n: P(fake.value + 2)}) == 2, n
+    assert call(pos=P(fake.value + 4), slots=P(fake.value + 4)) == 0
+    assert call(pos=P(fake.value + 4), pdt=1) == 2 and call(slots=P(fake.value + 4), sdt=1) == 2
+    names = "q qs kc ks vc vs bt act len mask ms out B S1 NQ NKV D BS NB MB layout scale ws wsb stream".split()
+    d = {k: fake for k in "q qs kc ks vc vs bt act len mask out".split()}
+    d.update(ms=64, B=0, S1=8, NQ=96, NKV=8, D=128, BS=128, NB=16, MB=4, layout=0, scale=0.08, ws=None, wsb=0,
+             stream=None)
+    call = caller(L.pa_fp8_tree_decode, names, d)
+    assert call(mask=P(fake.value + 1)) == 0
+    for n in "qs ks bt act len".split():
+        assert call(**{n: P(fake.value + 2)}) == 2 and b"4-byte" in L.pa_last_error(), n
+    names = "kc vc ks bt act len path acc new B S1 NKV D BS NB MB layout stream".split()
+    d = {k: fake for k in "kc vc ks bt act len path acc".split()}
+    d.update(new=other, B=0, S1=4, NKV=8, D=128, BS=128, NB=16, MB=4, layout=0, stream=None)
+    call = caller(L.pa_fp8_cache_keep_path, names, d)
+    assert call() == 0
+    for n in "ks bt act len path acc new".split():
+        assert call(**{n: P(d[n].value + 2)}) == 2 and b"misaligned" in L.pa_last_error(), n
