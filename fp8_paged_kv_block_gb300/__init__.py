@@ -505,6 +505,7 @@ def _norm_rope_args(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes, q_
                     interleaved, layout):
     torch = _torch()
     floats = (torch.float32, torch.bfloat16)
+    e4m3 = (torch.uint8, torch.float8_e4m3fn)            # what is written, whatever holds it
     _need(q, "q", floats, contiguous=False)
     for t, n in ((k, "k"), (v, "v")):
         _need(t, n, (q.dtype,), contiguous=False)
@@ -533,12 +534,12 @@ def _norm_rope_args(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes, q_
         _need(positions, "positions", (torch.int32, torch.int64))
         _shape(positions, "positions", T)
         pos_type = INDEX_I64 if positions.dtype == torch.int64 else INDEX_I32
-    _need(q_codes, "q_codes", _fp8_types())
+    _need(q_codes, "q_codes", e4m3)
     _shape(q_codes, "q_codes", T, NQ, D)
     _need(q_scale, "q_scale", torch.float32)
     _shape(q_scale, "q_scale", T, NQ)
     for t, n in ((key_cache, "key_cache"), (value_cache, "value_cache")):
-        _need(t, n, _fp8_types())
+        _need(t, n, e4m3)
     _need(slot_mapping, "slot_mapping", (torch.int32, torch.int64))
     _shape(slot_mapping, "slot_mapping", T)
     _need(key_scale_cache, "key_scale_cache", torch.float32)

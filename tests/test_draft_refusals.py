@@ -231,3 +231,21 @@ def test_elements_off_their_alignment_are_refused(L):
     assert call() == 0
     for n in "ks bt act len path acc new".split():
         assert call(**{n: P(d[n].value + 2)}) == 2 and b"misaligned" in L.pa_last_error(), n
+
+
+def test_append_writes_e4m3_codes_into_nothing_else(L, monkeypatch):
+    torch = pytest.importorskip("torch")
+    pa = _on_host(monkeypatch)
+    T, NQ, NKV, D = 3, 4, 2, 128
+
+    def prepare(**dt):
+        z = lambda n, *s: torch.zeros(s, dtype=dt.get(n, torch.uint8))  # noqa: E731
+        f = torch.zeros
+        return pa.prepare_qkv_norm_rope_append(
+            f(T, NQ, D), f(T, NKV, D), f(T, NKV, D), None, None, None, None, z("q_codes", T, NQ, D), f(T, NQ),
+            z("key_cache", 2, 128, NKV, D), z("value_cache", 2, 128, NKV, D), f(T, dtype=torch.int32),
+            f(2, 128, NKV), f(1, NKV, D), f(T, dtype=torch.int32), layout=pa.LAYOUT_BSND, stream=_Stream())
+    for n in ("q_codes", "key_cache", "value_cache"):
+        prepare(**{n: torch.float8_e4m3fn})
+        with pytest.raises(TypeError, match=n):
+            prepare(**{n: torch.float8_e5m2})
