@@ -258,7 +258,7 @@ def decode(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_act_s
     """
     args, keep = _decode_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table,
                               kv_act_seqs, out, S1, layout, s2_tile, softmax_scale, workspace,
-                              num_ctas, overlap_prologue, merge_wait_ns, wait_limit_ns)
+                              num_ctas, overlap_prologue, merge_wait_ns, wait_limit_ns, stream)
     _check(lib().pa_fp8_decode(*args, _stream(stream)), "pa_fp8_decode")
     del keep   # (a workspace made here lives until the launch is enqueued)
     return out
@@ -266,7 +266,7 @@ def decode(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_act_s
 
 def _decode_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_act_seqs, out,
                  S1, layout, s2_tile, softmax_scale, workspace, num_ctas, overlap_prologue,
-                 merge_wait_ns, wait_limit_ns):
+                 merge_wait_ns, wait_limit_ns, stream, ready=False):
     """pa_fp8_decode's arguments but the stream, validated, and the objects
     they point into."""
     torch = _torch()
@@ -287,8 +287,9 @@ def _decode_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
     if workspace is None:
-        workspace = DecodeWorkspace(B, S1, NQ, NKV, D, s2_tile=s2_tile, num_ctas=num_ctas,
-                                    device=q.device)
+        workspace = _own_workspace(lambda: DecodeWorkspace(B, S1, NQ, NKV, D, s2_tile=s2_tile,
+                                                           num_ctas=num_ctas, device=q.device),
+                                   stream, ready)
     cfg = _config(s2_tile, num_ctas, overlap_prologue, merge_wait_ns, wait_limit_ns)
     args = (_ptr(q), _ptr(q_scale), _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale),
             _ptr(block_table), _ptr(kv_act_seqs), _ptr(out), B, S1, NQ, NKV, D, BS, NB,
@@ -299,14 +300,30 @@ def _decode_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv
     return args, keep
 
 
+def _own_workspace(make, stream, ready=False):
+    """A workspace that the caller did not give, zeroed on the stream that uses
+    it and handed back to it. `ready`: the zeroing is waited for, as calls on
+    other streams may come (not in a capture, where nothing can be waited for:
+    the graph zeroes it)."""
+    torch = _torch()
+    with torch.cuda.stream(stream):
+        workspace = make()
+        if ready and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+    return workspace
+
+
 class _Prepared:
     """A library call whose arguments were validated and marshalled once, for
     a loop that makes the same call every step (the buffers' contents may
     change between calls, not their addresses, shapes or dtypes). Runs on the
     stream given when it was made (default: the current stream then), or on
-    the stream passed to the call."""
+    the stream passed to the call. `scratch` is a workspace that was made for
+    this call alone: its memory is not given to others before the streams that
+    it ran on are done. (A graph that captured the call does not hold it: the
+    callable lives as long as the graph.)"""
 
-    def __init__(self, fn, where, args, keep, stream):
+    def __init__(self, fn, where, args, keep, stream, scratch=None):
         # a function object of its own that takes ready ctypes values as they are:
         # converting a long argument list anew took longer than a short kernel
         raw = lib()[where]
@@ -316,9 +333,14 @@ class _Prepared:
         self._call = functools.partial(raw, *ready)
         self._where, self._keep = where, keep
         self._stream = _stream(stream)
+        self._scratch, self._streams = scratch, {self._stream.value}
 
     def __call__(self, stream=None):
-        st = self._call(self._stream if stream is None else _stream(stream))
+        on = self._stream if stream is None else _stream(stream)
+        if self._scratch is not None and on.value not in self._streams:
+            self._scratch.buf.record_stream(stream)
+            self._streams.add(on.value)
+        st = self._call(on)
         if st != PA_OK:
             _check(st, self._where)
 
@@ -331,8 +353,9 @@ def prepare_decode(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, 
     decode on the same buffers (arguments as for decode())."""
     args, keep = _decode_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table,
                               kv_act_seqs, out, S1, layout, s2_tile, softmax_scale, workspace,
-                              num_ctas, overlap_prologue, 0, 0)
-    return _Prepared(lib().pa_fp8_decode, "pa_fp8_decode", args, keep, stream)
+                              num_ctas, overlap_prologue, 0, 0, stream, ready=True)
+    return _Prepared(lib().pa_fp8_decode, "pa_fp8_decode", args, keep, stream,
+                     scratch=None if workspace is not None else keep[-2])
 
 
 # --------------------------------------------------------------------------
@@ -634,7 +657,8 @@ class TreeWorkspace:
 
 
 def _tree_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_act_seqs,
-               tree_mask, out, S1, tree_len, layout, softmax_scale, workspace, stream):
+               tree_mask, out, S1, tree_len, layout, softmax_scale, workspace, stream,
+               ready=False):
     torch = _torch()
     for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
         _need(t, n, (torch.uint8, torch.float8_e4m3fn))
@@ -672,9 +696,8 @@ def _tree_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_a
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
     if workspace is None:
-        # zeroed on the stream that uses it, and handed back to it
-        with torch.cuda.stream(stream):
-            workspace = TreeWorkspace(B, S1, NQ, NKV, D, device=q.device)
+        workspace = _own_workspace(lambda: TreeWorkspace(B, S1, NQ, NKV, D, device=q.device),
+                                   stream, ready)
     _one_device(q=q, q_scale=q_scale, k_cache=k_cache, k_scale=k_scale, v_cache=v_cache,
                 v_scale=v_scale, block_table=block_table, kv_act_seqs=kv_act_seqs,
                 tree_mask=tree_mask, tree_len=tree_len, out=out, workspace=workspace.buf)
@@ -713,8 +736,9 @@ def prepare_tree_decode(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_ta
     call on the same buffers."""
     args, keep = _tree_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table,
                             kv_act_seqs, tree_mask, out, S1, tree_len, layout, softmax_scale,
-                            workspace, stream)
-    return _Prepared(lib().pa_fp8_tree_decode, "pa_fp8_tree_decode", args, keep, stream)
+                            workspace, stream, ready=True)
+    return _Prepared(lib().pa_fp8_tree_decode, "pa_fp8_tree_decode", args, keep, stream,
+                     scratch=None if workspace is not None else keep[-1])
 
 
 def _verify_args(target_probs, draft_probs, draft_tokens, parents, uniforms, accepted, path,

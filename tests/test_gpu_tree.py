@@ -1032,3 +1032,57 @@ def test_tree_decode_nan_query_scales_give_nan_rows():
     c["qs"][bad] = float("nan")
     out = run_tree(c).cpu()
     assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], clean.cpu()[~bad])
+
+
+@pytest.mark.parametrize("what", ["tree_decode", "decode"])
+def test_prepared_calls_own_workspace_on_several_streams(what):
+    """A workspace that the call made itself is zeroed before the callable is
+    handed out, and its memory stays with streams that still run the call."""
+    pa = _pa()
+    B, S1, NQ, NKV = 2, 4, 12, 2
+    c = H.tree_case(26, [3000, 700], S1, NQ, NKV, 0)
+    g = _cuda(c)
+    shape = (B * S1, NQ, H.D)
+    want = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    base = (g["q"], g["qs"], g["kc"], g["ks"], g["vc"], g["vs"], g["bt"], g["act"])
+    if what == "decode":
+        size = pa.decode_workspace_size(B, S1, NQ, NKV)
+        pa.decode(*base, want, S1=S1, layout=0, workspace=pa.DecodeWorkspace(B, S1, NQ, NKV))
+        prepare = lambda out, st: pa.prepare_decode(*base, out, S1=S1, layout=0, stream=st)  # noqa: E731
+        direct = lambda out, st: pa.decode(*base, out, S1=S1, layout=0, stream=st)  # noqa: E731
+    else:
+        size = pa.tree_decode_workspace_size(B, S1, NQ, NKV)
+        pa.tree_decode(*base, g["mask"], want, S1=S1, layout=0, workspace=pa.TreeWorkspace(B, S1, NQ, NKV))
+        prepare = lambda out, st: pa.prepare_tree_decode(*base, g["mask"], out, S1=S1, layout=0, stream=st)  # noqa: E731
+        direct = lambda out, st: pa.tree_decode(*base, g["mask"], out, S1=S1, layout=0, stream=st)  # noqa: E731
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = [torch.zeros(shape, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(a):
+        torch.cuda._sleep(20_000_000)                    # some milliseconds
+    call = prepare(outs[0], a)
+    assert a.query()                                     # zeroed by now
+    with torch.cuda.stream(b):
+        torch.cuda._sleep(20_000_000)
+    call(stream=b)
+    del call
+    with torch.cuda.stream(a):                           # what would take the memory over
+        junk = [torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    call = prepare(outs[1], None)
+    call()
+    b.wait_stream(torch.cuda.current_stream())           # (one workspace: one call after the other)
+    call(stream=b)
+    direct(outs[2], a)                                   # made and given back on the call's stream
+    direct(outs[3], b)
+    torch.cuda.synchronize()
+    del junk
+    for out in outs:
+        if what == "decode":
+            # which CTA merges a sequence's parts, and so the order of FP32 sums, is not
+            # fixed: a few roundings and exponentials (2^-20 of the mass, which is at most
+            # max|V| = 448 times the largest scale), then a BF16 rounding either way (2^-7)
+            tol = 2.0 ** -7 * want.double().abs() + 2.0 ** -20 * 448 * float(c["vs"].max())
+            assert ((out.double() - want.double()).abs() <= tol).all()
+        else:
+            assert torch.equal(out, want)
