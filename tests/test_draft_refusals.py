@@ -249,3 +249,26 @@ def test_append_writes_e4m3_codes_into_nothing_else(L, monkeypatch):
         prepare(**{n: torch.float8_e4m3fn})
         with pytest.raises(TypeError, match=n):
             prepare(**{n: torch.float8_e5m2})
+
+
+def test_prepared_calls_refuse_another_current_device(L, monkeypatch):
+    """On a default stream the launch goes to the current device."""
+    torch = pytest.importorskip("torch")
+    pa = _on_host(monkeypatch)
+    ran = []
+    current = [0]
+    i32 = dict(dtype=torch.int32)
+    call = pa.prepare_cache_keep_path(
+        torch.zeros((1, 128, 1, 128), dtype=torch.uint8), torch.zeros((1, 128, 1, 128), dtype=torch.uint8),
+        torch.zeros((1, 128, 1)), torch.zeros((1, 1), **i32), torch.zeros(1, **i32), torch.zeros((1, 2), **i32),
+        torch.zeros(1, **i32), torch.zeros(1, **i32), layout=pa.LAYOUT_BSND, stream=_Stream())
+    call._call = lambda stream: ran.append(stream.value) or 0
+    call._device, call._current = 0, lambda: current[0]
+    call()
+    current[0] = 1
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        call()
+    other = _Stream()
+    other.cuda_stream = 4096
+    call(other)                                          # (the runtime itself tells such a launch's device)
+    assert ran == [None, 4096]
