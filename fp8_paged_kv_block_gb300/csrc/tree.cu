@@ -37,10 +37,10 @@
 // average); the same x 8: 31 us; 2 of up to 300 keys x 8 x 4 heads: 10 us.
 //   warps 0-7        softmax, warpgroup k of blocks k, k + 2, .. (thread = row =
 //                    tensor memory lane)
-//   warp 8           K and V blocks by TMA, key scales by cp.async
-//   warps 9, 10      issue S, issue P V
-//   warp 11          Q rows and scales of the next segment; tells the joining
+//   warp 8           K and V blocks by TMA, key scales by cp.async; tells the joining
 //                    kernel about the item at the run's begin
+//   warps 9, 10      issue S, issue P V
+//   warp 11          Q rows and scales of the next segment
 //   warps 12-15      V codes to FP16 in shared memory, zeros behind the end
 //
 // The items in (sequence, kv head, row tile) order are dealt to the CTAs in runs
@@ -99,7 +99,7 @@ struct Cut {
 
 // Workspace: error word, a Cut per CTA, then per CTA two partial items: O
 // [rows][128], m and l [rows]. Slot 2 c is of run c's first item, slot 2 c + 1
-// of its last. m = -inf: the part does not count.
+// of its last. l = 0: the row sees nothing there.
 constexpr size_t kCutOff = 256;
 constexpr size_t kPartOff = kCutOff + kMaxCtas * sizeof(Cut);
 
@@ -782,38 +782,20 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
 }
 
 // What the joining kernel has to know of the item at the begin of this CTA's run.
-__device__ void describe_cut(TreeSmem& sm, const TreeParams& p, Run run, uint32_t total, int lane)
+// Runs c0 to c1, those with its first and its last block's positions, have a block
+// of it each (a position behind the first block's is a block's), and no other run
+// has one. Empty runs lie behind the last item.
+__device__ void describe_cut(TreeSmem& sm, const TreeParams& p, const Run& run, uint32_t total, int lane)
 {
     const int c = blockIdx.x;
-    const uint32_t lo = run.pos;
     Cut cut = {};
-    Seg s;
-    // (an empty run has positions of the item behind it, but no part)
-    if (lo < total && c > 0) {
-        if (run.pos == run.hi) {
-            int a = 0, z = p.B - 1;
-            while (a < z) {
-                const int mid = (a + z + 1) >> 1;
-                if (sm.cum[mid] <= lo) a = mid;
-                else z = mid - 1;
-            }
-            run.b = a;
-        }
-        while (sm.cum[run.b + 1] <= lo) ++run.b;
-        s.b = run.b;
+    if (run.pos < total && c > 0) {
+        Seg s;
+        s.b = run.b;                         // (holds run.pos: the run is not empty)
         uint32_t base, end;
-        locate(lo, sm.cum[s.b], (sm.len[s.b] & 0xFF) * p.G, tiles_of(sm.len[s.b] >> 8), s, base, end);
-        if (lo > base) {
-            const int t0 = blocks_before(s, lo - base);
-            const int t1 = run.hi >= end ? s.tiles : blocks_before(s, run.hi - base);
-            if (t0 >= t1) {                  // no block of it here: a part that does not count
-                float* ml = part_of(p, c, true) + static_cast<int64_t>(p.part_rows) * kD;
-                for (int r = lane; r < s.rows; r += 32) {
-                    ml[r] = -INFINITY;
-                    ml[p.part_rows + r] = 0.0f;
-                }
-            }
-            // the runs that hold the first and the last block's positions
+        locate(run.pos, sm.cum[s.b], static_cast<int>(sm.len[s.b] & 0xFF) * p.G, tiles_of(sm.len[s.b] >> 8), s, base,
+               end);
+        if (run.pos > base) {
             const int c0 = cta_of(total, base + kItemCost, p.ctas), c1 = cta_of(total, end - 1, p.ctas);
             if (c == c0 + 1 && c0 < c1) {
                 cut.b = s.b;
@@ -918,9 +900,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kProdWarp) {
             producer(sm, p, &tk, &tv, run, lane);
+            // (behind the Q loader instead 16 x 64 drafted tokens take 150 us, not 129)
+            describe_cut(sm, p, run, total, lane);
         } else if (warp == kQWarp) {
             q_loader(sm, p, run, lane);
-            describe_cut(sm, p, run, total, lane);
         } else {
             mma_issuer(sm, p, run, tmem, warp - kMmaWarp);
         }
