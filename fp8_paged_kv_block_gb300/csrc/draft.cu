@@ -37,16 +37,16 @@ constexpr int kMaxNodes = 1024;
 // Sums pushed under mbarriers instead of a cluster barrier gained 1 us of 27 and
 // were not kept.
 //
-// A sequence gets 8 CTAs while the batch's CTAs number at most kResident, half as
-// many for twice the batch: more CTAs shorten a pass, and cost launches and
-// exchanges. kResident 608 or 1216 (two rounds of the GPU): 45 or 41 us on 128
+// A sequence gets 8 CTAs while the batch's CTAs number at most kCtasPerSm an SM, half
+// as many for twice the batch: more CTAs shorten a pass, and cost launches and
+// exchanges. 4 or 8 an SM (one or two rounds of the GPU): 45 or 41 us on 128
 // sequences of 16 x 131072, 60 or 53 on 500 of 5 x 50000, 29 or 30 on 256.
 constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSegs = kMaxCluster * kVWarps;
 constexpr int kMaxV = 1 << 18;
-constexpr int kResident = 1216;
+constexpr int kCtasPerSm = 8;
 
 struct VerifyParams {
     const float *p, *q;
@@ -535,7 +535,9 @@ extern "C" pa_status pa_tree_verify(const float* target_probs, const float* draf
     a.path = path;
     a.tokens = tokens;
     int cluster = kMaxCluster;
-    while (cluster > 1 && static_cast<int64_t>(B) * cluster > kResident) cluster >>= 1;
+    const int sms = device_sm_count();
+    PA_REQUIRE(sms > 0, PA_ERR_CUDA, "pa_tree_verify: cannot query the device");
+    while (cluster > 1 && static_cast<int64_t>(B) * cluster > kCtasPerSm * sms) cluster >>= 1;
     // segments of whole 128-value steps
     const int segs = cluster * kVWarps;
     a.seg = (V + segs * 128 - 1) / (segs * 128) * 128;
