@@ -1086,3 +1086,34 @@ def test_prepared_calls_own_workspace_on_several_streams(what):
             assert ((out.double() - want.double()).abs() <= tol).all()
         else:
             assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("S1,V", [(257, 515), (1024, 2048)])
+def test_verify_most_nodes(S1, V, draft):
+    """More nodes than a CTA has threads: a node with nearly all others as
+    rejected children, the same with repeated tokens, a chain that is accepted to
+    its end, random trees, and sequences of no and of one node."""
+    c = verify_case(1300 + S1, 7, S1, V, draft, width=6)
+    rng = np.random.default_rng(S1)
+    c["n"][:] = [S1, S1, S1, S1, 0, 1, S1 - 1]
+    for b in (0, 1):
+        c["par"][b, 1:] = 0
+        c["u"][b, 1:] = np.float32(0.999)
+        c["p"][b, 0] = np.float32(1 / V)
+        if draft:
+            c["q"][b, 0] = 0
+            c["q"][b, 0, :V // 2] = np.float32(4 / V)    # p / q = 1 / 4 where drafted from
+            c["tok"][b, 1:] = rng.integers(0, V // 2, S1 - 1)
+        else:
+            c["tok"][b, 1:] = rng.permutation(V)[:S1 - 1] if b == 0 else rng.integers(0, V // 8, S1 - 1)
+    c["par"][2, 1:] = np.arange(S1 - 1)
+    if draft:
+        c["q"][2] = c["p"][2]
+        c["u"][2, 1:] = np.minimum(c["u"][2, 1:], np.float32(0.99))
+    else:
+        c["u"][2, 1:] = 0
+    c["tok"][2, 1:] = c["p"][2, :-1].argmax(-1)
+    acc, path, tokens = check_verify(c)
+    assert acc[0] == 1 and acc[1] == 1 and acc[2] == S1 and acc[4] == 0 and acc[5] == 1
+    assert path[2].tolist() == list(range(S1))
