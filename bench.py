@@ -63,8 +63,8 @@ OVERLAP_APPEND = True
 # DRAM traffic of one decode launch on this workload, from an ncu capture
 # (dram__bytes_read.sum + dram__bytes_write.sum), valid only for the kernel
 # sources it was taken with.
-DECODE_TRAFFIC = {"sources_sha1": "9d4e79883dcc02b9e243733e33b6620daa0d42df",
-                  "bytes_per_launch": 57871616 + 126720}
+DECODE_TRAFFIC = {"sources_sha1": "ebd0b953088a889ca95b5612bb5a71699b810e8d",
+                  "bytes_per_launch": 57871360 + 118016}
 
 
 def parse_args(argv=None):
@@ -173,13 +173,23 @@ def whole_job_gbs(world, bytes_per_step, steps, ms):
     return world * bytes_per_step * steps / (ms * 1e-3) / 1e9
 
 
-def kernel_sources_sha1() -> str:
+# What a kernel's DRAM traffic depends on: its own file, the shared device code,
+# and the tensor maps of the caches (status.cu), which the decode reads through.
+DECODE_SOURCES = ("decode.cu", "common.cuh", "status.cu")
+MLA_SOURCES = ("mla.cu", "common.cuh")
+
+
+def sources_sha1(files) -> str:
     h = hashlib.sha1()
     csrc = os.path.join(ROOT, "fp8_paged_kv_block_gb300", "csrc")
-    for f in ("decode.cu", "common.cuh"):
+    for f in files:
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()
+
+
+def kernel_sources_sha1() -> str:
+    return sources_sha1(DECODE_SOURCES)
 
 
 def measured_hbm_peak():
@@ -1099,13 +1109,12 @@ MLA_VARIANTS = 2          # top-k selections rotated between steps (each ~172 MB
 # valid only for the kernel source it was taken with.
 # Captured on the 16-sequence case and scaled by the selected rows (x4): each
 # row is read from DRAM once, so the traffic grows in proportion.
-MLA_TRAFFIC = {"sources_sha1": "873bd441168e0c595677623988589fac528de244", "format": "page",
-               "bytes_per_launch": 4 * (54289920 + 344832)}
+MLA_TRAFFIC = {"sources_sha1": "270fdca2c159c8b8f31e5f8a2efa7d44f1eece11", "format": "page",
+               "bytes_per_launch": 4 * (54310656 + 296448)}
 
 
 def mla_sources_sha1() -> str:
-    with open(os.path.join(ROOT, "fp8_paged_kv_block_gb300", "csrc", "mla.cu"), "rb") as fh:
-        return hashlib.sha1(fh.read()).hexdigest()
+    return sources_sha1(MLA_SOURCES)
 
 
 def measured_bf16_peak():

@@ -100,3 +100,20 @@ def test_host_cpu_record():
     rec = bench.host_cpu()
     assert isinstance(rec["cpu_model"], str) and rec["cpu_model"]
     assert rec["nproc"] >= 1
+
+
+def test_traffic_records_hash_all_code_that_decides_the_traffic(monkeypatch, tmp_path):
+    """A captured traffic counts for the sources it was taken with: the kernel's
+    file, the shared device code and, for the decode, the caches' tensor maps."""
+    import os
+    import shutil
+    csrc = tmp_path / "fp8_paged_kv_block_gb300" / "csrc"
+    shutil.copytree(os.path.join(bench.ROOT, "fp8_paged_kv_block_gb300", "csrc"), csrc)
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    for sha, files in ((bench.kernel_sources_sha1, ("decode.cu", "common.cuh", "status.cu")),
+                       (bench.mla_sources_sha1, ("mla.cu", "common.cuh"))):
+        for f in files:
+            before = sha()
+            with open(csrc / f, "a") as fh:
+                fh.write("// changed\n")
+            assert sha() != before, f
