@@ -652,6 +652,17 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
                 for (int k = 2; k < 32; k += 2) m4[c] = max3(m4[c], v[32 * c + k], v[32 * c + k + 1]);
             }
             const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * rs;
+            // Past 2^22 the rounding of mx is no longer small beside the exponents, which
+            // take the products unrounded (one too large by 1 leaves FP16): there they are rounded as
+            // mx is. (Rounding all of them takes 2 to 3% longer.)
+            const bool big = fabsf(mx) > 0x1p22f;
+            float rx = rs;
+            if (__builtin_expect(__any_sync(0xffffffffu, big), 0)) {
+                const float f = big ? rs : 1.0f;
+#pragma unroll
+                for (int k = 0; k < kBS; ++k) v[k] *= f;
+                rx = big ? 1.0f : rs;
+            }
             // this P buffer's last P V is complete
             if (turn > 0) wait_for(&sm.o_done[w], (turn - 1) & 1, p.err, 128, &sm.abort);
             __syncwarp();
@@ -691,7 +702,7 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
             m = mn;
             tc_fence_after();
             const float ref = m == -INFINITY ? 0.0f : m - kShift;
-            const float2 rs2 = make_float2(rs, rs), nref = make_float2(-ref, -ref);
+            const float2 rs2 = make_float2(rx, rx), nref = make_float2(-ref, -ref);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {

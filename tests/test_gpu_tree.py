@@ -1117,3 +1117,35 @@ def test_verify_most_nodes(S1, V, draft):
     acc, path, tokens = check_verify(c)
     assert acc[0] == 1 and acc[1] == 1 and acc[2] == S1 and acc[4] == 0 and acc[5] == 1
     assert path[2].tolist() == list(range(S1))
+
+
+def test_tree_decode_scores_past_the_floats_integers():
+    """Scores of 1e8 to 1e14, where FP32 steps are larger than the exponents' whole
+    range: the largest score's key takes all, equal ones share."""
+    c = H.tree_case(27, [700, 5000], 4, 12, 2, 0)
+    kc, vc, ks = (H.by_position(c[k], 0) for k in ("kc", "vc", "ks"))
+    one = torch.full((), 1.0).to(H.F8).view(torch.uint8)
+    c["q"][:] = one
+    kc[:] = one                                          # S = 128 everywhere
+    keep = ks.clone()
+    for f in (1e7, 1e10, 1e13):
+        ks[:] = f
+        c["qs"][:] = 1.0
+        for b, (at, n) in enumerate(((650, 4), (77, 4))):
+            ks[c["bt"][b, at // 128].long(), at % 128] = 1.5 * f
+        out = run_tree(c).double().cpu()
+        for b, at in enumerate((650, 77)):
+            want = H.value(vc[c["bt"][b, at // 128].long(), at % 128]) * c["vs"][b].double()   # [NKV, D]
+            want = want.repeat_interleave(6, 0)[None].expand(4, 12, 128)
+            got = out[4 * b:4 * b + 4]
+            assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20).all(), f
+        # negative scales: all others are far above the one
+        c["qs"][:] = -1.0
+        assert torch.isfinite(run_tree(c)).all()
+    # all equal: the mean of what a row sees
+    ks[:] = 1e11
+    c["qs"][:] = 1.0
+    out = run_tree(c).double().cpu()
+    c["ks"] = torch.full_like(keep, 0.01)
+    ref, tol = H.tree_reference(c)
+    assert ((out - ref).abs() <= tol).all()
