@@ -609,10 +609,11 @@ PA_API pa_status pa_fp8_tree_decode(const void* q, const float* q_scale, const v
  * Without draft_probs (NULL: the drafts were not drawn at random) node s is
  * accepted if u[b][s] * z < R(x), else z = z - R(x) (FP64) and R(x) = 0.
  * At the end a token is drawn from R: the first i with sum_{k <= i} W_k >
- * floor(u[b][0] * sum W), W_k = floor(min(R_k, 1) * 2^45) as integers, so
- * that no order of summation changes it (sums of R use W too). If all W are
- * 0, target_probs[b][cur] takes R's place, and if its W are 0 the token is
- * -1. Tokens so drawn follow the target's distribution.
+ * floor(u[b][0] * sum W) (the product in FP64, sum W - 1 at most), W_k =
+ * floor(min(R_k, 1) * 2^45) as integers, so that no order of summation
+ * changes it (sums of R use W too). If all W are 0, target_probs[b][cur]
+ * takes R's place, and if its W are 0 the token is -1. Tokens so drawn follow
+ * the target's distribution.
  * target_probs, draft_probs  float [B, S1, V]; values outside [0, 1] are
  *              clamped where they enter a sum, NaN counts as 0.
  * draft_tokens int32 [B, S1] (node 0's is not read); a token outside [0, V)

@@ -1149,3 +1149,11 @@ def test_tree_decode_scores_past_the_floats_integers():
     c["ks"] = torch.full_like(keep, 0.01)
     ref, tol = H.tree_reference(c)
     assert ((out - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_tree_decode_most_rows(layout):
+    """The most drafted tokens and the largest group: 16384 rows a kv head, in
+    items that see nothing of one another."""
+    c = H.tree_case(28, [100, 0], 128, 128, 1, layout, n=[128, 61])
+    check_tree(c, run_tree(c))
