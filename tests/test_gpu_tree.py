@@ -1157,3 +1157,30 @@ def test_tree_decode_most_rows(layout):
     items that see nothing of one another."""
     c = H.tree_case(28, [100, 0], 128, 128, 1, layout, n=[128, 61])
     check_tree(c, run_tree(c))
+
+
+@pytest.mark.parametrize("inside", [False, True])
+def test_prepared_calls_own_workspace_in_a_graph(inside):
+    """Prepared before the capture, or within it: the callable's workspace serves
+    every replay."""
+    pa = _pa()
+    c = H.tree_case(29, [2000, 90], 4, 12, 2, 0)
+    want = run_tree(c)
+    g = _cuda(c)
+    out = torch.empty_like(want)
+    side = torch.cuda.Stream()
+    prepare = lambda: pa.prepare_tree_decode(  # noqa: E731
+        g["q"], g["qs"], g["kc"], g["ks"], g["vc"], g["vs"], g["bt"], g["act"], g["mask"], out, S1=4, layout=0)
+    torch.cuda.synchronize()
+    call = None if inside else prepare()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call = prepare() if inside else call
+        call(stream=side)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    del graph, call
+    torch.cuda.synchronize()
