@@ -333,27 +333,29 @@ class _Prepared:
         self._call = functools.partial(raw, *ready)
         self._where, self._keep = where, keep
         self._stream = _stream(stream)
-        self._null = self._stream.value is None
         self._scratch, self._streams = scratch, {self._stream.value}
         # (torch.cuda.current_device without its checks, which take longer than the rest)
         self._device, self._current = keep[0].device.index, _torch()._C._cuda_getDevice
+        self._several = _torch().cuda.device_count() > 1
 
     def __call__(self, stream=None):
-        on, null = self._stream, self._null
-        if stream is not None:
-            on = _stream(stream)
-            null = on.value is None
-            if self._scratch is not None and on.value not in self._streams:
-                self._scratch.buf.record_stream(stream)
-                self._streams.add(on.value)
-        # a default stream is whichever device's is current: another one's kernel would
-        # fault on these buffers (with other streams the launch itself fails)
-        if null and self._current() != self._device:
-            raise ValueError("%s: the buffers are on cuda:%s, the current device is cuda:%d"
-                             % (self._where, self._device, self._current()))
+        on = self._stream if stream is None and not self._several else self._checked(stream)
         st = self._call(on)
         if st != PA_OK:
             _check(st, self._where)
+
+    def _checked(self, stream):
+        """The handle of the stream to launch on."""
+        on = self._stream if stream is None else _stream(stream)
+        # a default stream is whichever device's is current: another one's kernel would
+        # fault on these buffers (with other streams the launch itself fails)
+        if on.value is None and self._several and self._current() != self._device:
+            raise ValueError("%s: the buffers are on cuda:%s, the current device is cuda:%d"
+                             % (self._where, self._device, self._current()))
+        if self._scratch is not None and on.value not in self._streams:
+            self._scratch.buf.record_stream(stream)
+            self._streams.add(on.value)
+        return on
 
 
 def prepare_decode(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_act_seqs, out,

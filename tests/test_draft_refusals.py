@@ -263,7 +263,7 @@ def test_prepared_calls_refuse_another_current_device(L, monkeypatch):
         torch.zeros((1, 128, 1)), torch.zeros((1, 1), **i32), torch.zeros(1, **i32), torch.zeros((1, 2), **i32),
         torch.zeros(1, **i32), torch.zeros(1, **i32), layout=pa.LAYOUT_BSND, stream=_Stream())
     call._call = lambda stream: ran.append(stream.value) or 0
-    call._device, call._current = 0, lambda: current[0]
+    call._device, call._current, call._several = 0, lambda: current[0], True
     call()
     current[0] = 1
     with pytest.raises(ValueError, match="current device is cuda:1"):
