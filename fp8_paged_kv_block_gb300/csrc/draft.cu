@@ -26,9 +26,10 @@ constexpr int kMaxNodes = 1024;
 //
 // Bound by the chain launch, gather (two loads), then per rejection a pass over
 // the row and an exchange between the CTAs: about 1.5 us of start, 3 us a pass.
-// 64 sequences of 16 nodes x 131072 values take 27 us (of 61 MB read once, 10 us
-// at the copy rate; the sequence with the most has four passes), 256 of 5 x 50000
-// 29 us, one of 8 x 32003 without probabilities 8 us. What made the chain short:
+// 64 sequences of 16 nodes x 131072 values take 23 to 32 us by their random numbers
+// (of 67 MB read once, 10 us at the copy rate; the sequence with the most has four
+// passes), 256 of 5 x 50000 29 to 38 us, one of 8 x 32003 without probabilities 8 us.
+// What made the chain short (on inputs of the 64 that take 27 us now):
 // - code: a launch runs most of it once, and cold code comes from L2. With passes
 //   and draw inlined and unrolled (61 KB a kernel instead of 27) the 64 took 39 us.
 // - four 16-byte loads of p and of q in flight a lane: with two 39 us, and 512
@@ -392,10 +393,10 @@ __global__ void __launch_bounds__(kVThreads, 4) tree_verify_kernel(const VerifyP
 // behind a barrier, written. path[i] >= i, so a round's writes, to lower rows
 // than any later round's sources, spoil nothing that is still to be read.
 // Latency-bound: a chain of three dependent loads (lengths and path, block table,
-// row), which more rows do not lengthen: 4.5 us on 16 sequences of 16 nodes x 8
-// heads, 8.8 us on 256 of 64 (10.7 with two heads a CTA, 8 chunks a thread and the
-// divisions in the unrolled loop: 24 KB of code instead of 12, and 1024 CTAs of
-// which 608 fit; 11.3 with eight heads a CTA, 12 with 8 chunks).
+// row), which more rows do not lengthen: 4.1 us a pass on 16 sequences of 16 nodes x 8
+// heads, 8.2 us on 256 of 64 (8.8 when 10.7 were taken with two heads a CTA, 8 chunks
+// a thread and the divisions in the unrolled loop: 24 KB of code instead of 12, and
+// 1024 CTAs of which 608 fit; 11.3 with eight heads a CTA, 12 with 8 chunks).
 constexpr int kKThreads = 256;
 constexpr int kKHeads = 4, kKBatch = 4, kKResident = 6;   // (6 CTAs an SM: 40 registers)
 

@@ -17,13 +17,14 @@
 //
 // A warp takes a run of jobs, so that angles and weights last for a token's, and
 // has the next job's rows on their way to shared memory while it works on one.
-// 8192 tokens of 96 + 2 x 8 heads of 128: BF16 81 us (331 MB, 4.1 TB/s; the
-// instructions issue at 67% of the clocks, 550 a job of 8 rows), FP32 94 us (566 MB,
-// 6.0 TB/s). With a job a warp and its rows in registers BF16 took 107 us, FP32
-// 115; rotating through shuffles and reducing each set by itself (820
-// instructions) 113 and 137. Three or four jobs in flight change nothing (83, 84);
-// six CTAs an SM, at 80 registers with spills, 93. Few tokens: 16 take 6 us, 777 of
-// 48 + 2 x 8 heads 11 us.
+// 8192 tokens of 96 + 2 x 8 heads of 128: BF16 82 us a pass (358 MB of inputs and
+// outputs, 4.4 TB/s; the instructions issue at 63% of the clocks, 560 a job of 8
+// rows), FP32 95 us (593 MB, 6.2 TB/s). With a job a warp and its rows in registers
+// BF16 took 107 us, FP32 115; rotating through shuffles and reducing each set by
+// itself (820 instructions) 113 and 137. Three or four jobs in flight change nothing
+// (83, 84); six CTAs an SM, at 80 registers with spills, 93. Few tokens: 16 take 4.1
+// us one after another in a graph, 8 to 11 launched by the host; 777 of 48 + 2 x 8
+// heads in FP32 8.6 us, 10 to 13.
 #include "common.cuh"
 
 #include <algorithm>

@@ -31,10 +31,12 @@
 // exponentials wait for that. A block then takes about 1800 clocks; HBM would
 // take 1400.
 //
-// Measured: 4 sequences of up to 131072 keys x 5 x 96 heads over 8: 128 us (648 MB,
-// 5.1 TB/s; steps of 64 keys with twice the buffers 147, three warpgroups 151); 16
-// of up to 4096 x 64: 129 us (111 GFLOP, 0.86 PFLOP/s, of items of 16 blocks on
-// average); the same x 8: 31 us; 2 of up to 300 keys x 8 x 4 heads: 10 us.
+// Measured, a pass: 4 sequences of up to 131072 keys x 5 x 96 heads over 8: 128 to
+// 133 us from box to box (645 MB, 4.9 TB/s; steps of 64 keys with twice the buffers
+// 147, three warpgroups 151); 16 of up to 4096 x 64: 131 us (111 GFLOP, 0.85 PFLOP/s,
+// of items of 16 blocks on average); the same x 8: 31 us; 2 of up to 300 keys x 8 x 4
+// heads: 10 us. Where the code lies counts: the loops' parts move against one
+// another, and the same arithmetic has taken up to 16% longer.
 //   warps 0-7        softmax, warpgroup k of blocks k, k + 2, .. (thread = row =
 //                    tensor memory lane)
 //   warp 8           K and V blocks by TMA, key scales by cp.async; tells the joining
