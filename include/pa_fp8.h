@@ -512,7 +512,8 @@ PA_API pa_status pa_mla_sparse_decode_kvc(const void* q_nope, const void* q_rope
  * pa_fp8_qkv_norm_rope_append -- per-head norm and rotation of q and k,
  * quantisation of q, and the append of k and v, in one pass. For token t,
  * head h, x = q[t][h] or k[t][h] (head_size values, FP32 arithmetic):
- *   y = x / sqrt(mean(x^2) + eps) * weight         (weight NULL: y = x)
+ *   y = x / sqrt(mean(x^2) + eps) * weight         (weight NULL: y = x; a row
+ *                                                  of zeros gives zeros)
  *   pairs (a, b) of the first rotary_dim channels: (a c - b s, b c + a s)
  *     with c = cos_sin[pos][i], s = cos_sin[pos][rotary_dim / 2 + i], pair i
  *     being channels (i, i + rotary_dim / 2), or (2 i, 2 i + 1) if
@@ -568,7 +569,8 @@ PA_API pa_status pa_fp8_qkv_norm_rope_append(
  * Other arguments as in pa_fp8_decode: kv_act_seqs is clamped to
  * max_blocks_per_seq * block_size, n to kv_act_seqs; block ids outside
  * [0, num_blocks) read block 0. Cache bytes at positions >= kv_act_seqs[b]
- * do not matter; E4M3 NaN codes below it are out of contract.
+ * do not matter. Below it a NaN code or scale of K (or of q) gives NaN to the
+ * rows that see the key, and to no others; NaN codes of V are out of contract.
  * D, block_size  128 and 128 (else PA_ERR_UNSUPPORTED). S1 at most 128, NQ /
  * NKV at most 128, B at most 1024, max_blocks_per_seq * 128 below 2^24, and
  * 7 * ceil(S1 * NQ / NKV / 128) * NKV * B * max_blocks_per_seq below 2^32 (else

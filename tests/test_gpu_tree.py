@@ -1184,3 +1184,81 @@ def test_prepared_calls_own_workspace_in_a_graph(inside):
         assert torch.equal(out, want)
     del graph, call
     torch.cuda.synchronize()
+
+
+def test_tree_decode_nans_in_nodes_that_are_not_seen():
+    """K codes and key scales of a drafted node that are NaN or infinite: rows
+    whose mask leaves the node out are what they are without it."""
+    c = H.tree_case(140, [125, 300, 0], 6, 12, 2, 0)
+    c["mask"][:] = torch.from_numpy(H.ancestor_mask([-1, 0, 0, 1, 2, 1]))
+    clean = run_tree(c).cpu().view(3, 6, 12, 128)
+    kc, ks = H.by_position(c["kc"], 0), H.by_position(c["ks"], 0)
+    for b, what in enumerate(("code", "scale", "inf")):
+        pos = int(c["act"][b]) - 6 + 2                   # node 2, an ancestor of 2 and 4
+        at = int(c["bt"][b, pos // 128]), pos % 128
+        if what == "code":
+            kc[at] = 0x7F
+        else:
+            ks[at] = float("nan" if what == "scale" else "inf")
+    out = run_tree(c).cpu().view(3, 6, 12, 128)
+    rest = [0, 1, 3, 5]
+    assert torch.equal(out[:, rest], clean[:, rest])
+    assert torch.isnan(out[:2, [2, 4]]).all()
+
+
+def test_tree_lengths_out_of_range_masks_of_any_byte_and_float8_tensors():
+    c = H.tree_case(141, [200, 30, 10, 129], 5, 8, 2, 1)
+    c["n"] = torch.tensor([9, -2, 5, 3], dtype=torch.int32)    # clamped to 5 and 0
+    c["mask"] = c["mask"].to(torch.uint8) * torch.tensor([1, 2, 128, 255], dtype=torch.uint8)[:, None, None]
+    want = run_tree(c)
+    check_tree(c, want)
+    f = dict(c, **{k: c[k].view(H.F8) for k in ("q", "kc", "vc")})
+    assert torch.equal(run_tree(f), want)
+
+
+def test_verify_and_keep_lengths_out_of_range_and_none():
+    c = verify_case(142, 6, 5, 300, True)
+    c["n"][:] = [9, -1, 5, 100, 0, 3]
+    check_verify(c)
+    c = keep_case(143, [100, 250, 7], 12, 2, 1)
+    c["n"] = torch.tensor([40, -3, 12], dtype=torch.int32)
+    c["act"] += 12
+    check_keep(c)
+    pa = _pa()
+    c["n"][:] = 12
+    want = keep_reference(c)
+    g = _cuda(c)
+    new = torch.zeros(3, dtype=torch.int32, device="cuda")
+    pa.cache_keep_path(g["kc"], g["vc"], g["ks"], g["bt"], g["act"], g["path"], g["acc"], new, layout=1)
+    for a, b in zip((g["kc"], g["vc"], g["ks"]), want):
+        assert torch.equal(H.by_position(a.cpu(), 1), b)
+    assert torch.equal(new.cpu(), want[3])
+
+
+def test_append_indices_of_both_widths_float8_outputs_and_strides_of_each_input():
+    """positions int64 beside slots int32 and the other way round; q, k and v of
+    three tensors with strides of their own."""
+    pa = _pa()
+    for pdt, sdt in ((torch.int64, torch.int32), (torch.int32, torch.int64)):
+        c = append_case(144, 23, 5, 2, 128, 64, torch.bfloat16, 0)
+        want = run_append(c)
+        got = [torch.zeros_like(want[0]).cuda().view(H.F8), torch.zeros_like(want[1]).cuda(),
+               torch.full_like(want[2], 0xA5).cuda().view(H.F8), torch.full_like(want[3], 0x5A).cuda().view(H.F8),
+               torch.full_like(want[4], -7.0).cuda()]
+        wide = lambda t, more: torch.cat([t.flatten(1), t.new_zeros(23, more)], 1).cuda()[:, :t[0].numel()].view(t.shape)  # noqa: E731
+        q, k, v = wide(c["q"], 8), c["k"].contiguous().cuda(), wide(c["v"], 4096)
+        assert len({q.stride(0), k.stride(0), v.stride(0)}) == 3
+        pa.qkv_norm_rope_append(q, k, v, c["qw"].cuda(), c["kw"].cuda(), c["cs"].cuda(), c["pos"].to(pdt).cuda(), got[0],
+                                got[1], got[2], got[3], c["slots"].to(sdt).cuda(), got[4], c["vs"].cuda(), c["tb"].cuda(),
+                                layout=0)
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x.cpu().view(y.dtype), y)
+
+
+def test_append_of_zeros_without_eps_writes_zeros():
+    c = append_case(145, 4, 3, 1, 64, 32, torch.float32, 0)
+    c["qkv"][1] = 0
+    got = run_append(c, eps=0.0)
+    assert (got[0][1] == 0).all() and (got[1][1] == 0).all()
+    assert torch.isfinite(H.value(got[0])).all() and torch.isfinite(got[1]).all()
