@@ -655,8 +655,8 @@ __device__ void softmax(TreeSmem& sm, const TreeParams& p, Run run, uint32_t tme
             }
             const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * rs;
             // Past 2^22 the rounding of mx is no longer small beside the exponents, which
-            // take the products unrounded (one too large by 1 leaves FP16): there they are rounded as
-            // mx is. (Rounding all of them takes 2 to 3% longer.)
+            // take the products unrounded (one too large by 1 leaves FP16): there they are
+            // rounded as mx is. (Rounding all of them takes 2 to 3% longer.)
             const bool big = fabsf(mx) > 0x1p22f;
             float rx = rs;
             if (__builtin_expect(__any_sync(0xffffffffu, big), 0)) {
