@@ -19,6 +19,11 @@ and a speculative decode step over the same cache:
   tree_decode(...)         attention of a tree of drafted tokens
   tree_verify(...)         drafted tokens against the target's probabilities
   cache_keep_path(...)     the accepted branch kept in the cache
+and a ragged serving step (requests bring one token or a prompt's chunk each):
+  plan_batch(...)          block tables, slots and positions from request lengths
+  qkv_norm_mrope_append(...) the append with several position axes (images, video)
+  window_attention(...)    attention to a sliding window and the first tokens
+  token_logprobs(...)      log probabilities, ranks, entropy and top alternatives
 """
 from __future__ import annotations
 
@@ -125,6 +130,22 @@ def lib():
         L.pa_fp8_cache_keep_path.argtypes = [P, P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32,
                                              i64, i32, i32, P]
         L.pa_fp8_cache_keep_path.restype = i32
+        L.pa_fp8_qkv_norm_mrope_append.argtypes = [
+            P, P, P, i32, i64, i64, i64, P, P, i32, f32, P, i32, i64, i32, P, i32, i32, i64, P, P,
+            P, P, P, P, i32, P, P, P, i32, i64, i32, i32, i32, i64, i32, i32, P]
+        L.pa_fp8_qkv_norm_mrope_append.restype = i32
+        L.pa_plan_batch.argtypes = [P, P, P, P, P, P, i32, P, P, P, P, P, i32, i64, i64, i64, i32,
+                                    i32, P]
+        L.pa_plan_batch.restype = i32
+        L.pa_fp8_window_attention_workspace_size.argtypes = [i32, i32, i32, i32,
+                                                             ctypes.POINTER(sz)]
+        L.pa_fp8_window_attention_workspace_size.restype = i32
+        L.pa_fp8_window_attention.argtypes = [P, P, P, P, P, P, P, P, P, P, i32, i64, i32, i32,
+                                              i32, i32, i32, i64, i32, i32, i64, i64, f32, P, sz,
+                                              P]
+        L.pa_fp8_window_attention.restype = i32
+        L.pa_token_logprobs.argtypes = [P, i32, i64, P, i32, i64, i32, P, P, P, i32, P, P, P]
+        L.pa_token_logprobs.restype = i32
         _lib = L
         return L
 
@@ -538,7 +559,9 @@ def _shape(t, name, *want):
 
 def _norm_rope_args(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes, q_scale, key_cache,
                     value_cache, slot_mapping, key_scale_cache, v_scale, token_batch, eps,
-                    interleaved, layout):
+                    interleaved, layout, pair_axis=None):
+    """pa_fp8_qkv_norm_rope_append's arguments but the stream, or with pair_axis
+    pa_fp8_qkv_norm_mrope_append's, and the objects they point into."""
     torch = _torch()
     floats = (torch.float32, torch.bfloat16)
     e4m3 = (torch.uint8, torch.float8_e4m3fn)            # what is written, whatever holds it
@@ -566,9 +589,28 @@ def _norm_rope_args(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes, q_
         max_pos, rd = cos_sin.shape
         if positions is None:
             raise ValueError("cos_sin needs positions")
-    if positions is not None:
+    axes = ()
+    if pair_axis is not None:
+        pair_axis = [int(a) for a in pair_axis]
+        if len(pair_axis) != rd // 2:
+            raise ValueError("pair_axis must name an axis for each of the %d pairs" % (rd // 2))
+        _need(positions, "positions", (torch.int32, torch.int64), contiguous=False)
+        if positions.dim() != 2:
+            raise ValueError("positions must be [axes, tokens]")
+        A = positions.shape[0]
+        _shape(positions, "positions", A, T)
+        if T > 0 and ((T > 1 and positions.stride(1) != 1) or (A > 1 and positions.stride(0) < T)):
+            raise ValueError("positions must have contiguous axes that do not overlap")
+        if any(not 0 <= a < A for a in pair_axis):
+            raise ValueError("pair_axis must be below the number of axes, %d" % A)
+        step = positions.stride(0) if A > 1 and T > 0 else T
+        host = (ctypes.c_uint8 * max(1, len(pair_axis)))(*pair_axis)
+        axes = (A, step, ctypes.addressof(host))
+        pair_axis = host
+    elif positions is not None:
         _need(positions, "positions", (torch.int32, torch.int64))
         _shape(positions, "positions", T)
+    if positions is not None:
         pos_type = INDEX_I64 if positions.dtype == torch.int64 else INDEX_I32
     _need(q_codes, "q_codes", e4m3)
     _shape(q_codes, "q_codes", T, NQ, D)
@@ -597,11 +639,11 @@ def _norm_rope_args(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes, q_
     args = (_ptr(q), _ptr(k), _ptr(v), _in_dtype(q), *step,
             _ptr(q_weight), _ptr(k_weight), DTYPE_BF16 if wdt == torch.bfloat16 else DTYPE_F32,
             float(eps), _ptr(cos_sin), rd, max_pos, int(bool(interleaved)), _ptr(positions),
-            pos_type, _ptr(q_codes), _ptr(q_scale), _ptr(key_cache), _ptr(value_cache),
+            pos_type, *axes, _ptr(q_codes), _ptr(q_scale), _ptr(key_cache), _ptr(value_cache),
             _ptr(slot_mapping), _slot_type(slot_mapping), _ptr(key_scale_cache), _ptr(v_scale),
             _ptr(token_batch), v_scale.shape[0], T, NQ, NKV, D, NB, BS, layout)
     keep = (q, k, v, q_weight, k_weight, cos_sin, positions, q_codes, q_scale, key_cache,
-            value_cache, slot_mapping, key_scale_cache, v_scale, token_batch)
+            value_cache, slot_mapping, key_scale_cache, v_scale, token_batch, pair_axis)
     return args, keep
 
 
@@ -641,6 +683,42 @@ def prepare_qkv_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions
                                  v_scale, token_batch, eps, interleaved, layout)
     return _Prepared(lib().pa_fp8_qkv_norm_rope_append, "pa_fp8_qkv_norm_rope_append", args, keep,
                      stream)
+
+
+def qkv_norm_mrope_append(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes, q_scale,
+                          key_cache, value_cache, slot_mapping, key_scale_cache, v_scale,
+                          token_batch, *, pair_axis, eps: float = 1e-5, interleaved: bool = False,
+                          layout: int = LAYOUT_BNBD, stream=None):
+    """qkv_norm_rope_append() for tokens with several positions, as the time,
+    height and width of an image's or a video's patches: positions int32/int64
+    [axes, T] (up to 4 axes, each contiguous), and pair i of the rotated channels
+    takes its angle from positions[pair_axis[i]]. pair_axis: a sequence of
+    rotary_dim/2 ints, such as [0] * 16 + [1] * 24 + [2] * 24 for sections of
+    axes one behind another. Everything else as there."""
+    if pair_axis is None or cos_sin is None:
+        raise TypeError("qkv_norm_mrope_append needs pair_axis and cos_sin")
+    args, keep = _norm_rope_args(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes,
+                                 q_scale, key_cache, value_cache, slot_mapping, key_scale_cache,
+                                 v_scale, token_batch, eps, interleaved, layout, pair_axis)
+    _check(lib().pa_fp8_qkv_norm_mrope_append(*args, _stream(stream)),
+           "pa_fp8_qkv_norm_mrope_append")
+    del keep
+
+
+def prepare_qkv_norm_mrope_append(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes,
+                                  q_scale, key_cache, value_cache, slot_mapping, key_scale_cache,
+                                  v_scale, token_batch, *, pair_axis, eps: float = 1e-5,
+                                  interleaved: bool = False, layout: int = LAYOUT_BNBD,
+                                  stream=None):
+    """qkv_norm_mrope_append() prepared once: returns a callable that launches
+    the same call on the same buffers."""
+    if pair_axis is None or cos_sin is None:
+        raise TypeError("qkv_norm_mrope_append needs pair_axis and cos_sin")
+    args, keep = _norm_rope_args(q, k, v, q_weight, k_weight, cos_sin, positions, q_codes,
+                                 q_scale, key_cache, value_cache, slot_mapping, key_scale_cache,
+                                 v_scale, token_batch, eps, interleaved, layout, pair_axis)
+    return _Prepared(lib().pa_fp8_qkv_norm_mrope_append, "pa_fp8_qkv_norm_mrope_append", args,
+                     keep, stream)
 
 
 def tree_decode_workspace_size(B: int, S1: int, NQ: int, NKV: int, D: int = 128) -> int:
@@ -876,6 +954,259 @@ def prepare_cache_keep_path(key_cache, value_cache, key_scale_cache, block_table
     return _Prepared(lib().pa_fp8_cache_keep_path, "pa_fp8_cache_keep_path", args, keep, stream)
 
 
+# --------------------------------------------------------------------------
+# A ragged serving step
+# --------------------------------------------------------------------------
+
+def _plan_args(kv_act_seqs, new_lens, pool, pool_head, block_table, slot_mapping, positions,
+               token_batch, cu_tokens, new_act_seqs, new_pool_head, num_blocks, block_size):
+    torch = _torch()
+    for t, n in ((kv_act_seqs, "kv_act_seqs"), (new_lens, "new_lens"), (pool, "pool"),
+                 (pool_head, "pool_head"), (block_table, "block_table"),
+                 (positions, "positions"), (token_batch, "token_batch"),
+                 (cu_tokens, "cu_tokens"), (new_act_seqs, "new_act_seqs"),
+                 (new_pool_head, "new_pool_head")):
+        _need(t, n, torch.int32)
+    _need(slot_mapping, "slot_mapping", (torch.int32, torch.int64))
+    if block_table.dim() != 2 or slot_mapping.dim() != 1 or pool.dim() != 1:
+        raise ValueError("block_table must be [B, max_blocks], slot_mapping [tokens] and pool "
+                         "[blocks]")
+    B, T = block_table.shape[0], slot_mapping.shape[0]
+    for t, n in ((kv_act_seqs, "kv_act_seqs"), (new_lens, "new_lens"),
+                 (new_act_seqs, "new_act_seqs")):
+        _shape(t, n, B)
+    for t, n in ((positions, "positions"), (token_batch, "token_batch")):
+        _shape(t, n, T)
+    _shape(cu_tokens, "cu_tokens", B + 1)
+    for t, n in ((pool_head, "pool_head"), (new_pool_head, "new_pool_head")):
+        _shape(t, n, 1)
+    _one_device(kv_act_seqs=kv_act_seqs, new_lens=new_lens, pool=pool, pool_head=pool_head,
+                block_table=block_table, slot_mapping=slot_mapping, positions=positions,
+                token_batch=token_batch, cu_tokens=cu_tokens, new_act_seqs=new_act_seqs,
+                new_pool_head=new_pool_head)
+    args = (_ptr(kv_act_seqs), _ptr(new_lens), _ptr(pool), _ptr(pool_head), _ptr(block_table),
+            _ptr(slot_mapping), _slot_type(slot_mapping), _ptr(positions), _ptr(token_batch),
+            _ptr(cu_tokens), _ptr(new_act_seqs), _ptr(new_pool_head), B, T, pool.shape[0],
+            int(num_blocks), int(block_size), block_table.shape[1])
+    keep = (kv_act_seqs, new_lens, pool, pool_head, block_table, slot_mapping, positions,
+            token_batch, cu_tokens, new_act_seqs, new_pool_head)
+    return args, keep
+
+
+def plan_batch(kv_act_seqs, new_lens, pool, pool_head, block_table, slot_mapping, positions,
+               token_batch, cu_tokens, new_act_seqs, new_pool_head, *, num_blocks: int,
+               block_size: int = 128, stream=None):
+    """Where a step's new tokens go, from the requests' lengths, on the device
+    (in place into block_table and the tensors behind it).
+
+    kv_act_seqs, new_lens int32 [B]: positions in the cache and new tokens of
+    each request; pool int32 [blocks]: ids of blocks, those from pool_head[0] on
+    free; block_table int32 [B, max_blocks]: gets the new blocks' entries.
+    slot_mapping int32/int64, positions and token_batch int32 [T]: of the tokens
+    that the requests bring, one request behind another, -1, 0 and 0 behind;
+    cu_tokens int32 [B + 1]: the requests' first rows; new_act_seqs int32 [B];
+    pool_head, new_pool_head int32 [1]. num_blocks: of the cache.
+
+    A request that does not fit its row of the block table, the T rows or what is
+    left of the pool is refused: its slots are -1 and its length stays. The
+    outputs overlap neither an input nor one another."""
+    args, keep = _plan_args(kv_act_seqs, new_lens, pool, pool_head, block_table, slot_mapping,
+                            positions, token_batch, cu_tokens, new_act_seqs, new_pool_head,
+                            num_blocks, block_size)
+    _check(lib().pa_plan_batch(*args, _stream(stream)), "pa_plan_batch")
+    del keep
+
+
+def prepare_plan_batch(kv_act_seqs, new_lens, pool, pool_head, block_table, slot_mapping,
+                       positions, token_batch, cu_tokens, new_act_seqs, new_pool_head, *,
+                       num_blocks: int, block_size: int = 128, stream=None):
+    """plan_batch() prepared once: returns a callable that launches the same call
+    on the same buffers."""
+    args, keep = _plan_args(kv_act_seqs, new_lens, pool, pool_head, block_table, slot_mapping,
+                            positions, token_batch, cu_tokens, new_act_seqs, new_pool_head,
+                            num_blocks, block_size)
+    return _Prepared(lib().pa_plan_batch, "pa_plan_batch", args, keep, stream)
+
+
+def window_attention_workspace_size(max_tokens: int, NQ: int, NKV: int, D: int = 128) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().pa_fp8_window_attention_workspace_size(max_tokens, NQ, NKV, D, ctypes.byref(n)),
+           "pa_fp8_window_attention_workspace_size")
+    return n.value
+
+
+class WindowWorkspace:
+    """Zero-initialised device scratch for window_attention (reusable: every call
+    leaves what must be zero at zero), for calls of at most max_tokens tokens a
+    sequence. Calls that may run at the same time, replays of two captured graphs
+    among them, need one each."""
+
+    def __init__(self, max_tokens, NQ, NKV, D=128, *, device=None):
+        torch = _torch()
+        self.nbytes = window_attention_workspace_size(max_tokens, NQ, NKV, D)
+        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+
+    def error_flags(self) -> int:
+        """Non-zero if a kernel wait gave up (bitmask of the wait sites)."""
+        return int(self.buf[:4].view(_torch().int32).item())
+
+    def clear_error_flags(self) -> None:
+        """Zero the error word (on the current stream)."""
+        self.buf[:4].zero_()
+
+
+def _window_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_act_seqs,
+                 cu_tokens, out, window, sinks, max_tokens, layout, softmax_scale, workspace,
+                 stream, ready=False):
+    torch = _torch()
+    for t, n in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, (torch.uint8, torch.float8_e4m3fn))
+    for t, n in ((q_scale, "q_scale"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need(t, n, torch.float32)
+    for t, n in ((block_table, "block_table"), (kv_act_seqs, "kv_act_seqs"),
+                 (cu_tokens, "cu_tokens")):
+        _need(t, n, torch.int32)
+    _need(out, "out", torch.bfloat16)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_size]")
+    T, NQ, D = q.shape
+    B = kv_act_seqs.shape[0]
+    NB, NKV, BS = _cache_dims(k_cache, layout)
+    cache = (NB, BS, NKV) if layout == LAYOUT_BSND else (NB, NKV, BS)
+    _shape(k_cache, "k_cache", *cache, D)
+    _shape(v_cache, "v_cache", *cache, D)
+    if k_scale.numel() != NB * BS * NKV:
+        raise ValueError("k_scale must have one scale a cache row")
+    _shape(q_scale, "q_scale", T, NQ)
+    _shape(v_scale, "v_scale", B, NKV, D)
+    _shape(out, "out", T, NQ, D)
+    _shape(kv_act_seqs, "kv_act_seqs", B)
+    _shape(cu_tokens, "cu_tokens", B + 1)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_blocks]")
+    if window is not None and window < 1:
+        raise ValueError("window must be 1 or more, or None for all keys")
+    if sinks < 0:
+        raise ValueError("sinks must be 0 or more")
+    if max_tokens is None:
+        max_tokens = max(1, T)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    if workspace is None:
+        workspace = _own_workspace(lambda: WindowWorkspace(max_tokens, NQ, NKV, D,
+                                                           device=q.device), stream, ready)
+    _one_device(q=q, q_scale=q_scale, k_cache=k_cache, k_scale=k_scale, v_cache=v_cache,
+                v_scale=v_scale, block_table=block_table, kv_act_seqs=kv_act_seqs,
+                cu_tokens=cu_tokens, out=out, workspace=workspace.buf)
+    args = (_ptr(q), _ptr(q_scale), _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale),
+            _ptr(block_table), _ptr(kv_act_seqs), _ptr(cu_tokens), _ptr(out), B, T,
+            int(max_tokens), NQ, NKV, D, BS, NB, block_table.shape[1], layout,
+            0 if window is None else int(window), int(sinks), float(softmax_scale),
+            _ptr(workspace.buf), workspace.nbytes)
+    keep = (q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_act_seqs, cu_tokens,
+            out, workspace)
+    return args, keep
+
+
+def window_attention(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table, kv_act_seqs,
+                     cu_tokens, out, *, window: int | None, sinks: int = 0,
+                     max_tokens: int | None = None, layout: int = LAYOUT_BSND,
+                     softmax_scale=None, workspace: WindowWorkspace | None = None, stream=None):
+    """Causal attention of a ragged batch to a sliding window and to the first
+    tokens, over the paged FP8 cache (in place into ``out``): the token at
+    position p sees the keys j <= p with p - j < window (all of them with None)
+    or j < sinks.
+
+    q [T, NQ, 128] E4M3, q_scale float32 [T, NQ], out bfloat16 [T, NQ, 128]: rows
+    cu_tokens[b] .. cu_tokens[b + 1] - 1 (int32 [B + 1]) are the last positions of
+    sequence b, which kv_act_seqs int32 [B] counts in; rows behind cu_tokens[B]
+    stay as they were. The caches, their scales and the block table as in
+    decode(); entries of blocks that no row sees need not be valid. max_tokens:
+    the most tokens a sequence has (default T; the scratch and the choice of the
+    kernel go by it, and tokens of a sequence behind it get zeros)."""
+    args, keep = _window_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table,
+                              kv_act_seqs, cu_tokens, out, window, sinks, max_tokens, layout,
+                              softmax_scale, workspace, stream)
+    _check(lib().pa_fp8_window_attention(*args, _stream(stream)), "pa_fp8_window_attention")
+    del keep   # (a workspace made here lives until the launch is enqueued)
+    return out
+
+
+def prepare_window_attention(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table,
+                             kv_act_seqs, cu_tokens, out, *, window: int | None, sinks: int = 0,
+                             max_tokens: int | None = None, layout: int = LAYOUT_BSND,
+                             softmax_scale=None, workspace: WindowWorkspace | None = None,
+                             stream=None):
+    """window_attention() prepared once: returns a callable that launches the same
+    call on the same buffers."""
+    args, keep = _window_args(q, q_scale, k_cache, k_scale, v_cache, v_scale, block_table,
+                              kv_act_seqs, cu_tokens, out, window, sinks, max_tokens, layout,
+                              softmax_scale, workspace, stream, ready=True)
+    return _Prepared(lib().pa_fp8_window_attention, "pa_fp8_window_attention", args, keep, stream,
+                     scratch=None if workspace is not None else keep[-1])
+
+
+def _logprob_args(logits, tokens, logprobs, ranks, entropy, top_ids, top_logprobs):
+    torch = _torch()
+    _need(logits, "logits", (torch.float32, torch.bfloat16), contiguous=False)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, V]")
+    R, V = logits.shape
+    if (V > 1 and logits.stride(1) != 1) or (R > 1 and logits.stride(0) < V):
+        raise ValueError("logits must have contiguous rows that do not overlap")
+    _need(tokens, "tokens", (torch.int32, torch.int64))
+    _shape(tokens, "tokens", R)
+    _need(logprobs, "logprobs", torch.float32)
+    _shape(logprobs, "logprobs", R)
+    for t, n, dt in ((ranks, "ranks", torch.int32), (entropy, "entropy", torch.float32)):
+        if t is not None:
+            _need(t, n, dt)
+            _shape(t, n, R)
+    top = 0
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs go together")
+    if top_ids is not None:
+        _need(top_ids, "top_ids", torch.int32)
+        if top_ids.dim() != 2:
+            raise ValueError("top_ids must be [rows, alternatives]")
+        top = top_ids.shape[1]
+        _shape(top_ids, "top_ids", R, top)
+        _need(top_logprobs, "top_logprobs", torch.float32)
+        _shape(top_logprobs, "top_logprobs", R, top)
+    _one_device(logits=logits, tokens=tokens, logprobs=logprobs, ranks=ranks, entropy=entropy,
+                top_ids=top_ids, top_logprobs=top_logprobs)
+    args = (_ptr(logits), _in_dtype(logits), logits.stride(0) if R > 1 else V, _ptr(tokens),
+            INDEX_I64 if tokens.dtype == torch.int64 else INDEX_I32, R, V, _ptr(logprobs),
+            _ptr(ranks), _ptr(entropy), top, _ptr(top_ids), _ptr(top_logprobs))
+    keep = (logits, tokens, logprobs, ranks, entropy, top_ids, top_logprobs)
+    return args, keep
+
+
+def token_logprobs(logits, tokens, logprobs, *, ranks=None, entropy=None, top_ids=None,
+                   top_logprobs=None, stream=None):
+    """Log probabilities of given tokens from logits (in place into logprobs and
+    the others that are given).
+
+    logits float32 or bfloat16 [R, V], rows any stride apart (a padded
+    vocabulary's view); tokens int32/int64 [R]; logprobs float32 [R]; ranks int32
+    [R]: how many logits are larger than the token's; entropy float32 [R];
+    top_ids int32 and top_logprobs float32 [R, k], k at most 32: the k most
+    probable tokens, of equal ones the lower index first. A logit of -inf has the
+    log probability -inf; a row with a NaN or +inf gets NaN, ranks and ids -1, a
+    token outside [0, V) NaN and rank -1."""
+    args, keep = _logprob_args(logits, tokens, logprobs, ranks, entropy, top_ids, top_logprobs)
+    _check(lib().pa_token_logprobs(*args, _stream(stream)), "pa_token_logprobs")
+    del keep
+
+
+def prepare_token_logprobs(logits, tokens, logprobs, *, ranks=None, entropy=None, top_ids=None,
+                           top_logprobs=None, stream=None):
+    """token_logprobs() prepared once: returns a callable that launches the same
+    call on the same buffers."""
+    args, keep = _logprob_args(logits, tokens, logprobs, ranks, entropy, top_ids, top_logprobs)
+    return _Prepared(lib().pa_token_logprobs, "pa_token_logprobs", args, keep, stream)
+
+
 __all__ = [
     "LAYOUT_BSND", "LAYOUT_BNBD", "PaError", "build", "lib", "decode", "decode_workspace_size",
     "auto_s2_tile", "prepare_decode", "prepare_cache_quant_scatter",
@@ -883,6 +1214,9 @@ __all__ = [
     "value_channel_scale", "qkv_norm_rope_append", "prepare_qkv_norm_rope_append",
     "tree_decode", "prepare_tree_decode", "tree_decode_workspace_size", "TreeWorkspace",
     "tree_verify", "prepare_tree_verify", "cache_keep_path", "prepare_cache_keep_path",
+    "plan_batch", "prepare_plan_batch", "qkv_norm_mrope_append", "prepare_qkv_norm_mrope_append",
+    "window_attention", "prepare_window_attention", "window_attention_workspace_size",
+    "WindowWorkspace", "token_logprobs", "prepare_token_logprobs",
 ]
 
 

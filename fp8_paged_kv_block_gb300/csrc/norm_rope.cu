@@ -38,6 +38,7 @@ constexpr int kSets = 4;
 constexpr int kBlocks = 5;                   // CTAs an SM: 96 registers
 constexpr int kStages = 2;                   // jobs of a warp in shared memory
 constexpr int kJob = kSets * 256;            // values of a job's rows
+constexpr int kMaxAxes = 4;
 
 struct NormRopeParams {
     const void *q, *k, *v;
@@ -50,6 +51,9 @@ struct NormRopeParams {
     int64_t max_pos;
     const void* pos;
     int pos_type;
+    int axes;                         // of positions, axis_stride elements apart
+    int64_t axis_stride;
+    uint32_t pair_axis[8];            // each pair's axis, 2 bits
     uint8_t* q_codes;
     float* q_scale;
     uint8_t *kc, *vc;
@@ -82,9 +86,9 @@ __device__ __forceinline__ void unpack(const uint2& r, float2& a, float2& b)
     a = make_float2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u));
     b = make_float2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u));
 }
-__device__ __forceinline__ void prefetch_l1(const void* p, int type, uint32_t i)
+__device__ __forceinline__ void prefetch_l1(const void* p, int type, int64_t i)
 {
-    const char* at = static_cast<const char*>(p) + static_cast<int64_t>(i) * (type == PA_INDEX_I64 ? 8 : 4);
+    const char* at = static_cast<const char*>(p) + i * (type == PA_INDEX_I64 ? 8 : 4);
     asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
 }
 
@@ -122,7 +126,11 @@ __device__ __forceinline__ float reduce_sets(const float (&a)[kSets], int lane, 
     return v;
 }
 
-template <typename T, int D, bool INTER>
+// AXES: a token has p.axes positions, and each pair its angle from the one that
+// pair_axis names. The four pairs of a lane may name different ones: their angles
+// are loaded one by one, once a token and kind, from rows that neighbouring lanes
+// mostly share.
+template <typename T, int D, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel(const NormRopeParams p)
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = kSets * RPW;
@@ -140,7 +148,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel
     int a_slot = 0;
     // the first token's position and slot on their way to L1 (the angles and rows wait
     // for them, and the rows' addresses take a while)
-    if (p.rd > 0) prefetch_l1(p.pos, p.pos_type, a_tok);
+    if (p.rd > 0) {
+        prefetch_l1(p.pos, p.pos_type, a_tok);
+        if (AXES) {
+            for (int a = 1; a < p.axes; ++a) prefetch_l1(p.pos, p.pos_type, a * p.axis_stride + a_tok);
+        }
+    }
     prefetch_l1(p.slots, p.slot_type, a_tok);
     auto fetch = [&] {
         if (ahead < end) {
@@ -185,7 +198,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel
         const void* w = is_q ? p.qw : p.kw;
         if (fresh || part == 0) {
             const int rd = is_v ? 0 : p.rd, half = rd >> 1;
-            int64_t pos = rd > 0 ? load_slot(p.pos, p.pos_type, t_now) : 0;
+            int64_t pos = !AXES && rd > 0 ? load_slot(p.pos, p.pos_type, t_now) : 0;
+            int64_t on[kMaxAxes] = {};       // rows of the axes' positions
+            if (AXES && rd > 0) {
+#pragma unroll
+                for (int a = 0; a < kMaxAxes; ++a) {
+                    if (a >= p.axes) break;
+                    on[a] = load_slot(p.pos, p.pos_type, a * p.axis_stride + t_now);
+                    on[a] = (on[a] < 0 ? 0 : (on[a] >= p.max_pos ? p.max_pos - 1 : on[a])) * rd;
+                }
+            }
             const int64_t s = is_q ? 0 : load_slot(p.slots, p.slot_type, t_now);
             if (INTER) {
                 c0 = 4 * sub;
@@ -211,7 +233,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) qkv_norm_rope_append_kernel
             }
             pos = pos < 0 ? 0 : (pos >= p.max_pos ? p.max_pos - 1 : pos);
             const float* a = p.cos_sin + pos * rd;
-            if (INTER) {
+            if (AXES) {
+                // pairs of the lane: e in 0..3, cs[0].x, cs[0].y, cs[1].x, cs[1].y
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (!(e < 2 || !INTER ? rot0 : rot1)) continue;
+                    const int i = INTER ? ((e < 2 ? c0 : c1) >> 1) + (e & 1) : c0 + e;
+                    const uint32_t x = p.pair_axis[i >> 4] >> (2 * (i & 15));
+                    const float* r = p.cos_sin + (x & 2 ? (x & 1 ? on[3] : on[2]) : (x & 1 ? on[1] : on[0])) + i;
+                    ((e & 1) ? cs[e >> 1].y : cs[e >> 1].x) = __ldg(r);
+                    ((e & 1) ? sn[e >> 1].y : sn[e >> 1].x) = __ldg(r + half);
+                }
+            } else if (INTER) {
                 if (rot0) {
                     cs[0] = __ldg(reinterpret_cast<const float2*>(a + (c0 >> 1)));
                     sn[0] = __ldg(reinterpret_cast<const float2*>(a + half + (c0 >> 1)));
@@ -404,8 +437,13 @@ void launch(NormRopeParams p, bool inter, int sms, cudaStream_t st)
     const uint32_t ctas = std::min((jobs - 1) / warps + 1, static_cast<uint32_t>(sms * kBlocks));
     p.per = jobs / (ctas * warps);
     p.longer = jobs % (ctas * warps);
-    if (inter) qkv_norm_rope_append_kernel<T, D, true><<<ctas, kThreads, 0, st>>>(p);
-    else qkv_norm_rope_append_kernel<T, D, false><<<ctas, kThreads, 0, st>>>(p);
+    if (p.axes) {
+        if (inter) qkv_norm_rope_append_kernel<T, D, true, true><<<ctas, kThreads, 0, st>>>(p);
+        else qkv_norm_rope_append_kernel<T, D, false, true><<<ctas, kThreads, 0, st>>>(p);
+    } else {
+        if (inter) qkv_norm_rope_append_kernel<T, D, true, false><<<ctas, kThreads, 0, st>>>(p);
+        else qkv_norm_rope_append_kernel<T, D, false, false><<<ctas, kThreads, 0, st>>>(p);
+    }
 }
 
 template <typename T>
@@ -416,21 +454,16 @@ void launch_d(const NormRopeParams& p, int D, bool inter, int sms, cudaStream_t 
     else launch<T, 256>(p, inter, sms, st);
 }
 
-}  // namespace
-}  // namespace pa
-
-using namespace pa;
-
-extern "C" pa_status pa_fp8_qkv_norm_rope_append(
-    const void* q, const void* k, const void* v, int in_dtype, int64_t q_stride, int64_t k_stride,
+// Both entry points; num_axes 0: one position a token.
+pa_status append(
+    const char* name, const void* q, const void* k, const void* v, int in_dtype, int64_t q_stride, int64_t k_stride,
     int64_t v_stride, const void* q_weight, const void* k_weight, int weight_dtype, float eps,
     const float* cos_sin, int rotary_dim, int64_t max_position, int interleaved,
-    const void* positions, int pos_type, void* q_codes, float* q_scale, void* key_cache,
-    void* value_cache, const void* slot_mapping, int slot_type, float* key_scale_cache,
-    const float* v_scale, const int32_t* token_batch, int num_batches, int64_t num_tokens, int NQ,
-    int NKV, int head_size, int64_t num_blocks, int block_size, int layout, void* stream)
+    const void* positions, int pos_type, int num_axes, int64_t axis_stride, const uint8_t* pair_axis, void* q_codes,
+    float* q_scale, void* key_cache, void* value_cache, const void* slot_mapping, int slot_type,
+    float* key_scale_cache, const float* v_scale, const int32_t* token_batch, int num_batches, int64_t num_tokens,
+    int NQ, int NKV, int head_size, int64_t num_blocks, int block_size, int layout, void* stream)
 {
-    const char* name = "pa_fp8_qkv_norm_rope_append";
     // (tensors of no tokens may have no address)
     PA_REQUIRE(key_cache && value_cache && key_scale_cache && v_scale &&
                    (num_tokens == 0 || (q && k && v && q_codes && q_scale && slot_mapping && token_batch)),
@@ -471,8 +504,16 @@ extern "C" pa_status pa_fp8_qkv_norm_rope_append(
                PA_ERR_UNSUPPORTED, "%s: more than 2^32 head rows", name);
     PA_REQUIRE(NQ <= 0x7FFFFFFF / head_size && NKV <= 0x7FFFFFFF / head_size, PA_ERR_UNSUPPORTED,
                "%s: a token of 2^31 values or more", name);
-    if (num_tokens == 0) return PA_OK;
     NormRopeParams p;
+    p.axes = num_axes;
+    p.axis_stride = axis_stride;
+    for (uint32_t& x : p.pair_axis) x = 0;
+    for (int i = 0; num_axes > 0 && i < rotary_dim / 2; ++i) {
+        PA_REQUIRE(pair_axis[i] < num_axes, PA_ERR_INVALID, "%s: pair %d on axis %d of %d", name, i, pair_axis[i],
+                   num_axes);
+        p.pair_axis[i >> 4] |= static_cast<uint32_t>(pair_axis[i]) << (2 * (i & 15));
+    }
+    if (num_tokens == 0) return PA_OK;
     p.q = q; p.k = k; p.v = v;
     p.qs = q_stride; p.ks = k_stride; p.vs = v_stride;
     p.qw = q_weight; p.kw = k_weight;
@@ -505,4 +546,47 @@ extern "C" pa_status pa_fp8_qkv_norm_rope_append(
     if (in_dtype == PA_DTYPE_F32) launch_d<float>(p, head_size, interleaved != 0, sms, st);
     else launch_d<__nv_bfloat16>(p, head_size, interleaved != 0, sms, st);
     return check_launch(name);
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" pa_status pa_fp8_qkv_norm_rope_append(
+    const void* q, const void* k, const void* v, int in_dtype, int64_t q_stride, int64_t k_stride,
+    int64_t v_stride, const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+    const float* cos_sin, int rotary_dim, int64_t max_position, int interleaved,
+    const void* positions, int pos_type, void* q_codes, float* q_scale, void* key_cache,
+    void* value_cache, const void* slot_mapping, int slot_type, float* key_scale_cache,
+    const float* v_scale, const int32_t* token_batch, int num_batches, int64_t num_tokens, int NQ,
+    int NKV, int head_size, int64_t num_blocks, int block_size, int layout, void* stream)
+{
+    return append("pa_fp8_qkv_norm_rope_append", q, k, v, in_dtype, q_stride, k_stride, v_stride, q_weight, k_weight,
+                  weight_dtype, eps, cos_sin, rotary_dim, max_position, interleaved, positions, pos_type, 0, 0, nullptr,
+                  q_codes, q_scale, key_cache, value_cache, slot_mapping, slot_type, key_scale_cache, v_scale,
+                  token_batch, num_batches, num_tokens, NQ, NKV, head_size, num_blocks, block_size, layout, stream);
+}
+
+extern "C" pa_status pa_fp8_qkv_norm_mrope_append(
+    const void* q, const void* k, const void* v, int in_dtype, int64_t q_stride, int64_t k_stride,
+    int64_t v_stride, const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+    const float* cos_sin, int rotary_dim, int64_t max_position, int interleaved,
+    const void* positions, int pos_type, int num_axes, int64_t axis_stride, const uint8_t* pair_axis,
+    void* q_codes, float* q_scale, void* key_cache, void* value_cache, const void* slot_mapping,
+    int slot_type, float* key_scale_cache, const float* v_scale, const int32_t* token_batch,
+    int num_batches, int64_t num_tokens, int NQ, int NKV, int head_size, int64_t num_blocks,
+    int block_size, int layout, void* stream)
+{
+    const char* name = "pa_fp8_qkv_norm_mrope_append";
+    PA_REQUIRE(num_axes > 0 && num_tokens >= 0 && axis_stride >= 0, PA_ERR_INVALID,
+               "%s: num_axes %d, axis_stride or num_tokens negative", name, num_axes);
+    PA_REQUIRE(num_axes <= kMaxAxes, PA_ERR_UNSUPPORTED, "%s: %d axes (at most %d)", name, num_axes, kMaxAxes);
+    PA_REQUIRE(rotary_dim <= 0 || pair_axis, PA_ERR_NULLPTR, "%s: NULL pair_axis", name);
+    PA_REQUIRE(rotary_dim <= 0 || num_axes == 1 || axis_stride >= num_tokens, PA_ERR_INVALID,
+               "%s: axes of positions overlap", name);
+    return append(name, q, k, v, in_dtype, q_stride, k_stride, v_stride, q_weight, k_weight, weight_dtype, eps, cos_sin,
+                  rotary_dim, max_position, interleaved, positions, pos_type, num_axes, axis_stride, pair_axis, q_codes,
+                  q_scale, key_cache, value_cache, slot_mapping, slot_type, key_scale_cache, v_scale, token_batch,
+                  num_batches, num_tokens, NQ, NKV, head_size, num_blocks, block_size, layout, stream);
 }

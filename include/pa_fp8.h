@@ -657,6 +657,161 @@ PA_API pa_status pa_fp8_cache_keep_path(void* key_cache, void* value_cache,
                                         int head_size, int block_size, int64_t num_blocks,
                                         int max_blocks_per_seq, int layout, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A ragged serving step over the paged FP8 cache: B requests, request b with
+ * kv_act_seqs[b] positions in the cache and new_lens[b] new tokens (one for a
+ * decoding request, a chunk for a prompt). The requests' tokens are rows one
+ * behind another: rows cu_tokens[b] .. cu_tokens[b + 1] - 1 of q, k, v and out
+ * are request b's. The pages have no counterpart to the four calls; they use
+ * the pages' cache layouts, scales and codes. One step is
+ *   pa_plan_batch                where the new tokens go: blocks, slots,
+ *                                positions, cu_tokens, new lengths;
+ *   pa_fp8_qkv_norm_mrope_append (or pa_fp8_qkv_norm_rope_append) q to FP8, k
+ *                                and v into the cache;
+ *   pa_fp8_window_attention      each token attends to its window and to the
+ *                                first tokens;
+ *   pa_token_logprobs            log probabilities of the tokens.
+ * A call of no tokens, rows or requests is checked and enqueues nothing (but
+ * for pa_plan_batch, whose sums have an entry); the tensors that then have no
+ * elements may be NULL. Every tensor is aligned to its elements; what needs
+ * more says so (PA_ERR_INVALID otherwise).
+ * ------------------------------------------------------------------------ */
+
+/* ------------------------------------------------------------------------
+ * pa_fp8_qkv_norm_mrope_append -- pa_fp8_qkv_norm_rope_append for tokens with
+ * several positions (time, height and width of an image's or a video's
+ * patches): pair i of the rotated channels takes its angle from cos_sin row
+ * positions[pair_axis[i]][t], clamped to [0, max_position).
+ * positions    int32 or int64 [num_axes, num_tokens] (pos_type), axes
+ *              axis_stride elements apart (at least num_tokens).
+ * num_axes     1 to 4 (more: PA_ERR_UNSUPPORTED).
+ * pair_axis    HOST memory, rotary_dim / 2 bytes, each below num_axes: sections
+ *              of axes one behind another, axes in turn, or any other order.
+ *              Read before the call returns. May be NULL with rotary_dim 0.
+ * Everything else as there.
+ * ------------------------------------------------------------------------ */
+PA_API pa_status pa_fp8_qkv_norm_mrope_append(
+    const void* q, const void* k, const void* v, int in_dtype, int64_t q_stride, int64_t k_stride,
+    int64_t v_stride, const void* q_weight, const void* k_weight, int weight_dtype, float eps,
+    const float* cos_sin, int rotary_dim, int64_t max_position, int interleaved,
+    const void* positions, int pos_type, int num_axes, int64_t axis_stride, const uint8_t* pair_axis,
+    void* q_codes, float* q_scale, void* key_cache, void* value_cache, const void* slot_mapping,
+    int slot_type, float* key_scale_cache, const float* v_scale, const int32_t* token_batch,
+    int num_batches, int64_t num_tokens, int NQ, int NKV, int head_size, int64_t num_blocks,
+    int block_size, int layout, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_plan_batch -- block tables, slots and positions of a step's tokens from
+ * the requests' lengths, on the device. With a = kv_act_seqs[b], n =
+ * new_lens[b] (both taken as 0 below 0):
+ *   cu_tokens[b]  = min(sum of n before request b, num_tokens)
+ *   need(b)       = ceil((a + n) / block_size) - ceil(a / block_size)
+ *   a request is refused (need 0) if a + n positions pass its row of the block
+ *     table or its tokens pass num_tokens, and (need counted all the same) if
+ *     it needs blocks and pool_head[0] + sum of need up to and with it passes
+ *     pool_size; the others are granted, those that need no block always.
+ *   new blocks    block_table[b][ceil(a / block_size) + k] = pool[pool_head[0]
+ *                 + sum of need before b + k], k < need(b), of granted requests
+ *   token i of request b, row t = cu_tokens[b] + i: positions[t] = a + i,
+ *     token_batch[t] = b, slot_mapping[t] = the slot of that position, or -1 if
+ *     the request is refused or the block's id lies outside [0, num_blocks)
+ *   rows behind the last request's: position 0, batch 0, slot -1
+ *   new_act_seqs[b] = a + n, or a if refused
+ *   new_pool_head[0] = pool_head[0] (taken into [0, pool_size]) + blocks taken
+ * The append writes nothing for slot -1, so a captured step may be padded. What
+ * pa_fp8_window_attention gives for a refused request's rows is not meaningful.
+ * kv_act_seqs, new_lens, new_act_seqs  int32 [B]; pool int32 [pool_size], ids of
+ *              blocks, those from pool_head[0] on free; pool_head,
+ *              new_pool_head int32 [1].
+ * block_table  int32 [B, max_blocks_per_seq], in place: entries of other
+ *              positions stay.
+ * slot_mapping int32 or int64 (slot_type) [num_tokens]; positions, token_batch
+ *              int32 [num_tokens]; cu_tokens int32 [B + 1].
+ * Outputs (block_table among them) overlap neither an input nor one another.
+ * B at most 1024; num_tokens, pool_size and max_blocks_per_seq * block_size
+ * below 2^31, and with int32 slots num_blocks * block_size (else
+ * PA_ERR_UNSUPPORTED). A call of no requests or no tokens runs like any other.
+ * ------------------------------------------------------------------------ */
+PA_API pa_status pa_plan_batch(const int32_t* kv_act_seqs, const int32_t* new_lens, const int32_t* pool,
+                               const int32_t* pool_head, int32_t* block_table, void* slot_mapping,
+                               int slot_type, int32_t* positions, int32_t* token_batch,
+                               int32_t* cu_tokens, int32_t* new_act_seqs, int32_t* new_pool_head, int B,
+                               int64_t num_tokens, int64_t pool_size, int64_t num_blocks,
+                               int block_size, int max_blocks_per_seq, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_fp8_window_attention -- causal attention of a ragged batch to a sliding
+ * window and to the sequence's first positions, over the paged FP8 cache. Rows
+ * cu_tokens[b] .. cu_tokens[b + 1] - 1 of q are the last positions of sequence
+ * b, kv_act_seqs[b] counting them in. For a row at position p, head h, kv head
+ * h / (NQ / NKV), over the keys j <= p with p - j < window or j < sinks:
+ *   S_j = (Q_fp8 . K_fp8,j) * q_scale * k_scale_j * softmax_scale
+ *   out = BF16((sum_j exp(S_j - M) V_fp8,j) * v_scale / sum_j exp(S_j - M))
+ * with M the maximum of the row's S_j; P = exp(S - M) enters the second
+ * contraction as FP16, as pa_fp8_tree_decode's.
+ * window       0: no window, all keys j <= p. sinks: 0 or more.
+ * cu_tokens    int32 [B + 1], not decreasing, from 0; values are clamped to
+ *              [0, num_tokens]. Rows of out behind cu_tokens[B] stay as they
+ *              were.
+ * max_tokens   the most tokens a sequence has; of one that has more, those
+ *              behind the first max_tokens get zeros.
+ * Rows whose position is negative (more tokens than kv_act_seqs[b]) get zeros.
+ * Only blocks that a row sees are read: block table entries of others need not
+ * be valid, so that blocks behind every window may have been given back. Block
+ * ids outside [0, num_blocks) read block 0; kv_act_seqs is clamped to
+ * max_blocks_per_seq * block_size. Cache bytes at positions that no row of the
+ * call sees do not matter. A NaN code or scale of K (or of q) gives NaN to the
+ * rows that see the key, and to no others; NaN codes of V at a position that a
+ * row sees are out of contract.
+ * D, block_size  128 and 128 (else PA_ERR_UNSUPPORTED). NQ / NKV at most 128, B
+ * at most 1024, max_blocks_per_seq * 128 below 2^24, num_tokens * NQ below 2^31
+ * and (num_tokens * NQ / NKV / 256 + 1 + B) * NKV * (2 max_blocks_per_seq + 8)
+ * below 2^32 (else PA_ERR_UNSUPPORTED).
+ * workspace    at least pa_fp8_window_attention_workspace_size() bytes of the
+ *              same max_tokens and heads (or of more tokens), 256-byte aligned,
+ *              its first 256 bytes zero before the first call (every call leaves
+ *              them so). Calls that share a workspace must not overlap in time:
+ *              two captured graphs that may run at once need one each. Its first
+ *              word is an error word as pa_fp8_decode's: a wait that gave up
+ *              (about 2 s) sets a bit, the output is then undefined.
+ * Alignment: q, k_cache, v_cache, v_scale and out 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+PA_API pa_status pa_fp8_window_attention_workspace_size(int max_tokens, int NQ, int NKV, int D,
+                                                        size_t* bytes);
+
+PA_API pa_status pa_fp8_window_attention(const void* q, const float* q_scale, const void* k_cache,
+                                         const float* k_scale, const void* v_cache,
+                                         const float* v_scale, const int32_t* block_table,
+                                         const int32_t* kv_act_seqs, const int32_t* cu_tokens,
+                                         void* out, int B, int64_t num_tokens, int max_tokens,
+                                         int NQ, int NKV, int D, int block_size, int64_t num_blocks,
+                                         int max_blocks_per_seq, int layout, int64_t window,
+                                         int64_t sinks, float softmax_scale, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_token_logprobs -- from rows of logits x, in FP32: with M the maximum of a
+ * row and L = sum_i exp(x_i - M),
+ *   logprobs[r] = x_t - M - log L, t = tokens[r]
+ *   ranks[r]    = number of i with x_i > x_t (0: the most probable)
+ *   entropy[r]  = log L - sum_i (x_i - M) exp(x_i - M) / L
+ *   top_ids[r][j], top_logprobs[r][j]  the j-th largest logit's index and log
+ *                 probability; of equal ones the lower index comes first.
+ * A logit of -inf (a masked token) has the log probability -inf and adds nothing;
+ * in a row of nothing else the entropy is 0. A row with a NaN or +inf gets NaN,
+ * rank -1 and ids -1; a token outside [0, V) gets NaN and rank -1.
+ * logits       FP32 or BF16 (dtype) [num_rows, V], rows row_stride elements
+ *              apart (at least V), aligned to their elements.
+ * tokens       int32 or int64 (token_type) [num_rows].
+ * ranks, entropy  int32 and float [num_rows], or NULL.
+ * top          0 to 32 (more: PA_ERR_UNSUPPORTED) and at most V; top_ids int32,
+ *              top_logprobs float [num_rows, top] (not used with 0).
+ * ------------------------------------------------------------------------ */
+PA_API pa_status pa_token_logprobs(const void* logits, int dtype, int64_t row_stride, const void* tokens,
+                                   int token_type, int64_t num_rows, int V, float* logprobs,
+                                   int32_t* ranks, float* entropy, int top, int32_t* top_ids,
+                                   float* top_logprobs, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
