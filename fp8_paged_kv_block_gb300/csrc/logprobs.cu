@@ -4,19 +4,27 @@
 //   m = max x, l = sum e^(x - m), s = sum (x - m) e^(x - m)
 //   log p(t) = x_t - m - log l,  H = log l - s / l,  rank = #{i: x_i > x_t}
 //
-// A row goes to a cluster of 1 to 8 CTAs, each of which takes a part of it in
-// chunks of 16 values a thread, the next chunk's loads under way while it works on
-// one. A thread keeps its own m, l and s (FP32, a few hundred terms each) and
-// rescales them when its maximum grows; they are joined at the end, over lanes,
-// warps and the cluster's CTAs.
+// A row goes to a cluster of 1 to 8 CTAs, each of which takes a part of it in chunks
+// of 64 bytes a thread, and a cluster takes one row after another. A thread copies its
+// own pieces of the next two chunks, the next row's among them, to shared memory (so
+// that no barrier stands between a copy and its use), keeps its own m, l and s (FP32, a
+// few hundred terms each) and rescales them when its maximum grows; they are joined at
+// a row's end, over lanes, warps and the cluster's CTAs. A value's exponent is one
+// fused operation, x log2 e - c with c = m log2 e as rounded; what the rounding is off
+// by is one factor of 16 terms, taken out of their sum. (Past 2^10 that factor is no
+// longer near 1: there, and where a term is -inf, x - m is formed first.)
 //
 // Alternatives: a value and its index make a 64-bit key, larger for the larger
-// value and, among equal ones, for the lower index, so that no two are equal. Values
-// above a bound that at least k values reach are collected in shared memory. The
-// first bound is the k-th largest of the maxima of 32 groups of a chunk; when a chunk
-// leaves kMany candidates or more, they are ranked by counting (a key's rank is the
-// number of larger ones), the first k kept, and the k-th is the new bound. Later
-// values equal to the bound lose to those that are there by their index.
+// value and, among equal ones, for the lower index, so that no two are equal. The pass
+// itself does nothing for them, a thread's maximum is there anyhow. Behind it the k-th
+// largest of the maxima of 32 groups of threads is a bound that k values at least
+// reach; the threads whose maximum does, k to twice as many, have their pieces read
+// again (from L2, a piece a thread), and values that reach the bound go to a list in
+// shared memory, which is put in order by counting (a key's rank is the number of larger
+// ones). A list of more than kShort is thinned first, by the same bound over 32 groups
+// of it; one that runs over (thousands of equal values) is made anew by `careful`, which
+// keeps it short as it goes. -inf is never listed: where fewer than k values are finite
+// the lowest indices of the others follow.
 #include "common.cuh"
 
 #include <cooperative_groups.h>
@@ -31,20 +39,24 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPer = 16;                     // values of a chunk a thread
-constexpr int kChunk = kThreads * kPer;
+constexpr int kPieces = 4;                   // 16-byte pieces of a chunk a thread
+constexpr int kStages = 2;                   // chunks on their way
+constexpr uint32_t kSlot = kPieces * kThreads * 16;   // bytes of a chunk
+constexpr int kPer = 16;                     // values a thread has in registers at once
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
-constexpr int kMany = 128;                   // candidates that are ranked at once
-constexpr int kBatch = 1024;                 // keys ranked together, two a thread
-constexpr int kCap = kChunk + kMany;
+constexpr int kList = 4096;                  // candidates
+constexpr int kShort = 256;                  // of which at most so many are put in order
+constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLeast = -0x1.fffffep127f;
 
 struct LogprobParams {
     const void* x;
     int64_t stride;
     const void* tok;
     int tok_type;
+    int64_t R;
     int V, k;
     float* lp;
     int* ranks;
@@ -60,22 +72,25 @@ struct Stats {
 
 struct TopSmem {
     alignas(16) uint64_t best[kMaxTop];      // in order
-    alignas(16) uint64_t work[kBatch];
-    alignas(16) uint64_t cand[kCap];
+    alignas(16) uint64_t work[kShort + 8];
+    alignas(16) uint64_t list[kList];
+    alignas(16) uint64_t far[kMaxCluster * kMaxTop + 8];   // the first's: every CTA's best
 };
 
 struct Smem {
-    Stats part[kWarps];
-    Stats all;                               // this CTA's, read by the cluster's first
+    Stats part[2][kWarps];                   // by row parity
+    Stats all[kMaxCluster];                  // the first's: every CTA's
     float group[2 * kWarps];
-    int count;
+    uint16_t who[kThreads];                  // threads whose maximum reaches the bound
+    int threads;
+    float bound;
+    int count, left;
 };
 
-// The larger one, NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b)
+__device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -94,289 +109,459 @@ __device__ __forceinline__ uint64_t key_of(float x, uint32_t i)
     return static_cast<uint64_t>(ordered(x + 0.0f)) << 32 | (0xFFFFFFFFu - i);
 }
 
-// Statistics over m = max(a.m, b.m); an empty side (m -inf) changes nothing.
-__device__ __forceinline__ Stats join(const Stats& a, const Stats& b)
-{
-    Stats r;
-    r.m = max_nan(a.m, b.m);
-    r.above = a.above + b.above;
-    r.l = r.s = 0.0f;
-    if (a.m != -INFINITY) {
-        const float d = a.m - r.m, f = ex2(d * kLog2e);
-        r.l += a.l * f;
-        r.s += f == 0.0f ? 0.0f : (a.s + d * a.l) * f;
-    }
-    if (b.m != -INFINITY) {
-        const float d = b.m - r.m, f = ex2(d * kLog2e);
-        r.l += b.l * f;
-        r.s += f == 0.0f ? 0.0f : (b.s + d * b.l) * f;
-    }
-    return r;
-}
-
+// The lanes' statistics over their common maximum. (An empty lane's m is -inf and adds
+// nothing; a NaN is in the sums, not in m, and stays there.)
 __device__ __forceinline__ Stats warp_join(Stats a)
 {
+    const float m = warp_max_f32(a.m), d = a.m - m;
+    const float f = a.m == m ? 1.0f : ex2(d * kLog2e);
+    a.s = f == 1.0f ? a.s : (f == 0.0f ? 0.0f : (a.s + d * a.l) * f);
+    a.l *= f;
+    a.m = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        Stats b;
-        b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-        b.l = __shfl_xor_sync(0xffffffffu, a.l, o);
-        b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-        b.above = __shfl_xor_sync(0xffffffffu, a.above, o);
-        a = join(a, b);
+        a.l += __shfl_xor_sync(0xffffffffu, a.l, o);
+        a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
     }
+    a.above = __reduce_add_sync(0xffffffffu, a.above);
     return a;
 }
 
-// The first k of n candidates to t.best in order (fewer if there are fewer); all
-// threads. Returns how many.
-__device__ __noinline__ int rank_candidates(TopSmem& t, int n, int k)
+// A value that the k-th largest (k <= 32) of the lanes' reaches, the same but for the
+// lower half of its bits: bit by bit, how many lanes have what is fixed and a one.
+__device__ __forceinline__ uint32_t kth_of_lanes(uint32_t x, int k)
 {
-    const int tid = threadIdx.x;
+    bool in = true;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int b = 31; b >= 16; --b) {
+        const uint32_t ones = __ballot_sync(0xffffffffu, in && (x >> b & 1));
+        const bool one = __popc(ones) >= k;
+        if (one) bits |= 1u << b;
+        else k -= __popc(ones);
+        in = in && (x >> b & 1) == one;
+    }
+    return bits;
+}
+
+// The first k of the n <= kShort keys at `keys` (16-byte aligned, room for eight more)
+// to `best` in order; all threads, a barrier before and after.
+__device__ __forceinline__ void put_in_order(uint64_t* best, uint64_t* keys, int n, int k)
+{
+    const int tid = threadIdx.x, end = (n + 7) & ~7;
+    if (tid >= n && tid < end) keys[tid] = 0;             // (below every key)
+    __syncthreads();
+    if (tid < n) {
+        const uint64_t mine = keys[tid];
+        const ulonglong2* all = reinterpret_cast<const ulonglong2*>(keys);
+        int rank = 0;
+#pragma unroll 1
+        for (int i = 0; i < end / 2; i += 4) {
+            ulonglong2 x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = all[i + j];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) rank += (x[j].x > mine) + (x[j].y > mine);
+        }
+        if (rank < k) best[rank] = mine;
+    }
+    __syncthreads();
+}
+
+// The first k of the list's n keys to t.best in order (fewer if there are fewer); all
+// threads, a barrier before and after. A long list is taken kShort at a time, the first
+// k of what was there among them, after what no group of 32 needs has left it.
+__device__ __noinline__ int first_of_list(TopSmem& t, Smem& sm, int n, int k)
+{
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (n > kShort) {
+        // values that the k-th largest of 32 groups' maxima reach, in place: a thread
+        // holds its keys while the others take theirs
+        uint64_t key[kList / kThreads];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kList / kThreads; ++i) {
+            key[i] = tid + i * kThreads < n ? t.list[tid + i * kThreads] : 0ull;
+            m = max(m, static_cast<uint32_t>(key[i] >> 32));
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if ((lane & 15) == 0) sm.group[tid >> 4] = __uint_as_float(m);
+        if (tid == 0) sm.left = 0;
+        __syncthreads();
+        const uint32_t bound = kth_of_lanes(__float_as_uint(sm.group[lane]), k);
+#pragma unroll
+        for (int i = 0; i < kList / kThreads; ++i)
+            if (tid + i * kThreads < n && static_cast<uint32_t>(key[i] >> 32) >= bound)
+                t.list[atomicAdd(&sm.left, 1)] = key[i];
+        __syncthreads();
+        n = sm.left;
+    }
     int kept = 0;
     for (int pos = 0; pos < n;) {
-        // the kept ones and as many others as make a batch
-        const int take = min(n - pos, kBatch - kept), m = kept + take, even = (m + 1) & ~1;
-        for (int i = tid; i < even; i += kThreads)
-            t.work[i] = i < kept ? t.best[i] : (i < m ? t.cand[pos + i - kept] : 0ull);
-        __syncthreads();
-        uint64_t mine[2];
-        int rank[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) mine[i] = tid + i * kThreads < m ? t.work[tid + i * kThreads] : 0ull;
-        const ulonglong2* all = reinterpret_cast<const ulonglong2*>(t.work);
-        if (tid < m) {
-#pragma unroll 4
-            for (int i = 0; i < even / 2; ++i) {
-                const ulonglong2 x = all[i];
-                rank[0] += (x.x > mine[0]) + (x.y > mine[0]);
-                rank[1] += (x.x > mine[1]) + (x.y > mine[1]);
-            }
-        }
-        // (best is read no more)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (tid + i * kThreads < m && rank[i] < k) t.best[rank[i]] = mine[i];
-        kept = min(m, k);
+        const int take = min(n - pos, kShort - kept);
+        if (tid < kept + take) t.work[tid] = tid < kept ? t.best[tid] : t.list[pos + tid - kept];
+        put_in_order(t.best, t.work, kept + take, k);
+        kept = min(kept + take, k);
         pos += take;
-        __syncthreads();
     }
     return kept;
 }
 
-template <typename T>
-struct Raw;
-template <>
-struct Raw<float> {
-    static constexpr int kVec = 4;
-    float4 r;
-    __device__ void load(const float* p) { r = __ldcs(reinterpret_cast<const float4*>(p)); }
-    __device__ void put(int i, float x) { (&r.x)[i] = x; }
-    __device__ float get(int i) const { return (&r.x)[i]; }
-};
-template <>
-struct Raw<__nv_bfloat16> {
-    static constexpr int kVec = 8;
-    uint4 r;
-    __device__ void load(const __nv_bfloat16* p) { r = __ldcs(reinterpret_cast<const uint4*>(p)); }
-    __device__ void put(int i, __nv_bfloat16 x)
-    {
-        uint32_t& w = (&r.x)[i >> 1];
-        const uint32_t u = *reinterpret_cast<const uint16_t*>(&x);
-        w = i & 1 ? (w & 0xFFFFu) | u << 16 : (w & 0xFFFF0000u) | u;
-    }
-    __device__ float get(int i) const
-    {
-        const uint32_t w = (&r.x)[i >> 1];
-        return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
-    }
-};
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float lowest(float) { return -INFINITY; }
 __device__ __forceinline__ __nv_bfloat16 lowest(__nv_bfloat16) { return __ushort_as_bfloat16(0xFF80); }
 
+__device__ __forceinline__ void unpack(const uint4& r, float* v, float)
+{
+    v[0] = __uint_as_float(r.x);
+    v[1] = __uint_as_float(r.y);
+    v[2] = __uint_as_float(r.z);
+    v[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void unpack(const uint4& r, float* v, __nv_bfloat16)
+{
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+// A CTA's part of a row: 16-byte pieces of memory, piece j with the values VEC j - shift
+// .. + VEC - 1, in chunks [c0, c1) of kPieces pieces a thread.
+template <typename T>
+struct Part {
+    static constexpr int VEC = 16 / sizeof(T);
+    const T* x;
+    int V, shift;
+    uint32_t c0, c1;
+
+    __device__ __forceinline__ Part(const LogprobParams& p, int64_t row, uint32_t rank, uint32_t ctas)
+    {
+        x = static_cast<const T*>(p.x) + row * p.stride;
+        V = p.V;
+        shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+        const uint32_t pieces = (static_cast<uint32_t>(V) + shift + VEC - 1) / VEC;
+        const uint32_t chunks = (pieces + kThreads * kPieces - 1) / (kThreads * kPieces);
+        c0 = chunks * rank / ctas;
+        c1 = chunks * (rank + 1) / ctas;
+    }
+    // the first value of this thread's first piece of a chunk; the next pieces are
+    // kThreads VEC values further
+    __device__ __forceinline__ int first_of(uint32_t c) const
+    {
+        return static_cast<int>(c * (kThreads * kPieces * VEC) + threadIdx.x * VEC) - shift;
+    }
+    // This thread's pieces of the chunk whose first value for it is i0, on their way to
+    // shared memory at dst, dst + 16 kThreads, ..
+    __device__ __forceinline__ void fetch(int i0, uint32_t dst) const
+    {
+        constexpr int kSpan = (kPieces - 1) * kThreads * VEC + VEC;
+        if (V >= kSpan && static_cast<uint32_t>(i0) <= static_cast<uint32_t>(V - kSpan)) {
+            const T* const at = x + i0;
+#pragma unroll
+            for (int v = 0; v < kPieces; ++v)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + v * (16 * kThreads)),
+                             "l"(at + v * (kThreads * VEC))
+                             : "memory");
+            return;
+        }
+#pragma unroll 1
+        for (int v = 0; v < kPieces; ++v) {
+            const int i = i0 + v * (kThreads * VEC);
+            T* const at = static_cast<T*>(__cvta_shared_to_generic(dst + v * (16 * kThreads)));
+            if (i >= 0 && i + VEC <= V) {
+                cp_async16(at, x + i, 16);
+            } else {
+                for (int e = 0; e < VEC; ++e) at[e] = i + e >= 0 && i + e < V ? x[i + e] : lowest(T());
+            }
+        }
+    }
+};
+
+// The candidates of a part whose list ran over: the first k of those behind are kept,
+// 2048 values at a time. Returns the list's length.
+template <typename T>
+__device__ __noinline__ int careful(TopSmem& t, Smem& sm, const T* x, int begin, int end, int k)
+{
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (tid == 0) sm.count = 0;
+    __syncthreads();
+    float bound = -INFINITY;
+    for (int at = begin; at < end; at += 4 * kThreads) {
+        for (int i = at + tid; i < min(at + 4 * kThreads, end); i += kThreads) {
+            const float v = as_float(x[i]);
+            // (what equals the bound comes behind those that are there)
+            if (v > bound) t.list[atomicAdd(&sm.count, 1)] = key_of(v, static_cast<uint32_t>(i));
+        }
+        __syncthreads();
+        const int n = sm.count;
+        if (n >= kShort) {
+            const int kept = first_of_list(t, sm, n, k);
+            if (tid < kept) t.list[tid] = t.best[tid];
+            if (tid == 0) sm.count = kept;
+            if (kept == k) bound = unordered(static_cast<uint32_t>(t.best[k - 1] >> 32));
+        }
+        __syncthreads();
+    }
+    return sm.count;
+}
+
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const LogprobParams p)
 {
-    constexpr int VEC = Raw<T>::kVec, NV = kPer / VEC;
+    constexpr int VEC = Part<T>::VEC;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    TopSmem& top = *reinterpret_cast<TopSmem*>(smem_raw);
+    uint4* const ring = reinterpret_cast<uint4*>(smem_raw) + threadIdx.x;
+    TopSmem& top = *reinterpret_cast<TopSmem*>(smem_raw + kStages * kSlot);
     __shared__ Smem sm;
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ctas = cluster.num_blocks(), rank = cluster.block_rank();
-    const int64_t row = blockIdx.x / ctas;
-    const T* const x = static_cast<const T*>(p.x) + row * p.stride;
-    // 16-byte pieces of memory: piece j has values VEC j - shift .. + VEC - 1
-    const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
-    const uint32_t pieces = (static_cast<uint32_t>(p.V) + shift + VEC - 1) / VEC;
-    // this CTA's pieces: whole chunks but for the last CTA's
-    const uint32_t chunks = (pieces + kThreads * NV - 1) / (kThreads * NV);
-    const uint32_t c0 = static_cast<uint64_t>(chunks) * rank / ctas, c1 = static_cast<uint64_t>(chunks) * (rank + 1) / ctas;
-    const int64_t tok = load_slot(p.tok, p.tok_type, row);
-    const bool given = tok >= 0 && tok < p.V;
-    const float xt = given ? as_float(x[tok]) : INFINITY;
+    const int64_t step = gridDim.x / ctas;
+    if (ctas > 1) cluster.barrier_arrive();
+    if (TOP && tid == 0) sm.count = sm.threads = 0;       // (ahead of the first row's barriers)
 
-    auto first_of = [&](uint32_t c, int v) { return static_cast<int64_t>(c * NV + v) * (kThreads * VEC) + tid * VEC - shift; };
-    Raw<T> next[NV];
-    auto load = [&](uint32_t c) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int64_t i = first_of(c, v);
-            if (i >= 0 && i + VEC <= p.V) {
-                next[v].load(x + i);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) next[v].put(e, i + e >= 0 && i + e < p.V ? x[i + e] : lowest(T()));
-            }
+    // ---- the next chunks on their way, over the row's end ----
+    int64_t a_row = blockIdx.x / ctas;
+    Part<T> a_part(p, a_row, rank, ctas);
+    uint32_t a_left = a_part.c1 - a_part.c0;
+    int a_i0 = a_part.first_of(a_part.c0);
+    const uint32_t ring_at = smem_u32(ring);
+    uint32_t a_slot = 0, slot = 0;
+    auto fetch = [&] {
+        while (a_left == 0 && a_row < p.R) {
+            a_row += step;
+            if (a_row >= p.R) break;
+            a_part = Part<T>(p, a_row, rank, ctas);
+            a_left = a_part.c1 - a_part.c0;
+            a_i0 = a_part.first_of(a_part.c0);
         }
+        if (a_left > 0) {
+            a_part.fetch(a_i0, ring_at + a_slot);
+            a_i0 += kThreads * kPieces * VEC;
+            --a_left;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        a_slot = a_slot + kSlot == kStages * kSlot ? 0 : a_slot + kSlot;
     };
-    if (TOP && tid == 0) sm.count = 0;
-    Stats st = {-INFINITY, 0.0f, 0.0f, 0};
-    float bound = -INFINITY;
-    bool full = false;                       // k values that reach the bound are there
-    int n = 0;                               // candidates
-    if (c0 < c1) load(c0);
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) fetch();
+    auto token = [&](int64_t row) { return row < p.R ? load_slot(p.tok, p.tok_type, row) : -1; };
+    auto logit = [&](int64_t row, int64_t t) {
+        return t >= 0 && t < p.V ? as_float(static_cast<const T*>(p.x)[row * p.stride + t]) : INFINITY;
+    };
+    int64_t tok = token(blockIdx.x / ctas);
+    float xt = logit(blockIdx.x / ctas, tok);
+    int parity = 0;
 #pragma unroll 1
-    for (uint32_t c = c0; c < c1; ++c) {
-        float v[kPer];
+    for (int64_t row = blockIdx.x / ctas; row < p.R; row += step, parity ^= 1) {
+        const Part<T> part(p, row, rank, ctas);
+        const int64_t tok_next = token(row + step);
+        Stats st = {-INFINITY, 0.0f, 0.0f, 0};            // (s in units of log2)
+        float c_now = 0.0f, off = 0.0f;                  // c, and c - m log2 e
+#pragma unroll 1
+        for (uint32_t c = part.c0; c < part.c1; ++c) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            const uint4* const in = ring + slot / 16;
+#pragma unroll 1
+            for (int at = 0; at < kPieces; at += kPer / VEC) {
+                float w[kPer];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) v[e] = next[e / VEC].get(e % VEC);
-        if (c + 1 < c1) load(c + 1);
-        float mx = v[0];
+                for (int i = 0; i < kPer / VEC; ++i) unpack(in[(at + i) * kThreads], w + i * VEC, T());
+                float mx = w[0];
 #pragma unroll
-        for (int e = 1; e < kPer; ++e) mx = max_nan(mx, v[e]);
-        // ---- the running statistics ----
-        const float m = max_nan(st.m, mx);
-        if (m != st.m) {
-            if (st.m != -INFINITY) {
-                const float d = st.m - m, f = ex2(d * kLog2e);
-                st.s = f == 0.0f ? 0.0f : (st.s + d * st.l) * f;
-                st.l *= f;
+                for (int e = 1; e < kPer; e += 2) mx = max3(mx, w[e], w[e + 1 < kPer ? e + 1 : e]);
+                // the token's rank (of a probable one few threads have values above it)
+                if (mx > xt) {
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) st.above += w[e] > xt;
+                }
+                const float m = fmaxf(st.m, mx);
+                if (m != st.m) {
+                    if (st.m != -INFINITY) {
+                        const float d = (st.m - m) * kLog2e, f = ex2(d);
+                        st.s = f == 0.0f ? 0.0f : (st.s + d * st.l) * f;
+                        st.l *= f;
+                    }
+                    st.m = m;
+                    c_now = m * kLog2e;
+                    off = fmaf(-m, kLog2e, c_now);
+                }
+                float sum = 0.0f, dot = NAN;
+                if (fabsf(m) <= 1024.0f) {
+                    const float2 neg = make_float2(-c_now, -c_now), log2e = make_float2(kLog2e, kLog2e);
+                    float2 l = make_float2(0.f, 0.f), s = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int e = 0; e < kPer; e += 2) {
+                        const float2 y = __ffma2_rn(make_float2(w[e], w[e + 1]), log2e, neg);
+                        const float2 x = make_float2(ex2(y.x), ex2(y.y));
+                        l = __fadd2_rn(l, x);
+                        s = __ffma2_rn(y, x, s);
+                    }
+                    sum = l.x + l.y;
+                    dot = s.x + s.y;
+                    dot = fmaf(off, fmaf(dot, kLn2, sum), dot);
+                    sum = fmaf(sum, off * kLn2, sum);
+                }
+                if (dot != dot) {
+                    // past the range, or -inf among them, whose product with its weight
+                    // of 0 is NaN. (One among the values makes both sums NaN.)
+                    const float ref = m == -INFINITY ? 0.0f : m;
+                    sum = dot = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) {
+                        const float y = (w[e] - ref) * kLog2e, x = ex2(y);
+                        sum += x;
+                        dot += x == 0.0f ? 0.0f : y * x;
+                    }
+                }
+                st.l += sum;
+                st.s += dot;
             }
-            st.m = m;
+            slot = slot + kSlot == kStages * kSlot ? 0 : slot + kSlot;
+            fetch();                         // (into the slot just read: this thread's own)
         }
-        const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            // (a value of -inf, whose product with its weight of 0 would be NaN: -2^100)
-            const float d = max_nan(v[e] - ref, -0x1p100f);
-            const float w = ex2(d * kLog2e);
-            st.l += w;
-            st.s += d * w;
-            st.above += v[e] > xt;
-        }
-        if (!TOP) continue;
-        // ---- candidates ----
-        const bool was_full = full;
-        if (!full) {
-            float g = mx;
+        st.s *= kLn2;
+        const float xt_next = logit(row + step, tok_next);
+        // ---- this CTA's statistics and alternatives, to the cluster's first ----
+        const float mine = st.m;
+        st = warp_join(st);
+        if (lane == 0) sm.part[parity][warp] = st;
+        if (TOP) {
+            float g = mine;
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
             if ((lane & 15) == 0) sm.group[tid >> 4] = g;
-            __syncthreads();
-            g = sm.group[lane];
-            int higher = 0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float o = __shfl_sync(0xffffffffu, g, i);
-                higher += o > g || (o == g && i < lane);
-            }
-            bound = __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, higher == p.k - 1)) - 1);
-            full = bound > -INFINITY;
-        }
-        if (was_full ? mx > bound : mx >= bound) {
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                const int64_t i = first_of(c, e / VEC) + e % VEC;
-                if ((was_full ? v[e] > bound : v[e] >= bound) && i >= 0 && i < p.V)
-                    top.cand[atomicAdd(&sm.count, 1)] = key_of(v[e], static_cast<uint32_t>(i));
-            }
         }
         __syncthreads();
-        n = sm.count;
-        if (n >= kMany) {
-            const int kept = rank_candidates(top, n, p.k);
-            // (the kept ones are candidates again)
-            if (tid < kept) top.cand[tid] = top.best[tid];
-            if (tid == 0) sm.count = kept;
-            if (kept == p.k) {
-                bound = unordered(static_cast<uint32_t>(top.best[p.k - 1] >> 32));
-                full = true;
-            }
-            n = kept;
+        if (warp == 0) {
+            st = sm.part[parity][lane & (kWarps - 1)];
+            if (lane >= kWarps) st = {-INFINITY, 0.0f, 0.0f, 0};
+            st = warp_join(st);
         }
-        __syncthreads();
-    }
-    // ---- this CTA's statistics and alternatives ----
-    st = warp_join(st);
-    if (lane == 0) sm.part[warp] = st;
-    __syncthreads();
-    if (warp == 0) {
-        st = sm.part[lane & (kWarps - 1)];
-        if (lane >= kWarps) st = {-INFINITY, 0.0f, 0.0f, 0};
-        st = warp_join(st);
-        if (lane == 0) sm.all = st;
-    }
-    if (TOP) {
-        const int kept = rank_candidates(top, n, p.k);
-        if (tid == 0) sm.count = kept;
-    }
-    if (ctas > 1) cluster.sync();
-    else __syncthreads();
-    if (rank == 0) {
-        if (ctas > 1) {
+        int kept = 0;
+        if (TOP) {
+            // (a group of -inf counts as one of the least finite value)
             if (warp == 0) {
-                st = {-INFINITY, 0.0f, 0.0f, 0};
-                if (lane < ctas) st = *cluster.map_shared_rank(&sm.all, lane);
-                st = warp_join(st);
-                if (lane == 0) sm.part[0] = st;
+                const uint32_t low = kth_of_lanes(ordered(fmaxf(sm.group[lane], kLeast)), p.k);
+                if (lane == 0) sm.bound = unordered(max(low, ordered(kLeast)));
             }
-            if (TOP) {
-                // lists one behind another; empty places are zeros, the lowest key
-                for (int i = tid; i < static_cast<int>(ctas) * p.k; i += kThreads) {
-                    const int r = i / p.k, j = i - r * p.k;
-                    const TopSmem* far = cluster.map_shared_rank(&top, r);
-                    top.cand[i] = j < *cluster.map_shared_rank(&sm.count, r) ? far->best[j] : 0ull;
+            __syncthreads();
+            const float bound = sm.bound;
+            if (mine >= bound) sm.who[atomicAdd(&sm.threads, 1)] = static_cast<uint16_t>(tid);
+            __syncthreads();
+            const int pieces = static_cast<int>(part.c1 - part.c0) * kPieces, all = sm.threads * pieces;
+#pragma unroll 2
+            for (int j = tid; j < all; j += kThreads) {
+                const int w = j / pieces;
+                const int i = part.first_of(part.c0) + (sm.who[w] - tid) * VEC + (j - w * pieces) * (kThreads * VEC);
+                float v[VEC];
+                if (i >= 0 && i + VEC <= p.V) {
+                    unpack(*reinterpret_cast<const uint4*>(part.x + i), v, T());
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) v[e] = i + e >= 0 && i + e < p.V ? as_float(part.x[i + e]) : -INFINITY;
+                }
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    if (v[e] >= bound) {
+                        const int at = atomicAdd(&sm.count, 1);
+                        if (at < kList) top.list[at] = key_of(v[e], static_cast<uint32_t>(i + e));
+                    }
                 }
             }
-        } else if (tid == 0) {
-            sm.part[0] = sm.all;
+            __syncthreads();
+            int n = sm.count;
+            if (n > kList)
+                n = careful(top, sm, part.x, max(part.first_of(part.c0) - tid * VEC, 0),
+                            min(part.first_of(part.c1) - tid * VEC, p.V), p.k);
+            kept = first_of_list(top, sm, n, p.k);
+            if (tid == 0) sm.count = sm.threads = 0;
         }
-        __syncthreads();
-        if (TOP && ctas > 1) rank_candidates(top, ctas * p.k, p.k);
-        const Stats all = sm.part[0];
-        // nothing but -inf: no distribution, the sum is 0. A NaN or +inf: the sum is NaN.
-        const float logl = logf(all.l);
-        const bool bad = !(all.l >= 0.0f);
-        auto logp = [&](float v) { return v == -INFINITY && !bad ? -INFINITY : v - all.m - logl; };
-        if (tid == 0) {
-            p.lp[row] = given ? logp(xt) : NAN;
-            if (p.ranks) p.ranks[row] = given && !bad ? all.above : -1;
-            if (p.entropy) p.entropy[row] = all.l == 0.0f ? 0.0f : logl - all.s / all.l;
+        if (ctas > 1) {
+            // (the first has begun, and is done with the row before)
+            cluster.barrier_wait();
+            if (tid == 0) *cluster.map_shared_rank(&sm.all[rank], 0) = st;
+            // (empty places: keys below all others, no two equal)
+            if (TOP && tid < p.k) {
+                const uint32_t i = rank * p.k + tid;
+                cluster.map_shared_rank(&top, 0)->far[i] = tid < kept ? top.best[tid] : i;
+            }
+            cluster.barrier_arrive();
+            if (rank == 0) {
+                cluster.barrier_wait();
+                if (warp == 0) {
+                    st = {-INFINITY, 0.0f, 0.0f, 0};
+                    if (lane < ctas) st = sm.all[lane];
+                    st = warp_join(st);
+                }
+                if (TOP) {
+                    put_in_order(top.best, top.far, static_cast<int>(ctas) * p.k, p.k);
+                }
+                cluster.barrier_arrive();
+            } else {
+                cluster.barrier_wait();
+                cluster.barrier_arrive();
+            }
+        } else if (TOP) {
+            if (tid >= kept && tid < p.k) top.best[tid] = 0;
         }
-        if (TOP && tid < p.k) {
-            const uint64_t key = top.best[tid];
-            p.top_ids[row * p.k + tid] = bad ? -1 : static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));
-            p.top_lp[row * p.k + tid] = bad ? NAN : logp(unordered(static_cast<uint32_t>(key >> 32)));
+        if (rank == 0 && warp == 0) {
+            // nothing but -inf: no distribution, the sum is 0. A NaN or +inf: the sum is NaN.
+            __syncwarp();
+            const bool given = tok >= 0 && tok < p.V;
+            const float logl = logf(st.l);
+            const bool bad = !(st.l >= 0.0f);
+            auto logp = [&](float x) { return x == -INFINITY && !bad ? -INFINITY : x - st.m - logl; };
+            if (lane == 0) {
+                p.lp[row] = given ? logp(xt) : NAN;
+                if (p.ranks) p.ranks[row] = given && !bad ? st.above : -1;
+                if (p.entropy) p.entropy[row] = st.l == 0.0f ? 0.0f : logl - st.s / st.l;
+            }
+            if (TOP) {
+                const uint64_t key = lane < p.k ? top.best[lane] : 0ull;
+                const int found = __popc(__ballot_sync(0xffffffffu, (key >> 32) != 0));
+                int id = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key));
+                float value = unordered(static_cast<uint32_t>(key >> 32));
+                if (found < p.k) {
+                    // fewer finite values than alternatives: -inf ones follow, of which at
+                    // least k - found lie among the first 64 values (or among all)
+                    const bool a = lane < p.V && as_float(part.x[lane]) == -INFINITY;
+                    const bool b = lane + 32 < p.V && as_float(part.x[lane + 32]) == -INFINITY;
+                    const uint32_t lo = __ballot_sync(0xffffffffu, a), hi = __ballot_sync(0xffffffffu, b);
+                    if (lane >= found) {
+                        uint64_t left = static_cast<uint64_t>(hi) << 32 | lo;
+                        for (int i = found; i < lane; ++i) left &= left - 1;
+                        id = __ffsll(static_cast<long long>(left)) - 1;
+                        value = -INFINITY;
+                    }
+                }
+                if (lane < p.k) {
+                    p.top_ids[row * p.k + lane] = bad ? -1 : id;
+                    p.top_lp[row * p.k + lane] = bad ? NAN : logp(value);
+                }
+            }
         }
+        tok = tok_next;
+        xt = xt_next;
     }
-    // (the others' shared memory is read until here)
-    if (ctas > 1) cluster.sync();
+    if (ctas > 1) cluster.barrier_wait();
 }
 
 template <typename T, bool TOP>
-cudaError_t launch(const LogprobParams& p, int64_t R, int ctas, cudaStream_t st)
+cudaError_t launch(const LogprobParams& p, int64_t clusters, int ctas, cudaStream_t st)
 {
-    const size_t smem = TOP ? sizeof(TopSmem) : 0;
-    if (TOP) {
-        const cudaError_t e = cudaFuncSetAttribute(token_logprobs_kernel<T, TOP>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
+    const size_t smem = kStages * kSlot + (TOP ? sizeof(TopSmem) : 0);
+    const cudaError_t e = cudaFuncSetAttribute(token_logprobs_kernel<T, TOP>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(static_cast<unsigned>(R * ctas));
+    lc.gridDim = dim3(static_cast<unsigned>(clusters * ctas));
     lc.blockDim = dim3(kThreads);
     lc.dynamicSmemBytes = smem;
     lc.stream = st;
@@ -410,7 +595,7 @@ extern "C" pa_status pa_token_logprobs(const void* logits, int dtype, int64_t ro
     PA_REQUIRE(top == 0 || num_rows == 0 || (top_ids && top_logprobs), PA_ERR_NULLPTR,
                "%s: NULL top_ids or top_logprobs", name);
     PA_REQUIRE(num_rows <= 1 || row_stride >= V, PA_ERR_INVALID, "%s: rows overlap (row_stride below V)", name);
-    PA_REQUIRE(V <= 0x7FFFFFFF - 2 * kChunk && num_rows <= 0x7FFFFFFF / kMaxCluster, PA_ERR_UNSUPPORTED,
+    PA_REQUIRE(V <= 0x7FFFFFFF - (1 << 16) && num_rows <= 0x7FFFFFFF, PA_ERR_UNSUPPORTED,
                "%s: too many rows or tokens", name);
     PA_REQUIRE(aligned(logits, dtype == PA_DTYPE_F32 ? 4 : 2) && aligned(tokens, token_type == PA_INDEX_I64 ? 8 : 4) &&
                    aligned(logprobs, 4) && aligned(ranks, 4) && aligned(entropy, 4) && aligned(top_ids, 4) &&
@@ -424,6 +609,7 @@ extern "C" pa_status pa_token_logprobs(const void* logits, int dtype, int64_t ro
     p.stride = num_rows > 1 ? row_stride : 0;
     p.tok = tokens;
     p.tok_type = token_type;
+    p.R = num_rows;
     p.V = V;
     p.k = top;
     p.lp = logprobs;
@@ -431,13 +617,15 @@ extern "C" pa_status pa_token_logprobs(const void* logits, int dtype, int64_t ro
     p.entropy = entropy;
     p.top_ids = top_ids;
     p.top_lp = top_logprobs;
-    // As many CTAs a row as fill the GPU, two an SM, and have a chunk each.
+    // As many CTAs a row as there are room for, two an SM, and as have a chunk each.
+    const int chunk = kThreads * kPieces * 16 / (dtype == PA_DTYPE_F32 ? 4 : 2);
     int ctas = kMaxCluster;
-    while (ctas > 1 && (num_rows * (ctas / 2) >= 2 * sms || V <= kChunk * (ctas / 2))) ctas /= 2;
+    while (ctas > 1 && (num_rows * ctas > 2 * sms || V <= chunk * (ctas / 2))) ctas /= 2;
+    const int64_t clusters = std::min<int64_t>(num_rows, 2 * sms / ctas);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (dtype == PA_DTYPE_F32) e = top ? launch<float, true>(p, num_rows, ctas, st) : launch<float, false>(p, num_rows, ctas, st);
-    else e = top ? launch<__nv_bfloat16, true>(p, num_rows, ctas, st) : launch<__nv_bfloat16, false>(p, num_rows, ctas, st);
+    if (dtype == PA_DTYPE_F32) e = top ? launch<float, true>(p, clusters, ctas, st) : launch<float, false>(p, clusters, ctas, st);
+    else e = top ? launch<__nv_bfloat16, true>(p, clusters, ctas, st) : launch<__nv_bfloat16, false>(p, clusters, ctas, st);
     PA_REQUIRE(e == cudaSuccess, PA_ERR_CUDA, "%s: launch: %s", name, cudaGetErrorString(e));
     return check_launch(name);
 }
