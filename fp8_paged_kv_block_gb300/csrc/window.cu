@@ -27,11 +27,20 @@
 //   warps 0-7        softmax (thread = row = tensor memory lane)
 //   warp 8           K and V blocks by TMA, key scales by cp.async
 //   warp 9           issues S and P V
-//   warps 10, 11     Q rows and scales of the next item
+//   warp 10          Q rows and scales of the next item
+//   warp 11          the run's items, one after another, for all others
 //   warps 12-15      V codes to FP16 in shared memory, zeros where no row sees the key
 // The issuing warp issues S of step j + 2 behind P V of step j, so that the tensor core
 // itself keeps them apart where they share columns, and an S that is complete says that
 // the warpgroup's last P V is.
+//
+// An item of at most 64 or 32 rows (a decoding request's: one token x the group) stands in
+// the tile twice or four times, and each copy's warps take the block's keys by halves or
+// quarters: with one copy three of a warpgroup's four warps would have no rows. The copies
+// have an O, an m and an l of their own and are joined with the warpgroups' at the end.
+//
+// Loops are rolled (32 scores at a time under a running maximum) and what is rare lies
+// behind branches that are marked so: the parts run at once out of one instruction cache.
 //
 // The items in (sequence, kv head, row) order are dealt to the CTAs in runs of equal
 // weight: a step counts 1, an item kItemCost besides. Items that a run's end cuts leave
@@ -56,16 +65,16 @@ constexpr int kTile = kBS * kD;              // bytes of a block of codes
 // K blocks, V blocks as codes and as FP16. The key scales' ring needs no barrier that
 // says a slot is free: block i + 8 is requested once K block i + 5 is free, i.e. its S
 // complete; that was issued behind block i + 3's P V, so that block i's softmax is done.
-constexpr int kKStages = 3, kVStages = 3, kHStages = 2, kSStages = 8;
-constexpr int kProdWarp = 8, kMmaWarp = 9, kQWarp = 10, kConvWarp = 12, kConvWarps = 4;
+constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kSStages = 8;
+constexpr int kProdWarp = 8, kMmaWarp = 9, kQWarp = 10, kSegWarp = 11, kConvWarp = 12, kConvWarps = 4;
 constexpr int kThreads = (kConvWarp + kConvWarps) * 32;
-// 256 x 200 + 256 x 56 = 512 x 128 registers
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;
+constexpr int kChunk = 32;                   // scores a softmax thread holds at once
 constexpr uint32_t kTmemCols = 512, kSCol = 2 * kD;   // O of either warpgroup, then S (and P)
 constexpr float kRaise = 8.0f;               // log2 units
 constexpr float kShift = 7.0f;
 constexpr int kItemCost = 8;                 // what an item costs besides its steps, in steps
-constexpr int kMinRun = 12;                  // the shortest run (2 at least: describe_cut)
+constexpr int kMinRun = 2;                   // the shortest run (2 at least: describe_cut)
+constexpr int kSegs = 4;                     // items ahead of the slowest part
 // Entries of the schedule in shared memory: an item each while the batch's number no
 // more than half of it, else 2, 4, .. one behind another.
 constexpr int kMaxEntries = 2 * kMaxB;
@@ -94,6 +103,9 @@ struct WindowParams {
     float* part;
     int part_rows;                           // rows of a partial item
     int B, T, max_tokens, NQ, NKV, G;
+    uint32_t g_mul;                          // 2^22 / G + 1: n / G = n g_mul >> 22 for n < 2^14
+    uint64_t g_inv;                          // 2^64 / G + 1 (G > 1)
+    int one_item;                            // a sequence makes one item at most
     int64_t num_blocks;
     int max_blocks, layout, ctas;
     int window, sinks;
@@ -101,22 +113,38 @@ struct WindowParams {
     float scale_log2;
 };
 
+struct Item {
+    int row0, rows;
+    int first, last;                         // positions of its first and last row's token
+    int lo, sink_blocks, blocks;             // first block of the windows, blocks of the sinks before it, in all
+};
+
+struct Seg {
+    Item x;
+    int b, h;
+    int t0, t1;                              // its blocks that this run has
+    int tok;                                 // the row of the sequence's first token
+    int first_of_run;
+};
+
 struct WindowSmem {
     alignas(1024) uint8_t k[kKStages][kTile];
     alignas(1024) uint8_t v[kVStages][kTile];
     alignas(1024) uint8_t vh[kHStages][2][kTile];   // FP16, channels 0-63 and 64-127
-    alignas(1024) uint8_t q[2][kTile];              // of either tile
+    alignas(1024) uint8_t q[2 * kTile];             // of either tile
     alignas(16) float ks[kSStages][kBS];
     alignas(16) float qs[2][kItemRows];             // by item parity, as vs
     alignas(16) float vs[2][kD];
-    float ml[2][2][kTileRows];
+    float m[2 * kTileRows], l[2 * kTileRows];       // of the warpgroups' threads
+    float2 join[8][256];                     // 16 or 32 channels of their rows
     // per sequence: position and row of its first token that sees a key, query rows a
     // kv head; entries before it
     int pos[kMaxB], tok[kMaxB], rows[kMaxB], first[kMaxB + 1];
     uint32_t cum[kMaxEntries + 1];           // weights before each entry, of one kv head
     uint64_t k_full[kSStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
     uint64_t h_full[kHStages], h_empty[kHStages];
-    uint64_t s_full[2], p_full[2], o_full[2], q_full, q_empty, drain;
+    uint64_t s_full[2], p_full[2], o_full[2], q_full, q_empty, joined, drain, seg_full[kSegs], seg_empty[kSegs];
+    Seg segs[kSegs];                         // the run's items; t1 = 0: the end
     uint32_t scan[kThreads / 32];
     uint32_t tmem;
     int abort;
@@ -124,35 +152,41 @@ struct WindowSmem {
 constexpr size_t kSmemBytes = offsetof(WindowSmem, abort) + sizeof(int) + 1024;   // (aligned by hand)
 static_assert(kSmemBytes <= 232448, "window attention shared memory over budget");
 
+// ---- waits -----------------------------------------------------------------------
+// wait_for with all but the first try out of line.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort)
+{
+    return wait_for(bar, parity, err, code, abort);
+}
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort)
+{
+    return __builtin_expect(mbar_try_wait(bar, parity), 1) || wait_on(bar, parity, err, code, abort);
+}
+
 // ---- the schedule -----------------------------------------------------------------
-struct Item {
-    int row0, rows;
-    int first, last;                         // positions of its first and last row's token
-    int lo, sink_blocks, blocks;             // first block of the windows, blocks of the sinks before it, in all
-};
+// n / G
+__device__ __forceinline__ int tokens_of(const WindowParams& p, int n)
+{
+    return p.G == 1 ? n : static_cast<int>(__umul64hi(static_cast<uint64_t>(n), p.g_inv));
+}
 
 __device__ __forceinline__ Item item_of(const WindowParams& p, int pos, int rows, int i)
 {
     Item x;
     x.row0 = i * kItemRows;
     x.rows = min(rows - x.row0, kItemRows);
-    x.first = pos + x.row0 / p.G;
-    x.last = pos + (x.row0 + x.rows - 1) / p.G;
+    x.first = pos + tokens_of(p, x.row0);
+    x.last = pos + tokens_of(p, x.row0 + x.rows - 1);
     x.lo = max(x.first - p.window + 1, 0) / kBS;
     x.sink_blocks = min((p.sinks + kBS - 1) / kBS, x.lo);
     x.blocks = x.sink_blocks + x.last / kBS - x.lo + 1;
     return x;
 }
+// copies of an item's rows in the tile
+__device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 4 : (rows <= 64 ? 2 : 1); }
 __device__ __forceinline__ int steps_a_block(int rows) { return rows > kTileRows ? 2 : 1; }
 __device__ __forceinline__ uint32_t weight_of(const Item& x) { return x.blocks * steps_a_block(x.rows) + kItemCost; }
 __device__ __forceinline__ int items_of(int rows) { return (rows + kItemRows - 1) / kItemRows; }
-
-struct Seg {
-    Item x;
-    int b, h;
-    int t0, t1;                              // its blocks that this run has
-    bool first_of_run;
-};
 
 struct Run {
     uint32_t pos, hi;                        // of the weights of all heads
@@ -186,6 +220,7 @@ __device__ __forceinline__ bool next_seg(const WindowSmem& sm, const WindowParam
         s.x = item_of(p, sm.pos[r.b], sm.rows[r.b], r.i);
         s.b = r.b;
         s.h = r.h;
+        s.tok = sm.tok[r.b];
         const uint32_t end = r.base + weight_of(s.x);
         s.t0 = blocks_before(s.x, r.pos - r.base);
         s.t1 = r.hi >= end ? s.x.blocks : blocks_before(s.x, r.hi - r.base);
@@ -292,30 +327,36 @@ __device__ uint32_t build_schedule(WindowSmem& sm, const WindowParams& p, int ti
         sm.rows[b] = s.live * p.G;
         items += items_of(s.live * p.G);
     }
-    uint32_t total;
-    block_scan(sm, items, total);
+    uint32_t total, entries;
     group = 1;
-    while (total > static_cast<uint32_t>(group) * (kMaxEntries - kMaxB)) group *= 2;
-    uint32_t mine = 0;
+    if (p.one_item) {
+        // a sequence an entry (of no weight if it has no rows)
+        entries = p.B;
+        for (int b = tid; b <= p.B; b += kThreads) sm.first[b] = b;
+    } else {
+        block_scan(sm, items, total);
+        while (total > static_cast<uint32_t>(group) * (kMaxEntries - kMaxB)) group *= 2;
+        uint32_t mine = 0;
 #pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        const int b = tid * kSeqs + j;
-        if (b < p.B) mine += (items_of(sm.rows[b]) + group - 1) / group;
-    }
-    uint32_t entries, at = block_scan(sm, mine, entries);
+        for (int j = 0; j < kSeqs; ++j) {
+            const int b = tid * kSeqs + j;
+            if (b < p.B) mine += (items_of(sm.rows[b]) + group - 1) / group;
+        }
+        uint32_t at = block_scan(sm, mine, entries);
 #pragma unroll
-    for (int j = 0; j < kSeqs; ++j) {
-        const int b = tid * kSeqs + j;
-        if (b >= p.B) break;
-        sm.first[b] = at;
-        at += (items_of(sm.rows[b]) + group - 1) / group;
+        for (int j = 0; j < kSeqs; ++j) {
+            const int b = tid * kSeqs + j;
+            if (b >= p.B) break;
+            sm.first[b] = at;
+            at += (items_of(sm.rows[b]) + group - 1) / group;
+        }
+        if (tid == 0) sm.first[p.B] = entries;
     }
-    if (tid == 0) sm.first[p.B] = entries;
     __syncthreads();
+    uint32_t mine = 0;
     // thread i takes entries per i, per i + 1, .. and sums up its own
     const int per = (static_cast<int>(entries) + kThreads - 1) / kThreads;
     const int e0 = min(tid * per, static_cast<int>(entries)), e1 = min(e0 + per, static_cast<int>(entries));
-    mine = 0;
     if (e0 < e1) {
         int lo = 0, up = p.B - 1;            // the last sequence with first <= e0
         while (lo < up) {
@@ -349,14 +390,52 @@ __device__ __forceinline__ float* part_of(const WindowParams& p, int cta, bool f
 }
 
 // ---- the warps' parts ------------------------------------------------------------------
-__device__ void producer(WindowSmem& sm, const WindowParams& p, const CUtensorMap* tk, const CUtensorMap* tv, Run run,
-                         int lane)
+// The items of the run, from one warp to all others, each of which goes through them
+// with a reader of its own.
+__device__ void scheduler(WindowSmem& sm, const WindowParams& p, Run run, int lane)
+{
+    bool more = true;
+    for (int i = 0; more; ++i) {
+        Seg s;
+        more = next_seg(sm, p, run, s);
+        await(&sm.seg_empty[i % kSegs], ((i / kSegs) & 1) ^ 1, p.err, 2048, &sm.abort);
+        if (!more) s.t1 = 0;
+        if (lane == 0) {
+            sm.segs[i % kSegs] = s;
+            mbar_arrive(&sm.seg_full[i % kSegs]);
+        }
+        __syncwarp();
+    }
+}
+constexpr int kSegReaders = 8 + 3 + kConvWarps;      // warps
+
+// (A lane reads a word and all have it from there: what the warp does stays one even where
+// a wait gave up and the entry is overwritten meanwhile.)
+struct SegReader {
+    int i = 0;
+    __device__ __forceinline__ bool next(WindowSmem& sm, const WindowParams& p, Seg& s, int lane)
+    {
+        constexpr int kWords = sizeof(Seg) / 4;
+        static_assert(kWords <= 32, "a word a lane");
+        await(&sm.seg_full[i % kSegs], (i / kSegs) & 1, p.err, 4096, &sm.abort);
+        const int mine = reinterpret_cast<const volatile int*>(&sm.segs[i % kSegs])[lane < kWords ? lane : 0];
+        int* const words = reinterpret_cast<int*>(&s);
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) words[k] = __shfl_sync(0xffffffffu, mine, k);
+        if (lane == 0) mbar_arrive(&sm.seg_empty[i % kSegs]);
+        ++i;
+        return s.t1 > 0;
+    }
+};
+
+__device__ void producer(WindowSmem& sm, const WindowParams& p, const CUtensorMap* tk, const CUtensorMap* tv, int lane)
 {
     const uint64_t pol = p.keep_l2 ? l2_keep_policy() : l2_evict_first_policy();
     Seg s;
     int kc = 0, vc = 0;                      // blocks requested so far
     bool stop = false;
-    while (!stop && next_seg(sm, p, run, s)) {
+    SegReader segs;
+    while (!stop && segs.next(sm, p, s, lane)) {
         const int* row = p.bt + static_cast<int64_t>(s.b) * p.max_blocks;
         int ids = 0;
         for (int t = s.t0; t < s.t1; ++t) {
@@ -369,7 +448,7 @@ __device__ void producer(WindowSmem& sm, const WindowParams& p, const CUtensorMa
             const int x = p.layout == PA_LAYOUT_BSND ? s.h * kD : 0;
             const int y = static_cast<int>(p.layout == PA_LAYOUT_BSND ? blk * kBS : (blk * p.NKV + s.h) * kBS);
             const int kslot = kc % kKStages, vslot = vc % kVStages, sslot = kc % kSStages;
-            if (!wait_for(&sm.k_empty[kslot], ((kc / kKStages) & 1) ^ 1, p.err, 1, &sm.abort)) stop = true;
+            if (!await(&sm.k_empty[kslot], ((kc / kKStages) & 1) ^ 1, p.err, 1, &sm.abort)) stop = true;
             if (__any_sync(0xffffffffu, stop)) {
                 stop = true;
                 break;
@@ -385,7 +464,7 @@ __device__ void producer(WindowSmem& sm, const WindowParams& p, const CUtensorMa
             }
             cp_async_arrive_noinc(&sm.k_full[sslot]);
             ++kc;
-            if (!wait_for(&sm.v_empty[vslot], ((vc / kVStages) & 1) ^ 1, p.err, 2, &sm.abort)) stop = true;
+            if (!await(&sm.v_empty[vslot], ((vc / kVStages) & 1) ^ 1, p.err, 2, &sm.abort)) stop = true;
             if (__any_sync(0xffffffffu, stop)) {
                 stop = true;
                 break;
@@ -408,7 +487,7 @@ __device__ void producer(WindowSmem& sm, const WindowParams& p, const CUtensorMa
 // V codes [key][channel] (128-byte swizzled rows) to FP16 in two chunks of 64 channels,
 // swizzled the same way; keys that no row of the item sees become zeros, so that no
 // stale code (a NaN among them) meets their P = 0.
-__device__ void converter(WindowSmem& sm, const WindowParams& p, Run run, int w, int lane)
+__device__ void converter(WindowSmem& sm, const WindowParams& p, int w, int lane)
 {
     // Lane l takes 16-byte unit u = l % 8 of eight rows whose numbers differ in the 8-row
     // group only, so that every address is a constant away from the first. Units 4-7 go
@@ -420,18 +499,19 @@ __device__ void converter(WindowSmem& sm, const WindowParams& p, Run run, int w,
     const int key0 = 64 * (w >> 1) + 4 * (w & 1) + ((lane >> 3) ^ (u >> 2));
     const uint32_t from = sw128(key0, u), to = sw128(key0, 2 * (u & 3)) + (u >> 2) * kTile,
                    to1 = sw128(key0, 2 * (u & 3) + 1) + (u >> 2) * kTile;
-    while (next_seg(sm, p, run, s)) {
+    SegReader segs;
+    while (segs.next(sm, p, s, lane)) {
         for (int t = s.t0; t < s.t1; ++t, ++c) {
             const int vslot = c % kVStages, hslot = c % kHStages;
-            wait_for(&sm.v_full[vslot], (c / kVStages) & 1, p.err, 4, &sm.abort);
+            await(&sm.v_full[vslot], (c / kVStages) & 1, p.err, 4, &sm.abort);
             const uint8_t* src = sm.v[vslot] + from;
             // keys [begin, end) and those below `sink` are seen
             const int k0 = block_at(s.x, t) * kBS, begin = s.x.first - p.window + 1 - k0, end = s.x.last + 1 - k0,
                       sink = p.sinks - k0;
             const bool whole = end >= kBS && (begin <= 0 || sink >= kBS);
-            wait_for(&sm.h_empty[hslot], ((c / kHStages) & 1) ^ 1, p.err, 8, &sm.abort);
+            await(&sm.h_empty[hslot], ((c / kHStages) & 1) ^ 1, p.err, 8, &sm.abort);
             uint8_t* dst = sm.vh[hslot][0];
-#pragma unroll
+#pragma unroll 1
             for (int i0 = 0; i0 < 8; i0 += 4) {
                 uint4 x[4];
 #pragma unroll
@@ -463,36 +543,6 @@ __device__ void converter(WindowSmem& sm, const WindowParams& p, Run run, int w,
     }
 }
 
-// A place in the run's sequence of steps.
-struct Cursor {
-    Run run;
-    Seg s;
-    int k, steps, per;                       // steps of the item behind and in all, steps a block
-    int item, block;                         // items and blocks before this item's
-    uint32_t step;                           // steps behind in all
-    bool more;
-
-    __device__ __forceinline__ void enter(const WindowSmem& sm, const WindowParams& p)
-    {
-        more = next_seg(sm, p, run, s);
-        if (!more) return;
-        per = steps_a_block(s.x.rows);
-        steps = (s.t1 - s.t0) * per;
-        k = 0;
-    }
-    __device__ __forceinline__ void advance(const WindowSmem& sm, const WindowParams& p)
-    {
-        ++step;
-        if (++k < steps) return;
-        ++item;
-        block += s.t1 - s.t0;
-        enter(sm, p);
-    }
-    __device__ __forceinline__ int block_now() const { return block + (per == 2 ? k >> 1 : k); }
-    __device__ __forceinline__ int tile() const { return per == 2 ? k & 1 : 0; }
-    __device__ __forceinline__ bool block_ends() const { return per == 1 || (k & 1); }
-};
-
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
 {
     uint32_t ok;
@@ -508,72 +558,97 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
 
 // The MMAs' warp: the whole warp polls, one elected thread issues. S of step j + 2 goes
 // behind P V of step j; which of the two goes next is whichever has its operands, so
-// that an item's last P V do not wait for the next one's Q.
-__device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, const Run& run, uint32_t tmem)
+// that an item's last P V do not wait for the next one's Q. (Polled: a warp is woken
+// sooner than out of a wait.)
+__device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, uint32_t tmem, int lane)
 {
     constexpr uint32_t kIdescS = idesc_e4m3(128, kBS, 0, 0);
     constexpr uint32_t kIdescO = idesc_f16(128, kD, 0, 1);   // P K-major in tensor memory, V MN-major
-    Cursor a, o;                             // S's, P V's
-    a.run = run;
-    a.item = a.block = 0;
-    a.step = 0;
-    a.enter(sm, p);
-    o = a;
-    uint32_t t0 = static_cast<uint32_t>(globaltimer_ns());
-    while (o.more) {
-        bool did = false;
-        if (a.more && a.step < o.step + 2) {
-            const int blk = a.block_now();
-            if (__all_sync(0xffffffffu, mbar_test(&sm.q_full, a.item & 1) &&
-                                            mbar_test(&sm.k_full[blk % kSStages], (blk / kSStages) & 1))) {
-                const int w = a.step & 1, kslot = blk % kKStages;
+    const uint64_t q0 = smem_desc(smem_u32(sm.q), 16, 1024, kSmem128BSwizzle);
+    const uint64_t k0 = smem_desc(smem_u32(sm.k[0]), 16, 1024, kSmem128BSwizzle);
+    const uint64_t v0 = smem_desc(smem_u32(sm.vh[0][0]), kTile, 1024, kSmem128BSwizzle);
+    SegReader segs;
+    // S's item: steps behind and in all, whether of two tiles; steps and whole blocks behind
+    // in all; P V's steps
+    uint32_t k = 0, steps = 0, a = 0, block = 0, o = 0;
+    bool pair = false, more = true;
+    // of the steps whose S is issued and whose P V is not: its block, 1: the item's first of
+    // the warpgroup, 2: its last, 4: the block's last
+    uint32_t block_of[2] = {0, 0}, flags[2] = {0, 0};
+    uint32_t idle = 0, t0 = 0;
+    auto enter = [&] {
+        Seg s;
+        more = segs.next(sm, p, s, lane);
+        pair = s.x.rows > kTileRows;
+        steps = (s.t1 - s.t0) * (pair ? 2 : 1);
+        k = 0;
+    };
+    enter();
+#pragma unroll 1
+    while (more || o < a) {
+        ++idle;
+        if (more && a < o + 2) {
+            const bool ready = (k > 0 || mbar_test(&sm.q_full, (segs.i - 1) & 1)) &&
+                               mbar_test(&sm.k_full[block % kSStages], (block / kSStages) & 1);
+            if (__all_sync(0xffffffffu, ready)) {
+                const uint32_t w = a & 1, kslot = block % kKStages;
+                const bool block_ends = !pair || (k & 1), ends = k + 1 == steps;
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t qd = smem_desc(smem_u32(sm.q[a.tile()]), 16, 1024, kSmem128BSwizzle);
-                    const uint64_t kd = smem_desc(smem_u32(sm.k[kslot]), 16, 1024, kSmem128BSwizzle);
+                    const uint64_t qd = q0 + (pair && (k & 1) ? kTile / 16 : 0), kd = k0 + kslot * (kTile / 16);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_e4m3(tmem + kSCol + kBS * w, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
+                    for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + kSCol + kBS * w, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
                     umma_commit(&sm.s_full[w]);
-                    if (a.block_ends()) umma_commit(&sm.k_empty[kslot]);
-                    if (a.k + 1 == a.steps) umma_commit(&sm.q_empty);
+                    if (block_ends) umma_commit(&sm.k_empty[kslot]);
+                    if (ends) umma_commit(&sm.q_empty);
                 }
                 __syncwarp();
-                a.advance(sm, p);
-                did = true;
+                const uint32_t f = (k < 2 ? 1 : 0) | (k + 2 >= steps ? 2 : 0) | (block_ends ? 4 : 0);
+                if (w) {
+                    block_of[1] = block;
+                    flags[1] = f;
+                } else {
+                    block_of[0] = block;
+                    flags[0] = f;
+                }
+                ++a;
+                ++k;
+                if (block_ends) ++block;
+                if (ends) enter();
+                idle = 0;
             }
         }
-        if (o.step < a.step) {
-            const int blk = o.block_now(), hslot = blk % kHStages, w = o.step & 1;
-            if (__all_sync(0xffffffffu, mbar_test(&sm.p_full[w], (o.step >> 1) & 1) &&
-                                            mbar_test(&sm.h_full[hslot], (blk / kHStages) & 1))) {
+        if (o < a) {
+            const uint32_t w = o & 1, blk = w ? block_of[1] : block_of[0], f = w ? flags[1] : flags[0], hslot = blk % kHStages;
+            const bool ready = mbar_test(&sm.p_full[w], (o >> 1) & 1) && mbar_test(&sm.h_full[hslot], (blk / kHStages) & 1);
+            if (__all_sync(0xffffffffu, ready)) {
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t vd = smem_desc(smem_u32(sm.vh[hslot][0]), kTile, 1024, kSmem128BSwizzle);
+                    const uint64_t vd = v0 + hslot * (2 * kTile / 16);
 #pragma unroll
                     for (int kk = 0; kk < kBS / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of V
                         umma_f16_ta(tmem + kD * w, tmem + kSCol + kBS * w + 8 * kk, vd + 128 * kk, kIdescO,
-                                    (o.k >= 2 || kk > 0) ? 1u : 0u);
-                    if (o.block_ends()) umma_commit(&sm.h_empty[hslot]);
-                    if (o.k + 2 >= o.steps) umma_commit(&sm.o_full[w]);
+                                    (!(f & 1) || kk > 0) ? 1u : 0u);
+                    if (f & 4) umma_commit(&sm.h_empty[hslot]);
+                    if (f & 2) umma_commit(&sm.o_full[w]);
                 }
                 __syncwarp();
-                o.advance(sm, p);
-                did = true;
+                ++o;
+                idle = 0;
             }
         }
-        const uint32_t now = static_cast<uint32_t>(globaltimer_ns());
-        if (did) {
-            t0 = now;
-        } else {
-            const volatile int* abort = &sm.abort;
-            const bool late = now - t0 > static_cast<uint32_t>(kWaitLimitNs);
-            if (__any_sync(0xffffffffu, late || *abort)) {
+        // the clock is read every 4096 fruitless polls
+        if (__builtin_expect(idle >= 4096, 0)) {
+            if ((idle & 4095) == 0) {
+                const uint32_t now = static_cast<uint32_t>(globaltimer_ns());
+                if (idle == 4096) t0 = now;
+                const volatile int* abort = &sm.abort;
+                const bool late = now - t0 > static_cast<uint32_t>(kWaitLimitNs);
                 if (late) {
                     sm.abort = 1;
                     atomicOr(p.err, 16);
                 }
-                break;
+                if (__any_sync(0xffffffffu, late || *abort)) break;
             }
         }
     }
@@ -585,31 +660,36 @@ __device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, const Run& run
     __syncwarp();
 }
 
-// Q rows (128-byte swizzled), q_scale and v_scale of each item, a tile a warp.
-__device__ void q_loader(WindowSmem& sm, const WindowParams& p, Run run, int w, int lane)
+// Q rows (128-byte swizzled), q_scale and v_scale of each item.
+__device__ void q_loader(WindowSmem& sm, const WindowParams& p, int lane)
 {
     Seg s;
-    for (int item = 0; next_seg(sm, p, run, s); ++item) {
+    SegReader segs;
+    for (int item = 0; segs.next(sm, p, s, lane); ++item) {
         const int buf = item & 1;
-        if (!__all_sync(0xffffffffu, wait_for(&sm.q_empty, (item & 1) ^ 1, p.err, 1024, &sm.abort))) break;
-        const int rows = min(max(s.x.rows - w * kTileRows, 0), kTileRows), row0 = s.x.row0 + w * kTileRows;
-        if (rows > 0) {
+        if (!__all_sync(0xffffffffu, await(&sm.q_empty, (item & 1) ^ 1, p.err, 1024, &sm.abort))) break;
+        // row r of the item: rest + r of the heads from token t on
+        const int period = kTileRows / copies_of(s.x.rows), t = tokens_of(p, s.x.row0), rest = s.x.row0 - t * p.G;
+        const int64_t first = static_cast<int64_t>(s.tok + t) * p.NQ + s.h * p.G;
+        auto row_of = [&](int of) {
+            const uint32_t n = rest + of, d = (n * p.g_mul) >> 22;
+            return static_cast<int>(d * p.NQ + n - d * p.G);
+        };
+        const uint8_t* const q = p.q + first * kD + 16 * (lane & 7);
+        // (a tile's rows, or the copies of fewer)
+        const int mask = s.x.rows > kTileRows ? ~0 : period - 1, tiles = s.x.rows > kTileRows ? 2 : 1;
 #pragma unroll 4
-            for (int i = 0; i < 32; ++i) {
-                const int r = 4 * i + (lane >> 3), u = lane & 7;
-                const bool in = r < rows;
-                cp_async16(sm.q[w] + sw128(r, u), p.q + q_row(p, sm.tok[s.b], s.h, row0 + (in ? r : 0)) * kD + 16 * u,
-                           in ? 16 : 0);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 32 * i + lane;
-                cp_async4(&sm.qs[buf][w * kTileRows + r],
-                          p.q_scale + q_row(p, sm.tok[s.b], s.h, row0 + (r < rows ? r : 0)), 4);
-            }
+        for (int i = 0; i < 32 * tiles; ++i) {
+            const int r = 4 * i + (lane >> 3), of = r & mask;
+            const bool in = of < s.x.rows;
+            cp_async16(sm.q + sw128(r, lane & 7), q + (in ? row_of(of) * kD : 0), in ? 16 : 0);
         }
-        if (w == 0)
-            cp_async16(&sm.vs[buf][4 * lane], p.v_scale + (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD + 4 * lane, 16);
+#pragma unroll 1
+        for (int r = lane; r < kTileRows * tiles; r += 32) {
+            const int of = r & mask;
+            cp_async4(&sm.qs[buf][r], p.q_scale + first + (of < s.x.rows ? row_of(of) : 0), 4);
+        }
+        cp_async16(&sm.vs[buf][4 * lane], p.v_scale + (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD + 4 * lane, 16);
         asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async_smem();
         __syncwarp();
@@ -617,28 +697,66 @@ __device__ void q_loader(WindowSmem& sm, const WindowParams& p, Run run, int w, 
     }
 }
 
-// bits 0 .. n - 1 of 64
-__device__ __forceinline__ uint64_t bits_below(int n) { return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1); }
+// bits 0 .. n - 1 of 32
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1); }
+
+// Columns [0, 16 n) of tensor memory times f: floats, or (halves) pairs of FP16.
+__device__ __noinline__ void scale_columns(uint32_t taddr, int n, float f, bool halves)
+{
+#pragma unroll 1
+    for (int c = 0; c < n; ++c) {
+        float o[16];
+        uint32_t y[16];
+        tmem_ld16(taddr + 16 * c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            y[i] = __float_as_uint(o[i] * f);
+            if (halves) {
+                const uint32_t u = __float_as_uint(o[i]);
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u));
+                y[i] = half2_bits(x.x * f, x.y * f);
+            }
+        }
+        tmem_st16(taddr + 16 * c, y);
+    }
+    tmem_wait_st();
+}
 
 // Warpgroup w: the thread of row 32 q4 + lane of its tile.
-__device__ void softmax(WindowSmem& sm, const WindowParams& p, Run run, uint32_t tmem, int w, int q4, int lane)
+__device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, int w, int q4, int lane)
 {
     const int trow = 32 * q4 + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * q4) << 16;
     const uint32_t O = tmem + lanes + kD * w, S = tmem + lanes + kSCol + kBS * w;
     Seg s;
-    uint32_t step0 = 0, turn = 0, outs = 0;  // steps of both before the item, own ones, items with own ones
+    uint32_t step0 = 0, turn = 0, outs = 0;  // steps of all warpgroups before the item, own ones, items with own ones
     int block0 = 0;                          // blocks before the item
+    SegReader segs;
+    uint32_t joins = 0;
+    // all softmax threads (a barrier with a limit, like every wait)
+    auto sync_all = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.joined);
+        await(&sm.joined, joins & 1, p.err, 8192, &sm.abort);
+        ++joins;
+        __syncwarp();
+        tc_fence_after();
+    };
 #pragma unroll 1
-    for (int item = 0; next_seg(sm, p, run, s); ++item) {
+    for (int item = 0; segs.next(sm, p, s, lane); ++item) {
         const bool pair = s.x.rows > kTileRows;
         const int nb = s.t1 - s.t0, steps = pair ? 2 * nb : nb;
         const int k_first = (w ^ static_cast<int>(step0)) & 1;   // this warpgroup's first step of the item
-        const int row = trow + (pair ? kTileRows * k_first : 0);
+        // the row in the item, and this thread's chunks of a block's keys
+        const int copies = copies_of(s.x.rows), row_off = pair ? kTileRows * k_first : 0;
+        const int row = (trow & (kTileRows / copies - 1)) + row_off;
+        const int c0 = trow / (kTileRows / copies) * (kBS / kChunk / copies), c1 = c0 + kBS / kChunk / copies;
         const bool live = row < s.x.rows, warp_live = row - lane < s.x.rows;
-        const int pos = sm.pos[s.b] + (s.x.row0 + (live ? row : 0)) / p.G;
-        wait_for(&sm.q_full, item & 1, p.err, 64, &sm.abort);
-        float rs = live ? sm.qs[item & 1][row] * p.scale_log2 : 1.0f;
+        const int pos = s.x.first + tokens_of(p, s.x.row0 + (live ? row : 0)) - tokens_of(p, s.x.row0);
+        await(&sm.q_full, item & 1, p.err, 64, &sm.abort);
+        float rs = live ? sm.qs[item & 1][trow + row_off] * p.scale_log2 : 1.0f;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_empty);
         // the maximum of S k_scale has to stay one under a negative scale: S changes sign
@@ -648,101 +766,99 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, Run run, uint32_t
         float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
         for (int k = k_first; k < steps; k += 2, ++turn) {
-            const int t = s.t0 + (pair ? k >> 1 : k), slot = (block0 + t - s.t0) % kSStages;
-            wait_for(&sm.s_full[w], turn & 1, p.err, 64, &sm.abort);
-            if (!warp_live) {                // a warp without rows keeps the others company
+            const int t = pair ? k >> 1 : k;
+            const uint32_t at = block0 + t;
+            await(&sm.s_full[w], turn & 1, p.err, 64, &sm.abort);
+            if (__builtin_expect(!warp_live, 0)) {   // a warp without rows keeps the others company
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.p_full[w]);
                 continue;
             }
-            tc_fence_after();
-            wait_for(&sm.k_full[slot], ((block0 + t - s.t0) / kSStages) & 1, p.err, 64, &sm.abort);
+            await(&sm.k_full[at % kSStages], (at / kSStages) & 1, p.err, 64, &sm.abort);
             __syncwarp();
-            float v[kBS];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(S + 32 * c, v + 32 * c);
-            tmem_wait_ld();
-            const float4* ks = reinterpret_cast<const float4*>(sm.ks[slot]);
-#pragma unroll
-            for (int c = 0; c < kBS / 4; ++c) {
-                const float4 k4 = ks[c];
-                const float2 a = __fmul2_rn(make_float2(v[4 * c], v[4 * c + 1]), make_float2(k4.x, k4.y));
-                const float2 b = __fmul2_rn(make_float2(v[4 * c + 2], v[4 * c + 3]), make_float2(k4.z, k4.w));
-                v[4 * c] = a.x;
-                v[4 * c + 1] = a.y;
-                v[4 * c + 2] = b.x;
-                v[4 * c + 3] = b.y;
-            }
-            if (any_flip) {
-#pragma unroll
-                for (int i = 0; i < kBS; ++i) v[i] = flip ? -v[i] : v[i];
-            }
-            const int k0 = block_at(s.x, t) * kBS, sink = p.sinks - k0;
-            if (s.x.first - k0 < kBS - 1 || (s.x.last - k0 >= p.window && sink < kBS)) {
-                // keys up to the row's own, and of those its window's and the sinks
-                const int end = pos + 1 - k0, begin = end - p.window;
-                const uint64_t lo = bits_below(end) & (~bits_below(begin) | bits_below(sink));
-                const uint64_t hi = bits_below(end - 64) & (~bits_below(begin - 64) | bits_below(sink - 64));
-#pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    if (!((lo >> i) & 1)) v[i] = -INFINITY;
-                    if (!((hi >> i) & 1)) v[64 + i] = -INFINITY;
-                }
-            }
-            float m4[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                m4[c] = fmaxf(v[32 * c], v[32 * c + 1]);
-#pragma unroll
-                for (int i = 2; i < 32; i += 2) m4[c] = max3(m4[c], v[32 * c + i], v[32 * c + i + 1]);
-            }
-            const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * rs;
-            // Past 2^22 the rounding of mx is no longer small beside the exponents, which
-            // take the products unrounded (one too large by 1 leaves FP16): there they are
-            // rounded as mx is.
-            const bool big = fabsf(mx) > 0x1p22f;
-            float rx = rs;
-            if (__builtin_expect(__any_sync(0xffffffffu, big), 0)) {
-                const float f = big ? rs : 1.0f;
-#pragma unroll
-                for (int i = 0; i < kBS; ++i) v[i] *= f;
-                rx = big ? 1.0f : rs;
-            }
-            const bool raise = mx > m + kRaise || (m == -INFINITY && mx > -INFINITY);
-            if (__any_sync(0xffffffffu, raise)) {
-                const float mn = raise ? mx : m, f = raise ? ex2(m - mn) : 1.0f;   // (0 while m is -inf)
-                m = mn;
-                l *= f;
-                if (k > k_first) {
-                    // (this step's S is complete, so the last step's P V is)
+            tc_fence_after();
+            const float4* ks = reinterpret_cast<const float4*>(sm.ks[at % kSStages]);
+            // keys up to the row's own (end), and of those its window's (from begin) and the
+            // sinks (below sink); whether any row does not see all
+            const int k0 = block_at(s.x, s.t0 + t) * kBS, sink = p.sinks - k0;
+            const bool part_seen = s.x.first - k0 < kBS - 1 || (s.x.last - k0 >= p.window && sink < kBS);
+            const int end = pos + 1 - k0, begin = end - p.window;
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float o[32];
-                        tmem_ld32(O + 32 * c, o);
-                        tmem_wait_ld();
+            for (int c = c0; c < c1; ++c) {
+                float v[kChunk];
+                tmem_ld32(S + kChunk * c, v);
+                tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] *= f;
-                        tmem_st32(O + 32 * c, o);
+                for (int i = 0; i < kChunk / 4; ++i) {
+                    const float4 k4 = ks[kChunk / 4 * c + i];
+                    const float2 a = __fmul2_rn(make_float2(v[4 * i], v[4 * i + 1]), make_float2(k4.x, k4.y));
+                    const float2 b = __fmul2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(k4.z, k4.w));
+                    v[4 * i] = a.x;
+                    v[4 * i + 1] = a.y;
+                    v[4 * i + 2] = b.x;
+                    v[4 * i + 3] = b.y;
+                }
+                if (__builtin_expect(part_seen || any_flip, 0)) {
+                    const uint32_t see = bits_below(end - kChunk * c) &
+                                         (~bits_below(begin - kChunk * c) | bits_below(sink - kChunk * c));
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) v[i] = !((see >> i) & 1) ? -INFINITY : (flip ? -v[i] : v[i]);
+                }
+                float m2[2] = {fmaxf(v[0], v[1]), fmaxf(v[16], v[17])};
+#pragma unroll
+                for (int i = 2; i < 16; i += 2) {
+                    m2[0] = max3(m2[0], v[i], v[i + 1]);
+                    m2[1] = max3(m2[1], v[16 + i], v[17 + i]);
+                }
+                const float mx = fmaxf(m2[0], m2[1]) * rs;
+                float rx = rs;
+                if (__builtin_expect(__any_sync(0xffffffffu, !(mx <= m + kRaise) || fabsf(mx) > 0x1p22f), 0)) {
+                    // Past 2^22 the rounding of mx is no longer small beside the exponents,
+                    // which take the products unrounded (one too large by 1 leaves FP16):
+                    // there they are rounded as mx is.
+                    const bool big = fabsf(mx) > 0x1p22f, raise = mx > m + kRaise;
+                    if (__any_sync(0xffffffffu, big)) {
+                        const float f = big ? rs : 1.0f;
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i) v[i] *= f;
+                        rx = big ? 1.0f : rs;
+                    }
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float mn = raise ? mx : m, f = raise ? ex2(m - mn) : 1.0f;   // (0 while m is -inf)
+                        m = mn;
+                        l *= f;
+                        sum = make_float2(sum.x * f, sum.y * f);
+                        // (this step's S is complete, so the last step's P V is)
+                        if (k > k_first) scale_columns(O, kD / 16, f, false);
+                        // P of the block's keys so far
+                        tmem_wait_st();
+                        if (c > c0) scale_columns(S + kChunk / 2 * c0, c - c0, f, true);
                     }
                 }
-            }
-            const float ref = m == -INFINITY ? 0.0f : m - kShift;
-            const float2 rs2 = make_float2(rx, rx), nref = make_float2(-ref, -ref);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float ref = m == -INFINITY ? 0.0f : m - kShift;
+                const float2 rs2 = make_float2(rx, rx), nref = make_float2(-ref, -ref);
+                uint32_t hp[kChunk / 2];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t hp[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float2 x = __ffma2_rn(make_float2(v[32 * c + 2 * i], v[32 * c + 2 * i + 1]), rs2, nref);
+                for (int i = 0; i < kChunk / 2; ++i) {
+                    float2 x = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), rs2, nref);
                     x.x = ex2(x.x);
                     x.y = ex2(x.y);
-                    sum[i & 1] = __fadd2_rn(sum[i & 1], x);
+                    sum = __fadd2_rn(sum, x);
                     hp[i] = half2_bits(x.x, x.y);
                 }
-                tmem_st16(S + 16 * c, hp);
+                tmem_st16(S + kChunk / 2 * c, hp);
             }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            l += sum.x + sum.y;
+            // the other copies' keys
+            if (copies > 1) {
+                uint32_t zero[kChunk / 2];
+#pragma unroll
+                for (int i = 0; i < kChunk / 2; ++i) zero[i] = 0;
+#pragma unroll 1
+                for (int c = 0; c < kBS / kChunk; ++c)
+                    if (c < c0 || c >= c1) tmem_st16(S + kChunk / 2 * c, zero);
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -750,83 +866,134 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, Run run, uint32_t
         }
         // ---- the item's (or its part's) output ----
         if (k_first < steps) {
-            wait_for(&sm.o_full[w], outs & 1, p.err, 128, &sm.abort);
+            await(&sm.o_full[w], outs & 1, p.err, 128, &sm.abort);
             ++outs;
         }
-        float f[2] = {1.0f, 1.0f}, lt = l, mf = m;
-        bool has[2] = {true, true};
-        if (!pair) {
-            // both warpgroups' sums over the same rows
-            sm.ml[0][w][trow] = m;
-            sm.ml[1][w][trow] = l;
-            __syncwarp();
-            tc_fence_before();
-            named_bar_sync(1, 256);
-            const float m0 = sm.ml[0][0][trow], m1 = sm.ml[0][1][trow];
-            const float l0 = sm.ml[1][0][trow], l1 = sm.ml[1][1][trow];
-            mf = fmaxf(m0, m1);
-            f[0] = m0 == mf ? 1.0f : ex2(m0 - mf);
-            f[1] = m1 == mf ? 1.0f : ex2(m1 - mf);
-            // (nothing summed, perhaps nothing written; a NaN has to reach the output)
-            has[0] = l0 != 0.0f;
-            has[1] = l1 != 0.0f;
-            lt = (has[0] ? l0 * f[0] : 0.0f) + (has[1] ? l1 * f[1] : 0.0f);
-        }
+        const bool whole = s.t0 == 0 && s.t1 == s.x.blocks;
+        float* const part = part_of(p, blockIdx.x, s.first_of_run);
+        float* const part_ml = part + static_cast<int64_t>(p.part_rows) * kD;
         __syncwarp();
         tc_fence_after();
-        if (warp_live) {
-            const bool whole = s.t0 == 0 && s.t1 == s.x.blocks;
-            const float inv = lt == 0.0f ? 0.0f : __fdiv_rn(1.0f, lt);
-            const int64_t at = live ? q_row(p, sm.tok[s.b], s.h, s.x.row0 + row) : 0;
-            float* const part = part_of(p, blockIdx.x, s.first_of_run);
+        if (pair) {
+            const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+            const int64_t at = q_row(p, s.tok, s.h, s.x.row0 + (live ? row : 0)) * kD;
 #pragma unroll 1
-            for (int c = pair ? 0 : w; c < kD / 32; c += pair ? 1 : 2) {
+            for (int c = 0; c < kD && warp_live; c += 16) {
                 __syncwarp();                // (rows behind the last one store nothing)
-                float o[32];
-                if (pair) {
-                    tmem_ld32(O + 32 * c, o);
-                    tmem_wait_ld();
-                } else {
-                    float o1[32];
-                    tmem_ld32(tmem + lanes + 32 * c, o);
-                    tmem_ld32(tmem + lanes + kD + 32 * c, o1);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = (has[0] ? o[i] * f[0] : 0.0f) + (has[1] ? o1[i] * f[1] : 0.0f);
-                }
+                float o[16];
+                tmem_ld16(O + c, o);
+                tmem_wait_ld();
                 if (!live) continue;
                 if (whole) {
-                    const float4* vs = reinterpret_cast<const float4*>(sm.vs[item & 1] + 32 * c);
-                    uint4* dst = reinterpret_cast<uint4*>(p.out + at * kD + 32 * c);
+                    const float4* vs = reinterpret_cast<const float4*>(sm.vs[item & 1] + c);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         const float4 a = vs[2 * i], e = vs[2 * i + 1];
                         const float* x = o + 8 * i;
                         const __nv_bfloat162 y0 = __floats2bfloat162_rn(x[0] * inv * a.x, x[1] * inv * a.y);
                         const __nv_bfloat162 y1 = __floats2bfloat162_rn(x[2] * inv * a.z, x[3] * inv * a.w);
                         const __nv_bfloat162 y2 = __floats2bfloat162_rn(x[4] * inv * e.x, x[5] * inv * e.y);
                         const __nv_bfloat162 y3 = __floats2bfloat162_rn(x[6] * inv * e.z, x[7] * inv * e.w);
-                        dst[i] = make_uint4(
+                        reinterpret_cast<uint4*>(p.out + at + c)[i] = make_uint4(
                             *reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1),
                             *reinterpret_cast<const uint32_t*>(&y2), *reinterpret_cast<const uint32_t*>(&y3));
                     }
                 } else {
-                    float4* dst = reinterpret_cast<float4*>(part + row * kD + 32 * c);
+                    float4* dst = reinterpret_cast<float4*>(part + row * kD + c);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
             }
-            if (!whole && live && (pair || w == 0)) {
-                float* ml = part + static_cast<int64_t>(p.part_rows) * kD;
-                ml[row] = mf;
-                ml[p.part_rows + row] = lt;
+            if (!whole && live) {
+                part_ml[row] = m;
+                part_ml[p.part_rows + row] = l;
+            }
+        } else {
+            // the sums of every row over warpgroups and copies (two, four or eight): 16 or 32
+            // rows and 32 or 16 of their channels at a time through shared memory, two of a
+            // row a thread
+            sm.m[w * kTileRows + trow] = m;
+            sm.l[w * kTileRows + trow] = l;
+            sync_all();
+            const int period = kTileRows / copies, parts = 2 * copies;
+            const int shift = s.x.rows <= 16 ? 4 : 3, at_once = 256 >> shift, units = 1 << shift;
+            const int of = (w * kTileRows + trow) >> shift, j = trow & (units - 1);
+            // the largest m of a row, and the sum of its l over that
+            auto total = [&](int r, float& mr, float& lr) {
+                float mi[8], li[8];
+                mr = -INFINITY;
+                lr = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    mi[i] = i < parts ? sm.m[r + i * period] : -INFINITY;
+                    li[i] = i < parts ? sm.l[r + i * period] : 0.0f;
+                    mr = fmaxf(mr, mi[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) lr += li[i] == 0.0f ? 0.0f : li[i] * (mi[i] == mr ? 1.0f : ex2(mi[i] - mr));
+            };
+            float mf, lt;
+            total(trow & (period - 1), mf, lt);
+            const bool has = l != 0.0f;      // (a NaN has to reach the output)
+            const float f = m == mf ? 1.0f : ex2(m - mf);
+#pragma unroll 1
+            for (int r0 = 0; r0 < s.x.rows; r0 += at_once) {
+                const int r = r0 + of, mine = (trow & (period - 1)) - r0;
+                const bool give = mine >= 0 && mine < at_once;
+                float mr;
+                total(r, mr, lt);
+                const float inv = lt == 0.0f ? 0.0f : __fdiv_rn(1.0f, lt);
+                const int64_t at = r < s.x.rows ? q_row(p, sm.tok[s.b], s.h, s.x.row0 + r) * kD : -1;
+                if (!whole && at >= 0 && j == 0) {
+                    part_ml[r] = mr;
+                    part_ml[p.part_rows + r] = lt;
+                }
+#pragma unroll 1
+                for (int c = 0; c < kD; c += 2 * units) {
+                    // (rows of a warp's own 32 are given or not together, but for the 16)
+                    if (__any_sync(0xffffffffu, give)) {
+#pragma unroll 1
+                        for (int u = 0; u < units; u += 8) {
+                            float o[16];
+                            tmem_ld16(O + c + 2 * u, o);
+                            tmem_wait_ld();
+                            if (give) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)   // (a row's units begin at another place each)
+                                    sm.join[w * 4 + q4][(mine << shift) + ((u + i + mine) & (units - 1))] =
+                                        has ? make_float2(o[2 * i] * f, o[2 * i + 1] * f) : make_float2(0.f, 0.f);
+                            }
+                        }
+                    }
+                    sync_all();
+                    float2 x[8], sum = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        // (parts of a row lie in every copy's warp that has it)
+                        const int from = (r + (i < parts ? i : 0) * period) >> 5;
+                        x[i] = sm.join[from][(of << shift) + ((j + of) & (units - 1))];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        sum.x += i < parts ? x[i].x : 0.0f;
+                        sum.y += i < parts ? x[i].y : 0.0f;
+                    }
+                    if (at >= 0) {
+                        if (whole) {
+                            const float2 vs = *reinterpret_cast<const float2*>(sm.vs[item & 1] + c + 2 * j);
+                            *reinterpret_cast<__nv_bfloat162*>(p.out + at + c + 2 * j) =
+                                __floats2bfloat162_rn(sum.x * inv * vs.x, sum.y * inv * vs.y);
+                        } else {
+                            *reinterpret_cast<float2*>(part + r * kD + c + 2 * j) = sum;
+                        }
+                    }
+                    sync_all();
+                }
             }
         }
+        // (the other's m and l are read until here; the last barrier was behind them)
         tc_fence_before();
         __syncwarp();
-        // (the other's O, m and l are read until here)
-        if (!pair) named_bar_sync(1, 256);
         step0 += steps;
         block0 += nb;
     }
@@ -861,7 +1028,7 @@ __device__ void describe_cut(WindowSmem& sm, const WindowParams& p, const Run& r
 
 __global__ void __launch_bounds__(kThreads, 1)
     window_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-                            const WindowParams p)
+                            const __grid_constant__ WindowParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uintptr_t raw = reinterpret_cast<uintptr_t>(smem_raw);
@@ -884,7 +1051,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.o_full[i], 1);
         }
-        mbar_init(&sm.q_full, 2);
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(&sm.seg_full[i], 1);
+            mbar_init(&sm.seg_empty[i], kSegReaders);
+        }
+        mbar_init(&sm.joined, 8);
+        mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 1 + 8);
         mbar_init(&sm.drain, 1);
         sm.abort = 0;
@@ -900,26 +1072,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sm.tmem;
     // runs of kMinRun positions at least
     const uint32_t ctas = max(1u, min(static_cast<uint32_t>(p.ctas), total / kMinRun));
-    Run run = {};
-    if (blockIdx.x < ctas && total > 0)
-        run = locate(sm, p, group, run_begin(total, blockIdx.x, ctas), run_begin(total, blockIdx.x + 1, ctas));
 
     if (warp < kProdWarp) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        softmax(sm, p, run, tmem, warp >> 2, warp & 3, lane);
-    } else if (warp < kConvWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == kProdWarp) {
-            producer(sm, p, &tk, &tv, run, lane);
-            describe_cut(sm, p, run, total, ctas, lane);
-        } else if (warp == kMmaWarp) {
-            mma_issuer(sm, p, run, tmem);
-        } else {
-            q_loader(sm, p, run, warp - kQWarp, lane);
-        }
-        __syncwarp();
+        softmax(sm, p, tmem, warp >> 2, warp & 3, lane);
+    } else if (warp == kProdWarp) {
+        producer(sm, p, &tk, &tv, lane);
+    } else if (warp == kMmaWarp) {
+        mma_issuer(sm, p, tmem, lane);
+    } else if (warp == kQWarp) {
+        q_loader(sm, p, lane);
+    } else if (warp == kSegWarp) {
+        Run run = {};
+        if (blockIdx.x < ctas && total > 0)
+            run = locate(sm, p, group, run_begin(total, blockIdx.x, ctas), run_begin(total, blockIdx.x + 1, ctas));
+        scheduler(sm, p, run, lane);
+        describe_cut(sm, p, run, total, ctas, lane);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // rows of tokens that see nothing
         for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
             const Sequence s = sequence(p, b);
@@ -930,9 +1098,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = tid - kConvWarp * 32; j < p.NQ * (kD / 8); j += kConvWarps * 32) dst[j] = make_uint4(0, 0, 0, 0);
             }
         }
-        converter(sm, p, run, warp - kConvWarp, lane);
-        __syncwarp();
+        converter(sm, p, warp - kConvWarp, lane);
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
@@ -1131,6 +1299,9 @@ extern "C" pa_status pa_fp8_window_attention(const void* q, const float* q_scale
     p.NQ = NQ;
     p.NKV = NKV;
     p.G = G;
+    p.g_mul = (1u << 22) / G + 1;
+    p.g_inv = ~0ull / G + 1;
+    p.one_item = static_cast<int64_t>(max_tokens) * G <= kItemRows;
     p.num_blocks = num_blocks;
     p.max_blocks = max_blocks_per_seq;
     p.layout = layout;
