@@ -76,8 +76,8 @@ constexpr int kItemCost = 8;                 // what an item costs besides its s
 constexpr int kMinRun = 2;                   // the shortest run (2 at least: describe_cut)
 constexpr int kSegs = 4;                     // items ahead of the slowest part
 // Entries of the schedule in shared memory: an item each while the batch's number no
-// more than half of it, else 2, 4, .. one behind another.
-constexpr int kMaxEntries = 2 * kMaxB;
+// more than 512 a kv head, else 2, 4, .. one behind another.
+constexpr int kMaxEntries = kMaxB + 512;
 
 // What the joining kernel has to know of the item at the begin of a run.
 struct Cut {
@@ -136,7 +136,8 @@ struct WindowSmem {
     alignas(16) float qs[2][kItemRows];             // by item parity, as vs
     alignas(16) float vs[2][kD];
     float m[2 * kTileRows], l[2 * kTileRows];       // of the warpgroups' threads
-    float2 join[8][256];                     // 16 or 32 channels of their rows
+    float4 join[kTileRows * 8];              // 32 or 64 channels of the lanes' rows
+    float inv[kTileRows];                    // 1 / L of an item's rows
     // per sequence: position and row of its first token that sees a key, query rows a
     // kv head; entries before it
     int pos[kMaxB], tok[kMaxB], rows[kMaxB], first[kMaxB + 1];
@@ -380,7 +381,7 @@ __device__ uint32_t build_schedule(WindowSmem& sm, const WindowParams& p, int ti
 // Row r of an item in q and out: a row of tokens x heads.
 __device__ __forceinline__ int64_t q_row(const WindowParams& p, int tok0, int h, int row)
 {
-    const int t = row / p.G;
+    const int t = tokens_of(p, row);
     return static_cast<int64_t>(tok0 + t) * p.NQ + h * p.G + (row - t * p.G);
 }
 
@@ -909,86 +910,77 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
                 part_ml[p.part_rows + row] = l;
             }
         } else {
-            // the sums of every row over warpgroups and copies (two, four or eight): 16 or 32
-            // rows and 32 or 16 of their channels at a time through shared memory, two of a
-            // row a thread
+            // the sums of every row: over the warpgroups in registers (their O lie in the same
+            // lanes), over the copies through shared memory, 32 channels of the 128 lanes or
+            // 64 of the 64 that count at a time
             sm.m[w * kTileRows + trow] = m;
             sm.l[w * kTileRows + trow] = l;
             sync_all();
-            const int period = kTileRows / copies, parts = 2 * copies;
-            const int shift = s.x.rows <= 16 ? 4 : 3, at_once = 256 >> shift, units = 1 << shift;
-            const int of = (w * kTileRows + trow) >> shift, j = trow & (units - 1);
-            // the largest m of a row, and the sum of its l over that
-            auto total = [&](int r, float& mr, float& lr) {
-                float mi[8], li[8];
-                mr = -INFINITY;
-                lr = 0.0f;
+            const int period = kTileRows / copies, narrow = s.x.rows <= 16 ? 1 : 0;
+            float mf = -INFINITY, lt = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    mi[i] = i < parts ? sm.m[r + i * period] : -INFINITY;
-                    li[i] = i < parts ? sm.l[r + i * period] : 0.0f;
-                    mr = fmaxf(mr, mi[i]);
+            for (int i = 0; i < 8; ++i)
+                if (i < 2 * copies) mf = fmaxf(mf, sm.m[(trow + i * period) & (2 * kTileRows - 1)]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int from = (trow + i * period) & (2 * kTileRows - 1);
+                if (i < 2 * copies && sm.l[from] != 0.0f)
+                    lt += sm.l[from] * (sm.m[from] == mf ? 1.0f : ex2(sm.m[from] - mf));
+            }
+            // (nothing summed, perhaps nothing written; a NaN has to reach the output)
+            const bool has0 = sm.l[trow] != 0.0f, has1 = sm.l[kTileRows + trow] != 0.0f;
+            const float m0 = sm.m[trow], m1 = sm.m[kTileRows + trow];
+            const float f0 = m0 == mf ? 1.0f : ex2(m0 - mf), f1 = m1 == mf ? 1.0f : ex2(m1 - mf);
+            if (w == 0 && trow < period) {
+                sm.inv[trow] = lt == 0.0f ? 0.0f : __fdiv_rn(1.0f, lt);
+                if (!whole && live) {
+                    part_ml[row] = mf;
+                    part_ml[p.part_rows + row] = lt;
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) lr += li[i] == 0.0f ? 0.0f : li[i] * (mi[i] == mr ? 1.0f : ex2(mi[i] - mr));
-            };
-            float mf, lt;
-            total(trow & (period - 1), mf, lt);
-            const bool has = l != 0.0f;      // (a NaN has to reach the output)
-            const float f = m == mf ? 1.0f : ex2(m - mf);
+            }
+            // a lane's units of four channels (8 or 16 of them), and its place in the buffer
+            const int units = 8 << narrow, lane_at = narrow ? 16 * q4 + (lane & 15) : trow;
+            const int tid = w * kTileRows + trow, j = tid & (units - 1);
 #pragma unroll 1
-            for (int r0 = 0; r0 < s.x.rows; r0 += at_once) {
-                const int r = r0 + of, mine = (trow & (period - 1)) - r0;
-                const bool give = mine >= 0 && mine < at_once;
-                float mr;
-                total(r, mr, lt);
-                const float inv = lt == 0.0f ? 0.0f : __fdiv_rn(1.0f, lt);
-                const int64_t at = r < s.x.rows ? q_row(p, sm.tok[s.b], s.h, s.x.row0 + r) * kD : -1;
-                if (!whole && at >= 0 && j == 0) {
-                    part_ml[r] = mr;
-                    part_ml[p.part_rows + r] = lt;
+            for (int c = 0; c < kD; c += 4 * units) {
+#pragma unroll 1
+                for (int u = w * units / 2; u < (w + 1) * units / 2; u += 4) {
+                    float x[16], y[16];
+                    tmem_ld16(tmem + lanes + c + 4 * u, x);
+                    tmem_ld16(tmem + lanes + kD + c + 4 * u, y);
+                    tmem_wait_ld();
+                    if (!narrow || lane < 16) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = (has0 ? x[i] * f0 : 0.0f) + (has1 ? y[i] * f1 : 0.0f);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)   // (a lane's units begin at another place each)
+                            sm.join[lane_at * units + ((u + i + lane_at) & (units - 1))] =
+                                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    }
                 }
+                sync_all();
 #pragma unroll 1
-                for (int c = 0; c < kD; c += 2 * units) {
-                    // (rows of a warp's own 32 are given or not together, but for the 16)
-                    if (__any_sync(0xffffffffu, give)) {
-#pragma unroll 1
-                        for (int u = 0; u < units; u += 8) {
-                            float o[16];
-                            tmem_ld16(O + c + 2 * u, o);
-                            tmem_wait_ld();
-                            if (give) {
+                for (int r = tid >> (3 + narrow); r < s.x.rows; r += 256 >> (3 + narrow)) {
+                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i)   // (a row's units begin at another place each)
-                                    sm.join[w * 4 + q4][(mine << shift) + ((u + i + mine) & (units - 1))] =
-                                        has ? make_float2(o[2 * i] * f, o[2 * i + 1] * f) : make_float2(0.f, 0.f);
-                            }
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        if (i >= copies) break;
+                        const int from = r + (narrow ? 16 : period) * i;
+                        const float4 x = sm.join[from * units + ((j + from) & (units - 1))];
+                        sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
                     }
-                    sync_all();
-                    float2 x[8], sum = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        // (parts of a row lie in every copy's warp that has it)
-                        const int from = (r + (i < parts ? i : 0) * period) >> 5;
-                        x[i] = sm.join[from][(of << shift) + ((j + of) & (units - 1))];
+                    if (whole) {
+                        const float inv = sm.inv[r];
+                        const float4 vs = *reinterpret_cast<const float4*>(sm.vs[item & 1] + c + 4 * j);
+                        const __nv_bfloat162 y0 = __floats2bfloat162_rn(sum.x * inv * vs.x, sum.y * inv * vs.y);
+                        const __nv_bfloat162 y1 = __floats2bfloat162_rn(sum.z * inv * vs.z, sum.w * inv * vs.w);
+                        *reinterpret_cast<uint2*>(p.out + q_row(p, s.tok, s.h, s.x.row0 + r) * kD + c + 4 * j) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+                    } else {
+                        *reinterpret_cast<float4*>(part + r * kD + c + 4 * j) = sum;
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        sum.x += i < parts ? x[i].x : 0.0f;
-                        sum.y += i < parts ? x[i].y : 0.0f;
-                    }
-                    if (at >= 0) {
-                        if (whole) {
-                            const float2 vs = *reinterpret_cast<const float2*>(sm.vs[item & 1] + c + 2 * j);
-                            *reinterpret_cast<__nv_bfloat162*>(p.out + at + c + 2 * j) =
-                                __floats2bfloat162_rn(sum.x * inv * vs.x, sum.y * inv * vs.y);
-                        } else {
-                            *reinterpret_cast<float2*>(part + r * kD + c + 2 * j) = sum;
-                        }
-                    }
-                    sync_all();
                 }
+                sync_all();
             }
         }
         // (the other's m and l are read until here; the last barrier was behind them)
