@@ -72,7 +72,7 @@ constexpr int kChunk = 32;                   // scores a softmax thread holds at
 constexpr uint32_t kTmemCols = 512, kSCol = 2 * kD;   // O of either warpgroup, then S (and P)
 constexpr float kRaise = 8.0f;               // log2 units
 constexpr float kShift = 7.0f;
-constexpr int kItemCost = 8;                 // what an item costs besides its steps, in steps
+constexpr int kItemCost = 5;                 // what an item costs besides its steps, in steps (3 to 11 tried)
 constexpr int kMinRun = 2;                   // the shortest run (2 at least: describe_cut)
 constexpr int kSegs = 4;                     // items ahead of the slowest part
 // Entries of the schedule in shared memory: an item each while the batch's number no
@@ -557,10 +557,12 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
     return ok != 0;
 }
 
-// The MMAs' warp: the whole warp polls, one elected thread issues. S of step j + 2 goes
-// behind P V of step j; which of the two goes next is whichever has its operands, so
-// that an item's last P V do not wait for the next one's Q. (Polled: a warp is woken
-// sooner than out of a wait.)
+// The MMAs' warp; one elected thread issues. S of step j + 2 goes behind P V of step j;
+// which of the two goes next is whichever has its operands, so that an item's last P V do
+// not wait for the next one's Q. The warp polls only while it waits for either: a poll
+// takes issue slots from the softmax warps on the same quarter of the SM, and every step
+// needs all four of a warpgroup's (polling throughout, two prompts of 5000 tokens with
+// 8 x 12 heads took 836 us, against 758).
 __device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, uint32_t tmem, int lane)
 {
     constexpr uint32_t kIdescS = idesc_e4m3(128, kBS, 0, 0);
@@ -621,7 +623,12 @@ __device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, uint32_t tmem,
         }
         if (o < a) {
             const uint32_t w = o & 1, blk = w ? block_of[1] : block_of[0], f = w ? flags[1] : flags[0], hslot = blk % kHStages;
-            const bool ready = mbar_test(&sm.p_full[w], (o >> 1) & 1) && mbar_test(&sm.h_full[hslot], (blk / kHStages) & 1);
+            bool ready;
+            if (more && a < o + 2)           // (S is waiting for Q or K, too)
+                ready = mbar_test(&sm.p_full[w], (o >> 1) & 1) && mbar_test(&sm.h_full[hslot], (blk / kHStages) & 1);
+            else
+                ready = await(&sm.h_full[hslot], (blk / kHStages) & 1, p.err, 32, &sm.abort) &&
+                        await(&sm.p_full[w], (o >> 1) & 1, p.err, 32, &sm.abort);
             if (__all_sync(0xffffffffu, ready)) {
                 tc_fence_after();
                 if (elect_one()) {

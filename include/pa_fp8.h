@@ -765,7 +765,7 @@ PA_API pa_status pa_plan_batch(const int32_t* kv_act_seqs, const int32_t* new_le
  * row sees are out of contract.
  * D, block_size  128 and 128 (else PA_ERR_UNSUPPORTED). NQ / NKV at most 128, B
  * at most 1024, max_blocks_per_seq * 128 below 2^24, num_tokens * NQ below 2^31
- * and (num_tokens * NQ / NKV / 256 + 1 + B) * NKV * (2 max_blocks_per_seq + 8)
+ * and (num_tokens * NQ / NKV / 256 + 1 + B) * NKV * (2 max_blocks_per_seq + 5)
  * below 2^32 (else PA_ERR_UNSUPPORTED).
  * workspace    at least pa_fp8_window_attention_workspace_size() bytes of the
  *              same max_tokens and heads (or of more tokens), 256-byte aligned,
