@@ -6,25 +6,36 @@
 //
 // A row goes to a cluster of 1 to 8 CTAs, each of which takes a part of it in chunks
 // of 64 bytes a thread, and a cluster takes one row after another. A thread copies its
-// own pieces of the next two chunks, the next row's among them, to shared memory (so
+// own pieces of the next three chunks, the next row's among them, to shared memory (so
 // that no barrier stands between a copy and its use), keeps its own m, l and s (FP32, a
 // few hundred terms each) and rescales them when its maximum grows; they are joined at
 // a row's end, over lanes, warps and the cluster's CTAs. A value's exponent is one
 // fused operation, x log2 e - c with c = m log2 e as rounded; what the rounding is off
 // by is one factor of 16 terms, taken out of their sum. (Past 2^10 that factor is no
-// longer near 1: there, and where a term is -inf, x - m is formed first.)
+// longer near 1: there, and where a term is -inf, x - m is formed first.) The rank counts
+// signs of x_t - x, or pairs of BF16 ones, only where a thread's 16 values have a larger
+// one: a comparison and a sum for each took 250 rows x 131072 from 24.8 to 28.9 us.
 //
 // Alternatives: a value and its index make a 64-bit key, larger for the larger
 // value and, among equal ones, for the lower index, so that no two are equal. The pass
 // itself does nothing for them, a thread's maximum is there anyhow. Behind it the k-th
 // largest of the maxima of 32 groups of threads is a bound that k values at least
 // reach; the threads whose maximum does, k to twice as many, have their pieces read
-// again (from L2, a piece a thread), and values that reach the bound go to a list in
+// again (from L2, a piece a lane), and values that reach the bound go to a list in
 // shared memory, which is put in order by counting (a key's rank is the number of larger
-// ones). A list of more than kShort is thinned first, by the same bound over 32 groups
-// of it; one that runs over (thousands of equal values) is made anew by `careful`, which
-// keeps it short as it goes. -inf is never listed: where fewer than k values are finite
-// the lowest indices of the others follow.
+// ones): by one warp without a barrier if there are at most 64, else by all, and more
+// than kShort are thinned first, by the same bound over 32 groups of the list; one that
+// runs over (thousands of equal values) is made anew by `careful`, which keeps it short as
+// it goes. -inf is never listed: where fewer than k values are finite the lowest indices
+// of the others follow.
+//
+// What bounds it: many rows, the reads (4096 rows x 50000 FP32 131 us, 6.3 TB/s; a copy's
+// rate would take 121). A row a CTA, what stands around the reads: the two
+// loads of the token's logit, one behind the other, 2 us, and 5 us of joins, bound, second
+// reading and order, every instruction of which runs once and out of a cold cache (250 rows
+// x 131072 BF16 with 20 alternatives 26 us, without 20; 38 such rows 14.4; one row of 32003
+// FP32 with 5 alternatives 8.3, 6.5 in a graph). Rows cut over clusters at any number of
+// rows cost more in joins than they balance (250 rows on 2, 4 and 8 CTAs 37, 60, 108 us).
 #include "common.cuh"
 
 #include <cooperative_groups.h>
@@ -40,12 +51,12 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPieces = 4;                   // 16-byte pieces of a chunk a thread
-constexpr int kStages = 2;                   // chunks on their way
+constexpr int kStages = 3;                   // chunks on their way
 constexpr uint32_t kSlot = kPieces * kThreads * 16;   // bytes of a chunk
 constexpr int kPer = 16;                     // values a thread has in registers at once
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
-constexpr int kList = 4096;                  // candidates
+constexpr int kList = 1024;                  // candidates
 constexpr int kShort = 256;                  // of which at most so many are put in order
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -82,9 +93,9 @@ struct Smem {
     Stats all[kMaxCluster];                  // the first's: every CTA's
     float group[2 * kWarps];
     uint16_t who[kThreads];                  // threads whose maximum reaches the bound
-    int threads;
+    int threads[2], count[2];                // by row parity
     float bound;
-    int count, left;
+    int left;
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c)
@@ -208,6 +219,25 @@ __device__ __noinline__ int first_of_list(TopSmem& t, Smem& sm, int n, int k)
     return kept;
 }
 
+// The same for n <= 64 keys, by the first warp alone: no barrier.
+__device__ __forceinline__ int first_of_few(TopSmem& t, int n, int k, int lane)
+{
+    if (lane == 0) t.list[n] = 0;
+    __syncwarp();
+    const uint64_t a = lane < n ? t.list[lane] : 0ull, b = lane + 32 < n ? t.list[lane + 32] : 0ull;
+    int ra = 0, rb = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; i += 2) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(t.list + i);
+        ra += (x.x > a) + (x.y > a);
+        rb += (x.x > b) + (x.y > b);
+    }
+    if (lane < n && ra < k) t.best[ra] = a;
+    if (lane + 32 < n && rb < k) t.best[rb] = b;
+    __syncwarp();
+    return min(n, k);
+}
+
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float lowest(float) { return -INFINITY; }
@@ -282,33 +312,33 @@ struct Part {
     }
 };
 
-// The candidates of a part whose list ran over: the first k of those behind are kept,
-// 2048 values at a time. Returns the list's length.
+// The candidates of a part whose list ran over: the first k of those behind are kept, a
+// value a thread at a time. Returns the list's length.
 template <typename T>
-__device__ __noinline__ int careful(TopSmem& t, Smem& sm, const T* x, int begin, int end, int k)
+__device__ __noinline__ int careful(TopSmem& t, Smem& sm, int& count, const T* x, int begin, int end, int k)
 {
     const int tid = threadIdx.x;
     __syncthreads();
-    if (tid == 0) sm.count = 0;
+    if (tid == 0) count = 0;
     __syncthreads();
     float bound = -INFINITY;
-    for (int at = begin; at < end; at += 4 * kThreads) {
-        for (int i = at + tid; i < min(at + 4 * kThreads, end); i += kThreads) {
-            const float v = as_float(x[i]);
-            // (what equals the bound comes behind those that are there)
-            if (v > bound) t.list[atomicAdd(&sm.count, 1)] = key_of(v, static_cast<uint32_t>(i));
-        }
+    static_assert(kShort + kThreads <= kList, "the list has room for what is kept and a value a thread");
+    for (int at = begin; at < end; at += kThreads) {
+        const int i = at + tid;
+        const float v = i < end ? as_float(x[i]) : -INFINITY;
+        // (what equals the bound comes behind those that are there)
+        if (v > bound) t.list[atomicAdd(&count, 1)] = key_of(v, static_cast<uint32_t>(i));
         __syncthreads();
-        const int n = sm.count;
+        const int n = count;
         if (n >= kShort) {
             const int kept = first_of_list(t, sm, n, k);
             if (tid < kept) t.list[tid] = t.best[tid];
-            if (tid == 0) sm.count = kept;
+            if (tid == 0) count = kept;
             if (kept == k) bound = unordered(static_cast<uint32_t>(t.best[k - 1] >> 32));
         }
         __syncthreads();
     }
-    return sm.count;
+    return count;
 }
 
 template <typename T, bool TOP>
@@ -324,7 +354,13 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
     const uint32_t ctas = cluster.num_blocks(), rank = cluster.block_rank();
     const int64_t step = gridDim.x / ctas;
     if (ctas > 1) cluster.barrier_arrive();
-    if (TOP && tid == 0) sm.count = sm.threads = 0;       // (ahead of the first row's barriers)
+    if (TOP && tid == 0) sm.count[0] = sm.threads[0] = 0; // (ahead of the first row's barriers)
+
+    auto token = [&](int64_t row) { return row < p.R ? load_slot(p.tok, p.tok_type, row) : -1; };
+    auto logit = [&](int64_t row, int64_t t) {
+        return t >= 0 && t < p.V ? as_float(static_cast<const T*>(p.x)[row * p.stride + t]) + 0.0f : INFINITY;   // (-0 as 0)
+    };
+    int64_t tok = token(blockIdx.x / ctas);
 
     // ---- the next chunks on their way, over the row's end ----
     int64_t a_row = blockIdx.x / ctas;
@@ -351,11 +387,6 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
     };
 #pragma unroll
     for (int i = 0; i < kStages; ++i) fetch();
-    auto token = [&](int64_t row) { return row < p.R ? load_slot(p.tok, p.tok_type, row) : -1; };
-    auto logit = [&](int64_t row, int64_t t) {
-        return t >= 0 && t < p.V ? as_float(static_cast<const T*>(p.x)[row * p.stride + t]) : INFINITY;
-    };
-    int64_t tok = token(blockIdx.x / ctas);
     float xt = logit(blockIdx.x / ctas, tok);
     int parity = 0;
 #pragma unroll 1
@@ -378,8 +409,30 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
                 for (int e = 1; e < kPer; e += 2) mx = max3(mx, w[e], w[e + 1 < kPer ? e + 1 : e]);
                 // the token's rank (of a probable one few threads have values above it)
                 if (mx > xt) {
+                    if constexpr (VEC == 4) {
+                        // signs of xt - x
+                        uint32_t signs = 0;
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e) st.above += w[e] > xt;
+                        for (int e = 0; e < kPer; e += 2) {
+                            const float2 d = __ffma2_rn(make_float2(w[e], w[e + 1]), make_float2(-1.f, -1.f), make_float2(xt, xt));
+                            signs = __funnelshift_l(__float_as_uint(d.x), signs, 1);
+                            signs = __funnelshift_l(__float_as_uint(d.y), signs, 1);
+                        }
+                        st.above += __popc(signs);
+                    } else {
+                        // ones, pair by pair (8 at most, BF16 exactly)
+                        const __nv_bfloat162 t2 = __float2bfloat162_rn(xt);
+                        __nv_bfloat162 n2 = __float2bfloat162_rn(0.0f);
+#pragma unroll
+                        for (int i = 0; i < kPer / VEC; ++i) {
+                            const uint4 r = in[(at + i) * kThreads];
+                            n2 = __hadd2(n2, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&r.x), t2));
+                            n2 = __hadd2(n2, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&r.y), t2));
+                            n2 = __hadd2(n2, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&r.z), t2));
+                            n2 = __hadd2(n2, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&r.w), t2));
+                        }
+                        st.above += static_cast<int>(__low2float(n2) + __high2float(n2));
+                    }
                 }
                 const float m = fmaxf(st.m, mx);
                 if (m != st.m) {
@@ -453,35 +506,49 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
             }
             __syncthreads();
             const float bound = sm.bound;
-            if (mine >= bound) sm.who[atomicAdd(&sm.threads, 1)] = static_cast<uint16_t>(tid);
+            int &threads = sm.threads[parity], &count = sm.count[parity];
+            if (mine >= bound) sm.who[atomicAdd(&threads, 1)] = static_cast<uint16_t>(tid);
+            if (tid == 0) sm.threads[parity ^ 1] = sm.count[parity ^ 1] = 0;
             __syncthreads();
-            const int pieces = static_cast<int>(part.c1 - part.c0) * kPieces, all = sm.threads * pieces;
-#pragma unroll 2
-            for (int j = tid; j < all; j += kThreads) {
-                const int w = j / pieces;
-                const int i = part.first_of(part.c0) + (sm.who[w] - tid) * VEC + (j - w * pieces) * (kThreads * VEC);
-                float v[VEC];
-                if (i >= 0 && i + VEC <= p.V) {
-                    unpack(*reinterpret_cast<const uint4*>(part.x + i), v, T());
-                } else {
+            // a thread's pieces to as many lanes, a warp's at most
+            const int pieces = static_cast<int>(part.c1 - part.c0) * kPieces, all = threads;
+            const int shift = pieces > 16 ? 5 : (pieces > 8 ? 4 : (pieces > 4 ? 3 : 2));
+            for (int w = tid >> shift; w < all; w += kThreads >> shift) {
+                const int i0 = part.first_of(part.c0) + (sm.who[w] - tid) * VEC;
+#pragma unroll 4
+                for (int j = tid & ((1 << shift) - 1); j < pieces; j += 1 << shift) {
+                    const int i = i0 + j * (kThreads * VEC);
+                    float v[VEC];
+                    if (i >= 0 && i + VEC <= p.V) {
+                        unpack(*reinterpret_cast<const uint4*>(part.x + i), v, T());
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) v[e] = i + e >= 0 && i + e < p.V ? as_float(part.x[i + e]) : -INFINITY;
-                }
+                        for (int e = 0; e < VEC; ++e)
+                            v[e] = i + e >= 0 && i + e < p.V ? as_float(part.x[i + e]) : -INFINITY;
+                    }
+                    float mx = v[0];
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    if (v[e] >= bound) {
-                        const int at = atomicAdd(&sm.count, 1);
-                        if (at < kList) top.list[at] = key_of(v[e], static_cast<uint32_t>(i + e));
+                    for (int e = 1; e < VEC; e += 2) mx = max3(mx, v[e], v[e + 1 < VEC ? e + 1 : e]);
+                    if (mx < bound) continue;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        if (v[e] >= bound) {
+                            const int at = atomicAdd(&count, 1);
+                            if (at < kList) top.list[at] = key_of(v[e], static_cast<uint32_t>(i + e));
+                        }
                     }
                 }
             }
             __syncthreads();
-            int n = sm.count;
-            if (n > kList)
-                n = careful(top, sm, part.x, max(part.first_of(part.c0) - tid * VEC, 0),
-                            min(part.first_of(part.c1) - tid * VEC, p.V), p.k);
-            kept = first_of_list(top, sm, n, p.k);
-            if (tid == 0) sm.count = sm.threads = 0;
+            int n = count;
+            if (n <= 2 * 32) {
+                if (warp == 0) kept = first_of_few(top, n, p.k, lane);
+            } else {
+                if (n > kList)
+                    n = careful(top, sm, count, part.x, max(part.first_of(part.c0) - tid * VEC, 0),
+                                min(part.first_of(part.c1) - tid * VEC, p.V), p.k);
+                kept = first_of_list(top, sm, n, p.k);
+            }
         }
         if (ctas > 1) {
             // (the first has begun, and is done with the row before)
@@ -617,10 +684,12 @@ extern "C" pa_status pa_token_logprobs(const void* logits, int dtype, int64_t ro
     p.entropy = entropy;
     p.top_ids = top_ids;
     p.top_lp = top_logprobs;
-    // As many CTAs a row as there are room for, two an SM, and as have a chunk each.
+    // As many CTAs a row as there is room for, two an SM, and as have a chunk each. (Clusters
+    // do not fill every group of SMs: 36 of 8 CTAs run at once on 152 SMs, 74 of 4, all 152
+    // of 2. 38 rows x 131072 took 22.7 us on clusters of 8, 14.4 on those of 4.)
     const int chunk = kThreads * kPieces * 16 / (dtype == PA_DTYPE_F32 ? 4 : 2);
     int ctas = kMaxCluster;
-    while (ctas > 1 && (num_rows * ctas > 2 * sms || V <= chunk * (ctas / 2))) ctas /= 2;
+    while (ctas > 1 && (num_rows * ctas > 2 * sms - (ctas > 2 ? 2 * ctas : 0) || V <= chunk * (ctas / 2))) ctas /= 2;
     const int64_t clusters = std::min<int64_t>(num_rows, 2 * sms / ctas);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;

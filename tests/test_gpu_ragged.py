@@ -585,6 +585,22 @@ def test_logprobs_orders_and_ties(kind, dtype):
     check_logprobs(x.expand(3, V).contiguous(), tok.expand(3).contiguous(), k)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [40, 9001, 70001])
+def test_logprobs_ranks_beside_zeros_and_the_largest_values(V, dtype):
+    """Zeros of either sign are equal; differences may leave the range of the type."""
+    i = torch.arange(V, device="cuda")
+    big = torch.finfo(dtype).max
+    zeros = torch.where(i % 3 == 0, 1.0, torch.where(i % 2 == 0, 0.0, -0.0))
+    ends = torch.where(i % 5 == 0, big, torch.where(i % 5 == 1, -big, torch.where(i % 5 == 2, -math.inf, i.float() / V)))
+    x = torch.stack([zeros, zeros, ends, ends, ends, ends]).to(dtype)
+    tok = _i32(1, 4, 5, 6, 7, 8)             # -0, 0, the largest, the least, -inf, one between
+    *_, rank, _, ids, _ = (None, *run_logprobs(x, tok, 20))
+    want = (x.double() > x.double().gather(1, tok.long()[:, None])).sum(-1)
+    assert torch.equal(rank.long(), want)
+    assert torch.equal(ids.long(), torch.argsort(x.double(), dim=-1, descending=True, stable=True)[:, :20])
+
+
 def test_logprobs_of_bad_rows_and_tokens():
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
