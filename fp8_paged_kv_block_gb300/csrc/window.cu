@@ -13,8 +13,9 @@
 //   O += FP16(P) V                    tcgen05 kind::f16, P from tensor memory
 //   out = BF16(O v_scale / L)
 //
-// The numbers are tree.cu's: P in FP16 (half a step 2^-11), V's codes as FP16 exactly,
-// m raised only when a block's maximum lies more than 2^8 above it.
+// The numbers are tree.cu's: P in FP16 (half a step 2^-11), V's codes as FP16 exactly. m
+// is raised only where P would leave FP16: the sum of a thread's 32 P, which it forms
+// anyhow, tells (2^15 at most); no maximum is looked up but then and at an item's begin.
 //
 // Two softmax warpgroups, each with an S and an O of its own in tensor memory (2 x 128
 // + 2 x 128 columns); P lies over its S's columns. A step is one tile of 128 rows and a
@@ -39,8 +40,24 @@
 // quarters: with one copy three of a warpgroup's four warps would have no rows. The copies
 // have an O, an m and an l of their own and are joined with the warpgroups' at the end.
 //
-// Loops are rolled (32 scores at a time under a running maximum) and what is rare lies
-// behind branches that are marked so: the parts run at once out of one instruction cache.
+// Loops are rolled (32 scores at a time) and what is rare lies behind branches that are
+// marked so: the parts run at once out of one instruction cache.
+//
+// What bounds it, on 152 SMs: prompts, the softmax warps' instructions. A step of 128 x 128
+// takes a warpgroup 3000 clocks of softmax (the four warps on a quarter of the SM issue in
+// 42% of the clocks, packed FP32 operations in two clocks each, exponentials in four) and
+// 1300 of waiting for P V and the next S, so that with two in flight the tensor core has
+// work a third of the time. Two prompts of 5000 tokens, 8 x 12 heads, window 4096: 698 us
+// (1.1 PFLOP/s); with a maximum of every 32 scores 747. Six chunks of up to 509 tokens
+// beside 31 decoding requests, window 1000: 185 us, 10000 clocks of an item's 40000 its
+// begin, its last P V and its output. Tried and slower: steps of 64 keys (905); S in halves,
+// the first ahead of P V (709); scores of the next 32 keys loaded ahead (868); two threads a
+// row (946); loops unrolled by two (707); four rows and a quarter of the columns a thread, so
+// that a key scale serves four scores (766 against 758 then, 163 against 120 for decoding).
+// Decoding, the blocks' reads: 64 requests of 8 x 12 heads, window 4096, 550 MB in 120 us
+// (117 in a graph, 4.7 TB/s), four requests of 110000 tokens 172 us (5.5 TB/s). An item ends
+// with 12000 clocks in which three blocks are read ahead. One token of one request: 14.4 us,
+// 12.2 in a graph, launches, schedule and one pass through every part.
 //
 // The items in (sequence, kv head, row) order are dealt to the CTAs in runs of equal
 // weight: a step counts 1, an item kItemCost besides. Items that a run's end cuts leave
@@ -70,8 +87,9 @@ constexpr int kProdWarp = 8, kMmaWarp = 9, kQWarp = 10, kSegWarp = 11, kConvWarp
 constexpr int kThreads = (kConvWarp + kConvWarps) * 32;
 constexpr int kChunk = 32;                   // scores a softmax thread holds at once
 constexpr uint32_t kTmemCols = 512, kSCol = 2 * kD;   // O of either warpgroup, then S (and P)
-constexpr float kRaise = 8.0f;               // log2 units
-constexpr float kShift = 7.0f;
+constexpr float kShift = 7.0f;               // log2 units
+constexpr float kRaise = 3.0f;
+constexpr float kLimit = 0x1p15f;            // of a chunk's sum; one that passes it has a P of 2^(3 + 7)
 constexpr int kItemCost = 5;                 // what an item costs besides its steps, in steps (3 to 11 tried)
 constexpr int kMinRun = 2;                   // the shortest run (2 at least: describe_cut)
 constexpr int kSegs = 4;                     // items ahead of the slowest part
@@ -771,7 +789,7 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
         const bool flip = rs < 0.0f, any_flip = __any_sync(0xffffffffu, flip);
         rs = fabsf(rs);
         if (rs < 1.17549435e-38f) rs = 1.17549435e-38f;       // (-inf times it stays -inf; a NaN stays, too)
-        float m = -INFINITY, l = 0.0f;
+        float m = -INFINITY, l = 0.0f, nref = 0.0f, limit = -1.0f;   // (nref: 7 - m, or 0; the first chunk sets m)
 #pragma unroll 1
         for (int k = k_first; k < steps; k += 2, ++turn) {
             const int t = pair ? k >> 1 : k;
@@ -813,28 +831,34 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) v[i] = !((see >> i) & 1) ? -INFINITY : (flip ? -v[i] : v[i]);
                 }
-                float m2[2] = {fmaxf(v[0], v[1]), fmaxf(v[16], v[17])};
-#pragma unroll
-                for (int i = 2; i < 16; i += 2) {
-                    m2[0] = max3(m2[0], v[i], v[i + 1]);
-                    m2[1] = max3(m2[1], v[16 + i], v[17 + i]);
-                }
-                const float mx = fmaxf(m2[0], m2[1]) * rs;
+                // P = 2^(x - m + 7). Its sum tells whether all are inside FP16; if not, or where
+                // there is no m yet, the maximum is looked up and it is done again.
+                uint32_t hp[kChunk / 2];
+                float2 part;
                 float rx = rs;
-                if (__builtin_expect(__any_sync(0xffffffffu, !(mx <= m + kRaise) || fabsf(mx) > 0x1p22f), 0)) {
-                    // Past 2^22 the rounding of mx is no longer small beside the exponents,
-                    // which take the products unrounded (one too large by 1 leaves FP16):
-                    // there they are rounded as mx is.
-                    const bool big = fabsf(mx) > 0x1p22f, raise = mx > m + kRaise;
-                    if (__any_sync(0xffffffffu, big)) {
-                        const float f = big ? rs : 1.0f;
+                bool again = false;
+#pragma unroll 1
+                for (;;) {
+                    const float2 rs2 = make_float2(rx, rx), ref2 = make_float2(nref, nref);
+                    part = make_float2(0.f, 0.f);
 #pragma unroll
-                        for (int i = 0; i < kChunk; ++i) v[i] *= f;
-                        rx = big ? 1.0f : rs;
+                    for (int i = 0; i < kChunk / 2; ++i) {
+                        float2 x = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), rs2, ref2);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        part = __fadd2_rn(part, x);
+                        hp[i] = half2_bits(x.x, x.y);
                     }
+                    if (__builtin_expect(again || __all_sync(0xffffffffu, part.x + part.y <= limit), 1)) break;
+                    again = true;
+                    float mx = fmaxf(v[0], v[1]);
+#pragma unroll
+                    for (int i = 2; i < kChunk; i += 2) mx = max3(mx, v[i], v[i + 1]);
+                    mx *= rs;
+                    const bool raise = mx > m + kRaise;
                     if (__any_sync(0xffffffffu, raise)) {
-                        const float mn = raise ? mx : m, f = raise ? ex2(m - mn) : 1.0f;   // (0 while m is -inf)
-                        m = mn;
+                        const float f = raise ? ex2(m - mx) : 1.0f;      // (0 while m is -inf)
+                        m = raise ? mx : m;
                         l *= f;
                         sum = make_float2(sum.x * f, sum.y * f);
                         // (this step's S is complete, so the last step's P V is)
@@ -843,18 +867,20 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
                         tmem_wait_st();
                         if (c > c0) scale_columns(S + kChunk / 2 * c0, c - c0, f, true);
                     }
-                }
-                const float ref = m == -INFINITY ? 0.0f : m - kShift;
-                const float2 rs2 = make_float2(rx, rx), nref = make_float2(-ref, -ref);
-                uint32_t hp[kChunk / 2];
+                    // Past 2^22 the rounding of m is no longer small beside the exponents, which
+                    // take the products unrounded (one too large by 1 leaves FP16): there they are
+                    // rounded as m is, every time.
+                    const bool none = m == -INFINITY, big = fabsf(m) > 0x1p22f && !none;
+                    nref = none ? 0.0f : kShift - m;
+                    limit = none || big ? -1.0f : kLimit;
+                    if (__any_sync(0xffffffffu, big)) {
+                        const float f = big ? rs : 1.0f;
 #pragma unroll
-                for (int i = 0; i < kChunk / 2; ++i) {
-                    float2 x = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), rs2, nref);
-                    x.x = ex2(x.x);
-                    x.y = ex2(x.y);
-                    sum = __fadd2_rn(sum, x);
-                    hp[i] = half2_bits(x.x, x.y);
+                        for (int i = 0; i < kChunk; ++i) v[i] *= f;
+                        rx = big ? 1.0f : rs;
+                    }
                 }
+                sum = __fadd2_rn(sum, part);
                 tmem_st16(S + kChunk / 2 * c, hp);
             }
             l += sum.x + sum.y;
