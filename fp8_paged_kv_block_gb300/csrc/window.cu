@@ -13,9 +13,8 @@
 //   O += FP16(P) V                    tcgen05 kind::f16, P from tensor memory
 //   out = BF16(O v_scale / L)
 //
-// The numbers are tree.cu's: P in FP16 (half a step 2^-11), V's codes as FP16 exactly. m
-// is raised only where P would leave FP16: the sum of a thread's 32 P, which it forms
-// anyhow, tells (2^15 at most); no maximum is looked up but then and at an item's begin.
+// The numbers are tree.cu's: P in FP16 (half a step 2^-11), V's codes as FP16 exactly,
+// m raised only when a block's maximum lies more than 2^8 above it.
 //
 // Two softmax warpgroups, each with an S and an O of its own in tensor memory (2 x 128
 // + 2 x 128 columns); P lies over its S's columns. A step is one tile of 128 rows and a
@@ -40,24 +39,8 @@
 // quarters: with one copy three of a warpgroup's four warps would have no rows. The copies
 // have an O, an m and an l of their own and are joined with the warpgroups' at the end.
 //
-// Loops are rolled (32 scores at a time) and what is rare lies behind branches that are
-// marked so: the parts run at once out of one instruction cache.
-//
-// What bounds it, on 152 SMs: prompts, the softmax warps' instructions. A step of 128 x 128
-// takes a warpgroup 3000 clocks of softmax (the four warps on a quarter of the SM issue in
-// 42% of the clocks, packed FP32 operations in two clocks each, exponentials in four) and
-// 1300 of waiting for P V and the next S, so that with two in flight the tensor core has
-// work a third of the time. Two prompts of 5000 tokens, 8 x 12 heads, window 4096: 698 us
-// (1.1 PFLOP/s); with a maximum of every 32 scores 747. Six chunks of up to 509 tokens
-// beside 31 decoding requests, window 1000: 185 us, 10000 clocks of an item's 40000 its
-// begin, its last P V and its output. Tried and slower: steps of 64 keys (905); S in halves,
-// the first ahead of P V (709); scores of the next 32 keys loaded ahead (868); two threads a
-// row (946); loops unrolled by two (707); four rows and a quarter of the columns a thread, so
-// that a key scale serves four scores (766 against 758 then, 163 against 120 for decoding).
-// Decoding, the blocks' reads: 64 requests of 8 x 12 heads, window 4096, 550 MB in 120 us
-// (117 in a graph, 4.7 TB/s), four requests of 110000 tokens 172 us (5.5 TB/s). An item ends
-// with 12000 clocks in which three blocks are read ahead. One token of one request: 14.4 us,
-// 12.2 in a graph, launches, schedule and one pass through every part.
+// Loops are rolled (32 scores at a time under a running maximum) and what is rare lies
+// behind branches that are marked so: the parts run at once out of one instruction cache.
 //
 // The items in (sequence, kv head, row) order are dealt to the CTAs in runs of equal
 // weight: a step counts 1, an item kItemCost besides. Items that a run's end cuts leave
@@ -172,14 +155,10 @@ constexpr size_t kSmemBytes = offsetof(WindowSmem, abort) + sizeof(int) + 1024; 
 static_assert(kSmemBytes <= 232448, "window attention shared memory over budget");
 
 // ---- waits -----------------------------------------------------------------------
-// wait_for with all but the first try out of line.
-__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort)
-{
-    return wait_for(bar, parity, err, code, abort);
-}
+// wait_for with all but the first try marked as rare.
 __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, int* err, int code, volatile int* abort)
 {
-    return __builtin_expect(mbar_try_wait(bar, parity), 1) || wait_on(bar, parity, err, code, abort);
+    return __builtin_expect(mbar_try_wait(bar, parity), 1) || wait_for(bar, parity, err, code, abort);
 }
 
 // ---- the schedule -----------------------------------------------------------------
@@ -686,11 +665,18 @@ __device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, uint32_t tmem,
     __syncwarp();
 }
 
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, const void* src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 // Q rows (128-byte swizzled), q_scale and v_scale of each item.
 __device__ void q_loader(WindowSmem& sm, const WindowParams& p, int lane)
 {
     Seg s;
     SegReader segs;
+    const int step_t = 4 / p.G, step_h = 4 - step_t * p.G;
+    const int64_t step = (static_cast<int64_t>(step_t) * p.NQ + step_h) * kD, wrap = static_cast<int64_t>(p.NQ - p.G) * kD;
     for (int item = 0; segs.next(sm, p, s, lane); ++item) {
         const int buf = item & 1;
         if (!__all_sync(0xffffffffu, await(&sm.q_empty, (item & 1) ^ 1, p.err, 1024, &sm.abort))) break;
@@ -701,18 +687,31 @@ __device__ void q_loader(WindowSmem& sm, const WindowParams& p, int lane)
             const uint32_t n = rest + of, d = (n * p.g_mul) >> 22;
             return static_cast<int>(d * p.NQ + n - d * p.G);
         };
-        const uint8_t* const q = p.q + first * kD + 16 * (lane & 7);
-        // (a tile's rows, or the copies of fewer)
-        const int mask = s.x.rows > kTileRows ? ~0 : period - 1, tiles = s.x.rows > kTileRows ? 2 : 1;
-#pragma unroll 4
-        for (int i = 0; i < 32 * tiles; ++i) {
-            const int r = 4 * i + (lane >> 3), of = r & mask;
-            const bool in = of < s.x.rows;
-            cp_async16(sm.q + sw128(r, lane & 7), q + (in ? row_of(of) * kD : 0), in ? 16 : 0);
+        // Four rows at once, a unit of 16 bytes a lane: the next four lie step further, or
+        // that and wrap where the lane's row is another token's. (A tile's rows or two's, or
+        // the copies of fewer.)
+        const int l3 = lane >> 3, u = lane & 7, once = s.x.rows > kTileRows ? kItemRows : period;
+        const uint32_t to = smem_u32(sm.q) + 128 * l3 + 16 * (u ^ l3);
+#pragma unroll 1
+        for (int r0 = 0; r0 < max(once, kTileRows); r0 += once) {
+            const uint8_t* src = p.q + (first + row_of(l3)) * kD + 16 * u;
+            int h = rest + l3;
+            h -= static_cast<int>((static_cast<uint32_t>(h) * p.g_mul) >> 22) * p.G;
+#pragma unroll 2
+            for (int r = 0; r < once; r += 4) {
+                const bool in = r + l3 < s.x.rows;
+                cp_async16_at(to + 128 * (r0 + r) ^ (16 * (r & 4)), in ? src : p.q, in ? 16 : 0);
+                src += step;
+                h += step_h;
+                if (h >= p.G) {
+                    h -= p.G;
+                    src += wrap;
+                }
+            }
         }
 #pragma unroll 1
-        for (int r = lane; r < kTileRows * tiles; r += 32) {
-            const int of = r & mask;
+        for (int r = lane; r < max(once, kTileRows); r += 32) {
+            const int of = r & (once - 1);
             cp_async4(&sm.qs[buf][r], p.q_scale + first + (of < s.x.rows ? row_of(of) : 0), 4);
         }
         cp_async16(&sm.vs[buf][4 * lane], p.v_scale + (static_cast<int64_t>(s.b) * p.NKV + s.h) * kD + 4 * lane, 16);
@@ -727,7 +726,7 @@ __device__ void q_loader(WindowSmem& sm, const WindowParams& p, int lane)
 __device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1); }
 
 // Columns [0, 16 n) of tensor memory times f: floats, or (halves) pairs of FP16.
-__device__ __noinline__ void scale_columns(uint32_t taddr, int n, float f, bool halves)
+__device__ __forceinline__ void scale_columns(uint32_t taddr, int n, float f, bool halves)
 {
 #pragma unroll 1
     for (int c = 0; c < n; ++c) {
