@@ -13,8 +13,9 @@
 //   O += FP16(P) V                    tcgen05 kind::f16, P from tensor memory
 //   out = BF16(O v_scale / L)
 //
-// The numbers are tree.cu's: P in FP16 (half a step 2^-11), V's codes as FP16 exactly,
-// m raised only when a block's maximum lies more than 2^8 above it.
+// The numbers are tree.cu's: P in FP16 (half a step 2^-11), V's codes as FP16 exactly. m
+// is raised only where P would leave FP16: the sum of a thread's 32 P, which it forms
+// anyhow, tells (2^15 at most); no maximum is looked up but then and at an item's begin.
 //
 // Two softmax warpgroups, each with an S and an O of its own in tensor memory (2 x 128
 // + 2 x 128 columns); P lies over its S's columns. A step is one tile of 128 rows and a
@@ -39,8 +40,25 @@
 // quarters: with one copy three of a warpgroup's four warps would have no rows. The copies
 // have an O, an m and an l of their own and are joined with the warpgroups' at the end.
 //
-// Loops are rolled (32 scores at a time under a running maximum) and what is rare lies
-// behind branches that are marked so: the parts run at once out of one instruction cache.
+// Loops are rolled (32 scores at a time) and what is rare lies behind branches that are
+// marked so: the parts run at once out of one instruction cache.
+//
+// What bounds it, on 152 SMs: prompts, the softmax warps' instructions. A step of 128 x 128
+// takes a warpgroup 2500 clocks of softmax (the four warps on a quarter of the SM issue in
+// 42% of the clocks, packed FP32 operations in two clocks each, exponentials in four) and
+// 1300 of waiting for P V and the next S, so that with two in flight the tensor core has
+// work 40% of the time. Two prompts of 5000 tokens, 8 x 12 heads, window 4096: 687 us
+// (1.1 PFLOP/s); with a maximum of every 32 scores 747. Six chunks of up to 509 tokens
+// beside 31 decoding requests, window 1000: 180 us; of an item's 37000 clocks 10000 go to its
+// begin, its last P V and its output. Tried and slower (against what was best then): steps
+// of 64 keys (905 to 780), S in halves with the first ahead of P V (709 to 697), scores of the
+// next 32 keys loaded ahead (868 to 747), two threads a row (946 to 780), loops unrolled by two
+// (707 to 697), four rows and a quarter of the columns a thread, so that a key scale serves
+// four scores (766 to 758, decoding 163 to 120), eight more warps for the output (804 to 688).
+// Decoding, the blocks' reads: 64 requests of 8 x 12 heads, window 4096, 550 MB in 117 us
+// (114 in a graph, 4.8 TB/s), four requests of 110000 tokens 171 us (5.5 TB/s); an item ends
+// with 10000 clocks in which only the next three blocks are read. One token of one request:
+// 14.4 us, 12.3 in a graph, launches, schedule and one pass through every part.
 //
 // The items in (sequence, kv head, row) order are dealt to the CTAs in runs of equal
 // weight: a step counts 1, an item kItemCost besides. Items that a run's end cuts leave
