@@ -1047,7 +1047,8 @@ class WindowWorkspace:
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device or "cuda")
 
     def error_flags(self) -> int:
-        """Non-zero if a kernel wait gave up (bitmask of the wait sites)."""
+        """Non-zero if a kernel wait gave up (bitmask of the wait sites) or cu_tokens
+        decreased (bit 16384)."""
         return int(self.buf[:4].view(_torch().int32).item())
 
     def clear_error_flags(self) -> None:

@@ -669,6 +669,19 @@ extern "C" pa_status pa_token_logprobs(const void* logits, int dtype, int64_t ro
                    aligned(top_logprobs, 4),
                PA_ERR_INVALID, "%s: misaligned pointer", name);
     if (num_rows == 0) return PA_OK;
+    // (rows are read while others' results are already written, and read again)
+    struct Range { const void* at; uint64_t bytes; };
+    const uint64_t r4 = 4ull * num_rows;
+    const Range in[] = {{logits, ((num_rows - 1) * static_cast<uint64_t>(row_stride) + V) * (dtype == PA_DTYPE_F32 ? 4 : 2)},
+                        {tokens, r4 * (token_type == PA_INDEX_I64 ? 2 : 1)}};
+    const Range out[] = {{logprobs, r4}, {ranks, ranks ? r4 : 0}, {entropy, entropy ? r4 : 0},
+                         {top_ids, top ? r4 * top : 0}, {top_logprobs, top ? r4 * top : 0}};
+    for (const Range& o : out) {
+        for (const Range& i : in)
+            PA_REQUIRE(!overlap(o.at, o.bytes, i.at, i.bytes), PA_ERR_INVALID, "%s: an output overlaps an input", name);
+        for (const Range& i : out)
+            PA_REQUIRE(&i == &o || !overlap(o.at, o.bytes, i.at, i.bytes), PA_ERR_INVALID, "%s: outputs overlap", name);
+    }
     const int sms = device_sm_count();
     PA_REQUIRE(sms > 0, PA_ERR_CUDA, "%s: cannot query the device", name);
     LogprobParams p;

@@ -328,15 +328,18 @@ __device__ __forceinline__ Sequence sequence(const WindowParams& p, int b)
     return s;
 }
 
-// Fills the schedule's arrays; the weight of all kv heads, and the items an entry.
+// Fills the schedule's arrays; the weight of all kv heads, and the items an entry. 0 where
+// cu_tokens decreases somewhere: rows would be counted twice, and the sums pass 32 bits.
 __device__ uint32_t build_schedule(WindowSmem& sm, const WindowParams& p, int tid, int& group)
 {
     constexpr int kSeqs = (kMaxB + kThreads - 1) / kThreads;
     int items = 0;
+    bool decreases = false;
 #pragma unroll
     for (int j = 0; j < kSeqs; ++j) {
         const int b = tid * kSeqs + j;
         if (b >= p.B) break;
+        decreases = decreases || __ldg(p.cu + b + 1) < __ldg(p.cu + b);
         const Sequence s = sequence(p, b);
         sm.pos[b] = s.pos;
         sm.tok[b] = s.tok + s.skip;
@@ -368,7 +371,10 @@ __device__ uint32_t build_schedule(WindowSmem& sm, const WindowParams& p, int ti
         }
         if (tid == 0) sm.first[p.B] = entries;
     }
-    __syncthreads();
+    if (__syncthreads_or(decreases)) {
+        if (tid == 0) atomicOr(p.err, 16384);
+        return 0;
+    }
     uint32_t mine = 0;
     // thread i takes entries per i, per i + 1, .. and sums up its own
     const int per = (static_cast<int>(entries) + kThreads - 1) / kThreads;
@@ -1311,6 +1317,14 @@ extern "C" pa_status pa_fp8_window_attention(const void* q, const float* q_scale
                workspace ? workspace_bytes : static_cast<size_t>(0), need);
     PA_REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, PA_ERR_INVALID,
                "%s: workspace must be 256-byte aligned", name);
+    // every CTA reads while others already write
+    struct Range { const void* at; uint64_t bytes; };
+    const uint64_t codes = static_cast<uint64_t>(num_tokens) * NQ * kD, cache = static_cast<uint64_t>(num_blocks) * kBS * NKV * kD;
+    const Range in[] = {{q, codes}, {q_scale, codes / kD * 4}, {k_cache, cache}, {k_scale, cache / kD * 4},
+                        {v_cache, cache}, {v_scale, 4ull * B * NKV * kD}, {block_table, 4ull * B * max_blocks_per_seq},
+                        {kv_act_seqs, 4ull * B}, {cu_tokens, 4ull * (B + 1)}};
+    for (const Range& i : in)
+        PA_REQUIRE(!overlap(out, 2 * codes, i.at, i.bytes), PA_ERR_INVALID, "%s: out overlaps an input", name);
     const int sms = device_sm_count();
     PA_REQUIRE(sms > 0, PA_ERR_CUDA, "%s: cannot query the device", name);
     CUtensorMap tk, tv;

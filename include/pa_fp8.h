@@ -750,9 +750,11 @@ PA_API pa_status pa_plan_batch(const int32_t* kv_act_seqs, const int32_t* new_le
  * with M the maximum of the row's S_j; P = exp(S - M) enters the second
  * contraction as FP16, as pa_fp8_tree_decode's.
  * window       0: no window, all keys j <= p. sinks: 0 or more.
- * cu_tokens    int32 [B + 1], not decreasing, from 0; values are clamped to
- *              [0, num_tokens]. Rows of out behind cu_tokens[B] stay as they
- *              were.
+ * cu_tokens    int32 [B + 1], not decreasing, from 0 (where it decreases, bit
+ *              16384 of the error word is set and out is undefined); values are
+ *              clamped to [0, num_tokens]. Rows of out behind cu_tokens[B] stay
+ *              as they were.
+ * out          overlaps no input (PA_ERR_INVALID).
  * max_tokens   the most tokens a sequence has; of one that has more, those
  *              behind the first max_tokens get zeros.
  * Rows whose position is negative (more tokens than kv_act_seqs[b]) get zeros.
@@ -806,6 +808,7 @@ PA_API pa_status pa_fp8_window_attention(const void* q, const float* q_scale, co
  * ranks, entropy  int32 and float [num_rows], or NULL.
  * top          0 to 32 (more: PA_ERR_UNSUPPORTED) and at most V; top_ids int32,
  *              top_logprobs float [num_rows, top] (not used with 0).
+ * Outputs overlap neither an input nor one another (PA_ERR_INVALID).
  * ------------------------------------------------------------------------ */
 PA_API pa_status pa_token_logprobs(const void* logits, int dtype, int64_t row_stride, const void* tokens,
                                    int token_type, int64_t num_rows, int V, float* logprobs,

@@ -136,6 +136,20 @@ def test_window_attention_lengths_out_of_order(most):
     check_window(c, run_window(c))
 
 
+@pytest.mark.parametrize("most", [5, 400])
+def test_window_attention_refuses_rows_that_decrease(most):
+    """A bit of the error word, no more; the next call is not touched by it."""
+    c = R.window_case(12, [300, 900, 20], [2, 5, 1], 8, 2, 0, None, 0)
+    c["max_tokens"] = most
+    g = _cuda(c)
+    ws, out = workspace(g), empty_out(g)
+    for cu in ([0, 8, 3, 8], [0, 8, 0, 8], [9, 7, 7, 8], [0, -2 ** 31, 2 ** 31 - 1, 0]):
+        window_call({**g, "cu": _i32(*cu)}, out, ws)
+        assert ws.error_flags() == 16384
+        ws.clear_error_flags()
+    check_window(c, run_window(c, ws))
+
+
 def test_window_attention_bad_block_ids_read_block_zero():
     c = R.window_case(11, [300, 200], [2, 1], 8, 2, 0, None, 0)
     c["bt"][0, 1], c["bt"][1, 0] = -3, c["kc"].shape[0]

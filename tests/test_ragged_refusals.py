@@ -89,6 +89,11 @@ def test_window_attention_refusals(L):  # noqa: F811
         assert call(**bad) == 5, bad
     assert call(ws=None) == 3
     assert call(wsb=small - 1) == 3 and b"needed" in L.pa_last_error()
+    apart = {k: P((i + 1) << 36) for i, k in enumerate("q qs kc ks vc vs bt act cu out".split())}
+    for k, size in dict(q=20 * 96 * 128, qs=20 * 96 * 4, kc=16 * 8 * 128 ** 2, ks=16 * 8 * 128 * 4, vc=16 * 8 * 128 ** 2,
+                        vs=4 * 8 * 128 * 4, bt=64, act=16, cu=20).items():
+        for at in (apart[k].value + size - 4 & ~15, apart[k].value - 20 * 96 * 256 + 16):
+            assert call(**{**apart, "out": P(at)}) == 2 and b"overlaps" in L.pa_last_error(), k
 
 
 def test_token_logprobs_refusals(L):  # noqa: F811
@@ -106,6 +111,12 @@ def test_token_logprobs_refusals(L):  # noqa: F811
         assert call(**bad) == 2, bad
     for bad in (dict(k=33), dict(V=(1 << 31) - 1, step=1 << 40), dict(R=1 << 40)):
         assert call(**bad) == 5, bad
+    apart = {k: P((i + 1) << 36) for i, k in enumerate("x tok lp rank ent ids tlp".split())}
+    for k, size in dict(x=4 * (3 * 1000 + 1000) // 2, tok=16, lp=16, rank=16, ent=16, ids=80, tlp=80).items():
+        for o, n in dict(lp=16, rank=16, ent=16, ids=80, tlp=80).items():
+            if o != k:
+                for at in (apart[k].value + size - 4, apart[k].value - n + 4):
+                    assert call(**{**apart, o: P(at)}) == 2 and b"overlap" in L.pa_last_error(), (k, o)
 
 
 def test_binding_refuses_wrong_shapes_and_host_tensors(L, monkeypatch):  # noqa: F811
