@@ -35,7 +35,8 @@
 // reading and order, every instruction of which runs once and out of a cold cache (250 rows
 // x 131072 BF16 with 20 alternatives 26 us, without 20; 38 such rows 14.4; one row of 32003
 // FP32 with 5 alternatives 8.3, 6.5 in a graph). Rows cut over clusters at any number of
-// rows cost more in joins than they balance (250 rows on 2, 4 and 8 CTAs 37, 60, 108 us).
+// rows cost more in joins than they balance (250 rows on 2, 4 and 8 CTAs 37, 60, 108 us, when
+// one took 29).
 #include "common.cuh"
 
 #include <cooperative_groups.h>
