@@ -43,22 +43,24 @@
 // Loops are rolled (32 scores at a time) and what is rare lies behind branches that are
 // marked so: the parts run at once out of one instruction cache.
 //
-// What bounds it, on 152 SMs: prompts, the softmax warps' instructions. A step of 128 x 128
-// takes a warpgroup 2500 clocks of softmax (the four warps on a quarter of the SM issue in
-// 42% of the clocks, packed FP32 operations in two clocks each, exponentials in four) and
-// 1300 of waiting for P V and the next S, so that with two in flight the tensor core has
-// work 40% of the time. Two prompts of 5000 tokens, 8 x 12 heads, window 4096: 687 us
-// (1.1 PFLOP/s); with a maximum of every 32 scores 747. Six chunks of up to 509 tokens
-// beside 31 decoding requests, window 1000: 180 us; of an item's 37000 clocks 10000 go to its
-// begin, its last P V and its output. Tried and slower (against what was best then): steps
-// of 64 keys (905 to 780), S in halves with the first ahead of P V (709 to 697), scores of the
-// next 32 keys loaded ahead (868 to 747), two threads a row (946 to 780), loops unrolled by two
-// (707 to 697), four rows and a quarter of the columns a thread, so that a key scale serves
-// four scores (766 to 758, decoding 163 to 120), eight more warps for the output (804 to 688).
-// Decoding, the blocks' reads: 64 requests of 8 x 12 heads, window 4096, 550 MB in 117 us
-// (114 in a graph, 4.8 TB/s), four requests of 110000 tokens 171 us (5.5 TB/s); an item ends
+// What bounds it, on 152 SMs: prompts, the chain of a step's hand-overs and the softmax
+// warps' part of it. A step of 128 x 128 takes a warpgroup 2500 clocks for its P (1700 with
+// nothing else on the SM; 1140 if the other warpgroup rests, too), 700 of waiting for P V and
+// the next S and 400 around them, so that with two in flight the tensor core has work 42% of
+// the time. Without the exponentials it would be 3% faster, without V's conversion 5%,
+// without the key scales 6%. Two prompts of 5000 tokens, 8 x 12 heads, window 4096: 609 us
+// (1.28 PFLOP/s); with a maximum of every 32 scores 747, before what need not wait for S or P
+// was put ahead of those waits 687. Six chunks of up to 509 tokens beside 31 decoding
+// requests, window 1000: 166 us; of an item's 34000 clocks 10000 go to its begin, its last P V
+// and its output. Tried and slower (against what was best then): steps of 64 keys (905 to 780),
+// S in halves with the first ahead of P V (709 to 697), scores of the next 32 keys loaded ahead
+// (868 to 747), key scales of the next 32 (666 to 650), two threads a row (946 to 780), loops
+// unrolled by two (707 to 697), four rows and a quarter of the columns a thread, so that a key
+// scale serves four scores (680 to 609), eight more warps for the output (804 to 688).
+// Decoding, the blocks' reads: 64 requests of 8 x 12 heads, window 4096, 550 MB in 115 us
+// (113 in a graph, 4.9 TB/s), four requests of 110000 tokens 171 us (5.5 TB/s); an item ends
 // with 10000 clocks in which only the next three blocks are read. One token of one request:
-// 14.4 us, 12.3 in a graph, launches, schedule and one pass through every part.
+// 14.4 us, 12.2 in a graph, launches, schedule and one pass through every part.
 //
 // The items in (sequence, kv head, row) order are dealt to the CTAs in runs of equal
 // weight: a step counts 1, an item kItemCost besides. Items that a run's end cuts leave
@@ -608,42 +610,50 @@ __device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, uint32_t tmem,
         k = 0;
     };
     enter();
+    // whether what the next step's S needs is there (the whole warp)
+    auto have_s = [&] {
+        return more && __all_sync(0xffffffffu, (k > 0 || mbar_test(&sm.q_full, (segs.i - 1) & 1)) &&
+                                                   mbar_test(&sm.k_full[block % kSStages], (block / kSStages) & 1));
+    };
+    // it, by one thread
+    auto issue_s = [&] {
+        const uint32_t w = a & 1, kslot = block % kKStages;
+        const uint64_t qd = q0 + (pair && (k & 1) ? kTile / 16 : 0), kd = k0 + kslot * (kTile / 16);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + kSCol + kBS * w, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
+        umma_commit(&sm.s_full[w]);
+        if (!pair || (k & 1)) umma_commit(&sm.k_empty[kslot]);
+        if (k + 1 == steps) umma_commit(&sm.q_empty);
+    };
+    auto advance_s = [&] {
+        const bool block_ends = !pair || (k & 1);
+        const uint32_t f = (k < 2 ? 1 : 0) | (k + 2 >= steps ? 2 : 0) | (block_ends ? 4 : 0);
+        if (a & 1) {
+            block_of[1] = block;
+            flags[1] = f;
+        } else {
+            block_of[0] = block;
+            flags[0] = f;
+        }
+        ++a;
+        if (block_ends) ++block;
+        if (++k == steps) enter();
+        idle = 0;
+    };
 #pragma unroll 1
     while (more || o < a) {
         ++idle;
-        if (more && a < o + 2) {
-            const bool ready = (k > 0 || mbar_test(&sm.q_full, (segs.i - 1) & 1)) &&
-                               mbar_test(&sm.k_full[block % kSStages], (block / kSStages) & 1);
-            if (__all_sync(0xffffffffu, ready)) {
-                const uint32_t w = a & 1, kslot = block % kKStages;
-                const bool block_ends = !pair || (k & 1), ends = k + 1 == steps;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t qd = q0 + (pair && (k & 1) ? kTile / 16 : 0), kd = k0 + kslot * (kTile / 16);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + kSCol + kBS * w, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
-                    umma_commit(&sm.s_full[w]);
-                    if (block_ends) umma_commit(&sm.k_empty[kslot]);
-                    if (ends) umma_commit(&sm.q_empty);
-                }
-                __syncwarp();
-                const uint32_t f = (k < 2 ? 1 : 0) | (k + 2 >= steps ? 2 : 0) | (block_ends ? 4 : 0);
-                if (w) {
-                    block_of[1] = block;
-                    flags[1] = f;
-                } else {
-                    block_of[0] = block;
-                    flags[0] = f;
-                }
-                ++a;
-                ++k;
-                if (block_ends) ++block;
-                if (ends) enter();
-                idle = 0;
-            }
+        if (a < o + 2 && have_s()) {
+            tc_fence_after();
+            if (elect_one()) issue_s();
+            __syncwarp();
+            advance_s();
         }
         if (o < a) {
             const uint32_t w = o & 1, blk = w ? block_of[1] : block_of[0], f = w ? flags[1] : flags[0], hslot = blk % kHStages;
+            // (the S after next follows at once where its operands are there by now: looking for
+            // them behind P costs 6% of a prompt)
+            const bool ahead = a == o + 2 && have_s();
             bool ready;
             if (more && a < o + 2)           // (S is waiting for Q or K, too)
                 ready = mbar_test(&sm.p_full[w], (o >> 1) & 1) && mbar_test(&sm.h_full[hslot], (blk / kHStages) & 1);
@@ -660,10 +670,12 @@ __device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, uint32_t tmem,
                                     (!(f & 1) || kk > 0) ? 1u : 0u);
                     if (f & 4) umma_commit(&sm.h_empty[hslot]);
                     if (f & 2) umma_commit(&sm.o_full[w]);
+                    if (ahead) issue_s();
                 }
                 __syncwarp();
                 ++o;
                 idle = 0;
+                if (ahead) advance_s();
             }
         }
         // the clock is read every 4096 fruitless polls
@@ -817,21 +829,23 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
         for (int k = k_first; k < steps; k += 2, ++turn) {
             const int t = pair ? k >> 1 : k;
             const uint32_t at = block0 + t;
-            await(&sm.s_full[w], turn & 1, p.err, 64, &sm.abort);
             if (__builtin_expect(!warp_live, 0)) {   // a warp without rows keeps the others company
+                await(&sm.s_full[w], turn & 1, p.err, 64, &sm.abort);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.p_full[w]);
                 continue;
             }
+            // (all that does not wait for S; behind it, it costs 6% of a prompt)
             await(&sm.k_full[at % kSStages], (at / kSStages) & 1, p.err, 64, &sm.abort);
-            __syncwarp();
-            tc_fence_after();
             const float4* ks = reinterpret_cast<const float4*>(sm.ks[at % kSStages]);
             // keys up to the row's own (end), and of those its window's (from begin) and the
             // sinks (below sink); whether any row does not see all
             const int k0 = block_at(s.x, s.t0 + t) * kBS, sink = p.sinks - k0;
             const bool part_seen = s.x.first - k0 < kBS - 1 || (s.x.last - k0 >= p.window && sink < kBS);
             const int end = pos + 1 - k0, begin = end - p.window;
+            await(&sm.s_full[w], turn & 1, p.err, 64, &sm.abort);
+            __syncwarp();
+            tc_fence_after();
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
             for (int c = c0; c < c1; ++c) {
@@ -906,7 +920,6 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
                 sum = __fadd2_rn(sum, part);
                 tmem_st16(S + kChunk / 2 * c, hp);
             }
-            l += sum.x + sum.y;
             // the other copies' keys
             if (copies > 1) {
                 uint32_t zero[kChunk / 2];
@@ -920,20 +933,25 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.p_full[w]);
+            l += sum.x + sum.y;
         }
         // ---- the item's (or its part's) output ----
-        if (k_first < steps) {
-            await(&sm.o_full[w], outs & 1, p.err, 128, &sm.abort);
-            ++outs;
-        }
         const bool whole = s.t0 == 0 && s.t1 == s.x.blocks;
         float* const part = part_of(p, blockIdx.x, s.first_of_run);
         float* const part_ml = part + static_cast<int64_t>(p.part_rows) * kD;
-        __syncwarp();
-        tc_fence_after();
+        // (behind all that does not need O)
+        auto o_complete = [&] {
+            if (k_first < steps) {
+                await(&sm.o_full[w], outs & 1, p.err, 128, &sm.abort);
+                ++outs;
+            }
+            __syncwarp();
+            tc_fence_after();
+        };
         if (pair) {
             const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
             const int64_t at = q_row(p, s.tok, s.h, s.x.row0 + (live ? row : 0)) * kD;
+            o_complete();
 #pragma unroll 1
             for (int c = 0; c < kD && warp_live; c += 16) {
                 __syncwarp();                // (rows behind the last one store nothing)
@@ -994,6 +1012,9 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
                     part_ml[p.part_rows + row] = lt;
                 }
             }
+            // (both warpgroups' O, which every thread reads)
+            o_complete();
+            sync_all();
             // a lane's units of four channels (8 or 16 of them), and its place in the buffer
             const int units = 8 << narrow, lane_at = narrow ? 16 * q4 + (lane & 15) : trow;
             const int tid = w * kTileRows + trow, j = tid & (units - 1);
