@@ -45,22 +45,25 @@
 //
 // What bounds it, on 152 SMs: prompts, the chain of a step's hand-overs and the softmax
 // warps' part of it. A step of 128 x 128 takes a warpgroup 2500 clocks for its P (1700 with
-// nothing else on the SM; 1140 if the other warpgroup rests, too), 700 of waiting for P V and
-// the next S and 400 around them, so that with two in flight the tensor core has work 42% of
-// the time. Without the exponentials it would be 3% faster, without V's conversion 5%,
-// without the key scales 6%. Two prompts of 5000 tokens, 8 x 12 heads, window 4096: 609 us
-// (1.28 PFLOP/s); with a maximum of every 32 scores 747, before what need not wait for S or P
-// was put ahead of those waits 687. Six chunks of up to 509 tokens beside 31 decoding
-// requests, window 1000: 166 us; of an item's 34000 clocks 10000 go to its begin, its last P V
-// and its output. Tried and slower (against what was best then): steps of 64 keys (905 to 780),
-// S in halves with the first ahead of P V (709 to 697), scores of the next 32 keys loaded ahead
-// (868 to 747), key scales of the next 32 (666 to 650), two threads a row (946 to 780), loops
-// unrolled by two (707 to 697), four rows and a quarter of the columns a thread, so that a key
-// scale serves four scores (680 to 609), eight more warps for the output (804 to 688).
-// Decoding, the blocks' reads: 64 requests of 8 x 12 heads, window 4096, 550 MB in 115 us
-// (113 in a graph, 4.9 TB/s), four requests of 110000 tokens 171 us (5.5 TB/s); an item ends
-// with 10000 clocks in which only the next three blocks are read. One token of one request:
-// 14.4 us, 12.2 in a graph, launches, schedule and one pass through every part.
+// nothing else on the SM; 1140 if the other warpgroup rests, too), 700 of waiting for P V
+// and the next S and 400 around them, so that with two in flight the tensor core has work
+// 42% of the time. Without the exponentials it would be 3% faster, without V's conversion
+// 5%, without the key scales 6%. Two prompts of 5000 tokens, 8 x 12 heads, window 4096: 612
+// us (1.27 PFLOP/s); with a maximum of every 32 scores 747, before what need not wait for S
+// or P was put ahead of those waits 687. Six chunks of up to 509 tokens beside 31 decoding
+// requests, window 1000: 156 us (166 before the parts of a window's first and last blocks
+// and of the sinks' that no row sees were left out); of an item's 32000 clocks 10000 go to
+// its begin, its last P V and its output. Tried and slower (against what was best then):
+// steps of 64 keys (905 to 780), S in halves with the first ahead of P V (709 to 697),
+// scores of the next 32 keys loaded ahead (868 to 747), key scales of the next 32 (666 to
+// 650), two threads a row (946 to 780), loops unrolled by two (707 to 697), four rows and a
+// quarter of the columns a thread, so that a key scale serves four scores (680 to 609),
+// eight more warps for the output (804 to 688), an issuing warp for each warpgroup (744 to
+// 609, taking turns 685), other K and V rings (the same). Decoding, the blocks' reads: 64
+// requests of 8 x 12 heads, window 4096, 550 MB in 115 us (113 in a graph, 4.9 TB/s), four
+// requests of 110000 tokens 171 us (5.5 TB/s); an item ends with 10000 clocks in which only
+// the next three blocks are read. One token of one request: 14.4 us, 12.2 in a graph,
+// launches, schedule and one pass through every part.
 //
 // The items in (sequence, kv head, row) order are dealt to the CTAs in runs of equal
 // weight: a step counts 1, an item kItemCost besides. Items that a run's end cuts leave
@@ -216,6 +219,20 @@ struct Run {
 __device__ __forceinline__ int block_at(const Item& x, int t)
 {
     return t < x.sink_blocks ? t : x.lo + t - x.sink_blocks;
+}
+
+// Chunks [a, b) of an item's block t that any of its rows sees: the others take no part.
+// (In the two blocks at a window's ends half of the keys on average, of a few sinks one
+// chunk: a window of 1000 of 10 blocks.)
+struct Span {
+    int a, b;
+};
+__device__ __forceinline__ Span chunks_of(const WindowParams& p, const Item& x, int t)
+{
+    const int k0 = block_at(x, t) * kBS, sink = p.sinks - k0;
+    const int begin = sink > 0 ? 0 : max(x.first - p.window + 1 - k0, 0);
+    const int end = t < x.sink_blocks ? sink : x.last + 1 - k0;
+    return {begin / kChunk, min((end + kChunk - 1) / kChunk, kBS / kChunk)};
 }
 
 // blocks of an item before position `off` behind its first one
@@ -599,11 +616,12 @@ __device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, uint32_t tmem,
     uint32_t k = 0, steps = 0, a = 0, block = 0, o = 0;
     bool pair = false, more = true;
     // of the steps whose S is issued and whose P V is not: its block, 1: the item's first of
-    // the warpgroup, 2: its last, 4: the block's last
+    // the warpgroup, 2: its last, 4: the block's last, 8: not all
+    // of its chunks but 16 and 64 times those from and to
     uint32_t block_of[2] = {0, 0}, flags[2] = {0, 0};
     uint32_t idle = 0, t0 = 0;
+    Seg s;
     auto enter = [&] {
-        Seg s;
         more = segs.next(sm, p, s, lane);
         pair = s.x.rows > kTileRows;
         steps = (s.t1 - s.t0) * (pair ? 2 : 1);
@@ -627,7 +645,12 @@ __device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, uint32_t tmem,
     };
     auto advance_s = [&] {
         const bool block_ends = !pair || (k & 1);
-        const uint32_t f = (k < 2 ? 1 : 0) | (k + 2 >= steps ? 2 : 0) | (block_ends ? 4 : 0);
+        uint32_t f = (k < 2 ? 1 : 0) | (k + 2 >= steps ? 2 : 0) | (block_ends ? 4 : 0);
+        const int t = s.t0 + static_cast<int>(pair ? k >> 1 : k);
+        if (__builtin_expect(t <= s.x.sink_blocks || t + 1 == s.x.blocks, 0)) {
+            const Span span = chunks_of(p, s.x, t);
+            if (span.b - span.a < kBS / kChunk) f |= 8 | span.a << 4 | span.b << 6;
+        }
         if (a & 1) {
             block_of[1] = block;
             flags[1] = f;
@@ -664,10 +687,18 @@ __device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, uint32_t tmem,
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t vd = v0 + hslot * (2 * kTile / 16);
+                    // 16 keys: 8 columns of P, 2048 bytes of V
+                    auto add = [&](int kk, bool more) {
+                        umma_f16_ta(tmem + kD * w, tmem + kSCol + kBS * w + 8 * kk, vd + 128 * kk, kIdescO, more ? 1u : 0u);
+                    };
+                    if (__builtin_expect(!(f & 8), 1)) {
 #pragma unroll
-                    for (int kk = 0; kk < kBS / 16; ++kk)   // 16 keys: 8 columns of P, 2048 bytes of V
-                        umma_f16_ta(tmem + kD * w, tmem + kSCol + kBS * w + 8 * kk, vd + 128 * kk, kIdescO,
-                                    (!(f & 1) || kk > 0) ? 1u : 0u);
+                        for (int kk = 0; kk < kBS / 16; ++kk) add(kk, !(f & 1) || kk > 0);
+                    } else {
+                        const int k_a = 2 * (f >> 4 & 3), k_b = 2 * (f >> 6);
+#pragma unroll 1
+                        for (int kk = k_a; kk < k_b; ++kk) add(kk, !(f & 1) || kk > k_a);
+                    }
                     if (f & 4) umma_commit(&sm.h_empty[hslot]);
                     if (f & 2) umma_commit(&sm.o_full[w]);
                     if (ahead) issue_s();
@@ -843,12 +874,14 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
             const int k0 = block_at(s.x, s.t0 + t) * kBS, sink = p.sinks - k0;
             const bool part_seen = s.x.first - k0 < kBS - 1 || (s.x.last - k0 >= p.window && sink < kBS);
             const int end = pos + 1 - k0, begin = end - p.window;
+            const Span span = chunks_of(p, s.x, s.t0 + t);
+            const int ca = max(c0, span.a), cb = min(c1, span.b);
             await(&sm.s_full[w], turn & 1, p.err, 64, &sm.abort);
             __syncwarp();
             tc_fence_after();
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
-            for (int c = c0; c < c1; ++c) {
+            for (int c = ca; c < cb; ++c) {
                 float v[kChunk];
                 tmem_ld32(S + kChunk * c, v);
                 tmem_wait_ld();
@@ -902,7 +935,7 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
                         if (k > k_first) scale_columns(O, kD / 16, f, false);
                         // P of the block's keys so far
                         tmem_wait_st();
-                        if (c > c0) scale_columns(S + kChunk / 2 * c0, c - c0, f, true);
+                        if (c > ca) scale_columns(S + kChunk / 2 * ca, c - ca, f, true);
                     }
                     // Past 2^22 the rounding of m is no longer small beside the exponents, which
                     // take the products unrounded (one too large by 1 leaves FP16): there they are
@@ -926,7 +959,7 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
 #pragma unroll
                 for (int i = 0; i < kChunk / 2; ++i) zero[i] = 0;
 #pragma unroll 1
-                for (int c = 0; c < kBS / kChunk; ++c)
+                for (int c = span.a; c < span.b; ++c)
                     if (c < c0 || c >= c1) tmem_st16(S + kChunk / 2 * c, zero);
             }
             tmem_wait_st();
