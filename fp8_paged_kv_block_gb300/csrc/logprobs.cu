@@ -8,13 +8,15 @@
 // of 64 bytes a thread, and a cluster takes one row after another. A thread copies its
 // own pieces of the next three chunks, the next row's among them, to shared memory (so
 // that no barrier stands between a copy and its use), keeps its own m, l and s (FP32, a
-// few hundred terms each) and rescales them when its maximum grows; they are joined at
-// a row's end, over lanes, warps and the cluster's CTAs. A value's exponent is one
-// fused operation, x log2 e - c with c = m log2 e as rounded; what the rounding is off
-// by is one factor of 16 terms, taken out of their sum. (Past 2^10 that factor is no
-// longer near 1: there, and where a term is -inf, x - m is formed first.) The rank counts
-// signs of x_t - x, or pairs of BF16 ones, only where a thread's 16 values have a larger
-// one: a comparison and a sum for each took 250 rows x 131072 from 24.8 to 28.9 us.
+// few hundred terms each) and rescales them when a value passes m by more than kRaise (m
+// need not be the maximum, and in the first chunks some lane's grows nearly every time);
+// they are joined at a row's end, over lanes, warps and the cluster's CTAs. A value's
+// exponent is one fused operation, x log2 e - c with c = m log2 e as rounded; what the
+// rounding is off by is one factor of all terms since m last grew, taken out of their sums.
+// (Past 2^10 that factor is no longer near 1: there, and where a term is -inf, x - m is
+// formed first.) The rank counts signs of x_t - x, or pairs of BF16 ones, only where a
+// thread's 16 values have a larger one: a comparison and a sum for each took 250 rows x
+// 131072 from 24.8 to 28.9 us.
 //
 // Alternatives: a value and its index make a 64-bit key, larger for the larger
 // value and, among equal ones, for the lower index, so that no two are equal. The pass
@@ -29,11 +31,11 @@
 // it goes. -inf is never listed: where fewer than k values are finite the lowest indices
 // of the others follow.
 //
-// What bounds it: many rows, the reads (4096 rows x 50000 FP32 131 us, 6.3 TB/s; a copy's
+// What bounds it: many rows, the reads (4096 rows x 50000 FP32 129 us, 6.4 TB/s; a copy's
 // rate would take 121). A row a CTA, what stands around the reads: the two
 // loads of the token's logit, one behind the other, 2 us, and 5 us of joins, bound, second
 // reading and order, every instruction of which runs once and out of a cold cache (250 rows
-// x 131072 BF16 with 20 alternatives 26 us, without 20; 38 such rows 14.4; one row of 32003
+// x 131072 BF16 with 20 alternatives 25.5 us, without 20.5; 38 such rows 14.4; one row of 32003
 // FP32 with 5 alternatives 8.3, 6.5 in a graph). Rows cut over clusters at any number of
 // rows cost more in joins than they balance (250 rows on 2, 4 and 8 CTAs 37, 60, 108 us, when
 // one took 29).
@@ -59,6 +61,7 @@ constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
 constexpr int kList = 1024;                  // candidates
 constexpr int kShort = 256;                  // of which at most so many are put in order
+constexpr float kRaise = 8.0f;               // what values may pass the thread's m by
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeast = -0x1.fffffep127f;
@@ -396,6 +399,15 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
         const int64_t tok_next = token(row + step);
         Stats st = {-INFINITY, 0.0f, 0.0f, 0};            // (s in units of log2)
         float c_now = 0.0f, off = 0.0f;                  // c, and c - m log2 e
+        float most = -INFINITY, raise_at = -INFINITY;    // the thread's maximum; m + kRaise
+        float l_raw = 0.0f, s_raw = 0.0f;                // sums over c since m last grew
+        auto settle = [&] {
+            const float sum = l_raw;
+            st.l += fmaf(sum, off * kLn2, sum);
+            st.s += fmaf(off, fmaf(s_raw, kLn2, sum), s_raw);
+            l_raw = 0.0f;
+            s_raw = 0.0f;
+        };
 #pragma unroll 1
         for (uint32_t c = part.c0; c < part.c1; ++c) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
@@ -435,21 +447,24 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
                         st.above += static_cast<int>(__low2float(n2) + __high2float(n2));
                     }
                 }
-                const float m = fmaxf(st.m, mx);
-                if (m != st.m) {
+                most = fmaxf(most, mx);
+                if (mx > raise_at) {
+                    settle();
                     if (st.m != -INFINITY) {
-                        const float d = (st.m - m) * kLog2e, f = ex2(d);
+                        const float d = (st.m - mx) * kLog2e, f = ex2(d);
                         st.s = f == 0.0f ? 0.0f : (st.s + d * st.l) * f;
                         st.l *= f;
                     }
-                    st.m = m;
-                    c_now = m * kLog2e;
-                    off = fmaf(-m, kLog2e, c_now);
+                    st.m = mx;
+                    raise_at = mx + kRaise;
+                    c_now = mx * kLog2e;
+                    off = fabsf(mx) <= 1024.0f ? fmaf(-mx, kLog2e, c_now) : 0.0f;
                 }
-                float sum = 0.0f, dot = NAN;
-                if (fabsf(m) <= 1024.0f) {
+                float dot = NAN;
+                float2 l = make_float2(0.f, 0.f);
+                if (fabsf(st.m) <= 1024.0f) {
                     const float2 neg = make_float2(-c_now, -c_now), log2e = make_float2(kLog2e, kLog2e);
-                    float2 l = make_float2(0.f, 0.f), s = make_float2(0.f, 0.f);
+                    float2 s = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int e = 0; e < kPer; e += 2) {
                         const float2 y = __ffma2_rn(make_float2(w[e], w[e + 1]), log2e, neg);
@@ -457,33 +472,35 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
                         l = __fadd2_rn(l, x);
                         s = __ffma2_rn(y, x, s);
                     }
-                    sum = l.x + l.y;
                     dot = s.x + s.y;
-                    dot = fmaf(off, fmaf(dot, kLn2, sum), dot);
-                    sum = fmaf(sum, off * kLn2, sum);
                 }
-                if (dot != dot) {
+                if (dot == dot) {
+                    l_raw += l.x + l.y;
+                    s_raw += dot;
+                } else {
                     // past the range, or -inf among them, whose product with its weight
                     // of 0 is NaN. (One among the values makes both sums NaN.)
-                    const float ref = m == -INFINITY ? 0.0f : m;
-                    sum = dot = 0.0f;
+                    const float ref = st.m == -INFINITY ? 0.0f : st.m;
+                    float sum = 0.0f;
+                    dot = 0.0f;
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) {
                         const float y = (w[e] - ref) * kLog2e, x = ex2(y);
                         sum += x;
                         dot += x == 0.0f ? 0.0f : y * x;
                     }
+                    st.l += sum;
+                    st.s += dot;
                 }
-                st.l += sum;
-                st.s += dot;
             }
             slot = slot + kSlot == kStages * kSlot ? 0 : slot + kSlot;
             fetch();                         // (into the slot just read: this thread's own)
         }
+        settle();
         st.s *= kLn2;
         const float xt_next = logit(row + step, tok_next);
         // ---- this CTA's statistics and alternatives, to the cluster's first ----
-        const float mine = st.m;
+        const float mine = most;
         st = warp_join(st);
         if (lane == 0) sm.part[parity][warp] = st;
         if (TOP) {
