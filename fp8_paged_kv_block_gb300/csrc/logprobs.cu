@@ -402,11 +402,9 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
         float most = -INFINITY, raise_at = -INFINITY;    // the thread's maximum; m + kRaise
         float l_raw = 0.0f, s_raw = 0.0f;                // sums over c since m last grew
         auto settle = [&] {
-            const float sum = l_raw;
-            st.l += fmaf(sum, off * kLn2, sum);
-            st.s += fmaf(off, fmaf(s_raw, kLn2, sum), s_raw);
-            l_raw = 0.0f;
-            s_raw = 0.0f;
+            st.l += fmaf(l_raw, off * kLn2, l_raw);
+            st.s += fmaf(off, fmaf(s_raw, kLn2, l_raw), s_raw);
+            l_raw = s_raw = 0.0f;
         };
 #pragma unroll 1
         for (uint32_t c = part.c0; c < part.c1; ++c) {
