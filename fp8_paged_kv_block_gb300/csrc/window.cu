@@ -35,10 +35,11 @@
 // itself keeps them apart where they share columns, and an S that is complete says that
 // the warpgroup's last P V is.
 //
-// An item of at most 64 or 32 rows (a decoding request's: one token x the group) stands in
-// the tile twice or four times, and each copy's warps take the block's keys by halves or
-// quarters: with one copy three of a warpgroup's four warps would have no rows. The copies
-// have an O, an m and an l of their own and are joined with the warpgroups' at the end.
+// An item of at most 64 rows (a decoding request's: one token x the group) stands in the
+// tile twice, and either copy's warps take a half of the block's keys: with one copy most of
+// a warpgroup's warps would have no rows (64 decoding requests 127 us, against 116; four
+// copies for 32 rows 117). The copies have an O, an m and an l of their own and are joined
+// with the warpgroups' at the end.
 //
 // Loops are rolled (32 scores at a time) and what is rare lies behind branches that are
 // marked so: the parts run at once out of one instruction cache.
@@ -96,8 +97,10 @@ constexpr uint32_t kTmemCols = 512, kSCol = 2 * kD;   // O of either warpgroup, 
 constexpr float kShift = 7.0f;               // log2 units
 constexpr float kRaise = 3.0f;
 constexpr float kLimit = 0x1p15f;            // of a chunk's sum; one that passes it has a P of 2^(3 + 7)
-constexpr int kItemCost = 5;                 // what an item costs besides its steps, in steps (3 to 11 tried)
-constexpr int kMinRun = 2;                   // the shortest run (2 at least: describe_cut)
+constexpr int kItemCost = 5;                 // of an item besides its steps, in steps (3 to 11 tried)
+// The shortest run (2 at least: describe_cut). One token, 8 x 12 heads, window 1024: 16.5 us,
+// with 6 18.5, with 12 22.4.
+constexpr int kMinRun = 2;
 constexpr int kSegs = 4;                     // items ahead of the slowest part
 // Entries of the schedule in shared memory: an item each while the batch's number no
 // more than 512 a kv head, else 2, 4, .. one behind another.
@@ -129,11 +132,10 @@ struct WindowParams {
     int B, T, max_tokens, NQ, NKV, G;
     uint32_t g_mul;                          // 2^22 / G + 1: n / G = n g_mul >> 22 for n < 2^14
     uint64_t g_inv;                          // 2^64 / G + 1 (G > 1)
-    int one_item;                            // a sequence makes one item at most
+    int one_item;                            // a sequence makes one item at most (no scan: 14.4 us for 15.1)
     int64_t num_blocks;
     int max_blocks, layout, ctas;
     int window, sinks;
-    int keep_l2;                             // K/V blocks serve several items
     float scale_log2;
 };
 
@@ -204,7 +206,7 @@ __device__ __forceinline__ Item item_of(const WindowParams& p, int pos, int rows
     return x;
 }
 // copies of an item's rows in the tile
-__device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 4 : (rows <= 64 ? 2 : 1); }
+__device__ __forceinline__ int copies_of(int rows) { return rows <= kTileRows / 2 ? 2 : 1; }
 __device__ __forceinline__ int steps_a_block(int rows) { return rows > kTileRows ? 2 : 1; }
 __device__ __forceinline__ uint32_t weight_of(const Item& x) { return x.blocks * steps_a_block(x.rows) + kItemCost; }
 __device__ __forceinline__ int items_of(int rows) { return (rows + kItemRows - 1) / kItemRows; }
@@ -471,7 +473,7 @@ struct SegReader {
 
 __device__ void producer(WindowSmem& sm, const WindowParams& p, const CUtensorMap* tk, const CUtensorMap* tv, int lane)
 {
-    const uint64_t pol = p.keep_l2 ? l2_keep_policy() : l2_evict_first_policy();
+    const uint64_t pol = l2_evict_first_policy();   // (kept for the other items of a prompt: no faster)
     Seg s;
     int kc = 0, vc = 0;                      // blocks requested so far
     bool stop = false;
@@ -1023,13 +1025,13 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
             sm.m[w * kTileRows + trow] = m;
             sm.l[w * kTileRows + trow] = l;
             sync_all();
-            const int period = kTileRows / copies, narrow = s.x.rows <= 16 ? 1 : 0;
+            const int period = kTileRows / copies, narrow = s.x.rows <= 32 ? 1 : 0;
             float mf = -INFINITY, lt = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
                 if (i < 2 * copies) mf = fmaxf(mf, sm.m[(trow + i * period) & (2 * kTileRows - 1)]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 const int from = (trow + i * period) & (2 * kTileRows - 1);
                 if (i < 2 * copies && sm.l[from] != 0.0f)
                     lt += sm.l[from] * (sm.m[from] == mf ? 1.0f : ex2(sm.m[from] - mf));
@@ -1049,33 +1051,31 @@ __device__ void softmax(WindowSmem& sm, const WindowParams& p, uint32_t tmem, in
             o_complete();
             sync_all();
             // a lane's units of four channels (8 or 16 of them), and its place in the buffer
-            const int units = 8 << narrow, lane_at = narrow ? 16 * q4 + (lane & 15) : trow;
+            const int units = 8 << narrow, lane_at = narrow ? 32 * (q4 >> 1) + lane : trow;
             const int tid = w * kTileRows + trow, j = tid & (units - 1);
 #pragma unroll 1
             for (int c = 0; c < kD; c += 4 * units) {
 #pragma unroll 1
-                for (int u = w * units / 2; u < (w + 1) * units / 2; u += 4) {
+                for (int u = w * units / 2; u < (w + 1) * units / 2 && !(narrow && (q4 & 1)); u += 4) {
                     float x[16], y[16];
                     tmem_ld16(tmem + lanes + c + 4 * u, x);
                     tmem_ld16(tmem + lanes + kD + c + 4 * u, y);
                     tmem_wait_ld();
-                    if (!narrow || lane < 16) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = (has0 ? x[i] * f0 : 0.0f) + (has1 ? y[i] * f1 : 0.0f);
+                    for (int i = 0; i < 16; ++i) x[i] = (has0 ? x[i] * f0 : 0.0f) + (has1 ? y[i] * f1 : 0.0f);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)   // (a lane's units begin at another place each)
-                            sm.join[lane_at * units + ((u + i + lane_at) & (units - 1))] =
-                                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                    }
+                    for (int i = 0; i < 4; ++i)      // (a lane's units begin at another place each)
+                        sm.join[lane_at * units + ((u + i + lane_at) & (units - 1))] =
+                            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                 }
                 sync_all();
 #pragma unroll 1
                 for (int r = tid >> (3 + narrow); r < s.x.rows; r += 256 >> (3 + narrow)) {
                     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         if (i >= copies) break;
-                        const int from = r + (narrow ? 16 : period) * i;
+                        const int from = r + (narrow ? 32 : period) * i;
                         const float4 x = sm.join[from * units + ((j + from) & (units - 1))];
                         sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
                     }
@@ -1418,7 +1418,6 @@ extern "C" pa_status pa_fp8_window_attention(const void* q, const float* q_scale
     p.ctas = sms < kMaxCtas ? sms : kMaxCtas;
     p.window = win;
     p.sinks = first;
-    p.keep_l2 = static_cast<int64_t>(max_tokens) * G > kItemRows;
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
 
     cudaError_t e = cudaFuncSetAttribute(window_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
