@@ -559,6 +559,10 @@ __device__ void converter(WindowSmem& sm, const WindowParams& p, int w, int lane
                 uint4 x[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(src + 1024 * (i0 + i));
+                if (i0 > 0) {                // (all codes are read: the next block's may come, 2% of a long decode)
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.v_empty[vslot]);
+                }
                 if (!whole) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -578,10 +582,7 @@ __device__ void converter(WindowSmem& sm, const WindowParams& p, int w, int lane
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sm.h_full[hslot]);
-                mbar_arrive(&sm.v_empty[vslot]);
-            }
+            if (lane == 0) mbar_arrive(&sm.h_full[hslot]);
         }
     }
 }
