@@ -601,12 +601,13 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
     return ok != 0;
 }
 
-// The MMAs' warp; one elected thread issues. S of step j + 2 goes behind P V of step j;
-// which of the two goes next is whichever has its operands, so that an item's last P V do
-// not wait for the next one's Q. The warp polls only while it waits for either: a poll
-// takes issue slots from the softmax warps on the same quarter of the SM, and every step
-// needs all four of a warpgroup's (polling throughout, two prompts of 5000 tokens with
-// 8 x 12 heads took 836 us, against 758).
+// The MMAs' warp; one elected thread issues. P V of a step and S of the step after next,
+// which is the same warpgroup's, go one behind the other, so that the tensor core itself
+// keeps them apart where they share columns. It has at most a step's work ahead, so that
+// what this warp does between two steps is time that it idles, and a warp that polls takes
+// issue slots from the softmax warps on its quarter of the SM, which every step waits for:
+// nothing is polled (throughout, two prompts of 5000 tokens took 836 us, against 758), and
+// whether the next S's operands are there is looked up ahead of the wait for P.
 __device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, uint32_t tmem, int lane)
 {
     constexpr uint32_t kIdescS = idesc_e4m3(128, kBS, 0, 0);
@@ -614,119 +615,96 @@ __device__ void mma_issuer(WindowSmem& sm, const WindowParams& p, uint32_t tmem,
     const uint64_t q0 = smem_desc(smem_u32(sm.q), 16, 1024, kSmem128BSwizzle);
     const uint64_t k0 = smem_desc(smem_u32(sm.k[0]), 16, 1024, kSmem128BSwizzle);
     const uint64_t v0 = smem_desc(smem_u32(sm.vh[0][0]), kTile, 1024, kSmem128BSwizzle);
-    SegReader segs;
-    // S's item: steps behind and in all, whether of two tiles; steps and whole blocks behind
-    // in all; P V's steps
-    uint32_t k = 0, steps = 0, a = 0, block = 0, o = 0;
-    bool pair = false, more = true;
-    // of the steps whose S is issued and whose P V is not: its block, 1: the item's first of
-    // the warpgroup, 2: its last, 4: the block's last, 8: not all
-    // of its chunks but 16 and 64 times those from and to
-    uint32_t block_of[2] = {0, 0}, flags[2] = {0, 0};
-    uint32_t idle = 0, t0 = 0;
     Seg s;
-    auto enter = [&] {
-        more = segs.next(sm, p, s, lane);
-        pair = s.x.rows > kTileRows;
-        steps = (s.t1 - s.t0) * (pair ? 2 : 1);
-        k = 0;
+    SegReader segs;
+    uint32_t block0 = 0, step0 = 0;              // blocks and steps before the item
+    auto have_k = [&](uint32_t block) { return mbar_test(&sm.k_full[block % kSStages], (block / kSStages) & 1); };
+    auto await_k = [&](uint32_t block) {
+        await(&sm.k_full[block % kSStages], (block / kSStages) & 1, p.err, 16, &sm.abort);
+        __syncwarp();
+        tc_fence_after();
     };
-    enter();
-    // whether what the next step's S needs is there (the whole warp)
-    auto have_s = [&] {
-        return more && __all_sync(0xffffffffu, (k > 0 || mbar_test(&sm.q_full, (segs.i - 1) & 1)) &&
-                                                   mbar_test(&sm.k_full[block % kSStages], (block / kSStages) & 1));
+    auto await_h = [&](uint32_t block) {
+        await(&sm.h_full[block % kHStages], (block / kHStages) & 1, p.err, 32, &sm.abort);
     };
-    // it, by one thread
-    auto issue_s = [&] {
-        const uint32_t w = a & 1, kslot = block % kKStages;
-        const uint64_t qd = q0 + (pair && (k & 1) ? kTile / 16 : 0), kd = k0 + kslot * (kTile / 16);
+    auto await_p = [&](uint32_t step) {
+        await(&sm.p_full[step & 1], (step >> 1) & 1, p.err, 32, &sm.abort);
+        __syncwarp();
+        tc_fence_after();
+    };
+    // by one thread
+    auto issue_s = [&](uint32_t w, uint32_t block, uint32_t tile) {
+        const uint64_t qd = q0 + tile * (kTile / 16), kd = k0 + (block % kKStages) * (kTile / 16);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) umma_e4m3(tmem + kSCol + kBS * w, qd + 2 * kk, kd + 2 * kk, kIdescS, kk);
         umma_commit(&sm.s_full[w]);
-        if (!pair || (k & 1)) umma_commit(&sm.k_empty[kslot]);
-        if (k + 1 == steps) umma_commit(&sm.q_empty);
     };
-    auto advance_s = [&] {
-        const bool block_ends = !pair || (k & 1);
-        uint32_t f = (k < 2 ? 1 : 0) | (k + 2 >= steps ? 2 : 0) | (block_ends ? 4 : 0);
-        const int t = s.t0 + static_cast<int>(pair ? k >> 1 : k);
-        if (__builtin_expect(t <= s.x.sink_blocks || t + 1 == s.x.blocks, 0)) {
-            const Span span = chunks_of(p, s.x, t);
-            if (span.b - span.a < kBS / kChunk) f |= 8 | span.a << 4 | span.b << 6;
-        }
-        if (a & 1) {
-            block_of[1] = block;
-            flags[1] = f;
-        } else {
-            block_of[0] = block;
-            flags[0] = f;
-        }
-        ++a;
-        if (block_ends) ++block;
-        if (++k == steps) enter();
-        idle = 0;
-    };
-#pragma unroll 1
-    while (more || o < a) {
-        ++idle;
-        if (a < o + 2 && have_s()) {
-            tc_fence_after();
-            if (elect_one()) issue_s();
-            __syncwarp();
-            advance_s();
-        }
-        if (o < a) {
-            const uint32_t w = o & 1, blk = w ? block_of[1] : block_of[0], f = w ? flags[1] : flags[0], hslot = blk % kHStages;
-            // (the S after next follows at once where its operands are there by now: looking for
-            // them behind P costs 6% of a prompt)
-            const bool ahead = a == o + 2 && have_s();
-            bool ready;
-            if (more && a < o + 2)           // (S is waiting for Q or K, too)
-                ready = mbar_test(&sm.p_full[w], (o >> 1) & 1) && mbar_test(&sm.h_full[hslot], (blk / kHStages) & 1);
-            else
-                ready = await(&sm.h_full[hslot], (blk / kHStages) & 1, p.err, 32, &sm.abort) &&
-                        await(&sm.p_full[w], (o >> 1) & 1, p.err, 32, &sm.abort);
-            if (__all_sync(0xffffffffu, ready)) {
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t vd = v0 + hslot * (2 * kTile / 16);
-                    // 16 keys: 8 columns of P, 2048 bytes of V
-                    auto add = [&](int kk, bool more) {
-                        umma_f16_ta(tmem + kD * w, tmem + kSCol + kBS * w + 8 * kk, vd + 128 * kk, kIdescO, more ? 1u : 0u);
-                    };
-                    if (__builtin_expect(!(f & 8), 1)) {
+    auto issue_pv = [&](uint32_t w, uint32_t block, bool begin, Span span) {
+        const uint64_t vd = v0 + (block % kHStages) * (2 * kTile / 16);
+        // 16 keys: 8 columns of P, 2048 bytes of V
+        auto add = [&](int kk, bool more) {
+            umma_f16_ta(tmem + kD * w, tmem + kSCol + kBS * w + 8 * kk, vd + 128 * kk, kIdescO, more ? 1u : 0u);
+        };
+        if (__builtin_expect(span.b - span.a == kBS / kChunk, 1)) {
 #pragma unroll
-                        for (int kk = 0; kk < kBS / 16; ++kk) add(kk, !(f & 1) || kk > 0);
-                    } else {
-                        const int k_a = 2 * (f >> 4 & 3), k_b = 2 * (f >> 6);
+            for (int kk = 0; kk < kBS / 16; ++kk) add(kk, !begin || kk > 0);
+        } else {
 #pragma unroll 1
-                        for (int kk = k_a; kk < k_b; ++kk) add(kk, !(f & 1) || kk > k_a);
-                    }
-                    if (f & 4) umma_commit(&sm.h_empty[hslot]);
-                    if (f & 2) umma_commit(&sm.o_full[w]);
-                    if (ahead) issue_s();
-                }
+            for (int kk = 2 * span.a; kk < 2 * span.b; ++kk) add(kk, !begin || kk > 2 * span.a);
+        }
+    };
+#pragma unroll 1
+    for (int item = 0; segs.next(sm, p, s, lane); ++item) {
+        const int nb = s.t1 - s.t0;
+        auto span_of = [&](int i) {
+            Span span = {0, kBS / kChunk};
+            if (__builtin_expect(s.t0 + i <= s.x.sink_blocks || s.t0 + i + 1 == s.x.blocks, 0)) span = chunks_of(p, s.x, s.t0 + i);
+            return span;
+        };
+        await(&sm.q_full, item & 1, p.err, 16, &sm.abort);
+        await_k(block0);
+        const bool pair = s.x.rows > kTileRows;
+        const int steps = pair ? 2 * nb : nb;
+        // S of step k, and what its end frees
+        auto issue_step = [&](int k) {
+            const uint32_t block = block0 + (pair ? k >> 1 : k);
+            const bool block_ends = !pair || (k & 1);
+            issue_s((step0 + k) & 1, block, pair ? k & 1 : 0);
+            if (block_ends) umma_commit(&sm.k_empty[block % kKStages]);
+            if (k + 1 == steps) umma_commit(&sm.q_empty);
+        };
+        if (elect_one()) issue_step(0);
+        __syncwarp();
+        if (steps > 1) {
+            if (!pair) await_k(block0 + 1);
+            if (elect_one()) issue_step(1);
+            __syncwarp();
+        }
+#pragma unroll 1
+        for (int k = 0; k < steps; ++k) {
+            const int i = pair ? k >> 1 : k;
+            const uint32_t w = (step0 + k) & 1, block = block0 + i, next = block + (pair ? 1 : 2);
+            const bool second = pair && (k & 1);     // (the first has seen K and V)
+            const bool more = k + 2 < steps;
+            const Span span = span_of(i);
+            const bool ahead = more && (second || __all_sync(0xffffffffu, have_k(next)));
+            if (!second) await_h(block);
+            await_p(step0 + k);
+            if (elect_one()) {
+                issue_pv(w, block, k < 2, span);
+                if (!pair || second) umma_commit(&sm.h_empty[block % kHStages]);
+                if (!more) umma_commit(&sm.o_full[w]);
+                if (ahead) issue_step(k + 2);
+            }
+            __syncwarp();
+            if (more && !ahead) {
+                await_k(next);
+                if (elect_one()) issue_step(k + 2);
                 __syncwarp();
-                ++o;
-                idle = 0;
-                if (ahead) advance_s();
             }
         }
-        // the clock is read every 4096 fruitless polls
-        if (__builtin_expect(idle >= 4096, 0)) {
-            if ((idle & 4095) == 0) {
-                const uint32_t now = static_cast<uint32_t>(globaltimer_ns());
-                if (idle == 4096) t0 = now;
-                const volatile int* abort = &sm.abort;
-                const bool late = now - t0 > static_cast<uint32_t>(kWaitLimitNs);
-                if (late) {
-                    sm.abort = 1;
-                    atomicOr(p.err, 16);
-                }
-                if (__any_sync(0xffffffffu, late || *abort)) break;
-            }
-        }
+        step0 += steps;
+        block0 += nb;
     }
     __syncwarp();
     if (elect_one()) {
