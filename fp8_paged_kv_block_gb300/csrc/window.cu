@@ -560,10 +560,6 @@ __device__ void converter(WindowSmem& sm, const WindowParams& p, int w, int lane
                 uint4 x[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const uint4*>(src + 1024 * (i0 + i));
-                if (i0 > 0) {                // (all codes are read: the next block's may come, 2% of a long decode)
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.v_empty[vslot]);
-                }
                 if (!whole) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -581,6 +577,10 @@ __device__ void converter(WindowSmem& sm, const WindowParams& p, int w, int lane
                                    codes_to_half2(x[i].w & 0xFFFFu), codes_to_half2(x[i].w >> 16));
                 }
             }
+            // (the codes are free once the stores have them: an arrival behind the loads alone
+            // let the next block's overtake them)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.v_empty[vslot]);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.h_full[hslot]);

@@ -136,6 +136,19 @@ def test_window_attention_lengths_out_of_order(most):
     check_window(c, run_window(c))
 
 
+@pytest.mark.parametrize("layout", [0, 1])
+def test_window_attention_of_a_mixed_batch_time_after_time(layout):
+    """Chunks and single tokens of many lengths, sinks behind most windows: each part of the
+    kernel runs ahead of the others now and then."""
+    ctx = [1, 1903, 0, 127, 1, 1, 129, 1, 127, 127, 127, 129, 129, 129, 0, 128, 129]
+    new = [22, 0, 1, 2, 35, 1, 1, 22, 0, 1, 487, 2, 1, 1, 598, 1, 39]
+    c = R.window_case(61, ctx, new, 32, 2, layout, 129, 700)
+    first = run_window(c)
+    check_window(c, first)
+    for _ in range(20):
+        assert torch.equal(run_window(c).view(torch.int16), first.view(torch.int16))
+
+
 @pytest.mark.parametrize("most", [5, 400])
 def test_window_attention_refuses_rows_that_decrease(most):
     """A bit of the error word, no more; the next call is not touched by it."""
