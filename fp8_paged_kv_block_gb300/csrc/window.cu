@@ -49,10 +49,10 @@
 // nothing else on the SM; 1140 if the other warpgroup rests, too), 700 of waiting for P V
 // and the next S and 400 around them, so that with two in flight the tensor core has work
 // 42% of the time. Without the exponentials it would be 3% faster, without V's conversion
-// 5%, without the key scales 6%. Two prompts of 5000 tokens, 8 x 12 heads, window 4096: 611
+// 5%, without the key scales 6%. Two prompts of 5000 tokens, 8 x 12 heads, window 4096: 613
 // us (1.27 PFLOP/s); with a maximum of every 32 scores 747, before what need not wait for S
 // or P was put ahead of those waits 687. Six chunks of up to 509 tokens beside 31 decoding
-// requests, window 1000: 155 us (166 before the parts of a window's first and last blocks
+// requests, window 1000: 154 us (166 before the parts of a window's first and last blocks
 // and of the sinks' that no row sees were left out); of an item's 32000 clocks 10000 go to
 // its begin, its last P V and its output. Tried and slower (against what was best then):
 // steps of 64 keys (905 to 780), S in halves with the first ahead of P V (709 to 697),
@@ -60,12 +60,12 @@
 // 650), two threads a row (946 to 780), loops unrolled by two (707 to 697), four rows and a
 // quarter of the columns a thread, so that a key scale serves four scores (680 to 609),
 // eight more warps for the output (804 to 688), an issuing warp for each warpgroup (744 to
-// 609, taking turns 685), other K and V rings (the same; a third block of V's codes in the
-// second tile's place 164 for 168 on the longest decoding, but 622 for 611 on prompts).
-// Decoding, the blocks' reads: 64 requests of 8 x 12 heads, window 4096, 550 MB in 113 us
-// (111 in a graph, 5.0 TB/s), four requests of 110000 tokens 168 us (5.6 TB/s); an item ends
-// with 10000 clocks in which only the next three blocks are read. One token of one request:
-// 14.4 us, 12.2 in a graph, launches, schedule and one pass through every part.
+// 609, taking turns 685), a loop that polls across the items' ends (decoding 114.7 to 113,
+// prompts the same), other K and V rings (the same). Decoding, the blocks' reads: 64
+// requests of 8 x 12 heads, window 4096, 550 MB in 113 us (111 in a graph, 5.0 TB/s), four
+// requests of 110000 tokens 170 us (5.5 TB/s); an item ends with 10000 clocks in which only
+// the next three blocks are read. One token of one request: 14.4 us, 12.2 in a graph,
+// launches, schedule and one pass through every part.
 //
 // The items in (sequence, kv head, row) order are dealt to the CTAs in runs of equal
 // weight: a step counts 1, an item kItemCost besides. Items that a run's end cuts leave
