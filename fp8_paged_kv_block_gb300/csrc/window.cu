@@ -60,12 +60,13 @@
 // 650), two threads a row (946 to 780), loops unrolled by two (707 to 697), four rows and a
 // quarter of the columns a thread, so that a key scale serves four scores (680 to 609),
 // eight more warps for the output (804 to 688), an issuing warp for each warpgroup (744 to
-// 609, taking turns 685), a loop that polls across the items' ends (decoding 114.7 to 113,
-// prompts the same), other K and V rings (the same). Decoding, the blocks' reads: 64
-// requests of 8 x 12 heads, window 4096, 550 MB in 113 us (111 in a graph, 5.0 TB/s), four
-// requests of 110000 tokens 170 us (5.5 TB/s); an item ends with 10000 clocks in which only
-// the next three blocks are read. One token of one request: 14.4 us, 12.2 in a graph,
-// launches, schedule and one pass through every part.
+// 609, taking turns 685), an issuing loop that polls for the next item while the last one's
+// P V are due (decoding 115 to 113, one token 14.4 to 13.7, but prompts 608 to 613), other K
+// and V rings (the same). Decoding, the blocks' reads: 64 requests of 8 x 12 heads, window
+// 4096, 550 MB in 113 us (111 in a graph, 5.0 TB/s), four requests of 110000 tokens 170 us
+// (5.5 TB/s); an item ends with 10000 clocks in which only the next three blocks are read.
+// One token of one request: 13.7 us, 11.5 in a graph, launches, schedule and one pass
+// through every part.
 //
 // The items in (sequence, kv head, row) order are dealt to the CTAs in runs of equal
 // weight: a step counts 1, an item kItemCost besides. Items that a run's end cuts leave
@@ -133,7 +134,7 @@ struct WindowParams {
     int B, T, max_tokens, NQ, NKV, G;
     uint32_t g_mul;                          // 2^22 / G + 1: n / G = n g_mul >> 22 for n < 2^14
     uint64_t g_inv;                          // 2^64 / G + 1 (G > 1)
-    int one_item;                            // a sequence makes one item at most (no scan: 14.4 us for 15.1)
+    int one_item;                            // a sequence makes one item at most (no scan: 0.7 us of 15)
     int64_t num_blocks;
     int max_blocks, layout, ctas;
     int window, sinks;
