@@ -18,11 +18,11 @@ pa_status check_launch(const char* what);
 int device_sm_count();
 pa_status make_cache_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows);
 
-// Whether na bytes from a and nb bytes from b have one in common (NULL: none).
+// Whether na bytes from a and nb bytes from b have one in common (NULL or no bytes: none).
 inline bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb)
 {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && (x <= y ? y - x < na : x - y < nb);
+    return a && b && na && nb && (x <= y ? y - x < na : x - y < nb);
 }
 }  // namespace pa
 

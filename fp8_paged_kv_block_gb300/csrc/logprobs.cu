@@ -681,8 +681,8 @@ extern "C" pa_status pa_token_logprobs(const void* logits, int dtype, int64_t ro
     PA_REQUIRE(V <= 0x7FFFFFFF - (1 << 16) && num_rows <= 0x7FFFFFFF, PA_ERR_UNSUPPORTED,
                "%s: too many rows or tokens", name);
     PA_REQUIRE(aligned(logits, dtype == PA_DTYPE_F32 ? 4 : 2) && aligned(tokens, token_type == PA_INDEX_I64 ? 8 : 4) &&
-                   aligned(logprobs, 4) && aligned(ranks, 4) && aligned(entropy, 4) && aligned(top_ids, 4) &&
-                   aligned(top_logprobs, 4),
+                   aligned(logprobs, 4) && aligned(ranks, 4) && aligned(entropy, 4) &&
+                   (top == 0 || (aligned(top_ids, 4) && aligned(top_logprobs, 4))),
                PA_ERR_INVALID, "%s: misaligned pointer", name);
     if (num_rows == 0) return PA_OK;
     // (rows are read while others' results are already written, and read again)

@@ -727,7 +727,8 @@ PA_API pa_status pa_fp8_qkv_norm_mrope_append(
  *              positions stay.
  * slot_mapping int32 or int64 (slot_type) [num_tokens]; positions, token_batch
  *              int32 [num_tokens]; cu_tokens int32 [B + 1].
- * Outputs (block_table among them) overlap neither an input nor one another.
+ * Outputs (block_table among them) overlap neither an input nor one another
+ * (a tensor without elements, a used-up pool say, overlaps nothing).
  * B at most 1024; num_tokens, pool_size and max_blocks_per_seq * block_size
  * below 2^31, and with int32 slots num_blocks * block_size (else
  * PA_ERR_UNSUPPORTED). A call of no requests or no tokens runs like any other.
@@ -807,7 +808,7 @@ PA_API pa_status pa_fp8_window_attention(const void* q, const float* q_scale, co
  * tokens       int32 or int64 (token_type) [num_rows].
  * ranks, entropy  int32 and float [num_rows], or NULL.
  * top          0 to 32 (more: PA_ERR_UNSUPPORTED) and at most V; top_ids int32,
- *              top_logprobs float [num_rows, top] (not used with 0).
+ *              top_logprobs float [num_rows, top] (not used with 0: any address).
  * Outputs overlap neither an input nor one another (PA_ERR_INVALID).
  * ------------------------------------------------------------------------ */
 PA_API pa_status pa_token_logprobs(const void* logits, int dtype, int64_t row_stride, const void* tokens,

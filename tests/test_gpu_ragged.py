@@ -788,3 +788,20 @@ def test_ragged_step(layout, graph):
                                                 tlp[:n]))
         act.copy_(new_act)
         head.copy_(new_head)
+
+
+# ---- empty tensors, slices of others ------------------------------------------------------
+
+def test_empty_slices_of_other_tensors():
+    """A used-up pool that begins where the block table does, and alternatives of width 0
+    cut from the log probabilities: neither has an element to overlap with."""
+    pa = _pa()
+    bt = _i32(2, -1, 3, -1).reshape(2, 2)
+    slots, pos, tb, cu, nact, nhead = (torch.full((n,), 77, dtype=torch.int32, device="cuda") for n in (2, 2, 2, 3, 2, 1))
+    pa.plan_batch(_i32(5, 127), _i32(1, 1), bt.view(-1)[:0], _i32(0), bt, slots, pos, tb, cu, nact, nhead, num_blocks=9)
+    assert slots.tolist() == [2 * 128 + 5, 3 * 128 + 127] and nact.tolist() == [6, 128] and nhead.tolist() == [0]
+    x, tok = torch.randn((3, 500), device="cuda"), _i32(1, 2, 3)
+    lp, ids = torch.empty(3, device="cuda"), torch.empty((3, 4), dtype=torch.int32, device="cuda")
+    pa.token_logprobs(x, tok, lp, ranks=ids.view(-1)[:3], top_ids=ids[:, :0], top_logprobs=lp.view(3, 1)[:, :0])
+    want = R.logprob_reference(x, tok, 1)
+    assert ((lp.double() - want[0]).abs() <= 2.0 ** -14).all() and torch.equal(ids.view(-1)[:3].long(), want[1].long())

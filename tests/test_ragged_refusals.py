@@ -196,3 +196,27 @@ def test_binding_refuses_wrong_shapes_and_host_tensors(L, monkeypatch):  # noqa:
             mrope(**bad)
     with pytest.raises(TypeError):
         mrope(pair_axis=None)
+
+
+def test_empty_ranges_overlap_nothing(L):  # noqa: F811
+    """What has no elements may lie anywhere, an empty slice of another tensor among
+    it. (Each call has one overlap that counts, tested behind the empty ranges, so
+    that it is refused for that one and launches nothing.)"""
+    pool = _buf().value
+    at = lambda i: P(pool + 512 * i)  # noqa: E731
+    names = "act lens pool head bt slots sdt pos tb cu nact nhead B T P NB BS W stream".split()
+    d = {k: at(i) for i, k in enumerate("act lens pool head bt slots pos tb cu nact nhead".split())}
+    d.update(sdt=0, B=4, T=8, P=0, NB=16, BS=128, W=4, stream=None, tb=d["cu"])
+    call = caller(L.pa_plan_batch, names, d)
+    for off in (0, 16):                                  # a used-up pool, at the table's begin and inside it
+        assert call(pool=P(d["bt"].value + off)) == 2 and b"outputs overlap" in L.pa_last_error(), off
+    # no tokens: their tensors anywhere
+    none = {k: P(d["bt"].value + 16) for k in "slots pos tb".split()}
+    assert call(T=0, nhead=d["head"], **none) == 2 and b"an output overlaps an input" in L.pa_last_error()
+    names = "x dt step tok tdt R V lp rank ent k ids tlp stream".split()
+    d = {k: P((i + 1) << 36) for i, k in enumerate("x tok lp rank ent ids tlp".split())}
+    d.update(dt=1, step=1000, tdt=0, R=4, V=1000, k=0, stream=None, rank=d["tok"])
+    call = caller(L.pa_token_logprobs, names, d)
+    for off in (0, 8, 1):                                # (not used with 0 alternatives: any address)
+        stale = P(d["lp"].value + off)
+        assert call(ids=stale, tlp=stale) == 2 and b"an output overlaps an input" in L.pa_last_error(), off
