@@ -29,7 +29,7 @@
 //   warp 8           K and V blocks by TMA, key scales by cp.async
 //   warp 9           issues S and P V
 //   warp 10          Q rows and scales of the next item
-//   warp 11          the run's items, one after another, for all others
+//   warp 11          the run's items, one after another, for all others; zeros where a token sees nothing
 //   warps 12-15      V codes to FP16 in shared memory, zeros where no row sees the key
 // The issuing warp issues S of step j + 2 behind P V of step j, so that the tensor core
 // itself keeps them apart where they share columns, and an S that is complete says that
@@ -1112,6 +1112,32 @@ __device__ void describe_cut(WindowSmem& sm, const WindowParams& p, const Run& r
     if (lane == 0) p.cuts[c] = cut;
 }
 
+// Zeros for the tokens that see nothing: those before, between and behind the sequences'
+// live ones. Token t is CTA t % gridDim's, whose scheduling warp writes it while the others
+// are at the run's last items: a refused chunk of 5000 tokens beside 32 decoding requests of
+// 96 heads (123 MB) takes the call from 31 us to 46, and took it to 1884 when one CTA wrote a
+// sequence's, ahead of its items.
+__device__ void zero_rows(const WindowSmem& sm, const WindowParams& p, int lane)
+{
+    const int ctas = gridDim.x;
+    for (int g0 = 0; g0 <= p.B; g0 += 32) {
+        const int g = g0 + lane;
+        int at = 0, end = 0;                 // between sequence g - 1's live tokens and sequence g's
+        if (g <= p.B) {
+            at = g > 0 ? sm.tok[g - 1] + tokens_of(p, sm.rows[g - 1]) : min(max(__ldg(p.cu), 0), p.T);
+            end = g < p.B ? sm.tok[g] : min(max(__ldg(p.cu + p.B), 0), p.T);
+        }
+        for (uint32_t some = __ballot_sync(0xffffffffu, at < end); some != 0; some &= some - 1) {
+            const int a = __shfl_sync(0xffffffffu, at, __ffs(some) - 1), e = __shfl_sync(0xffffffffu, end, __ffs(some) - 1);
+            const int64_t first = static_cast<int64_t>(a) + (static_cast<int>(blockIdx.x) + ctas - a % ctas) % ctas;
+            for (int64_t t = first; t < e; t += ctas) {
+                uint4* dst = reinterpret_cast<uint4*>(p.out + t * p.NQ * kD);
+                for (int j = lane; j < p.NQ * (kD / 8); j += 32) dst[j] = make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     window_attention_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                             const __grid_constant__ WindowParams p)
@@ -1173,17 +1199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             run = locate(sm, p, group, run_begin(total, blockIdx.x, ctas), run_begin(total, blockIdx.x + 1, ctas));
         scheduler(sm, p, run, lane);
         describe_cut(sm, p, run, total, ctas, lane);
+        zero_rows(sm, p, lane);
     } else {
-        // rows of tokens that see nothing
-        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-            const Sequence s = sequence(p, b);
-            for (int i = 0; i < s.n; ++i) {
-                if (i == s.skip) i += s.live;
-                if (i >= s.n) break;
-                uint4* dst = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(s.tok + i) * p.NQ * kD);
-                for (int j = tid - kConvWarp * 32; j < p.NQ * (kD / 8); j += kConvWarps * 32) dst[j] = make_uint4(0, 0, 0, 0);
-            }
-        }
         converter(sm, p, warp - kConvWarp, lane);
     }
     __syncwarp();

@@ -805,3 +805,49 @@ def test_empty_slices_of_other_tensors():
     pa.token_logprobs(x, tok, lp, ranks=ids.view(-1)[:3], top_ids=ids[:, :0], top_logprobs=lp.view(3, 1)[:, :0])
     want = R.logprob_reference(x, tok, 1)
     assert ((lp.double() - want[0]).abs() <= 2.0 ** -14).all() and torch.equal(ids.view(-1)[:3].long(), want[1].long())
+
+
+# ---- rows that see nothing ------------------------------------------------------------
+
+@pytest.mark.parametrize("most", [2000, 300, 2])
+def test_window_attention_rows_that_see_nothing_are_zeros_among_others(most):
+    """Refused chunks (their tokens are rows, their lengths as before), positions below
+    zero, and tokens behind max_tokens, between and behind sequences that are served."""
+    ctx, new = [0, 0, 900, 0, 40, 0, 3, 0, 0], [700, 1, 3, 0, 400, 1, 2, 2000, 55]
+    c = R.window_case(62, ctx, new, 12, 2, 0, 200, 4, rows_behind=9, device="cuda")
+    c["act"] = torch.tensor([0, 1, 903, 0, 250, 1, 5, 0, 20], dtype=torch.int32, device="cuda")
+    c["bt"] = torch.where((c["bt"] < 0) | (c["bt"] > 10 ** 5), 1, c["bt"])
+    for k in ("kc", "vc", "ks"):                          # (other positions are seen now)
+        c[k][(c[k] == R.NAN_CODE) if k != "ks" else c[k].isnan()] = 1
+    c["max_tokens"] = most
+    check_window(c, run_window(c))
+
+
+def test_window_attention_a_refused_chunk_does_not_hold_up_the_others():
+    """The zeros of 5000 rows of a refused prompt beside 32 decoding requests (123 MB) are
+    spread over the GPU: at most five times what writing them alone takes."""
+    c = R.window_case(63, [1000] * 33, [1] * 32 + [5000], 96, 8, 0, 500, 4, device="cuda")
+    c["act"][32] = 0
+    alone = dict(c, cu=c["cu"].clone())
+    alone["cu"][33] = 32
+    ws, out = workspace(c), empty_out(c)
+
+    def best(call):
+        t = []
+        for _ in range(12):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            torch.cuda._sleep(200000)                      # (the launches are all enqueued by then)
+            a.record()
+            call()
+            b.record()
+            torch.cuda.synchronize()
+            t.append(a.elapsed_time(b))
+        return min(t[2:])
+    with_it, without = (best(window_call(d, out, ws, prepare=True)) for d in (c, alone))
+    zeros = best(lambda: out[32:].zero_())
+    print("with %.4f without %.4f zeros %.4f ms" % (with_it, without, zeros))
+    out.fill_(math.nan)
+    window_call(c, out, ws)
+    torch.cuda.synchronize()
+    assert not out[32:].any() and not out.isnan().any() and ws.error_flags() == 0
+    assert with_it - without <= 5 * zeros, (with_it, without, zeros)
