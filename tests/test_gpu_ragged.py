@@ -851,3 +851,69 @@ def test_window_attention_a_refused_chunk_does_not_hold_up_the_others():
     torch.cuda.synchronize()
     assert not out[32:].any() and not out.isnan().any() and ws.error_flags() == 0
     assert with_it - without <= 5 * zeros, (with_it, without, zeros)
+
+
+# ---- log probabilities far from zero --------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rise", [0, 5, 9])
+@pytest.mark.parametrize("base", [30, 1000, -900, 1023, -1026, 5000, -70000])
+@pytest.mark.parametrize("masked", [False, True])
+def test_logprobs_of_one_thread_far_from_zero(base, rise, dtype, masked):
+    """A row's weight in the values of one thread, so that what its reference's rounding
+    is off by (up to 2^-14 of the exponent at 1000) is not averaged over threads. Two
+    groups of 16 values, the second higher by `rise`: less and more than what makes a
+    thread take another reference.
+
+    FP32: an exponential is off by 2^-22 and by 2^-24 of its exponent (times ln 2), which
+    is below 2^5 where it counts (2^-19.5); its thread's sum has 18 roundings (2^-19.8);
+    the joins change nothing, all other threads' sums are 0 beside it. Together 2^-18 of
+    L, which is log L's error; the logarithm's and the differences' are 2^-22 of them.
+    Entropy: the same weights are in s and L, so that their errors count times the mean
+    distance of x from its mean, below 4, and s has roundings of its own, 2^-19.5 of its
+    terms' magnitudes, below 8 L."""
+    V, rows, off = 16384, 320, 2.0 ** -18
+    piece = 4 if dtype == torch.float32 else 8             # values; a thread's next is 512 pieces further
+    g = torch.Generator(device="cuda")
+    g.manual_seed(abs(base) + rise)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    x = torch.full((rows, V), base - 400.0, device="cuda").add_(rnd(rows, V))
+    thread = torch.randint(0, 512, (rows, 1, 1), generator=g, device="cuda")
+    at = torch.arange(32 // piece, device="cuda")[None, :, None] * 512 * piece + thread * piece
+    at = (at + torch.arange(piece, device="cuda")).flatten(1)
+    high = base + 2 * rnd(rows, 32)
+    high[:, 16:] += rise
+    x.scatter_(1, at, high)
+    if masked:
+        x[torch.rand(x.shape, generator=g, device="cuda") < 0.3] = -math.inf
+    x = x.to(dtype)
+    tok = at[torch.arange(rows, device="cuda"), torch.randint(0, 32, (rows,), generator=g, device="cuda")].int()
+    got = run_logprobs(x, tok, 5)
+    lp, rank, ent, ids, tlp = R.logprob_reference(x, tok, 5)
+    for a, b, t in ((got[0], lp, off), (got[4], tlp, off), (got[2], ent, 5 * off + 8 * 2.0 ** -19.5)):
+        assert torch.equal(a.isinf(), b.isinf()) and torch.equal(a.isnan(), b.isnan())
+        fin = b.isfinite()
+        err = (a.double() - b).abs()[fin] - 2.0 ** -22 * b.abs()[fin]
+        assert err.max() <= t, (float(err.max()), t)
+    assert torch.equal(got[1].long(), rank.long()) and torch.equal(got[3].long(), ids)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,V,lo,hi", [(400, 40000, 1000, 1060), (3, 40000, -1060, -1000), (400, 9001, 900, 905),
+                                          (2, 131072, 990, 1000), (400, 20000, 1e4, 1e4 + 40)])
+def test_logprobs_of_rising_rows_far_from_zero(rows, V, lo, hi, dtype):
+    """Rows that rise past 1024, where exponents are formed in another way, past it, or
+    stay below: up to 8 references a thread, each changed by a factor that is off by
+    2^-19.2 (its exponent, below 2^5, rounded, and its exponential), and three joins off by as much
+    and five sums; 2^-18 for the thread's own sums as above: together below 2^-15.5."""
+    i = torch.arange(V, device="cuda", dtype=torch.float64)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    x = (lo + (hi - lo) * i / V + 0.5 * torch.randn((rows, V), generator=g, device="cuda", dtype=torch.float64)).to(dtype)
+    tok = torch.randint(0, V, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    got = run_logprobs(x, tok, 5)
+    lp, rank, ent, ids, tlp = R.logprob_reference(x, tok, 5)
+    off = 2.0 ** -15.5
+    for a, b, t in ((got[0], lp, off), (got[4], tlp, off), (got[2], ent, off * (math.log(V) + 3))):
+        assert ((a.double() - b).abs() <= t + 2.0 ** -22 * b.abs()).all()
+    assert torch.equal(got[1].long(), rank.long()) and torch.equal(got[3].long(), ids)
