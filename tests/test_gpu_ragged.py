@@ -917,3 +917,59 @@ def test_logprobs_of_rising_rows_far_from_zero(rows, V, lo, hi, dtype):
     for a, b, t in ((got[0], lp, off), (got[4], tlp, off), (got[2], ent, off * (math.log(V) + 3))):
         assert ((a.double() - b).abs() <= t + 2.0 ** -22 * b.abs()).all()
     assert torch.equal(got[1].long(), rank.long()) and torch.equal(got[3].long(), ids)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_ragged_step_ranks(graph):
+    """The four calls one after another, eager and captured, with the ranks among the
+    outputs of the last: counts of what lies above the token in the step's own logits."""
+    pa = _pa()
+    rng = np.random.default_rng(64)
+    B, T, NQ, NKV, V, NB = 3, 40, 8, 2, 777, 6
+    f = lambda *s: torch.from_numpy(rng.standard_normal(s, dtype=np.float32)).cuda()  # noqa: E731
+    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+    act, new_act, lens, head, new_head = z(B), z(B), z(B), z(1), z(1)
+    bt, pool = torch.full((B, 2), -1, dtype=torch.int32, device="cuda"), torch.arange(NB, dtype=torch.int32, device="cuda")
+    slots, pos, tb, cu, tok = z(T), z(T), z(T), z(B + 1), z(T)
+    kc, vc, ks = z(NB, BS, NKV, D, dt=torch.uint8), z(NB, BS, NKV, D, dt=torch.uint8), z(NB, BS, NKV, dt=torch.float32)
+    qc, qs, vs = z(T, NQ, D, dt=torch.uint8), z(T, NQ, dt=torch.float32), torch.full((B, NKV, D), 0.02, device="cuda")
+    ang, w, w_out = f(300, 16), 1 + f(D) / 8, f(NQ * D, V) / 30
+    cs, qkv = torch.cat([ang.cos(), ang.sin()], 1), z(T, NQ + 2 * NKV, D, dt=torch.float32)
+    out, logits = z(T, NQ, D, dt=torch.bfloat16), z(T, V, dt=torch.float32)
+    lp, rank, ent, ids, tlp = z(T, dt=torch.float32), z(T), z(T, dt=torch.float32), z(T, 4), z(T, 4, dt=torch.float32)
+    ws = pa.WindowWorkspace(T, NQ, NKV)
+
+    def step():
+        pa.plan_batch(act, lens, pool, head, bt, slots, pos, tb, cu, new_act, new_head, num_blocks=NB)
+        pa.qkv_norm_mrope_append(qkv[:, :NQ], qkv[:, NQ:NQ + NKV], qkv[:, NQ + NKV:], w, w, cs, pos[None], qc, qs, kc, vc,
+                                 slots, ks, vs, tb, pair_axis=[0] * 16, layout=pa.LAYOUT_BSND)
+        pa.window_attention(qc, qs, kc, ks, vc, vs, bt, new_act, cu, out, window=20, sinks=2, layout=pa.LAYOUT_BSND,
+                            workspace=ws)
+        torch.matmul(out.float().view(T, -1), w_out, out=logits)
+        pa.token_logprobs(logits, tok, lp, ranks=rank, entropy=ent, top_ids=ids, top_logprobs=tlp)
+
+    call = step
+    if graph:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()                                         # (of no tokens)
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        call = g.replay
+    for new in ([30, 1, 0], [1, 5, 33]):
+        lens.copy_(_i32(*new))
+        qkv.copy_(f(T, NQ + 2 * NKV, D))
+        tok.copy_(torch.from_numpy(rng.integers(0, V, T).astype(np.int32)))
+        rank.fill_(-7)
+        call()
+        torch.cuda.synchronize()
+        n = sum(new)
+        assert ws.error_flags() == 0 and int(cu[-1]) == n
+        own = logits.gather(1, tok.long()[:, None])
+        assert torch.equal(rank[:n].long(), (logits > own).sum(-1)[:n]) and rank[:n].float().std() > 100
+        check_logprobs(logits[:n], tok[:n], 4, tuple(t[:n] for t in (lp, rank, ent, ids, tlp)))
+        act.copy_(new_act)
+        head.copy_(new_head)
