@@ -88,6 +88,10 @@ constexpr int kMaxCtas = 192;
 constexpr int kTileRows = 128;
 constexpr int kItemRows = 2 * kTileRows;
 constexpr int kTile = kBS * kD;              // bytes of a block of codes
+// What g_mul stands for: the product, 2^22 (1 + kItemRows / G) + G + kItemRows at most, in 32 bits
+// for every G (1 is the worst), and its excess of n / 2^22 below 1 / G.
+static_assert((1ull << 22) * (1 + kItemRows) + kMaxGroup + kItemRows < (1ull << 32), "n g_mul leaves 32 bits");
+static_assert(kMaxGroup * (kMaxGroup + kItemRows) < (1 << 22), "n g_mul >> 22 passes n / G");
 // K blocks, V blocks as codes and as FP16. The key scales' ring needs no barrier that
 // says a slot is free: block i + 8 is requested once K block i + 5 is free, i.e. its S
 // complete; that was issued behind block i + 3's P V, so that block i's softmax is done.
@@ -132,7 +136,7 @@ struct WindowParams {
     float* part;
     int part_rows;                           // rows of a partial item
     int B, T, max_tokens, NQ, NKV, G;
-    uint32_t g_mul;                          // 2^22 / G + 1: n / G = n g_mul >> 22 for n < 2^14
+    uint32_t g_mul;                          // 2^22 / G + 1: n / G = n g_mul >> 22 for n < G + kItemRows
     uint64_t g_inv;                          // 2^64 / G + 1 (G > 1)
     int one_item;                            // a sequence makes one item at most (no scan: 0.7 us of 15)
     int64_t num_blocks;
