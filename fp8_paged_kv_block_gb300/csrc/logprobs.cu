@@ -31,14 +31,18 @@
 // it goes. -inf is never listed: where fewer than k values are finite the lowest indices
 // of the others follow.
 //
-// What bounds it: many rows, the reads (4096 rows x 50000 FP32 129 us, 6.4 TB/s; a copy's
-// rate would take 121). A row a CTA, what stands around the reads: the two
+// What bounds it: many long rows without alternatives, the reads (4096 rows x 50000 FP32 129
+// us, 6.4 TB/s; a copy's rate would take 121). A row a CTA, what stands around the reads: the two
 // loads of the token's logit, one behind the other, 2 us, and 5 us of joins, bound, second
 // reading and order, every instruction of which runs once and out of a cold cache (250 rows
-// x 131072 BF16 with 20 alternatives 25.5 us, without 20.5; 38 such rows 14.4; one row of 32003
-// FP32 with 5 alternatives 8.3, 6.5 in a graph). Rows cut over clusters at any number of
-// rows cost more in joins than they balance (250 rows on 2, 4 and 8 CTAs 37, 60, 108 us, when
-// one took 29).
+// x 131072 BF16 with 20 alternatives 25 us, without 20.5; 38 such rows 14.4; one row of 32003
+// FP32 with 5 alternatives 8.2, 6.5 in a graph). A CTA's rows have these ends one behind
+// another: 4096 x 50000 FP32 with 20 alternatives 206 us, 4096 x 13000 BF16 59 without and 92
+// with them, where the reads are 16. A -inf among a thread's 16 values has their exponentials
+// formed twice: 250 x 131072 BF16 of which 1% or 99% are masked 33 us. All four forms are held
+// to 64 registers for two CTAs an SM and spill 4 to 36 bytes. Rows cut over clusters at
+// any number of rows cost more in joins than they balance (250 rows on 2, 4 and 8 CTAs 37, 60,
+// 108 us, when one took 29).
 #include "common.cuh"
 
 #include <cooperative_groups.h>
